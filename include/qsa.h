@@ -68,6 +68,10 @@ extern "C" {
 #define QSA_MAX_FEW_ROWS 8         /* rows per sequence on the few-row scoring path */
 #define QSA_MAX_BLOCKS (1 << 18)   /* complete blocks per sequence (1,048,576 tokens) */
 #define QSA_SCORE_GROUP 16         /* blocks per group of the group maxima (qsa_score_blocks) */
+#define QSA_MIN_PAGE_TOKENS 16     /* tokens in a page of a paged cache: a power of two from here ... */
+#define QSA_MAX_PAGE_TOKENS 1024   /* ... to here */
+#define QSA_MAX_PAGE_REQUESTS 1024 /* sequences that one qsa_pages_* call takes */
+#define QSA_MAX_CACHES 256         /* cache layers that one qsa_pages_* call takes */
 
 typedef enum qsa_status {
   QSA_OK = 0,
@@ -197,8 +201,11 @@ int32_t qsa_wait_timeouts(void);
  *                         launch's result is invalid;
  *   QSA_ERR_DEVICE_CHECK  the attention met selected block ids outside
  *                         [0, nb) among a row's first cnt entries (skipped),
- *                         or the selection met NaN scores among its
- *                         candidates (NaN ranks above every number);
+ *                         the selection met NaN scores among its
+ *                         candidates (NaN ranks above every number), the
+ *                         paged calls met page numbers outside the cache
+ *                         (their tokens skipped), or a qsa_pages_* call had
+ *                         requests that it could not serve;
  *   QSA_OK                neither.
  * qsa_last_error() gives the counts.  The counters belong to the current
  * device (each GPU keeps its own) and cover all its streams and threads; a
@@ -527,6 +534,194 @@ qsa_status qsa_sparse_attn_noalloc(const qsa_seq* seqs, int32_t n_seqs, const qs
 qsa_status qsa_lse_merge(const float* o_parts, const float* lse_parts, int32_t n_parts,
                          int64_t n_rows, int32_t head_dim, void* out, qsa_dtype out_dtype,
                          float* lse_out, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Paged K/V caches: the other attention layers of a model beside its QSA
+ * layers (dense, or with a sliding window), over the cache a serving loop
+ * keeps in pages.  A page holds the K and V of page_tokens consecutive tokens
+ * of one sequence; a page table row lists a sequence's pages in token order,
+ * and one table serves the caches of all layers.  Page tables, lengths and row
+ * ranges are DEVICE arrays that the kernels read, so a captured call follows
+ * the values they hold when it is replayed.
+ */
+
+/* One layer's paged cache (host struct).  Element (page, h, slot, d) of K -- KV
+ * head h, the page's slot-th token, channel d -- is at
+ *   k[page * page_stride + h * head_stride + slot * tok_stride + d];
+ * V likewise.  QSA_FP8_E4M3: k and v hold E4M3 codes and the (K, V) f16 scale
+ * pair of (page, h, slot) is the 4-byte record at kv_scale + 4 * (page *
+ * scale_page_stride + h * scale_head_stride + slot * scale_tok_stride), as for
+ * segments.  f32, bf16 and fp8 caches; QSA_Q8_0 caches are not paged
+ * (QSA_ERR_UNSUPPORTED: the scales of its 32-channel blocks do not factor out
+ * of a row's product, which is what lets the pages be read as stored). */
+typedef struct qsa_paged_cache {
+  const void* k;               /* device, kv_dtype; written by the calls that write a cache */
+  const void* v;
+  int64_t page_stride;         /* elements between pages */
+  int64_t head_stride;         /* elements between KV heads of a page */
+  int64_t tok_stride;          /* elements between tokens of a page, >= head_dim */
+  const void* kv_scale;        /* fp8: device scale records */
+  int64_t scale_page_stride;   /* fp8: records */
+  int64_t scale_head_stride;
+  int64_t scale_tok_stride;
+  int32_t n_pages;             /* pages in k and v */
+  int32_t page_tokens;         /* a power of two, QSA_MIN_PAGE_TOKENS .. QSA_MAX_PAGE_TOKENS */
+} qsa_paged_cache;
+
+/* The sequences and query rows of a call (host struct of device arrays).  Rows
+ * row_start[i] .. row_start[i + 1] - 1 of q belong to sequence i; with n of
+ * them and lens[i] = L tokens in the cache (the rows' own included), row j of
+ * them sits at position L - n + j and sees tokens 0 .. L - n + j.  A sequence
+ * may have no rows.  Rows of q outside every range (before row_start[0], after
+ * row_start[n_seqs]) belong to nobody: nothing of them is read and their
+ * outputs are left as they were. */
+typedef struct qsa_paged_batch {
+  const int32_t* table;        /* device [n_seqs, table_ld] page numbers */
+  int64_t table_ld;            /* entries of a table row; tokens past them have no page */
+  const int32_t* lens;         /* device [n_seqs] tokens of each sequence */
+  const int32_t* row_start;    /* device [n_seqs + 1], ascending */
+  int32_t n_seqs;
+  int32_t n_rows;              /* rows of q and out (or of k_new and v_new) */
+  int32_t max_rows;            /* the most rows one sequence has; more are computed too, only slower */
+} qsa_paged_batch;
+
+/*
+ * Attention of a batch's rows over their sequences' whole paged caches, or over
+ * a sliding window of it with a few first tokens that stay visible.  For row r
+ * at position p of sequence i and query head h (KV head g = h / (Hq / Hkv)),
+ *   T_r = {t <= p},                                   window == 0
+ *   T_r = {t <= p : t > p - window or t < n_sinks},   window >= 1
+ * with z_t = scale * q[r][h] . k_t[g],
+ *   lse[r][h] = log(sum_{t in T_r} exp z_t),
+ *   out[r][h] = sum_{t in T_r} exp(z_t - lse) v_t[g].
+ * A row that sees no token (a negative position, or none of its pages in the
+ * table) gets out = 0 and lse = -inf.  Tokens that no row of the call sees are
+ * not part of any sum, whatever their pages hold (NaN and infinities too);
+ * pages that hold no visible token are not read.  A V value that some row sees
+ * must be finite for the sums of that sequence's other rows of the call to be.
+ * Table entries outside [0, n_pages) under visible tokens: those tokens are
+ * skipped and qsa_check_device_status reports them.
+ *   cache, batch   host structs
+ *   cfg            as for qsa_sparse_attn: Hq / Hkv <= 16, head_dim 128 or 256,
+ *                  q_dtype = kv_dtype (bf16 for an fp8 cache); n_splits: the most
+ *                  runs the call's keys are divided into (CTAs that share
+ *                  them), 0 = as many as the GPU takes at a time
+ *   window         0 (no window) or the tokens a row sees, its own included
+ *   n_sinks        >= 0 first tokens that stay visible (no meaning without a window)
+ *   q              device [n_rows, Hq, head_dim], cfg->q_dtype
+ *   out            device [n_rows, Hq, head_dim], cfg->out_dtype
+ *   lse            device f32 [n_rows, Hq]; may be NULL
+ *   workspace      device scratch of >= qsa_paged_attn_workspace_size bytes; it
+ *                  depends on max_rows, cfg and the device, not on the lengths;
+ *                  contents need no initialisation; two calls that share one
+ *                  must not run concurrently (captured calls neither)
+ * Sums and softmax statistics are 32-bit; bf16 and fp8 caches: the weights
+ * exp(z - m) are rounded to bf16 for the product with V (at most 2^-8 of each,
+ * independently), out once to out_dtype.  The result depends on the
+ * lengths and the number of runs, not on timing: it is reproducible.
+ * Errors: QSA_ERR_INVALID_ARG, QSA_ERR_UNSUPPORTED, QSA_ERR_MISALIGNED,
+ * QSA_ERR_WORKSPACE, QSA_ERR_CUDA.  n_rows == 0 or n_seqs == 0 is a no-op.
+ */
+size_t qsa_paged_attn_workspace_size(const qsa_paged_batch* batch, const qsa_attn_config* cfg);
+
+qsa_status qsa_paged_attn(const qsa_paged_cache* cache, const qsa_paged_batch* batch, const qsa_attn_config* cfg,
+                          int32_t window, int32_t n_sinks, const void* q, void* out, float* lse, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/*
+ * Writing new tokens into their pages: row r at position p of sequence i (as
+ * above: the lengths already count the new tokens) goes to slot p mod
+ * page_tokens of page table[i][p / page_tokens], copied, or quantized exactly
+ * as qsa_append_tokens does (bf16 rows into an fp8 cache).
+ *   cfg            n_kv_heads, head_dim, kv_dtype (the other fields are checked
+ *                  as for qsa_paged_attn)
+ *   k_new, v_new   device, element (r, h, d) at r * row_stride + h * head_stride
+ *                  + d: slices of one fused projection will do; kv_dtype, or
+ *                  bf16 for an fp8 cache
+ *   row_stride, head_stride   elements, multiples of 16 bytes
+ * Rows at negative positions or without a page in the table are skipped, the
+ * latter reported by qsa_check_device_status.  A page that several sequences
+ * share must not be written (qsa_pages_fork gives each a last page of its own).
+ * Errors: as qsa_paged_attn.  n_rows == 0 or n_seqs == 0 is a no-op.
+ */
+qsa_status qsa_paged_append(const qsa_paged_cache* cache, const qsa_paged_batch* batch, const qsa_attn_config* cfg,
+                            const void* k_new, const void* v_new, int64_t row_stride, int64_t head_stride,
+                            void* stream);
+
+/*
+ * Who holds which page: a page table of n_seqs places for sequences, their
+ * lengths, and how many of them use each page (0: the page is free).  All of
+ * it is caller-owned device memory that starts as table = -1, lens = 0, refs
+ * = 0; the calls below keep it and run without the host knowing its contents.
+ * A page used by several sequences is full, so no append writes it.
+ */
+typedef struct qsa_page_pool {
+  int32_t* table;              /* device [n_seqs, table_ld] */
+  int64_t table_ld;
+  int32_t* lens;               /* device [n_seqs] */
+  int32_t* refs;               /* device [n_pages] */
+  int32_t n_seqs;
+  int32_t n_pages;
+  int32_t page_tokens;
+} qsa_page_pool;
+
+/*
+ * The calls take a device list of at most QSA_MAX_PAGE_REQUESTS places and
+ * serve its requests as if all of them read the pool first; a new page is
+ * always the free page with the lowest number, in list order, so results are
+ * reproducible.  A request that cannot be served changes nothing and is
+ * counted by qsa_check_device_status: a place outside [0, n_seqs), a place
+ * listed before, too few free pages left for it after those before it, and
+ * what each call adds.  n == 0 is a no-op.
+ *
+ * qsa_pages_extend   lens[seqs[i]] += n_new[i], with new pages for tokens past
+ *                    the last one.  Not served: n_new[i] < 0, more tokens than
+ *                    table_ld pages hold.
+ * qsa_pages_fork     dst[i] (an empty place) becomes a copy of src[i]'s first
+ *                    min(keep[i], lens[src[i]]) tokens (keep NULL: all): full
+ *                    pages are shared, a last page that is not full is copied
+ *                    to a new page -- its used tokens, in all n_caches caches;
+ *                    the rest of the new page is left as it was.  A source may
+ *                    be listed several times.  Not served: dst[i] holds tokens.
+ * qsa_pages_free     seqs[i] keeps its first keep[i] tokens (keep NULL: none)
+ *                    and gives up the pages behind them; their table entries
+ *                    become -1.  Not served: keep[i] < 0, or a last page that
+ *                    would be kept in part and is shared (fork its first
+ *                    keep[i] tokens instead).
+ * qsa_pages_compact  moves the pages in use with the highest numbers to the
+ *                    free pages with the lowest, until the pages in use are
+ *                    0 .. used - 1 (whole pages, in all n_caches caches; in
+ *                    ascending order on both sides), and writes `used` to
+ *                    *n_used (device, may be NULL): what lies behind them can
+ *                    be given back.
+ * qsa_pages_copy     copies page src[i] to page dst[i], whole, in all n_caches
+ *                    caches, for device lists of n (any number) pages.  The
+ *                    destinations are distinct and none of them is a source;
+ *                    numbers outside [0, n_pages) are skipped and counted.
+ *
+ *   caches           host array of n_caches <= QSA_MAX_CACHES caches, each with the
+ *                    pool's page_tokens and at least its n_pages pages
+ *   cfg              n_kv_heads, head_dim, kv_dtype of all of them
+ *   workspace        device scratch of qsa_pages_workspace_size bytes; as for
+ *                    the other calls
+ * Errors: QSA_ERR_INVALID_ARG, QSA_ERR_UNSUPPORTED (sizes, dtypes),
+ * QSA_ERR_MISALIGNED, QSA_ERR_WORKSPACE, QSA_ERR_CUDA.
+ */
+size_t qsa_pages_workspace_size(const qsa_page_pool* pool);
+
+qsa_status qsa_pages_extend(const qsa_page_pool* pool, const int32_t* seqs, const int32_t* n_new, int32_t n,
+                            void* stream);
+qsa_status qsa_pages_fork(const qsa_page_pool* pool, const qsa_paged_cache* caches, int32_t n_caches,
+                          const qsa_attn_config* cfg, const int32_t* src, const int32_t* dst, const int32_t* keep,
+                          int32_t n, void* workspace, size_t workspace_bytes, void* stream);
+qsa_status qsa_pages_free(const qsa_page_pool* pool, const int32_t* seqs, const int32_t* keep, int32_t n,
+                          void* stream);
+qsa_status qsa_pages_compact(const qsa_page_pool* pool, const qsa_paged_cache* caches, int32_t n_caches,
+                             const qsa_attn_config* cfg, int32_t* n_used, void* workspace, size_t workspace_bytes,
+                             void* stream);
+qsa_status qsa_pages_copy(const qsa_paged_cache* caches, int32_t n_caches, const qsa_attn_config* cfg,
+                          const int32_t* src, const int32_t* dst, int32_t n, void* stream);
 
 #ifdef __cplusplus
 }

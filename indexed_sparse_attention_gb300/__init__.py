@@ -71,7 +71,9 @@ EXPORTS = ("qsa_status_string", "qsa_last_error", "qsa_version", "qsa_pool_index
            "qsa_score_select_topk_blocked", "qsa_append_tokens", "qsa_arena_create", "qsa_arena_ensure",
            "qsa_arena_base", "qsa_arena_mapped", "qsa_arena_reserved", "qsa_arena_granularity", "qsa_arena_destroy",
            "qsa_check_device_status", "qsa_selftest_wait_timeout", "qsa_pool_score_blocks",
-           "qsa_append_score_blocks")
+           "qsa_append_score_blocks", "qsa_paged_attn_workspace_size", "qsa_paged_attn", "qsa_paged_append",
+           "qsa_pages_workspace_size", "qsa_pages_extend", "qsa_pages_fork", "qsa_pages_free", "qsa_pages_compact",
+           "qsa_pages_copy")
 NOALLOC_SCRATCH_BYTES = 4 << 20
 
 
@@ -128,6 +130,7 @@ def lib() -> ctypes.CDLL:
                  "qsa_sparse_attn", "qsa_sparse_attn_noalloc", "qsa_lse_merge", "qsa_score_select_topk_blocked",
                  "qsa_append_tokens", "qsa_arena_create", "qsa_arena_ensure", "qsa_arena_destroy"):
         getattr(L, name).restype = i32
+    paged.declare(L)
     _lib = L
     return L
 
@@ -640,3 +643,9 @@ class LayerStep:
         finally:
             torch.cuda.nvtx.range_pop()
         return self.out, self.lse
+
+
+# The paged caches' part of the binding builds on the names above.
+from . import paged  # noqa: E402
+from .paged import (PagedBatch, PagedCache, PagedStep, PagePool, paged_append, paged_attn,  # noqa: E402, F401
+                    paged_attn_workspace_size)

@@ -10,24 +10,16 @@
 #include <string>
 #include <vector>
 
-#include <nvtx3/nvToolsExt.h>
-
-#include "qsa_internal.cuh"
+#include "qsa_host.cuh"
+#include "qsa_paged.cuh"
 
 namespace {
 
 thread_local std::string g_last_error;
 
-// An NVTX range around each call that enqueues work (named after the entry
-// point): a profiler attributes the call's launches to the QSA step they
-// serve.  Without a profiler attached the push and pop are no-ops.
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-  NvtxRange(const NvtxRange&) = delete;
-  NvtxRange& operator=(const NvtxRange&) = delete;
-};
+}  // namespace
 
+namespace qsa {
 qsa_status fail(qsa_status s, const char* fmt, ...) {
   char buf[512];
   va_list ap;
@@ -46,15 +38,11 @@ qsa_status ok() {
 qsa_status cuda_fail(cudaError_t e, const char* where) {
   return fail(QSA_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
 }
+}  // namespace qsa
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+using namespace qsa;
 
-bool quantized(int d) { return d == QSA_FP8_E4M3 || d == QSA_Q8_0; }
-size_t dtype_size(qsa_dtype d) { return d == QSA_F32 ? 4 : quantized(d) ? 1 : 2; }
-
-bool valid_dtype(int d) { return d == QSA_F32 || d == QSA_BF16; }
-// K/V state types: the value types plus the fp8 state.
-bool valid_kv_dtype(int d) { return valid_dtype(d) || quantized(d); }
+namespace {
 
 // Complete blocks the last (furthest) row of a sequence sees: floor(L / 4).
 int64_t max_visible_blocks(const qsa_seq& s) { return s.n_tokens / 4; }
@@ -77,8 +65,6 @@ qsa_status check_rows(const qsa_seq* seqs, int32_t n_seqs, const char* fn, int64
   *total_rows = rows;
   return QSA_OK;
 }
-
-cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
 std::mutex g_dev_mu;
 int g_sm_count[64];
@@ -118,10 +104,6 @@ int device_sm_count() {
 }
 }  // namespace qsa
 
-using namespace qsa;
-
-#define QSA_API extern "C" __attribute__((visibility("default")))
-
 QSA_API const char* qsa_status_string(qsa_status s) {
   switch (s) {
     case QSA_OK: return "QSA_OK";
@@ -158,13 +140,19 @@ QSA_API qsa_status qsa_check_device_status(void* stream) {
   std::lock_guard<std::mutex> lock(mu);
   const int w = qsa_wait_timeouts(), st = selftest_timeouts_take();
   const int bad_a = attn_bad_ids_take(), bad_t = attn_tc_bad_ids_take(), nan = select_nan_keys_take();
-  if (w < 0 || st < 0 || bad_a < 0 || bad_t < 0 || nan < 0)
+  const int pages_a = paged_bad_pages_take(), pages_w = paged_append_bad_pages_take(), unserved = pages_unserved_take();
+  if (w < 0 || st < 0 || bad_a < 0 || bad_t < 0 || nan < 0 || pages_a < 0 || pages_w < 0 || unserved < 0)
     return fail(QSA_ERR_CUDA, "%s: the device counters could not be read", fn);
   const int waits = (w - seen_waits[dev]) + st, bad = bad_a + bad_t;
   seen_waits[dev] = w;
   if (waits > 0)
     return fail(QSA_ERR_TIMEOUT, "%s: %d device wait(s) gave up; %d out-of-range selected ids, %d NaN scores", fn,
                 waits, bad, nan);
+  if (pages_a + pages_w > 0 || unserved > 0)
+    return fail(QSA_ERR_DEVICE_CHECK,
+                "%s: %d page table entries outside the cache under visible or new tokens (skipped), %d page requests "
+                "not served; %d out-of-range selected ids, %d NaN scores",
+                fn, pages_a + pages_w, unserved, bad, nan);
   if (bad > 0 || nan > 0)
     return fail(QSA_ERR_DEVICE_CHECK, "%s: %d out-of-range selected ids (skipped), %d NaN scores among the selection's candidates",
                 fn, bad, nan);
@@ -616,6 +604,26 @@ QSA_API qsa_status qsa_score_select_topk_blocked(const qsa_seq* seqs, int32_t n_
 }
 
 // ------------------------------------------------------------------ step 4
+namespace qsa {
+qsa_status check_attn_config(const qsa_attn_config* cfg, const char* fn) {
+  if (!cfg) return fail(QSA_ERR_INVALID_ARG, "%s: null config", fn);
+  if (cfg->n_q_heads < 1 || cfg->n_kv_heads < 1 || cfg->n_q_heads % cfg->n_kv_heads != 0)
+    return fail(QSA_ERR_INVALID_ARG, "%s: n_q_heads=%d must be a positive multiple of n_kv_heads=%d", fn,
+                cfg->n_q_heads, cfg->n_kv_heads);
+  if (cfg->n_q_heads / cfg->n_kv_heads > 16)
+    return fail(QSA_ERR_UNSUPPORTED, "%s: more than 16 query heads per KV head", fn);
+  if (cfg->head_dim != 128 && cfg->head_dim != 256)
+    return fail(QSA_ERR_UNSUPPORTED, "%s: head_dim=%d (supported: 128, 256)", fn, cfg->head_dim);
+  if (!valid_dtype(cfg->q_dtype) || !valid_kv_dtype(cfg->kv_dtype) || !valid_dtype(cfg->out_dtype))
+    return fail(QSA_ERR_UNSUPPORTED, "%s: unknown dtype", fn);
+  if (quantized(cfg->kv_dtype) ? cfg->q_dtype != QSA_BF16 : cfg->q_dtype != cfg->kv_dtype)
+    return fail(QSA_ERR_UNSUPPORTED, "%s: q_dtype must equal kv_dtype (bf16 with quantized K/V)", fn);
+  if (!(cfg->scale >= 0.f) || isinf(cfg->scale)) return fail(QSA_ERR_INVALID_ARG, "%s: bad scale", fn);
+  return QSA_OK;
+}
+
+}  // namespace qsa
+
 namespace {
 
 // Longest selected list any row of the call can have: 4 tokens per listed
@@ -633,23 +641,6 @@ AttnPlan plan_splits(const qsa_seq* seqs, int32_t n_seqs, const qsa_attn_config*
 
 size_t attn_ws_bytes(const AttnPlan& sp, int64_t rows, const qsa_attn_config* cfg) {
   return attn_workspace_bytes(sp, rows, cfg->n_q_heads, cfg->head_dim);
-}
-
-qsa_status check_attn_config(const qsa_attn_config* cfg, const char* fn) {
-  if (!cfg) return fail(QSA_ERR_INVALID_ARG, "%s: null config", fn);
-  if (cfg->n_q_heads < 1 || cfg->n_kv_heads < 1 || cfg->n_q_heads % cfg->n_kv_heads != 0)
-    return fail(QSA_ERR_INVALID_ARG, "%s: n_q_heads=%d must be a positive multiple of n_kv_heads=%d", fn,
-                cfg->n_q_heads, cfg->n_kv_heads);
-  if (cfg->n_q_heads / cfg->n_kv_heads > 16)
-    return fail(QSA_ERR_UNSUPPORTED, "%s: more than 16 query heads per KV head", fn);
-  if (cfg->head_dim != 128 && cfg->head_dim != 256)
-    return fail(QSA_ERR_UNSUPPORTED, "%s: head_dim=%d (supported: 128, 256)", fn, cfg->head_dim);
-  if (!valid_dtype(cfg->q_dtype) || !valid_kv_dtype(cfg->kv_dtype) || !valid_dtype(cfg->out_dtype))
-    return fail(QSA_ERR_UNSUPPORTED, "%s: unknown dtype", fn);
-  if (quantized(cfg->kv_dtype) ? cfg->q_dtype != QSA_BF16 : cfg->q_dtype != cfg->kv_dtype)
-    return fail(QSA_ERR_UNSUPPORTED, "%s: q_dtype must equal kv_dtype (bf16 with quantized K/V)", fn);
-  if (!(cfg->scale >= 0.f) || isinf(cfg->scale)) return fail(QSA_ERR_INVALID_ARG, "%s: bad scale", fn);
-  return QSA_OK;
 }
 
 qsa_status check_segments(const qsa_seq* seqs, int32_t n_seqs, const qsa_attn_config* cfg, const char* fn) {

@@ -1,0 +1,365 @@
+"""Paged K/V caches: attention over them, their writer, and their pages
+(include/qsa.h, "Paged K/V caches").  Argument marshalling only.
+
+    pages = PagePool(table, lens, refs, caches)          # who holds which page
+    pages.extend(seqs, n_new)                            # room for the step's tokens
+    step = PagedStep(caches[layer], batch, q, window=W, n_sinks=S)
+    out, lse = step.run(k_new, v_new)                    # append, then attend
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import dataclasses
+from typing import Sequence
+
+import torch
+
+from . import AttnConfig, BF16, F32, FP8, _check, _dtype_code, _ptr, lib
+
+
+class PagedCacheDesc(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("tok_stride", ctypes.c_int64), ("kv_scale", ctypes.c_void_p),
+                ("scale_page_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64),
+                ("scale_tok_stride", ctypes.c_int64), ("n_pages", ctypes.c_int32), ("page_tokens", ctypes.c_int32)]
+
+
+class PagedBatchDesc(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("table_ld", ctypes.c_int64), ("lens", ctypes.c_void_p),
+                ("row_start", ctypes.c_void_p), ("n_seqs", ctypes.c_int32), ("n_rows", ctypes.c_int32),
+                ("max_rows", ctypes.c_int32)]
+
+
+class PagePoolDesc(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("table_ld", ctypes.c_int64), ("lens", ctypes.c_void_p),
+                ("refs", ctypes.c_void_p), ("n_seqs", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32)]
+
+
+MIN_PAGE_TOKENS, MAX_PAGE_TOKENS = 16, 1024
+MAX_PAGE_REQUESTS = 1024
+MAX_CACHES = 256
+
+
+def declare(L: ctypes.CDLL):
+    """Argument types of the entry points, on the loaded library."""
+    vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    cachep, batchp, poolp, cfgp = (ctypes.POINTER(t) for t in (PagedCacheDesc, PagedBatchDesc, PagePoolDesc, AttnConfig))
+    L.qsa_paged_attn_workspace_size.argtypes = [batchp, cfgp]
+    L.qsa_paged_attn_workspace_size.restype = sz
+    L.qsa_paged_attn.argtypes = [cachep, batchp, cfgp, i32, i32, vp, vp, vp, vp, sz, vp]
+    L.qsa_paged_append.argtypes = [cachep, batchp, cfgp, vp, vp, i64, i64, vp]
+    L.qsa_pages_workspace_size.argtypes = [poolp]
+    L.qsa_pages_workspace_size.restype = sz
+    L.qsa_pages_extend.argtypes = [poolp, vp, vp, i32, vp]
+    L.qsa_pages_fork.argtypes = [poolp, cachep, i32, cfgp, vp, vp, vp, i32, vp, sz, vp]
+    L.qsa_pages_free.argtypes = [poolp, vp, vp, i32, vp]
+    L.qsa_pages_compact.argtypes = [poolp, cachep, i32, cfgp, vp, vp, sz, vp]
+    L.qsa_pages_copy.argtypes = [cachep, i32, cfgp, vp, vp, i32, vp]
+    for name in ("attn", "append"):
+        getattr(L, f"qsa_paged_{name}").restype = i32
+    for name in ("extend", "fork", "free", "compact", "copy"):
+        getattr(L, f"qsa_pages_{name}").restype = i32
+
+
+# ---------------------------------------------------------------------- devices and streams
+
+@contextlib.contextmanager
+def _device_of(t: torch.Tensor):
+    """The tensor's device as the current one (the library launches there)."""
+    if not t.is_cuda or t.device.index == torch.cuda.current_device():
+        yield
+        return
+    with torch.cuda.device(t.device):
+        yield
+
+
+def _raw_stream(stream, device) -> int:
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _scratch(n_bytes: int, device, stream) -> torch.Tensor:
+    """A workspace that lives until the work on `stream` is done with it."""
+    ws = torch.empty(max(int(n_bytes), 16), dtype=torch.uint8, device=device)
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(_raw_stream(stream, device), device=device)
+        ws.record_stream(stream)
+    return ws
+
+
+def _int_list(name: str, t: torch.Tensor, like: torch.Tensor) -> torch.Tensor:
+    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous int32 vector")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, the pool on {like.device}")
+    return t
+
+
+# ---------------------------------------------------------------------- descriptions
+
+class PagedCache:
+    """One layer's cache: k, v are [n_pages, Hkv, page_tokens, D] views (channel
+    stride 1, equal strides; any order of the other axes in memory).  fp8: E4M3
+    codes (float8_e4m3fn or uint8) and kv_scale, an [n_pages, Hkv, page_tokens, 2]
+    float16 view of the (K, V) scale pairs."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, kv_scale: torch.Tensor | None = None):
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
+            raise ValueError("k and v must be [n_pages, Hkv, page_tokens, D] of one shape, dtype and device")
+        if k.stride(3) != 1 or k.stride() != v.stride():
+            raise TypeError("k and v need unit channel stride and equal strides")
+        self.k, self.v, self.kv_scale = k, v, kv_scale
+        self.n_pages, self.n_kv_heads, self.page_tokens, self.head_dim = (int(x) for x in k.shape)
+        self.kv_dtype = _dtype_code(k)
+        d = self.desc = PagedCacheDesc()
+        d.k, d.v = k.data_ptr(), v.data_ptr()
+        d.page_stride, d.head_stride, d.tok_stride = k.stride(0), k.stride(1), k.stride(2)
+        d.n_pages, d.page_tokens = self.n_pages, self.page_tokens
+        if (kv_scale is not None) != (self.kv_dtype == FP8):
+            raise ValueError("kv_scale goes with an fp8 cache")
+        if kv_scale is not None:
+            s = kv_scale
+            if s.dtype != torch.float16 or tuple(s.shape) != (*k.shape[:3], 2) or s.stride(3) != 1 or any(
+                    s.stride(i) % 2 for i in range(3)):
+                raise TypeError("kv_scale must be a float16 [n_pages, Hkv, page_tokens, 2] view of whole scale records")
+            if s.device != k.device:
+                raise ValueError("kv_scale on another device than k")
+            d.kv_scale = s.data_ptr()
+            d.scale_page_stride, d.scale_head_stride, d.scale_tok_stride = (s.stride(i) // 2 for i in range(3))
+        self.byref = ctypes.byref(d)
+
+    @property
+    def row_dtype(self):
+        """The dtype of new rows (and of queries)."""
+        return torch.float32 if self.kv_dtype == F32 else torch.bfloat16
+
+    def config(self, n_q_heads: int | None = None, out_dtype=torch.float32, scale: float = 0.0,
+               n_splits: int = 0) -> AttnConfig:
+        hq = self.n_kv_heads if n_q_heads is None else int(n_q_heads)
+        return AttnConfig(hq, self.n_kv_heads, self.head_dim, F32 if self.kv_dtype == F32 else BF16, self.kv_dtype,
+                          _dtype_code(torch.empty(0, dtype=out_dtype)), float(scale), int(n_splits))
+
+
+class PagedBatch:
+    """The sequences and rows of a call.  table [n_seqs, >= pages], lens [n_seqs]
+    and row_start [n_seqs + 1] are int32 tensors on the GPU, read when the work
+    runs; n_rows is the rows of q, max_rows the most that one sequence has."""
+
+    def __init__(self, table: torch.Tensor, lens: torch.Tensor, row_start: torch.Tensor, *, n_rows: int,
+                 max_rows: int | None = None):
+        if any(t.dtype != torch.int32 for t in (table, lens, row_start)):
+            raise TypeError("table, lens and row_start must be int32")
+        if table.dim() != 2 or not table.is_contiguous():
+            raise TypeError("table must be a contiguous [n_seqs, pages]")
+        n = int(table.shape[0])
+        if tuple(lens.shape) != (n,) or tuple(row_start.shape) != (n + 1,) or not (
+                lens.is_contiguous() and row_start.is_contiguous()):
+            raise ValueError("lens must be [n_seqs] and row_start [n_seqs + 1], contiguous")
+        if len({t.device for t in (table, lens, row_start)}) != 1:
+            raise ValueError("table, lens and row_start on different devices")
+        self.table, self.lens, self.row_start = table, lens, row_start
+        self.n_seqs, self.n_rows = n, int(n_rows)
+        self.max_rows = self.n_rows if max_rows is None else int(max_rows)
+        ld = int(table.shape[1])
+        self.desc = PagedBatchDesc(table.data_ptr(), ld, lens.data_ptr(), row_start.data_ptr(), n, self.n_rows,
+                                   self.max_rows)
+        self.byref = ctypes.byref(self.desc)
+
+
+def _check_rows(what: str, t: torch.Tensor, shape, dtype, device):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{what} must be {list(shape)} of {dtype} on {device}, not {list(t.shape)} of {t.dtype} on {t.device}")
+
+
+# ---------------------------------------------------------------------- calls
+
+def paged_attn_workspace_size(batch: PagedBatch, cfg: AttnConfig) -> int:
+    with _device_of(batch.table):
+        return int(lib().qsa_paged_attn_workspace_size(batch.byref, ctypes.byref(cfg)))
+
+
+def paged_attn(cache: PagedCache, batch: PagedBatch, q: torch.Tensor, out: torch.Tensor,
+               lse: torch.Tensor | None = None, *, window: int = 0, n_sinks: int = 0, scale: float = 0.0,
+               n_splits: int = 0, workspace: torch.Tensor | None = None, stream=None, cfg: AttnConfig | None = None):
+    """Attention of the batch's rows q [n_rows, Hq, D] over their paged caches:
+    every token up to the row's own, or with window >= 1 the last `window` of
+    them and the first n_sinks tokens."""
+    dev = cache.k.device
+    _check_rows("q", q, (batch.n_rows, q.shape[1] if q.dim() == 3 else 0, cache.head_dim), cache.row_dtype, dev)
+    _check_rows("out", out, q.shape, out.dtype, dev)
+    if lse is not None:
+        _check_rows("lse", lse, q.shape[:2], torch.float32, dev)
+    if not (q.is_contiguous() and out.is_contiguous() and (lse is None or lse.is_contiguous())):
+        raise ValueError("q, out and lse must be contiguous")
+    if batch.table.device != dev:
+        raise ValueError("the batch's arrays are on another device than the cache")
+    if cfg is None:
+        cfg = cache.config(q.shape[1], out.dtype, scale, n_splits)
+    with _device_of(q):
+        if workspace is None:
+            workspace = _scratch(lib().qsa_paged_attn_workspace_size(batch.byref, ctypes.byref(cfg)), dev, stream)
+        _check("qsa_paged_attn", lib().qsa_paged_attn(
+            cache.byref, batch.byref, ctypes.byref(cfg), int(window), int(n_sinks), q.data_ptr(), out.data_ptr(),
+            _ptr(lse), workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev)))
+
+
+def paged_append(cache: PagedCache, batch: PagedBatch, k_new: torch.Tensor, v_new: torch.Tensor, stream=None):
+    """Write the batch's rows k_new, v_new ([n_rows, Hkv, D], unit channel stride,
+    equal strides: slices of one projection will do) into their pages."""
+    dev = cache.k.device
+    shape = (batch.n_rows, cache.n_kv_heads, cache.head_dim)
+    _check_rows("k_new", k_new, shape, cache.row_dtype, dev)
+    _check_rows("v_new", v_new, shape, cache.row_dtype, dev)
+    if k_new.stride() != v_new.stride() or (k_new.numel() and k_new.stride(2) != 1):
+        raise ValueError("k_new and v_new need unit channel stride and equal strides")
+    if batch.table.device != dev:
+        raise ValueError("the batch's arrays are on another device than the cache")
+    cfg = cache.config()
+    with _device_of(k_new):
+        _check("qsa_paged_append", lib().qsa_paged_append(
+            cache.byref, batch.byref, ctypes.byref(cfg), k_new.data_ptr(), v_new.data_ptr(), k_new.stride(0),
+            k_new.stride(1), _raw_stream(stream, dev)))
+
+
+class PagedStep:
+    """Preallocated buffers for one layer's attention over its paged cache, so
+    the same call can be replayed (or captured in a CUDA graph): `out`, `lse`
+    and the workspace belong to the step, and what the table, the lengths and
+    the row ranges hold is read when the work runs."""
+
+    def __init__(self, cache: PagedCache, batch: PagedBatch, q: torch.Tensor, *, out_dtype=torch.float32,
+                 window: int = 0, n_sinks: int = 0, scale: float = 0.0, n_splits: int = 0):
+        dev = cache.k.device
+        _check_rows("q", q, (batch.n_rows, q.shape[1] if q.dim() == 3 else 0, cache.head_dim), cache.row_dtype, dev)
+        if not q.is_contiguous():
+            raise ValueError("q must be contiguous")
+        if batch.table.device != dev:
+            raise ValueError("the batch's arrays are on another device than the cache")
+        self.cache, self.batch, self.q = cache, batch, q
+        self.window, self.n_sinks = int(window), int(n_sinks)
+        self.cfg = cache.config(q.shape[1], out_dtype, scale, n_splits)
+        self.out = torch.empty(q.shape, dtype=out_dtype, device=dev)
+        self.lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
+        self.ws = torch.empty(max(paged_attn_workspace_size(batch, self.cfg), 16), dtype=torch.uint8, device=dev)
+        self._args = (cache.byref, batch.byref, ctypes.byref(self.cfg), self.window, self.n_sinks, q.data_ptr(),
+                      self.out.data_ptr(), self.lse.data_ptr(), self.ws.data_ptr(), self.ws.numel())
+
+    def append(self, k_new: torch.Tensor, v_new: torch.Tensor, stream=None):
+        paged_append(self.cache, self.batch, k_new, v_new, stream)
+
+    def attend(self, stream=None):
+        dev = self.q.device
+        if dev.index == torch.cuda.current_device():
+            status = lib().qsa_paged_attn(*self._args, _raw_stream(stream, dev))
+        else:
+            with torch.cuda.device(dev):
+                status = lib().qsa_paged_attn(*self._args, _raw_stream(stream, dev))
+        if status:
+            _check("qsa_paged_attn", status)
+        return self.out, self.lse
+
+    def run(self, k_new: torch.Tensor | None = None, v_new: torch.Tensor | None = None, stream=None):
+        """Append (when given new rows), then attend."""
+        if k_new is not None:
+            self.append(k_new, v_new, stream)
+        return self.attend(stream)
+
+
+@dataclasses.dataclass
+class _Caches:
+    array: ctypes.Array
+    n: int
+    cfg: AttnConfig
+
+
+def _cache_array(caches: Sequence[PagedCache]) -> _Caches:
+    caches = list(caches)
+    if len({(c.n_kv_heads, c.head_dim, c.kv_dtype, c.page_tokens) for c in caches}) > 1:
+        raise ValueError("the caches of a pool have one head layout, dtype and page size")
+    arr = (PagedCacheDesc * max(len(caches), 1))(*[c.desc for c in caches])
+    return _Caches(arr, len(caches), caches[0].config() if caches else AttnConfig(1, 1, 128, F32, F32, F32, 0.0, 0))
+
+
+class PagePool:
+    """Who holds which page, on the GPU: table [places, pages] (-1: none), lens
+    [places] and refs [n_pages] are int32 tensors, and caches are the layers
+    whose pages move together.  Every call is asynchronous; requests that could
+    not be served are counted (check_device_status) and change nothing."""
+
+    def __init__(self, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, caches: Sequence[PagedCache] = (),
+                 page_tokens: int | None = None):
+        if table.dtype != torch.int32 or table.dim() != 2 or not table.is_contiguous():
+            raise TypeError("table must be a contiguous int32 [places, pages]")
+        _int_list("lens", lens, table)
+        _int_list("refs", refs, table)
+        if lens.numel() != table.shape[0]:
+            raise ValueError("lens must have one entry for each row of table")
+        if page_tokens is None:
+            if not caches:
+                raise ValueError("page_tokens is needed without caches")
+            page_tokens = caches[0].page_tokens
+        if any(c.k.device != table.device for c in caches):
+            raise ValueError("the pool's arrays are on another device than a cache")
+        self.table, self.lens, self.refs, self.caches = table, lens, refs, list(caches)
+        self.page_tokens = int(page_tokens)
+        self._c = _cache_array(self.caches)
+        self.desc = PagePoolDesc(table.data_ptr(), int(table.shape[1]), lens.data_ptr(), refs.data_ptr(),
+                                 int(table.shape[0]), int(refs.numel()), self.page_tokens)
+        self.byref = ctypes.byref(self.desc)
+        with _device_of(table):
+            self.ws = torch.empty(max(int(lib().qsa_pages_workspace_size(self.byref)), 16), dtype=torch.uint8,
+                                  device=table.device)
+
+    @classmethod
+    def empty(cls, n_places: int, pages_each: int, caches: Sequence[PagedCache]) -> "PagePool":
+        """A pool over the caches' pages in which every page is free."""
+        dev, n = caches[0].k.device, min(c.n_pages for c in caches)
+        return cls(torch.full((n_places, pages_each), -1, dtype=torch.int32, device=dev),
+                   torch.zeros(n_places, dtype=torch.int32, device=dev),
+                   torch.zeros(n, dtype=torch.int32, device=dev), caches)
+
+    def _call(self, name, stream, *args):
+        with _device_of(self.table):
+            _check(name, getattr(lib(), name)(*args, _raw_stream(stream, self.table.device)))
+
+    def _pair(self, a_name, a, b_name, b):
+        _int_list(a_name, a, self.table)
+        if b is not None and _int_list(b_name, b, self.table).numel() != a.numel():
+            raise ValueError(f"{a_name} and {b_name} must have the same length")
+        return a.numel()
+
+    def extend(self, seqs: torch.Tensor, n_new: torch.Tensor, stream=None):
+        """lens[seqs] += n_new, with the lowest free pages for what they lack."""
+        n = self._pair("seqs", seqs, "n_new", n_new)
+        self._call("qsa_pages_extend", stream, self.byref, seqs.data_ptr(), n_new.data_ptr(), n)
+
+    def fork(self, src: torch.Tensor, dst: torch.Tensor, keep: torch.Tensor | None = None, stream=None):
+        """The empty places dst become copies of src (their first keep tokens):
+        full pages shared, a last page that is not full copied in every cache."""
+        n = self._pair("src", src, "dst", dst)
+        self._pair("src", src, "keep", keep)
+        self._call("qsa_pages_fork", stream, self.byref, self._c.array, self._c.n, ctypes.byref(self._c.cfg),
+                   src.data_ptr(), dst.data_ptr(), _ptr(keep), n, self.ws.data_ptr(), self.ws.numel())
+
+    def free(self, seqs: torch.Tensor, keep: torch.Tensor | None = None, stream=None):
+        """Give up the pages of seqs behind their first keep tokens (default: all)."""
+        n = self._pair("seqs", seqs, "keep", keep)
+        self._call("qsa_pages_free", stream, self.byref, seqs.data_ptr(), _ptr(keep), n)
+
+    def compact(self, n_used: torch.Tensor | None = None, stream=None):
+        """Move the pages in use to the lowest numbers; n_used (int32, one element
+        on the GPU) receives how many there are."""
+        if n_used is not None:
+            _int_list("n_used", n_used, self.table)
+        self._call("qsa_pages_compact", stream, self.byref, self._c.array, self._c.n, ctypes.byref(self._c.cfg),
+                   _ptr(n_used), self.ws.data_ptr(), self.ws.numel())
+
+    def copy(self, src: torch.Tensor, dst: torch.Tensor, stream=None):
+        """Copy pages src[i] to dst[i], whole, in every cache."""
+        n = self._pair("src", src, "dst", dst)
+        self._call("qsa_pages_copy", stream, self._c.array, self._c.n, ctypes.byref(self._c.cfg), src.data_ptr(),
+                   dst.data_ptr(), n)
