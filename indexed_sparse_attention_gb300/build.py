@@ -19,7 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libqsa.so")
 SOURCES = ["qsa_api.cu", "qsa_score.cu", "qsa_score_tc.cu", "qsa_select.cu", "qsa_attn.cu", "qsa_attn_tc.cu", "qsa_append.cu", "qsa_arena.cu", "qsa_check.cu",
-           "qsa_paged_api.cu", "qsa_paged.cu", "qsa_paged_append.cu", "qsa_pages.cu"]
+           "qsa_paged_api.cu", "qsa_paged.cu", "qsa_paged_tc.cu", "qsa_paged_append.cu", "qsa_pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

@@ -123,9 +123,10 @@ QSA_API const char* qsa_last_error(void) { return g_last_error.c_str(); }
 QSA_API int32_t qsa_version(void) { return QSA_VERSION; }
 
 QSA_API int32_t qsa_wait_timeouts(void) {
-  const int a = score_wait_timeouts(), b = score_tc_wait_timeouts(), c = attn_tc_wait_timeouts();
-  if (a < 0 || b < 0 || c < 0) return -1;
-  return a + b + c;
+  const int a = score_wait_timeouts(), b = score_tc_wait_timeouts(), c = attn_tc_wait_timeouts(),
+            d = paged_tc_wait_timeouts();
+  if (a < 0 || b < 0 || c < 0 || d < 0) return -1;
+  return a + b + c + d;
 }
 
 QSA_API qsa_status qsa_check_device_status(void* stream) {
@@ -140,19 +141,19 @@ QSA_API qsa_status qsa_check_device_status(void* stream) {
   std::lock_guard<std::mutex> lock(mu);
   const int w = qsa_wait_timeouts(), st = selftest_timeouts_take();
   const int bad_a = attn_bad_ids_take(), bad_t = attn_tc_bad_ids_take(), nan = select_nan_keys_take();
-  const int pages_a = paged_bad_pages_take(), pages_w = paged_append_bad_pages_take(), unserved = pages_unserved_take();
-  if (w < 0 || st < 0 || bad_a < 0 || bad_t < 0 || nan < 0 || pages_a < 0 || pages_w < 0 || unserved < 0)
+  const int pages_a = paged_bad_pages_take(), pages_t = paged_tc_bad_pages_take(), pages_w = paged_append_bad_pages_take(), unserved = pages_unserved_take();
+  if (w < 0 || st < 0 || bad_a < 0 || bad_t < 0 || nan < 0 || pages_a < 0 || pages_t < 0 || pages_w < 0 || unserved < 0)
     return fail(QSA_ERR_CUDA, "%s: the device counters could not be read", fn);
   const int waits = (w - seen_waits[dev]) + st, bad = bad_a + bad_t;
   seen_waits[dev] = w;
   if (waits > 0)
     return fail(QSA_ERR_TIMEOUT, "%s: %d device wait(s) gave up; %d out-of-range selected ids, %d NaN scores", fn,
                 waits, bad, nan);
-  if (pages_a + pages_w > 0 || unserved > 0)
+  if (pages_a + pages_t + pages_w > 0 || unserved > 0)
     return fail(QSA_ERR_DEVICE_CHECK,
                 "%s: %d page table entries outside the cache under visible or new tokens (skipped), %d page requests "
                 "not served; %d out-of-range selected ids, %d NaN scores",
-                fn, pages_a + pages_w, unserved, bad, nan);
+                fn, pages_a + pages_t + pages_w, unserved, bad, nan);
   if (bad > 0 || nan > 0)
     return fail(QSA_ERR_DEVICE_CHECK, "%s: %d out-of-range selected ids (skipped), %d NaN scores among the selection's candidates",
                 fn, bad, nan);

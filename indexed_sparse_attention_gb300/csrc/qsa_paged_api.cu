@@ -28,7 +28,7 @@ qsa_status check_cache(const qsa_paged_cache* c, const qsa_attn_config* cfg, con
       (c->page_tokens & (c->page_tokens - 1)) != 0)
     return fail(QSA_ERR_UNSUPPORTED, "%s: page_tokens=%d (a power of two in %d..%d)", fn, c->page_tokens,
                 QSA_MIN_PAGE_TOKENS, QSA_MAX_PAGE_TOKENS);
-  const int64_t es = (int64_t)dtype_size(cfg->kv_dtype), most = (int64_t)1 << 40;
+  const int64_t es = (int64_t)dtype_size(cfg->kv_dtype), most = (int64_t)1 << 38;   // a tensor map holds strides below 2^40 bytes
   if (c->tok_stride < cfg->head_dim || c->head_stride < cfg->head_dim || c->page_stride < cfg->head_dim ||
       c->tok_stride > most || c->head_stride > most || c->page_stride > most)
     return fail(QSA_ERR_INVALID_ARG, "%s: cache strides page=%lld head=%lld tok=%lld (each >= head_dim=%d)", fn,
@@ -59,15 +59,24 @@ qsa_status check_batch(const qsa_paged_batch* b, const char* fn) {
 
 // Kernel of a call and how it divides the work.
 struct Plan {
+  bool tensor_cores;
   int mt;     // entries of an item
   int grid;   // runs
 };
 
 Plan plan_attn(const qsa_paged_batch* b, const qsa_attn_config* cfg) {
-  (void)b;
   Plan pl;
-  pl.mt = 16;
-  pl.grid = 2 * device_sm_count();
+  pl.tensor_cores = cfg->kv_dtype == QSA_BF16;
+  if (pl.tensor_cores) {
+    // As many entries as a sequence has, up to the 128 rows of the MMA: Q's
+    // share of the shared memory goes to the ring.
+    const int64_t entries = (int64_t)b->max_rows * (cfg->n_q_heads / cfg->n_kv_heads);
+    pl.mt = (int)std::min<int64_t>(128, std::max<int64_t>(16, (entries + 15) / 16 * 16));
+    pl.grid = device_sm_count();
+  } else {
+    pl.mt = 16;
+    pl.grid = 2 * device_sm_count();
+  }
   if (cfg->n_splits > 0) pl.grid = std::min(pl.grid, cfg->n_splits);
   return pl;
 }
@@ -151,7 +160,8 @@ QSA_API qsa_status qsa_paged_attn(const qsa_paged_cache* cache, const qsa_paged_
   p.part_lse = reinterpret_cast<float*>(ws + lse_offset(pl));
   p.part_o = reinterpret_cast<float*>(ws + out_offset(pl));
   cudaStream_t st = as_stream(stream);
-  cudaError_t e = launch_paged_simt(p, cfg->kv_dtype, cfg->head_dim, pl.grid, st);
+  cudaError_t e = pl.tensor_cores ? launch_paged_tc(p, cfg->head_dim, pl.grid, st)
+                                  : launch_paged_simt(p, cfg->kv_dtype, cfg->head_dim, pl.grid, st);
   if (e == cudaSuccess) e = launch_paged_merge(p, cfg->head_dim, pl.grid, st);
   return e == cudaSuccess ? ok() : cuda_fail(e, fn);
 }

@@ -484,3 +484,11 @@ def test_a_serving_run(dtype, D, window, sinks):
     assert used.item() == len({int(p) for s in range(places) for p in pool.table[s, :-(-len(tokens[s]) // page)].tolist()})
     step([0, 1, 3, 4], [1, 1, 20, 2])
     assert qsa.check_device_status() == (0, "")
+
+
+def test_runs_of_many_windowed_items():
+    # Runs that hold several items of several tiles each, with and without first tokens apart from the window.
+    x = make_paged([900 + 37 * i for i in range(40)], [1] * 40, dtype="bf16", Hkv=2, G=2, page=32, seed=40)
+    for n in (3, 0):
+        check(x, window=600, sinks=4, n_splits=n)
+        check(x, window=300, n_splits=n)
