@@ -52,7 +52,7 @@ constexpr int kSlab = kKT * 128;              // bytes of 64 channels of a tile
 constexpr int kMaxSlabs = 14;
 constexpr int kCopyWarp = 8, kMmaWarp = 9, kQWarp = 10;
 constexpr int kThreads = 32 * 11;
-constexpr uint32_t kTmemCols = 512, kOCol = 256;
+constexpr uint32_t kTmemCols = 512;
 constexpr int kSmemLimit = 227 * 1024;
 constexpr float kMoveMax = 8.f;               // log2 of the weight at which the running maximum is moved
 
@@ -69,22 +69,24 @@ struct TcParams {
 };
 
 // Shared memory: this, then Q, then the ring (both on 1,024-byte boundaries).
-// A wait by parity tells a phase from its neighbours only: the barriers that
-// follow the tiles come in pairs, for even and odd tiles, so that a waiting
-// thread knows the phase before the awaited one to be over (tile j's logits
-// come after the product of tile j - 2).
+// A wait by parity tells a phase from its neighbours only, so a waiting thread
+// has to know the phase before the awaited one to be over.  pv_done comes in a
+// pair, for even and odd tiles: tile j's logits follow the output product of
+// tile j - NB or later ones, NB <= 3, so whoever has seen them may wait for the
+// product of tile j - 1, and after that for tile j's.
 struct Head {
   uint64_t full[kMaxSlabs], empty[kMaxSlabs];
-  uint64_t s_full[2], p_full[2], pv_done[2], o_free, q_full, q_free, mma_done;
+  uint64_t s_full[3], p_full[3], pv_done[2], m_done[2], o_free, q_full, q_free, mma_done;
   int64_t scan[kThreads / 32];
   Start start;
   uint32_t tmem;
   int abort;
   uint32_t bad[8];              // 16-token pieces of a tile that have no page
-  float stat[2][2][128];        // row maxima (and sums) of the two key halves
+  float m_run[128];             // the entries' running maxima
+  float sums[2][128];           // the two groups' sums of weights
 };
-static_assert(sizeof(Head) <= 3072, "shared memory head");
 constexpr int kHeadBytes = 3072;
+static_assert(sizeof(Head) <= kHeadBytes, "shared memory head");
 
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -103,6 +105,12 @@ __device__ __forceinline__ void tma_4d(void* dst, const CUtensorMap* map, int x,
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
 }
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+  return one != 0;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -115,26 +123,19 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 #define R8(a, i) "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3]), "=r"(a[i + 4]), "=r"(a[i + 5]), "=r"(a[i + 6]), "=r"(a[i + 7])
 #define S8(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3]), "r"(a[i + 4]), "r"(a[i + 5]), "r"(a[i + 6]), "r"(a[i + 7])
-// 64 consecutive columns of this thread's TMEM lane, waited for.
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, "
-      "%38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, "
-      "%60, %61, %62, %63}, [%64];\n"
-      "tcgen05.wait::ld.sync.aligned;\n"
-      : R8(r, 0), R8(r, 8), R8(r, 16), R8(r, 24), R8(r, 32), R8(r, 40), R8(r, 48), R8(r, 56)
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_ld32u(uint32_t taddr, uint32_t (&r)[32]) {
+#define U8(a, i) "+r"(a[i]), "+r"(a[i + 1]), "+r"(a[i + 2]), "+r"(a[i + 3]), "+r"(a[i + 4]), "+r"(a[i + 5]), "+r"(a[i + 6]), "+r"(a[i + 7])
+// 32 consecutive columns of this thread's TMEM lane; the values are there after
+// tmem_ld_wait of the same array.
+__device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
       "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
-      "tcgen05.wait::ld.sync.aligned;\n"
       : R8(r, 0), R8(r, 8), R8(r, 16), R8(r, 24)
       : "r"(taddr)
       : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n" : U8(r, 0), U8(r, 8), U8(r, 16), U8(r, 24) : : "memory");
 }
 // 32 consecutive columns, waited for.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -145,6 +146,36 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       S8(r, 8), S8(r, 16), S8(r, 24), "r"(taddr)
       : "memory");
 }
+// 16 consecutive columns; tmem_st_wait before others read them.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15};\n" ::S8(r, 0),
+      S8(r, 8), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+// Two binary32 values in a register pair, and arithmetic on both at once.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t r, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+#undef U8
 #undef R8
 #undef S8
 
@@ -163,9 +194,12 @@ __device__ __forceinline__ ItemRows item_rows(const PagedParams& p, const Cursor
   return r;
 }
 
-// Place of tile j's K and V (T tiles in all) in an item's order of copies and
-// products K0 K1 V0 K2 V1 ... V(T-1).
-__device__ __forceinline__ int place_v(int j, int T) { return j < T - 1 ? 2 * j + 2 : 2 * T - 1; }
+// Place of tile j's V among the copies (and products) of an item of T tiles,
+// K and V counted: K runs NB - 1 tiles ahead, K0 .. K(NB-2), K(NB-1), V0, K(NB), V1, ...
+template <int NB>
+__device__ __forceinline__ int place_v(int j, int T) {
+  return j + min(T, j + NB);
+}
 
 // A ring position: slab index and the parity of its use.
 struct Ring {
@@ -181,7 +215,10 @@ struct Ring {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_constant__ TcParams tp) {
-  constexpr int NS = D / 64;   // slabs of a tile
+  constexpr int NS = D / 64;             // slabs of a tile
+  constexpr int NB = D == 128 ? 3 : 2;   // buffers of logits in TMEM
+  constexpr uint32_t kOCol = NB * kKT;   // O behind them
+  static_assert(kOCol + D <= kTmemCols, "TMEM columns");
   const PagedParams& p = tp.p;
   extern __shared__ __align__(1024) uint8_t raw[];
   Head& h = *reinterpret_cast<Head*>(raw);
@@ -197,10 +234,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
       bar_init(&h.full[i], 1);
       bar_init(&h.empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 3; ++i) {
       bar_init(&h.s_full[i], 1);
-      bar_init(&h.p_full[i], soft_threads);
+      bar_init(&h.p_full[i], soft_threads / 2);
+    }
+    for (int i = 0; i < 2; ++i) {
       bar_init(&h.pv_done[i], 1);
+      bar_init(&h.m_done[i], soft_threads / 2);
     }
     bar_init(&h.o_free, soft_threads);
     bar_init(&h.q_full, 1);
@@ -225,11 +265,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
   } else if (warp == kCopyWarp) {
     // ------------------------------------------------------------ K and V
     const int box = min(1 << p.page_shift, kKT), n_box = kKT / box;
+    const bool leader = elect_one();
     Ring ring_at;
     int tj = 0;
-    for (bool more = true; more; more = c.next(p, p.mt)) {
+    for (bool more = true; more; more = __shfl_sync(0xffffffffu, (int)c.next(p, p.mt), 0) != 0) {
       const ItemRows ir = item_rows(p, c);
-      const int T = c.x1 - c.x;
+      const int T = __shfl_sync(0xffffffffu, c.x1 - c.x, 0);
       // Lane b: the page of the tile's b-th box (n_pages: nothing to read, or no page).
       auto look_up = [&](int j, bool& missing) {
         missing = false;
@@ -242,42 +283,55 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         missing = true;
         return p.n_pages;
       };
+      // One lane issues, with values that all lanes agree on (see the products below).
       auto copy = [&](const CUtensorMap* map, int j, int page) {
-        const int t = c.tiles.token(c.x + j) + lane * box;
+        const int slot_in_page = c.tiles.token(c.x + j) & ((1 << p.page_shift) - 1);
+#pragma unroll
         for (int s = 0; s < NS; ++s) {
-          if (lane == 0) {
-            if (ring_at.use > 0) bar_wait(&h.empty[ring_at.slot], (ring_at.use - 1) & 1, &g_timeouts, abrt);
-            bar_expect_tx(&h.full[ring_at.slot], kSlab);
+          uint64_t* full = &h.full[ring_at.slot];
+          if (ring_at.use > 0) bar_wait(&h.empty[ring_at.slot], (ring_at.use - 1) & 1, &g_timeouts, abrt);
+          __syncwarp();
+          if (leader) bar_expect_tx(full, kSlab);
+          uint8_t* dst = ring + ring_at.slot * kSlab;
+          for (int b = 0; b < n_box; ++b) {
+            const int to = __shfl_sync(0xffffffffu, page, b);
+            if (leader) tma_4d(dst + b * box * 128, map, s * 64, slot_in_page, c.head, to, full);
           }
           __syncwarp();
-          if (lane < n_box)
-            tma_4d(ring + ring_at.slot * kSlab + lane * box * 128, map, s * 64, t & ((1 << p.page_shift) - 1), c.head,
-                   page, &h.full[ring_at.slot]);
           ring_at.step(n_slabs);
         }
       };
+      auto announce = [&](int j, bool missing) {   // 16-token pieces of tile j without a page
+        const uint32_t bad =
+            __reduce_or_sync(0xffffffffu, missing ? ((1u << (box / 16)) - 1u) << (lane * (box / 16)) : 0u);
+        if (missing) atomicAdd(&g_bad_pages, 1);
+        if (leader) h.bad[(tj + j) & 7] = bad;
+      };
+      int pages[NB];   // of tiles j .. j + NB - 1
       bool missing;
-      int now = look_up(0, missing), next = p.n_pages;
-      for (int j = 0; j < T; ++j) {
-        if (j == 0) {
-          const uint32_t piece = missing ? ((1u << (box / 16)) - 1u) << (lane * (box / 16)) : 0u;
-          const uint32_t bad = __reduce_or_sync(0xffffffffu, piece);
-          if (missing) atomicAdd(&g_bad_pages, 1);
-          if (lane == 0) h.bad[tj & 7] = bad;
-          copy(&tp.k, 0, now);
+#pragma unroll
+      for (int i = 0; i < NB; ++i) pages[i] = p.n_pages;
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        if (i < T) pages[i] = look_up(i, missing);
+        if (i < NB - 1 && i < T) {
+          announce(i, missing);
+          copy(&tp.k, i, pages[i]);
         }
-        if (j + 1 < T) {
-          next = look_up(j + 1, missing);
-          const uint32_t piece = missing ? ((1u << (box / 16)) - 1u) << (lane * (box / 16)) : 0u;
-          const uint32_t bad = __reduce_or_sync(0xffffffffu, piece);
-          if (missing) atomicAdd(&g_bad_pages, 1);
-          if (lane == 0) h.bad[(tj + 1) & 7] = bad;
-          copy(&tp.k, j + 1, next);
-        }
-        copy(&tp.v, j, now);
-        now = next;
-        ++tj;
       }
+      for (int j = 0; j < T; ++j) {
+        if (j + NB - 1 < T) {
+          announce(j + NB - 1, missing);
+          copy(&tp.k, j + NB - 1, pages[NB - 1]);
+        }
+        int ahead = p.n_pages;
+        if (j + NB < T) ahead = look_up(j + NB, missing);   // in flight beside V's copies
+        copy(&tp.v, j, pages[0]);
+#pragma unroll
+        for (int i = 0; i + 1 < NB; ++i) pages[i] = pages[i + 1];
+        pages[NB - 1] = ahead;
+      }
+      tj += T;
     }
     // Every copy has landed before the CTA ends (after a wait that gave up too).
     if (lane < n_slabs) {
@@ -306,59 +360,78 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
-    if (lane == 0) {
-      Ring at;
-      int tj = 0, it = 0;
-      for (bool more = true; more; more = c.next(p, p.mt), ++it) {
-        const int T = c.x1 - c.x;
-        auto logits = [&](int j) {   // S = Q K_j^T
-          const uint32_t d = tmem + (uint32_t)((tj + j) & 1) * kKT;
-          for (int s = 0; s < NS; ++s) {
-            bar_wait(&h.full[at.slot], at.use & 1, &g_timeouts, abrt);
-            fence_after();
-            const uint8_t* k = ring + at.slot * kSlab;
+    // The whole warp walks through the tiles with values that are the same in
+    // all its lanes, and one lane issues: descriptors then stay in uniform
+    // registers.  (One lane that walks alone has to move each of them over:
+    // 115 cycles an MMA instead of the 32 and 64 that the products take.)
+    const bool leader = elect_one();
+    const uint64_t q_desc = desc_sw128(q_s, 16, 1024), k_desc = desc_sw128(ring, 16, 1024),
+                   v_desc = desc_sw128(ring, kSlab, 1024);
+    const uint32_t q_step = (uint32_t)q_slab >> 4;
+    Ring at;
+    int tj = 0, it = 0;
+    for (bool more = true; more; more = __shfl_sync(0xffffffffu, (int)c.next(p, p.mt), 0) != 0, ++it) {
+      const int T = __shfl_sync(0xffffffffu, c.x1 - c.x, 0);
+      auto logits = [&](int j) {   // S = Q K_j^T
+        const int buf = (tj + j) % NB;
+        const uint32_t d = tmem + (uint32_t)(buf * kKT);
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              mma_bf16(d, desc_sw128(q_s + s * q_slab + 32 * x, 16, 1024), desc_sw128(k + 32 * x, 16, 1024), kIdescS,
-                       (s | x) != 0 ? 1u : 0u);
-            commit(&h.empty[at.slot]);
-            at.step(n_slabs);
-          }
-          commit(&h.s_full[(tj + j) & 1]);
-          if (j == T - 1) commit(&h.q_free);
-        };
-        bar_wait(&h.q_full, (uint32_t)(it & 1), &g_timeouts, abrt);
-        fence_after();
-        logits(0);
-        for (int j = 0; j < T; ++j) {
-          if (j + 1 < T) logits(j + 1);
-          const int buf = (tj + j) & 1;
-          bar_wait(&h.p_full[buf], (uint32_t)(((tj + j) >> 1) & 1), &g_timeouts, abrt);
-          if (j == 0 && it > 0) bar_wait(&h.o_free, (uint32_t)((it - 1) & 1), &g_timeouts, abrt);
+        for (int s = 0; s < NS; ++s) {
+          bar_wait(&h.full[at.slot], at.use & 1, &g_timeouts, abrt);
           fence_after();
-          for (int s = 0; s < NS; ++s) {
-            bar_wait(&h.full[at.slot], at.use & 1, &g_timeouts, abrt);
-            fence_after();
-            const uint8_t* v = ring + at.slot * kSlab;
+          if (leader) {
+            const uint64_t k = k_desc + (uint32_t)(at.slot * (kSlab >> 4)), q = q_desc + s * q_step;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) mma_bf16(d, q + 2 * x, k + 2 * x, kIdescS, (s | x) != 0 ? 1u : 0u);
+            commit(&h.empty[at.slot]);
+            if (s == NS - 1) commit(&h.s_full[buf]);
+            if (s == NS - 1 && j == T - 1) commit(&h.q_free);
+          }
+          __syncwarp();
+          at.step(n_slabs);
+        }
+      };
+      bar_wait(&h.q_full, (uint32_t)(it & 1), &g_timeouts, abrt);
+      fence_after();
+      // Logits run NB - 1 tiles ahead of the output: tile j + NB - 1 takes the
+      // buffer whose weights, tile j - 1's, the product before it reads.
+#pragma unroll
+      for (int j = 0; j < NB - 1; ++j)
+        if (j < T) logits(j);
+      for (int j = 0; j < T; ++j) {
+        if (j + NB - 1 < T) logits(j + NB - 1);
+        const int buf = (tj + j) % NB;
+        bar_wait(&h.p_full[buf], (uint32_t)(((tj + j) / NB) & 1), &g_timeouts, abrt);
+        if (j == 0 && it > 0) bar_wait(&h.o_free, (uint32_t)((it - 1) & 1), &g_timeouts, abrt);
+        fence_after();
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+          bar_wait(&h.full[at.slot], at.use & 1, &g_timeouts, abrt);
+          fence_after();
+          if (leader) {
+            const uint64_t v = v_desc + (uint32_t)(at.slot * (kSlab >> 4));
 #pragma unroll
             for (int x = 0; x < kKT / 16; ++x)
-              mma_bf16_ts(tmem + kOCol + (uint32_t)(s * 64), tmem + (uint32_t)(buf * kKT + 8 * x),
-                          desc_sw128(v + x * 2048, kSlab, 1024), kIdescO, (j | x) != 0 ? 1u : 0u);
+              mma_bf16_ts(tmem + kOCol + (uint32_t)(s * 64), tmem + (uint32_t)(buf * kKT + 8 * x), v + 128 * x, kIdescO,
+                          (j | x) != 0 ? 1u : 0u);
             commit(&h.empty[at.slot]);
-            at.step(n_slabs);
+            if (s == NS - 1) commit(&h.pv_done[(tj + j) & 1]);
           }
-          commit(&h.pv_done[buf]);
+          __syncwarp();
+          at.step(n_slabs);
         }
-        tj += T;
       }
-      commit(&h.mma_done);   // every MMA has completed before TMEM is released
-      bar_wait(&h.mma_done, 0u, &g_timeouts);
+      tj += T;
     }
+    if (leader) commit(&h.mma_done);   // every MMA has completed before TMEM is released
+    __syncwarp();
+    bar_wait(&h.mma_done, 0u, &g_timeouts);
   } else if ((warp & 3) < quarters) {
     // ------------------------------------------------------------ softmax and output
-    const int half = warp >> 2, row = 32 * (warp & 3) + lane;
+    // Two groups of four warps take the tiles in turn: one group's exponentials
+    // run beside the other's maxima.  A thread owns one entry.
+    const int group = warp >> 2, row = 32 * (warp & 3) + lane;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const int stid = (half * quarters + (warp & 3)) * 32 + lane;   // among the softmax threads
     const float zc = p.scale * kLog2e, move = fminf(kMoveMax / zc, 1e30f);
     int tj = 0, tiles_before = 0;   // tiles done; tiles of K and V before this item in the ring's order
     for (bool more = true; more;) {
@@ -366,82 +439,120 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
       const int T = c.x1 - c.x;
       const bool mine = row < ir.nf;
       const int pos = ir.pos0 + (ir.f0 + min(row, ir.nf - 1)) / p.group;
-      const int low = p.window > 0 ? pos - p.window + 1 : INT32_MIN;   // first token of the row's window
+      const int low = p.window > 0 ? pos - p.window + 1 : 0;             // first token of the row's window
       const int dead = p.window > 0 ? ir.first - p.window : INT32_MIN;   // [n_sinks, dead]: no row's tokens
-      float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < T; ++j, ++tj) {
-        const int buf = tj & 1, t0 = c.tiles.token(c.x + j);
-        uint32_t sr[64];
-        bar_wait(&h.s_full[buf], (uint32_t)((tj >> 1) & 1), &g_timeouts, abrt);
+      float m = -INFINITY, l = 0.f;   // the maximum that this thread's sum l is relative to
+      for (int j = (tj ^ group) & 1; j < T; j += 2) {
+        const int g = tj + j, buf = g % NB, t0 = c.tiles.token(c.x + j);
+        const uint32_t s_col = lanes + (uint32_t)(buf * kKT);
+        bar_wait(&h.s_full[buf], (uint32_t)((g / NB) & 1), &g_timeouts, abrt);
         __syncwarp();
         fence_after();
-        tmem_ld64(lanes + (uint32_t)(buf * kKT + half * 64), sr);
-        const uint32_t bad = h.bad[tj & 7];
+        const uint32_t bad = h.bad[g & 7];
         const bool partly = bad != 0 || t0 + kKT - 1 > ir.first ||
                             (p.window > 0 && t0 <= ir.last - p.window && t0 + kKT > p.n_sinks);
-        if (!mine) {
-#pragma unroll
-          for (int i = 0; i < 64; ++i) sr[i] = 0xff800000u;   // -infinity
-        } else if (partly) {
-          const int tb = t0 + half * 64;
-#pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            const int t = tb + i;
-            const bool see = t <= pos && (t >= low || t < p.n_sinks) && !((bad >> (half * 4 + i / 16)) & 1u);
-            sr[i] = see ? sr[i] : 0xff800000u;
-          }
-        }
-        float mx = __uint_as_float(sr[0]);
-#pragma unroll
-        for (int i = 1; i < 64; ++i) mx = fmaxf(mx, __uint_as_float(sr[i]));
-        h.stat[buf][half][row] = mx;
-        named_sync(1, soft_threads);
-        mx = fmaxf(mx, h.stat[buf][half ^ 1][row]);
-        if (j == 0) {
-          m = mx;
-        } else {
-          const bool moves = mx > m + move;   // (from -infinity too)
-          if (__any_sync(0xffffffffu, moves)) {
-            const float alpha = moves ? ex2((m - mx) * zc) : 1.f;
-            if (moves) m = mx;
-            l *= alpha;
-            bar_wait(&h.pv_done[(tj - 1) & 1], (uint32_t)(((tj - 1) >> 1) & 1), &g_timeouts, abrt);
-            fence_after();
-            __syncwarp();
+        uint32_t xa[32], xb[32];
+        // What a row does not see becomes -infinity, in TMEM: the passes below
+        // stay short (with the masks unrolled into them they no longer fit the
+        // instruction cache and take four times as long).
+        if (partly || ir.nf < p.mt) {
 #pragma unroll 1
-            for (int s = 0; s < D / 64; ++s) {   // this half's channels, 32 at a time
-              uint32_t o[32];
-              const uint32_t at = lanes + kOCol + (uint32_t)(half * (D / 2) + s * 32);
-              tmem_ld32u(at, o);
+          for (int col = 0; col < kKT; col += 32) {
+            tmem_ld32_start(s_col + (uint32_t)col, xa);
+            tmem_ld_wait(xa);
+            const int t = t0 + col;
+            const uint32_t gone = bad >> (col / 16);
+            // Keys t .. t + 31: seen are those up to pos, from low on or among the first n_sinks.
+            const int hi = mine ? pos - t : -1, lo = low - t, sk = p.n_sinks - t;
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tmem_st32(at, o);
-            }
+            for (int i = 0; i < 32; ++i)
+              xa[i] = i <= hi && (i >= lo || i < sk) && !((gone >> (i / 16)) & 1u) ? xa[i] : 0xff800000u;
+            tmem_st32(s_col + (uint32_t)col, xa);
           }
         }
-        // Weights: in bf16 for the product, their sum in 32 bits.
-        const float shift = m == -INFINITY ? 0.f : -m * zc;
-        uint32_t pr[32];
-        float s0 = 0.f, s1 = 0.f;
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto take_max = [&](uint32_t(&x)[32]) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float a = ex2(fmaf(__uint_as_float(sr[2 * i]), zc, shift));
-          const float b = ex2(fmaf(__uint_as_float(sr[2 * i + 1]), zc, shift));
-          s0 += a;
-          s1 += b;
-          pr[i] = pack_bf16(a, b);
+          for (int i = 0; i < 32; i += 2)
+            m4[(i >> 1) & 3] = fmaxf(fmaxf(m4[(i >> 1) & 3], __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
+        };
+        tmem_ld32_start(s_col, xa);
+        tmem_ld_wait(xa);
+#pragma unroll 1
+        for (uint32_t col = 0; col < kKT; col += 64) {
+          tmem_ld32_start(s_col + col + 32, xb);
+          take_max(xa);
+          tmem_ld_wait(xb);
+          tmem_ld32_start(s_col + ((col + 64) & (kKT - 1)), xa);   // at the end the first ones again, for the weights
+          take_max(xb);
+          tmem_ld_wait(xa);
         }
-        l += s0 + s1;
+        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        // The running maximum after the tile before this one, then after this one.
+        if (g > 0) bar_wait(&h.m_done[group ^ 1], (uint32_t)(((g - 1) >> 1) & 1), &g_timeouts, abrt);
+        const float before = j == 0 ? -INFINITY : h.m_run[row];
+        const bool moves = j == 0 ? mx != -INFINITY : mx > before + move;
+        const float now = moves ? mx : before;
+        h.m_run[row] = now;
+        bar_arrive(&h.m_done[group]);
+        if (now != m) {
+          l *= ex2((m - now) * zc);
+          m = now;
+        }
+        if (j > 0 && __any_sync(0xffffffffu, moves)) {
+          const float alpha = moves ? ex2((before - now) * zc) : 1.f;
+          bar_wait(&h.pv_done[(g - 1) & 1], (uint32_t)(((g - 1) >> 1) & 1), &g_timeouts, abrt);
+          __syncwarp();
+          fence_after();
+#pragma unroll 1
+          for (int s = 0; s < D / 32; ++s) {
+            tmem_ld32_start(lanes + kOCol + (uint32_t)(32 * s), xb);
+            tmem_ld_wait(xb);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) xb[i] = __float_as_uint(__uint_as_float(xb[i]) * alpha);
+            tmem_st32(lanes + kOCol + (uint32_t)(32 * s), xb);
+          }
+        }
+        // Weights: in bf16 for the product, their sum in 32 bits.  32 logits
+        // become 16 columns of weights, always behind the logits still to be read.
+        const float shift = m == -INFINITY ? 0.f : -m * zc;
+        const uint64_t zc2 = pack2(zc, zc), shift2 = pack2(shift, shift);
+        uint64_t sum2[2] = {0ull, 0ull};
+        auto weigh = [&](uint32_t(&x)[32], uint32_t to) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float a, b;
+            unpack2(fma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), zc2, shift2), a, b);
+            a = ex2(a);
+            b = ex2(b);
+            sum2[i & 1] = add2(sum2[i & 1], pack2(a, b));
+            w[i] = pack_bf16(a, b);
+          }
+          tmem_st16(to, w);
+        };
         __syncwarp();
-        tmem_st32(lanes + (uint32_t)(buf * kKT + half * 32), pr);
+#pragma unroll 1
+        for (uint32_t col = 0; col < kKT; col += 64) {
+          tmem_ld32_start(s_col + col + 32, xb);
+          weigh(xa, s_col + col / 2);
+          tmem_ld_wait(xb);
+          if (col == 0) tmem_ld32_start(s_col + 64, xa);
+          weigh(xb, s_col + col / 2 + 16);
+          if (col == 0) tmem_ld_wait(xa);
+        }
+        float s0, s1;
+        unpack2(add2(sum2[0], sum2[1]), s0, s1);
+        l += s0 + s1;
+        tmem_st_wait();
         fence_before();
         // Tokens that no row sees: their V may be anything, and P = 0 there.
         if (t0 + kKT - 1 > ir.last || (p.window > 0 && max(t0, p.n_sinks) <= min(dead, t0 + kKT - 1))) {
-          const int v0 = (tiles_before + place_v(j, T)) * NS;
+          const int v0 = (tiles_before + place_v<NB>(j, T)) * NS;
           for (int s = 0; s < NS; ++s) {
             const int slot = (v0 + s) % n_slabs;
             bar_wait(&h.full[slot], (uint32_t)(((v0 + s) / n_slabs) & 1), &g_timeouts, abrt);
-            for (int tk = stid; tk < kKT; tk += soft_threads) {
+            for (int tk = row; tk < kKT; tk += 32 * quarters) {
               const int t = t0 + tk;
               if (t <= ir.last && (t > dead || t < p.n_sinks)) continue;
               uint4* v = reinterpret_cast<uint4*>(ring + slot * kSlab + tk * 128);
@@ -453,25 +564,32 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         }
         bar_arrive(&h.p_full[buf]);
       }
-      // The item's result, or this run's part of it.
-      float* sums = h.stat[tj & 1][0];
-      sums[half * 128 + row] = l;
+      tj += T;
+      // The item's result, or this run's part of it: both groups' sums, relative
+      // to the last maximum.
       named_sync(1, soft_threads);
-      l += sums[(half ^ 1) * 128 + row];
+      const float m_last = h.m_run[row];
+      if (m_last != m) l *= ex2((m - m_last) * zc);
+      m = m_last;
+      h.sums[group][row] = l;
       named_sync(1, soft_threads);
+      l += h.sums[group ^ 1][row];
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const bool whole = c.whole();
       const int64_t part = (int64_t)c.slot(blockIdx.x) * p.mt + row;
       const int r = (ir.f0 + row) / p.group;
       const int64_t entry = (int64_t)(c.s.row0 + r) * p.n_q_heads + c.head * p.group + (ir.f0 + row - r * p.group);
+      if (tj > 1) bar_wait(&h.pv_done[tj & 1], (uint32_t)(((tj - 2) >> 1) & 1), &g_timeouts, abrt);
       bar_wait(&h.pv_done[(tj - 1) & 1], (uint32_t)(((tj - 1) >> 1) & 1), &g_timeouts, abrt);
+      __syncwarp();
       fence_after();
 #pragma unroll 1
       for (int s = 0; s < D / 64; ++s) {
         uint32_t o[32];
-        const int d = half * (D / 2) + s * 32;
+        const int d = group * (D / 2) + s * 32;
         __syncwarp();
-        tmem_ld32u(lanes + kOCol + (uint32_t)d, o);
+        tmem_ld32_start(lanes + kOCol + (uint32_t)d, o);
+        tmem_ld_wait(o);
         if (!mine) continue;
         if (!whole || p.out_dtype == QSA_F32) {
           float4* to = reinterpret_cast<float4*>((whole ? static_cast<float*>(p.out) + entry * D : p.part_o + part * D) + d);
@@ -493,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
       }
       fence_before();
       bar_arrive(&h.o_free);
-      if (mine && half == 0) {
+      if (mine && group == 0) {
         const float lse2 = l > 0.f ? fmaf(m, zc, log2f(l)) : -INFINITY;
         if (!whole) p.part_lse[part] = lse2;
         else if (p.lse) p.lse[entry] = lse2 * kLn2;
@@ -501,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
       tiles_before += 2 * T;
       const Cursor<kKT> last = c;
       more = c.next(p, p.mt);
-      if (!more && stid == 0) describe_part(p, last, st, blockIdx.x);
+      if (!more && warp == 0 && lane == 0) describe_part(p, last, st, blockIdx.x);
     }
   }
   __syncwarp();
