@@ -27,7 +27,7 @@
 //
 // Roles: warps 0-7 softmax and output (warp w: entries 32 (w % 4) .., keys 64
 // (w / 4) ..; warps without entries idle), warp 8 copies K and V, warp 9
-// issues the MMAs, warp 10 loads Q.  Every wait gives up after about two
+// issues the MMAs, warps 10-11 load Q.  Every wait gives up after about two
 // seconds (counted; the CTA then runs to its end).
 #include <math.h>
 
@@ -50,8 +50,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kKT = 128;                      // keys of a tile
 constexpr int kSlab = kKT * 128;              // bytes of 64 channels of a tile
 constexpr int kMaxSlabs = 14;
-constexpr int kCopyWarp = 8, kMmaWarp = 9, kQWarp = 10;
-constexpr int kThreads = 32 * 11;
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kQWarp = 10, kQWarps = 2;
+constexpr int kThreads = 32 * 12;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSmemLimit = 227 * 1024;
 constexpr float kMoveMax = 8.f;               // log2 of the weight at which the running maximum is moved
@@ -104,6 +104,18 @@ __device__ __forceinline__ void tma_4d(void* dst, const CUtensorMap* map, int x,
 }
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
+}
+// 32 bytes, as one store where the address allows it (a whole sector: a thread
+// writes a row of its own), else as two.
+__device__ __forceinline__ void st_global32(void* to, const uint32_t* x) {
+  if ((reinterpret_cast<uintptr_t>(to) & 31u) == 0) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(to), "r"(x[0]), "r"(x[1]),
+                 "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(to)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+    static_cast<uint4*>(to)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+  }
 }
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
@@ -194,6 +206,9 @@ __device__ __forceinline__ ItemRows item_rows(const PagedParams& p, const Cursor
   return r;
 }
 
+// Bits 0 .. n - 1 (n of any sign and size).
+__device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+
 // Place of tile j's V among the copies (and products) of an item of T tiles,
 // K and V counted: K runs NB - 1 tiles ahead, K0 .. K(NB-2), K(NB-1), V0, K(NB), V1, ...
 template <int NB>
@@ -243,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
       bar_init(&h.m_done[i], soft_threads / 2);
     }
     bar_init(&h.o_free, soft_threads);
-    bar_init(&h.q_full, 1);
+    bar_init(&h.q_full, kQWarps);
     bar_init(&h.q_free, 1);
     bar_init(&h.mma_done, 1);
     h.abort = 0;
@@ -338,20 +353,30 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
       const uint32_t uses = ring_at.use + (lane < ring_at.slot ? 1u : 0u);
       if (uses > 0) bar_wait(&h.full[lane], (uses - 1) & 1, &g_timeouts);
     }
-  } else if (warp == kQWarp) {
+  } else if (warp >= kQWarp) {
     // ------------------------------------------------------------ Q
     int it = 0;
     for (bool more = true; more; more = c.next(p, p.mt), ++it) {
       const ItemRows ir = item_rows(p, c);
       if (it > 0) bar_wait(&h.q_free, (uint32_t)((it - 1) & 1), &g_timeouts, abrt);
-      constexpr int PER = D / 8;   // 16-byte pieces of an entry
+      constexpr int PER = D / 8;                     // 16-byte pieces of an entry
+      constexpr int kStep = kQWarps * 32 / PER;      // entries that the two warps copy together
       const int piece = lane % PER;
-      for (int f = lane / PER; f < p.mt; f += 32 / PER) {
+      int f = (warp - kQWarp) * (32 / PER) + lane / PER;
+      int row = (ir.f0 + f) / p.group, head = ir.f0 + f - row * p.group;
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
+                                 ((int64_t)c.s.row0 * p.n_q_heads + c.head * p.group) * D + piece * 8;
+      uint8_t* dst = q_s + (piece >> 3) * q_slab;
+#pragma unroll 4
+      for (; f < p.mt; f += kStep) {
         const bool ok = f < ir.nf;
-        const int row = (ir.f0 + f) / p.group;
-        const int64_t at = ok ? (int64_t)(c.s.row0 + row) * p.n_q_heads + c.head * p.group + (ir.f0 + f - row * p.group) : 0;
-        cp_async16(q_s + (piece >> 3) * q_slab + f * 128 + (((piece & 7) ^ (f & 7)) << 4),
-                   static_cast<const __nv_bfloat16*>(p.q) + at * D + piece * 8, ok);
+        const int64_t at = ok ? ((int64_t)row * p.n_q_heads + head) * D : 0;
+        cp_async16(dst + f * 128 + (((piece & 7) ^ (f & 7)) << 4), src + at, ok);
+        head += kStep;
+        while (head >= p.group) {
+          head -= p.group;
+          ++row;
+        }
       }
       cp_async_wait_all();
       fence_async_smem();
@@ -455,18 +480,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         // What a row does not see becomes -infinity, in TMEM: the passes below
         // stay short (with the masks unrolled into them they no longer fit the
         // instruction cache and take four times as long).
-        if (partly || ir.nf < p.mt) {
+        if (partly || ir.nf < 32 * quarters) {
 #pragma unroll 1
           for (int col = 0; col < kKT; col += 32) {
+            // Keys t .. t + 31: seen are those up to pos, from low on or among the first n_sinks.
+            const int t = t0 + col;
+            uint32_t see = below(pos + 1 - t) & (~below(low - t) | below(p.n_sinks - t));
+            see &= ~((((bad >> (col / 16)) & 1u) * 0xffffu) | (((bad >> (col / 16 + 1)) & 1u) * 0xffff0000u));
+            if (!mine) see = 0u;
+            if (__all_sync(0xffffffffu, see == 0xffffffffu)) continue;
             tmem_ld32_start(s_col + (uint32_t)col, xa);
             tmem_ld_wait(xa);
-            const int t = t0 + col;
-            const uint32_t gone = bad >> (col / 16);
-            // Keys t .. t + 31: seen are those up to pos, from low on or among the first n_sinks.
-            const int hi = mine ? pos - t : -1, lo = low - t, sk = p.n_sinks - t;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              xa[i] = i <= hi && (i >= lo || i < sk) && !((gone >> (i / 16)) & 1u) ? xa[i] : 0xff800000u;
+            for (int i = 0; i < 32; ++i) xa[i] = see & (1u << i) ? xa[i] : 0xff800000u;
             tmem_st32(s_col + (uint32_t)col, xa);
           }
         }
@@ -547,18 +573,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         tmem_st_wait();
         fence_before();
         // Tokens that no row sees: their V may be anything, and P = 0 there.
-        if (t0 + kKT - 1 > ir.last || (p.window > 0 && max(t0, p.n_sinks) <= min(dead, t0 + kKT - 1))) {
+        auto slot_of = [&](int t) { return min(max(t - t0, 0), kKT); };   // within the tile
+        const int cut = slot_of(ir.last + 1);                               // slots from here on,
+        const int gap0 = p.window > 0 ? slot_of(p.n_sinks) : 0, gap1 = p.window > 0 ? slot_of(dead + 1) : 0;
+        if (cut < kKT || gap0 < gap1) {                                     // and [gap0, gap1)
           const int v0 = (tiles_before + place_v<NB>(j, T)) * NS;
           for (int s = 0; s < NS; ++s) {
             const int slot = (v0 + s) % n_slabs;
             bar_wait(&h.full[slot], (uint32_t)(((v0 + s) / n_slabs) & 1), &g_timeouts, abrt);
-            for (int tk = row; tk < kKT; tk += 32 * quarters) {
-              const int t = t0 + tk;
-              if (t <= ir.last && (t > dead || t < p.n_sinks)) continue;
-              uint4* v = reinterpret_cast<uint4*>(ring + slot * kSlab + tk * 128);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
-            }
+            uint4* v = reinterpret_cast<uint4*>(ring + slot * kSlab);
+            for (int i = gap0 * 8 + row; i < gap1 * 8; i += 32 * quarters) v[i] = make_uint4(0u, 0u, 0u, 0u);
+            for (int i = cut * 8 + row; i < kKT * 8; i += 32 * quarters) v[i] = make_uint4(0u, 0u, 0u, 0u);
           }
           fence_async_smem();
         }
@@ -592,21 +617,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         tmem_ld_wait(o);
         if (!mine) continue;
         if (!whole || p.out_dtype == QSA_F32) {
-          float4* to = reinterpret_cast<float4*>((whole ? static_cast<float*>(p.out) + entry * D : p.part_o + part * D) + d);
+          float* to = (whole ? static_cast<float*>(p.out) + entry * D : p.part_o + part * D) + d;
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            to[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
-                                __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) st_global32(to + 8 * i, o + 8 * i);
         } else {
-          uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + entry * D + d);
+          __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + entry * D + d;
+          uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
+          for (int i = 0; i < 16; ++i)
+            w[i] = pack_bf16(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = pack_bf16(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
-            to[i] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+          for (int i = 0; i < 2; ++i) st_global32(to + 16 * i, w + 8 * i);
         }
       }
       fence_before();

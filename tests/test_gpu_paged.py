@@ -126,6 +126,25 @@ def test_divisions_agree_and_repeat(dtype):
         assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp8", "f32"])
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+def test_outputs_and_workspaces_on_16_bytes(dtype, out_dtype):
+    # Addresses that are multiples of 16 but not of 32.
+    x = make_paged([700, 9, 40], [4, 1, 40], dtype=dtype, D=128, page=64, seed=14)
+    cache, batch, q = x.device()
+    cfg = cache.config(24, out_dtype)
+    need = qsa.paged_attn_workspace_size(batch, cfg)
+    ws = torch.empty(need + 16, dtype=torch.uint8, device=dev())[16:]
+    es = torch.empty(0, dtype=out_dtype).element_size()
+    out = torch.empty(q.numel() + 16 // es, dtype=out_dtype, device=dev())[16 // es:].view(q.shape)
+    q2 = torch.empty(q.numel() + 16 // q.element_size(), dtype=q.dtype, device=dev())[16 // q.element_size():].view(q.shape)
+    q2.copy_(q)
+    lse = torch.empty(q.numel() // 128 + 1, device=dev())[1:].view(q.shape[:2])
+    assert out.data_ptr() % 32 == 16 and ws.data_ptr() % 32 == 16
+    qsa.paged_attn(cache, batch, q2, out, lse, workspace=ws, cfg=cfg)
+    assert_attended(out, lse, attend64(x))
+
+
 def test_many_sequences():
     # More sequences than a CTA has threads: the division takes its two passes.
     rng = random.Random(8)
