@@ -8,7 +8,7 @@
 //                     shared memory; two S buffers of 128 TMEM columns, so the
 //                     next tile's logits are computed while this one's softmax runs;
 //   P_j = exp(S_j - m), rounded to bf16, over S_j's own columns in TMEM;
-//   O  += P_j V_j     M = 128, N = 64 channels a slab, K = 128 keys, P from TMEM and
+//   O  += P_j V_j     M = 128, N = 128 channels a slab, K = 128 keys, P from TMEM and
 //                     V from shared memory (MN-major), O in 128 or 256 TMEM columns.
 // A thread owns one entry and half of the tile's keys, so row statistics need
 // one exchange with the thread of the other half and no shuffles.  The running
@@ -16,8 +16,8 @@
 // 2^8 in the weight: weights stay below 2^8, which the 32-bit sums and bf16's
 // exponent hold as well as 1, and the quotient by l is the same.
 //
-// K and V come through TMA, 64 channels x 128 tokens (16 KB) a slab, one tensor
-// copy for each page that a slab touches (pages of more than 128 tokens: one),
+// K and V come through TMA, 128 channels x 128 tokens (32 KB) a slab, one tensor
+// copy for each page and 64 channels (pages of 128 tokens and more: one a slab),
 // into a ring of as many slabs as fit beside Q.  Copies of pages without visible
 // tokens are aimed past the last page, which fills zeros without reading.
 // Slots of V that belong to no visible token are cleared before the product, as
@@ -48,8 +48,9 @@ using namespace tc;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kKT = 128;                      // keys of a tile
-constexpr int kSlab = kKT * 128;              // bytes of 64 channels of a tile
-constexpr int kMaxSlabs = 14;
+constexpr int kHalf = kKT * 128;              // bytes of 64 channels of a tile
+constexpr int kSlab = 2 * kHalf;              // bytes of 128 channels: what the ring holds
+constexpr int kMaxSlabs = 6;
 constexpr int kCopyWarp = 8, kMmaWarp = 9, kQWarp = 10, kQWarps = 2;
 constexpr int kThreads = 32 * 12;
 constexpr uint32_t kTmemCols = 512;
@@ -57,16 +58,27 @@ constexpr int kSmemLimit = 227 * 1024;
 constexpr float kMoveMax = 8.f;               // log2 of the weight at which the running maximum is moved
 
 constexpr uint32_t kIdescS = idesc_bf16(128, kKT, false, false);
-constexpr uint32_t kIdescO = idesc_bf16(128, 64, false, true);
+constexpr uint32_t kIdescO = idesc_bf16(128, 128, false, true);
 
 __device__ int g_timeouts;
 __device__ int g_bad_pages;
 
 struct TcParams {
-  CUtensorMap k, v;      // {D, page_tokens, Hkv, n_pages}, boxes of 64 channels x min(page_tokens, 128) tokens
+  // {64 channels, page_tokens, D / 64, Hkv, n_pages}: boxes of 64 channels x min(page_tokens, 128)
+  // tokens, of two channel blocks where the page has 128 tokens.
+  CUtensorMap k, v;
   PagedParams p;
   int32_t n_slabs;
 };
+
+// bar_wait with everything behind its first try out of line: the loops of the
+// roles stay small (they share the instruction caches).
+__device__ __noinline__ void wait_slow(uint64_t* b, uint32_t parity, int* abort) {
+  bar_wait(b, parity, &g_timeouts, abort);
+}
+__device__ __forceinline__ void wait(uint64_t* b, uint32_t parity, int* abort) {
+  if (!bar_try(b, parity)) wait_slow(b, parity, abort);
+}
 
 // Shared memory: this, then Q, then the ring (both on 1,024-byte boundaries).
 // A wait by parity tells a phase from its neighbours only, so a waiting thread
@@ -95,11 +107,13 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, 
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void tma_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
+// A box of a page's tokens: (token of the page, 64-channel block, KV head, page).
+__device__ __forceinline__ void tma_5d(void* dst, const CUtensorMap* map, int token, int block, int head, int page,
+                                       uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];\n" ::
-          "r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], "
+      "[%7];\n" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(token), "r"(block), "r"(head), "r"(page), "r"(smem_addr(bar))
       : "memory");
 }
 __device__ __forceinline__ void named_sync(int id, int threads) {
@@ -230,7 +244,7 @@ struct Ring {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_constant__ TcParams tp) {
-  constexpr int NS = D / 64;             // slabs of a tile
+  constexpr int NS = D / 128;            // slabs of a tile
   constexpr int NB = D == 128 ? 3 : 2;   // buffers of logits in TMEM
   constexpr uint32_t kOCol = NB * kKT;   // O behind them
   static_assert(kOCol + D <= kTmemCols, "TMEM columns");
@@ -239,10 +253,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
   Head& h = *reinterpret_cast<Head*>(raw);
   uint8_t* q_s = raw + kHeadBytes;
   const int q_slab = p.mt * 128, n_slabs = tp.n_slabs;
-  uint8_t* ring = q_s + NS * q_slab;
+  uint8_t* ring = q_s + 2 * NS * q_slab;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int quarters = (p.mt + 31) / 32, soft_threads = 64 * quarters;
-  volatile int* abrt = &h.abort;
+  int* abrt = &h.abort;
 
   if (tid == 0) {
     for (int i = 0; i < n_slabs; ++i) {
@@ -301,16 +315,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
       // One lane issues, with values that all lanes agree on (see the products below).
       auto copy = [&](const CUtensorMap* map, int j, int page) {
         const int slot_in_page = c.tiles.token(c.x + j) & ((1 << p.page_shift) - 1);
-#pragma unroll
+#pragma unroll 1
         for (int s = 0; s < NS; ++s) {
           uint64_t* full = &h.full[ring_at.slot];
-          if (ring_at.use > 0) bar_wait(&h.empty[ring_at.slot], (ring_at.use - 1) & 1, &g_timeouts, abrt);
+          if (ring_at.use > 0) wait(&h.empty[ring_at.slot], (ring_at.use - 1) & 1, abrt);
           __syncwarp();
-          if (leader) bar_expect_tx(full, kSlab);
           uint8_t* dst = ring + ring_at.slot * kSlab;
-          for (int b = 0; b < n_box; ++b) {
-            const int to = __shfl_sync(0xffffffffu, page, b);
-            if (leader) tma_4d(dst + b * box * 128, map, s * 64, slot_in_page, c.head, to, full);
+          if (leader) bar_expect_tx(full, kSlab);
+          if (n_box == 1) {   // both halves at once
+            const int to = __shfl_sync(0xffffffffu, page, 0);
+            if (leader) tma_5d(dst, map, slot_in_page, 2 * s, c.head, to, full);
+          } else {
+#pragma unroll 1
+            for (int b = 0; b < n_box; ++b) {
+              const int to = __shfl_sync(0xffffffffu, page, b);
+              if (leader) {
+                tma_5d(dst + b * box * 128, map, 0, 2 * s, c.head, to, full);
+                tma_5d(dst + kHalf + b * box * 128, map, 0, 2 * s + 1, c.head, to, full);
+              }
+            }
           }
           __syncwarp();
           ring_at.step(n_slabs);
@@ -358,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     int it = 0;
     for (bool more = true; more; more = c.next(p, p.mt), ++it) {
       const ItemRows ir = item_rows(p, c);
-      if (it > 0) bar_wait(&h.q_free, (uint32_t)((it - 1) & 1), &g_timeouts, abrt);
+      if (it > 0) wait(&h.q_free, (uint32_t)((it - 1) & 1), abrt);
       constexpr int PER = D / 8;                     // 16-byte pieces of an entry
       constexpr int kStep = kQWarps * 32 / PER;      // entries that the two warps copy together
       const int piece = lane % PER;
@@ -391,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     // 115 cycles an MMA instead of the 32 and 64 that the products take.)
     const bool leader = elect_one();
     const uint64_t q_desc = desc_sw128(q_s, 16, 1024), k_desc = desc_sw128(ring, 16, 1024),
-                   v_desc = desc_sw128(ring, kSlab, 1024);
+                   v_desc = desc_sw128(ring, kHalf, 1024);
     const uint32_t q_step = (uint32_t)q_slab >> 4;
     Ring at;
     int tj = 0, it = 0;
@@ -402,12 +425,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         const uint32_t d = tmem + (uint32_t)(buf * kKT);
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
-          bar_wait(&h.full[at.slot], at.use & 1, &g_timeouts, abrt);
+          wait(&h.full[at.slot], at.use & 1, abrt);
           fence_after();
           if (leader) {
-            const uint64_t k = k_desc + (uint32_t)(at.slot * (kSlab >> 4)), q = q_desc + s * q_step;
+            const uint64_t k = k_desc + (uint32_t)(at.slot * (kSlab >> 4)), q = q_desc + 2 * s * q_step;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) mma_bf16(d, q + 2 * x, k + 2 * x, kIdescS, (s | x) != 0 ? 1u : 0u);
+            for (int x = 0; x < 8; ++x)
+              mma_bf16(d, q + (x >> 2) * q_step + 2 * (x & 3), k + (x >> 2) * (kHalf >> 4) + 2 * (x & 3), kIdescS,
+                       (s | x) != 0 ? 1u : 0u);
             commit(&h.empty[at.slot]);
             if (s == NS - 1) commit(&h.s_full[buf]);
             if (s == NS - 1 && j == T - 1) commit(&h.q_free);
@@ -416,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
           at.step(n_slabs);
         }
       };
-      bar_wait(&h.q_full, (uint32_t)(it & 1), &g_timeouts, abrt);
+      wait(&h.q_full, (uint32_t)(it & 1), abrt);
       fence_after();
       // Logits run NB - 1 tiles ahead of the output: tile j + NB - 1 takes the
       // buffer whose weights, tile j - 1's, the product before it reads.
@@ -426,18 +451,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
       for (int j = 0; j < T; ++j) {
         if (j + NB - 1 < T) logits(j + NB - 1);
         const int buf = (tj + j) % NB;
-        bar_wait(&h.p_full[buf], (uint32_t)(((tj + j) / NB) & 1), &g_timeouts, abrt);
-        if (j == 0 && it > 0) bar_wait(&h.o_free, (uint32_t)((it - 1) & 1), &g_timeouts, abrt);
+        wait(&h.p_full[buf], (uint32_t)(((tj + j) / NB) & 1), abrt);
+        if (j == 0 && it > 0) wait(&h.o_free, (uint32_t)((it - 1) & 1), abrt);
         fence_after();
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
-          bar_wait(&h.full[at.slot], at.use & 1, &g_timeouts, abrt);
+          wait(&h.full[at.slot], at.use & 1, abrt);
           fence_after();
           if (leader) {
             const uint64_t v = v_desc + (uint32_t)(at.slot * (kSlab >> 4));
 #pragma unroll
             for (int x = 0; x < kKT / 16; ++x)
-              mma_bf16_ts(tmem + kOCol + (uint32_t)(s * 64), tmem + (uint32_t)(buf * kKT + 8 * x), v + 128 * x, kIdescO,
+              mma_bf16_ts(tmem + kOCol + (uint32_t)(s * 128), tmem + (uint32_t)(buf * kKT + 8 * x), v + 128 * x, kIdescO,
                           (j | x) != 0 ? 1u : 0u);
             commit(&h.empty[at.slot]);
             if (s == NS - 1) commit(&h.pv_done[(tj + j) & 1]);
@@ -470,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
       for (int j = (tj ^ group) & 1; j < T; j += 2) {
         const int g = tj + j, buf = g % NB, t0 = c.tiles.token(c.x + j);
         const uint32_t s_col = lanes + (uint32_t)(buf * kKT);
-        bar_wait(&h.s_full[buf], (uint32_t)((g / NB) & 1), &g_timeouts, abrt);
+        wait(&h.s_full[buf], (uint32_t)((g / NB) & 1), abrt);
         __syncwarp();
         fence_after();
         const uint32_t bad = h.bad[g & 7];
@@ -515,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         }
         const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         // The running maximum after the tile before this one, then after this one.
-        if (g > 0) bar_wait(&h.m_done[group ^ 1], (uint32_t)(((g - 1) >> 1) & 1), &g_timeouts, abrt);
+        if (g > 0) wait(&h.m_done[group ^ 1], (uint32_t)(((g - 1) >> 1) & 1), abrt);
         const float before = j == 0 ? -INFINITY : h.m_run[row];
         const bool moves = j == 0 ? mx != -INFINITY : mx > before + move;
         const float now = moves ? mx : before;
@@ -527,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         }
         if (j > 0 && __any_sync(0xffffffffu, moves)) {
           const float alpha = moves ? ex2((before - now) * zc) : 1.f;
-          bar_wait(&h.pv_done[(g - 1) & 1], (uint32_t)(((g - 1) >> 1) & 1), &g_timeouts, abrt);
+          wait(&h.pv_done[(g - 1) & 1], (uint32_t)(((g - 1) >> 1) & 1), abrt);
           __syncwarp();
           fence_after();
 #pragma unroll 1
@@ -580,10 +605,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
           const int v0 = (tiles_before + place_v<NB>(j, T)) * NS;
           for (int s = 0; s < NS; ++s) {
             const int slot = (v0 + s) % n_slabs;
-            bar_wait(&h.full[slot], (uint32_t)(((v0 + s) / n_slabs) & 1), &g_timeouts, abrt);
-            uint4* v = reinterpret_cast<uint4*>(ring + slot * kSlab);
-            for (int i = gap0 * 8 + row; i < gap1 * 8; i += 32 * quarters) v[i] = make_uint4(0u, 0u, 0u, 0u);
-            for (int i = cut * 8 + row; i < kKT * 8; i += 32 * quarters) v[i] = make_uint4(0u, 0u, 0u, 0u);
+            wait(&h.full[slot], (uint32_t)(((v0 + s) / n_slabs) & 1), abrt);
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+              uint4* v = reinterpret_cast<uint4*>(ring + slot * kSlab + half * kHalf);
+#pragma unroll 1
+              for (int i = gap0 * 8 + row; i < gap1 * 8; i += 32 * quarters) v[i] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+              for (int i = cut * 8 + row; i < kKT * 8; i += 32 * quarters) v[i] = make_uint4(0u, 0u, 0u, 0u);
+            }
           }
           fence_async_smem();
         }
@@ -604,8 +634,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
       const int64_t part = (int64_t)c.slot(blockIdx.x) * p.mt + row;
       const int r = (ir.f0 + row) / p.group;
       const int64_t entry = (int64_t)(c.s.row0 + r) * p.n_q_heads + c.head * p.group + (ir.f0 + row - r * p.group);
-      if (tj > 1) bar_wait(&h.pv_done[tj & 1], (uint32_t)(((tj - 2) >> 1) & 1), &g_timeouts, abrt);
-      bar_wait(&h.pv_done[(tj - 1) & 1], (uint32_t)(((tj - 1) >> 1) & 1), &g_timeouts, abrt);
+      if (tj > 1) wait(&h.pv_done[tj & 1], (uint32_t)(((tj - 2) >> 1) & 1), abrt);
+      wait(&h.pv_done[(tj - 1) & 1], (uint32_t)(((tj - 1) >> 1) & 1), abrt);
       __syncwarp();
       fence_after();
 #pragma unroll 1
@@ -671,12 +701,12 @@ bool encode_pages(CUtensorMap* map, const void* base, const PagedParams& p, int 
   PFN_cuTensorMapEncodeTiled_v12000 f = encoder();
   if (!f) return false;
   const cuuint64_t page = (cuuint64_t)1 << p.page_shift;
-  const cuuint64_t dims[4] = {(cuuint64_t)head_dim, page, (cuuint64_t)p.n_kv_heads, (cuuint64_t)p.n_pages};
-  const cuuint64_t strides[3] = {(cuuint64_t)p.tok_stride * 2, (cuuint64_t)p.head_stride * 2,
+  const cuuint64_t dims[5] = {64, page, (cuuint64_t)head_dim / 64, (cuuint64_t)p.n_kv_heads, (cuuint64_t)p.n_pages};
+  const cuuint64_t strides[4] = {(cuuint64_t)p.tok_stride * 2, 128, (cuuint64_t)p.head_stride * 2,
                                  (cuuint64_t)p.page_stride * 2};
-  const cuuint32_t box[4] = {64, (cuuint32_t)(page < kKT ? page : kKT), 1, 1};
-  const cuuint32_t step[4] = {1, 1, 1, 1};
-  return f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, step,
+  const cuuint32_t box[5] = {64, (cuuint32_t)(page < kKT ? page : kKT), page < kKT ? 1u : 2u, 1, 1};
+  const cuuint32_t step[5] = {1, 1, 1, 1, 1};
+  return f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, step,
            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
