@@ -113,8 +113,8 @@ size_t pages_workspace_bytes(const qsa_page_pool& pool);
 int pages_unserved_take();
 
 cudaError_t launch_paged_simt(const PagedParams& p, qsa_dtype kv_dtype, int head_dim, int grid, cudaStream_t st);
-// On the tensor cores (qsa_paged_tc.cu): bf16 caches.
-cudaError_t launch_paged_tc(const PagedParams& p, int head_dim, int grid, cudaStream_t st);
+// On the tensor cores (qsa_paged_tc.cu): bf16 and fp8 caches.
+cudaError_t launch_paged_tc(const PagedParams& p, qsa_dtype kv_dtype, int head_dim, int grid, cudaStream_t st);
 int paged_tc_bad_pages_take();
 int paged_tc_wait_timeouts();
 cudaError_t launch_paged_merge(const PagedParams& p, int head_dim, int grid, cudaStream_t st);

@@ -66,7 +66,7 @@ struct Plan {
 
 Plan plan_attn(const qsa_paged_batch* b, const qsa_attn_config* cfg) {
   Plan pl;
-  pl.tensor_cores = cfg->kv_dtype == QSA_BF16;
+  pl.tensor_cores = cfg->kv_dtype != QSA_F32;
   if (pl.tensor_cores) {
     // As many entries as a sequence has, up to the 128 rows of the MMA: Q's
     // share of the shared memory goes to the ring.
@@ -160,7 +160,7 @@ QSA_API qsa_status qsa_paged_attn(const qsa_paged_cache* cache, const qsa_paged_
   p.part_lse = reinterpret_cast<float*>(ws + lse_offset(pl));
   p.part_o = reinterpret_cast<float*>(ws + out_offset(pl));
   cudaStream_t st = as_stream(stream);
-  cudaError_t e = pl.tensor_cores ? launch_paged_tc(p, cfg->head_dim, pl.grid, st)
+  cudaError_t e = pl.tensor_cores ? launch_paged_tc(p, cfg->kv_dtype, cfg->head_dim, pl.grid, st)
                                   : launch_paged_simt(p, cfg->kv_dtype, cfg->head_dim, pl.grid, st);
   if (e == cudaSuccess) e = launch_paged_merge(p, cfg->head_dim, pl.grid, st);
   return e == cudaSuccess ? ok() : cuda_fail(e, fn);

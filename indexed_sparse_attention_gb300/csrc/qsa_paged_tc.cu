@@ -31,10 +31,13 @@
 // seconds (counted; the CTA then runs to its end).
 #include <math.h>
 
+#include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <mutex>
 
+#include "qsa_attn_common.cuh"
 #include "qsa_paged.cuh"
 #include "qsa_tc.cuh"
 
@@ -51,8 +54,10 @@ constexpr int kKT = 128;                      // keys of a tile
 constexpr int kHalf = kKT * 128;              // bytes of 64 channels of a tile
 constexpr int kSlab = 2 * kHalf;              // bytes of 128 channels: what the ring holds
 constexpr int kMaxSlabs = 6;
-constexpr int kCopyWarp = 8, kMmaWarp = 9, kQWarp = 10, kQWarps = 2;
-constexpr int kThreads = 32 * 12;
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kQWarp = 10, kQWarps = 2, kCodeWarp = 12, kCodeWarps = 4;
+__host__ __device__ constexpr int threads_of(bool f8) { return 32 * (f8 ? kCodeWarp + kCodeWarps : kCodeWarp); }
+constexpr int kCodeSlab = kKT * 128;          // bytes of the codes of a slab (fp8 caches)
+constexpr int kMaxCodeSlabs = 8;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSmemLimit = 227 * 1024;
 constexpr float kMoveMax = 8.f;               // log2 of the weight at which the running maximum is moved
@@ -69,6 +74,7 @@ struct TcParams {
   CUtensorMap k, v;
   PagedParams p;
   int32_t n_slabs;
+  int32_t n_code_slabs;   // fp8 caches: the ring of codes behind the ring of slabs
 };
 
 // bar_wait with everything behind its first try out of line: the loops of the
@@ -89,7 +95,8 @@ __device__ __forceinline__ void wait(uint64_t* b, uint32_t parity, int* abort) {
 struct Head {
   uint64_t full[kMaxSlabs], empty[kMaxSlabs];
   uint64_t s_full[3], p_full[3], pv_done[2], m_done[2], o_free, q_full, q_free, mma_done;
-  int64_t scan[kThreads / 32];
+  uint64_t code_full[kMaxCodeSlabs], code_empty[kMaxCodeSlabs];
+  int64_t scan[16];
   Start start;
   uint32_t tmem;
   int abort;
@@ -98,6 +105,11 @@ struct Head {
   float sums[2][128];           // the two groups' sums of weights
 };
 constexpr int kHeadBytes = 3072;
+// fp8 caches: scales of the tiles in flight, behind the head.
+struct Scales {
+  float k[4][kKT];   // times the logit scale and log2(e)
+  float v[4][kKT];
+};
 static_assert(sizeof(Head) <= kHeadBytes, "shared memory head");
 
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -114,6 +126,13 @@ __device__ __forceinline__ void tma_5d(void* dst, const CUtensorMap* map, int to
       "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], "
       "[%7];\n" ::"r"(smem_addr(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(token), "r"(block), "r"(head), "r"(page), "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];\n" ::
+          "r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
       : "memory");
 }
 __device__ __forceinline__ void named_sync(int id, int threads) {
@@ -196,6 +215,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -242,8 +266,8 @@ struct Ring {
   }
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_constant__ TcParams tp) {
+template <int D, bool F8>
+__global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __grid_constant__ TcParams tp) {
   constexpr int NS = D / 128;            // slabs of a tile
   constexpr int NB = D == 128 ? 3 : 2;   // buffers of logits in TMEM
   constexpr uint32_t kOCol = NB * kKT;   // O behind them
@@ -251,17 +275,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
   const PagedParams& p = tp.p;
   extern __shared__ __align__(1024) uint8_t raw[];
   Head& h = *reinterpret_cast<Head*>(raw);
-  uint8_t* q_s = raw + kHeadBytes;
+  Scales& sc = *reinterpret_cast<Scales*>(raw + kHeadBytes);
+  uint8_t* q_s = raw + kHeadBytes + (F8 ? sizeof(Scales) : 0);
   const int q_slab = p.mt * 128, n_slabs = tp.n_slabs;
   uint8_t* ring = q_s + 2 * NS * q_slab;
+  uint8_t* codes = ring + n_slabs * kSlab;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int quarters = (p.mt + 31) / 32, soft_threads = 64 * quarters;
   int* abrt = &h.abort;
 
   if (tid == 0) {
     for (int i = 0; i < n_slabs; ++i) {
-      bar_init(&h.full[i], 1);
+      bar_init(&h.full[i], F8 ? kCodeWarps : 1);
       bar_init(&h.empty[i], 1);
+    }
+    for (int i = 0; F8 && i < tp.n_code_slabs; ++i) {
+      bar_init(&h.code_full[i], 1);
+      bar_init(&h.code_empty[i], kCodeWarps);
     }
     for (int i = 0; i < 3; ++i) {
       bar_init(&h.s_full[i], 1);
@@ -285,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
   const uint32_t tmem = h.tmem;
   grid_dependency_wait();
   grid_dependency_release();
-  const Start st = find_run<kThreads, kKT>(p, p.mt, blockIdx.x, gridDim.x, h.scan, &h.start);
+  const Start st = find_run<threads_of(F8), kKT>(p, p.mt, blockIdx.x, gridDim.x, h.scan, &h.start);
   Cursor<kKT> c;
   c.begin(p, p.mt, st);
 
@@ -295,6 +325,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     // ------------------------------------------------------------ K and V
     const int box = min(1 << p.page_shift, kKT), n_box = kKT / box;
     const bool leader = elect_one();
+    // bf16: into the ring of operands; fp8: codes into their own ring.
+    uint64_t* fulls = F8 ? h.code_full : h.full;
+    uint64_t* empties = F8 ? h.code_empty : h.empty;
+    uint8_t* const to_ring = F8 ? codes : ring;
+    const int n_ring = F8 ? tp.n_code_slabs : n_slabs;
     Ring ring_at;
     int tj = 0;
     for (bool more = true; more; more = __shfl_sync(0xffffffffu, (int)c.next(p, p.mt), 0) != 0) {
@@ -317,26 +352,36 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         const int slot_in_page = c.tiles.token(c.x + j) & ((1 << p.page_shift) - 1);
 #pragma unroll 1
         for (int s = 0; s < NS; ++s) {
-          uint64_t* full = &h.full[ring_at.slot];
-          if (ring_at.use > 0) wait(&h.empty[ring_at.slot], (ring_at.use - 1) & 1, abrt);
+          uint64_t* full = fulls + ring_at.slot;
+          if (ring_at.use > 0) wait(empties + ring_at.slot, (ring_at.use - 1) & 1, abrt);
           __syncwarp();
-          uint8_t* dst = ring + ring_at.slot * kSlab;
-          if (leader) bar_expect_tx(full, kSlab);
-          if (n_box == 1) {   // both halves at once
-            const int to = __shfl_sync(0xffffffffu, page, 0);
-            if (leader) tma_5d(dst, map, slot_in_page, 2 * s, c.head, to, full);
-          } else {
+          if constexpr (F8) {
+            uint8_t* dst = to_ring + ring_at.slot * kCodeSlab;
+            if (leader) bar_expect_tx(full, kCodeSlab);
 #pragma unroll 1
             for (int b = 0; b < n_box; ++b) {
               const int to = __shfl_sync(0xffffffffu, page, b);
-              if (leader) {
-                tma_5d(dst + b * box * 128, map, 0, 2 * s, c.head, to, full);
-                tma_5d(dst + kHalf + b * box * 128, map, 0, 2 * s + 1, c.head, to, full);
+              if (leader) tma_4d(dst + b * box * 128, map, 128 * s, slot_in_page, c.head, to, full);
+            }
+          } else {
+            uint8_t* dst = to_ring + ring_at.slot * kSlab;
+            if (leader) bar_expect_tx(full, kSlab);
+            if (n_box == 1) {   // both halves at once
+              const int to = __shfl_sync(0xffffffffu, page, 0);
+              if (leader) tma_5d(dst, map, slot_in_page, 2 * s, c.head, to, full);
+            } else {
+#pragma unroll 1
+              for (int b = 0; b < n_box; ++b) {
+                const int to = __shfl_sync(0xffffffffu, page, b);
+                if (leader) {
+                  tma_5d(dst + b * box * 128, map, 0, 2 * s, c.head, to, full);
+                  tma_5d(dst + kHalf + b * box * 128, map, 0, 2 * s + 1, c.head, to, full);
+                }
               }
             }
           }
           __syncwarp();
-          ring_at.step(n_slabs);
+          ring_at.step(n_ring);
         }
       };
       auto announce = [&](int j, bool missing) {   // 16-token pieces of tile j without a page
@@ -372,9 +417,99 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
       tj += T;
     }
     // Every copy has landed before the CTA ends (after a wait that gave up too).
-    if (lane < n_slabs) {
+    if (lane < n_ring) {
       const uint32_t uses = ring_at.use + (lane < ring_at.slot ? 1u : 0u);
-      if (uses > 0) bar_wait(&h.full[lane], (uses - 1) & 1, &g_timeouts);
+      if (uses > 0) bar_wait(fulls + lane, (uses - 1) & 1, &g_timeouts);
+    }
+  } else if (F8 && warp >= kCodeWarp) {
+    // ------------------------------------------------------------ codes to bf16
+    // A slab's codes, 16 a thread at a time, to the layout the products read;
+    // exact.  Tokens that no row sees become zeros, whatever their codes and
+    // scales.  Thread i also keeps token i's scales, whose page it looks up two
+    // tiles ahead and loads one tile ahead.
+    const int ct = tid - 32 * kCodeWarp;
+    const float zs = p.scale * kLog2e;
+    Ring from, to;
+    int tj = 0;
+    for (bool more = true; more; more = c.next(p, p.mt)) {
+      const ItemRows ir = item_rows(p, c);
+      const int T = c.x1 - c.x;
+      auto visible = [&](int t) {
+        return t <= ir.last && (p.window == 0 || t > ir.first - p.window || t < p.n_sinks);
+      };
+      auto look_up = [&](int j) {   // the page of the thread's token of tile j, -1: none
+        const int t = c.tiles.token(c.x + j) + ct;
+        int32_t page = -1;
+        return j < T && visible(t) && page_of(p, c.seq, t, page) ? page : -1;
+      };
+      auto load = [&](int j, int page) {
+        const int slot = (c.tiles.token(c.x + j) + ct) & ((1 << p.page_shift) - 1);
+        return page < 0 ? 0x00003c00u   // K scale 1, V scale 0
+                        : __ldg(reinterpret_cast<const uint32_t*>(
+                              p.kv_scale + 4 * (page * p.s_page_stride + c.head * p.s_head_stride + slot * p.s_tok_stride)));
+      };
+      auto convert = [&](int j) {
+        const int t0 = c.tiles.token(c.x + j);
+        // Tokens [0, cut) of the tile less [gap0, gap1) are seen by some row.
+        auto slot_of = [&](int t) { return min(max(t - t0, 0), kKT); };
+        const int cut = slot_of(ir.last + 1);
+        const int gap0 = p.window > 0 ? slot_of(p.n_sinks) : 0;
+        const int gap1 = p.window > 0 ? slot_of(ir.first - p.window + 1) : 0;
+#pragma unroll 1
+        for (int s = 0; s < NS; ++s) {
+          wait(&h.code_full[from.slot], from.use & 1, abrt);
+          if (to.use > 0) wait(&h.empty[to.slot], (to.use - 1) & 1, abrt);
+          const uint8_t* src = codes + from.slot * kCodeSlab;
+          uint8_t* dst = ring + to.slot * kSlab;
+          const int piece = ct & 7;   // 16 channels of a token
+#pragma unroll 4
+          for (int tk = ct >> 3; tk < kKT; tk += 4 * kCodeWarps) {
+            uint4 x = *reinterpret_cast<const uint4*>(src + tk * 128 + piece * 16);
+            if (tk >= cut || (tk >= gap0 && tk < gap1)) x = make_uint4(0u, 0u, 0u, 0u);
+            uint4 lo, hi;
+            lo.x = attn::e4m3x2_to_bf16x2(x.x & 0xffffu);
+            lo.y = attn::e4m3x2_to_bf16x2(x.x >> 16);
+            lo.z = attn::e4m3x2_to_bf16x2(x.y & 0xffffu);
+            lo.w = attn::e4m3x2_to_bf16x2(x.y >> 16);
+            hi.x = attn::e4m3x2_to_bf16x2(x.z & 0xffffu);
+            hi.y = attn::e4m3x2_to_bf16x2(x.z >> 16);
+            hi.z = attn::e4m3x2_to_bf16x2(x.w & 0xffffu);
+            hi.w = attn::e4m3x2_to_bf16x2(x.w >> 16);
+            // Pieces 4-7 go to the slab's second half and write their second
+            // chunk first: the eight lanes of a token then write all 32 banks.
+            uint8_t* row = dst + (piece >> 2) * kHalf + tk * 128;
+            const int c0 = 2 * (piece & 3), swap = piece >> 2;
+            *reinterpret_cast<uint4*>(row + (((c0 + swap) ^ (tk & 7)) << 4)) = swap ? hi : lo;
+            *reinterpret_cast<uint4*>(row + (((c0 + 1 - swap) ^ (tk & 7)) << 4)) = swap ? lo : hi;
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            bar_arrive(&h.full[to.slot]);
+            bar_arrive(&h.code_empty[from.slot]);
+          }
+          from.step(tp.n_code_slabs);
+          to.step(n_slabs);
+        }
+      };
+      int page = look_up(0);
+      uint32_t record = load(0, page);
+      page = look_up(1);
+      auto keys = [&](int j) {   // scales and K of tile j
+        const __half2 s = *reinterpret_cast<const __half2*>(&record);
+        // (At least 1e-30: minus infinity times it stays minus infinity.)
+        sc.k[(tj + j) & 3][ct] = fmaxf(__low2float(s) * zs, 1e-30f);
+        sc.v[(tj + j) & 3][ct] = __high2float(s);
+        record = load(j + 1, page);
+        page = look_up(j + 2);
+        convert(j);
+      };
+#pragma unroll 1
+      for (int j = 0; j < T + NB - 1; ++j) {
+        if (j < T) keys(j);
+        if (j >= NB - 1) convert(j - (NB - 1));
+      }
+      tj += T;
     }
   } else if (warp >= kQWarp) {
     // ------------------------------------------------------------ Q
@@ -482,7 +617,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     // run beside the other's maxima.  A thread owns one entry.
     const int group = warp >> 2, row = 32 * (warp & 3) + lane;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const float zc = p.scale * kLog2e, move = fminf(kMoveMax / zc, 1e30f);
+    // Logits to base 2; the scales of an fp8 cache's keys hold the factor already.
+    const float zc = F8 ? 1.f : p.scale * kLog2e, move = fminf(kMoveMax / zc, 1e30f);
     int tj = 0, tiles_before = 0;   // tiles done; tiles of K and V before this item in the ring's order
     for (bool more = true; more;) {
       const ItemRows ir = item_rows(p, c);
@@ -522,7 +658,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
           }
         }
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        auto take_max = [&](uint32_t(&x)[32]) {
+        const float* ks = F8 ? sc.k[g & 3] : nullptr;
+        const float* vs = F8 ? sc.v[g & 3] : nullptr;
+        auto take_max = [&](uint32_t(&x)[32], uint32_t col) {
+          if constexpr (F8) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(ks + col + i);
+              x[i] = __float_as_uint(__uint_as_float(x[i]) * f.x);
+              x[i + 1] = __float_as_uint(__uint_as_float(x[i + 1]) * f.y);
+              x[i + 2] = __float_as_uint(__uint_as_float(x[i + 2]) * f.z);
+              x[i + 3] = __float_as_uint(__uint_as_float(x[i + 3]) * f.w);
+            }
+          }
 #pragma unroll
           for (int i = 0; i < 32; i += 2)
             m4[(i >> 1) & 3] = fmaxf(fmaxf(m4[(i >> 1) & 3], __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
@@ -532,10 +680,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
 #pragma unroll 1
         for (uint32_t col = 0; col < kKT; col += 64) {
           tmem_ld32_start(s_col + col + 32, xb);
-          take_max(xa);
+          take_max(xa, col);
           tmem_ld_wait(xb);
           tmem_ld32_start(s_col + ((col + 64) & (kKT - 1)), xa);   // at the end the first ones again, for the weights
-          take_max(xb);
+          take_max(xb, col + 32);
           tmem_ld_wait(xa);
         }
         const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
@@ -567,29 +715,38 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         // Weights: in bf16 for the product, their sum in 32 bits.  32 logits
         // become 16 columns of weights, always behind the logits still to be read.
         const float shift = m == -INFINITY ? 0.f : -m * zc;
-        const uint64_t zc2 = pack2(zc, zc), shift2 = pack2(shift, shift);
+        [[maybe_unused]] const uint64_t zc2 = pack2(zc, zc);
+        const uint64_t shift2 = pack2(shift, shift);
         uint64_t sum2[2] = {0ull, 0ull};
-        auto weigh = [&](uint32_t(&x)[32], uint32_t to) {
+        auto weigh = [&](uint32_t(&x)[32], uint32_t col) {
           uint32_t w[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             float a, b;
-            unpack2(fma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), zc2, shift2), a, b);
+            uint64_t z = pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+            if constexpr (F8) z = fma2(z, *reinterpret_cast<const uint64_t*>(ks + col + 2 * i), shift2);
+            else z = fma2(z, zc2, shift2);
+            unpack2(z, a, b);
             a = ex2(a);
             b = ex2(b);
-            sum2[i & 1] = add2(sum2[i & 1], pack2(a, b));
+            uint64_t e = pack2(a, b);
+            sum2[i & 1] = add2(sum2[i & 1], e);
+            if constexpr (F8) {   // V's scale goes with the weight, which is rounded once
+              e = mul2(e, *reinterpret_cast<const uint64_t*>(vs + col + 2 * i));
+              unpack2(e, a, b);
+            }
             w[i] = pack_bf16(a, b);
           }
-          tmem_st16(to, w);
+          tmem_st16(s_col + col / 2, w);
         };
         __syncwarp();
 #pragma unroll 1
         for (uint32_t col = 0; col < kKT; col += 64) {
           tmem_ld32_start(s_col + col + 32, xb);
-          weigh(xa, s_col + col / 2);
+          weigh(xa, col);
           tmem_ld_wait(xb);
           if (col == 0) tmem_ld32_start(s_col + 64, xa);
-          weigh(xb, s_col + col / 2 + 16);
+          weigh(xb, col + 32);
           if (col == 0) tmem_ld_wait(xa);
         }
         float s0, s1;
@@ -601,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         auto slot_of = [&](int t) { return min(max(t - t0, 0), kKT); };   // within the tile
         const int cut = slot_of(ir.last + 1);                               // slots from here on,
         const int gap0 = p.window > 0 ? slot_of(p.n_sinks) : 0, gap1 = p.window > 0 ? slot_of(dead + 1) : 0;
-        if (cut < kKT || gap0 < gap1) {                                     // and [gap0, gap1)
+        if (!F8 && (cut < kKT || gap0 < gap1)) {                                   // and [gap0, gap1)
           const int v0 = (tiles_before + place_v<NB>(j, T)) * NS;
           for (int s = 0; s < NS; ++s) {
             const int slot = (v0 + s) % n_slabs;
@@ -697,36 +854,52 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
-bool encode_pages(CUtensorMap* map, const void* base, const PagedParams& p, int head_dim) {
+bool encode_pages(CUtensorMap* map, const void* base, const PagedParams& p, int head_dim, bool f8) {
   PFN_cuTensorMapEncodeTiled_v12000 f = encoder();
   if (!f) return false;
   const cuuint64_t page = (cuuint64_t)1 << p.page_shift;
+  const cuuint32_t tokens = (cuuint32_t)(page < kKT ? page : kKT);
+  const cuuint32_t step[5] = {1, 1, 1, 1, 1};
+  if (f8) {
+    const cuuint64_t dims[4] = {(cuuint64_t)head_dim, page, (cuuint64_t)p.n_kv_heads, (cuuint64_t)p.n_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)p.tok_stride, (cuuint64_t)p.head_stride, (cuuint64_t)p.page_stride};
+    const cuuint32_t box[4] = {128, tokens, 1, 1};
+    return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, step,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  }
   const cuuint64_t dims[5] = {64, page, (cuuint64_t)head_dim / 64, (cuuint64_t)p.n_kv_heads, (cuuint64_t)p.n_pages};
   const cuuint64_t strides[4] = {(cuuint64_t)p.tok_stride * 2, 128, (cuuint64_t)p.head_stride * 2,
                                  (cuuint64_t)p.page_stride * 2};
-  const cuuint32_t box[5] = {64, (cuuint32_t)(page < kKT ? page : kKT), page < kKT ? 1u : 2u, 1, 1};
-  const cuuint32_t step[5] = {1, 1, 1, 1, 1};
+  const cuuint32_t box[5] = {64, tokens, page < kKT ? 1u : 2u, 1, 1};
   return f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, step,
            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-}  // namespace
-
-cudaError_t launch_paged_tc(const PagedParams& p, int head_dim, int grid, cudaStream_t st) {
+template <int D, bool F8>
+cudaError_t launch_d(const PagedParams& p, int grid, cudaStream_t st) {
   TcParams tp{};
   tp.p = p;
-  if (!encode_pages(&tp.k, p.k, p, head_dim) || !encode_pages(&tp.v, p.v, p, head_dim)) return cudaErrorInvalidValue;
-  const int q_bytes = p.mt * head_dim * 2;
-  const int slabs = (kSmemLimit - kHeadBytes - q_bytes) / kSlab;
-  tp.n_slabs = slabs < kMaxSlabs ? slabs : kMaxSlabs;
-  const size_t smem = (size_t)kHeadBytes + q_bytes + (size_t)tp.n_slabs * kSlab;
-  const void* kernel = head_dim == 256 ? (const void*)paged_tc_kernel<256> : (const void*)paged_tc_kernel<128>;
-  cudaError_t e = allow_dynamic_smem(kernel, kSmemLimit);
+  if (!encode_pages(&tp.k, p.k, p, D, F8) || !encode_pages(&tp.v, p.v, p, D, F8)) return cudaErrorInvalidValue;
+  const int fixed = kHeadBytes + (F8 ? (int)sizeof(Scales) : 0) + p.mt * D * 2, room = kSmemLimit - fixed;
+  if (F8) {   // operands of a tile's K and half of V, the rest for codes
+    tp.n_slabs = 3;
+    tp.n_code_slabs = std::min((room - tp.n_slabs * kSlab) / kCodeSlab, kMaxCodeSlabs);
+  } else {
+    tp.n_slabs = std::min(room / kSlab, kMaxSlabs);
+  }
+  const size_t smem = (size_t)fixed + (size_t)tp.n_slabs * kSlab + (size_t)tp.n_code_slabs * kCodeSlab;
+  cudaError_t e = allow_dynamic_smem((const void*)paged_tc_kernel<D, F8>, kSmemLimit);
   if (e != cudaSuccess) return e;
-  return head_dim == 256
-             ? launch_kernel(paged_tc_kernel<256>, dim3((unsigned)grid), dim3(kThreads), smem, st, 0u, tp)
-             : launch_kernel(paged_tc_kernel<128>, dim3((unsigned)grid), dim3(kThreads), smem, st, 0u, tp);
+  return launch_kernel(paged_tc_kernel<D, F8>, dim3((unsigned)grid), dim3(threads_of(F8)), smem, st, 0u, tp);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_tc(const PagedParams& p, qsa_dtype kv_dtype, int head_dim, int grid, cudaStream_t st) {
+  if (kv_dtype == QSA_FP8_E4M3) return head_dim == 256 ? launch_d<256, true>(p, grid, st) : launch_d<128, true>(p, grid, st);
+  return head_dim == 256 ? launch_d<256, false>(p, grid, st) : launch_d<128, false>(p, grid, st);
 }
 
 int paged_tc_bad_pages_take() { return take_counter(g_bad_pages); }
