@@ -100,7 +100,7 @@ struct Head {
   Start start;
   uint32_t tmem;
   int abort;
-  uint32_t bad[8];              // 16-token pieces of a tile that have no page
+  uint32_t bad[16];             // 16-token pieces of a tile that have no page (at most 11 slabs are under way)
   float m_run[128];             // the entries' running maxima
   float sums[2][128];           // the two groups' sums of weights
 };
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
         const uint32_t bad =
             __reduce_or_sync(0xffffffffu, missing ? ((1u << (box / 16)) - 1u) << (lane * (box / 16)) : 0u);
         if (missing) atomicAdd(&g_bad_pages, 1);
-        if (leader) h.bad[(tj + j) & 7] = bad;
+        if (leader) h.bad[(tj + j) & 15] = bad;
       };
       int pages[NB];   // of tiles j .. j + NB - 1
       bool missing;
@@ -448,7 +448,10 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
                         : __ldg(reinterpret_cast<const uint32_t*>(
                               p.kv_scale + 4 * (page * p.s_page_stride + c.head * p.s_head_stride + slot * p.s_tok_stride)));
       };
-      auto convert = [&](int j) {
+      int page = look_up(0);
+      uint32_t record = load(0, page);
+      page = look_up(1);
+      auto convert = [&](int j, bool keys) {   // K of tile j with both scales, or V
         const int t0 = c.tiles.token(c.x + j);
         // Tokens [0, cut) of the tile less [gap0, gap1) are seen by some row.
         auto slot_of = [&](int t) { return min(max(t - t0, 0), kKT); };
@@ -459,6 +462,18 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
         for (int s = 0; s < NS; ++s) {
           wait(&h.code_full[from.slot], from.use & 1, abrt);
           if (to.use > 0) wait(&h.empty[to.slot], (to.use - 1) & 1, abrt);
+          if (keys && s == 0) {
+            // The slot that is free now held a slab three before this one: tile
+            // j - 4's output is done, so its scales may go.  (At least 1e-30: minus
+            // infinity times it stays minus infinity.)
+            const __half2 both = *reinterpret_cast<const __half2*>(&record);
+            if (ct < kKT) {
+              sc.k[(tj + j) & 3][ct] = fmaxf(__low2float(both) * zs, 1e-30f);
+              sc.v[(tj + j) & 3][ct] = __high2float(both);
+            }
+            record = load(j + 1, page);
+            page = look_up(j + 2);
+          }
           const uint8_t* src = codes + from.slot * kCodeSlab;
           uint8_t* dst = ring + to.slot * kSlab;
           const int piece = ct & 7;   // 16 channels of a token
@@ -492,22 +507,10 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
           to.step(n_slabs);
         }
       };
-      int page = look_up(0);
-      uint32_t record = load(0, page);
-      page = look_up(1);
-      auto keys = [&](int j) {   // scales and K of tile j
-        const __half2 s = *reinterpret_cast<const __half2*>(&record);
-        // (At least 1e-30: minus infinity times it stays minus infinity.)
-        sc.k[(tj + j) & 3][ct] = fmaxf(__low2float(s) * zs, 1e-30f);
-        sc.v[(tj + j) & 3][ct] = __high2float(s);
-        record = load(j + 1, page);
-        page = look_up(j + 2);
-        convert(j);
-      };
 #pragma unroll 1
       for (int j = 0; j < T + NB - 1; ++j) {
-        if (j < T) keys(j);
-        if (j >= NB - 1) convert(j - (NB - 1));
+        if (j < T) convert(j, true);
+        if (j >= NB - 1) convert(j - (NB - 1), false);
       }
       tj += T;
     }
@@ -634,7 +637,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
         wait(&h.s_full[buf], (uint32_t)((g / NB) & 1), abrt);
         __syncwarp();
         fence_after();
-        const uint32_t bad = h.bad[g & 7];
+        const uint32_t bad = h.bad[g & 15];
         const bool partly = bad != 0 || t0 + kKT - 1 > ir.first ||
                             (p.window > 0 && t0 <= ir.last - p.window && t0 + kKT > p.n_sinks);
         uint32_t xa[32], xb[32];

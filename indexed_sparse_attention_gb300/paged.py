@@ -8,7 +8,6 @@
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import dataclasses
 from typing import Sequence
@@ -65,20 +64,23 @@ def declare(L: ctypes.CDLL):
 
 # ---------------------------------------------------------------------- devices and streams
 
-@contextlib.contextmanager
-def _device_of(t: torch.Tensor):
-    """The tensor's device as the current one (the library launches there)."""
-    if not t.is_cuda or t.device.index == torch.cuda.current_device():
-        yield
-        return
-    with torch.cuda.device(t.device):
-        yield
-
-
 def _raw_stream(stream, device) -> int:
     if stream is None:
         return torch.cuda.current_stream(device).cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _call(name: str, device, stream, *args):
+    """One library call with the tensors' device as the current one (the library
+    launches there), on `stream` or that device's current stream."""
+    fn = getattr(lib(), name)
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(stream, device))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _raw_stream(stream, device))
+    if status:
+        _check(name, status)
 
 
 def _scratch(n_bytes: int, device, stream) -> torch.Tensor:
@@ -131,11 +133,10 @@ class PagedCache:
             d.kv_scale = s.data_ptr()
             d.scale_page_stride, d.scale_head_stride, d.scale_tok_stride = (s.stride(i) // 2 for i in range(3))
         self.byref = ctypes.byref(d)
-
-    @property
-    def row_dtype(self):
-        """The dtype of new rows (and of queries)."""
-        return torch.float32 if self.kv_dtype == F32 else torch.bfloat16
+        self.device = k.device
+        self.row_dtype = torch.float32 if self.kv_dtype == F32 else torch.bfloat16   # of new rows and queries
+        self._row_cfg = self.config()
+        self._row_cfg_ref = ctypes.byref(self._row_cfg)
 
     def config(self, n_q_heads: int | None = None, out_dtype=torch.float32, scale: float = 0.0,
                n_splits: int = 0) -> AttnConfig:
@@ -171,15 +172,32 @@ class PagedBatch:
 
 
 def _check_rows(what: str, t: torch.Tensor, shape, dtype, device):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device:
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
         raise ValueError(f"{what} must be {list(shape)} of {dtype} on {device}, not {list(t.shape)} of {t.dtype} on {t.device}")
+
+
+def _check_batch(cache: PagedCache, batch: PagedBatch):
+    if batch.table.device != cache.device:
+        raise ValueError("the batch's arrays are on another device than the cache")
+
+
+def _check_queries(cache: PagedCache, batch: PagedBatch, q: torch.Tensor):
+    _check_rows("q", q, (batch.n_rows, q.shape[1] if q.dim() == 3 else 0, cache.head_dim), cache.row_dtype, cache.device)
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    _check_batch(cache, batch)
 
 
 # ---------------------------------------------------------------------- calls
 
 def paged_attn_workspace_size(batch: PagedBatch, cfg: AttnConfig) -> int:
-    with _device_of(batch.table):
+    """Bytes of scratch, on the batch's device (they follow its number of SMs)."""
+    def size():
         return int(lib().qsa_paged_attn_workspace_size(batch.byref, ctypes.byref(cfg)))
+    if not batch.table.is_cuda or batch.table.device.index == torch.cuda.current_device():
+        return size()
+    with torch.cuda.device(batch.table.device):
+        return size()
 
 
 def paged_attn(cache: PagedCache, batch: PagedBatch, q: torch.Tensor, out: torch.Tensor,
@@ -188,41 +206,32 @@ def paged_attn(cache: PagedCache, batch: PagedBatch, q: torch.Tensor, out: torch
     """Attention of the batch's rows q [n_rows, Hq, D] over their paged caches:
     every token up to the row's own, or with window >= 1 the last `window` of
     them and the first n_sinks tokens."""
-    dev = cache.k.device
-    _check_rows("q", q, (batch.n_rows, q.shape[1] if q.dim() == 3 else 0, cache.head_dim), cache.row_dtype, dev)
-    _check_rows("out", out, q.shape, out.dtype, dev)
+    _check_queries(cache, batch, q)
+    _check_rows("out", out, q.shape, out.dtype, cache.device)
     if lse is not None:
-        _check_rows("lse", lse, q.shape[:2], torch.float32, dev)
-    if not (q.is_contiguous() and out.is_contiguous() and (lse is None or lse.is_contiguous())):
-        raise ValueError("q, out and lse must be contiguous")
-    if batch.table.device != dev:
-        raise ValueError("the batch's arrays are on another device than the cache")
+        _check_rows("lse", lse, q.shape[:2], torch.float32, cache.device)
+    if not (out.is_contiguous() and (lse is None or lse.is_contiguous())):
+        raise ValueError("out and lse must be contiguous")
     if cfg is None:
         cfg = cache.config(q.shape[1], out.dtype, scale, n_splits)
-    with _device_of(q):
-        if workspace is None:
-            workspace = _scratch(lib().qsa_paged_attn_workspace_size(batch.byref, ctypes.byref(cfg)), dev, stream)
-        _check("qsa_paged_attn", lib().qsa_paged_attn(
-            cache.byref, batch.byref, ctypes.byref(cfg), int(window), int(n_sinks), q.data_ptr(), out.data_ptr(),
-            _ptr(lse), workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev)))
+    if workspace is None:
+        workspace = _scratch(paged_attn_workspace_size(batch, cfg), cache.device, stream)
+    _call("qsa_paged_attn", cache.device, stream, cache.byref, batch.byref, ctypes.byref(cfg), int(window),
+          int(n_sinks), q.data_ptr(), out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel())
 
 
 def paged_append(cache: PagedCache, batch: PagedBatch, k_new: torch.Tensor, v_new: torch.Tensor, stream=None):
     """Write the batch's rows k_new, v_new ([n_rows, Hkv, D], unit channel stride,
     equal strides: slices of one projection will do) into their pages."""
-    dev = cache.k.device
     shape = (batch.n_rows, cache.n_kv_heads, cache.head_dim)
-    _check_rows("k_new", k_new, shape, cache.row_dtype, dev)
-    _check_rows("v_new", v_new, shape, cache.row_dtype, dev)
-    if k_new.stride() != v_new.stride() or (k_new.numel() and k_new.stride(2) != 1):
+    _check_rows("k_new", k_new, shape, cache.row_dtype, cache.device)
+    _check_rows("v_new", v_new, shape, cache.row_dtype, cache.device)
+    strides = k_new.stride()
+    if strides != v_new.stride() or strides[2] != 1:
         raise ValueError("k_new and v_new need unit channel stride and equal strides")
-    if batch.table.device != dev:
-        raise ValueError("the batch's arrays are on another device than the cache")
-    cfg = cache.config()
-    with _device_of(k_new):
-        _check("qsa_paged_append", lib().qsa_paged_append(
-            cache.byref, batch.byref, ctypes.byref(cfg), k_new.data_ptr(), v_new.data_ptr(), k_new.stride(0),
-            k_new.stride(1), _raw_stream(stream, dev)))
+    _check_batch(cache, batch)
+    _call("qsa_paged_append", cache.device, stream, cache.byref, batch.byref, cache._row_cfg_ref, k_new.data_ptr(),
+          v_new.data_ptr(), strides[0], strides[1])
 
 
 class PagedStep:
@@ -233,12 +242,8 @@ class PagedStep:
 
     def __init__(self, cache: PagedCache, batch: PagedBatch, q: torch.Tensor, *, out_dtype=torch.float32,
                  window: int = 0, n_sinks: int = 0, scale: float = 0.0, n_splits: int = 0):
-        dev = cache.k.device
-        _check_rows("q", q, (batch.n_rows, q.shape[1] if q.dim() == 3 else 0, cache.head_dim), cache.row_dtype, dev)
-        if not q.is_contiguous():
-            raise ValueError("q must be contiguous")
-        if batch.table.device != dev:
-            raise ValueError("the batch's arrays are on another device than the cache")
+        _check_queries(cache, batch, q)
+        dev = cache.device
         self.cache, self.batch, self.q = cache, batch, q
         self.window, self.n_sinks = int(window), int(n_sinks)
         self.cfg = cache.config(q.shape[1], out_dtype, scale, n_splits)
@@ -252,14 +257,7 @@ class PagedStep:
         paged_append(self.cache, self.batch, k_new, v_new, stream)
 
     def attend(self, stream=None):
-        dev = self.q.device
-        if dev.index == torch.cuda.current_device():
-            status = lib().qsa_paged_attn(*self._args, _raw_stream(stream, dev))
-        else:
-            with torch.cuda.device(dev):
-                status = lib().qsa_paged_attn(*self._args, _raw_stream(stream, dev))
-        if status:
-            _check("qsa_paged_attn", status)
+        _call("qsa_paged_attn", self.q.device, stream, *self._args)
         return self.out, self.lse
 
     def run(self, k_new: torch.Tensor | None = None, v_new: torch.Tensor | None = None, stream=None):
@@ -302,7 +300,7 @@ class PagePool:
             if not caches:
                 raise ValueError("page_tokens is needed without caches")
             page_tokens = caches[0].page_tokens
-        if any(c.k.device != table.device for c in caches):
+        if any(c.device != table.device for c in caches):
             raise ValueError("the pool's arrays are on another device than a cache")
         self.table, self.lens, self.refs, self.caches = table, lens, refs, list(caches)
         self.page_tokens = int(page_tokens)
@@ -310,21 +308,17 @@ class PagePool:
         self.desc = PagePoolDesc(table.data_ptr(), int(table.shape[1]), lens.data_ptr(), refs.data_ptr(),
                                  int(table.shape[0]), int(refs.numel()), self.page_tokens)
         self.byref = ctypes.byref(self.desc)
-        with _device_of(table):
-            self.ws = torch.empty(max(int(lib().qsa_pages_workspace_size(self.byref)), 16), dtype=torch.uint8,
-                                  device=table.device)
+        self.ws = torch.empty(max(int(lib().qsa_pages_workspace_size(self.byref)), 16), dtype=torch.uint8,
+                              device=table.device)
+        self._cfg_ref = ctypes.byref(self._c.cfg)
 
     @classmethod
     def empty(cls, n_places: int, pages_each: int, caches: Sequence[PagedCache]) -> "PagePool":
         """A pool over the caches' pages in which every page is free."""
-        dev, n = caches[0].k.device, min(c.n_pages for c in caches)
+        dev, n = caches[0].device, min(c.n_pages for c in caches)
         return cls(torch.full((n_places, pages_each), -1, dtype=torch.int32, device=dev),
                    torch.zeros(n_places, dtype=torch.int32, device=dev),
                    torch.zeros(n, dtype=torch.int32, device=dev), caches)
-
-    def _call(self, name, stream, *args):
-        with _device_of(self.table):
-            _check(name, getattr(lib(), name)(*args, _raw_stream(stream, self.table.device)))
 
     def _pair(self, a_name, a, b_name, b):
         _int_list(a_name, a, self.table)
@@ -335,31 +329,31 @@ class PagePool:
     def extend(self, seqs: torch.Tensor, n_new: torch.Tensor, stream=None):
         """lens[seqs] += n_new, with the lowest free pages for what they lack."""
         n = self._pair("seqs", seqs, "n_new", n_new)
-        self._call("qsa_pages_extend", stream, self.byref, seqs.data_ptr(), n_new.data_ptr(), n)
+        _call("qsa_pages_extend", self.table.device, stream, self.byref, seqs.data_ptr(), n_new.data_ptr(), n)
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor, keep: torch.Tensor | None = None, stream=None):
         """The empty places dst become copies of src (their first keep tokens):
         full pages shared, a last page that is not full copied in every cache."""
         n = self._pair("src", src, "dst", dst)
         self._pair("src", src, "keep", keep)
-        self._call("qsa_pages_fork", stream, self.byref, self._c.array, self._c.n, ctypes.byref(self._c.cfg),
+        _call("qsa_pages_fork", self.table.device, stream, self.byref, self._c.array, self._c.n, self._cfg_ref,
                    src.data_ptr(), dst.data_ptr(), _ptr(keep), n, self.ws.data_ptr(), self.ws.numel())
 
     def free(self, seqs: torch.Tensor, keep: torch.Tensor | None = None, stream=None):
         """Give up the pages of seqs behind their first keep tokens (default: all)."""
         n = self._pair("seqs", seqs, "keep", keep)
-        self._call("qsa_pages_free", stream, self.byref, seqs.data_ptr(), _ptr(keep), n)
+        _call("qsa_pages_free", self.table.device, stream, self.byref, seqs.data_ptr(), _ptr(keep), n)
 
     def compact(self, n_used: torch.Tensor | None = None, stream=None):
         """Move the pages in use to the lowest numbers; n_used (int32, one element
         on the GPU) receives how many there are."""
         if n_used is not None:
             _int_list("n_used", n_used, self.table)
-        self._call("qsa_pages_compact", stream, self.byref, self._c.array, self._c.n, ctypes.byref(self._c.cfg),
+        _call("qsa_pages_compact", self.table.device, stream, self.byref, self._c.array, self._c.n, self._cfg_ref,
                    _ptr(n_used), self.ws.data_ptr(), self.ws.numel())
 
     def copy(self, src: torch.Tensor, dst: torch.Tensor, stream=None):
         """Copy pages src[i] to dst[i], whole, in every cache."""
         n = self._pair("src", src, "dst", dst)
-        self._call("qsa_pages_copy", stream, self._c.array, self._c.n, ctypes.byref(self._c.cfg), src.data_ptr(),
+        _call("qsa_pages_copy", self.table.device, stream, self._c.array, self._c.n, self._cfg_ref, src.data_ptr(),
                    dst.data_ptr(), n)

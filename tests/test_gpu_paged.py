@@ -122,8 +122,9 @@ def test_divisions_agree_and_repeat(dtype):
     for n in (1, 2, 3, 7, 50, 0):
         out, lse = run(x, n_splits=n)
         assert_attended(out, lse, ref)
-        again, lse2 = run(x, n_splits=n)
-        assert torch.equal(out, again) and torch.equal(lse, lse2)
+        for _ in range(5):
+            again, lse2 = run(x, n_splits=n)
+            assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp8", "f32"])
