@@ -176,6 +176,7 @@ struct Start {
   int64_t t0, all;
   int32_t ctas;
   int32_t seq, m, head, x;
+  SeqRows s;           // of seq
 };
 
 // Sum of one value per thread over the CTA, and the exclusive prefix (THREADS
@@ -230,11 +231,69 @@ __device__ __forceinline__ int64_t seq_cost(const PagedParams& p, int mt, int i0
   return cost * p.n_kv_heads;
 }
 
+// Position r among the tiles of sequence i (as SeqRows s), as a run's start.
+template <int KT>
+__device__ __forceinline__ void place_in_seq(const PagedParams& p, int mt, int i, const SeqRows& s, int64_t r, Start& st) {
+  int m = 0;
+  Tiles<KT> t = item_tiles<KT>(p, s, mt, m);
+  while (r >= (int64_t)t.count * p.n_kv_heads) {
+    r -= (int64_t)t.count * p.n_kv_heads;
+    t = item_tiles<KT>(p, s, mt, ++m);
+  }
+  st.seq = i;
+  st.m = m;
+  st.head = (int32_t)r / t.count;   // (below a tile count times the heads: 32 bits)
+  st.x = (int32_t)r - st.head * t.count;
+  st.s = s;
+}
+
+// find_run for at most 32 sequences of few items: every warp finds the run by
+// itself, one sequence a lane, with one round of loads and no barrier.  False
+// (for all warps) where the call is larger.
+template <int KT>
+__device__ __forceinline__ bool find_run_small(const PagedParams& p, int mt, int cta, int n_ctas, Start& st) {
+  if (p.n_seqs > 32) return false;
+  const int lane = threadIdx.x & 31;
+  SeqRows s{0, 0, 0};
+  int items = 0;
+  uint32_t cost = 0;
+  if (lane < p.n_seqs) {
+    s = seq_rows(p, lane);
+    items = item_count(p, s, mt);
+    if (items <= kLongSeq)
+      for (int m = 0; m < items; ++m) cost += (uint32_t)item_tiles<KT>(p, s, mt, m).count;
+  }
+  if (__any_sync(0xffffffffu, items > kLongSeq || cost * (uint64_t)p.n_kv_heads > (1u << 16))) return false;
+  cost *= (uint32_t)p.n_kv_heads;
+  uint32_t inc = cost;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t up = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += up;
+  }
+  const uint32_t all = __shfl_sync(0xffffffffu, inc, 31);   // at most 2^21: times the CTAs within 32 bits
+  const uint32_t ctas = min((uint32_t)n_ctas, all);
+  st = Start{0, 0, (int64_t)all, (int32_t)ctas, 0, 0, 0, 0, {0, 0, 0}};
+  if ((uint32_t)cta >= ctas) return true;
+  const uint32_t t0 = all * (uint32_t)cta / ctas, t1 = all * ((uint32_t)cta + 1) / ctas;
+  const int i = __ffs(__ballot_sync(0xffffffffu, inc > t0)) - 1;   // the first sequence that ends behind t0
+  s.len = __shfl_sync(0xffffffffu, s.len, i);
+  s.row0 = __shfl_sync(0xffffffffu, s.row0, i);
+  s.n = __shfl_sync(0xffffffffu, s.n, i);
+  const uint32_t before = __shfl_sync(0xffffffffu, inc - cost, i);
+  st.n = t1 - t0;
+  st.t0 = t0;
+  place_in_seq<KT>(p, mt, i, s, t0 - before, st);
+  return true;
+}
+
 // The run of CTA `cta` of at most `n_ctas` (all THREADS threads call; the
 // result is the same for all).  Up to THREADS sequences take one pass; more
 // take one for the number of tiles and one to find the run's start.
 template <int THREADS, int KT>
 __device__ Start find_run(const PagedParams& p, int mt, int cta, int n_ctas, int64_t* scan_s, Start* out_s) {
+  Start small;
+  if (find_run_small<KT>(p, mt, cta, n_ctas, small)) return small;
   int64_t all = 0, cost = 0, before = 0;
   for (int i0 = 0; i0 < p.n_seqs; i0 += THREADS) {
     int64_t total;
@@ -244,7 +303,7 @@ __device__ Start find_run(const PagedParams& p, int mt, int cta, int n_ctas, int
   }
   const int ctas = (int)min((int64_t)n_ctas, all);   // every run holds a tile
   const int64_t t0 = cta < ctas ? all * cta / ctas : 0, t1 = cta < ctas ? all * (cta + 1) / ctas : 0;
-  if (threadIdx.x == 0) *out_s = Start{0, 0, all, ctas, 0, 0, 0, 0};
+  if (threadIdx.x == 0) *out_s = Start{0, 0, all, ctas, 0, 0, 0, 0, {0, 0, 0}};
   __syncthreads();
   if (t1 <= t0) return *out_s;
   int64_t base = 0;
@@ -256,16 +315,10 @@ __device__ Start find_run(const PagedParams& p, int mt, int cta, int n_ctas, int
       base += total;
     }
     if (cost > 0 && t0 >= before && t0 < before + cost) {   // this thread's sequence holds the run's first tile
+      Start st{t1 - t0, t0, all, ctas, 0, 0, 0, 0, {0, 0, 0}};
       const int i = i0 + (int)threadIdx.x;
-      const SeqRows s = seq_rows(p, i);
-      int64_t r = t0 - before;
-      int m = 0;
-      Tiles<KT> t = item_tiles<KT>(p, s, mt, m);
-      while (r >= (int64_t)t.count * p.n_kv_heads) {
-        r -= (int64_t)t.count * p.n_kv_heads;
-        t = item_tiles<KT>(p, s, mt, ++m);
-      }
-      *out_s = Start{t1 - t0, t0, all, ctas, i, m, (int32_t)(r / t.count), (int32_t)(r % t.count)};
+      place_in_seq<KT>(p, mt, i, seq_rows(p, i), t0 - before, st);
+      *out_s = st;
     }
   }
   __syncthreads();
@@ -291,7 +344,7 @@ struct Cursor {
     x = st.x;
     left = st.n;
     if (left <= 0) return;
-    s = seq_rows(p, seq);
+    s = st.s;
     items = item_count(p, s, mt);
     open(p, mt);
   }

@@ -335,17 +335,14 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
     for (bool more = true; more; more = __shfl_sync(0xffffffffu, (int)c.next(p, p.mt), 0) != 0) {
       const ItemRows ir = item_rows(p, c);
       const int T = __shfl_sync(0xffffffffu, c.x1 - c.x, 0);
-      // Lane b: the page of the tile's b-th box (n_pages: nothing to read, or no page).
-      auto look_up = [&](int j, bool& missing) {
-        missing = false;
-        if (lane >= n_box) return p.n_pages;
+      // Lane b: the page of the tile's b-th box; n_pages: nothing to read, -1: no page.
+      auto look_up = [&](int j) {
         const int t = c.tiles.token(c.x + j) + lane * box;
         const int end = min(t + box - 1, ir.last);
-        if (t > ir.last || !(p.window == 0 || end > ir.first - p.window || t < p.n_sinks)) return p.n_pages;
-        int32_t page;
-        if (page_of(p, c.seq, t, page)) return page;
-        missing = true;
-        return p.n_pages;
+        const bool wanted = lane < n_box && t <= ir.last && (p.window == 0 || end > ir.first - p.window || t < p.n_sinks);
+        const int64_t at = (int64_t)t >> p.page_shift;
+        const int32_t page = wanted && at < p.table_ld ? __ldcg(p.table + c.seq * p.table_ld + at) : -1;
+        return !wanted ? p.n_pages : (uint32_t)page < (uint32_t)p.n_pages ? page : -1;
       };
       // One lane issues, with values that all lanes agree on (see the products below).
       auto copy = [&](const CUtensorMap* map, int j, int page) {
@@ -384,31 +381,32 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
           ring_at.step(n_ring);
         }
       };
-      auto announce = [&](int j, bool missing) {   // 16-token pieces of tile j without a page
+      // Marks the 16-token pieces of tile j that have no page, whose copies then
+      // go past the last page.
+      auto announce = [&](int j, int& page) {
+        const bool missing = page < 0;
         const uint32_t bad =
             __reduce_or_sync(0xffffffffu, missing ? ((1u << (box / 16)) - 1u) << (lane * (box / 16)) : 0u);
         if (missing) atomicAdd(&g_bad_pages, 1);
+        if (missing) page = p.n_pages;
         if (leader) h.bad[(tj + j) & 15] = bad;
       };
       int pages[NB];   // of tiles j .. j + NB - 1
-      bool missing;
 #pragma unroll
-      for (int i = 0; i < NB; ++i) pages[i] = p.n_pages;
+      for (int i = 0; i < NB; ++i) pages[i] = i < T ? look_up(i) : p.n_pages;
 #pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        if (i < T) pages[i] = look_up(i, missing);
-        if (i < NB - 1 && i < T) {
-          announce(i, missing);
+      for (int i = 0; i < NB - 1; ++i) {
+        if (i < T) {
+          announce(i, pages[i]);
           copy(&tp.k, i, pages[i]);
         }
       }
       for (int j = 0; j < T; ++j) {
         if (j + NB - 1 < T) {
-          announce(j + NB - 1, missing);
+          announce(j + NB - 1, pages[NB - 1]);
           copy(&tp.k, j + NB - 1, pages[NB - 1]);
         }
-        int ahead = p.n_pages;
-        if (j + NB < T) ahead = look_up(j + NB, missing);   // in flight beside V's copies
+        const int ahead = j + NB < T ? look_up(j + NB) : p.n_pages;   // in flight beside V's copies
         copy(&tp.v, j, pages[0]);
 #pragma unroll
         for (int i = 0; i + 1 < NB; ++i) pages[i] = pages[i + 1];

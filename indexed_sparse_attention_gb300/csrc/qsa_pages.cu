@@ -70,26 +70,54 @@ __device__ __forceinline__ bool valid_place(const int* list_s, int i, int n_seqs
   return true;
 }
 
+// Pages of one round of the plan: 8 consecutive ones a thread.
+constexpr int kRound = 8 * kPlanThreads;
+
+// Which of pages [first, first + 8) are free, as bits (none past the pool's end).
+__device__ __forceinline__ uint32_t free_bits(const qsa_page_pool& pool, int first) {
+  uint32_t bits = 0u;
+  int r[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) r[k] = first + k < pool.n_pages ? __ldcg(pool.refs + first + k) : 1;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) bits |= (r[k] == 0 ? 1u : 0u) << k;
+  return bits;
+}
+
 // Gives request i (this thread's) its `need` new pages: the lowest free ones in
-// list order.  Returns whether it is served; give(page, rank) is called for each
-// page handed out, by any thread, with its rank over all requests, after
-// off_s[0 .. n] holds every request's first rank.
+// list order.  Returns whether it is served; give(page, rank, n_free) is called
+// for each page handed out, by any thread, with its rank over all requests, once
+// off_s[0 .. n] holds every request's first rank.  n_free is the number of free
+// pages as far as it matters (those behind the last one wanted are not counted).
 template <typename Give>
 __device__ __forceinline__ bool take_pages(const qsa_page_pool& pool, int n, int need, int* scan_s, int* off_s,
                                            Give give) {
   const int i = (int)threadIdx.x;
-  int wanted, n_free;
+  // (The first round's pages are on their way while the needs are summed.)
+  uint32_t bits = free_bits(pool, 8 * i);
+  int wanted, n_free = 0, rank = 0;
   const int off = scan(need, scan_s, wanted);
   if (i < n) off_s[i] = off;
   if (i == 0) off_s[n] = wanted;
-  const Slice sl = slice(pool.n_pages);
-  int mine = 0;
-#pragma unroll 8
-  for (int k = sl.lo; k < sl.hi; ++k) mine += __ldcg(pool.refs + k) == 0;
-  int rank = scan(mine, scan_s, n_free);   // (its barriers publish off_s)
+  int rounds = 0;
+  for (int lo = 0; lo < pool.n_pages && n_free < wanted; lo += kRound, ++rounds) {
+    if (rounds > 0) bits = free_bits(pool, lo + 8 * i);
+    int found;
+    rank = n_free + scan(__popc(bits), scan_s, found);   // (its barriers publish off_s)
+    n_free += found;
+  }
   const bool served = need == 0 || off + need <= n_free;
-  for (int k = sl.lo; k < sl.hi && rank < wanted; ++k)
-    if (__ldcg(pool.refs + k) == 0) give(k, rank++, n_free);
+  const int many = rounds;
+  int base = 0;
+  for (int k = 0; k < many; ++k) {
+    if (many > 1) {   // the ranks of the earlier rounds again
+      int found;
+      bits = free_bits(pool, k * kRound + 8 * i);
+      rank = base + scan(__popc(bits), scan_s, found);
+      base += found;
+    }
+    for (uint32_t b = bits; b && rank < wanted; b &= b - 1) give(k * kRound + 8 * i + __ffs(b) - 1, rank++, n_free);
+  }
   return served;
 }
 
@@ -238,10 +266,16 @@ __global__ void __launch_bounds__(kCopyThreads) fork_kernel(const qsa_page_pool 
   const int32_t* from = pool.table + f.src * pool.table_ld;
   if (rows && blockIdx.y == 0) {
     int32_t* to = pool.table + f.dst * pool.table_ld;
-    for (int j = (int)threadIdx.x; j < full; j += kCopyThreads) {
-      const int32_t page = __ldcg(from + j);
-      to[j] = page;
-      if ((uint32_t)page < (uint32_t)pool.n_pages) atomicAdd(pool.refs + page, 1);
+    constexpr int kBatch = 4;
+    for (int j0 = (int)threadIdx.x; j0 < full; j0 += kBatch * kCopyThreads) {
+      int32_t page[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) page[k] = j0 + k * kCopyThreads < full ? __ldcg(from + j0 + k * kCopyThreads) : -1;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (j0 + k * kCopyThreads < full) to[j0 + k * kCopyThreads] = page[k];
+        if ((uint32_t)page[k] < (uint32_t)pool.n_pages) atomicAdd(pool.refs + page[k], 1);
+      }
     }
     if (threadIdx.x == 0) {
       if (f.page >= 0) to[full] = f.page;
@@ -260,14 +294,23 @@ __global__ void __launch_bounds__(kCopyThreads) fork_kernel(const qsa_page_pool 
 __device__ __forceinline__ void give_up(const qsa_page_pool& pool, int s, int keep, int len, int t0, int n) {
   int32_t* row = pool.table + s * pool.table_ld;
   const int last = pages_for(len, pool.page_tokens);
-  for (int j = pages_for(keep, pool.page_tokens) + t0; j < last; j += n) {
-    const int32_t page = __ldcg(row + j);
-    row[j] = -1;
-    if ((uint32_t)page >= (uint32_t)pool.n_pages) continue;
-    if (atomicSub(pool.refs + page, 1) <= 0) {   // nobody used it: not this call's doing
-      atomicAdd(pool.refs + page, 1);
-      atomicAdd(&g_unserved, 1);
+  constexpr int kBatch = 4;   // entries of a thread whose loads, then counts, are in flight together
+  for (int j0 = pages_for(keep, pool.page_tokens) + t0; j0 < last; j0 += kBatch * n) {
+    int32_t page[kBatch];
+    int was[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) page[k] = j0 + k * n < last ? __ldcg(row + j0 + k * n) : -1;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (j0 + k * n < last) row[j0 + k * n] = -1;
+      was[k] = (uint32_t)page[k] < (uint32_t)pool.n_pages ? atomicSub(pool.refs + page[k], 1) : 1;
     }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (was[k] <= 0) {   // nobody used it: not this call's doing
+        atomicAdd(pool.refs + page[k], 1);
+        atomicAdd(&g_unserved, 1);
+      }
   }
 }
 
