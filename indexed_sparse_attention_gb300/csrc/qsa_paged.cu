@@ -10,8 +10,6 @@
 // sums): a tile's new maximum m' rescales l and the output by exp(m - m').
 #include <math.h>
 
-#include <algorithm>
-
 #include "qsa_attn_common.cuh"
 #include "qsa_paged.cuh"
 
@@ -183,88 +181,142 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const PagedPar
 }
 
 // ------------------------------------------------------------------ joining
-// CTA (c, f): the item that crosses out of run c, entry f: parts in the slots
-// 2c + 1, 2(c + 1), 2(c + 2), ...; warp w takes parts w, w + 8, ... and the
-// warps' sums are added in shared memory in a fixed order.
+// The items that cross runs, joined by their log-sum-exp.  An item's parts lie
+// in the slots 2c + 1, 2(c + 1), 2(c + 2), ... of the run c it starts in.  A CTA
+// takes units of eight warps' work from the list of all such items' entries:
+// an entry of few parts is one warp's, one of many parts that of up to eight,
+// which add up in shared memory in a fixed order.  (One CTA per entry of every
+// run, most of them without work, took 50 us of a 2,048-row call's 255.)
 constexpr int kJoinWarps = 8;
+constexpr int kJoinThreads = 32 * kJoinWarps;
+constexpr int kMaxRuns = 1024;
+
+__device__ __forceinline__ int join_warps(int n_parts) { return n_parts >= 24 ? 8 : n_parts >= 12 ? 4 : n_parts >= 6 ? 2 : 1; }
 
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedParams p, int n_runs) {
   constexpr int CPL = D / 32;
   __shared__ float acc_s[kJoinWarps][D];
   __shared__ float m_s[kJoinWarps], w_s[kJoinWarps];
+  __shared__ int off_s[kMaxRuns + 1];
+  __shared__ int64_t scan_s[kJoinWarps];
   grid_dependency_sync();
-  const int cta = blockIdx.x, f = blockIdx.y;
-  const PagedPart d = p.parts[cta];
-  if (f >= d.nf || d.n_parts == 0) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float m = -INFINITY, w = 0.f, acc[CPL];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int64_t units = 0;
+  for (int c0 = 0; c0 < n_runs; c0 += kJoinThreads) {
+    int n = 0;
+    if (c0 + tid < n_runs) {
+      const int4 d = *reinterpret_cast<const int4*>(p.parts + c0 + tid);   // n_parts, row0, f0, nf
+      if (d.x > 0) n = (d.w * join_warps(d.x) + kJoinWarps - 1) / kJoinWarps;
+    }
+    int64_t total;
+    const int64_t before = units + cta_scan<kJoinThreads>(n, scan_s, total);
+    if (c0 + tid < n_runs) off_s[c0 + tid] = (int)before;
+    units += total;
+  }
+  if (tid == 0) off_s[n_runs] = (int)units;
+  __syncthreads();
+  for (int u = blockIdx.x; u < (int)units; u += gridDim.x) {
+    int cta = 0, hi = n_runs;   // off_s[cta] <= u < off_s[hi]
+    while (hi - cta > 1) {
+      const int mid = (cta + hi) / 2;
+      if (off_s[mid] <= u) cta = mid;
+      else hi = mid;
+    }
+    const PagedPart d = p.parts[cta];
+    const int w = join_warps(d.n_parts), sub = warp & (w - 1);
+    const int f = (u - off_s[cta]) * (kJoinWarps / w) + warp / w;
+    float m = -INFINITY, l = 0.f, acc[CPL];
 #pragma unroll
-  for (int i = 0; i < CPL; ++i) acc[i] = 0.f;
-  constexpr int kBatch = 4;   // parts whose loads are in flight together
-  for (int s0 = warp; s0 < d.n_parts; s0 += kJoinWarps * kBatch) {
-    float ls[kBatch], v[kBatch][CPL];
+    for (int i = 0; i < CPL; ++i) acc[i] = 0.f;
+    constexpr int kBatch = 4;   // parts whose loads are in flight together
+    for (int s0 = sub; s0 < d.n_parts && f < d.nf; s0 += w * kBatch) {
+      float ls[kBatch];
+      float4 v[kBatch][CPL / 4];
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int s = s0 + k * kJoinWarps;
-      const int64_t at = ((int64_t)2 * (cta + s) + (s == 0 ? 1 : 0)) * p.mt + f;
-      ls[k] = s < d.n_parts ? p.part_lse[at] : -INFINITY;
+      for (int k = 0; k < kBatch; ++k) {
+        const int s = s0 + k * w;
+        const int64_t at = ((int64_t)2 * (cta + s) + (s == 0 ? 1 : 0)) * p.mt + f;
+        ls[k] = s < d.n_parts ? p.part_lse[at] : -INFINITY;
 #pragma unroll
-      for (int i = 0; i < CPL / 4; ++i) {
-        const float4 x = s < d.n_parts ? reinterpret_cast<const float4*>(p.part_o + at * D)[i * 32 + lane]
-                                       : make_float4(0.f, 0.f, 0.f, 0.f);
-        v[k][4 * i] = x.x;
-        v[k][4 * i + 1] = x.y;
-        v[k][4 * i + 2] = x.z;
-        v[k][4 * i + 3] = x.w;
+        for (int i = 0; i < CPL / 4; ++i)
+          v[k][i] = s < d.n_parts ? reinterpret_cast<const float4*>(p.part_o + at * D)[i * 32 + lane]
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      float mn = m;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) mn = fmaxf(mn, ls[k]);
+      if (mn == -INFINITY) continue;
+      const float a = exp2f(m - mn);
+      l *= a;
+#pragma unroll
+      for (int i = 0; i < CPL; ++i) acc[i] *= a;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (ls[k] == -INFINITY) continue;
+        const float e = exp2f(ls[k] - mn);
+        l += e;
+#pragma unroll
+        for (int i = 0; i < CPL / 4; ++i) {
+          acc[4 * i] = fmaf(e, v[k][i].x, acc[4 * i]);
+          acc[4 * i + 1] = fmaf(e, v[k][i].y, acc[4 * i + 1]);
+          acc[4 * i + 2] = fmaf(e, v[k][i].z, acc[4 * i + 2]);
+          acc[4 * i + 3] = fmaf(e, v[k][i].w, acc[4 * i + 3]);
+        }
+      }
+      m = mn;
+    }
+    if (w > 1) {   // the other warps' sums, each against the largest maximum
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < CPL / 4; ++i)
+        reinterpret_cast<float4*>(acc_s[warp])[i * 32 + lane] =
+            make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+      if (lane == 0) {
+        m_s[warp] = m;
+        w_s[warp] = l;
+      }
+      __syncthreads();
+      if (sub == 0) {
+        float M = m;
+        for (int k = 1; k < w; ++k) M = fmaxf(M, m_s[warp + k]);
+        const float own = m == -INFINITY ? 0.f : exp2f(m - M);
+        l *= own;
+#pragma unroll
+        for (int i = 0; i < CPL; ++i) acc[i] *= own;
+        for (int k = 1; k < w; ++k) {
+          if (m_s[warp + k] == -INFINITY) continue;
+          const float e = exp2f(m_s[warp + k] - M);
+          l = fmaf(e, w_s[warp + k], l);
+#pragma unroll
+          for (int i = 0; i < CPL / 4; ++i) {
+            const float4 x = reinterpret_cast<const float4*>(acc_s[warp + k])[i * 32 + lane];
+            acc[4 * i] = fmaf(e, x.x, acc[4 * i]);
+            acc[4 * i + 1] = fmaf(e, x.y, acc[4 * i + 1]);
+            acc[4 * i + 2] = fmaf(e, x.z, acc[4 * i + 2]);
+            acc[4 * i + 3] = fmaf(e, x.w, acc[4 * i + 3]);
+          }
+        }
+        m = M;
       }
     }
-    float mn = m;
+    if (sub != 0 || f >= d.nf) continue;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int r = (d.f0 + f) / p.group;
+    const int64_t at = (int64_t)(d.row0 + r) * p.n_q_heads + d.head * p.group + (d.f0 + f - r * p.group);
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) mn = fmaxf(mn, ls[k]);
-    if (mn == -INFINITY) continue;
-    const float a = exp2f(m - mn);
-    w *= a;
-#pragma unroll
-    for (int i = 0; i < CPL; ++i) acc[i] *= a;
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      if (ls[k] == -INFINITY) continue;
-      const float e = exp2f(ls[k] - mn);
-      w += e;
-#pragma unroll
-      for (int i = 0; i < CPL; ++i) acc[i] = fmaf(e, v[k][i], acc[i]);
+    for (int i = 0; i < CPL / 4; ++i) {
+      const float4 o = make_float4(acc[4 * i] * inv, acc[4 * i + 1] * inv, acc[4 * i + 2] * inv, acc[4 * i + 3] * inv);
+      if (p.out_dtype == QSA_F32) {
+        reinterpret_cast<float4*>(static_cast<float*>(p.out) + at * D)[i * 32 + lane] = o;
+      } else {
+        __nv_bfloat162* to = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + at * D) + (i * 32 + lane) * 2;
+        to[0] = __floats2bfloat162_rn(o.x, o.y);
+        to[1] = __floats2bfloat162_rn(o.z, o.w);
+      }
     }
-    m = mn;
+    if (lane == 0 && p.lse) p.lse[at] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
   }
-#pragma unroll
-  for (int i = 0; i < CPL / 4; ++i)
-    reinterpret_cast<float4*>(acc_s[warp])[i * 32 + lane] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
-  if (lane == 0) {
-    m_s[warp] = m;
-    w_s[warp] = w;
-  }
-  __syncthreads();
-  float M = -INFINITY;
-#pragma unroll
-  for (int k = 0; k < kJoinWarps; ++k) M = fmaxf(M, m_s[k]);
-  float e[kJoinWarps], W = 0.f;
-#pragma unroll
-  for (int k = 0; k < kJoinWarps; ++k) {
-    e[k] = m_s[k] == -INFINITY ? 0.f : exp2f(m_s[k] - M);
-    W = fmaf(e[k], w_s[k], W);
-  }
-  const float inv = W > 0.f ? 1.f / W : 0.f;
-  const int r = (d.f0 + f) / p.group;
-  const int64_t at = (int64_t)(d.row0 + r) * p.n_q_heads + d.head * p.group + (d.f0 + f - r * p.group);
-  for (int x = threadIdx.x; x < D; x += kJoinWarps * 32) {
-    float o = 0.f;
-#pragma unroll
-    for (int k = 0; k < kJoinWarps; ++k) o = fmaf(e[k], acc_s[k][x], o);
-    if (p.out_dtype == QSA_F32) static_cast<float*>(p.out)[at * D + x] = o * inv;
-    else static_cast<__nv_bfloat16*>(p.out)[at * D + x] = __float2bfloat16(o * inv);
-  }
-  if (threadIdx.x == 0 && p.lse) p.lse[at] = W > 0.f ? (M + log2f(W)) * kLn2 : -INFINITY;
 }
 
 template <int D, int DT>
@@ -285,10 +337,12 @@ cudaError_t launch_paged_simt(const PagedParams& p, qsa_dtype kv_dtype, int head
   return head_dim == 256 ? launch_simt<256, QSA_FP8_E4M3>(p, grid, st) : launch_simt<128, QSA_FP8_E4M3>(p, grid, st);
 }
 
-cudaError_t launch_paged_merge(const PagedParams& p, int head_dim, int grid, cudaStream_t st) {
-  const dim3 g((unsigned)grid, (unsigned)p.mt), b(kJoinWarps * 32);
-  return head_dim == 256 ? launch_kernel(paged_join_kernel<256>, g, b, 0, st, 0u, p)
-                         : launch_kernel(paged_join_kernel<128>, g, b, 0, st, 0u, p);
+cudaError_t launch_paged_merge(const PagedParams& p, int head_dim, int runs, cudaStream_t st) {
+  if (runs < 2) return cudaSuccess;   // one run holds every item whole
+  if (runs > kMaxRuns) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)(4 * device_sm_count())), block(kJoinThreads);
+  return head_dim == 256 ? launch_kernel(paged_join_kernel<256>, grid, block, 0, st, 0u, p, runs)
+                         : launch_kernel(paged_join_kernel<128>, grid, block, 0, st, 0u, p, runs);
 }
 
 int paged_bad_pages_take() { return take_counter(g_bad_pages); }

@@ -52,7 +52,7 @@ struct PagedParams {
 };
 
 // An item whose key tiles are spread over n_parts CTAs, from this entry's on.
-struct PagedPart {
+struct alignas(16) PagedPart {
   int32_t n_parts;   // 0: no such item starts here
   int32_t row0;      // the sequence's first row
   int32_t f0;        // the item's first entry
@@ -117,7 +117,7 @@ cudaError_t launch_paged_simt(const PagedParams& p, qsa_dtype kv_dtype, int head
 cudaError_t launch_paged_tc(const PagedParams& p, qsa_dtype kv_dtype, int head_dim, int grid, cudaStream_t st);
 int paged_tc_bad_pages_take();
 int paged_tc_wait_timeouts();
-cudaError_t launch_paged_merge(const PagedParams& p, int head_dim, int grid, cudaStream_t st);
+cudaError_t launch_paged_merge(const PagedParams& p, int head_dim, int runs, cudaStream_t st);
 int paged_bad_pages_take();
 
 namespace paged {

@@ -642,14 +642,13 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
         // What a row does not see becomes -infinity, in TMEM: the passes below
         // stay short (with the masks unrolled into them they no longer fit the
         // instruction cache and take four times as long).
-        if (partly || ir.nf < 32 * quarters) {
+        if (partly) {
 #pragma unroll 1
           for (int col = 0; col < kKT; col += 32) {
             // Keys t .. t + 31: seen are those up to pos, from low on or among the first n_sinks.
             const int t = t0 + col;
             uint32_t see = below(pos + 1 - t) & (~below(low - t) | below(p.n_sinks - t));
             see &= ~((((bad >> (col / 16)) & 1u) * 0xffffu) | (((bad >> (col / 16 + 1)) & 1u) * 0xffff0000u));
-            if (!mine) see = 0u;
             if (__all_sync(0xffffffffu, see == 0xffffffffu)) continue;
             tmem_ld32_start(s_col + (uint32_t)col, xa);
             tmem_ld_wait(xa);
@@ -687,7 +686,9 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
           take_max(xb, col + 32);
           tmem_ld_wait(xa);
         }
-        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        // Lanes without an entry hold whatever their rows of Q gave; nothing reads
+        // their weights, and they must not move a maximum.
+        const float mx = mine ? fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) : -INFINITY;
         // The running maximum after the tile before this one, then after this one.
         if (g > 0) wait(&h.m_done[group ^ 1], (uint32_t)(((g - 1) >> 1) & 1), abrt);
         const float before = j == 0 ? -INFINITY : h.m_run[row];
