@@ -68,10 +68,10 @@ Plan plan_attn(const qsa_paged_batch* b, const qsa_attn_config* cfg) {
   Plan pl;
   pl.tensor_cores = cfg->kv_dtype != QSA_F32;
   if (pl.tensor_cores) {
-    // As many entries as a sequence has, up to the 128 rows of the MMA: Q's
-    // share of the shared memory goes to the ring.
-    const int64_t entries = (int64_t)b->max_rows * (cfg->n_q_heads / cfg->n_kv_heads);
-    pl.mt = (int)std::min<int64_t>(128, std::max<int64_t>(16, (entries + 15) / 16 * 16));
+    // Whole rows, as many as a sequence has, up to the 128 entries that are the
+    // MMA's rows: what Q does not take of the shared memory is the ring's.
+    const int group = cfg->n_q_heads / cfg->n_kv_heads;
+    pl.mt = group * std::max(1, std::min(b->max_rows, 128 / group));
     pl.grid = device_sm_count();
   } else {
     pl.mt = 16;

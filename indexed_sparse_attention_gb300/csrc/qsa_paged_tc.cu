@@ -26,8 +26,8 @@
 // not read.
 //
 // Roles: warps 0-7 softmax and output (warp w: entries 32 (w % 4) .., keys 64
-// (w / 4) ..; warps without entries idle), warp 8 copies K and V, warp 9
-// issues the MMAs, warps 10-11 load Q.  Every wait gives up after about two
+// (w / 4) ..; warps without entries idle), warps 8 and 10 copy K and V, warp 9
+// issues the MMAs, warp 11 copies Q.  Every wait gives up after about two
 // seconds (counted; the CTA then runs to its end).
 #include <math.h>
 
@@ -53,11 +53,11 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kKT = 128;                      // keys of a tile
 constexpr int kHalf = kKT * 128;              // bytes of 64 channels of a tile
 constexpr int kSlab = 2 * kHalf;              // bytes of 128 channels: what the ring holds
-constexpr int kMaxSlabs = 6;
-constexpr int kCopyWarp = 8, kMmaWarp = 9, kQWarp = 10, kQWarps = 2, kCodeWarp = 12, kCodeWarps = 4;
+constexpr int kMaxSlabs = 3;                 // of K, and of V
+constexpr int kKeyWarp = 8, kMmaWarp = 9, kValueWarp = 10, kQWarp = 11, kCodeWarp = 12, kCodeWarps = 4;
 __host__ __device__ constexpr int threads_of(bool f8) { return 32 * (f8 ? kCodeWarp + kCodeWarps : kCodeWarp); }
 constexpr int kCodeSlab = kKT * 128;          // bytes of the codes of a slab (fp8 caches)
-constexpr int kMaxCodeSlabs = 8;
+constexpr int kMaxCodeSlabs = 4;             // of K, and of V
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSmemLimit = 227 * 1024;
 constexpr float kMoveMax = 8.f;               // log2 of the weight at which the running maximum is moved
@@ -72,9 +72,10 @@ struct TcParams {
   // {64 channels, page_tokens, D / 64, Hkv, n_pages}: boxes of 64 channels x min(page_tokens, 128)
   // tokens, of two channel blocks where the page has 128 tokens.
   CUtensorMap k, v;
+  CUtensorMap q;         // {D, Hq, n_rows}: boxes of 64 channels x a KV head's query heads x an item's rows
   PagedParams p;
-  int32_t n_slabs;
-  int32_t n_code_slabs;   // fp8 caches: the ring of codes behind the ring of slabs
+  int32_t n_k, n_v;              // slabs in the rings of K and V
+  int32_t n_code_k, n_code_v;    // fp8 caches: slabs of codes
 };
 
 // bar_wait with everything behind its first try out of line: the loops of the
@@ -93,22 +94,22 @@ __device__ __forceinline__ void wait(uint64_t* b, uint32_t parity, int* abort) {
 // tile j - NB or later ones, NB <= 3, so whoever has seen them may wait for the
 // product of tile j - 1, and after that for tile j's.
 struct Head {
-  uint64_t full[kMaxSlabs], empty[kMaxSlabs];
+  uint64_t full[2][kMaxSlabs], empty[2][kMaxSlabs];   // K, V
   uint64_t s_full[3], p_full[3], pv_done[2], m_done[2], o_free, q_full, q_free, mma_done;
-  uint64_t code_full[kMaxCodeSlabs], code_empty[kMaxCodeSlabs];
+  uint64_t code_full[2][kMaxCodeSlabs], code_empty[2][kMaxCodeSlabs];
   int64_t scan[16];
   Start start;
   uint32_t tmem;
   int abort;
-  uint32_t bad[16];             // 16-token pieces of a tile that have no page (at most 11 slabs are under way)
+  uint32_t bad[16];             // 16-token pieces of a tile that have no page (fewer are under way)
   float m_run[128];             // the entries' running maxima
   float sums[2][128];           // the two groups' sums of weights
 };
 constexpr int kHeadBytes = 3072;
 // fp8 caches: scales of the tiles in flight, behind the head.
 struct Scales {
-  float k[4][kKT];   // times the logit scale and log2(e)
-  float v[4][kKT];
+  float k[8][kKT];   // times the logit scale and log2(e)
+  float v[8][kKT];
 };
 static_assert(sizeof(Head) <= kHeadBytes, "shared memory head");
 
@@ -126,6 +127,13 @@ __device__ __forceinline__ void tma_5d(void* dst, const CUtensorMap* map, int to
       "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], "
       "[%7];\n" ::"r"(smem_addr(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(token), "r"(block), "r"(head), "r"(page), "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::
+          "r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
       : "memory");
 }
 __device__ __forceinline__ void tma_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
@@ -247,13 +255,6 @@ __device__ __forceinline__ ItemRows item_rows(const PagedParams& p, const Cursor
 // Bits 0 .. n - 1 (n of any sign and size).
 __device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
 
-// Place of tile j's V among the copies (and products) of an item of T tiles,
-// K and V counted: K runs NB - 1 tiles ahead, K0 .. K(NB-2), K(NB-1), V0, K(NB), V1, ...
-template <int NB>
-__device__ __forceinline__ int place_v(int j, int T) {
-  return j + min(T, j + NB);
-}
-
 // A ring position: slab index and the parity of its use.
 struct Ring {
   int slot = 0;
@@ -277,21 +278,25 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
   Head& h = *reinterpret_cast<Head*>(raw);
   Scales& sc = *reinterpret_cast<Scales*>(raw + kHeadBytes);
   uint8_t* q_s = raw + kHeadBytes + (F8 ? sizeof(Scales) : 0);
-  const int q_slab = p.mt * 128, n_slabs = tp.n_slabs;
-  uint8_t* ring = q_s + 2 * NS * q_slab;
-  uint8_t* codes = ring + n_slabs * kSlab;
+  const int q_slab = (p.mt * 128 + 1023) / 1024 * 1024;
+  uint8_t* k_ring = q_s + 2 * NS * q_slab;
+  uint8_t* v_ring = k_ring + tp.n_k * kSlab;
+  uint8_t* k_codes = v_ring + tp.n_v * kSlab;
+  uint8_t* v_codes = k_codes + tp.n_code_k * kCodeSlab;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int quarters = (p.mt + 31) / 32, soft_threads = 64 * quarters;
   int* abrt = &h.abort;
 
   if (tid == 0) {
-    for (int i = 0; i < n_slabs; ++i) {
-      bar_init(&h.full[i], F8 ? kCodeWarps : 1);
-      bar_init(&h.empty[i], 1);
-    }
-    for (int i = 0; F8 && i < tp.n_code_slabs; ++i) {
-      bar_init(&h.code_full[i], 1);
-      bar_init(&h.code_empty[i], kCodeWarps);
+    for (int kv = 0; kv < 2; ++kv) {
+      for (int i = 0; i < kMaxSlabs; ++i) {
+        bar_init(&h.full[kv][i], F8 ? kCodeWarps : 1);
+        bar_init(&h.empty[kv][i], 1);
+      }
+      for (int i = 0; F8 && i < kMaxCodeSlabs; ++i) {
+        bar_init(&h.code_full[kv][i], 1);
+        bar_init(&h.code_empty[kv][i], kCodeWarps);
+      }
     }
     for (int i = 0; i < 3; ++i) {
       bar_init(&h.s_full[i], 1);
@@ -302,7 +307,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       bar_init(&h.m_done[i], soft_threads / 2);
     }
     bar_init(&h.o_free, soft_threads);
-    bar_init(&h.q_full, kQWarps);
+    bar_init(&h.q_full, 1);
     bar_init(&h.q_free, 1);
     bar_init(&h.mma_done, 1);
     h.abort = 0;
@@ -321,16 +326,20 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
 
   if (st.n == 0) {
     if (tid == 0) p.parts[blockIdx.x] = PagedPart{};
-  } else if (warp == kCopyWarp) {
-    // ------------------------------------------------------------ K and V
-    const int box = min(1 << p.page_shift, kKT), n_box = kKT / box;
+  } else if (warp == kKeyWarp || warp == kValueWarp) {
+    // ------------------------------------------------------------ K, or V
+    // (bf16: into the ring of operands; fp8: codes into their own.)  One lane
+    // issues, with values that all lanes agree on; see the products below.
+    const int kv = warp == kValueWarp ? 1 : 0;
+    const CUtensorMap* map = kv ? &tp.v : &tp.k;
+    const int box = min(1 << p.page_shift, kKT), n_box = kKT / box, page_mask = (1 << p.page_shift) - 1;
+    constexpr int kBytes = F8 ? kCodeSlab : kSlab;
+    uint64_t* fulls = F8 ? h.code_full[kv] : h.full[kv];
+    uint64_t* empties = F8 ? h.code_empty[kv] : h.empty[kv];
+    uint8_t* const to_ring = F8 ? (kv ? v_codes : k_codes) : (kv ? v_ring : k_ring);
+    const int n_ring = F8 ? (kv ? tp.n_code_v : tp.n_code_k) : (kv ? tp.n_v : tp.n_k);
     const bool leader = elect_one();
-    // bf16: into the ring of operands; fp8: codes into their own ring.
-    uint64_t* fulls = F8 ? h.code_full : h.full;
-    uint64_t* empties = F8 ? h.code_empty : h.empty;
-    uint8_t* const to_ring = F8 ? codes : ring;
-    const int n_ring = F8 ? tp.n_code_slabs : n_slabs;
-    Ring ring_at;
+    Ring at;
     int tj = 0;
     for (bool more = true; more; more = __shfl_sync(0xffffffffu, (int)c.next(p, p.mt), 0) != 0) {
       const ItemRows ir = item_rows(p, c);
@@ -340,83 +349,62 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
         const int t = c.tiles.token(c.x + j) + lane * box;
         const int end = min(t + box - 1, ir.last);
         const bool wanted = lane < n_box && t <= ir.last && (p.window == 0 || end > ir.first - p.window || t < p.n_sinks);
-        const int64_t at = (int64_t)t >> p.page_shift;
-        const int32_t page = wanted && at < p.table_ld ? __ldcg(p.table + c.seq * p.table_ld + at) : -1;
+        const int64_t slot = (int64_t)t >> p.page_shift;
+        const int32_t page = wanted && slot < p.table_ld ? __ldcg(p.table + c.seq * p.table_ld + slot) : -1;
         return !wanted ? p.n_pages : (uint32_t)page < (uint32_t)p.n_pages ? page : -1;
       };
-      // One lane issues, with values that all lanes agree on (see the products below).
-      auto copy = [&](const CUtensorMap* map, int j, int page) {
-        const int slot_in_page = c.tiles.token(c.x + j) & ((1 << p.page_shift) - 1);
+      // Pages are looked up two tiles ahead.
+      int page = look_up(0), next = T > 1 ? look_up(1) : 0;
+#pragma unroll 1
+      for (int j = 0; j < T; ++j) {
+        const int ahead = j + 2 < T ? look_up(j + 2) : 0;
+        if (__any_sync(0xffffffffu, page < 0)) {   // copies of missing pages go past the last one
+          const bool missing = page < 0;
+          const uint32_t bad =
+              __reduce_or_sync(0xffffffffu, missing ? ((1u << (box / 16)) - 1u) << (lane * (box / 16)) : 0u);
+          if (missing) page = p.n_pages;
+          if (missing && kv == 0) atomicAdd(&g_bad_pages, 1);
+          if (leader && kv == 0) h.bad[(tj + j) & 15] = bad;   // 16-token pieces of the tile
+        } else if (leader && kv == 0) {
+          h.bad[(tj + j) & 15] = 0u;
+        }
+        const int slot_in_page = c.tiles.token(c.x + j) & page_mask;
 #pragma unroll 1
         for (int s = 0; s < NS; ++s) {
-          uint64_t* full = fulls + ring_at.slot;
-          if (ring_at.use > 0) wait(empties + ring_at.slot, (ring_at.use - 1) & 1, abrt);
+          uint64_t* full = fulls + at.slot;
+          uint8_t* dst = to_ring + at.slot * kBytes;
+          if (at.use > 0) wait(empties + at.slot, (at.use - 1) & 1, abrt);
           __syncwarp();
-          if constexpr (F8) {
-            uint8_t* dst = to_ring + ring_at.slot * kCodeSlab;
-            if (leader) bar_expect_tx(full, kCodeSlab);
+          if (leader) bar_expect_tx(full, kBytes);
+          if (!F8 && n_box == 1) {   // both halves at once
+            const int to = __shfl_sync(0xffffffffu, page, 0);
+            if (leader) tma_5d(dst, map, slot_in_page, 2 * s, c.head, to, full);
+          } else {
 #pragma unroll 1
             for (int b = 0; b < n_box; ++b) {
               const int to = __shfl_sync(0xffffffffu, page, b);
-              if (leader) tma_4d(dst + b * box * 128, map, 128 * s, slot_in_page, c.head, to, full);
-            }
-          } else {
-            uint8_t* dst = to_ring + ring_at.slot * kSlab;
-            if (leader) bar_expect_tx(full, kSlab);
-            if (n_box == 1) {   // both halves at once
-              const int to = __shfl_sync(0xffffffffu, page, 0);
-              if (leader) tma_5d(dst, map, slot_in_page, 2 * s, c.head, to, full);
-            } else {
-#pragma unroll 1
-              for (int b = 0; b < n_box; ++b) {
-                const int to = __shfl_sync(0xffffffffu, page, b);
-                if (leader) {
-                  tma_5d(dst + b * box * 128, map, 0, 2 * s, c.head, to, full);
-                  tma_5d(dst + kHalf + b * box * 128, map, 0, 2 * s + 1, c.head, to, full);
+              if (leader) {
+                if constexpr (F8) {
+                  tma_4d(dst, map, 128 * s, slot_in_page, c.head, to, full);
+                } else {
+                  tma_5d(dst, map, 0, 2 * s, c.head, to, full);
+                  tma_5d(dst + kHalf, map, 0, 2 * s + 1, c.head, to, full);
                 }
               }
+              dst += box * 128;
             }
           }
           __syncwarp();
-          ring_at.step(n_ring);
+          at.step(n_ring);
         }
-      };
-      // Marks the 16-token pieces of tile j that have no page, whose copies then
-      // go past the last page.
-      auto announce = [&](int j, int& page) {
-        const bool missing = page < 0;
-        const uint32_t bad =
-            __reduce_or_sync(0xffffffffu, missing ? ((1u << (box / 16)) - 1u) << (lane * (box / 16)) : 0u);
-        if (missing) atomicAdd(&g_bad_pages, 1);
-        if (missing) page = p.n_pages;
-        if (leader) h.bad[(tj + j) & 15] = bad;
-      };
-      int pages[NB];   // of tiles j .. j + NB - 1
-#pragma unroll
-      for (int i = 0; i < NB; ++i) pages[i] = i < T ? look_up(i) : p.n_pages;
-#pragma unroll
-      for (int i = 0; i < NB - 1; ++i) {
-        if (i < T) {
-          announce(i, pages[i]);
-          copy(&tp.k, i, pages[i]);
-        }
-      }
-      for (int j = 0; j < T; ++j) {
-        if (j + NB - 1 < T) {
-          announce(j + NB - 1, pages[NB - 1]);
-          copy(&tp.k, j + NB - 1, pages[NB - 1]);
-        }
-        const int ahead = j + NB < T ? look_up(j + NB) : p.n_pages;   // in flight beside V's copies
-        copy(&tp.v, j, pages[0]);
-#pragma unroll
-        for (int i = 0; i + 1 < NB; ++i) pages[i] = pages[i + 1];
-        pages[NB - 1] = ahead;
+        page = next;
+        next = ahead;
       }
       tj += T;
     }
     // Every copy has landed before the CTA ends (after a wait that gave up too).
     if (lane < n_ring) {
-      const uint32_t uses = ring_at.use + (lane < ring_at.slot ? 1u : 0u);
+      const uint32_t uses = at.use + (lane < at.slot ? 1u : 0u);
       if (uses > 0) bar_wait(fulls + lane, (uses - 1) & 1, &g_timeouts);
     }
   } else if (F8 && warp >= kCodeWarp) {
@@ -427,7 +415,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
     // tiles ahead and loads one tile ahead.
     const int ct = tid - 32 * kCodeWarp;
     const float zs = p.scale * kLog2e;
-    Ring from, to;
+    Ring from[2], to[2];
     int tj = 0;
     for (bool more = true; more; more = c.next(p, p.mt)) {
       const ItemRows ir = item_rows(p, c);
@@ -449,7 +437,8 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       int page = look_up(0);
       uint32_t record = load(0, page);
       page = look_up(1);
-      auto convert = [&](int j, bool keys) {   // K of tile j with both scales, or V
+      auto convert = [&](int j, int kv) {   // K of tile j with both scales, or V
+        Ring &in = from[kv], &out = to[kv];
         const int t0 = c.tiles.token(c.x + j);
         // Tokens [0, cut) of the tile less [gap0, gap1) are seen by some row.
         auto slot_of = [&](int t) { return min(max(t - t0, 0), kKT); };
@@ -458,22 +447,22 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
         const int gap1 = p.window > 0 ? slot_of(ir.first - p.window + 1) : 0;
 #pragma unroll 1
         for (int s = 0; s < NS; ++s) {
-          wait(&h.code_full[from.slot], from.use & 1, abrt);
-          if (to.use > 0) wait(&h.empty[to.slot], (to.use - 1) & 1, abrt);
-          if (keys && s == 0) {
-            // The slot that is free now held a slab three before this one: tile
-            // j - 4's output is done, so its scales may go.  (At least 1e-30: minus
-            // infinity times it stays minus infinity.)
+          wait(&h.code_full[kv][in.slot], in.use & 1, abrt);
+          if (out.use > 0) wait(&h.empty[kv][out.slot], (out.use - 1) & 1, abrt);
+          if (kv == 0 && s == 0) {
+            // V is at most two tiles ahead of its product, K at most NB: the output
+            // of the tile eight before this one is done, and its scales may go.
+            // (At least 1e-30: minus infinity times it stays minus infinity.)
             const __half2 both = *reinterpret_cast<const __half2*>(&record);
             if (ct < kKT) {
-              sc.k[(tj + j) & 3][ct] = fmaxf(__low2float(both) * zs, 1e-30f);
-              sc.v[(tj + j) & 3][ct] = __high2float(both);
+              sc.k[(tj + j) & 7][ct] = fmaxf(__low2float(both) * zs, 1e-30f);
+              sc.v[(tj + j) & 7][ct] = __high2float(both);
             }
             record = load(j + 1, page);
             page = look_up(j + 2);
           }
-          const uint8_t* src = codes + from.slot * kCodeSlab;
-          uint8_t* dst = ring + to.slot * kSlab;
+          const uint8_t* src = (kv ? v_codes : k_codes) + in.slot * kCodeSlab;
+          uint8_t* dst = (kv ? v_ring : k_ring) + out.slot * kSlab;
           const int piece = ct & 7;   // 16 channels of a token
 #pragma unroll 4
           for (int tk = ct >> 3; tk < kKT; tk += 4 * kCodeWarps) {
@@ -498,50 +487,38 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
           fence_async_smem();
           __syncwarp();
           if (lane == 0) {
-            bar_arrive(&h.full[to.slot]);
-            bar_arrive(&h.code_empty[from.slot]);
+            bar_arrive(&h.full[kv][out.slot]);
+            bar_arrive(&h.code_empty[kv][in.slot]);
           }
-          from.step(tp.n_code_slabs);
-          to.step(n_slabs);
+          in.step(kv ? tp.n_code_v : tp.n_code_k);
+          out.step(kv ? tp.n_v : tp.n_k);
         }
       };
 #pragma unroll 1
       for (int j = 0; j < T + NB - 1; ++j) {
-        if (j < T) convert(j, true);
-        if (j >= NB - 1) convert(j - (NB - 1), false);
+        if (j < T) convert(j, 0);
+        if (j >= NB - 1) convert(j - (NB - 1), 1);
       }
       tj += T;
     }
-  } else if (warp >= kQWarp) {
+  } else if (warp == kQWarp) {
     // ------------------------------------------------------------ Q
+    // An item holds whole rows, so its entries are one box for each 64 channels.
+    const bool leader = elect_one();
+    const int rows = p.mt / p.group;
     int it = 0;
-    for (bool more = true; more; more = c.next(p, p.mt), ++it) {
-      const ItemRows ir = item_rows(p, c);
+    for (bool more = true; more; more = __shfl_sync(0xffffffffu, (int)c.next(p, p.mt), 0) != 0, ++it) {
       if (it > 0) wait(&h.q_free, (uint32_t)((it - 1) & 1), abrt);
-      constexpr int PER = D / 8;                     // 16-byte pieces of an entry
-      constexpr int kStep = kQWarps * 32 / PER;      // entries that the two warps copy together
-      const int piece = lane % PER;
-      int f = (warp - kQWarp) * (32 / PER) + lane / PER;
-      int row = (ir.f0 + f) / p.group, head = ir.f0 + f - row * p.group;
-      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
-                                 ((int64_t)c.s.row0 * p.n_q_heads + c.head * p.group) * D + piece * 8;
-      uint8_t* dst = q_s + (piece >> 3) * q_slab;
-#pragma unroll 4
-      for (; f < p.mt; f += kStep) {
-        const bool ok = f < ir.nf;
-        const int64_t at = ok ? ((int64_t)row * p.n_q_heads + head) * D : 0;
-        cp_async16(dst + f * 128 + (((piece & 7) ^ (f & 7)) << 4), src + at, ok);
-        head += kStep;
-        while (head >= p.group) {
-          head -= p.group;
-          ++row;
-        }
-      }
-      cp_async_wait_all();
-      fence_async_smem();
       __syncwarp();
-      if (lane == 0) bar_arrive(&h.q_full);
+      if (leader) {
+        bar_expect_tx(&h.q_full, 2 * NS * p.mt * 128);
+#pragma unroll 1
+        for (int s = 0; s < 2 * NS; ++s)
+          tma_3d(q_s + s * q_slab, &tp.q, 64 * s, c.head * p.group, c.s.row0 + c.m * rows, &h.q_full);
+      }
+      __syncwarp();
     }
+    bar_wait(&h.q_full, (uint32_t)((it - 1) & 1), &g_timeouts);   // landed before the CTA ends
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
     // The whole warp walks through the tiles with values that are the same in
@@ -549,10 +526,10 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
     // registers.  (One lane that walks alone has to move each of them over:
     // 115 cycles an MMA instead of the 32 and 64 that the products take.)
     const bool leader = elect_one();
-    const uint64_t q_desc = desc_sw128(q_s, 16, 1024), k_desc = desc_sw128(ring, 16, 1024),
-                   v_desc = desc_sw128(ring, kHalf, 1024);
+    const uint64_t q_desc = desc_sw128(q_s, 16, 1024), k_desc = desc_sw128(k_ring, 16, 1024),
+                   v_desc = desc_sw128(v_ring, kHalf, 1024);
     const uint32_t q_step = (uint32_t)q_slab >> 4;
-    Ring at;
+    Ring ka, va;
     int tj = 0, it = 0;
     for (bool more = true; more; more = __shfl_sync(0xffffffffu, (int)c.next(p, p.mt), 0) != 0, ++it) {
       const int T = __shfl_sync(0xffffffffu, c.x1 - c.x, 0);
@@ -561,20 +538,20 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
         const uint32_t d = tmem + (uint32_t)(buf * kKT);
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
-          wait(&h.full[at.slot], at.use & 1, abrt);
+          wait(&h.full[0][ka.slot], ka.use & 1, abrt);
           fence_after();
           if (leader) {
-            const uint64_t k = k_desc + (uint32_t)(at.slot * (kSlab >> 4)), q = q_desc + 2 * s * q_step;
+            const uint64_t k = k_desc + (uint32_t)(ka.slot * (kSlab >> 4)), q = q_desc + 2 * s * q_step;
 #pragma unroll
             for (int x = 0; x < 8; ++x)
               mma_bf16(d, q + (x >> 2) * q_step + 2 * (x & 3), k + (x >> 2) * (kHalf >> 4) + 2 * (x & 3), kIdescS,
                        (s | x) != 0 ? 1u : 0u);
-            commit(&h.empty[at.slot]);
+            commit(&h.empty[0][ka.slot]);
             if (s == NS - 1) commit(&h.s_full[buf]);
             if (s == NS - 1 && j == T - 1) commit(&h.q_free);
           }
           __syncwarp();
-          at.step(n_slabs);
+          ka.step(tp.n_k);
         }
       };
       wait(&h.q_full, (uint32_t)(it & 1), abrt);
@@ -592,19 +569,19 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
         fence_after();
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
-          wait(&h.full[at.slot], at.use & 1, abrt);
+          wait(&h.full[1][va.slot], va.use & 1, abrt);
           fence_after();
           if (leader) {
-            const uint64_t v = v_desc + (uint32_t)(at.slot * (kSlab >> 4));
+            const uint64_t v = v_desc + (uint32_t)(va.slot * (kSlab >> 4));
 #pragma unroll
             for (int x = 0; x < kKT / 16; ++x)
               mma_bf16_ts(tmem + kOCol + (uint32_t)(s * 128), tmem + (uint32_t)(buf * kKT + 8 * x), v + 128 * x, kIdescO,
                           (j | x) != 0 ? 1u : 0u);
-            commit(&h.empty[at.slot]);
+            commit(&h.empty[1][va.slot]);
             if (s == NS - 1) commit(&h.pv_done[(tj + j) & 1]);
           }
           __syncwarp();
-          at.step(n_slabs);
+          va.step(tp.n_v);
         }
       }
       tj += T;
@@ -620,7 +597,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     // Logits to base 2; the scales of an fp8 cache's keys hold the factor already.
     const float zc = F8 ? 1.f : p.scale * kLog2e, move = fminf(kMoveMax / zc, 1e30f);
-    int tj = 0, tiles_before = 0;   // tiles done; tiles of K and V before this item in the ring's order
+    int tj = 0;   // tiles done
     for (bool more = true; more;) {
       const ItemRows ir = item_rows(p, c);
       const int T = c.x1 - c.x;
@@ -658,8 +635,8 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
           }
         }
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        const float* ks = F8 ? sc.k[g & 3] : nullptr;
-        const float* vs = F8 ? sc.v[g & 3] : nullptr;
+        const float* ks = F8 ? sc.k[g & 7] : nullptr;
+        const float* vs = F8 ? sc.v[g & 7] : nullptr;
         auto take_max = [&](uint32_t(&x)[32], uint32_t col) {
           if constexpr (F8) {
 #pragma unroll
@@ -761,13 +738,13 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
         const int cut = slot_of(ir.last + 1);                               // slots from here on,
         const int gap0 = p.window > 0 ? slot_of(p.n_sinks) : 0, gap1 = p.window > 0 ? slot_of(dead + 1) : 0;
         if (!F8 && (cut < kKT || gap0 < gap1)) {                                   // and [gap0, gap1)
-          const int v0 = (tiles_before + place_v<NB>(j, T)) * NS;
+          const int v0 = g * NS;
           for (int s = 0; s < NS; ++s) {
-            const int slot = (v0 + s) % n_slabs;
-            wait(&h.full[slot], (uint32_t)(((v0 + s) / n_slabs) & 1), abrt);
+            const int slot = (v0 + s) % tp.n_v;
+            wait(&h.full[1][slot], (uint32_t)(((v0 + s) / tp.n_v) & 1), abrt);
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
-              uint4* v = reinterpret_cast<uint4*>(ring + slot * kSlab + half * kHalf);
+              uint4* v = reinterpret_cast<uint4*>(v_ring + slot * kSlab + half * kHalf);
 #pragma unroll 1
               for (int i = gap0 * 8 + row; i < gap1 * 8; i += 32 * quarters) v[i] = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll 1
@@ -828,7 +805,6 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
         if (!whole) p.part_lse[part] = lse2;
         else if (p.lse) p.lse[entry] = lse2 * kLn2;
       }
-      tiles_before += 2 * T;
       const Cursor<kKT> last = c;
       more = c.next(p, p.mt);
       if (!more && warp == 0 && lane == 0) describe_part(p, last, st, blockIdx.x);
@@ -879,19 +855,38 @@ bool encode_pages(CUtensorMap* map, const void* base, const PagedParams& p, int 
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_queries(CUtensorMap* map, const PagedParams& p, int head_dim) {
+  PFN_cuTensorMapEncodeTiled_v12000 f = encoder();
+  if (!f) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)p.n_q_heads, (cuuint64_t)p.n_rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)head_dim * 2 * (cuuint64_t)p.n_q_heads};
+  const cuuint32_t box[3] = {64, (cuuint32_t)p.group, (cuuint32_t)(p.mt / p.group)};
+  const cuuint32_t step[3] = {1, 1, 1};
+  return f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p.q), dims, strides, box, step,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, bool F8>
 cudaError_t launch_d(const PagedParams& p, int grid, cudaStream_t st) {
   TcParams tp{};
   tp.p = p;
-  if (!encode_pages(&tp.k, p.k, p, D, F8) || !encode_pages(&tp.v, p.v, p, D, F8)) return cudaErrorInvalidValue;
-  const int fixed = kHeadBytes + (F8 ? (int)sizeof(Scales) : 0) + p.mt * D * 2, room = kSmemLimit - fixed;
-  if (F8) {   // operands of a tile's K and half of V, the rest for codes
-    tp.n_slabs = 3;
-    tp.n_code_slabs = std::min((room - tp.n_slabs * kSlab) / kCodeSlab, kMaxCodeSlabs);
+  if (!encode_pages(&tp.k, p.k, p, D, F8) || !encode_pages(&tp.v, p.v, p, D, F8) || !encode_queries(&tp.q, p, D))
+    return cudaErrorInvalidValue;
+  const int q_slab = (p.mt * 128 + 1023) / 1024 * 1024;
+  const int fixed = kHeadBytes + (F8 ? (int)sizeof(Scales) : 0) + D / 64 * q_slab, room = kSmemLimit - fixed;
+  if (F8) {   // few operands, the rest for codes
+    tp.n_k = 2;
+    tp.n_v = 1;
+    const int n = (room - 3 * kSlab) / kCodeSlab;
+    tp.n_code_k = std::min((n + 1) / 2, kMaxCodeSlabs);
+    tp.n_code_v = std::min(n / 2, kMaxCodeSlabs);
   } else {
-    tp.n_slabs = std::min(room / kSlab, kMaxSlabs);
+    const int n = room / kSlab;
+    tp.n_k = std::min((n + 1) / 2, kMaxSlabs);
+    tp.n_v = std::min(n / 2, kMaxSlabs);
   }
-  const size_t smem = (size_t)fixed + (size_t)tp.n_slabs * kSlab + (size_t)tp.n_code_slabs * kCodeSlab;
+  const size_t smem = (size_t)fixed + (size_t)(tp.n_k + tp.n_v) * kSlab + (size_t)(tp.n_code_k + tp.n_code_v) * kCodeSlab;
   cudaError_t e = allow_dynamic_smem((const void*)paged_tc_kernel<D, F8>, kSmemLimit);
   if (e != cudaSuccess) return e;
   return launch_kernel(paged_tc_kernel<D, F8>, dim3((unsigned)grid), dim3(threads_of(F8)), smem, st, 0u, tp);
