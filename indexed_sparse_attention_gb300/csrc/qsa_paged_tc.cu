@@ -80,11 +80,11 @@ struct TcParams {
 
 // bar_wait with everything behind its first try out of line: the loops of the
 // roles stay small (they share the instruction caches).
-__device__ __noinline__ void wait_slow(uint64_t* b, uint32_t parity, int* abort) {
-  bar_wait(b, parity, &g_timeouts, abort);
+__device__ __noinline__ bool wait_slow(uint64_t* b, uint32_t parity, int* abort) {
+  return bar_wait(b, parity, &g_timeouts, abort);
 }
-__device__ __forceinline__ void wait(uint64_t* b, uint32_t parity, int* abort) {
-  if (!bar_try(b, parity)) wait_slow(b, parity, abort);
+__device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, int* abort) {
+  return bar_try(b, parity) || wait_slow(b, parity, abort);
 }
 
 // Shared memory: this, then Q, then the ring (both on 1,024-byte boundaries).
@@ -334,6 +334,9 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
     const CUtensorMap* map = kv ? &tp.v : &tp.k;
     const int box = min(1 << p.page_shift, kKT), n_box = kKT / box, page_mask = (1 << p.page_shift) - 1;
     constexpr int kBytes = F8 ? kCodeSlab : kSlab;
+    const int n_copies = F8 || n_box == 1 ? n_box : 2 * n_box;   // copies of a slab; lane b's: box b % n_box, ...
+    const int my_box = lane % n_box, half = !F8 && n_box > 1 && lane >= n_box ? 1 : 0;   // ... channels 64 * half on
+    const int at_box = my_box * box * 128 + half * kHalf;
     uint64_t* fulls = F8 ? h.code_full[kv] : h.full[kv];
     uint64_t* empties = F8 ? h.code_empty[kv] : h.empty[kv];
     uint8_t* const to_ring = F8 ? (kv ? v_codes : k_codes) : (kv ? v_ring : k_ring);
@@ -341,14 +344,15 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
     const bool leader = elect_one();
     Ring at;
     int tj = 0;
-    for (bool more = true; more; more = __shfl_sync(0xffffffffu, (int)c.next(p, p.mt), 0) != 0) {
+    bool live = true;   // no wait of this CTA has given up: nothing is issued after one has
+    for (bool more = true; more && live; more = __shfl_sync(0xffffffffu, (int)c.next(p, p.mt), 0) != 0) {
       const ItemRows ir = item_rows(p, c);
       const int T = __shfl_sync(0xffffffffu, c.x1 - c.x, 0);
-      // Lane b: the page of the tile's b-th box; n_pages: nothing to read, -1: no page.
+      // The page of the lane's box of a tile; n_pages: nothing to read, -1: no page.
       auto look_up = [&](int j) {
-        const int t = c.tiles.token(c.x + j) + lane * box;
+        const int t = c.tiles.token(c.x + j) + my_box * box;
         const int end = min(t + box - 1, ir.last);
-        const bool wanted = lane < n_box && t <= ir.last && (p.window == 0 || end > ir.first - p.window || t < p.n_sinks);
+        const bool wanted = lane < n_copies && t <= ir.last && (p.window == 0 || end > ir.first - p.window || t < p.n_sinks);
         const int64_t slot = (int64_t)t >> p.page_shift;
         const int32_t page = wanted && slot < p.table_ld ? __ldcg(p.table + c.seq * p.table_ld + slot) : -1;
         return !wanted ? p.n_pages : (uint32_t)page < (uint32_t)p.n_pages ? page : -1;
@@ -356,14 +360,14 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       // Pages are looked up two tiles ahead.
       int page = look_up(0), next = T > 1 ? look_up(1) : 0;
 #pragma unroll 1
-      for (int j = 0; j < T; ++j) {
+      for (int j = 0; j < T && live; ++j) {
         const int ahead = j + 2 < T ? look_up(j + 2) : 0;
         if (__any_sync(0xffffffffu, page < 0)) {   // copies of missing pages go past the last one
           const bool missing = page < 0;
           const uint32_t bad =
-              __reduce_or_sync(0xffffffffu, missing ? ((1u << (box / 16)) - 1u) << (lane * (box / 16)) : 0u);
+              __reduce_or_sync(0xffffffffu, missing ? ((1u << (box / 16)) - 1u) << (my_box * (box / 16)) : 0u);
           if (missing) page = p.n_pages;
-          if (missing && kv == 0) atomicAdd(&g_bad_pages, 1);
+          if (missing && kv == 0 && half == 0) atomicAdd(&g_bad_pages, 1);
           if (leader && kv == 0) h.bad[(tj + j) & 15] = bad;   // 16-token pieces of the tile
         } else if (leader && kv == 0) {
           h.bad[(tj + j) & 15] = 0u;
@@ -373,26 +377,15 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
         for (int s = 0; s < NS; ++s) {
           uint64_t* full = fulls + at.slot;
           uint8_t* dst = to_ring + at.slot * kBytes;
-          if (at.use > 0) wait(empties + at.slot, (at.use - 1) & 1, abrt);
-          __syncwarp();
+          if (at.use > 0 && !wait(empties + at.slot, (at.use - 1) & 1, abrt)) live = false;
+          live = __all_sync(0xffffffffu, live);
+          if (!live) break;
           if (leader) bar_expect_tx(full, kBytes);
-          if (!F8 && n_box == 1) {   // both halves at once
-            const int to = __shfl_sync(0xffffffffu, page, 0);
-            if (leader) tma_5d(dst, map, slot_in_page, 2 * s, c.head, to, full);
-          } else {
-#pragma unroll 1
-            for (int b = 0; b < n_box; ++b) {
-              const int to = __shfl_sync(0xffffffffu, page, b);
-              if (leader) {
-                if constexpr (F8) {
-                  tma_4d(dst, map, 128 * s, slot_in_page, c.head, to, full);
-                } else {
-                  tma_5d(dst, map, 0, 2 * s, c.head, to, full);
-                  tma_5d(dst + kHalf, map, 0, 2 * s + 1, c.head, to, full);
-                }
-              }
-              dst += box * 128;
-            }
+          __syncwarp();
+          // A lane a box: of 128 channels (fp8, or pages of 128 tokens), or of 64.
+          if (lane < n_copies) {
+            if constexpr (F8) tma_4d(dst + at_box, map, 128 * s, slot_in_page, c.head, page, full);
+            else tma_5d(dst + at_box, map, slot_in_page, 2 * s + half, c.head, page, full);
           }
           __syncwarp();
           at.step(n_ring);
@@ -508,8 +501,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
     const int rows = p.mt / p.group;
     int it = 0;
     for (bool more = true; more; more = __shfl_sync(0xffffffffu, (int)c.next(p, p.mt), 0) != 0, ++it) {
-      if (it > 0) wait(&h.q_free, (uint32_t)((it - 1) & 1), abrt);
-      __syncwarp();
+      if (!__all_sync(0xffffffffu, it == 0 || wait(&h.q_free, (uint32_t)((it - 1) & 1), abrt))) break;
       if (leader) {
         bar_expect_tx(&h.q_full, 2 * NS * p.mt * 128);
 #pragma unroll 1
@@ -530,61 +522,63 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
                    v_desc = desc_sw128(v_ring, kHalf, 1024);
     const uint32_t q_step = (uint32_t)q_slab >> 4;
     Ring ka, va;
-    int tj = 0, it = 0;
+    int it = 0;
+    int s_buf = 0, p_buf = 0, odd = 0;   // buffers of the next logits and the next weights; parity of the next output
+    uint32_t p_phase = 0;                // bit b: the phase of p_full[b] to wait for
+    bool live = true;                    // as above
     for (bool more = true; more; more = __shfl_sync(0xffffffffu, (int)c.next(p, p.mt), 0) != 0, ++it) {
       const int T = __shfl_sync(0xffffffffu, c.x1 - c.x, 0);
-      auto logits = [&](int j) {   // S = Q K_j^T
-        const int buf = (tj + j) % NB;
-        const uint32_t d = tmem + (uint32_t)(buf * kKT);
+      auto logits = [&](bool last) {   // S = Q K^T of the next tile
+        const uint32_t d = tmem + (uint32_t)(s_buf * kKT);
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
-          wait(&h.full[0][ka.slot], ka.use & 1, abrt);
+          live = __all_sync(0xffffffffu, wait(&h.full[0][ka.slot], ka.use & 1, abrt) && live);
           fence_after();
-          if (leader) {
+          if (leader && live) {
             const uint64_t k = k_desc + (uint32_t)(ka.slot * (kSlab >> 4)), q = q_desc + 2 * s * q_step;
 #pragma unroll
             for (int x = 0; x < 8; ++x)
               mma_bf16(d, q + (x >> 2) * q_step + 2 * (x & 3), k + (x >> 2) * (kHalf >> 4) + 2 * (x & 3), kIdescS,
                        (s | x) != 0 ? 1u : 0u);
             commit(&h.empty[0][ka.slot]);
-            if (s == NS - 1) commit(&h.s_full[buf]);
-            if (s == NS - 1 && j == T - 1) commit(&h.q_free);
+            if (s == NS - 1) commit(&h.s_full[s_buf]);
+            if (s == NS - 1 && last) commit(&h.q_free);
           }
           __syncwarp();
           ka.step(tp.n_k);
         }
+        s_buf = s_buf + 1 == NB ? 0 : s_buf + 1;
       };
       wait(&h.q_full, (uint32_t)(it & 1), abrt);
-      fence_after();
-      // Logits run NB - 1 tiles ahead of the output: tile j + NB - 1 takes the
-      // buffer whose weights, tile j - 1's, the product before it reads.
-#pragma unroll
-      for (int j = 0; j < NB - 1; ++j)
-        if (j < T) logits(j);
+#pragma unroll 1
+      for (int j = 0; j < min(NB, T); ++j) logits(j == T - 1);
+      // Then an output product and the logits NB tiles ahead of it, which take the
+      // buffer that its weights leave.
+#pragma unroll 1
       for (int j = 0; j < T; ++j) {
-        if (j + NB - 1 < T) logits(j + NB - 1);
-        const int buf = (tj + j) % NB;
-        wait(&h.p_full[buf], (uint32_t)(((tj + j) / NB) & 1), abrt);
+        live = wait(&h.p_full[p_buf], (p_phase >> p_buf) & 1, abrt) && live;
+        p_phase ^= 1u << p_buf;
         if (j == 0 && it > 0) wait(&h.o_free, (uint32_t)((it - 1) & 1), abrt);
-        fence_after();
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
-          wait(&h.full[1][va.slot], va.use & 1, abrt);
+          live = __all_sync(0xffffffffu, wait(&h.full[1][va.slot], va.use & 1, abrt) && live);
           fence_after();
-          if (leader) {
+          if (leader && live) {
             const uint64_t v = v_desc + (uint32_t)(va.slot * (kSlab >> 4));
 #pragma unroll
             for (int x = 0; x < kKT / 16; ++x)
-              mma_bf16_ts(tmem + kOCol + (uint32_t)(s * 128), tmem + (uint32_t)(buf * kKT + 8 * x), v + 128 * x, kIdescO,
-                          (j | x) != 0 ? 1u : 0u);
+              mma_bf16_ts(tmem + kOCol + (uint32_t)(s * 128), tmem + (uint32_t)(p_buf * kKT + 8 * x), v + 128 * x,
+                          kIdescO, (j | x) != 0 ? 1u : 0u);
             commit(&h.empty[1][va.slot]);
-            if (s == NS - 1) commit(&h.pv_done[(tj + j) & 1]);
+            if (s == NS - 1) commit(&h.pv_done[odd]);
           }
           __syncwarp();
           va.step(tp.n_v);
         }
+        odd ^= 1;
+        p_buf = p_buf + 1 == NB ? 0 : p_buf + 1;
+        if (j + NB < T) logits(j + NB == T - 1);
       }
-      tj += T;
     }
     if (leader) commit(&h.mma_done);   // every MMA has completed before TMEM is released
     __syncwarp();
