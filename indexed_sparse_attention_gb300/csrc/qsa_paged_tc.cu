@@ -95,7 +95,7 @@ __device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, int* abort) {
 // product of tile j - 1, and after that for tile j's.
 struct Head {
   uint64_t full[2][kMaxSlabs], empty[2][kMaxSlabs];   // K, V
-  uint64_t s_full[3], p_full[3], pv_done[2], m_done[2], o_free, q_full, q_free, mma_done;
+  uint64_t s_full[3], p_full[2][3], pv_done[2], m_done[2], o_free, q_full, q_free, mma_done;
   uint64_t code_full[2][kMaxCodeSlabs], code_empty[2][kMaxCodeSlabs];
   int64_t scan[16];
   Start start;
@@ -300,13 +300,14 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
     }
     for (int i = 0; i < 3; ++i) {
       bar_init(&h.s_full[i], 1);
-      bar_init(&h.p_full[i], soft_threads / 2);
+      bar_init(&h.p_full[0][i], quarters);
+      bar_init(&h.p_full[1][i], quarters);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(&h.pv_done[i], 1);
-      bar_init(&h.m_done[i], soft_threads / 2);
+      bar_init(&h.m_done[i], quarters);
     }
-    bar_init(&h.o_free, soft_threads);
+    bar_init(&h.o_free, 2 * quarters);
     bar_init(&h.q_full, 1);
     bar_init(&h.q_free, 1);
     bar_init(&h.mma_done, 1);
@@ -443,7 +444,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
           wait(&h.code_full[kv][in.slot], in.use & 1, abrt);
           if (out.use > 0) wait(&h.empty[kv][out.slot], (out.use - 1) & 1, abrt);
           if (kv == 0 && s == 0) {
-            // V is at most two tiles ahead of its product, K at most NB: the output
+            // V is at most three tiles ahead of its product, K at most NB: the output
             // of the tile eight before this one is done, and its scales may go.
             // (At least 1e-30: minus infinity times it stays minus infinity.)
             const __half2 both = *reinterpret_cast<const __half2*>(&record);
@@ -556,24 +557,33 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       // buffer that its weights leave.
 #pragma unroll 1
       for (int j = 0; j < T; ++j) {
-        live = wait(&h.p_full[p_buf], (p_phase >> p_buf) & 1, abrt) && live;
+        // The weights come in two halves of 64 keys, the first while the second is
+        // still being computed.
+        const uint32_t phase = (p_phase >> p_buf) & 1;
         p_phase ^= 1u << p_buf;
-        if (j == 0 && it > 0) wait(&h.o_free, (uint32_t)((it - 1) & 1), abrt);
+        const Ring first = va;
 #pragma unroll
-        for (int s = 0; s < NS; ++s) {
-          live = __all_sync(0xffffffffu, wait(&h.full[1][va.slot], va.use & 1, abrt) && live);
-          fence_after();
-          if (leader && live) {
-            const uint64_t v = v_desc + (uint32_t)(va.slot * (kSlab >> 4));
+        for (int part = 0; part < 2; ++part) {
+          live = wait(&h.p_full[part][p_buf], phase, abrt) && live;
+          if (part == 0 && j == 0 && it > 0) wait(&h.o_free, (uint32_t)((it - 1) & 1), abrt);
+          va = first;
 #pragma unroll
-            for (int x = 0; x < kKT / 16; ++x)
-              mma_bf16_ts(tmem + kOCol + (uint32_t)(s * 128), tmem + (uint32_t)(p_buf * kKT + 8 * x), v + 128 * x,
-                          kIdescO, (j | x) != 0 ? 1u : 0u);
-            commit(&h.empty[1][va.slot]);
-            if (s == NS - 1) commit(&h.pv_done[odd]);
+          for (int s = 0; s < NS; ++s) {
+            if (part == 0) live = wait(&h.full[1][va.slot], va.use & 1, abrt) && live;
+            live = __all_sync(0xffffffffu, live);
+            fence_after();
+            if (leader && live) {
+              const uint64_t v = v_desc + (uint32_t)(va.slot * (kSlab >> 4));
+#pragma unroll
+              for (int x = 4 * part; x < 4 * part + 4; ++x)
+                mma_bf16_ts(tmem + kOCol + (uint32_t)(s * 128), tmem + (uint32_t)(p_buf * kKT + 8 * x), v + 128 * x,
+                            kIdescO, (j | x) != 0 ? 1u : 0u);
+              if (part == 1) commit(&h.empty[1][va.slot]);
+              if (part == 1 && s == NS - 1) commit(&h.pv_done[odd]);
+            }
+            __syncwarp();
+            va.step(tp.n_v);
           }
-          __syncwarp();
-          va.step(tp.n_v);
         }
         odd ^= 1;
         p_buf = p_buf + 1 == NB ? 0 : p_buf + 1;
@@ -666,7 +676,8 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
         const bool moves = j == 0 ? mx != -INFINITY : mx > before + move;
         const float now = moves ? mx : before;
         h.m_run[row] = now;
-        bar_arrive(&h.m_done[group]);
+        __syncwarp();
+        if (lane == 0) bar_arrive(&h.m_done[group]);
         if (now != m) {
           l *= ex2((m - now) * zc);
           m = now;
@@ -684,6 +695,26 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
             for (int i = 0; i < 32; ++i) xb[i] = __float_as_uint(__uint_as_float(xb[i]) * alpha);
             tmem_st32(lanes + kOCol + (uint32_t)(32 * s), xb);
           }
+        }
+        // Tokens that no row sees: their V may be anything, and P = 0 there.
+        auto slot_of = [&](int t) { return min(max(t - t0, 0), kKT); };   // within the tile
+        const int cut = slot_of(ir.last + 1);                               // slots from here on,
+        const int gap0 = p.window > 0 ? slot_of(p.n_sinks) : 0, gap1 = p.window > 0 ? slot_of(dead + 1) : 0;
+        if (!F8 && (cut < kKT || gap0 < gap1)) {                                   // and [gap0, gap1)
+          const int v0 = g * NS;
+          for (int s = 0; s < NS; ++s) {
+            const int slot = (v0 + s) % tp.n_v;
+            wait(&h.full[1][slot], (uint32_t)(((v0 + s) / tp.n_v) & 1), abrt);
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+              uint4* v = reinterpret_cast<uint4*>(v_ring + slot * kSlab + half * kHalf);
+#pragma unroll 1
+              for (int i = gap0 * 8 + row; i < gap1 * 8; i += 32 * quarters) v[i] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+              for (int i = cut * 8 + row; i < kKT * 8; i += 32 * quarters) v[i] = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+          fence_async_smem();
         }
         // Weights: in bf16 for the product, their sum in 32 bits.  32 logits
         // become 16 columns of weights, always behind the logits still to be read.
@@ -720,34 +751,15 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
           tmem_ld_wait(xb);
           if (col == 0) tmem_ld32_start(s_col + 64, xa);
           weigh(xb, col + 32);
+          tmem_st_wait();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(&h.p_full[col / 64][buf]);
           if (col == 0) tmem_ld_wait(xa);
         }
         float s0, s1;
         unpack2(add2(sum2[0], sum2[1]), s0, s1);
         l += s0 + s1;
-        tmem_st_wait();
-        fence_before();
-        // Tokens that no row sees: their V may be anything, and P = 0 there.
-        auto slot_of = [&](int t) { return min(max(t - t0, 0), kKT); };   // within the tile
-        const int cut = slot_of(ir.last + 1);                               // slots from here on,
-        const int gap0 = p.window > 0 ? slot_of(p.n_sinks) : 0, gap1 = p.window > 0 ? slot_of(dead + 1) : 0;
-        if (!F8 && (cut < kKT || gap0 < gap1)) {                                   // and [gap0, gap1)
-          const int v0 = g * NS;
-          for (int s = 0; s < NS; ++s) {
-            const int slot = (v0 + s) % tp.n_v;
-            wait(&h.full[1][slot], (uint32_t)(((v0 + s) / tp.n_v) & 1), abrt);
-#pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-              uint4* v = reinterpret_cast<uint4*>(v_ring + slot * kSlab + half * kHalf);
-#pragma unroll 1
-              for (int i = gap0 * 8 + row; i < gap1 * 8; i += 32 * quarters) v[i] = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll 1
-              for (int i = cut * 8 + row; i < kKT * 8; i += 32 * quarters) v[i] = make_uint4(0u, 0u, 0u, 0u);
-            }
-          }
-          fence_async_smem();
-        }
-        bar_arrive(&h.p_full[buf]);
       }
       tj += T;
       // The item's result, or this run's part of it: both groups' sums, relative
@@ -793,7 +805,8 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
         }
       }
       fence_before();
-      bar_arrive(&h.o_free);
+      __syncwarp();
+      if (lane == 0) bar_arrive(&h.o_free);
       if (mine && group == 0) {
         const float lse2 = l > 0.f ? fmaf(m, zc, log2f(l)) : -INFINITY;
         if (!whole) p.part_lse[part] = lse2;
@@ -869,10 +882,10 @@ cudaError_t launch_d(const PagedParams& p, int grid, cudaStream_t st) {
     return cudaErrorInvalidValue;
   const int q_slab = (p.mt * 128 + 1023) / 1024 * 1024;
   const int fixed = kHeadBytes + (F8 ? (int)sizeof(Scales) : 0) + D / 64 * q_slab, room = kSmemLimit - fixed;
-  if (F8) {   // few operands, the rest for codes
-    tp.n_k = 2;
-    tp.n_v = 1;
-    const int n = (room - 3 * kSlab) / kCodeSlab;
+  if (F8) {   // operands of a whole tile of V, of K as the codes leave room, the rest for codes
+    tp.n_v = 2;
+    tp.n_k = room >= 4 * kSlab + 4 * kCodeSlab ? 2 : 1;
+    const int n = (room - (tp.n_k + tp.n_v) * kSlab) / kCodeSlab;
     tp.n_code_k = std::min((n + 1) / 2, kMaxCodeSlabs);
     tp.n_code_v = std::min(n / 2, kMaxCodeSlabs);
   } else {
