@@ -1,6 +1,5 @@
-// Attention of a batch's newest rows over a paged K/V cache: the CUDA-core
-// kernel, and the joining of an item's parts (see qsa_paged.cuh for the
-// division of the work).
+// Attention of a batch's newest rows over a paged K/V cache in f32, and the
+// joining of an item's parts (see qsa_paged.cuh for the division of the work).
 //
 // For entry f = (row at position p, query head) of KV head g, with
 // z_t = scale * q . k_t over the tokens t that the row sees:
@@ -10,7 +9,6 @@
 // sums): a tile's new maximum m' rescales l and the output by exp(m - m').
 #include <math.h>
 
-#include "qsa_attn_common.cuh"
 #include "qsa_paged.cuh"
 
 namespace qsa {
@@ -24,160 +22,288 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ int g_bad_pages;   // table entries outside [0, n_pages) among the tokens that a call read
 
-// ------------------------------------------------------------------ CUDA-core kernel
-// 256 threads; an item is 16 entries, a key tile 32 tokens.  Thread -> channel
-// d = tid % D of entries tid / D, tid / D + 256 / D, ...
-constexpr int kSimtThreads = 256;
-constexpr int kSimtMT = 16;
-constexpr int kSimtKT = 32;
+// ------------------------------------------------------------------ f32 caches
+// Products of f32 values on the tensor pipe, by tf32 halves: x = hi + lo with hi
+// = x rounded to 11 significant bits and lo = x - hi rounded likewise, and
+//   a b = hi_a hi_b + hi_a lo_b + lo_a hi_b  (+ lo_a lo_b, below 2^-22 |a b|, left out)
+// with 32-bit accumulation: as exact as a 32-bit sum of rounded products.
+//
+// An item is 16 or 32 entries (one or two times the rows of m16n8k8), a key tile
+// 32 tokens: warp w takes 16 entries (w / 4) and 8 tokens (w % 4) of it and keeps
+// its own maximum, sum and output over its keys, so a tile needs no exchange; the
+// four warps of an entry are joined like an item's parts at its end.
+// K and V rows lie in shared memory padded by four words, which puts the eight
+// rows and four columns (K), or four row pairs and eight columns (V), of a
+// fragment into different banks; two tiles in flight.  A decode's time is that
+// of its K and V from HBM; a chunk's that of the three products.
+constexpr int kF32Threads = 256;
+constexpr int kF32MT = 32;
+constexpr int kF32KT = 32;
 
 template <int D>
-struct SimtLayout {
-  static constexpr int kK = kSimtKT * (D + 1);   // rows padded by one word: threads of a warp read different banks
-  static constexpr int kV = kSimtKT * D;
-  static constexpr size_t floats = kSimtMT * D + kK + kV + kSimtMT * 33 + 3 * kSimtMT;
-  static constexpr size_t bytes = floats * 4 + kSimtKT * 4;
+struct F32Layout {
+  static constexpr int kRow = D + 4;                       // words of a row in shared memory
+  static constexpr int kTile = kF32KT * kRow;              // words of K, or of V, of a tile
+  static constexpr int kQ = 2 * kF32MT * kRow;             // hi, lo
+  static constexpr size_t bytes = 4 * (size_t)(kQ + 4 * kTile);
+  static_assert(8 * 16 * kRow <= 4 * kTile, "the warps' outputs are joined in the tiles' place");
 };
 
-// One element of the cache as a 32-bit value (fp8: without its scale).
-template <int DT>
-__device__ __forceinline__ float cache_value(const void* base, int64_t off) {
-  if constexpr (DT == QSA_F32) return static_cast<const float*>(base)[off];
-  if constexpr (DT == QSA_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(base)[off]);
-  const uint32_t two = attn::e4m3x2_to_bf16x2(static_cast<const uint8_t*>(base)[off]);
-  return bf16_lo(two);
+__device__ __forceinline__ uint32_t tf32(float x) {
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  hi = tf32(x);
+  lo = tf32(x - __uint_as_float(hi));
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float quad_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+__device__ __forceinline__ float quad_sum(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
 
-template <int D, int DT>
-__global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const PagedParams p) {
-  constexpr int HS = kSimtThreads / D, NE = kSimtMT / HS;
+template <int D>
+__global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(const PagedParams p) {
+  using L = F32Layout<D>;
+  constexpr int ROW = L::kRow, NT = D / 8;
+  constexpr float kMoveMax = 8.f;   // as in the bf16 kernel: the maximum moves when a weight would pass 2^8
   extern __shared__ __align__(16) float fsm[];
-  float* q_s = fsm;                                 // [16][D]
-  float* k_s = q_s + kSimtMT * D;                   // [32][D + 1]
-  float* v_s = k_s + SimtLayout<D>::kK;             // [32][D]
-  float* z_s = v_s + SimtLayout<D>::kV;             // [16][33]
-  float* m_s = z_s + kSimtMT * 33;
-  float* l_s = m_s + kSimtMT;
-  float* a_s = l_s + kSimtMT;
-  int* ok_s = reinterpret_cast<int*>(a_s + kSimtMT);
-  __shared__ int64_t scan_s[kSimtThreads / 32];
+  float* q_s = fsm;                 // hi [16][ROW], then lo
+  float* kv_s = fsm + L::kQ;        // two tiles of [K 32][ROW], [V 32][ROW]
+  __shared__ int64_t scan_s[kF32Threads / 32];
   __shared__ Start start_s;
+  __shared__ uint8_t seen_s[2][8];  // tokens of a tile that some row sees and that have a page, four a byte
+  __shared__ float m_s[4][kF32MT], l_s[4][kF32MT];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int gr = lane >> 2, gc = lane & 3;   // a fragment's row group and column
+  const int keys = warp & 3, rows16 = warp >> 2;
   grid_dependency_sync();
-  const Start st = find_run<kSimtThreads, kSimtKT>(p, p.mt, blockIdx.x, gridDim.x, scan_s, &start_s);
-  Cursor<kSimtKT> c;
+  const Start st = find_run<kF32Threads, kF32KT>(p, p.mt, blockIdx.x, gridDim.x, scan_s, &start_s);
+  Cursor<kF32KT> c;
   c.begin(p, p.mt, st);
   const float zscale = p.scale * kLog2e;
-  const int d = tid % D, hs = tid / D;
+  if (st.n == 0 && tid == 0) p.parts[blockIdx.x] = PagedPart{};
   for (bool more = st.n > 0; more;) {
-    const int f0 = c.m * kSimtMT, nf = min(kSimtMT, c.s.n * p.group - f0);
+    const int f0 = c.m * p.mt, nf = min(p.mt, c.s.n * p.group - f0);
     const int pos0 = c.s.len - c.s.n;
+    const int first = pos0 + f0 / p.group, last = pos0 + (f0 + nf - 1) / p.group;
     // Entry f of the item -> its row and query head.
     auto entry = [&](int f) {
       const int r = (f0 + f) / p.group;
-      return ((int64_t)(c.s.row0 + r) * p.n_q_heads + c.head * p.group + (f0 + f - r * p.group));
+      return (int64_t)(c.s.row0 + r) * p.n_q_heads + c.head * p.group + (f0 + f - r * p.group);
     };
+    const int T = c.x1 - c.x;
+    // Thread -> token tid / 8 of a tile, every eighth 16-byte piece of its rows.
+    // Page of the thread's token: -1 where no row sees it, or it has no page.
+    const int mine = tid >> 3;
+    auto look_up = [&](int x) {
+      const int t = c.tiles.token(c.x + x) + mine;
+      if (x >= T || t > last || !(p.window == 0 || t > first - p.window || t < p.n_sinks)) return -1;
+      int32_t page;
+      if (page_of(p, c.seq, t, page)) return (int)page;
+      if ((tid & 7) == 0) atomicAdd(&g_bad_pages, 1);
+      return -1;
+    };
+    auto load = [&](int x, int page) {
+      float* dst = kv_s + (x & 1) * 2 * L::kTile + mine * ROW;
+      const bool ok = page >= 0;
+      const int64_t slot = (c.tiles.token(c.x + x) + mine) & ((1 << p.page_shift) - 1);
+      const int64_t off = ok ? page * p.page_stride + c.head * p.head_stride + slot * p.tok_stride : 0;
+      const float* k = static_cast<const float*>(p.k) + off;
+      const float* v = static_cast<const float*>(p.v) + off;
+#pragma unroll
+      for (int i = tid & 7; i < D / 4; i += 8) {
+        cp_async16(dst + 4 * i, k + 4 * i, ok);
+        cp_async16(dst + L::kTile + 4 * i, v + 4 * i, ok);
+      }
+      const uint32_t b = __ballot_sync(0xffffffffu, ok);   // eight lanes a token
+      if (lane == 0) seen_s[x & 1][warp] = (uint8_t)((b & 1u) | ((b >> 7) & 2u) | ((b >> 14) & 4u) | ((b >> 21) & 8u));
+    };
+    __syncthreads();   // the last item's joining is done with the tiles' place
+    int page = look_up(0);
+    load(0, page);
+    cp_async_commit();
+    page = look_up(1);
+    for (int i = tid; i < p.mt * D; i += kF32Threads) {
+      const int f = i / D, d = i % D;
+      uint32_t hi = 0u, lo = 0u;
+      if (f < nf) split_tf32(static_cast<const float*>(p.q)[entry(f) * D + d], hi, lo);
+      q_s[f * ROW + d] = __uint_as_float(hi);
+      q_s[kF32MT * ROW + f * ROW + d] = __uint_as_float(lo);
+    }
+    float o[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    // Rows gr and gr + 8 of the warp's 16 entries, and what they see.
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    int pos[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) pos[h] = pos0 + (f0 + min(16 * rows16 + gr + 8 * h, nf - 1)) / p.group;
+    for (int x = 0; x < T; ++x) {
+      if (x + 1 < T) load(x + 1, page);
+      cp_async_commit();
+      page = look_up(x + 2);
+      cp_async_wait<1>();
+      __syncthreads();
+      const float* ks = kv_s + (x & 1) * 2 * L::kTile + 8 * keys * ROW;   // the warp's 8 keys
+      const float* vs = ks + L::kTile;
+      const uint32_t seen = seen_s[x & 1][2 * keys] | ((uint32_t)seen_s[x & 1][2 * keys + 1] << 4);
+      const int t0 = c.tiles.token(c.x + x) + 8 * keys;
+      if (seen != 0u && 16 * rows16 < nf) {
+        // Logits of 16 entries x 8 keys: six sums (three products, even and odd
+        // steps), so that the chains stay short.
+        float z[6][4];
+#pragma unroll
+        for (int i = 0; i < 6; ++i) z[i][0] = z[i][1] = z[i][2] = z[i][3] = 0.f;
+        const float* qh = q_s + (16 * rows16 + gr) * ROW + gc;
+        const float* ql = qh + kF32MT * ROW;
+        const float* kk = ks + gr * ROW + gc;
+#pragma unroll 8
+        for (int d = 0; d < D; d += 8) {
+          const int e = (d >> 3) & 1;
+          const uint32_t ah[4] = {__float_as_uint(qh[d]), __float_as_uint(qh[8 * ROW + d]), __float_as_uint(qh[d + 4]),
+                                  __float_as_uint(qh[8 * ROW + d + 4])};
+          const uint32_t al[4] = {__float_as_uint(ql[d]), __float_as_uint(ql[8 * ROW + d]), __float_as_uint(ql[d + 4]),
+                                  __float_as_uint(ql[8 * ROW + d + 4])};
+          uint32_t bh0, bl0, bh1, bl1;
+          split_tf32(kk[d], bh0, bl0);
+          split_tf32(kk[d + 4], bh1, bl1);
+          mma_tf32(z[3 * e], ah, bh0, bh1);
+          mma_tf32(z[3 * e + 1], ah, bl0, bl1);
+          mma_tf32(z[3 * e + 2], al, bh0, bh1);
+        }
+        // Entry (row gr + 8 h, key 2 gc + i) is s[2 h + i].
+        float s[4], mx[2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int h = i >> 1, key = 2 * gc + (i & 1);
+          const float v = ((z[0][i] + z[3][i]) + ((z[1][i] + z[4][i]) + (z[2][i] + z[5][i]))) * zscale;
+          s[i] = ((seen >> key) & 1u) && sees(p, pos[h], t0 + key) ? v : -INFINITY;
+        }
+        bool moves = false;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          mx[h] = quad_max(fmaxf(s[2 * h], s[2 * h + 1]));
+          moves |= mx[h] > m[h] + kMoveMax || (m[h] == -INFINITY && mx[h] != -INFINITY);
+        }
+        if (__any_sync(0xffffffffu, moves)) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float mn = fmaxf(m[h], mx[h]);
+            const float a = mn == -INFINITY ? 1.f : exp2f(m[h] - mn);
+            m[h] = mn;
+            l[h] *= a;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+              o[i][2 * h] *= a;
+              o[i][2 * h + 1] *= a;
+            }
+          }
+        }
+        // Weights, which are the A fragment of the output product as they lie: its
+        // column gc is key 2 gc, its column gc + 4 key 2 gc + 1.
+        float w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int h = i >> 1;
+          w[i] = m[h] == -INFINITY ? 0.f : exp2f(s[i] - m[h]);
+          l[h] += w[i];
+        }
+        uint32_t ph[4], pl[4];
+        split_tf32(w[0], ph[0], pl[0]);
+        split_tf32(w[2], ph[1], pl[1]);
+        split_tf32(w[1], ph[2], pl[2]);
+        split_tf32(w[3], ph[3], pl[3]);
+        const float* vv = vs + 2 * gc * ROW + gr;
+        constexpr int kAt = 4;   // channel blocks whose products are interleaved
+#pragma unroll
+        for (int i = 0; i < NT; i += kAt) {
+          uint32_t bh[kAt][2], bl[kAt][2];
+#pragma unroll
+          for (int k = 0; k < kAt; ++k) {
+            split_tf32(vv[8 * (i + k)], bh[k][0], bl[k][0]);
+            split_tf32(vv[ROW + 8 * (i + k)], bh[k][1], bl[k][1]);
+          }
+#pragma unroll
+          for (int k = 0; k < kAt; ++k) mma_tf32(o[i + k], ph, bh[k][0], bh[k][1]);
+#pragma unroll
+          for (int k = 0; k < kAt; ++k) mma_tf32(o[i + k], ph, bl[k][0], bl[k][1]);
+#pragma unroll
+          for (int k = 0; k < kAt; ++k) mma_tf32(o[i + k], pl, bh[k][0], bh[k][1]);
+        }
+      }
+      __syncthreads();   // the tile may be overwritten
+    }
+    cp_async_wait<0>();
+    // The four warps' outputs, sums and maxima of each entry, joined in shared memory.
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] = quad_sum(l[h]);
+      if (gc == 0) {
+        m_s[keys][16 * rows16 + gr + 8 * h] = m[h];
+        l_s[keys][16 * rows16 + gr + 8 * h] = l[h];
+      }
+    }
+    float* o_s = kv_s + warp * 16 * ROW;   // warp 4 (f / 16) + keys: entry f
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<float2*>(o_s + (gr + 8 * h) * ROW + 8 * i + 2 * gc) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
     __syncthreads();
-    for (int i = tid; i < nf * D; i += kSimtThreads) {
-      const int64_t at = entry(i / D) * D + i % D;
-      q_s[i] = DT == QSA_F32 ? static_cast<const float*>(p.q)[at]
-                             : __bfloat162float(static_cast<const __nv_bfloat16*>(p.q)[at]);
-    }
-    if (tid < kSimtMT) {
-      m_s[tid] = -INFINITY;
-      l_s[tid] = 0.f;
-    }
-    float acc[NE];
-#pragma unroll
-    for (int j = 0; j < NE; ++j) acc[j] = 0.f;
-    // Tokens that no row of the item sees are not read.
-    const int pos_last = pos0 + (f0 + nf - 1) / p.group, pos_first = pos0 + f0 / p.group;
-    for (int x = c.x; x < c.x1; ++x) {
-      const int t0 = c.tiles.token(x);
-      __syncthreads();
-      for (int tk = warp; tk < kSimtKT; tk += kSimtThreads / 32) {
-        const int t = t0 + tk;
-        int32_t page = 0;
-        bool ok = t <= pos_last && (p.window == 0 || t > pos_first - p.window || t < p.n_sinks);
-        if (ok && !page_of(p, c.seq, t, page)) {
-          if (lane == 0) atomicAdd(&g_bad_pages, 1);
-          ok = false;
-        }
-        const int64_t slot = t & ((1 << p.page_shift) - 1);
-        const int64_t off = page * p.page_stride + c.head * p.head_stride + slot * p.tok_stride;
-        float ks = 1.f, vs = 1.f;
-        if (DT == QSA_FP8_E4M3 && ok) {
-          const __half2 s = *reinterpret_cast<const __half2*>(
-              p.kv_scale + 4 * (page * p.s_page_stride + c.head * p.s_head_stride + slot * p.s_tok_stride));
-          ks = __low2float(s);
-          vs = __high2float(s);
-        }
-        for (int e = lane; e < D; e += 32) {
-          k_s[tk * (D + 1) + e] = ok ? cache_value<DT>(p.k, off + e) * ks : 0.f;
-          v_s[tk * D + e] = ok ? cache_value<DT>(p.v, off + e) * vs : 0.f;
-        }
-        if (lane == 0) ok_s[tk] = ok ? 1 : 0;
-      }
-      __syncthreads();
-      for (int i = tid; i < nf * kSimtKT; i += kSimtThreads) {
-        const int f = i / kSimtKT, tk = i % kSimtKT;
-        float dot = 0.f;
-        for (int e = 0; e < D; ++e) dot = fmaf(q_s[f * D + e], k_s[tk * (D + 1) + e], dot);
-        z_s[f * 33 + tk] = ok_s[tk] && sees(p, pos0 + (f0 + f) / p.group, t0 + tk) ? dot * zscale : -INFINITY;
-      }
-      __syncthreads();
-      for (int f = warp; f < nf; f += kSimtThreads / 32) {
-        const float z = z_s[f * 33 + lane], mo = m_s[f];
-        float mn = fmaxf(mo, z);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-        const float pz = mn == -INFINITY ? 0.f : exp2f(z - mn);
-        float sum = pz;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        z_s[f * 33 + lane] = pz;
-        if (lane == 0) {
-          const float alpha = mo == -INFINITY ? 0.f : exp2f(mo - mn);
-          a_s[f] = alpha;
-          m_s[f] = mn;
-          l_s[f] = l_s[f] * alpha + sum;
-        }
-      }
-      __syncthreads();
-#pragma unroll
-      for (int j = 0; j < NE; ++j) {
-        const int f = hs + j * HS;
-        if (f < nf) {
-          float a = acc[j] * a_s[f];
-          for (int tk = 0; tk < kSimtKT; ++tk) a = fmaf(z_s[f * 33 + tk], v_s[tk * D + d], a);
-          acc[j] = a;
-        }
-      }
-    }
-    // The item's result, or this run's part of it.
     const bool whole = c.whole();
     const int64_t slot = whole ? 0 : (int64_t)c.slot(blockIdx.x) * p.mt;
+    for (int f = warp; f < nf; f += kF32Threads / 32) {
+      float M = -INFINITY, W = 0.f, e[4];
 #pragma unroll
-    for (int j = 0; j < NE; ++j) {
-      const int f = hs + j * HS;
-      if (f >= nf) continue;
-      const float l = l_s[f];
-      const float o = l > 0.f ? acc[j] / l : 0.f;
-      if (!whole) {
-        p.part_o[(slot + f) * D + d] = o;
-        if (d == 0) p.part_lse[slot + f] = l > 0.f ? m_s[f] + log2f(l) : -INFINITY;
-        continue;
+      for (int k = 0; k < 4; ++k) M = fmaxf(M, m_s[k][f]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        e[k] = m_s[k][f] == -INFINITY ? 0.f : exp2f(m_s[k][f] - M);
+        W = fmaf(e[k], l_s[k][f], W);
       }
-      const int64_t at = entry(f);
-      if (p.out_dtype == QSA_F32) static_cast<float*>(p.out)[at * D + d] = o;
-      else static_cast<__nv_bfloat16*>(p.out)[at * D + d] = __float2bfloat16(o);
-      if (d == 0 && p.lse) p.lse[at] = l > 0.f ? (m_s[f] + log2f(l)) * kLn2 : -INFINITY;
+      const float inv = W > 0.f ? 1.f / W : 0.f;
+      const int64_t at = whole ? entry(f) : slot + f;
+      for (int d = 4 * lane; d < D; d += 128) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float4 y = *reinterpret_cast<const float4*>(kv_s + ((4 * (f >> 4) + k) * 16 + (f & 15)) * ROW + d);
+          x.x = fmaf(e[k], y.x, x.x);
+          x.y = fmaf(e[k], y.y, x.y);
+          x.z = fmaf(e[k], y.z, x.z);
+          x.w = fmaf(e[k], y.w, x.w);
+        }
+        x = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+        if (!whole || p.out_dtype == QSA_F32) {
+          *reinterpret_cast<float4*>((whole ? static_cast<float*>(p.out) : p.part_o) + at * D + d) = x;
+        } else {
+          __nv_bfloat162* to = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + at * D + d);
+          to[0] = __floats2bfloat162_rn(x.x, x.y);
+          to[1] = __floats2bfloat162_rn(x.z, x.w);
+        }
+      }
+      if (lane == 0) {
+        const float lse2 = W > 0.f ? M + log2f(W) : -INFINITY;
+        if (!whole) p.part_lse[at] = lse2;
+        else if (p.lse) p.lse[at] = lse2 * kLn2;
+      }
     }
-    Cursor<kSimtKT> last = c;
+    const Cursor<kF32KT> done = c;
     more = c.next(p, p.mt);
-    if (!more && tid == 0) describe_part(p, last, st, blockIdx.x);
+    if (!more && tid == 0) describe_part(p, done, st, blockIdx.x);
   }
-  if (st.n == 0 && tid == 0) p.parts[blockIdx.x] = PagedPart{};
 }
 
 // ------------------------------------------------------------------ joining
@@ -319,22 +445,18 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
   }
 }
 
-template <int D, int DT>
-cudaError_t launch_simt(const PagedParams& p, int grid, cudaStream_t st) {
-  const size_t smem = SimtLayout<D>::bytes;
-  cudaError_t e = allow_dynamic_smem((const void*)paged_simt_kernel<D, DT>, smem);
+template <int D>
+cudaError_t launch_f32(const PagedParams& p, int grid, cudaStream_t st) {
+  const size_t smem = F32Layout<D>::bytes;
+  cudaError_t e = allow_dynamic_smem((const void*)paged_f32_kernel<D>, smem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(paged_simt_kernel<D, DT>, dim3((unsigned)grid), dim3(kSimtThreads), smem, st, 0u, p);
+  return launch_kernel(paged_f32_kernel<D>, dim3((unsigned)grid), dim3(kF32Threads), smem, st, 0u, p);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_simt(const PagedParams& p, qsa_dtype kv_dtype, int head_dim, int grid, cudaStream_t st) {
-  if (kv_dtype == QSA_F32)
-    return head_dim == 256 ? launch_simt<256, QSA_F32>(p, grid, st) : launch_simt<128, QSA_F32>(p, grid, st);
-  if (kv_dtype == QSA_BF16)
-    return head_dim == 256 ? launch_simt<256, QSA_BF16>(p, grid, st) : launch_simt<128, QSA_BF16>(p, grid, st);
-  return head_dim == 256 ? launch_simt<256, QSA_FP8_E4M3>(p, grid, st) : launch_simt<128, QSA_FP8_E4M3>(p, grid, st);
+cudaError_t launch_paged_f32(const PagedParams& p, int head_dim, int grid, cudaStream_t st) {
+  return head_dim == 256 ? launch_f32<256>(p, grid, st) : launch_f32<128>(p, grid, st);
 }
 
 cudaError_t launch_paged_merge(const PagedParams& p, int head_dim, int runs, cudaStream_t st) {

@@ -112,7 +112,8 @@ cudaError_t launch_pages_copy(const PageCaches& caches, const int32_t* src, cons
 size_t pages_workspace_bytes(const qsa_page_pool& pool);
 int pages_unserved_take();
 
-cudaError_t launch_paged_simt(const PagedParams& p, qsa_dtype kv_dtype, int head_dim, int grid, cudaStream_t st);
+// f32 caches (qsa_paged.cu).
+cudaError_t launch_paged_f32(const PagedParams& p, int head_dim, int grid, cudaStream_t st);
 // On the tensor cores (qsa_paged_tc.cu): bf16 and fp8 caches.
 cudaError_t launch_paged_tc(const PagedParams& p, qsa_dtype kv_dtype, int head_dim, int grid, cudaStream_t st);
 int paged_tc_bad_pages_take();

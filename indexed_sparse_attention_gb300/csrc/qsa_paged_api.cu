@@ -74,8 +74,8 @@ Plan plan_attn(const qsa_paged_batch* b, const qsa_attn_config* cfg) {
     pl.mt = group * std::max(1, std::min(b->max_rows, 128 / group));
     pl.grid = device_sm_count();
   } else {
-    pl.mt = 16;
-    pl.grid = 2 * device_sm_count();
+    pl.mt = (int64_t)b->max_rows * (cfg->n_q_heads / cfg->n_kv_heads) <= 16 ? 16 : 32;
+    pl.grid = (cfg->head_dim == 128 ? 2 : 1) * device_sm_count();   // as the shared memory holds
   }
   if (cfg->n_splits > 0) pl.grid = std::min(pl.grid, cfg->n_splits);
   return pl;
@@ -161,7 +161,7 @@ QSA_API qsa_status qsa_paged_attn(const qsa_paged_cache* cache, const qsa_paged_
   p.part_o = reinterpret_cast<float*>(ws + out_offset(pl));
   cudaStream_t st = as_stream(stream);
   cudaError_t e = pl.tensor_cores ? launch_paged_tc(p, cfg->kv_dtype, cfg->head_dim, pl.grid, st)
-                                  : launch_paged_simt(p, cfg->kv_dtype, cfg->head_dim, pl.grid, st);
+                                  : launch_paged_f32(p, cfg->head_dim, pl.grid, st);
   if (e == cudaSuccess) e = launch_paged_merge(p, cfg->head_dim, pl.grid, st);
   return e == cudaSuccess ? ok() : cuda_fail(e, fn);
 }
