@@ -124,9 +124,9 @@ QSA_API int32_t qsa_version(void) { return QSA_VERSION; }
 
 QSA_API int32_t qsa_wait_timeouts(void) {
   const int a = score_wait_timeouts(), b = score_tc_wait_timeouts(), c = attn_tc_wait_timeouts(),
-            d = paged_tc_wait_timeouts();
-  if (a < 0 || b < 0 || c < 0 || d < 0) return -1;
-  return a + b + c + d;
+            d = paged_tc_wait_timeouts(), e = paged_f32_wait_timeouts();
+  if (a < 0 || b < 0 || c < 0 || d < 0 || e < 0) return -1;
+  return a + b + c + d + e;
 }
 
 QSA_API qsa_status qsa_check_device_status(void* stream) {

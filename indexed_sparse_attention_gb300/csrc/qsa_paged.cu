@@ -10,16 +10,19 @@
 #include <math.h>
 
 #include "qsa_paged.cuh"
+#include "qsa_tc.cuh"
 
 namespace qsa {
 
 namespace {
 
 using namespace paged;
+using namespace tc;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+__device__ int g_f32_timeouts;
 __device__ int g_bad_pages;   // table entries outside [0, n_pages) among the tokens that a call read
 
 // ------------------------------------------------------------------ f32 caches
@@ -32,37 +35,44 @@ __device__ int g_bad_pages;   // table entries outside [0, n_pages) among the to
 // 32 tokens: warp w takes 16 entries (w / 4) and 8 tokens (w % 4) of it and keeps
 // its own maximum, sum and output over its keys, so a tile needs no exchange; the
 // four warps of an entry are joined like an item's parts at its end.
-// K and V rows lie in shared memory padded by four words, which puts the eight
-// rows and four columns (K), or four row pairs and eight columns (V), of a
-// fragment into different banks; two tiles in flight.  A decode's time is that
-// of its K and V from HBM; a chunk's that of the three products.
+// Each row of K and V is one bulk copy, two tiles in flight.  Rows in shared memory
+// are padded, Q's and K's by eight words and V's by four, which puts the eight
+// rows and four column pairs (Q, K), or four row pairs and eight columns (V), of
+// a fragment into different banks.
 constexpr int kF32Threads = 256;
 constexpr int kF32MT = 32;
 constexpr int kF32KT = 32;
 
 template <int D>
 struct F32Layout {
-  static constexpr int kRow = D + 4;                       // words of a row in shared memory
-  static constexpr int kTile = kF32KT * kRow;              // words of K, or of V, of a tile
+  static constexpr int kRow = D + 8, kRowV = D + 4;        // words of a row of Q and K, and of V
+  static constexpr int kK = kF32KT * kRow, kTile = kK + kF32KT * kRowV;   // words of K, and of K and V, of a tile
   static constexpr int kQ = 2 * kF32MT * kRow;             // hi, lo
-  static constexpr size_t bytes = 4 * (size_t)(kQ + 4 * kTile);
-  static_assert(8 * 16 * kRow <= 4 * kTile, "the warps' outputs are joined in the tiles' place");
+  static constexpr size_t bytes = 4 * (size_t)(kQ + 2 * kTile);
+  static_assert(8 * 16 * kRowV <= 2 * kTile, "the warps' outputs are joined in the tiles' place");
+  static_assert((4 * kRow) % 16 == 0 && (4 * kRowV) % 16 == 0 && (4 * kQ) % 16 == 0, "rows on 16-byte boundaries");
 };
 
-__device__ __forceinline__ uint32_t tf32(float x) {
-  uint32_t r;
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
-  return r;
-}
+// The halves of x.  Adding half a unit of the 11th significant bit to the pattern
+// and clearing the 13 bits below rounds to nearest (halves away from zero); of lo
+// the tensor pipe ignores those bits itself.  (In plain integer operations: the
+// conversion instruction took most of the kernel's time.)
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-  hi = tf32(x);
-  lo = tf32(x - __uint_as_float(hi));
+  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;
 }
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm(
       "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// bytes (a multiple of 16) from global to shared memory, counted by the barrier.
+__device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                   smem_addr(dst)),
+               "l"(src), "r"(bytes), "r"(smem_addr(bar))
+               : "memory");
 }
 __device__ __forceinline__ float quad_max(float v) {
   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
@@ -76,24 +86,34 @@ __device__ __forceinline__ float quad_sum(float v) {
 template <int D>
 __global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(const PagedParams p) {
   using L = F32Layout<D>;
-  constexpr int ROW = L::kRow, NT = D / 8;
+  constexpr int ROW = L::kRow, ROWV = L::kRowV, NT = D / 8;
   constexpr float kMoveMax = 8.f;   // as in the bf16 kernel: the maximum moves when a weight would pass 2^8
   extern __shared__ __align__(16) float fsm[];
   float* q_s = fsm;                 // hi [16][ROW], then lo
-  float* kv_s = fsm + L::kQ;        // two tiles of [K 32][ROW], [V 32][ROW]
+  float* kv_s = fsm + L::kQ;        // two tiles of [K 32][ROW], [V 32][ROWV]
   __shared__ int64_t scan_s[kF32Threads / 32];
   __shared__ Start start_s;
-  __shared__ uint8_t seen_s[2][8];  // tokens of a tile that some row sees and that have a page, four a byte
+  __shared__ uint64_t full[2];
+  __shared__ int abort_s;
+  __shared__ uint8_t seen_s[2][4];  // tokens of a tile that some row sees and that have a page
   __shared__ float m_s[4][kF32MT], l_s[4][kF32MT];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gr = lane >> 2, gc = lane & 3;   // a fragment's row group and column
   const int keys = warp & 3, rows16 = warp >> 2;
+  if (tid == 0) {
+    bar_init(&full[0], kF32Threads);
+    bar_init(&full[1], kF32Threads);
+    bar_init_fence();
+    abort_s = 0;
+  }
+  __syncthreads();
   grid_dependency_sync();
   const Start st = find_run<kF32Threads, kF32KT>(p, p.mt, blockIdx.x, gridDim.x, scan_s, &start_s);
   Cursor<kF32KT> c;
   c.begin(p, p.mt, st);
   const float zscale = p.scale * kLog2e;
   if (st.n == 0 && tid == 0) p.parts[blockIdx.x] = PagedPart{};
+  int tj = 0;   // tiles done: tile g of the run is in buffer g & 1, phase g >> 1
   for (bool more = st.n > 0; more;) {
     const int f0 = c.m * p.mt, nf = min(p.mt, c.s.n * p.group - f0);
     const int pos0 = c.s.len - c.s.n;
@@ -104,43 +124,70 @@ __global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(const PagedParam
       return (int64_t)(c.s.row0 + r) * p.n_q_heads + c.head * p.group + (f0 + f - r * p.group);
     };
     const int T = c.x1 - c.x;
-    // Thread -> token tid / 8 of a tile, every eighth 16-byte piece of its rows.
+    // Thread i < 64 -> token i / 2 of a tile, its K or its V row.
     // Page of the thread's token: -1 where no row sees it, or it has no page.
-    const int mine = tid >> 3;
+    const int mine = tid >> 1, is_v = tid & 1;
     auto look_up = [&](int x) {
+      if (tid >= 2 * kF32KT || x >= T) return -1;
       const int t = c.tiles.token(c.x + x) + mine;
-      if (x >= T || t > last || !(p.window == 0 || t > first - p.window || t < p.n_sinks)) return -1;
+      if (t > last || !(p.window == 0 || t > first - p.window || t < p.n_sinks)) return -1;
       int32_t page;
       if (page_of(p, c.seq, t, page)) return (int)page;
-      if ((tid & 7) == 0) atomicAdd(&g_bad_pages, 1);
+      if (!is_v) atomicAdd(&g_bad_pages, 1);
       return -1;
     };
-    auto load = [&](int x, int page) {
-      float* dst = kv_s + (x & 1) * 2 * L::kTile + mine * ROW;
-      const bool ok = page >= 0;
-      const int64_t slot = (c.tiles.token(c.x + x) + mine) & ((1 << p.page_shift) - 1);
-      const int64_t off = ok ? page * p.page_stride + c.head * p.head_stride + slot * p.tok_stride : 0;
-      const float* k = static_cast<const float*>(p.k) + off;
-      const float* v = static_cast<const float*>(p.v) + off;
+    auto load = [&](int x, int page) {   // every thread arrives; a row that is not there becomes zeros
+      const int b = (tj + x) & 1;
+      if (tid < 2 * kF32KT) {
+        float* dst = kv_s + b * L::kTile + (is_v ? L::kK + mine * ROWV : mine * ROW);
+        const bool ok = page >= 0;
+        if (ok) {
+          const int64_t slot = (c.tiles.token(c.x + x) + mine) & ((1 << p.page_shift) - 1);
+          const float* src = static_cast<const float*>(is_v ? p.v : p.k) + page * p.page_stride +
+                             c.head * p.head_stride + slot * p.tok_stride;
+          fence_async_smem();   // (zeros may have been stored there)
+          bar_expect_tx(&full[b], 4 * D);
+          bulk_copy(dst, src, 4 * D, &full[b]);
+        } else {
+          for (int i = 0; i < D / 4; ++i) reinterpret_cast<float4*>(dst)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          bar_arrive(&full[b]);
+        }
+        const uint32_t v = __ballot_sync(0xffffffffu, ok);   // two lanes a token, 16 tokens a warp
+        uint32_t bits = 0u;
 #pragma unroll
-      for (int i = tid & 7; i < D / 4; i += 8) {
-        cp_async16(dst + 4 * i, k + 4 * i, ok);
-        cp_async16(dst + L::kTile + 4 * i, v + 4 * i, ok);
+        for (int i = 0; i < 16; ++i) bits |= ((v >> (2 * i)) & 1u) << i;
+        if (lane == 0) seen_s[b][2 * warp] = (uint8_t)bits, seen_s[b][2 * warp + 1] = (uint8_t)(bits >> 8);
+      } else {
+        bar_arrive(&full[b]);
       }
-      const uint32_t b = __ballot_sync(0xffffffffu, ok);   // eight lanes a token
-      if (lane == 0) seen_s[x & 1][warp] = (uint8_t)((b & 1u) | ((b >> 7) & 2u) | ((b >> 14) & 4u) | ((b >> 21) & 8u));
     };
-    __syncthreads();   // the last item's joining is done with the tiles' place
+    fence_async_smem();   // (plain stores before the copies that follow)
+    __syncthreads();      // the last item's joining is done with the tiles' place
     int page = look_up(0);
     load(0, page);
-    cp_async_commit();
     page = look_up(1);
-    for (int i = tid; i < p.mt * D; i += kF32Threads) {
-      const int f = i / D, d = i % D;
-      uint32_t hi = 0u, lo = 0u;
-      if (f < nf) split_tf32(static_cast<const float*>(p.q)[entry(f) * D + d], hi, lo);
-      q_s[f * ROW + d] = __uint_as_float(hi);
-      q_s[kF32MT * ROW + f * ROW + d] = __uint_as_float(lo);
+    // Q, eight 16-byte pieces of it a thread at a time.
+    for (int i0 = tid; i0 < p.mt * (D / 4); i0 += 4 * kF32Threads) {
+      float4 x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = i0 + k * kF32Threads, f = i / (D / 4);
+        x[k] = f < nf ? __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + entry(f) * D) + i % (D / 4))
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = i0 + k * kF32Threads, f = i / (D / 4);
+        if (f >= p.mt) continue;
+        uint4 hi, lo;
+        split_tf32(x[k].x, hi.x, lo.x);
+        split_tf32(x[k].y, hi.y, lo.y);
+        split_tf32(x[k].z, hi.z, lo.z);
+        split_tf32(x[k].w, hi.w, lo.w);
+        float* to = q_s + f * ROW + 4 * (i % (D / 4));
+        *reinterpret_cast<uint4*>(to) = hi;
+        *reinterpret_cast<uint4*>(to + kF32MT * ROW) = lo;
+      }
     }
     float o[NT][4];
 #pragma unroll
@@ -152,13 +199,13 @@ __global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(const PagedParam
     for (int h = 0; h < 2; ++h) pos[h] = pos0 + (f0 + min(16 * rows16 + gr + 8 * h, nf - 1)) / p.group;
     for (int x = 0; x < T; ++x) {
       if (x + 1 < T) load(x + 1, page);
-      cp_async_commit();
       page = look_up(x + 2);
-      cp_async_wait<1>();
-      __syncthreads();
-      const float* ks = kv_s + (x & 1) * 2 * L::kTile + 8 * keys * ROW;   // the warp's 8 keys
-      const float* vs = ks + L::kTile;
-      const uint32_t seen = seen_s[x & 1][2 * keys] | ((uint32_t)seen_s[x & 1][2 * keys + 1] << 4);
+      const int b = (tj + x) & 1;
+      bar_wait(&full[b], (uint32_t)(((tj + x) >> 1) & 1), &g_f32_timeouts, &abort_s);
+      if (x == 0) __syncthreads();   // Q is there
+      const float* ks = kv_s + b * L::kTile + 8 * keys * ROW;   // the warp's 8 keys
+      const float* vs = kv_s + b * L::kTile + L::kK + 8 * keys * ROWV;
+      const uint32_t seen = seen_s[b][keys];
       const int t0 = c.tiles.token(c.x + x) + 8 * keys;
       if (seen != 0u && 16 * rows16 < nf) {
         // Logits of 16 entries x 8 keys: six sums (three products, even and odd
@@ -166,19 +213,20 @@ __global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(const PagedParam
         float z[6][4];
 #pragma unroll
         for (int i = 0; i < 6; ++i) z[i][0] = z[i][1] = z[i][2] = z[i][3] = 0.f;
-        const float* qh = q_s + (16 * rows16 + gr) * ROW + gc;
+        // (A step's column gc is channel 2 gc, its column gc + 4 channel 2 gc + 1.)
+        const float* qh = q_s + (16 * rows16 + gr) * ROW + 2 * gc;
         const float* ql = qh + kF32MT * ROW;
-        const float* kk = ks + gr * ROW + gc;
+        const float* kk = ks + gr * ROW + 2 * gc;
+        auto two = [](const float* x) { return *reinterpret_cast<const uint2*>(x); };
 #pragma unroll 8
         for (int d = 0; d < D; d += 8) {
           const int e = (d >> 3) & 1;
-          const uint32_t ah[4] = {__float_as_uint(qh[d]), __float_as_uint(qh[8 * ROW + d]), __float_as_uint(qh[d + 4]),
-                                  __float_as_uint(qh[8 * ROW + d + 4])};
-          const uint32_t al[4] = {__float_as_uint(ql[d]), __float_as_uint(ql[8 * ROW + d]), __float_as_uint(ql[d + 4]),
-                                  __float_as_uint(ql[8 * ROW + d + 4])};
+          const uint2 h0 = two(qh + d), h1 = two(qh + 8 * ROW + d), l0 = two(ql + d), l1 = two(ql + 8 * ROW + d);
+          const uint2 k = two(kk + d);
+          const uint32_t ah[4] = {h0.x, h1.x, h0.y, h1.y}, al[4] = {l0.x, l1.x, l0.y, l1.y};
           uint32_t bh0, bl0, bh1, bl1;
-          split_tf32(kk[d], bh0, bl0);
-          split_tf32(kk[d + 4], bh1, bl1);
+          split_tf32(__uint_as_float(k.x), bh0, bl0);
+          split_tf32(__uint_as_float(k.y), bh1, bl1);
           mma_tf32(z[3 * e], ah, bh0, bh1);
           mma_tf32(z[3 * e + 1], ah, bl0, bl1);
           mma_tf32(z[3 * e + 2], al, bh0, bh1);
@@ -225,7 +273,7 @@ __global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(const PagedParam
         split_tf32(w[2], ph[1], pl[1]);
         split_tf32(w[1], ph[2], pl[2]);
         split_tf32(w[3], ph[3], pl[3]);
-        const float* vv = vs + 2 * gc * ROW + gr;
+        const float* vv = vs + 2 * gc * ROWV + gr;
         constexpr int kAt = 4;   // channel blocks whose products are interleaved
 #pragma unroll
         for (int i = 0; i < NT; i += kAt) {
@@ -233,7 +281,7 @@ __global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(const PagedParam
 #pragma unroll
           for (int k = 0; k < kAt; ++k) {
             split_tf32(vv[8 * (i + k)], bh[k][0], bl[k][0]);
-            split_tf32(vv[ROW + 8 * (i + k)], bh[k][1], bl[k][1]);
+            split_tf32(vv[ROWV + 8 * (i + k)], bh[k][1], bl[k][1]);
           }
 #pragma unroll
           for (int k = 0; k < kAt; ++k) mma_tf32(o[i + k], ph, bh[k][0], bh[k][1]);
@@ -245,7 +293,7 @@ __global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(const PagedParam
       }
       __syncthreads();   // the tile may be overwritten
     }
-    cp_async_wait<0>();
+    tj += T;
     // The four warps' outputs, sums and maxima of each entry, joined in shared memory.
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -255,12 +303,12 @@ __global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(const PagedParam
         l_s[keys][16 * rows16 + gr + 8 * h] = l[h];
       }
     }
-    float* o_s = kv_s + warp * 16 * ROW;   // warp 4 (f / 16) + keys: entry f
+    float* o_s = kv_s + warp * 16 * ROWV;   // warp 4 (f / 16) + keys: entry f
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<float2*>(o_s + (gr + 8 * h) * ROW + 8 * i + 2 * gc) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
+        *reinterpret_cast<float2*>(o_s + (gr + 8 * h) * ROWV + 8 * i + 2 * gc) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
     __syncthreads();
     const bool whole = c.whole();
     const int64_t slot = whole ? 0 : (int64_t)c.slot(blockIdx.x) * p.mt;
@@ -279,7 +327,7 @@ __global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(const PagedParam
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float4 y = *reinterpret_cast<const float4*>(kv_s + ((4 * (f >> 4) + k) * 16 + (f & 15)) * ROW + d);
+          const float4 y = *reinterpret_cast<const float4*>(kv_s + ((4 * (f >> 4) + k) * 16 + (f & 15)) * ROWV + d);
           x.x = fmaf(e[k], y.x, x.x);
           x.y = fmaf(e[k], y.y, x.y);
           x.z = fmaf(e[k], y.z, x.z);
@@ -465,6 +513,11 @@ cudaError_t launch_paged_merge(const PagedParams& p, int head_dim, int runs, cud
   const dim3 grid((unsigned)(4 * device_sm_count())), block(kJoinThreads);
   return head_dim == 256 ? launch_kernel(paged_join_kernel<256>, grid, block, 0, st, 0u, p, runs)
                          : launch_kernel(paged_join_kernel<128>, grid, block, 0, st, 0u, p, runs);
+}
+
+int paged_f32_wait_timeouts() {
+  int v = 0;
+  return cudaMemcpyFromSymbol(&v, g_f32_timeouts, sizeof(int)) == cudaSuccess ? v : -1;
 }
 
 int paged_bad_pages_take() { return take_counter(g_bad_pages); }

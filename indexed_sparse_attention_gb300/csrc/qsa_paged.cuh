@@ -120,6 +120,7 @@ int paged_tc_bad_pages_take();
 int paged_tc_wait_timeouts();
 cudaError_t launch_paged_merge(const PagedParams& p, int head_dim, int runs, cudaStream_t st);
 int paged_bad_pages_take();
+int paged_f32_wait_timeouts();
 
 namespace paged {
 
@@ -248,43 +249,91 @@ __device__ __forceinline__ void place_in_seq(const PagedParams& p, int mt, int i
   st.s = s;
 }
 
-// find_run for at most 32 sequences of few items: every warp finds the run by
-// itself, one sequence a lane, with one round of loads and no barrier.  False
-// (for all warps) where the call is larger.
+// Key tiles of item m of a sequence, all KV heads; 0 behind its last item.
+template <int KT>
+__device__ __forceinline__ uint32_t item_cost(const PagedParams& p, int mt, const SeqRows& s, int items, int m) {
+  return m < items ? (uint32_t)item_tiles<KT>(p, s, mt, m).count * (uint32_t)p.n_kv_heads : 0u;
+}
+__device__ __forceinline__ uint32_t warp_prefix(uint32_t v, int lane) {   // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t up = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += up;
+  }
+  return v;
+}
+
+// find_run for at most 32 sequences: every warp finds the run by itself, one
+// sequence a lane (a sequence of several items: one item a lane), with one round
+// of loads and no barrier.  False (for all warps) where the call is larger.
 template <int KT>
 __device__ __forceinline__ bool find_run_small(const PagedParams& p, int mt, int cta, int n_ctas, Start& st) {
   if (p.n_seqs > 32) return false;
   const int lane = threadIdx.x & 31;
-  SeqRows s{0, 0, 0};
-  int items = 0;
-  uint32_t cost = 0;
-  if (lane < p.n_seqs) {
-    s = seq_rows(p, lane);
-    items = item_count(p, s, mt);
-    if (items <= kLongSeq)
-      for (int m = 0; m < items; ++m) cost += (uint32_t)item_tiles<KT>(p, s, mt, m).count;
+  SeqRows mine{0, 0, 0};
+  if (lane < p.n_seqs) mine = seq_rows(p, lane);
+  const int items = lane < p.n_seqs ? item_count(p, mine, mt) : 0;
+  auto of = [&](int i) {   // lane i's sequence
+    return SeqRows{__shfl_sync(0xffffffffu, mine.len, i), __shfl_sync(0xffffffffu, mine.row0, i),
+                   __shfl_sync(0xffffffffu, mine.n, i)};
+  };
+  uint32_t cost = items == 1 ? item_cost<KT>(p, mt, mine, 1, 0) : 0u;
+  bool large = items > 4096 || cost > (1u << 20);
+#pragma unroll 1
+  for (uint32_t rest = __ballot_sync(0xffffffffu, items > 1 && !large); rest; rest &= rest - 1) {
+    const int i = __ffs(rest) - 1, n = __shfl_sync(0xffffffffu, items, i);
+    const SeqRows s = of(i);
+    uint32_t sum = 0;
+#pragma unroll 1
+    for (int m = lane; m < n; m += 32) sum += min(item_cost<KT>(p, mt, s, n, m), 1u << 13);   // (an item past it: large)
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    if (lane == i) {
+      cost = sum;
+      large |= sum > (1u << 20) || item_cost<KT>(p, mt, s, n, n - 1) >= (1u << 13);
+    }
   }
-  if (__any_sync(0xffffffffu, items > kLongSeq || cost * (uint64_t)p.n_kv_heads > (1u << 16))) return false;
-  cost *= (uint32_t)p.n_kv_heads;
-  uint32_t inc = cost;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t up = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += up;
-  }
-  const uint32_t all = __shfl_sync(0xffffffffu, inc, 31);   // at most 2^21: times the CTAs within 32 bits
+  if (__any_sync(0xffffffffu, large)) return false;
+  const uint32_t inc = warp_prefix(cost, lane);
+  const uint32_t all = __shfl_sync(0xffffffffu, inc, 31);   // at most 2^25
   const uint32_t ctas = min((uint32_t)n_ctas, all);
   st = Start{0, 0, (int64_t)all, (int32_t)ctas, 0, 0, 0, 0, {0, 0, 0}};
   if ((uint32_t)cta >= ctas) return true;
-  const uint32_t t0 = all * (uint32_t)cta / ctas, t1 = all * ((uint32_t)cta + 1) / ctas;
+  uint32_t t0, t1;
+  if (all < (1u << 22)) {   // (at most 1,024 CTAs)
+    t0 = all * (uint32_t)cta / ctas;
+    t1 = all * ((uint32_t)cta + 1) / ctas;
+  } else {
+    t0 = (uint32_t)((uint64_t)all * cta / ctas);
+    t1 = (uint32_t)((uint64_t)all * (cta + 1) / ctas);
+  }
   const int i = __ffs(__ballot_sync(0xffffffffu, inc > t0)) - 1;   // the first sequence that ends behind t0
-  s.len = __shfl_sync(0xffffffffu, s.len, i);
-  s.row0 = __shfl_sync(0xffffffffu, s.row0, i);
-  s.n = __shfl_sync(0xffffffffu, s.n, i);
-  const uint32_t before = __shfl_sync(0xffffffffu, inc - cost, i);
+  const int n = __shfl_sync(0xffffffffu, items, i);
+  const SeqRows s = of(i);
+  uint32_t r = t0 - __shfl_sync(0xffffffffu, inc - cost, i);
+  int m = 0;
+  uint32_t c = 0;
+#pragma unroll 1
+  for (int m0 = 0;; m0 += 32) {   // the first item that ends behind the rest
+    c = item_cost<KT>(p, mt, s, n, m0 + lane);
+    const uint32_t end = warp_prefix(c, lane);
+    const uint32_t hit = __ballot_sync(0xffffffffu, end > r);
+    if (hit || m0 + 32 >= n) {
+      const int k = __ffs(hit) - 1;
+      m = m0 + k;
+      r -= __shfl_sync(0xffffffffu, end - c, k);
+      c = __shfl_sync(0xffffffffu, c, k);
+      break;
+    }
+    r -= __shfl_sync(0xffffffffu, end, 31);
+  }
+  const uint32_t count = c / (uint32_t)p.n_kv_heads;
   st.n = t1 - t0;
   st.t0 = t0;
-  place_in_seq<KT>(p, mt, i, s, t0 - before, st);
+  st.seq = i;
+  st.m = m;
+  st.head = (int32_t)(r / count);
+  st.x = (int32_t)(r - (uint32_t)st.head * count);
+  st.s = s;
   return true;
 }
 

@@ -72,11 +72,10 @@ Plan plan_attn(const qsa_paged_batch* b, const qsa_attn_config* cfg) {
     // MMA's rows: what Q does not take of the shared memory is the ring's.
     const int group = cfg->n_q_heads / cfg->n_kv_heads;
     pl.mt = group * std::max(1, std::min(b->max_rows, 128 / group));
-    pl.grid = device_sm_count();
   } else {
     pl.mt = (int64_t)b->max_rows * (cfg->n_q_heads / cfg->n_kv_heads) <= 16 ? 16 : 32;
-    pl.grid = (cfg->head_dim == 128 ? 2 : 1) * device_sm_count();   // as the shared memory holds
   }
+  pl.grid = device_sm_count();   // a CTA takes an SM's shared memory or registers
   if (cfg->n_splits > 0) pl.grid = std::min(pl.grid, cfg->n_splits);
   return pl;
 }
