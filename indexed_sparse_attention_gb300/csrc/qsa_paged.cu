@@ -28,29 +28,39 @@ __device__ int g_bad_pages;   // table entries outside [0, n_pages) among the to
 // ------------------------------------------------------------------ f32 caches
 // Products of f32 values on the tensor pipe, by tf32 halves: x = hi + lo with hi
 // = x rounded to 11 significant bits and lo = x - hi rounded likewise, and
-//   a b = hi_a hi_b + hi_a lo_b + lo_a hi_b  (+ lo_a lo_b, below 2^-22 |a b|, left out)
-// with 32-bit accumulation: as exact as a 32-bit sum of rounded products.
+//   a b = hi_a hi_b + hi_a lo_b + lo_a hi_b  (+ lo_a lo_b, below 2^-22 |a b|, left out).
+// The tensor pipe cuts its 32-bit sums off instead of rounding them, so few are
+// taken on one accumulator: a tile's sums are added to the running ones in plain
+// 32-bit arithmetic.  (With the running ones as accumulators, outputs were 2.8e-6
+// off 64 bits on a windowed batch where plain 32-bit sums are 1.5e-6 off.)
 //
-// An item is 16 or 32 entries (one or two times the rows of m16n8k8), a key tile
-// 32 tokens: warp w takes 16 entries (w / 4) and 8 tokens (w % 4) of it and keeps
-// its own maximum, sum and output over its keys, so a tile needs no exchange; the
-// four warps of an entry are joined like an item's parts at its end.
-// Each row of K and V is one bulk copy, two tiles in flight.  Rows in shared memory
-// are padded, Q's and K's by eight words and V's by four, which puts the eight
-// rows and four column pairs (Q, K), or four row pairs and eight columns (V), of
-// a fragment into different banks.
-constexpr int kF32Threads = 256;
-constexpr int kF32MT = 32;
+// An item is 16 or 32 entries (RT = one or two times the rows of m16n8k8), a key
+// tile 32 tokens.  Warp w of eight takes the channels [w D / 8, (w + 1) D / 8) of
+// both products: it holds its channels of Q (both halves) in registers and reads
+// each K and V value once, where a split by keys had every warp read all of Q
+// (the shared memory's bandwidth was the bound then).  Per tile:
+//   the warps' partial logits over their channels, to shared memory;
+//   their sums, masks, maxima and weights, a thread four keys of one entry;
+//   the output product of the weights with the warp's channels of V.
+// Warp 8 copies: each row of K and V is one bulk copy.  Rows in shared memory are
+// padded, K's by eight words and V's by four, which puts the eight rows and four
+// column pairs (K), or four row pairs and eight columns (V), of a fragment into
+// different banks.
+constexpr int kF32Warps = 8;                       // without the copying one
+constexpr int kF32Threads = 32 * (kF32Warps + 1);
 constexpr int kF32KT = 32;
+constexpr int kF32MaxStages = 4;
 
-template <int D>
+template <int D, int RT>
 struct F32Layout {
-  static constexpr int kRow = D + 8, kRowV = D + 4;        // words of a row of Q and K, and of V
+  static constexpr int kRow = D + 8, kRowV = D + 4;        // words of a row of K, and of V
   static constexpr int kK = kF32KT * kRow, kTile = kK + kF32KT * kRowV;   // words of K, and of K and V, of a tile
-  static constexpr int kQ = 2 * kF32MT * kRow;             // hi, lo
-  static constexpr size_t bytes = 4 * (size_t)(kQ + 2 * kTile);
-  static_assert(8 * 16 * kRowV <= 2 * kTile, "the warps' outputs are joined in the tiles' place");
-  static_assert((4 * kRow) % 16 == 0 && (4 * kRowV) % 16 == 0 && (4 * kQ) % 16 == 0, "rows on 16-byte boundaries");
+  static constexpr int kStages = D == 256 ? 2 : 4;
+  static constexpr int kSRow = kF32KT + 4, kPRow = kF32KT + 8;   // rows of partial logits, and of weights
+  static constexpr int kS = kF32Warps * 16 * RT * kSRow, kP = 2 * 16 * RT * kPRow;
+  static constexpr size_t bytes = 4 * (size_t)(kStages * kTile + kS + kP);
+  static_assert((4 * kRow) % 16 == 0 && (4 * kRowV) % 16 == 0 && (4 * kK) % 16 == 0 && (4 * kTile) % 16 == 0 &&
+                    (4 * kS) % 16 == 0, "rows on 16-byte boundaries");
 };
 
 // The halves of x.  Adding half a unit of the 11th significant bit to the pattern
@@ -62,8 +72,7 @@ __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) 
   lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;
 }
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -74,35 +83,31 @@ __device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t b
                "l"(src), "r"(bytes), "r"(smem_addr(bar))
                : "memory");
 }
-__device__ __forceinline__ float quad_max(float v) {
-  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-}
-__device__ __forceinline__ float quad_sum(float v) {
-  v += __shfl_xor_sync(0xffffffffu, v, 1);
-  return v + __shfl_xor_sync(0xffffffffu, v, 2);
-}
+__device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kF32Warps) : "memory"); }
 
-template <int D>
-__global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(const PagedParams p) {
-  using L = F32Layout<D>;
-  constexpr int ROW = L::kRow, ROWV = L::kRowV, NT = D / 8;
-  constexpr float kMoveMax = 8.f;   // as in the bf16 kernel: the maximum moves when a weight would pass 2^8
+template <int D, int RT>
+__global__ void __launch_bounds__(kF32Threads, 1) paged_f32_kernel(const PagedParams p) {
+  using L = F32Layout<D, RT>;
+  constexpr int ROW = L::kRow, ROWV = L::kRowV, ST = L::kStages;
+  constexpr int C = D / kF32Warps;          // channels of a warp
+  constexpr int KS = C / 8, NT = C / 8;     // steps of the logits' product, channel blocks of the output's
+  constexpr float kMoveMax = 8.f;           // as in the bf16 kernel: the maximum moves when a weight would pass 2^8
   extern __shared__ __align__(16) float fsm[];
-  float* q_s = fsm;                 // hi [16][ROW], then lo
-  float* kv_s = fsm + L::kQ;        // two tiles of [K 32][ROW], [V 32][ROWV]
+  float* kv_s = fsm;                        // stages of [K 32][ROW], [V 32][ROWV]
+  float* s_s = kv_s + ST * L::kTile;        // [8 warps][16 RT entries][kSRow]
+  float* p_s = s_s + L::kS;                 // weights: hi [16 RT][kPRow], then lo
   __shared__ int64_t scan_s[kF32Threads / 32];
   __shared__ Start start_s;
-  __shared__ uint64_t full[2];
+  __shared__ uint64_t full[ST], empty[ST];
   __shared__ int abort_s;
-  __shared__ uint8_t seen_s[2][4];  // tokens of a tile that some row sees and that have a page
-  __shared__ float m_s[4][kF32MT], l_s[4][kF32MT];
+  __shared__ uint32_t seen_s[2 * kF32MaxStages];   // tokens of a tile that some row sees and that have a page
+  __shared__ float a_s[16 * RT], l_s[16 * RT];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int gr = lane >> 2, gc = lane & 3;   // a fragment's row group and column
-  const int keys = warp & 3, rows16 = warp >> 2;
   if (tid == 0) {
-    bar_init(&full[0], kF32Threads);
-    bar_init(&full[1], kF32Threads);
+    for (int i = 0; i < ST; ++i) {
+      bar_init(&full[i], 32);
+      bar_init(&empty[i], kF32Warps);
+    }
     bar_init_fence();
     abort_s = 0;
   }
@@ -111,246 +116,250 @@ __global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(const PagedParam
   const Start st = find_run<kF32Threads, kF32KT>(p, p.mt, blockIdx.x, gridDim.x, scan_s, &start_s);
   Cursor<kF32KT> c;
   c.begin(p, p.mt, st);
+  if (st.n == 0) {
+    if (tid == 0) p.parts[blockIdx.x] = PagedPart{};
+    return;
+  }
+
+  if (warp == kF32Warps) {
+    // ------------------------------------------------------------ copies
+    // Lane i: token i's rows; a row that is not there becomes zeros.
+    int g = 0;
+    bool live = true;
+    for (bool more = true; more && live; more = c.next(p, p.mt)) {
+      const int f0 = c.m * p.mt, nf = min(p.mt, c.s.n * p.group - f0), pos0 = c.s.len - c.s.n;
+      const int first = pos0 + f0 / p.group, last = pos0 + (f0 + nf - 1) / p.group;
+      const int T = c.x1 - c.x;
+      auto look_up = [&](int x) {   // page of the lane's token: -1 where no row sees it, or it has none
+        const int t = c.tiles.token(c.x + x) + lane;
+        if (x >= T || t > last || !(p.window == 0 || t > first - p.window || t < p.n_sinks)) return -1;
+        int32_t page;
+        if (page_of(p, c.seq, t, page)) return (int)page;
+        atomicAdd(&g_bad_pages, 1);
+        return -1;
+      };
+      int page = look_up(0);
+      for (int x = 0; x < T; ++x, ++g) {
+        const int next = look_up(x + 1);
+        const int b = g % ST;
+        live = g < ST || bar_wait(&empty[b], (uint32_t)((g / ST - 1) & 1), &g_f32_timeouts, &abort_s);
+        live = __all_sync(0xffffffffu, live);
+        if (!live) break;
+        float* dst = kv_s + b * L::kTile;
+        const bool ok = page >= 0;
+        const uint32_t seen = __ballot_sync(0xffffffffu, ok);
+        if (lane == 0) seen_s[g & (2 * kF32MaxStages - 1)] = seen;
+        __syncwarp();
+        if (ok) {
+          const int64_t slot = (c.tiles.token(c.x + x) + lane) & ((1 << p.page_shift) - 1);
+          const int64_t off = page * p.page_stride + c.head * p.head_stride + slot * p.tok_stride;
+          fence_async_smem();   // (zeros may have been stored there)
+          bar_expect_tx(&full[b], 8 * D);
+          bulk_copy(dst + lane * ROW, static_cast<const float*>(p.k) + off, 4 * D, &full[b]);
+          bulk_copy(dst + L::kK + lane * ROWV, static_cast<const float*>(p.v) + off, 4 * D, &full[b]);
+        } else {
+          for (int i = 0; i < D / 4; ++i) {
+            reinterpret_cast<float4*>(dst + lane * ROW)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            reinterpret_cast<float4*>(dst + L::kK + lane * ROWV)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+          bar_arrive(&full[b]);
+        }
+        page = next;
+      }
+    }
+    // Every copy has landed before the CTA ends.
+    for (int i = max(g - ST, 0); i < g; ++i) bar_wait(&full[i % ST], (uint32_t)((i / ST) & 1), &g_f32_timeouts);
+    return;
+  }
+
+  // -------------------------------------------------------------- products
+  const int gr = lane >> 2, gc = lane & 3;   // a fragment's row group and column
   const float zscale = p.scale * kLog2e;
-  if (st.n == 0 && tid == 0) p.parts[blockIdx.x] = PagedPart{};
-  int tj = 0;   // tiles done: tile g of the run is in buffer g & 1, phase g >> 1
-  for (bool more = st.n > 0; more;) {
+  // The entry and four keys whose logits this thread sums (with RT = 1: half the threads).
+  const int row = tid >> 3, key0 = 4 * (tid & 7);
+  int g = 0;
+  for (bool more = true; more;) {
     const int f0 = c.m * p.mt, nf = min(p.mt, c.s.n * p.group - f0);
     const int pos0 = c.s.len - c.s.n;
-    const int first = pos0 + f0 / p.group, last = pos0 + (f0 + nf - 1) / p.group;
     // Entry f of the item -> its row and query head.
     auto entry = [&](int f) {
       const int r = (f0 + f) / p.group;
       return (int64_t)(c.s.row0 + r) * p.n_q_heads + c.head * p.group + (f0 + f - r * p.group);
     };
     const int T = c.x1 - c.x;
-    // Thread i < 64 -> token i / 2 of a tile, its K or its V row.
-    // Page of the thread's token: -1 where no row sees it, or it has no page.
-    const int mine = tid >> 1, is_v = tid & 1;
-    auto look_up = [&](int x) {
-      if (tid >= 2 * kF32KT || x >= T) return -1;
-      const int t = c.tiles.token(c.x + x) + mine;
-      if (t > last || !(p.window == 0 || t > first - p.window || t < p.n_sinks)) return -1;
-      int32_t page;
-      if (page_of(p, c.seq, t, page)) return (int)page;
-      if (!is_v) atomicAdd(&g_bad_pages, 1);
-      return -1;
-    };
-    auto load = [&](int x, int page) {   // every thread arrives; a row that is not there becomes zeros
-      const int b = (tj + x) & 1;
-      if (tid < 2 * kF32KT) {
-        float* dst = kv_s + b * L::kTile + (is_v ? L::kK + mine * ROWV : mine * ROW);
-        const bool ok = page >= 0;
-        if (ok) {
-          const int64_t slot = (c.tiles.token(c.x + x) + mine) & ((1 << p.page_shift) - 1);
-          const float* src = static_cast<const float*>(is_v ? p.v : p.k) + page * p.page_stride +
-                             c.head * p.head_stride + slot * p.tok_stride;
-          fence_async_smem();   // (zeros may have been stored there)
-          bar_expect_tx(&full[b], 4 * D);
-          bulk_copy(dst, src, 4 * D, &full[b]);
-        } else {
-          for (int i = 0; i < D / 4; ++i) reinterpret_cast<float4*>(dst)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-          bar_arrive(&full[b]);
-        }
-        const uint32_t v = __ballot_sync(0xffffffffu, ok);   // two lanes a token, 16 tokens a warp
-        uint32_t bits = 0u;
+    // The warp's channels of Q: a step's column gc is channel 2 gc, its column
+    // gc + 4 channel 2 gc + 1.
+    uint32_t qh[RT][KS][4], ql[RT][KS][4];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) bits |= ((v >> (2 * i)) & 1u) << i;
-        if (lane == 0) seen_s[b][2 * warp] = (uint8_t)bits, seen_s[b][2 * warp + 1] = (uint8_t)(bits >> 8);
-      } else {
-        bar_arrive(&full[b]);
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int f = 16 * r + gr + 8 * h;
+        const float* q = static_cast<const float*>(p.q) + (f < nf ? entry(f) : 0) * D + warp * C + 2 * gc;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const float2 x = f < nf ? __ldg(reinterpret_cast<const float2*>(q + 8 * k)) : make_float2(0.f, 0.f);
+          split_tf32(x.x, qh[r][k][h], ql[r][k][h]);
+          split_tf32(x.y, qh[r][k][h + 2], ql[r][k][h + 2]);
+        }
       }
-    };
-    fence_async_smem();   // (plain stores before the copies that follow)
-    __syncthreads();      // the last item's joining is done with the tiles' place
-    int page = look_up(0);
-    load(0, page);
-    page = look_up(1);
-    // Q, eight 16-byte pieces of it a thread at a time.
-    for (int i0 = tid; i0 < p.mt * (D / 4); i0 += 4 * kF32Threads) {
-      float4 x[4];
+    float o[RT][NT][4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int i = i0 + k * kF32Threads, f = i / (D / 4);
-        x[k] = f < nf ? __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + entry(f) * D) + i % (D / 4))
-                      : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int i = i0 + k * kF32Threads, f = i / (D / 4);
-        if (f >= p.mt) continue;
-        uint4 hi, lo;
-        split_tf32(x[k].x, hi.x, lo.x);
-        split_tf32(x[k].y, hi.y, lo.y);
-        split_tf32(x[k].z, hi.z, lo.z);
-        split_tf32(x[k].w, hi.w, lo.w);
-        float* to = q_s + f * ROW + 4 * (i % (D / 4));
-        *reinterpret_cast<uint4*>(to) = hi;
-        *reinterpret_cast<uint4*>(to + kF32MT * ROW) = lo;
-      }
-    }
-    float o[NT][4];
+      for (int i = 0; i < NT; ++i) o[r][i][0] = o[r][i][1] = o[r][i][2] = o[r][i][3] = 0.f;
+    float m = -INFINITY, l = 0.f;
+    const int pos = pos0 + (f0 + min(row, nf - 1)) / p.group;
+    for (int x = 0; x < T; ++x, ++g) {
+      const int b = g % ST;
+      bar_wait(&full[b], (uint32_t)((g / ST) & 1), &g_f32_timeouts, &abort_s);
+      const float* ks = kv_s + b * L::kTile + gr * ROW + warp * C + 2 * gc;
+      const float* vs = kv_s + b * L::kTile + L::kK + 2 * gc * ROWV + warp * C + gr;
+      float* to = s_s + (warp * 16 * RT + gr) * L::kSRow + 2 * gc;
+#pragma unroll 1
+      for (int n0 = 0; n0 < 4; n0 += 2) {   // two blocks of eight keys at a time: registers
+        float z[RT][2][4], zx[RT][2][4];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    // Rows gr and gr + 8 of the warp's 16 entries, and what they see.
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    int pos[2];
+        for (int r = 0; r < RT; ++r)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) pos[h] = pos0 + (f0 + min(16 * rows16 + gr + 8 * h, nf - 1)) / p.group;
-    for (int x = 0; x < T; ++x) {
-      if (x + 1 < T) load(x + 1, page);
-      page = look_up(x + 2);
-      const int b = (tj + x) & 1;
-      bar_wait(&full[b], (uint32_t)(((tj + x) >> 1) & 1), &g_f32_timeouts, &abort_s);
-      if (x == 0) __syncthreads();   // Q is there
-      const float* ks = kv_s + b * L::kTile + 8 * keys * ROW;   // the warp's 8 keys
-      const float* vs = kv_s + b * L::kTile + L::kK + 8 * keys * ROWV;
-      const uint32_t seen = seen_s[b][keys];
-      const int t0 = c.tiles.token(c.x + x) + 8 * keys;
-      if (seen != 0u && 16 * rows16 < nf) {
-        // Logits of 16 entries x 8 keys: six sums (three products, even and odd
-        // steps), so that the chains stay short.
-        float z[6][4];
+          for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int i = 0; i < 6; ++i) z[i][0] = z[i][1] = z[i][2] = z[i][3] = 0.f;
-        // (A step's column gc is channel 2 gc, its column gc + 4 channel 2 gc + 1.)
-        const float* qh = q_s + (16 * rows16 + gr) * ROW + 2 * gc;
-        const float* ql = qh + kF32MT * ROW;
-        const float* kk = ks + gr * ROW + 2 * gc;
-        auto two = [](const float* x) { return *reinterpret_cast<const uint2*>(x); };
-#pragma unroll 8
-        for (int d = 0; d < D; d += 8) {
-          const int e = (d >> 3) & 1;
-          const uint2 h0 = two(qh + d), h1 = two(qh + 8 * ROW + d), l0 = two(ql + d), l1 = two(ql + 8 * ROW + d);
-          const uint2 k = two(kk + d);
-          const uint32_t ah[4] = {h0.x, h1.x, h0.y, h1.y}, al[4] = {l0.x, l1.x, l0.y, l1.y};
-          uint32_t bh0, bl0, bh1, bl1;
-          split_tf32(__uint_as_float(k.x), bh0, bl0);
-          split_tf32(__uint_as_float(k.y), bh1, bl1);
-          mma_tf32(z[3 * e], ah, bh0, bh1);
-          mma_tf32(z[3 * e + 1], ah, bl0, bl1);
-          mma_tf32(z[3 * e + 2], al, bh0, bh1);
-        }
-        // Entry (row gr + 8 h, key 2 gc + i) is s[2 h + i].
-        float s[4], mx[2];
+            for (int i = 0; i < 4; ++i) z[r][n][i] = zx[r][n][i] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int h = i >> 1, key = 2 * gc + (i & 1);
-          const float v = ((z[0][i] + z[3][i]) + ((z[1][i] + z[4][i]) + (z[2][i] + z[5][i]))) * zscale;
-          s[i] = ((seen >> key) & 1u) && sees(p, pos[h], t0 + key) ? v : -INFINITY;
-        }
-        bool moves = false;
+        for (int k = 0; k < KS; ++k) {
+          uint32_t bh[2][2], bl[2][2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          mx[h] = quad_max(fmaxf(s[2 * h], s[2 * h + 1]));
-          moves |= mx[h] > m[h] + kMoveMax || (m[h] == -INFINITY && mx[h] != -INFINITY);
-        }
-        if (__any_sync(0xffffffffu, moves)) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float mn = fmaxf(m[h], mx[h]);
-            const float a = mn == -INFINITY ? 1.f : exp2f(m[h] - mn);
-            m[h] = mn;
-            l[h] *= a;
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              o[i][2 * h] *= a;
-              o[i][2 * h + 1] *= a;
-            }
-          }
-        }
-        // Weights, which are the A fragment of the output product as they lie: its
-        // column gc is key 2 gc, its column gc + 4 key 2 gc + 1.
-        float w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int h = i >> 1;
-          w[i] = m[h] == -INFINITY ? 0.f : exp2f(s[i] - m[h]);
-          l[h] += w[i];
-        }
-        uint32_t ph[4], pl[4];
-        split_tf32(w[0], ph[0], pl[0]);
-        split_tf32(w[2], ph[1], pl[1]);
-        split_tf32(w[1], ph[2], pl[2]);
-        split_tf32(w[3], ph[3], pl[3]);
-        const float* vv = vs + 2 * gc * ROWV + gr;
-        constexpr int kAt = 4;   // channel blocks whose products are interleaved
-#pragma unroll
-        for (int i = 0; i < NT; i += kAt) {
-          uint32_t bh[kAt][2], bl[kAt][2];
-#pragma unroll
-          for (int k = 0; k < kAt; ++k) {
-            split_tf32(vv[8 * (i + k)], bh[k][0], bl[k][0]);
-            split_tf32(vv[ROWV + 8 * (i + k)], bh[k][1], bl[k][1]);
+          for (int n = 0; n < 2; ++n) {
+            const float2 y = *reinterpret_cast<const float2*>(ks + 8 * (n0 + n) * ROW + 8 * k);
+            split_tf32(y.x, bh[n][0], bl[n][0]);
+            split_tf32(y.y, bh[n][1], bl[n][1]);
           }
 #pragma unroll
-          for (int k = 0; k < kAt; ++k) mma_tf32(o[i + k], ph, bh[k][0], bh[k][1]);
+          for (int r = 0; r < RT; ++r) {
 #pragma unroll
-          for (int k = 0; k < kAt; ++k) mma_tf32(o[i + k], ph, bl[k][0], bl[k][1]);
+            for (int n = 0; n < 2; ++n) mma_tf32(z[r][n], qh[r][k], bh[n][0], bh[n][1]);
 #pragma unroll
-          for (int k = 0; k < kAt; ++k) mma_tf32(o[i + k], pl, bh[k][0], bh[k][1]);
+            for (int n = 0; n < 2; ++n) mma_tf32(zx[r][n], qh[r][k], bl[n][0], bl[n][1]);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) mma_tf32(zx[r][n], ql[r][k], bh[n][0], bh[n][1]);
+          }
         }
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              *reinterpret_cast<float2*>(to + (16 * r + 8 * h) * L::kSRow + 8 * (n0 + n)) =
+                  make_float2(z[r][n][2 * h] + zx[r][n][2 * h], z[r][n][2 * h + 1] + zx[r][n][2 * h + 1]);
       }
-      __syncthreads();   // the tile may be overwritten
-    }
-    tj += T;
-    // The four warps' outputs, sums and maxima of each entry, joined in shared memory.
+      compute_sync();
+      if (row < 16 * RT) {
+        float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      l[h] = quad_sum(l[h]);
-      if (gc == 0) {
-        m_s[keys][16 * rows16 + gr + 8 * h] = m[h];
-        l_s[keys][16 * rows16 + gr + 8 * h] = l[h];
+        for (int w = 0; w < kF32Warps; ++w) {
+          const float4 y = *reinterpret_cast<const float4*>(s_s + (w * 16 * RT + row) * L::kSRow + key0);
+          z.x += y.x;
+          z.y += y.y;
+          z.z += y.z;
+          z.w += y.w;
+        }
+        const uint32_t seen = seen_s[g & (2 * kF32MaxStages - 1)] >> key0;
+        const int t0 = c.tiles.token(c.x + x) + key0;
+        float v[4] = {z.x * zscale, z.y * zscale, z.z * zscale, z.w * zscale};
+        float mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (!((seen >> i) & 1u) || !sees(p, pos, t0 + i)) v[i] = -INFINITY;
+          mx = fmaxf(mx, v[i]);
+        }
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        const float mn = mx > m + kMoveMax || m == -INFINITY ? mx : m;
+        const float a = mn == m ? 1.f : exp2f(m - mn);
+        m = mn;
+        l *= a;
+        if ((tid & 7) == 0) a_s[row] = a;
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float w = m == -INFINITY ? 0.f : exp2f(v[i] - m);
+          l += w;
+          split_tf32(w, hi[i], lo[i]);
+        }
+        *reinterpret_cast<uint4*>(p_s + row * L::kPRow + key0) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(p_s + (16 * RT + row) * L::kPRow + key0) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
+      compute_sync();
+      // A step is eight keys: its column gc key 2 gc, its column gc + 4 key 2 gc + 1.
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        float t[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) t[n][0] = t[n][1] = t[n][2] = t[n][3] = 0.f;
+#pragma unroll 1
+        for (int k = 0; k < kF32KT / 8; ++k) {
+          auto two = [&](int half, int f) {
+            return *reinterpret_cast<const uint2*>(p_s + (16 * RT * half + 16 * r + f) * L::kPRow + 8 * k + 2 * gc);
+          };
+          const uint2 h0 = two(0, gr), h1 = two(0, gr + 8), l0 = two(1, gr), l1 = two(1, gr + 8);
+          const uint32_t ph[4] = {h0.x, h1.x, h0.y, h1.y}, pl[4] = {l0.x, l1.x, l0.y, l1.y};
+          uint32_t bh[NT][2], bl[NT][2];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            split_tf32(vs[8 * k * ROWV + 8 * n], bh[n][0], bl[n][0]);
+            split_tf32(vs[(8 * k + 1) * ROWV + 8 * n], bh[n][1], bl[n][1]);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_tf32(t[n], ph, bl[n][0], bl[n][1]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_tf32(t[n], pl, bh[n][0], bh[n][1]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_tf32(t[n], ph, bh[n][0], bh[n][1]);
+        }
+        const float a0 = a_s[16 * r + gr], a1 = a_s[16 * r + gr + 8];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[r][n][i] = fmaf(o[r][n][i], i < 2 ? a0 : a1, t[n][i]);
+      }
+      __syncwarp();
+      if (lane == 0) bar_arrive(&empty[b]);
     }
-    float* o_s = kv_s + warp * 16 * ROWV;   // warp 4 (f / 16) + keys: entry f
+    // The item's result, or this run's part of it.
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<float2*>(o_s + (gr + 8 * h) * ROWV + 8 * i + 2 * gc) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
-    __syncthreads();
+    for (int d = 1; d < 8; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
     const bool whole = c.whole();
     const int64_t slot = whole ? 0 : (int64_t)c.slot(blockIdx.x) * p.mt;
-    for (int f = warp; f < nf; f += kF32Threads / 32) {
-      float M = -INFINITY, W = 0.f, e[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) M = fmaxf(M, m_s[k][f]);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        e[k] = m_s[k][f] == -INFINITY ? 0.f : exp2f(m_s[k][f] - M);
-        W = fmaf(e[k], l_s[k][f], W);
-      }
-      const float inv = W > 0.f ? 1.f / W : 0.f;
-      const int64_t at = whole ? entry(f) : slot + f;
-      for (int d = 4 * lane; d < D; d += 128) {
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float4 y = *reinterpret_cast<const float4*>(kv_s + ((4 * (f >> 4) + k) * 16 + (f & 15)) * ROWV + d);
-          x.x = fmaf(e[k], y.x, x.x);
-          x.y = fmaf(e[k], y.y, x.y);
-          x.z = fmaf(e[k], y.z, x.z);
-          x.w = fmaf(e[k], y.w, x.w);
-        }
-        x = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-        if (!whole || p.out_dtype == QSA_F32) {
-          *reinterpret_cast<float4*>((whole ? static_cast<float*>(p.out) : p.part_o) + at * D + d) = x;
-        } else {
-          __nv_bfloat162* to = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + at * D + d);
-          to[0] = __floats2bfloat162_rn(x.x, x.y);
-          to[1] = __floats2bfloat162_rn(x.z, x.w);
-        }
-      }
-      if (lane == 0) {
-        const float lse2 = W > 0.f ? M + log2f(W) : -INFINITY;
-        if (!whole) p.part_lse[at] = lse2;
-        else if (p.lse) p.lse[at] = lse2 * kLn2;
-      }
+    if ((tid & 7) == 0 && row < nf) {
+      l_s[row] = l > 0.f ? 1.f / l : 0.f;
+      const float lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
+      if (!whole) p.part_lse[slot + row] = lse2;
+      else if (p.lse) p.lse[entry(row)] = lse2 * kLn2;
     }
+    compute_sync();
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int f = 16 * r + gr + 8 * h;
+        if (f >= nf) continue;
+        const float inv = l_s[f];
+        const int64_t at = (whole ? entry(f) : slot + f) * D + warp * C + 2 * gc;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          const float x0 = o[r][i][2 * h] * inv, x1 = o[r][i][2 * h + 1] * inv;
+          if (!whole || p.out_dtype == QSA_F32)
+            *reinterpret_cast<float2*>((whole ? static_cast<float*>(p.out) : p.part_o) + at + 8 * i) = make_float2(x0, x1);
+          else
+            *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + at + 8 * i) =
+                __floats2bfloat162_rn(x0, x1);
+        }
+      }
     const Cursor<kF32KT> done = c;
     more = c.next(p, p.mt);
     if (!more && tid == 0) describe_part(p, done, st, blockIdx.x);
+    compute_sync();   // l_s has been read
   }
 }
 
@@ -493,18 +502,19 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
   }
 }
 
-template <int D>
+template <int D, int RT>
 cudaError_t launch_f32(const PagedParams& p, int grid, cudaStream_t st) {
-  const size_t smem = F32Layout<D>::bytes;
-  cudaError_t e = allow_dynamic_smem((const void*)paged_f32_kernel<D>, smem);
+  const size_t smem = F32Layout<D, RT>::bytes;
+  cudaError_t e = allow_dynamic_smem((const void*)paged_f32_kernel<D, RT>, smem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(paged_f32_kernel<D>, dim3((unsigned)grid), dim3(kF32Threads), smem, st, 0u, p);
+  return launch_kernel(paged_f32_kernel<D, RT>, dim3((unsigned)grid), dim3(kF32Threads), smem, st, 0u, p);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_f32(const PagedParams& p, int head_dim, int grid, cudaStream_t st) {
-  return head_dim == 256 ? launch_f32<256>(p, grid, st) : launch_f32<128>(p, grid, st);
+  if (p.mt == 16) return head_dim == 256 ? launch_f32<256, 1>(p, grid, st) : launch_f32<128, 1>(p, grid, st);
+  return head_dim == 256 ? launch_f32<256, 2>(p, grid, st) : launch_f32<128, 2>(p, grid, st);
 }
 
 cudaError_t launch_paged_merge(const PagedParams& p, int head_dim, int runs, cudaStream_t st) {
