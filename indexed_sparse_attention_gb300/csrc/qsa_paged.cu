@@ -36,7 +36,7 @@ __device__ int g_bad_pages;   // table entries outside [0, n_pages) among the to
 //
 // An item is 16 or 32 entries (RT = one or two times the rows of m16n8k8), a key
 // tile 32 tokens.  Warp w of eight takes the channels [w D / 8, (w + 1) D / 8) of
-// both products: it holds its channels of Q (both halves) in registers and reads
+// both products: it holds its channels of Q in registers and reads
 // each K and V value once, where a split by keys had every warp read all of Q
 // (the shared memory's bandwidth was the bound then).  Per tile:
 //   the warps' partial logits over their channels, to shared memory;
@@ -83,6 +83,11 @@ __device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t b
                "l"(src), "r"(bytes), "r"(smem_addr(bar))
                : "memory");
 }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kF32Warps) : "memory"); }
 
 template <int D, int RT>
@@ -128,7 +133,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) paged_f32_kernel(const PagedPa
     bool live = true;
     for (bool more = true; more && live; more = c.next(p, p.mt)) {
       const int f0 = c.m * p.mt, nf = min(p.mt, c.s.n * p.group - f0), pos0 = c.s.len - c.s.n;
-      const int first = pos0 + f0 / p.group, last = pos0 + (f0 + nf - 1) / p.group;
+      const int first = pos0 + row_of(p, f0), last = pos0 + row_of(p, f0 + nf - 1);
       const int T = c.x1 - c.x;
       auto look_up = [&](int x) {   // page of the lane's token: -1 where no row sees it, or it has none
         const int t = c.tiles.token(c.x + x) + lane;
@@ -181,15 +186,16 @@ __global__ void __launch_bounds__(kF32Threads, 1) paged_f32_kernel(const PagedPa
   for (bool more = true; more;) {
     const int f0 = c.m * p.mt, nf = min(p.mt, c.s.n * p.group - f0);
     const int pos0 = c.s.len - c.s.n;
+    const int first = pos0 + row_of(p, f0), last = pos0 + row_of(p, f0 + nf - 1);
     // Entry f of the item -> its row and query head.
     auto entry = [&](int f) {
-      const int r = (f0 + f) / p.group;
+      const int r = row_of(p, f0 + f);
       return (int64_t)(c.s.row0 + r) * p.n_q_heads + c.head * p.group + (f0 + f - r * p.group);
     };
     const int T = c.x1 - c.x;
     // The warp's channels of Q: a step's column gc is channel 2 gc, its column
     // gc + 4 channel 2 gc + 1.
-    uint32_t qh[RT][KS][4], ql[RT][KS][4];
+    float q_r[RT][KS][4];   // (split where it is used: both halves would not fit the registers)
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -199,8 +205,8 @@ __global__ void __launch_bounds__(kF32Threads, 1) paged_f32_kernel(const PagedPa
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           const float2 x = f < nf ? __ldg(reinterpret_cast<const float2*>(q + 8 * k)) : make_float2(0.f, 0.f);
-          split_tf32(x.x, qh[r][k][h], ql[r][k][h]);
-          split_tf32(x.y, qh[r][k][h + 2], ql[r][k][h + 2]);
+          q_r[r][k][h] = x.x;
+          q_r[r][k][h + 2] = x.y;
         }
       }
     float o[RT][NT][4];
@@ -209,81 +215,86 @@ __global__ void __launch_bounds__(kF32Threads, 1) paged_f32_kernel(const PagedPa
 #pragma unroll
       for (int i = 0; i < NT; ++i) o[r][i][0] = o[r][i][1] = o[r][i][2] = o[r][i][3] = 0.f;
     float m = -INFINITY, l = 0.f;
-    const int pos = pos0 + (f0 + min(row, nf - 1)) / p.group;
+    const int pos = pos0 + row_of(p, f0 + min(row, nf - 1));
     for (int x = 0; x < T; ++x, ++g) {
       const int b = g % ST;
       bar_wait(&full[b], (uint32_t)((g / ST) & 1), &g_f32_timeouts, &abort_s);
       const float* ks = kv_s + b * L::kTile + gr * ROW + warp * C + 2 * gc;
       const float* vs = kv_s + b * L::kTile + L::kK + 2 * gc * ROWV + warp * C + gr;
       float* to = s_s + (warp * 16 * RT + gr) * L::kSRow + 2 * gc;
-#pragma unroll 1
-      for (int n0 = 0; n0 < 4; n0 += 2) {   // two blocks of eight keys at a time: registers
-        float z[RT][2][4], zx[RT][2][4];
+      {
+        float z[RT][4][4];
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) z[r][n][i] = zx[r][n][i] = 0.f;
+          for (int n = 0; n < 4; ++n) z[r][n][0] = z[r][n][1] = z[r][n][2] = z[r][n][3] = 0.f;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          uint32_t bh[2][2], bl[2][2];
+          uint32_t bh[4][2], bl[4][2];
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const float2 y = *reinterpret_cast<const float2*>(ks + 8 * (n0 + n) * ROW + 8 * k);
+          for (int n = 0; n < 4; ++n) {
+            const float2 y = *reinterpret_cast<const float2*>(ks + 8 * n * ROW + 8 * k);
             split_tf32(y.x, bh[n][0], bl[n][0]);
             split_tf32(y.y, bh[n][1], bl[n][1]);
           }
 #pragma unroll
           for (int r = 0; r < RT; ++r) {
+            uint32_t qh[4], ql[4];
 #pragma unroll
-            for (int n = 0; n < 2; ++n) mma_tf32(z[r][n], qh[r][k], bh[n][0], bh[n][1]);
+            for (int i = 0; i < 4; ++i) {
+              float q = q_r[r][k][i];
+              asm volatile("" : "+f"(q));   // (else the halves are computed once and spilled)
+              split_tf32(q, qh[i], ql[i]);
+            }
 #pragma unroll
-            for (int n = 0; n < 2; ++n) mma_tf32(zx[r][n], qh[r][k], bl[n][0], bl[n][1]);
+            for (int n = 0; n < 4; ++n) mma_tf32(z[r][n], qh, bl[n][0], bl[n][1]);
 #pragma unroll
-            for (int n = 0; n < 2; ++n) mma_tf32(zx[r][n], ql[r][k], bh[n][0], bh[n][1]);
+            for (int n = 0; n < 4; ++n) mma_tf32(z[r][n], ql, bh[n][0], bh[n][1]);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) mma_tf32(z[r][n], qh, bh[n][0], bh[n][1]);
           }
         }
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int n = 0; n < 4; ++n)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-              *reinterpret_cast<float2*>(to + (16 * r + 8 * h) * L::kSRow + 8 * (n0 + n)) =
-                  make_float2(z[r][n][2 * h] + zx[r][n][2 * h], z[r][n][2 * h + 1] + zx[r][n][2 * h + 1]);
+              *reinterpret_cast<float2*>(to + (16 * r + 8 * h) * L::kSRow + 8 * n) =
+                  make_float2(z[r][n][2 * h], z[r][n][2 * h + 1]);
       }
       compute_sync();
       if (row < 16 * RT) {
-        float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 y[kF32Warps];
 #pragma unroll
-        for (int w = 0; w < kF32Warps; ++w) {
-          const float4 y = *reinterpret_cast<const float4*>(s_s + (w * 16 * RT + row) * L::kSRow + key0);
-          z.x += y.x;
-          z.y += y.y;
-          z.z += y.z;
-          z.w += y.w;
-        }
-        const uint32_t seen = seen_s[g & (2 * kF32MaxStages - 1)] >> key0;
-        const int t0 = c.tiles.token(c.x + x) + key0;
-        float v[4] = {z.x * zscale, z.y * zscale, z.z * zscale, z.w * zscale};
-        float mx = -INFINITY;
+        for (int w = 0; w < kF32Warps; ++w)
+          y[w] = *reinterpret_cast<const float4*>(s_s + (w * 16 * RT + row) * L::kSRow + key0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (!((seen >> i) & 1u) || !sees(p, pos, t0 + i)) v[i] = -INFINITY;
-          mx = fmaxf(mx, v[i]);
+        for (int d = kF32Warps / 2; d > 0; d >>= 1)
+#pragma unroll
+          for (int w = 0; w < d; ++w)
+            y[w] = make_float4(y[w].x + y[w + d].x, y[w].y + y[w + d].y, y[w].z + y[w + d].z, y[w].w + y[w + d].w);
+        const uint32_t seen = seen_s[g & (2 * kF32MaxStages - 1)];
+        const int t0 = c.tiles.token(c.x + x);
+        float v[4] = {y[0].x * zscale, y[0].y * zscale, y[0].z * zscale, y[0].w * zscale};
+        if (seen != 0xffffffffu || t0 + kF32KT - 1 > first || (p.window > 0 && t0 <= last - p.window)) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!((seen >> (key0 + i)) & 1u) || !sees(p, pos, t0 + key0 + i)) v[i] = -INFINITY;
         }
+        float mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
 #pragma unroll
         for (int d = 1; d < 8; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
         const float mn = mx > m + kMoveMax || m == -INFINITY ? mx : m;
-        const float a = mn == m ? 1.f : exp2f(m - mn);
+        const float a = mn == m ? 1.f : ex2(m - mn);
+        const float shift = mn == -INFINITY ? 0.f : mn;
         m = mn;
         l *= a;
         if ((tid & 7) == 0) a_s[row] = a;
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float w = m == -INFINITY ? 0.f : exp2f(v[i] - m);
+          const float w = ex2(v[i] - shift);
           l += w;
           split_tf32(w, hi[i], lo[i]);
         }
@@ -292,36 +303,41 @@ __global__ void __launch_bounds__(kF32Threads, 1) paged_f32_kernel(const PagedPa
       }
       compute_sync();
       // A step is eight keys: its column gc key 2 gc, its column gc + 4 key 2 gc + 1.
+      float t[RT][NT][4];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        float t[NT][4];
+      for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) t[n][0] = t[n][1] = t[n][2] = t[n][3] = 0.f;
-#pragma unroll 1
-        for (int k = 0; k < kF32KT / 8; ++k) {
+        for (int n = 0; n < NT; ++n) t[r][n][0] = t[r][n][1] = t[r][n][2] = t[r][n][3] = 0.f;
+#pragma unroll 2
+      for (int k = 0; k < kF32KT / 8; ++k) {
+        uint32_t bh[NT][2], bl[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          split_tf32(vs[8 * k * ROWV + 8 * n], bh[n][0], bl[n][0]);
+          split_tf32(vs[(8 * k + 1) * ROWV + 8 * n], bh[n][1], bl[n][1]);
+        }
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
           auto two = [&](int half, int f) {
             return *reinterpret_cast<const uint2*>(p_s + (16 * RT * half + 16 * r + f) * L::kPRow + 8 * k + 2 * gc);
           };
           const uint2 h0 = two(0, gr), h1 = two(0, gr + 8), l0 = two(1, gr), l1 = two(1, gr + 8);
           const uint32_t ph[4] = {h0.x, h1.x, h0.y, h1.y}, pl[4] = {l0.x, l1.x, l0.y, l1.y};
-          uint32_t bh[NT][2], bl[NT][2];
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            split_tf32(vs[8 * k * ROWV + 8 * n], bh[n][0], bl[n][0]);
-            split_tf32(vs[(8 * k + 1) * ROWV + 8 * n], bh[n][1], bl[n][1]);
-          }
+          for (int n = 0; n < NT; ++n) mma_tf32(t[r][n], ph, bl[n][0], bl[n][1]);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma_tf32(t[n], ph, bl[n][0], bl[n][1]);
+          for (int n = 0; n < NT; ++n) mma_tf32(t[r][n], pl, bh[n][0], bh[n][1]);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma_tf32(t[n], pl, bh[n][0], bh[n][1]);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) mma_tf32(t[n], ph, bh[n][0], bh[n][1]);
+          for (int n = 0; n < NT; ++n) mma_tf32(t[r][n], ph, bh[n][0], bh[n][1]);
         }
+      }
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
         const float a0 = a_s[16 * r + gr], a1 = a_s[16 * r + gr + 8];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[r][n][i] = fmaf(o[r][n][i], i < 2 ? a0 : a1, t[n][i]);
+          for (int i = 0; i < 4; ++i) o[r][n][i] = fmaf(o[r][n][i], i < 2 ? a0 : a1, t[r][n][i]);
       }
       __syncwarp();
       if (lane == 0) bar_arrive(&empty[b]);
@@ -485,7 +501,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
     }
     if (sub != 0 || f >= d.nf) continue;
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    const int r = (d.f0 + f) / p.group;
+    const int r = row_of(p, d.f0 + f);
     const int64_t at = (int64_t)(d.row0 + r) * p.n_q_heads + d.head * p.group + (d.f0 + f - r * p.group);
 #pragma unroll
     for (int i = 0; i < CPL / 4; ++i) {

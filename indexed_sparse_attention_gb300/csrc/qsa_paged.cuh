@@ -39,6 +39,7 @@ struct PagedParams {
   int32_t n_seqs;
   int32_t n_rows;            // rows of q and out
   int32_t n_q_heads, n_kv_heads, group;
+  uint32_t group_magic;      // ceil(2^32 / group); group 1: not used
   float scale;
   int32_t window, n_sinks;   // window 0: every token up to the row's own
   const void* q;             // [n_rows, Hq, D]
@@ -137,6 +138,13 @@ __device__ __forceinline__ SeqRows seq_rows(const PagedParams& p, int i) {
   return s;
 }
 
+// Row of entry f: f / group, for f below 2^28 (f * (magic * group - 2^32) is below
+// 2^32 then, as group <= 16).  Divisions by a value that only the host knows are
+// most of what finding a run and opening an item take.
+__device__ __forceinline__ int row_of(const PagedParams& p, int f) {
+  return p.group == 1 ? f : (int)__umulhi((uint32_t)f, p.group_magic);
+}
+
 template <int KT>
 struct Tiles {
   int32_t count;      // key tiles of the item (at least 1)
@@ -148,7 +156,7 @@ struct Tiles {
 // The key tiles of entries [m MT, (m + 1) MT) of a sequence's rows.
 template <int KT>
 __device__ __forceinline__ Tiles<KT> item_tiles(const PagedParams& p, const SeqRows& s, int mt, int m) {
-  const int j0 = m * mt / p.group, j1 = min(s.n - 1, ((m + 1) * mt - 1) / p.group);
+  const int j0 = row_of(p, m * mt), j1 = min(s.n - 1, row_of(p, (m + 1) * mt - 1));
   const int p0 = s.len - s.n + j0, p1 = s.len - s.n + j1;
   const int end = max(p1 + 1, 0);
   const int last = (end + KT - 1) / KT;

@@ -50,7 +50,7 @@ qsa_status check_batch(const qsa_paged_batch* b, const char* fn) {
   if (!b) return fail(QSA_ERR_INVALID_ARG, "%s: null batch", fn);
   if (b->n_seqs < 0 || b->n_rows < 0 || b->max_rows < 0)
     return fail(QSA_ERR_INVALID_ARG, "%s: n_seqs=%d, n_rows=%d, max_rows=%d", fn, b->n_seqs, b->n_rows, b->max_rows);
-  if (b->n_rows > INT32_MAX / 64) return fail(QSA_ERR_UNSUPPORTED, "%s: too many rows", fn);
+  if (b->n_rows > (1 << 24) - 256) return fail(QSA_ERR_UNSUPPORTED, "%s: too many rows", fn);   // entries below 2^28
   if (b->n_seqs == 0 || b->n_rows == 0) return QSA_OK;
   if (!b->table || !b->lens || !b->row_start) return fail(QSA_ERR_INVALID_ARG, "%s: batch has a null array", fn);
   if (b->table_ld < 1) return fail(QSA_ERR_INVALID_ARG, "%s: table_ld=%lld", fn, (long long)b->table_ld);
@@ -146,6 +146,7 @@ QSA_API qsa_status qsa_paged_attn(const qsa_paged_cache* cache, const qsa_paged_
   p.n_q_heads = cfg->n_q_heads;
   p.n_kv_heads = cfg->n_kv_heads;
   p.group = cfg->n_q_heads / cfg->n_kv_heads;
+  p.group_magic = p.group == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32) + p.group - 1) / p.group);
   p.scale = cfg->scale > 0.f ? cfg->scale : 1.0f / sqrtf((float)cfg->head_dim);
   p.window = window;
   p.n_sinks = n_sinks;

@@ -247,8 +247,8 @@ __device__ __forceinline__ ItemRows item_rows(const PagedParams& p, const Cursor
   r.f0 = c.m * p.mt;
   r.nf = min(p.mt, c.s.n * p.group - r.f0);
   r.pos0 = c.s.len - c.s.n;
-  r.first = r.pos0 + r.f0 / p.group;
-  r.last = r.pos0 + (r.f0 + r.nf - 1) / p.group;
+  r.first = r.pos0 + row_of(p, r.f0);
+  r.last = r.pos0 + row_of(p, r.f0 + r.nf - 1);
   return r;
 }
 
@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       const ItemRows ir = item_rows(p, c);
       const int T = c.x1 - c.x;
       const bool mine = row < ir.nf;
-      const int pos = ir.pos0 + (ir.f0 + min(row, ir.nf - 1)) / p.group;
+      const int pos = ir.pos0 + row_of(p, ir.f0 + min(row, ir.nf - 1));
       const int low = p.window > 0 ? pos - p.window + 1 : 0;             // first token of the row's window
       const int dead = p.window > 0 ? ir.first - p.window : INT32_MIN;   // [n_sinks, dead]: no row's tokens
       float m = -INFINITY, l = 0.f;   // the maximum that this thread's sum l is relative to
@@ -774,7 +774,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const bool whole = c.whole();
       const int64_t part = (int64_t)c.slot(blockIdx.x) * p.mt + row;
-      const int r = (ir.f0 + row) / p.group;
+      const int r = row_of(p, ir.f0 + row);
       const int64_t entry = (int64_t)(c.s.row0 + r) * p.n_q_heads + c.head * p.group + (ir.f0 + row - r * p.group);
       if (tj > 1) wait(&h.pv_done[tj & 1], (uint32_t)(((tj - 2) >> 1) & 1), abrt);
       wait(&h.pv_done[(tj - 1) & 1], (uint32_t)(((tj - 1) >> 1) & 1), abrt);
