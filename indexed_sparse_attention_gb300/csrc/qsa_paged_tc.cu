@@ -105,7 +105,7 @@ struct Head {
   float m_run[128];             // the entries' running maxima
   float sums[2][128];           // the two groups' sums of weights
 };
-constexpr int kHeadBytes = 3072;
+constexpr int kHeadBytes = 3 * 1024;
 // fp8 caches: scales of the tiles in flight, behind the head.
 struct Scales {
   float k[8][kKT];   // times the logit scale and log2(e)

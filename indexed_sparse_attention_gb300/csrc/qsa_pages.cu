@@ -41,8 +41,8 @@ __device__ __forceinline__ int scan(int v, int* smem, int& total) {
   return (warp ? before : 0) + inc - v;
 }
 
-__device__ __forceinline__ int pages_for(int64_t tokens, int page_tokens) {
-  return (int)((tokens + page_tokens - 1) / page_tokens);
+__device__ __forceinline__ int pages_for(int64_t tokens, int page_tokens) {   // (a power of two)
+  return (int)((tokens + page_tokens - 1) >> (__ffs(page_tokens) - 1));
 }
 
 // Tokens of place s, within what its table row holds.
@@ -61,13 +61,23 @@ __device__ __forceinline__ Slice slice(int n_pages) {
   return Slice{lo, min(lo + per, n_pages)};
 }
 
-// Whether place s of list entry i is in the pool and not listed before.
-__device__ __forceinline__ bool valid_place(const int* list_s, int i, int n_seqs) {
-  const int s = list_s[i];
-  if (s < 0 || s >= n_seqs) return false;
-  for (int j = 0; j < i; ++j)
-    if (list_s[j] == s) return false;
-  return true;
+// Whether the place of this thread's list entry is in the pool and not listed
+// before; list_s holds the n entries.  All threads call it.  A warp compares its
+// 32 entries with each other by one match and with the warps' before, four at a
+// time: a loop over the entries before, of a length of its own in each lane, was
+// most of the time of a call with 32 requests (extending them 16.5 us, 3 this way).
+__device__ __forceinline__ bool valid_place(const int* list_s, int n, int n_seqs) {
+  const int i = (int)threadIdx.x, lane = i & 31;
+  const int s = i < n ? list_s[i] : -1;
+  bool first = (__match_any_sync(0xffffffffu, s) & ((1u << lane) - 1u)) == 0u;
+  if ((i & ~31) < n) {
+#pragma unroll 1
+    for (int j = 0; j < (i & ~31); j += 4) {
+      const int4 e = *reinterpret_cast<const int4*>(list_s + j);
+      first = first && e.x != s && e.y != s && e.z != s && e.w != s;
+    }
+  }
+  return i < n && first && s >= 0 && s < n_seqs;
 }
 
 // Pages of one round of the plan: 8 consecutive ones a thread.
@@ -136,7 +146,7 @@ __device__ __forceinline__ int request_of(const int* off_s, int n, int r) {
 // ------------------------------------------------------------------ extend
 __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const qsa_page_pool pool, const int32_t* seqs,
                                                               const int32_t* n_new, int n) {
-  __shared__ int list_s[QSA_MAX_PAGE_REQUESTS], off_s[QSA_MAX_PAGE_REQUESTS + 1], have_s[QSA_MAX_PAGE_REQUESTS];
+  __shared__ __align__(16) int list_s[QSA_MAX_PAGE_REQUESTS], off_s[QSA_MAX_PAGE_REQUESTS + 1], have_s[QSA_MAX_PAGE_REQUESTS];
   __shared__ int scan_s[32];
   grid_dependency_sync();
   const int i = (int)threadIdx.x;
@@ -144,7 +154,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const qsa_page_poo
   __syncthreads();
   int need = 0, len = 0, add = 0;
   bool valid = false;
-  if (i < n && valid_place(list_s, i, pool.n_seqs)) {
+  if (valid_place(list_s, n, pool.n_seqs)) {
     len = place_len(pool, list_s[i]);
     add = __ldcg(n_new + i);
     const int64_t after = (int64_t)len + add;
@@ -176,7 +186,7 @@ struct ForkPlan {
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const qsa_page_pool pool, const int32_t* src,
                                                                  const int32_t* dst, const int32_t* keep, int n,
                                                                  ForkPlan* plan) {
-  __shared__ int list_s[QSA_MAX_PAGE_REQUESTS], off_s[QSA_MAX_PAGE_REQUESTS + 1], page_s[QSA_MAX_PAGE_REQUESTS];
+  __shared__ __align__(16) int list_s[QSA_MAX_PAGE_REQUESTS], off_s[QSA_MAX_PAGE_REQUESTS + 1], page_s[QSA_MAX_PAGE_REQUESTS];
   __shared__ int scan_s[32];
   grid_dependency_sync();
   const int i = (int)threadIdx.x;
@@ -187,7 +197,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const qsa_page_
   __syncthreads();
   int need = 0, len = 0, s = 0;
   bool valid = false;
-  if (i < n && valid_place(list_s, i, pool.n_seqs)) {
+  if (valid_place(list_s, n, pool.n_seqs)) {
     s = __ldcg(src + i);
     if (s >= 0 && s < pool.n_seqs && __ldcg(pool.lens + list_s[i]) == 0) {
       len = place_len(pool, s);
@@ -335,14 +345,15 @@ __global__ void __launch_bounds__(kCopyThreads) free_kernel(const qsa_page_pool 
 // counts that the others of the call change.
 __global__ void __launch_bounds__(kPlanThreads) cut_kernel(const qsa_page_pool pool, const int32_t* seqs,
                                                            const int32_t* keep, int n) {
-  __shared__ int list_s[QSA_MAX_PAGE_REQUESTS], len_s[QSA_MAX_PAGE_REQUESTS], keep_s[QSA_MAX_PAGE_REQUESTS];
+  __shared__ __align__(16) int list_s[QSA_MAX_PAGE_REQUESTS], len_s[QSA_MAX_PAGE_REQUESTS], keep_s[QSA_MAX_PAGE_REQUESTS];
   grid_dependency_sync();
   const int i = (int)threadIdx.x;
   if (i < n) list_s[i] = __ldcg(seqs + i);
   __syncthreads();
+  const bool listed = valid_place(list_s, n, pool.n_seqs);
   if (i < n) {
     int k = -1, len = 0;
-    if (valid_place(list_s, i, pool.n_seqs)) {
+    if (listed) {
       len = place_len(pool, list_s[i]);
       k = __ldcg(keep + i);
       if (k >= len && k >= 0) k = len;   // nothing to give up
