@@ -53,17 +53,20 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kKT = 128;                      // keys of a tile
 constexpr int kHalf = kKT * 128;              // bytes of 64 channels of a tile
 constexpr int kSlab = 2 * kHalf;              // bytes of 128 channels: what the ring holds
-constexpr int kMaxSlabs = 3;                 // of K, and of V
+constexpr int kMaxSlabs = 6;                 // of K, and of V (bf16: 3, see Head::pv_done)
 constexpr int kKeyWarp = 8, kMmaWarp = 9, kValueWarp = 10, kQWarp = 11, kCodeWarp = 12, kCodeWarps = 4;
-__host__ __device__ constexpr int threads_of(bool f8) { return 32 * (f8 ? kCodeWarp + kCodeWarps : kCodeWarp); }
+constexpr int kSoftWarps = 8;
+__host__ __device__ constexpr int threads_of(bool f8) { return 32 * (f8 ? kCodeWarp + kCodeWarps : kQWarp + 1); }
 constexpr int kCodeSlab = kKT * 128;          // bytes of the codes of a slab (fp8 caches)
-constexpr int kMaxCodeSlabs = 4;             // of K, and of V
+constexpr int kMaxCodeSlabs = 4;             // of V
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSmemLimit = 227 * 1024;
 constexpr float kMoveMax = 8.f;               // log2 of the weight at which the running maximum is moved
 
 constexpr uint32_t kIdescS = idesc_bf16(128, kKT, false, false);
 constexpr uint32_t kIdescO = idesc_bf16(128, 128, false, true);
+// kind::f8f6f4 with a 32-bit accumulator: E4M3 A and B (bits 7-12 = 0), both K-major.
+constexpr uint32_t kIdescS8 = (1u << 4) | ((uint32_t)(kKT >> 3) << 17) | (8u << 24);
 
 __device__ int g_timeouts;
 __device__ int g_bad_pages;
@@ -74,8 +77,8 @@ struct TcParams {
   CUtensorMap k, v;
   CUtensorMap q;         // {D, Hq, n_rows}: boxes of 64 channels x a KV head's query heads x an item's rows
   PagedParams p;
-  int32_t n_k, n_v;              // slabs in the rings of K and V
-  int32_t n_code_k, n_code_v;    // fp8 caches: slabs of codes
+  int32_t n_k, n_v;              // slabs in the rings of K (fp8 caches: of codes) and V
+  int32_t n_code_v;              // fp8 caches: slabs of V's codes
 };
 
 // bar_wait with everything behind its first try out of line: the loops of the
@@ -96,7 +99,7 @@ __device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, int* abort) {
 struct Head {
   uint64_t full[2][kMaxSlabs], empty[2][kMaxSlabs];   // K, V
   uint64_t s_full[3], p_full[2][3], pv_done[2], m_done[2], o_free, q_full, q_free, mma_done;
-  uint64_t code_full[2][kMaxCodeSlabs], code_empty[2][kMaxCodeSlabs];
+  uint64_t code_full[kMaxCodeSlabs], code_empty[kMaxCodeSlabs], sc_full[8];   // fp8 caches: V's codes, scales
   int64_t scan[16];
   Start start;
   uint32_t tmem;
@@ -110,6 +113,7 @@ constexpr int kHeadBytes = 3 * 1024;
 struct Scales {
   float k[8][kKT];   // times the logit scale and log2(e)
   float v[8][kKT];
+  float q[4][128];   // of an item's rows of Q: the power of two that its codes were divided by
 };
 static_assert(sizeof(Head) <= kHeadBytes, "shared memory head");
 
@@ -119,6 +123,25 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, 
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// D[tmem] (+)= A[smem] B[smem] of 8-bit types, 32 of K.
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Two values to E4M3, the first in the low byte, and back.
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+  unsigned short r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t two) {
+  uint32_t h2;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((unsigned short)two));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h2));
 }
 // A box of a page's tokens: (token of the page, 64-channel block, KV head, page).
 __device__ __forceinline__ void tma_5d(void* dst, const CUtensorMap* map, int token, int block, int head, int page,
@@ -280,9 +303,9 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
   uint8_t* q_s = raw + kHeadBytes + (F8 ? sizeof(Scales) : 0);
   const int q_slab = (p.mt * 128 + 1023) / 1024 * 1024;
   uint8_t* k_ring = q_s + 2 * NS * q_slab;
-  uint8_t* v_ring = k_ring + tp.n_k * kSlab;
-  uint8_t* k_codes = v_ring + tp.n_v * kSlab;
-  uint8_t* v_codes = k_codes + tp.n_code_k * kCodeSlab;
+  constexpr int kKeySlab = F8 ? kCodeSlab : kSlab;   // (the products take K's codes as they are)
+  uint8_t* v_ring = k_ring + tp.n_k * kKeySlab;
+  uint8_t* v_codes = v_ring + tp.n_v * kSlab;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int quarters = (p.mt + 31) / 32, soft_threads = 64 * quarters;
   int* abrt = &h.abort;
@@ -290,14 +313,15 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
   if (tid == 0) {
     for (int kv = 0; kv < 2; ++kv) {
       for (int i = 0; i < kMaxSlabs; ++i) {
-        bar_init(&h.full[kv][i], F8 ? kCodeWarps : 1);
+        bar_init(&h.full[kv][i], F8 && kv == 1 ? kCodeWarps : 1);
         bar_init(&h.empty[kv][i], 1);
       }
-      for (int i = 0; F8 && i < kMaxCodeSlabs; ++i) {
-        bar_init(&h.code_full[kv][i], 1);
-        bar_init(&h.code_empty[kv][i], kCodeWarps);
-      }
     }
+    for (int i = 0; F8 && i < kMaxCodeSlabs; ++i) {
+      bar_init(&h.code_full[i], 1);
+      bar_init(&h.code_empty[i], kCodeWarps);
+    }
+    for (int i = 0; F8 && i < 8; ++i) bar_init(&h.sc_full[i], kCodeWarps);
     for (int i = 0; i < 3; ++i) {
       bar_init(&h.s_full[i], 1);
       bar_init(&h.p_full[0][i], quarters);
@@ -308,7 +332,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       bar_init(&h.m_done[i], quarters);
     }
     bar_init(&h.o_free, 2 * quarters);
-    bar_init(&h.q_full, 1);
+    bar_init(&h.q_full, F8 ? kCodeWarps : 1);
     bar_init(&h.q_free, 1);
     bar_init(&h.mma_done, 1);
     h.abort = 0;
@@ -338,10 +362,10 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
     const int n_copies = F8 || n_box == 1 ? n_box : 2 * n_box;   // copies of a slab; lane b's: box b % n_box, ...
     const int my_box = lane % n_box, half = !F8 && n_box > 1 && lane >= n_box ? 1 : 0;   // ... channels 64 * half on
     const int at_box = my_box * box * 128 + half * kHalf;
-    uint64_t* fulls = F8 ? h.code_full[kv] : h.full[kv];
-    uint64_t* empties = F8 ? h.code_empty[kv] : h.empty[kv];
-    uint8_t* const to_ring = F8 ? (kv ? v_codes : k_codes) : (kv ? v_ring : k_ring);
-    const int n_ring = F8 ? (kv ? tp.n_code_v : tp.n_code_k) : (kv ? tp.n_v : tp.n_k);
+    uint64_t* fulls = F8 && kv ? h.code_full : h.full[kv];
+    uint64_t* empties = F8 && kv ? h.code_empty : h.empty[kv];
+    uint8_t* const to_ring = kv ? (F8 ? v_codes : v_ring) : k_ring;
+    const int n_ring = kv ? (F8 ? tp.n_code_v : tp.n_v) : tp.n_k;
     const bool leader = elect_one();
     Ring at;
     int tj = 0;
@@ -402,16 +426,12 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       if (uses > 0) bar_wait(fulls + lane, (uses - 1) & 1, &g_timeouts);
     }
   } else if (F8 && warp >= kCodeWarp) {
-    // ------------------------------------------------------------ codes to bf16
-    // A slab's codes, 16 a thread at a time, to the layout the products read;
-    // exact.  Tokens that no row sees become zeros, whatever their codes and
-    // scales.  Thread i also keeps token i's scales, whose page it looks up two
-    // tiles ahead and loads one tile ahead.
-    const int ct = tid - 32 * kCodeWarp;
+    // ------------------------------------------------------------ fp8: Q, scales, V
+    const int ct = tid - 32 * kCodeWarp, cw = warp - kCodeWarp;
     const float zs = p.scale * kLog2e;
-    Ring from[2], to[2];
-    int tj = 0;
-    for (bool more = true; more; more = c.next(p, p.mt)) {
+    Ring in, out;
+    int tj = 0, it = 0;
+    for (bool more = true; more; more = c.next(p, p.mt), ++it) {
       const ItemRows ir = item_rows(p, c);
       const int T = c.x1 - c.x;
       auto visible = [&](int t) {
@@ -429,10 +449,94 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
                               p.kv_scale + 4 * (page * p.s_page_stride + c.head * p.s_head_stride + slot * p.s_tok_stride)));
       };
       int page = look_up(0);
+      // Q as E4M3: with the row's largest magnitude brought to [2^7, 2^8) by a power
+      // of two, a value is the sum of its nearest code and the nearest code of what
+      // that leaves.  bf16 has 8 significant bits and a code 4, so the sum is exact
+      // from 2^-9 of the row's maximum on; below, it is off by at most 2^-10, 2^-17
+      // of that maximum.  (Larger rows of Q than that against smaller channels reach
+      // the logits less than the weights' own rounding to bf16, 2^-9, reaches the
+      // output.)  A warp a row, D / 32 channels a lane, four rows in flight.
+      if (it > 0) wait(&h.q_free, (uint32_t)((it - 1) & 1), abrt);
+      {
+        constexpr int kCh = D / 32, kBatch = 4;
+        const int at_x = (lane * kCh) & 127;   // channel within the slab of 128
+        uint8_t* const hi_s = q_s + (lane * kCh >> 7) * q_slab;
+        uint8_t* const lo_s = hi_s + NS * q_slab;
+#pragma unroll 1
+        for (int r0 = cw; r0 < ir.nf; r0 += kBatch * kCodeWarps) {
+          uint32_t x[kBatch][kCh / 2];
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            const int f = ir.f0 + min(r0 + b * kCodeWarps, ir.nf - 1), r = row_of(p, f);
+            const int64_t entry = (int64_t)(c.s.row0 + r) * p.n_q_heads + c.head * p.group + (f - r * p.group);
+            const char* from = static_cast<const char*>(p.q) + (entry * D + lane * kCh) * 2;
+            if constexpr (kCh == 8) {
+              const uint4 v = __ldg(reinterpret_cast<const uint4*>(from));
+              x[b][0] = v.x, x[b][1] = v.y, x[b][2] = v.z, x[b][3] = v.w;
+            } else {
+              const uint2 v = __ldg(reinterpret_cast<const uint2*>(from));
+              x[b][0] = v.x, x[b][1] = v.y;
+            }
+          }
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            const int row = r0 + b * kCodeWarps;
+            uint32_t most = 0u;   // the largest magnitude's bits (ordered as the values are; NaN above all)
+#pragma unroll
+            for (int i = 0; i < kCh / 2; ++i)
+              most = max(most, max((x[b][i] << 16) & 0x7fff0000u, x[b][i] & 0x7fff0000u));
+            most = __reduce_max_sync(0xffffffffu, most);
+            // 2^(exponent - 7), at least 2^-100: a row of smaller values keeps fewer bits.
+            const int e = max((int)(most >> 23) - 127 - 7, -100);
+            const float up = __uint_as_float((uint32_t)(127 - e) << 23);
+            const bool odd = most >= 0x7f800000u;   // infinity or NaN: the row's logits are NaN
+            uint32_t hi[kCh / 4], lo[kCh / 4];
+#pragma unroll
+            for (int i = 0; i < kCh / 4; ++i) {
+              const float v0 = __uint_as_float(x[b][2 * i] << 16) * up, v1 = __uint_as_float(x[b][2 * i] & 0xffff0000u) * up,
+                          v2 = __uint_as_float(x[b][2 * i + 1] << 16) * up,
+                          v3 = __uint_as_float(x[b][2 * i + 1] & 0xffff0000u) * up;
+              const uint32_t h01 = to_e4m3x2(v0, v1), h23 = to_e4m3x2(v2, v3);
+              const float2 b01 = from_e4m3x2(h01), b23 = from_e4m3x2(h23);
+              hi[i] = odd ? 0x7f7f7f7fu : h01 | h23 << 16;
+              lo[i] = odd ? 0u : to_e4m3x2(v0 - b01.x, v1 - b01.y) | to_e4m3x2(v2 - b23.x, v3 - b23.y) << 16;
+            }
+            if (row < ir.nf) {
+              const int at = row * 128 + ((((at_x >> 4) ^ (row & 7)) << 4) | (at_x & 15));
+              if constexpr (kCh == 8) {
+                *reinterpret_cast<uint2*>(hi_s + at) = make_uint2(hi[0], hi[1]);
+                *reinterpret_cast<uint2*>(lo_s + at) = make_uint2(lo[0], lo[1]);
+              } else {
+                *reinterpret_cast<uint32_t*>(hi_s + at) = hi[0];
+                *reinterpret_cast<uint32_t*>(lo_s + at) = lo[0];
+              }
+              if (lane == 0) sc.q[it & 3][row] = odd ? 1.f : __uint_as_float((uint32_t)(127 + e) << 23);
+            }
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&h.q_full);
+      }
       uint32_t record = load(0, page);
       page = look_up(1);
-      auto convert = [&](int j, int kv) {   // K of tile j with both scales, or V
-        Ring &in = from[kv], &out = to[kv];
+      // A tile's scales; each thread has its token's page two tiles ahead and its
+      // record one tile ahead.  The tile eight before it is done: what was converted
+      // last is V of the tile NB before it, into a slot that the tile n_v / NS <= 5
+      // further back had left.
+      auto put_scales = [&](int j) {
+        const __half2 both = *reinterpret_cast<const __half2*>(&record);
+        // (At least 1e-30: minus infinity times it stays minus infinity.)
+        sc.k[(tj + j) & 7][ct] = fmaxf(__low2float(both) * zs, 1e-30f);
+        sc.v[(tj + j) & 7][ct] = __high2float(both);
+        __syncwarp();
+        if (lane == 0) bar_arrive(&h.sc_full[(tj + j) & 7]);
+        record = load(j + 1, page);
+        page = look_up(j + 2);
+      };
+      // V's codes, 16 a thread at a time, to bf16 in the layout the product reads;
+      // exact.  Tokens that no row sees become zeros, whatever their codes.
+      auto convert = [&](int j) {
         const int t0 = c.tiles.token(c.x + j);
         // Tokens [0, cut) of the tile less [gap0, gap1) are seen by some row.
         auto slot_of = [&](int t) { return min(max(t - t0, 0), kKT); };
@@ -441,22 +545,10 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
         const int gap1 = p.window > 0 ? slot_of(ir.first - p.window + 1) : 0;
 #pragma unroll 1
         for (int s = 0; s < NS; ++s) {
-          wait(&h.code_full[kv][in.slot], in.use & 1, abrt);
-          if (out.use > 0) wait(&h.empty[kv][out.slot], (out.use - 1) & 1, abrt);
-          if (kv == 0 && s == 0) {
-            // V is at most three tiles ahead of its product, K at most NB: the output
-            // of the tile eight before this one is done, and its scales may go.
-            // (At least 1e-30: minus infinity times it stays minus infinity.)
-            const __half2 both = *reinterpret_cast<const __half2*>(&record);
-            if (ct < kKT) {
-              sc.k[(tj + j) & 7][ct] = fmaxf(__low2float(both) * zs, 1e-30f);
-              sc.v[(tj + j) & 7][ct] = __high2float(both);
-            }
-            record = load(j + 1, page);
-            page = look_up(j + 2);
-          }
-          const uint8_t* src = (kv ? v_codes : k_codes) + in.slot * kCodeSlab;
-          uint8_t* dst = (kv ? v_ring : k_ring) + out.slot * kSlab;
+          wait(&h.code_full[in.slot], in.use & 1, abrt);
+          if (out.use > 0) wait(&h.empty[1][out.slot], (out.use - 1) & 1, abrt);
+          const uint8_t* src = v_codes + in.slot * kCodeSlab;
+          uint8_t* dst = v_ring + out.slot * kSlab;
           const int piece = ct & 7;   // 16 channels of a token
 #pragma unroll 4
           for (int tk = ct >> 3; tk < kKT; tk += 4 * kCodeWarps) {
@@ -481,21 +573,21 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
           fence_async_smem();
           __syncwarp();
           if (lane == 0) {
-            bar_arrive(&h.full[kv][out.slot]);
-            bar_arrive(&h.code_empty[kv][in.slot]);
+            bar_arrive(&h.full[1][out.slot]);
+            bar_arrive(&h.code_empty[in.slot]);
           }
-          in.step(kv ? tp.n_code_v : tp.n_code_k);
-          out.step(kv ? tp.n_v : tp.n_k);
+          in.step(tp.n_code_v);
+          out.step(tp.n_v);
         }
       };
 #pragma unroll 1
       for (int j = 0; j < T + NB - 1; ++j) {
-        if (j < T) convert(j, 0);
-        if (j >= NB - 1) convert(j - (NB - 1), 1);
+        if (j < T) put_scales(j);
+        if (j >= NB - 1) convert(j - (NB - 1));
       }
       tj += T;
     }
-  } else if (warp == kQWarp) {
+  } else if (!F8 && warp == kQWarp) {
     // ------------------------------------------------------------ Q
     // An item holds whole rows, so its entries are one box for each 64 channels.
     const bool leader = elect_one();
@@ -536,9 +628,12 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
           live = __all_sync(0xffffffffu, wait(&h.full[0][ka.slot], ka.use & 1, abrt) && live);
           fence_after();
           if (leader && live) {
-            const uint64_t k = k_desc + (uint32_t)(ka.slot * (kSlab >> 4)), q = q_desc + 2 * s * q_step;
+            const uint64_t k = k_desc + (uint32_t)(ka.slot * (kKeySlab >> 4)), q = q_desc + (F8 ? 1 : 2) * s * q_step;
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
+            for (int x = 0; F8 && x < 8; ++x)   // both codes of Q's values
+              mma_f8(d, q + (x >> 2) * NS * q_step + 2 * (x & 3), k + 2 * (x & 3), kIdescS8, (s | x) != 0 ? 1u : 0u);
+#pragma unroll
+            for (int x = 0; !F8 && x < 8; ++x)
               mma_bf16(d, q + (x >> 2) * q_step + 2 * (x & 3), k + (x >> 2) * (kHalf >> 4) + 2 * (x & 3), kIdescS,
                        (s | x) != 0 ? 1u : 0u);
             commit(&h.empty[0][ka.slot]);
@@ -593,15 +688,17 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
     if (leader) commit(&h.mma_done);   // every MMA has completed before TMEM is released
     __syncwarp();
     bar_wait(&h.mma_done, 0u, &g_timeouts);
-  } else if ((warp & 3) < quarters) {
+  } else if (warp < kSoftWarps && (warp & 3) < quarters) {
     // ------------------------------------------------------------ softmax and output
     // Two groups of four warps take the tiles in turn: one group's exponentials
     // run beside the other's maxima.  A thread owns one entry.
     const int group = warp >> 2, row = 32 * (warp & 3) + lane;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    // Logits to base 2; the scales of an fp8 cache's keys hold the factor already.
-    const float zc = F8 ? 1.f : p.scale * kLog2e, move = fminf(kMoveMax / zc, 1e30f);
+    // Logits to base 2; the scales of an fp8 cache's keys hold the factor already,
+    // and what is left is the power of two that the row of Q was divided by.
+    float zc = p.scale * kLog2e, move = fminf(kMoveMax / zc, 1e30f);
     int tj = 0;   // tiles done
+    [[maybe_unused]] int it = 0;
     for (bool more = true; more;) {
       const ItemRows ir = item_rows(p, c);
       const int T = c.x1 - c.x;
@@ -609,6 +706,12 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       const int pos = ir.pos0 + row_of(p, ir.f0 + min(row, ir.nf - 1));
       const int low = p.window > 0 ? pos - p.window + 1 : 0;             // first token of the row's window
       const int dead = p.window > 0 ? ir.first - p.window : INT32_MIN;   // [n_sinks, dead]: no row's tokens
+      if constexpr (F8) {
+        wait(&h.q_full, (uint32_t)(it & 1), abrt);
+        zc = mine ? sc.q[it & 3][row] : 1.f;   // (four items: a group may be one behind the other, Q one ahead)
+        move = fminf(kMoveMax / zc, 1e30f);
+        ++it;
+      }
       float m = -INFINITY, l = 0.f;   // the maximum that this thread's sum l is relative to
       for (int j = (tj ^ group) & 1; j < T; j += 2) {
         const int g = tj + j, buf = g % NB, t0 = c.tiles.token(c.x + j);
@@ -639,6 +742,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
           }
         }
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if constexpr (F8) wait(&h.sc_full[g & 7], (uint32_t)((g >> 3) & 1), abrt);
         const float* ks = F8 ? sc.k[g & 7] : nullptr;
         const float* vs = F8 ? sc.v[g & 7] : nullptr;
         auto take_max = [&](uint32_t(&x)[32], uint32_t col) {
@@ -719,7 +823,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
         // Weights: in bf16 for the product, their sum in 32 bits.  32 logits
         // become 16 columns of weights, always behind the logits still to be read.
         const float shift = m == -INFINITY ? 0.f : -m * zc;
-        [[maybe_unused]] const uint64_t zc2 = pack2(zc, zc);
+        const uint64_t zc2 = pack2(zc, zc);
         const uint64_t shift2 = pack2(shift, shift);
         uint64_t sum2[2] = {0ull, 0ull};
         auto weigh = [&](uint32_t(&x)[32], uint32_t col) {
@@ -728,8 +832,8 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
           for (int i = 0; i < 16; ++i) {
             float a, b;
             uint64_t z = pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-            if constexpr (F8) z = fma2(z, *reinterpret_cast<const uint64_t*>(ks + col + 2 * i), shift2);
-            else z = fma2(z, zc2, shift2);
+            if constexpr (F8) z = mul2(z, *reinterpret_cast<const uint64_t*>(ks + col + 2 * i));
+            z = fma2(z, zc2, shift2);
             unpack2(z, a, b);
             a = ex2(a);
             b = ex2(b);
@@ -839,7 +943,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
-bool encode_pages(CUtensorMap* map, const void* base, const PagedParams& p, int head_dim, bool f8) {
+bool encode_pages(CUtensorMap* map, const void* base, const PagedParams& p, int head_dim, bool f8, bool swizzle) {
   PFN_cuTensorMapEncodeTiled_v12000 f = encoder();
   if (!f) return false;
   const cuuint64_t page = (cuuint64_t)1 << p.page_shift;
@@ -850,7 +954,8 @@ bool encode_pages(CUtensorMap* map, const void* base, const PagedParams& p, int 
     const cuuint64_t strides[3] = {(cuuint64_t)p.tok_stride, (cuuint64_t)p.head_stride, (cuuint64_t)p.page_stride};
     const cuuint32_t box[4] = {128, tokens, 1, 1};
     return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, step,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   }
   const cuuint64_t dims[5] = {64, page, (cuuint64_t)head_dim / 64, (cuuint64_t)p.n_kv_heads, (cuuint64_t)p.n_pages};
@@ -878,22 +983,23 @@ template <int D, bool F8>
 cudaError_t launch_d(const PagedParams& p, int grid, cudaStream_t st) {
   TcParams tp{};
   tp.p = p;
-  if (!encode_pages(&tp.k, p.k, p, D, F8) || !encode_pages(&tp.v, p.v, p, D, F8) || !encode_queries(&tp.q, p, D))
+  if (!encode_pages(&tp.k, p.k, p, D, F8, true) || !encode_pages(&tp.v, p.v, p, D, F8, !F8) ||
+      (!F8 && !encode_queries(&tp.q, p, D)))
     return cudaErrorInvalidValue;
   const int q_slab = (p.mt * 128 + 1023) / 1024 * 1024;
   const int fixed = kHeadBytes + (F8 ? (int)sizeof(Scales) : 0) + D / 64 * q_slab, room = kSmemLimit - fixed;
-  if (F8) {   // operands of a whole tile of V, of K as the codes leave room, the rest for codes
+  if (F8) {   // operands of a whole tile of V, the rest for codes
     tp.n_v = 2;
-    tp.n_k = room >= 4 * kSlab + 4 * kCodeSlab ? 2 : 1;
-    const int n = (room - (tp.n_k + tp.n_v) * kSlab) / kCodeSlab;
-    tp.n_code_k = std::min((n + 1) / 2, kMaxCodeSlabs);
+    const int n = (room - tp.n_v * kSlab) / kCodeSlab;
     tp.n_code_v = std::min(n / 2, kMaxCodeSlabs);
+    tp.n_k = std::min(n - tp.n_code_v, kMaxSlabs);
   } else {
     const int n = room / kSlab;
-    tp.n_k = std::min((n + 1) / 2, kMaxSlabs);
-    tp.n_v = std::min(n / 2, kMaxSlabs);
+    tp.n_k = std::min((n + 1) / 2, 3);
+    tp.n_v = std::min(n / 2, 3);
   }
-  const size_t smem = (size_t)fixed + (size_t)(tp.n_k + tp.n_v) * kSlab + (size_t)(tp.n_code_k + tp.n_code_v) * kCodeSlab;
+  const size_t smem = (size_t)fixed + (size_t)tp.n_k * (F8 ? kCodeSlab : kSlab) + (size_t)tp.n_v * kSlab +
+                      (size_t)tp.n_code_v * kCodeSlab;
   cudaError_t e = allow_dynamic_smem((const void*)paged_tc_kernel<D, F8>, kSmemLimit);
   if (e != cudaSuccess) return e;
   return launch_kernel(paged_tc_kernel<D, F8>, dim3((unsigned)grid), dim3(threads_of(F8)), smem, st, 0u, tp);

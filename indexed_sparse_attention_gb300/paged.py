@@ -64,9 +64,14 @@ def declare(L: ctypes.CDLL):
 
 # ---------------------------------------------------------------------- devices and streams
 
+#: The handle of a device's current stream; torch.cuda.current_stream builds a Stream object around it (2 us a call).
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _raw_stream(stream, device) -> int:
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return _current_stream(device.index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
