@@ -348,8 +348,8 @@ __global__ void __launch_bounds__(kF32Threads, 1) paged_f32_kernel(const PagedPa
     const bool whole = c.whole();
     const int64_t slot = whole ? 0 : (int64_t)c.slot(blockIdx.x) * p.mt;
     if ((tid & 7) == 0 && row < nf) {
-      l_s[row] = l > 0.f ? 1.f / l : 0.f;
-      const float lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
+      l_s[row] = l == 0.f ? 0.f : 1.f / l;
+      const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);   // (a row of NaN keeps it)
       if (!whole) p.part_lse[slot + row] = lse2;
       else if (p.lse) p.lse[entry(row)] = lse2 * kLn2;
     }
@@ -389,6 +389,13 @@ __global__ void __launch_bounds__(kF32Threads, 1) paged_f32_kernel(const PagedPa
 constexpr int kJoinWarps = 8;
 constexpr int kJoinThreads = 32 * kJoinWarps;
 constexpr int kMaxRuns = 1024;
+
+// The larger one; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
 __device__ __forceinline__ int join_warps(int n_parts) { return n_parts >= 24 ? 8 : n_parts >= 12 ? 4 : n_parts >= 6 ? 2 : 1; }
 
@@ -444,7 +451,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
       }
       float mn = m;
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) mn = fmaxf(mn, ls[k]);
+      for (int k = 0; k < kBatch; ++k) mn = max_nan(mn, ls[k]);
       if (mn == -INFINITY) continue;
       const float a = exp2f(m - mn);
       l *= a;
@@ -500,7 +507,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
       }
     }
     if (sub != 0 || f >= d.nf) continue;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     const int r = row_of(p, d.f0 + f);
     const int64_t at = (int64_t)(d.row0 + r) * p.n_q_heads + d.head * p.group + (d.f0 + f - r * p.group);
 #pragma unroll
@@ -514,7 +521,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
         to[1] = __floats2bfloat162_rn(o.z, o.w);
       }
     }
-    if (lane == 0 && p.lse) p.lse[at] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if (lane == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
 }
 

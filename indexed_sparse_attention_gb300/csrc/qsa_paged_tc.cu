@@ -875,7 +875,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       h.sums[group][row] = l;
       named_sync(1, soft_threads);
       l += h.sums[group ^ 1][row];
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = l == 0.f ? 0.f : 1.f / l;   // (NaN stays)
       const bool whole = c.whole();
       const int64_t part = (int64_t)c.slot(blockIdx.x) * p.mt + row;
       const int r = row_of(p, ir.f0 + row);
@@ -912,7 +912,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       __syncwarp();
       if (lane == 0) bar_arrive(&h.o_free);
       if (mine && group == 0) {
-        const float lse2 = l > 0.f ? fmaf(m, zc, log2f(l)) : -INFINITY;
+        const float lse2 = l == 0.f ? -INFINITY : fmaf(m, zc, log2f(l));
         if (!whole) p.part_lse[part] = lse2;
         else if (p.lse) p.lse[entry] = lse2 * kLn2;
       }

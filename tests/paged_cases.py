@@ -6,8 +6,15 @@ visible tokens; all sums in binary32):
   logits   a dot product of D terms and its scaling: |dz| <= (D + 4) u zmag,
            zmag = max_t scale * sum_d |q_d k_td|; two roundings of the base-2
            exponent: 2 u (|z| + |m|) <= 4 u zmag; ex2 is within 2 ulp: 4 u.
+           fp8 caches: Q goes into the product as the sum of two E4M3 codes, of the
+           value times a power of two that brings the row's maximum qmax to
+           [2^7, 2^8), and of what the first leaves.  bf16's 8 significant bits are
+           two codes' 4, and E4M3's smallest step is 2^-9, so values from 2^-2 on
+           are exact; below, half a step is lost: dq <= min(2^-10, |q|) after the
+           scaling, 2^-17 qmax where |q| < 2^-9 qmax.  |dz| grows by
+           zlost = max_t scale * sum_d dq_d |k_td|.
   weights  so each weight is off by a factor 1 +- e with e = (2 D + 24) u zmag +
-           8 u (weight and maximum), and the sums of n terms add n u.
+           8 u + 2 zlost (weight and maximum), and the sums of n terms add n u.
   out      |d out| <= 2 (e + (n + 16) u) wabs, wabs = sum_t w_t |v_t| / sum_t w_t;
            for bf16 and fp8 caches each weight is rounded to bf16 before the
            product with V: another 2^-8 wabs; a bf16 output: 2^-8 |out|.
@@ -152,6 +159,11 @@ def attend64(x: Paged, window=0, sinks=0, scale=None):
             w = torch.exp(z - L[..., None]).nan_to_num(0.0)
             cnt = see.sum(1)[:, None].double()
             e = (2 * D + 24) * U * mag + 8 * U
+            if x.scale is not None:
+                qmax = qh.abs().amax(-1, keepdim=True)
+                dq = torch.where(qh.abs() < 2.0 ** -9 * qmax, torch.minimum(qh.abs(), 2.0 ** -17 * qmax), 0.0)
+                lost = torch.einsum("rgd,td->rgt", dq, kh.abs()) * scale
+                e = e + 2 * lost.masked_fill(~see[:, None], 0.0).amax(-1)
             sl = slice(h * G, (h + 1) * G)
             out[r0:r0 + r, sl] = torch.einsum("rgt,td->rgd", w, vh)
             wabs = torch.einsum("rgt,td->rgd", w, vh.abs())

@@ -79,6 +79,35 @@ def test_page_sizes_and_scale():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp8", "f32"])
+@pytest.mark.parametrize("D", [128, 256])
+def test_queries_of_any_size(dtype, D):
+    # A channel far above the others, rows of zeros, of the smallest and of large values, next to ordinary ones.
+    x = make_paged([400, 130, 5], [9, 1, 2], dtype=dtype, D=D, seed=31, poison=True)
+    x.q[0, :, 5] *= 150
+    x.q[1] *= 2.0 ** -110
+    x.q[2] = 0
+    x.q[3] *= 2.0 ** -130
+    x.q[4, :, D - 1] = 2.0 ** -120
+    x.q[5, 1::2] *= 300
+    x.q[9, :, :D // 2] *= 0.001
+    check(x)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8", "f32"])
+def test_queries_that_are_no_numbers_stay_in_their_rows(dtype):
+    x = make_paged([300, 40], [5, 2], dtype=dtype, D=128, seed=32)
+    good = run(x)
+    x.q[1, 3, 7] = float("nan")
+    x.q[2, 4, 100] = float("inf")
+    bad = run(x)
+    rows = torch.ones(x.q.shape[:2], dtype=torch.bool)
+    rows[1, 3] = rows[2, 4] = False
+    for a, b in zip(good, bad):
+        assert torch.equal(a.cpu()[rows], b.cpu()[rows])
+    assert torch.isnan(bad[0][1, 3]).all() and torch.isnan(bad[0][2, 4]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8", "f32"])
 def test_tokens_outside_the_window_may_hold_anything(dtype):
     # Everything before the window and behind the sinks is NaN: in K, in V and in the scales.
     W, S, n, r = 100, 20, 600, 3
