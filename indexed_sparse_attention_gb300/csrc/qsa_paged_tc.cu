@@ -308,18 +308,20 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
   uint8_t* v_codes = v_ring + tp.n_v * kSlab;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int quarters = (p.mt + 31) / 32, soft_threads = 64 * quarters;
+  // Warps that convert V's codes: their own four, and those of the softmax's eight without entries.
+  const int code_warps = kCodeWarps + (kSoftWarps - 2 * quarters);
   int* abrt = &h.abort;
 
   if (tid == 0) {
     for (int kv = 0; kv < 2; ++kv) {
       for (int i = 0; i < kMaxSlabs; ++i) {
-        bar_init(&h.full[kv][i], F8 && kv == 1 ? kCodeWarps : 1);
+        bar_init(&h.full[kv][i], F8 && kv == 1 ? code_warps : 1);
         bar_init(&h.empty[kv][i], 1);
       }
     }
     for (int i = 0; F8 && i < kMaxCodeSlabs; ++i) {
       bar_init(&h.code_full[i], 1);
-      bar_init(&h.code_empty[i], kCodeWarps);
+      bar_init(&h.code_empty[i], code_warps);
     }
     for (int i = 0; F8 && i < 8; ++i) bar_init(&h.sc_full[i], kCodeWarps);
     for (int i = 0; i < 3; ++i) {
@@ -425,9 +427,11 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       const uint32_t uses = at.use + (lane < at.slot ? 1u : 0u);
       if (uses > 0) bar_wait(fulls + lane, (uses - 1) & 1, &g_timeouts);
     }
-  } else if (F8 && warp >= kCodeWarp) {
+  } else if (F8 && (warp >= kCodeWarp || (warp < kSoftWarps && (warp & 3) >= quarters))) {
     // ------------------------------------------------------------ fp8: Q, scales, V
-    const int ct = tid - 32 * kCodeWarp, cw = warp - kCodeWarp;
+    const int cw = warp >= kCodeWarp ? warp - kCodeWarp : kCodeWarps + (warp >> 2) * (4 - quarters) + (warp & 3) - quarters;
+    const int ct = 32 * cw + lane;
+    const bool own = cw < kCodeWarps;   // Q and the scales are these warps'
     const float zs = p.scale * kLog2e;
     Ring in, out;
     int tj = 0, it = 0;
@@ -440,7 +444,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       auto look_up = [&](int j) {   // the page of the thread's token of tile j, -1: none
         const int t = c.tiles.token(c.x + j) + ct;
         int32_t page = -1;
-        return j < T && visible(t) && page_of(p, c.seq, t, page) ? page : -1;
+        return own && j < T && visible(t) && page_of(p, c.seq, t, page) ? page : -1;
       };
       auto load = [&](int j, int page) {
         const int slot = (c.tiles.token(c.x + j) + ct) & ((1 << p.page_shift) - 1);
@@ -456,8 +460,8 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       // of that maximum.  (Larger rows of Q than that against smaller channels reach
       // the logits less than the weights' own rounding to bf16, 2^-9, reaches the
       // output.)  A warp a row, D / 32 channels a lane, four rows in flight.
-      if (it > 0) wait(&h.q_free, (uint32_t)((it - 1) & 1), abrt);
-      {
+      if (own) {
+        if (it > 0) wait(&h.q_free, (uint32_t)((it - 1) & 1), abrt);
         constexpr int kCh = D / 32, kBatch = 4;
         const int at_x = (lane * kCh) & 127;   // channel within the slab of 128
         uint8_t* const hi_s = q_s + (lane * kCh >> 7) * q_slab;
@@ -534,7 +538,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
         record = load(j + 1, page);
         page = look_up(j + 2);
       };
-      // V's codes, 16 a thread at a time, to bf16 in the layout the product reads;
+      // V's codes to bf16 in the layout the product reads;
       // exact.  Tokens that no row sees become zeros, whatever their codes.
       auto convert = [&](int j) {
         const int t0 = c.tiles.token(c.x + j);
@@ -543,32 +547,29 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
         const int cut = slot_of(ir.last + 1);
         const int gap0 = p.window > 0 ? slot_of(p.n_sinks) : 0;
         const int gap1 = p.window > 0 ? slot_of(ir.first - p.window + 1) : 0;
+        const bool some = cut < kKT || gap0 < gap1;
 #pragma unroll 1
         for (int s = 0; s < NS; ++s) {
           wait(&h.code_full[in.slot], in.use & 1, abrt);
           if (out.use > 0) wait(&h.empty[1][out.slot], (out.use - 1) & 1, abrt);
           const uint8_t* src = v_codes + in.slot * kCodeSlab;
           uint8_t* dst = v_ring + out.slot * kSlab;
-          const int piece = ct & 7;   // 16 channels of a token
+          // Eight threads a token, each 8 channels of one half of the slab and then of
+          // the other, tokens next to each other in opposite order: the loads of a
+          // warp and the stores of eight threads then touch all 32 banks.
+          const int piece = ct & 7, odd = (ct >> 3) & 1;
 #pragma unroll 4
-          for (int tk = ct >> 3; tk < kKT; tk += 4 * kCodeWarps) {
-            uint4 x = *reinterpret_cast<const uint4*>(src + tk * 128 + piece * 16);
-            if (tk >= cut || (tk >= gap0 && tk < gap1)) x = make_uint4(0u, 0u, 0u, 0u);
-            uint4 lo, hi;
-            lo.x = attn::e4m3x2_to_bf16x2(x.x & 0xffffu);
-            lo.y = attn::e4m3x2_to_bf16x2(x.x >> 16);
-            lo.z = attn::e4m3x2_to_bf16x2(x.y & 0xffffu);
-            lo.w = attn::e4m3x2_to_bf16x2(x.y >> 16);
-            hi.x = attn::e4m3x2_to_bf16x2(x.z & 0xffffu);
-            hi.y = attn::e4m3x2_to_bf16x2(x.z >> 16);
-            hi.z = attn::e4m3x2_to_bf16x2(x.w & 0xffffu);
-            hi.w = attn::e4m3x2_to_bf16x2(x.w >> 16);
-            // Pieces 4-7 go to the slab's second half and write their second
-            // chunk first: the eight lanes of a token then write all 32 banks.
-            uint8_t* row = dst + (piece >> 2) * kHalf + tk * 128;
-            const int c0 = 2 * (piece & 3), swap = piece >> 2;
-            *reinterpret_cast<uint4*>(row + (((c0 + swap) ^ (tk & 7)) << 4)) = swap ? hi : lo;
-            *reinterpret_cast<uint4*>(row + (((c0 + 1 - swap) ^ (tk & 7)) << 4)) = swap ? lo : hi;
+          for (int tk = ct >> 3; tk < kKT; tk += 4 * code_warps) {
+            uint2 x[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) x[i] = *reinterpret_cast<const uint2*>(src + tk * 128 + (i ^ odd) * 64 + piece * 8);
+            if (some && (tk >= cut || (tk >= gap0 && tk < gap1))) x[0] = x[1] = make_uint2(0u, 0u);
+            uint8_t* row = dst + tk * 128 + ((piece ^ (tk & 7)) << 4);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              *reinterpret_cast<uint4*>(row + (i ^ odd) * kHalf) =
+                  make_uint4(attn::e4m3x2_to_bf16x2(x[i].x & 0xffffu), attn::e4m3x2_to_bf16x2(x[i].x >> 16),
+                             attn::e4m3x2_to_bf16x2(x[i].y & 0xffffu), attn::e4m3x2_to_bf16x2(x[i].y >> 16));
           }
           fence_async_smem();
           __syncwarp();
@@ -582,7 +583,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       };
 #pragma unroll 1
       for (int j = 0; j < T + NB - 1; ++j) {
-        if (j < T) put_scales(j);
+        if (own && j < T) put_scales(j);
         if (j >= NB - 1) convert(j - (NB - 1));
       }
       tj += T;
