@@ -382,12 +382,15 @@ __global__ void __launch_bounds__(kF32Threads, 1) paged_f32_kernel(const PagedPa
 // ------------------------------------------------------------------ joining
 // The items that cross runs, joined by their log-sum-exp.  An item's parts lie
 // in the slots 2c + 1, 2(c + 1), 2(c + 2), ... of the run c it starts in.  A CTA
-// takes units of eight warps' work from the list of all such items' entries:
-// an entry of few parts is one warp's, one of many parts that of up to eight,
-// which add up in shared memory in a fixed order.  (One CTA per entry of every
-// run, most of them without work, took 50 us of a 2,048-row call's 255.)
-constexpr int kJoinWarps = 8;
+// takes units of 16 warps' work from the list of all such items' entries and
+// blocks of 128 channels: one of few parts is one warp's, one of many parts that
+// of up to 16, which add up in shared memory in a fixed order.  The launch is a
+// chain of latencies, so a warp has up to eight parts in flight and 16 warps
+// cover the parts of a call of one sequence at once.  (One CTA per entry of
+// every run, most of them without work, took 50 us of a 2,048-row call's 255.)
+constexpr int kJoinWarps = 16;
 constexpr int kJoinThreads = 32 * kJoinWarps;
+constexpr int kJoinBatch = 8;   // parts whose loads are in flight together
 constexpr int kMaxRuns = 1024;
 
 // The larger one; NaN if either is.
@@ -397,131 +400,127 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-__device__ __forceinline__ int join_warps(int n_parts) { return n_parts >= 24 ? 8 : n_parts >= 12 ? 4 : n_parts >= 6 ? 2 : 1; }
+__device__ __forceinline__ int join_warps_log2(int n_parts) {
+  return n_parts > 64 ? 4 : n_parts > 32 ? 3 : n_parts > 16 ? 2 : n_parts > 8 ? 1 : 0;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedParams p, int n_runs) {
-  constexpr int CPL = D / 32;
-  __shared__ float acc_s[kJoinWarps][D];
-  __shared__ float m_s[kJoinWarps], w_s[kJoinWarps];
-  __shared__ int off_s[kMaxRuns + 1];
-  __shared__ int64_t scan_s[kJoinWarps];
+  constexpr int CB = D / 128;
+  __shared__ float4 acc_s[kJoinWarps][32];
+  __shared__ float m_s[kJoinWarps], l_s[kJoinWarps];
+  __shared__ int off_s[kMaxRuns + 1], sums_s[kJoinWarps], first_s;
   grid_dependency_sync();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int64_t units = 0;
+  int units = 0;   // (an item has at most 128 entries)
   for (int c0 = 0; c0 < n_runs; c0 += kJoinThreads) {
     int n = 0;
     if (c0 + tid < n_runs) {
-      const int4 d = *reinterpret_cast<const int4*>(p.parts + c0 + tid);   // n_parts, row0, f0, nf
-      if (d.x > 0) n = (d.w * join_warps(d.x) + kJoinWarps - 1) / kJoinWarps;
+      const int4 d = *reinterpret_cast<const int4*>(p.parts + c0 + tid);
+      if (d.x > 0) n = (((d.w & 255) * CB << join_warps_log2(d.x)) + kJoinWarps - 1) / kJoinWarps;
     }
-    int64_t total;
-    const int64_t before = units + cta_scan<kJoinThreads>(n, scan_s, total);
-    if (c0 + tid < n_runs) off_s[c0 + tid] = (int)before;
-    units += total;
+    int inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += up;
+    }
+    if (c0 > 0) __syncthreads();
+    if (lane == 31) sums_s[warp] = inc;
+    __syncthreads();
+    int before = units + inc - n;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      const int x = sums_s[w];
+      if (w < warp) before += x;
+      units += x;
+    }
+    if (c0 + tid < n_runs) off_s[c0 + tid] = before;
+    if ((int)blockIdx.x >= before && (int)blockIdx.x < before + n) first_s = c0 + tid;   // the run of this CTA's first unit
   }
-  if (tid == 0) off_s[n_runs] = (int)units;
+  if (tid == 0) off_s[n_runs] = units;
   __syncthreads();
-  for (int u = blockIdx.x; u < (int)units; u += gridDim.x) {
-    int cta = 0, hi = n_runs;   // off_s[cta] <= u < off_s[hi]
-    while (hi - cta > 1) {
-      const int mid = (cta + hi) / 2;
-      if (off_s[mid] <= u) cta = mid;
-      else hi = mid;
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    int cta = first_s;
+    if (u != (int)blockIdx.x) {
+      int hi = n_runs;   // off_s[cta] <= u < off_s[hi]
+      cta = 0;
+      while (hi - cta > 1) {
+        const int mid = (cta + hi) / 2;
+        if (off_s[mid] <= u) cta = mid;
+        else hi = mid;
+      }
     }
     const PagedPart d = p.parts[cta];
-    const int w = join_warps(d.n_parts), sub = warp & (w - 1);
-    const int f = (u - off_s[cta]) * (kJoinWarps / w) + warp / w;
-    float m = -INFINITY, l = 0.f, acc[CPL];
+    const int nf = d.nf_head & 255, lw = join_warps_log2(d.n_parts), w = 1 << lw, sub = warp & (w - 1);
+    const int k = ((u - off_s[cta]) * kJoinWarps + warp) >> lw, f = k / CB, at_c = k % CB * 32 + lane;
+    float m = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = sub; s0 < d.n_parts && f < nf; s0 += w * kJoinBatch) {
+      float ls[kJoinBatch];
+      float4 v[kJoinBatch];
 #pragma unroll
-    for (int i = 0; i < CPL; ++i) acc[i] = 0.f;
-    constexpr int kBatch = 4;   // parts whose loads are in flight together
-    for (int s0 = sub; s0 < d.n_parts && f < d.nf; s0 += w * kBatch) {
-      float ls[kBatch];
-      float4 v[kBatch][CPL / 4];
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int s = s0 + k * w;
+      for (int i = 0; i < kJoinBatch; ++i) {
+        const int s = s0 + i * w;
         const int64_t at = ((int64_t)2 * (cta + s) + (s == 0 ? 1 : 0)) * p.mt + f;
-        ls[k] = s < d.n_parts ? p.part_lse[at] : -INFINITY;
-#pragma unroll
-        for (int i = 0; i < CPL / 4; ++i)
-          v[k][i] = s < d.n_parts ? reinterpret_cast<const float4*>(p.part_o + at * D)[i * 32 + lane]
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+        ls[i] = s < d.n_parts ? p.part_lse[at] : -INFINITY;
+        v[i] = s < d.n_parts ? reinterpret_cast<const float4*>(p.part_o + at * D)[at_c] : make_float4(0.f, 0.f, 0.f, 0.f);
       }
       float mn = m;
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) mn = max_nan(mn, ls[k]);
-      if (mn == -INFINITY) continue;
-      const float a = exp2f(m - mn);
+      for (int i = 0; i < kJoinBatch; ++i) mn = max_nan(mn, ls[i]);
+      if (mn == -INFINITY) continue;   // (parts without a visible token are all zeros)
+      const float a = ex2(m - mn);
       l *= a;
+      acc = make_float4(acc.x * a, acc.y * a, acc.z * a, acc.w * a);
 #pragma unroll
-      for (int i = 0; i < CPL; ++i) acc[i] *= a;
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        if (ls[k] == -INFINITY) continue;
-        const float e = exp2f(ls[k] - mn);
+      for (int i = 0; i < kJoinBatch; ++i) {
+        const float e = ex2(ls[i] - mn);
         l += e;
-#pragma unroll
-        for (int i = 0; i < CPL / 4; ++i) {
-          acc[4 * i] = fmaf(e, v[k][i].x, acc[4 * i]);
-          acc[4 * i + 1] = fmaf(e, v[k][i].y, acc[4 * i + 1]);
-          acc[4 * i + 2] = fmaf(e, v[k][i].z, acc[4 * i + 2]);
-          acc[4 * i + 3] = fmaf(e, v[k][i].w, acc[4 * i + 3]);
-        }
+        acc = make_float4(fmaf(e, v[i].x, acc.x), fmaf(e, v[i].y, acc.y), fmaf(e, v[i].z, acc.z), fmaf(e, v[i].w, acc.w));
       }
       m = mn;
     }
     if (w > 1) {   // the other warps' sums, each against the largest maximum
       __syncthreads();
-#pragma unroll
-      for (int i = 0; i < CPL / 4; ++i)
-        reinterpret_cast<float4*>(acc_s[warp])[i * 32 + lane] =
-            make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+      acc_s[warp][lane] = acc;
       if (lane == 0) {
         m_s[warp] = m;
-        w_s[warp] = l;
+        l_s[warp] = l;
       }
       __syncthreads();
-      if (sub == 0) {
-        float M = m;
-        for (int k = 1; k < w; ++k) M = fmaxf(M, m_s[warp + k]);
-        const float own = m == -INFINITY ? 0.f : exp2f(m - M);
-        l *= own;
+      if (sub == 0 && f < nf) {
+        const float mi = lane < w ? m_s[warp + lane] : -INFINITY, li = lane < w ? l_s[warp + lane] : 0.f;
+        float M = mi;
 #pragma unroll
-        for (int i = 0; i < CPL; ++i) acc[i] *= own;
-        for (int k = 1; k < w; ++k) {
-          if (m_s[warp + k] == -INFINITY) continue;
-          const float e = exp2f(m_s[warp + k] - M);
-          l = fmaf(e, w_s[warp + k], l);
+        for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
+        const float e = mi == -INFINITY ? 0.f : ex2(mi - M);
+        l = e * li;
 #pragma unroll
-          for (int i = 0; i < CPL / 4; ++i) {
-            const float4 x = reinterpret_cast<const float4*>(acc_s[warp + k])[i * 32 + lane];
-            acc[4 * i] = fmaf(e, x.x, acc[4 * i]);
-            acc[4 * i + 1] = fmaf(e, x.y, acc[4 * i + 1]);
-            acc[4 * i + 2] = fmaf(e, x.z, acc[4 * i + 2]);
-            acc[4 * i + 3] = fmaf(e, x.w, acc[4 * i + 3]);
-          }
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int i = 0; i < w; ++i) {
+          const float ei = __shfl_sync(0xffffffffu, e, i);
+          const float4 x = acc_s[warp + i][lane];
+          acc = make_float4(fmaf(ei, x.x, acc.x), fmaf(ei, x.y, acc.y), fmaf(ei, x.z, acc.z), fmaf(ei, x.w, acc.w));
         }
         m = M;
       }
     }
-    if (sub != 0 || f >= d.nf) continue;
+    if (sub != 0 || f >= nf) continue;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const int r = row_of(p, d.f0 + f);
-    const int64_t at = (int64_t)(d.row0 + r) * p.n_q_heads + d.head * p.group + (d.f0 + f - r * p.group);
-#pragma unroll
-    for (int i = 0; i < CPL / 4; ++i) {
-      const float4 o = make_float4(acc[4 * i] * inv, acc[4 * i + 1] * inv, acc[4 * i + 2] * inv, acc[4 * i + 3] * inv);
-      if (p.out_dtype == QSA_F32) {
-        reinterpret_cast<float4*>(static_cast<float*>(p.out) + at * D)[i * 32 + lane] = o;
-      } else {
-        __nv_bfloat162* to = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + at * D) + (i * 32 + lane) * 2;
-        to[0] = __floats2bfloat162_rn(o.x, o.y);
-        to[1] = __floats2bfloat162_rn(o.z, o.w);
-      }
+    const int64_t at = (int64_t)(d.row0 + r) * p.n_q_heads + (d.nf_head >> 8) * p.group + (d.f0 + f - r * p.group);
+    const float4 o = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    if (p.out_dtype == QSA_F32) {
+      reinterpret_cast<float4*>(static_cast<float*>(p.out) + at * D)[at_c] = o;
+    } else {
+      __nv_bfloat162* to = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + at * D) + at_c * 2;
+      to[0] = __floats2bfloat162_rn(o.x, o.y);
+      to[1] = __floats2bfloat162_rn(o.z, o.w);
     }
-    if (lane == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    if (lane == 0 && k % CB == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
 }
 
@@ -543,7 +542,7 @@ cudaError_t launch_paged_f32(const PagedParams& p, int head_dim, int grid, cudaS
 cudaError_t launch_paged_merge(const PagedParams& p, int head_dim, int runs, cudaStream_t st) {
   if (runs < 2) return cudaSuccess;   // one run holds every item whole
   if (runs > kMaxRuns) return cudaErrorInvalidValue;
-  const dim3 grid((unsigned)(4 * device_sm_count())), block(kJoinThreads);
+  const dim3 grid((unsigned)(2 * device_sm_count())), block(kJoinThreads);
   return head_dim == 256 ? launch_kernel(paged_join_kernel<256>, grid, block, 0, st, 0u, p, runs)
                          : launch_kernel(paged_join_kernel<128>, grid, block, 0, st, 0u, p, runs);
 }

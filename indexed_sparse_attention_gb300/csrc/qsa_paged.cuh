@@ -57,9 +57,7 @@ struct alignas(16) PagedPart {
   int32_t n_parts;   // 0: no such item starts here
   int32_t row0;      // the sequence's first row
   int32_t f0;        // the item's first entry
-  int32_t nf;        // its entries
-  int32_t head;      // KV head
-  int32_t pad[3];
+  int32_t nf_head;   // its entries (at most 128), and 2^8 times the KV head
 };
 
 // Writing rows into their pages (qsa_paged_append.cu).
@@ -449,8 +447,7 @@ __device__ __forceinline__ void describe_part(const PagedParams& p, const Cursor
     d.n_parts = part_count(c, st.t0 + st.n - (c.x1 - c.x), st, cta);
     d.row0 = c.s.row0;
     d.f0 = c.m * p.mt;
-    d.nf = min(p.mt, c.s.n * p.group - d.f0);
-    d.head = c.head;
+    d.nf_head = min(p.mt, c.s.n * p.group - d.f0) | c.head << 8;
   }
   p.parts[cta] = d;
 }

@@ -707,12 +707,12 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       const int pos = ir.pos0 + row_of(p, ir.f0 + min(row, ir.nf - 1));
       const int low = p.window > 0 ? pos - p.window + 1 : 0;             // first token of the row's window
       const int dead = p.window > 0 ? ir.first - p.window : INT32_MIN;   // [n_sinks, dead]: no row's tokens
-      if constexpr (F8) {
-        wait(&h.q_full, (uint32_t)(it & 1), abrt);
-        zc = mine ? sc.q[it & 3][row] : 1.f;   // (four items: a group may be one behind the other, Q one ahead)
+      // (Not known before a tile's scales are, which follow Q's.  Four items: a group
+      // may be one behind the other, Q one ahead of both.)
+      auto factor = [&] {
+        zc = mine ? sc.q[it & 3][row] : 1.f;
         move = fminf(kMoveMax / zc, 1e30f);
-        ++it;
-      }
+      };
       float m = -INFINITY, l = 0.f;   // the maximum that this thread's sum l is relative to
       for (int j = (tj ^ group) & 1; j < T; j += 2) {
         const int g = tj + j, buf = g % NB, t0 = c.tiles.token(c.x + j);
@@ -743,7 +743,10 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
           }
         }
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        if constexpr (F8) wait(&h.sc_full[g & 7], (uint32_t)((g >> 3) & 1), abrt);
+        if constexpr (F8) {
+          wait(&h.sc_full[g & 7], (uint32_t)((g >> 3) & 1), abrt);
+          factor();
+        }
         const float* ks = F8 ? sc.k[g & 7] : nullptr;
         const float* vs = F8 ? sc.v[g & 7] : nullptr;
         auto take_max = [&](uint32_t(&x)[32], uint32_t col) {
@@ -870,6 +873,10 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       // The item's result, or this run's part of it: both groups' sums, relative
       // to the last maximum.
       named_sync(1, soft_threads);
+      if constexpr (F8) {   // (a group without a tile of the item)
+        factor();
+        ++it;
+      }
       const float m_last = h.m_run[row];
       if (m_last != m) l *= ex2((m - m_last) * zc);
       m = m_last;

@@ -105,6 +105,7 @@ def test_queries_that_are_no_numbers_stay_in_their_rows(dtype):
     for a, b in zip(good, bad):
         assert torch.equal(a.cpu()[rows], b.cpu()[rows])
     assert torch.isnan(bad[0][1, 3]).all() and torch.isnan(bad[0][2, 4]).all()
+    assert qsa.check_device_status() == (0, "")
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp8", "f32"])
@@ -154,6 +155,20 @@ def test_divisions_agree_and_repeat(dtype):
         for _ in range(5):
             again, lse2 = run(x, n_splits=n)
             assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8", "f32"])
+@pytest.mark.parametrize("D", [128, 256])
+def test_one_run_of_short_items(dtype, D):
+    # The roles of a run work on different items at once, one to three tiles each.
+    lens = [1 + (37 * i) % 390 for i in range(40)]
+    x = make_paged(lens, [1 + i % 3 if n > 3 else 1 for i, n in enumerate(lens)], dtype=dtype, D=D, page=32, seed=33)
+    for n in (1, 2, 5):
+        first = check(x, n_splits=n)
+        for _ in range(10):
+            again = run(x, n_splits=n)
+            assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    assert qsa.check_device_status() == (0, "")
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp8", "f32"])
