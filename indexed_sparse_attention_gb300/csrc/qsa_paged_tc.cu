@@ -53,7 +53,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kKT = 128;                      // keys of a tile
 constexpr int kHalf = kKT * 128;              // bytes of 64 channels of a tile
 constexpr int kSlab = 2 * kHalf;              // bytes of 128 channels: what the ring holds
-constexpr int kMaxSlabs = 6;                 // of K, and of V (bf16: 3, see Head::pv_done)
+constexpr int kMaxSlabs = 6;                 // of K, and of V
 constexpr int kKeyWarp = 8, kMmaWarp = 9, kValueWarp = 10, kQWarp = 11, kCodeWarp = 12, kCodeWarps = 4;
 constexpr int kSoftWarps = 8;
 __host__ __device__ constexpr int threads_of(bool f8) { return 32 * (f8 ? kCodeWarp + kCodeWarps : kQWarp + 1); }
@@ -94,11 +94,11 @@ __device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, int* abort) {
 // A wait by parity tells a phase from its neighbours only, so a waiting thread
 // has to know the phase before the awaited one to be over.  pv_done comes in a
 // pair, for even and odd tiles: tile j's logits follow the output product of
-// tile j - NB or later ones, NB <= 3, so whoever has seen them may wait for the
+// tile j - NB or later ones, NB = 2, so whoever has seen them may wait for the
 // product of tile j - 1, and after that for tile j's.
 struct Head {
   uint64_t full[2][kMaxSlabs], empty[2][kMaxSlabs];   // K, V
-  uint64_t s_full[3], p_full[2][3], pv_done[2], m_done[2], o_free, q_full, q_free, mma_done;
+  uint64_t s_full[2], p_full[2][2], pv_done[2], m_done[2], o_free, q_full, q_free, q_used, mma_done;
   uint64_t code_full[kMaxCodeSlabs], code_empty[kMaxCodeSlabs], sc_full[8];   // fp8 caches: V's codes, scales
   int64_t scan[16];
   Start start;
@@ -131,6 +131,19 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
       " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// As mma_bf16_ts, of 8-bit types.
+__device__ __forceinline__ void mma_f8_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// 32 bytes of each of 128 rows from shared memory to 8 TMEM columns; products
+// that the same thread issues later see them.
+__device__ __forceinline__ void tmem_cp_rows(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.128x256b [%0], %1;\n" ::"r"(taddr), "l"(desc) : "memory");
 }
 // Two values to E4M3, the first in the low byte, and back.
 __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
@@ -293,9 +306,14 @@ struct Ring {
 template <int D, bool F8>
 __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __grid_constant__ TcParams tp) {
   constexpr int NS = D / 128;            // slabs of a tile
-  constexpr int NB = D == 128 ? 3 : 2;   // buffers of logits in TMEM
+  constexpr int NB = 2;                  // buffers of logits in TMEM
   constexpr uint32_t kOCol = NB * kKT;   // O behind them
-  static_assert(kOCol + D <= kTmemCols, "TMEM columns");
+  // Behind O, for D = 128, Q: the product then reads only K from shared memory,
+  // whose 128 bytes a cycle K and Q together take all of (2,048 rows over 16k
+  // tokens: 319 -> 292 us).  For D = 256 TMEM is full.
+  constexpr bool QT = D == 128;
+  constexpr uint32_t kQCol = kOCol + D;
+  static_assert(kQCol + (QT ? 64 : 0) <= kTmemCols, "TMEM columns");
   const PagedParams& p = tp.p;
   extern __shared__ __align__(1024) uint8_t raw[];
   Head& h = *reinterpret_cast<Head*>(raw);
@@ -324,7 +342,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       bar_init(&h.code_empty[i], code_warps);
     }
     for (int i = 0; F8 && i < 8; ++i) bar_init(&h.sc_full[i], kCodeWarps);
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < 2; ++i) {
       bar_init(&h.s_full[i], 1);
       bar_init(&h.p_full[0][i], quarters);
       bar_init(&h.p_full[1][i], quarters);
@@ -336,6 +354,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
     bar_init(&h.o_free, 2 * quarters);
     bar_init(&h.q_full, F8 ? kCodeWarps : 1);
     bar_init(&h.q_free, 1);
+    bar_init(&h.q_used, 1);
     bar_init(&h.mma_done, 1);
     h.abort = 0;
     bar_init_fence();
@@ -631,22 +650,38 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
           if (leader && live) {
             const uint64_t k = k_desc + (uint32_t)(ka.slot * (kKeySlab >> 4)), q = q_desc + (F8 ? 1 : 2) * s * q_step;
 #pragma unroll
-            for (int x = 0; F8 && x < 8; ++x)   // both codes of Q's values
+            for (int x = 0; QT && x < 8; ++x) {
+              if constexpr (F8) mma_f8_ts(d, tmem + kQCol + 8u * x, k + 2 * (x & 3), kIdescS8, x != 0 ? 1u : 0u);
+              else
+                mma_bf16_ts(d, tmem + kQCol + 8u * x, k + (x >> 2) * (kHalf >> 4) + 2 * (x & 3), kIdescS, x != 0 ? 1u : 0u);
+            }
+#pragma unroll
+            for (int x = 0; !QT && F8 && x < 8; ++x)   // both codes of Q's values
               mma_f8(d, q + (x >> 2) * NS * q_step + 2 * (x & 3), k + 2 * (x & 3), kIdescS8, (s | x) != 0 ? 1u : 0u);
 #pragma unroll
-            for (int x = 0; !F8 && x < 8; ++x)
+            for (int x = 0; !QT && !F8 && x < 8; ++x)
               mma_bf16(d, q + (x >> 2) * q_step + 2 * (x & 3), k + (x >> 2) * (kHalf >> 4) + 2 * (x & 3), kIdescS,
                        (s | x) != 0 ? 1u : 0u);
             commit(&h.empty[0][ka.slot]);
             if (s == NS - 1) commit(&h.s_full[s_buf]);
-            if (s == NS - 1 && last) commit(&h.q_free);
+            if (s == NS - 1 && last) commit(QT ? &h.q_used : &h.q_free);
           }
           __syncwarp();
           ka.step(tp.n_k);
         }
         s_buf = s_buf + 1 == NB ? 0 : s_buf + 1;
       };
-      wait(&h.q_full, (uint32_t)(it & 1), abrt);
+      live = __all_sync(0xffffffffu, wait(&h.q_full, (uint32_t)(it & 1), abrt) && live);
+      if constexpr (QT) {   // the item before has had its logits
+        if (it > 0) live = __all_sync(0xffffffffu, wait(&h.q_used, (uint32_t)((it - 1) & 1), abrt) && live);
+        fence_after();
+        if (leader && live) {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) tmem_cp_rows(tmem + kQCol + 8u * x, q_desc + (x >> 2) * q_step + 2 * (x & 3));
+          commit(&h.q_free);
+        }
+        __syncwarp();
+      }
 #pragma unroll 1
       for (int j = 0; j < min(NB, T); ++j) logits(j == T - 1);
       // Then an output product and the logits NB tiles ahead of it, which take the
