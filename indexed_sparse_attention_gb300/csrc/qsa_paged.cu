@@ -385,12 +385,12 @@ __global__ void __launch_bounds__(kF32Threads, 1) paged_f32_kernel(const PagedPa
 // takes units of 16 warps' work from the list of all such items' entries and
 // blocks of 128 channels: one of few parts is one warp's, one of many parts that
 // of up to 16, which add up in shared memory in a fixed order.  The launch is a
-// chain of latencies, so a warp has up to eight parts in flight and 16 warps
+// chain of latencies, so a warp has up to six parts in flight and 16 warps
 // cover the parts of a call of one sequence at once.  (One CTA per entry of
 // every run, most of them without work, took 50 us of a 2,048-row call's 255.)
 constexpr int kJoinWarps = 16;
 constexpr int kJoinThreads = 32 * kJoinWarps;
-constexpr int kJoinBatch = 8;   // parts whose loads are in flight together
+constexpr int kJoinBatch = 6;   // parts whose loads are in flight together
 constexpr int kMaxRuns = 1024;
 
 // The larger one; NaN if either is.
@@ -403,8 +403,75 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 __device__ __forceinline__ int join_warps_log2(int n_parts) {
   return n_parts > 64 ? 4 : n_parts > 32 ? 3 : n_parts > 16 ? 2 : n_parts > 8 ? 1 : 0;
 }
+// Entries (and blocks) of an item of n_parts parts that a warp takes at a time.
+template <bool MANY>
+__device__ __forceinline__ int join_entries(int n_parts) {
+  return !MANY || n_parts > 4 ? 1 : n_parts > 2 ? 2 : 4;
+}
+template <bool MANY>
+__device__ __forceinline__ int join_units(int n_parts, int n) {   // of n entries and blocks
+  const int per = kJoinWarps * join_entries<MANY>(n_parts);
+  return ((n << join_warps_log2(n_parts)) + per - 1) / per;
+}
 
+// Writes four channels of a joined entry f of the item, by lane-wide position at_c.
 template <int D>
+__device__ __forceinline__ void join_write(const PagedParams& p, const PagedPart& d, int f, int at_c, bool first, float m,
+                                           float l, float4 acc) {
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int r = row_of(p, d.f0 + f);
+  const int64_t at = (int64_t)(d.row0 + r) * p.n_q_heads + (d.nf_head >> 8) * p.group + (d.f0 + f - r * p.group);
+  const float4 o = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  if (p.out_dtype == QSA_F32) {
+    reinterpret_cast<float4*>(static_cast<float*>(p.out) + at * D)[at_c] = o;
+  } else {
+    __nv_bfloat162* to = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + at * D) + at_c * 2;
+    to[0] = __floats2bfloat162_rn(o.x, o.y);
+    to[1] = __floats2bfloat162_rn(o.z, o.w);
+  }
+  if (first && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// E entries (and blocks) of at most P parts, from k0 on, by one warp: all their
+// loads are in flight together.  (One entry at a time, a call of 2,048 rows over
+// a window spent 14 us here, 8 dependent rounds a warp.)
+template <int D, int P, int E>
+__device__ __forceinline__ void join_few(const PagedParams& p, const PagedPart& d, int cta, int k0) {
+  constexpr int CB = D / 128;
+  const int lane = (int)threadIdx.x & 31, nf = d.nf_head & 255;
+  float ls[E * P];
+  float4 v[E * P];
+#pragma unroll
+  for (int i = 0; i < E * P; ++i) {
+    const int k = k0 + i / P, f = k / CB, s = i % P;
+    const bool there = f < nf && s < d.n_parts;
+    const int at = (2 * (cta + s) + (s == 0 ? 1 : 0)) * p.mt + f;   // (at most 2^18, the float4 below 2^24)
+    ls[i] = there ? p.part_lse[at] : -INFINITY;
+    v[i] = there ? reinterpret_cast<const float4*>(p.part_o)[at * (D / 4) + k % CB * 32 + lane]
+                 : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int k = k0 + e, f = k / CB;
+    if (f >= nf) break;
+    float m = ls[e * P];
+#pragma unroll
+    for (int s = 1; s < P; ++s) m = max_nan(m, ls[e * P + s]);
+    float l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int s = 0; s < P; ++s) {
+      const float w = ls[e * P + s] == -INFINITY ? 0.f : ex2(ls[e * P + s] - m);
+      const float4 x = v[e * P + s];
+      l += w;
+      acc = make_float4(fmaf(w, x.x, acc.x), fmaf(w, x.y, acc.y), fmaf(w, x.z, acc.z), fmaf(w, x.w, acc.w));
+    }
+    join_write<D>(p, d, f, k % CB * 32 + lane, lane == 0 && k % CB == 0, m, l, acc);
+  }
+}
+
+// MANY: calls whose items have many entries, of few parts each (chunks of rows).
+template <int D, bool MANY>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedParams p, int n_runs) {
   constexpr int CB = D / 128;
   __shared__ float4 acc_s[kJoinWarps][32];
@@ -417,7 +484,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
     int n = 0;
     if (c0 + tid < n_runs) {
       const int4 d = *reinterpret_cast<const int4*>(p.parts + c0 + tid);
-      if (d.x > 0) n = (((d.w & 255) * CB << join_warps_log2(d.x)) + kJoinWarps - 1) / kJoinWarps;
+      if (d.x > 0) n = join_units<MANY>(d.x, (d.w & 255) * CB);
     }
     int inc = n;
 #pragma unroll
@@ -453,6 +520,12 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
     }
     const PagedPart d = p.parts[cta];
     const int nf = d.nf_head & 255, lw = join_warps_log2(d.n_parts), w = 1 << lw, sub = warp & (w - 1);
+    if (MANY && d.n_parts <= 4) {
+      const int k0 = ((u - off_s[cta]) * kJoinWarps + warp) * join_entries<MANY>(d.n_parts);
+      if (d.n_parts <= 2) join_few<D, 2, 4>(p, d, cta, k0);
+      else join_few<D, 4, 2>(p, d, cta, k0);
+      continue;
+    }
     const int k = ((u - off_s[cta]) * kJoinWarps + warp) >> lw, f = k / CB, at_c = k % CB * 32 + lane;
     float m = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -462,9 +535,10 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
 #pragma unroll
       for (int i = 0; i < kJoinBatch; ++i) {
         const int s = s0 + i * w;
-        const int64_t at = ((int64_t)2 * (cta + s) + (s == 0 ? 1 : 0)) * p.mt + f;
+        const int at = (2 * (cta + s) + (s == 0 ? 1 : 0)) * p.mt + f;
         ls[i] = s < d.n_parts ? p.part_lse[at] : -INFINITY;
-        v[i] = s < d.n_parts ? reinterpret_cast<const float4*>(p.part_o + at * D)[at_c] : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[i] = s < d.n_parts ? reinterpret_cast<const float4*>(p.part_o)[at * (D / 4) + at_c]
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
       }
       float mn = m;
 #pragma unroll
@@ -491,36 +565,23 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
       __syncthreads();
       if (sub == 0 && f < nf) {
         const float mi = lane < w ? m_s[warp + lane] : -INFINITY, li = lane < w ? l_s[warp + lane] : 0.f;
-        float M = mi;
+        m = mi;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
-        const float e = mi == -INFINITY ? 0.f : ex2(mi - M);
+        for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float e = mi == -INFINITY ? 0.f : ex2(mi - m);
         l = e * li;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
         acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
+#pragma unroll 4
         for (int i = 0; i < w; ++i) {
           const float ei = __shfl_sync(0xffffffffu, e, i);
           const float4 x = acc_s[warp + i][lane];
           acc = make_float4(fmaf(ei, x.x, acc.x), fmaf(ei, x.y, acc.y), fmaf(ei, x.z, acc.z), fmaf(ei, x.w, acc.w));
         }
-        m = M;
       }
     }
-    if (sub != 0 || f >= nf) continue;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int r = row_of(p, d.f0 + f);
-    const int64_t at = (int64_t)(d.row0 + r) * p.n_q_heads + (d.nf_head >> 8) * p.group + (d.f0 + f - r * p.group);
-    const float4 o = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    if (p.out_dtype == QSA_F32) {
-      reinterpret_cast<float4*>(static_cast<float*>(p.out) + at * D)[at_c] = o;
-    } else {
-      __nv_bfloat162* to = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + at * D) + at_c * 2;
-      to[0] = __floats2bfloat162_rn(o.x, o.y);
-      to[1] = __floats2bfloat162_rn(o.z, o.w);
-    }
-    if (lane == 0 && k % CB == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    if (sub == 0 && f < nf) join_write<D>(p, d, f, at_c, lane == 0 && k % CB == 0, m, l, acc);
   }
 }
 
@@ -543,8 +604,11 @@ cudaError_t launch_paged_merge(const PagedParams& p, int head_dim, int runs, cud
   if (runs < 2) return cudaSuccess;   // one run holds every item whole
   if (runs > kMaxRuns) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)(2 * device_sm_count())), block(kJoinThreads);
-  return head_dim == 256 ? launch_kernel(paged_join_kernel<256>, grid, block, 0, st, 0u, p, runs)
-                         : launch_kernel(paged_join_kernel<128>, grid, block, 0, st, 0u, p, runs);
+  if (p.mt > 64)
+    return head_dim == 256 ? launch_kernel(paged_join_kernel<256, true>, grid, block, 0, st, 0u, p, runs)
+                           : launch_kernel(paged_join_kernel<128, true>, grid, block, 0, st, 0u, p, runs);
+  return head_dim == 256 ? launch_kernel(paged_join_kernel<256, false>, grid, block, 0, st, 0u, p, runs)
+                         : launch_kernel(paged_join_kernel<128, false>, grid, block, 0, st, 0u, p, runs);
 }
 
 int paged_f32_wait_timeouts() {

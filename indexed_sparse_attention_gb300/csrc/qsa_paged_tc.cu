@@ -98,6 +98,7 @@ __device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, int* abort) {
 // product of tile j - 1, and after that for tile j's.
 struct Head {
   uint64_t full[2][kMaxSlabs], empty[2][kMaxSlabs];   // K, V
+  uint64_t v_ready[kMaxSlabs];                        // bf16: V, without what no row sees
   uint64_t s_full[2], p_full[2][2], pv_done[2], m_done[2], o_free, q_full, q_free, q_used, mma_done;
   uint64_t code_full[kMaxCodeSlabs], code_empty[kMaxCodeSlabs], sc_full[8];   // fp8 caches: V's codes, scales
   int64_t scan[16];
@@ -337,6 +338,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
         bar_init(&h.empty[kv][i], 1);
       }
     }
+    for (int i = 0; i < kMaxSlabs; ++i) bar_init(&h.v_ready[i], 1);
     for (int i = 0; F8 && i < kMaxCodeSlabs; ++i) {
       bar_init(&h.code_full[i], 1);
       bar_init(&h.code_empty[i], code_warps);
@@ -608,22 +610,76 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       tj += T;
     }
   } else if (!F8 && warp == kQWarp) {
-    // ------------------------------------------------------------ Q
+    // ------------------------------------------------------------ Q, and V's ends
     // An item holds whole rows, so its entries are one box for each 64 channels.
+    // The next item's are copied before the last tile's V is waited for.
+    //
+    // V's slabs pass through this warp on their way to the product: slots of tokens
+    // that no row sees become zeros (P = 0 there, but 0 x NaN would reach O).  Boxes
+    // without a visible token hold zeros already, so at most two boxes' parts of a
+    // tile are left.  (Done by the softmax's warps before their weights, an item's
+    // first and last tiles waited for V as well as for the logits: 5,000 cycles.)
     const bool leader = elect_one();
     const int rows = p.mt / p.group;
-    int it = 0;
-    for (bool more = true; more; more = __shfl_sync(0xffffffffu, (int)c.next(p, p.mt), 0) != 0, ++it) {
-      if (!__all_sync(0xffffffffu, it == 0 || wait(&h.q_free, (uint32_t)((it - 1) & 1), abrt))) break;
+    const int box = min(1 << p.page_shift, kKT);
+    bool live = true;
+    auto load_q = [&](const Cursor<kKT>& i) {
       if (leader) {
         bar_expect_tx(&h.q_full, 2 * NS * p.mt * 128);
 #pragma unroll 1
         for (int s = 0; s < 2 * NS; ++s)
-          tma_3d(q_s + s * q_slab, &tp.q, 64 * s, c.head * p.group, c.s.row0 + c.m * rows, &h.q_full);
+          tma_3d(q_s + s * q_slab, &tp.q, 64 * s, i.head * p.group, i.s.row0 + i.m * rows, &h.q_full);
       }
       __syncwarp();
+    };
+    Cursor<kKT> ahead = c;
+    Ring va;
+    int it = 0, loads = 1;
+    load_q(ahead);
+    for (bool more = true; more && live; more = __shfl_sync(0xffffffffu, (int)c.next(p, p.mt), 0) != 0, ++it) {
+      const ItemRows ir = item_rows(p, c);
+      const int T = __shfl_sync(0xffffffffu, c.x1 - c.x, 0);
+#pragma unroll 1
+      for (int j = 0; j < T && live; ++j) {
+        if (j == T - 1 && __shfl_sync(0xffffffffu, (int)ahead.next(p, p.mt), 0) != 0) {
+          live = __all_sync(0xffffffffu, wait(&h.q_free, (uint32_t)(it & 1), abrt));
+          if (!live) break;
+          load_q(ahead);
+          ++loads;
+        }
+        // Tokens [0, cut) of the tile less [gap0, gap1) are seen by some row.
+        const int t0 = c.tiles.token(c.x + j);
+        auto slot_of = [&](int t) { return min(max(t - t0, 0), kKT); };
+        const int cut = slot_of(ir.last + 1), gap0 = p.window > 0 ? slot_of(p.n_sinks) : 0,
+                  gap1 = p.window > 0 ? slot_of(ir.first - p.window + 1) : 0;
+#pragma unroll 1
+        for (int s = 0; s < NS; ++s) {
+          live = __all_sync(0xffffffffu, wait(&h.full[1][va.slot], va.use & 1, abrt));
+          if (!live) break;
+          if (cut < kKT || gap0 < gap1) {
+            uint8_t* const slab = v_ring + va.slot * kSlab;
+            auto clear = [&](int from, int to) {
+#pragma unroll 1
+              for (int i = from * 8 + lane; i < to * 8; i += 32) {
+                reinterpret_cast<uint4*>(slab)[i] = make_uint4(0u, 0u, 0u, 0u);
+                reinterpret_cast<uint4*>(slab + kHalf)[i] = make_uint4(0u, 0u, 0u, 0u);
+              }
+            };
+            clear(cut, (cut + box - 1) & -box);
+            if (gap0 < gap1) {
+              const int up = min((gap0 + box - 1) & -box, gap1);
+              clear(gap0, up);
+              clear(max(gap1 & -box, up), gap1);
+            }
+            fence_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) bar_arrive(&h.v_ready[va.slot]);
+          va.step(tp.n_v);
+        }
+      }
     }
-    bar_wait(&h.q_full, (uint32_t)((it - 1) & 1), &g_timeouts);   // landed before the CTA ends
+    bar_wait(&h.q_full, (uint32_t)((loads - 1) & 1), &g_timeouts);   // landed before the CTA ends
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
     // The whole warp walks through the tiles with values that are the same in
@@ -700,7 +756,10 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
           va = first;
 #pragma unroll
           for (int s = 0; s < NS; ++s) {
-            if (part == 0) live = wait(&h.full[1][va.slot], va.use & 1, abrt) && live;
+            if (part == 0) {
+              if constexpr (!F8) live = wait(&h.v_ready[va.slot], va.use & 1, abrt) && live;
+              live = wait(&h.full[1][va.slot], va.use & 1, abrt) && live;
+            }
             live = __all_sync(0xffffffffu, live);
             fence_after();
             if (leader && live) {
@@ -740,8 +799,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       const int T = c.x1 - c.x;
       const bool mine = row < ir.nf;
       const int pos = ir.pos0 + row_of(p, ir.f0 + min(row, ir.nf - 1));
-      const int low = p.window > 0 ? pos - p.window + 1 : 0;             // first token of the row's window
-      const int dead = p.window > 0 ? ir.first - p.window : INT32_MIN;   // [n_sinks, dead]: no row's tokens
+      const int low = p.window > 0 ? pos - p.window + 1 : 0;   // first token of the row's window
       // (Not known before a tile's scales are, which follow Q's.  Four items: a group
       // may be one behind the other, Q one ahead of both.)
       auto factor = [&] {
@@ -838,26 +896,6 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
             for (int i = 0; i < 32; ++i) xb[i] = __float_as_uint(__uint_as_float(xb[i]) * alpha);
             tmem_st32(lanes + kOCol + (uint32_t)(32 * s), xb);
           }
-        }
-        // Tokens that no row sees: their V may be anything, and P = 0 there.
-        auto slot_of = [&](int t) { return min(max(t - t0, 0), kKT); };   // within the tile
-        const int cut = slot_of(ir.last + 1);                               // slots from here on,
-        const int gap0 = p.window > 0 ? slot_of(p.n_sinks) : 0, gap1 = p.window > 0 ? slot_of(dead + 1) : 0;
-        if (!F8 && (cut < kKT || gap0 < gap1)) {                                   // and [gap0, gap1)
-          const int v0 = g * NS;
-          for (int s = 0; s < NS; ++s) {
-            const int slot = (v0 + s) % tp.n_v;
-            wait(&h.full[1][slot], (uint32_t)(((v0 + s) / tp.n_v) & 1), abrt);
-#pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-              uint4* v = reinterpret_cast<uint4*>(v_ring + slot * kSlab + half * kHalf);
-#pragma unroll 1
-              for (int i = gap0 * 8 + row; i < gap1 * 8; i += 32 * quarters) v[i] = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll 1
-              for (int i = cut * 8 + row; i < kKT * 8; i += 32 * quarters) v[i] = make_uint4(0u, 0u, 0u, 0u);
-            }
-          }
-          fence_async_smem();
         }
         // Weights: in bf16 for the product, their sum in 32 bits.  32 logits
         // become 16 columns of weights, always behind the logits still to be read.
