@@ -269,38 +269,56 @@ __device__ __forceinline__ uint32_t warp_prefix(uint32_t v, int lane) {   // inc
   return v;
 }
 
-// find_run for at most 32 sequences: every warp finds the run by itself, one
-// sequence a lane (a sequence of several items: one item a lane), with one round
+// find_run for at most 64 sequences: every warp finds the run by itself, two
+// sequences a lane (a sequence of several items: one item a lane), with one round
 // of loads and no barrier.  False (for all warps) where the call is larger.
 template <int KT>
 __device__ __forceinline__ bool find_run_small(const PagedParams& p, int mt, int cta, int n_ctas, Start& st) {
-  if (p.n_seqs > 32) return false;
+  if (p.n_seqs > 64) return false;
   const int lane = threadIdx.x & 31;
-  SeqRows mine{0, 0, 0};
-  if (lane < p.n_seqs) mine = seq_rows(p, lane);
-  const int items = lane < p.n_seqs ? item_count(p, mine, mt) : 0;
-  auto of = [&](int i) {   // lane i's sequence
-    return SeqRows{__shfl_sync(0xffffffffu, mine.len, i), __shfl_sync(0xffffffffu, mine.row0, i),
-                   __shfl_sync(0xffffffffu, mine.n, i)};
+  const bool pairs = p.n_seqs > 32;   // lane's sequences: lane, or 2 lane and 2 lane + 1
+  const int i0 = pairs ? 2 * lane : lane, i1 = i0 + 1;
+  SeqRows mine[2] = {{0, 0, 0}, {0, 0, 0}};
+  if (i0 < p.n_seqs) mine[0] = seq_rows(p, i0);
+  if (pairs && i1 < p.n_seqs) mine[1] = seq_rows(p, i1);
+  auto of = [&](int i) {   // sequence i
+    const int k = pairs ? i & 1 : 0, from = pairs ? i >> 1 : i;
+    SeqRows a{__shfl_sync(0xffffffffu, mine[0].len, from), __shfl_sync(0xffffffffu, mine[0].row0, from),
+              __shfl_sync(0xffffffffu, mine[0].n, from)};
+    const SeqRows b{__shfl_sync(0xffffffffu, mine[1].len, from), __shfl_sync(0xffffffffu, mine[1].row0, from),
+                    __shfl_sync(0xffffffffu, mine[1].n, from)};
+    return k ? b : a;
   };
-  uint32_t cost = items == 1 ? item_cost<KT>(p, mt, mine, 1, 0) : 0u;
-  bool large = items > 4096 || cost > (1u << 20);
+  uint32_t cost[2];
+  uint32_t several[2];   // sequences of more than one item
+  bool large = false;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int n = item_count(p, mine[k], mt);
+    cost[k] = n == 1 ? item_cost<KT>(p, mt, mine[k], 1, 0) : 0u;
+    large |= n > 4096 || cost[k] > (1u << 20);
+    several[k] = __ballot_sync(0xffffffffu, n > 1 && !large);
+  }
 #pragma unroll 1
-  for (uint32_t rest = __ballot_sync(0xffffffffu, items > 1 && !large); rest; rest &= rest - 1) {
-    const int i = __ffs(rest) - 1, n = __shfl_sync(0xffffffffu, items, i);
-    const SeqRows s = of(i);
+  while (several[0] | several[1]) {
+    const int k = several[0] ? 0 : 1, from = __ffs(k == 0 ? several[0] : several[1]) - 1;
+    if (k == 0) several[0] &= several[0] - 1;
+    else several[1] &= several[1] - 1;
+    const SeqRows s = of(pairs ? 2 * from + k : from);
+    const int n = item_count(p, s, mt);
     uint32_t sum = 0;
 #pragma unroll 1
     for (int m = lane; m < n; m += 32) sum += min(item_cost<KT>(p, mt, s, n, m), 1u << 13);   // (an item past it: large)
     sum = __reduce_add_sync(0xffffffffu, sum);
-    if (lane == i) {
-      cost = sum;
+    if (lane == from) {
+      if (k == 0) cost[0] = sum;
+      else cost[1] = sum;
       large |= sum > (1u << 20) || item_cost<KT>(p, mt, s, n, n - 1) >= (1u << 13);
     }
   }
   if (__any_sync(0xffffffffu, large)) return false;
-  const uint32_t inc = warp_prefix(cost, lane);
-  const uint32_t all = __shfl_sync(0xffffffffu, inc, 31);   // at most 2^25
+  const uint32_t inc = warp_prefix(cost[0] + cost[1], lane);
+  const uint32_t all = __shfl_sync(0xffffffffu, inc, 31);   // at most 2^26
   const uint32_t ctas = min((uint32_t)n_ctas, all);
   st = Start{0, 0, (int64_t)all, (int32_t)ctas, 0, 0, 0, 0, {0, 0, 0}};
   if ((uint32_t)cta >= ctas) return true;
@@ -312,10 +330,14 @@ __device__ __forceinline__ bool find_run_small(const PagedParams& p, int mt, int
     t0 = (uint32_t)((uint64_t)all * cta / ctas);
     t1 = (uint32_t)((uint64_t)all * (cta + 1) / ctas);
   }
-  const int i = __ffs(__ballot_sync(0xffffffffu, inc > t0)) - 1;   // the first sequence that ends behind t0
-  const int n = __shfl_sync(0xffffffffu, items, i);
+  const int from = __ffs(__ballot_sync(0xffffffffu, inc > t0)) - 1;   // the first lane whose sequences end behind t0
+  uint32_t r = t0 - __shfl_sync(0xffffffffu, inc - cost[0] - cost[1], from);
+  const uint32_t first = __shfl_sync(0xffffffffu, cost[0], from);
+  const bool second = r >= first;
+  if (second) r -= first;
+  const int i = pairs ? 2 * from + (second ? 1 : 0) : from;
   const SeqRows s = of(i);
-  uint32_t r = t0 - __shfl_sync(0xffffffffu, inc - cost, i);
+  const int n = item_count(p, s, mt);
   int m = 0;
   uint32_t c = 0;
 #pragma unroll 1

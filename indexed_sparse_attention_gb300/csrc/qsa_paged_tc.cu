@@ -195,6 +195,10 @@ __device__ __forceinline__ void st_global32(void* to, const uint32_t* x) {
     static_cast<uint4*>(to)[1] = make_uint4(x[4], x[5], x[6], x[7]);
   }
 }
+// Fetches a tensor map ahead of its first copy.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
@@ -362,6 +366,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
     bar_init_fence();
   }
   if (warp == kMmaWarp) tmem_alloc(&h.tmem, kTmemCols);
+  if (warp == kQWarp && lane < (F8 ? 2 : 3)) prefetch_map(lane == 0 ? &tp.k : lane == 1 ? &tp.v : &tp.q);
   fence_before();
   __syncthreads();
   fence_after();
@@ -690,6 +695,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
     const uint64_t q_desc = desc_sw128(q_s, 16, 1024), k_desc = desc_sw128(k_ring, 16, 1024),
                    v_desc = desc_sw128(v_ring, kHalf, 1024);
     const uint32_t q_step = (uint32_t)q_slab >> 4;
+    uint64_t* const v_full = F8 ? h.full[1] : h.v_ready;   // (who passes bf16's V on has waited for the copies)
     Ring ka, va;
     int it = 0;
     int s_buf = 0, p_buf = 0, odd = 0;   // buffers of the next logits and the next weights; parity of the next output
@@ -756,10 +762,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
           va = first;
 #pragma unroll
           for (int s = 0; s < NS; ++s) {
-            if (part == 0) {
-              if constexpr (!F8) live = wait(&h.v_ready[va.slot], va.use & 1, abrt) && live;
-              live = wait(&h.full[1][va.slot], va.use & 1, abrt) && live;
-            }
+            if (part == 0) live = wait(v_full + va.slot, va.use & 1, abrt) && live;
             live = __all_sync(0xffffffffu, live);
             fence_after();
             if (leader && live) {
