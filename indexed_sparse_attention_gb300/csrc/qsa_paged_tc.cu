@@ -401,25 +401,28 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
     for (bool more = true; more && live; more = __shfl_sync(0xffffffffu, (int)c.next(p, p.mt), 0) != 0) {
       const ItemRows ir = item_rows(p, c);
       const int T = __shfl_sync(0xffffffffu, c.x1 - c.x, 0);
-      // The page of the lane's box of a tile; n_pages: nothing to read, -1: no page.
+      auto wanted = [&](int j) {   // whether the lane's box of a tile holds a visible token
+        const int t = c.tiles.token(c.x + j) + my_box * box, end = min(t + box - 1, ir.last);
+        return lane < n_copies && t <= ir.last && (p.window == 0 || end > ir.first - p.window || t < p.n_sinks);
+      };
+      // The table's entry for it, not looked at before the tile's turn: that would
+      // wait for the load.
       auto look_up = [&](int j) {
-        const int t = c.tiles.token(c.x + j) + my_box * box;
-        const int end = min(t + box - 1, ir.last);
-        const bool wanted = lane < n_copies && t <= ir.last && (p.window == 0 || end > ir.first - p.window || t < p.n_sinks);
-        const int64_t slot = (int64_t)t >> p.page_shift;
-        const int32_t page = wanted && slot < p.table_ld ? __ldcg(p.table + c.seq * p.table_ld + slot) : -1;
-        return !wanted ? p.n_pages : (uint32_t)page < (uint32_t)p.n_pages ? page : -1;
+        const int64_t slot = (int64_t)(c.tiles.token(c.x + j) + my_box * box) >> p.page_shift;
+        int32_t page = -1;
+        if (wanted(j) && slot < p.table_ld) page = __ldcg(p.table + c.seq * p.table_ld + slot);
+        return page;
       };
       // Pages are looked up two tiles ahead.
       int page = look_up(0), next = T > 1 ? look_up(1) : 0;
 #pragma unroll 1
       for (int j = 0; j < T && live; ++j) {
         const int ahead = j + 2 < T ? look_up(j + 2) : 0;
-        if (__any_sync(0xffffffffu, page < 0)) {   // copies of missing pages go past the last one
-          const bool missing = page < 0;
+        const bool want = wanted(j), missing = want && (uint32_t)page >= (uint32_t)p.n_pages;
+        if (!want || missing) page = p.n_pages;   // copies of nothing go past the last page
+        if (__any_sync(0xffffffffu, missing)) {
           const uint32_t bad =
               __reduce_or_sync(0xffffffffu, missing ? ((1u << (box / 16)) - 1u) << (my_box * (box / 16)) : 0u);
-          if (missing) page = p.n_pages;
           if (missing && kv == 0 && half == 0) atomicAdd(&g_bad_pages, 1);
           if (leader && kv == 0) h.bad[(tj + j) & 15] = bad;   // 16-token pieces of the tile
         } else if (leader && kv == 0) {
@@ -467,16 +470,20 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       auto visible = [&](int t) {
         return t <= ir.last && (p.window == 0 || t > ir.first - p.window || t < p.n_sinks);
       };
-      auto look_up = [&](int j) {   // the page of the thread's token of tile j, -1: none
+      auto look_up = [&](int j) {   // the table's entry for the thread's token of tile j (not looked at), -1: none
         const int t = c.tiles.token(c.x + j) + ct;
+        const int64_t slot = (int64_t)t >> p.page_shift;
         int32_t page = -1;
-        return own && j < T && visible(t) && page_of(p, c.seq, t, page) ? page : -1;
+        if (own && j < T && visible(t) && slot < p.table_ld) page = __ldcg(p.table + c.seq * p.table_ld + slot);
+        return page;
       };
       auto load = [&](int j, int page) {
         const int slot = (c.tiles.token(c.x + j) + ct) & ((1 << p.page_shift) - 1);
-        return page < 0 ? 0x00003c00u   // K scale 1, V scale 0
-                        : __ldg(reinterpret_cast<const uint32_t*>(
-                              p.kv_scale + 4 * (page * p.s_page_stride + c.head * p.s_head_stride + slot * p.s_tok_stride)));
+        uint32_t record = 0x00003c00u;   // K scale 1, V scale 0
+        if ((uint32_t)page < (uint32_t)p.n_pages)
+          record = __ldg(reinterpret_cast<const uint32_t*>(
+              p.kv_scale + 4 * (page * p.s_page_stride + c.head * p.s_head_stride + slot * p.s_tok_stride)));
+        return record;
       };
       int page = look_up(0);
       // Q as E4M3: with the row's largest magnitude brought to [2^7, 2^8) by a power
