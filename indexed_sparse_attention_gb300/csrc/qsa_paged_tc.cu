@@ -376,6 +376,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
   const Start st = find_run<threads_of(F8), kKT>(p, p.mt, blockIdx.x, gridDim.x, h.scan, &h.start);
   Cursor<kKT> c;
   c.begin(p, p.mt, st);
+  if (tid == 0) h.start = st;   // for the end (this thread's): registers are short
 
   if (st.n == 0) {
     if (tid == 0) p.parts[blockIdx.x] = PagedPart{};
@@ -856,11 +857,12 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
           if constexpr (F8) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(ks + col + i);
-              x[i] = __float_as_uint(__uint_as_float(x[i]) * f.x);
-              x[i + 1] = __float_as_uint(__uint_as_float(x[i + 1]) * f.y);
-              x[i + 2] = __float_as_uint(__uint_as_float(x[i + 2]) * f.z);
-              x[i + 3] = __float_as_uint(__uint_as_float(x[i + 3]) * f.w);
+              const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(ks + col + i);
+              float a[4];
+              unpack2(mul2(pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), f.x), a[0], a[1]);
+              unpack2(mul2(pack2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), f.y), a[2], a[3]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[i + e] = __float_as_uint(a[e]);
             }
           }
 #pragma unroll
@@ -915,11 +917,18 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
         uint64_t sum2[2] = {0ull, 0ull};
         auto weigh = [&](uint32_t(&x)[32], uint32_t col) {
           uint32_t w[16];
+          [[maybe_unused]] ulonglong2 kk = {0ull, 0ull}, vv = {0ull, 0ull};   // scales of four keys
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             float a, b;
             uint64_t z = pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-            if constexpr (F8) z = mul2(z, *reinterpret_cast<const uint64_t*>(ks + col + 2 * i));
+            if constexpr (F8) {
+              if (!(i & 1)) {
+                kk = *reinterpret_cast<const ulonglong2*>(ks + col + 2 * i);
+                vv = *reinterpret_cast<const ulonglong2*>(vs + col + 2 * i);
+              }
+              z = mul2(z, i & 1 ? kk.y : kk.x);
+            }
             z = fma2(z, zc2, shift2);
             unpack2(z, a, b);
             a = ex2(a);
@@ -927,7 +936,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
             uint64_t e = pack2(a, b);
             sum2[i & 1] = add2(sum2[i & 1], e);
             if constexpr (F8) {   // V's scale goes with the weight, which is rounded once
-              e = mul2(e, *reinterpret_cast<const uint64_t*>(vs + col + 2 * i));
+              e = mul2(e, i & 1 ? vv.y : vv.x);
               unpack2(e, a, b);
             }
             w[i] = pack_bf16(a, b);
@@ -1007,9 +1016,8 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
         if (!whole) p.part_lse[part] = lse2;
         else if (p.lse) p.lse[entry] = lse2 * kLn2;
       }
-      const Cursor<kKT> last = c;
       more = c.next(p, p.mt);
-      if (!more && warp == 0 && lane == 0) describe_part(p, last, st, blockIdx.x);
+      if (!more && tid == 0) describe_part(p, c, h.start, blockIdx.x);   // (still at its last item)
     }
   }
   __syncwarp();
