@@ -12,8 +12,8 @@
 //
 // Division.  The key tiles of all items, one after the other in the order
 // (sequence, tile, KV head, key tile), are cut into one contiguous run of
-// nearly equal length per CTA, whatever the lengths of the sequences: CTA c of
-// C takes tiles [c N / C, (c + 1) N / C).  An item inside one run is written
+// nearly equal length per CTA, whatever the lengths of the sequences: of N tiles,
+// each of C CTAs takes N / C and the first N mod C one more.  An item inside one run is written
 // to the output at once; the parts of an item that crosses runs go to the
 // workspace (at most two per CTA: the item its run starts inside, and the item
 // its run ends inside) and are joined by their log-sum-exp in a second launch.
@@ -174,7 +174,17 @@ __device__ __forceinline__ Tiles<KT> item_tiles(const PagedParams& p, const SeqR
   return t;
 }
 __device__ __forceinline__ int item_count(const PagedParams& p, const SeqRows& s, int mt) {
-  return (s.n * p.group + mt - 1) / mt;
+  const int f = s.n * p.group;
+  if (f <= mt) return f > 0 ? 1 : 0;   // (no division where the call is short)
+  return (f + mt - 1) / mt;
+}
+
+// a / b for a below 2^22, b above 0.
+__device__ __forceinline__ uint32_t divide_small(uint32_t a, uint32_t b) {
+  uint32_t q = (uint32_t)((float)a * __frcp_rn((float)b));   // off by one at most
+  if (q * b > a) --q;
+  else if ((q + 1) * b <= a) ++q;
+  return q;
 }
 
 // Where a CTA's run starts: key tile x of item (seq, m, head); tile t0 of the
@@ -289,11 +299,12 @@ __device__ __forceinline__ bool find_run_small(const PagedParams& p, int mt, int
                     __shfl_sync(0xffffffffu, mine[1].n, from)};
     return k ? b : a;
   };
-  uint32_t cost[2];
-  uint32_t several[2];   // sequences of more than one item
+  uint32_t cost[2] = {0u, 0u};
+  uint32_t several[2] = {0u, 0u};   // sequences of more than one item
   bool large = false;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
+    if (k == 1 && !pairs) break;
     const int n = item_count(p, mine[k], mt);
     cost[k] = n == 1 ? item_cost<KT>(p, mt, mine[k], 1, 0) : 0u;
     large |= n > 4096 || cost[k] > (1u << 20);
@@ -322,14 +333,8 @@ __device__ __forceinline__ bool find_run_small(const PagedParams& p, int mt, int
   const uint32_t ctas = min((uint32_t)n_ctas, all);
   st = Start{0, 0, (int64_t)all, (int32_t)ctas, 0, 0, 0, 0, {0, 0, 0}};
   if ((uint32_t)cta >= ctas) return true;
-  uint32_t t0, t1;
-  if (all < (1u << 22)) {   // (at most 1,024 CTAs)
-    t0 = all * (uint32_t)cta / ctas;
-    t1 = all * ((uint32_t)cta + 1) / ctas;
-  } else {
-    t0 = (uint32_t)((uint64_t)all * cta / ctas);
-    t1 = (uint32_t)((uint64_t)all * (cta + 1) / ctas);
-  }
+  const uint32_t base = all == ctas ? 1u : all < (1u << 22) ? divide_small(all, ctas) : all / ctas, rem = all - base * ctas;
+  const uint32_t t0 = base * (uint32_t)cta + min((uint32_t)cta, rem), tiles = base + ((uint32_t)cta < rem ? 1u : 0u);
   const int from = __ffs(__ballot_sync(0xffffffffu, inc > t0)) - 1;   // the first lane whose sequences end behind t0
   uint32_t r = t0 - __shfl_sync(0xffffffffu, inc - cost[0] - cost[1], from);
   const uint32_t first = __shfl_sync(0xffffffffu, cost[0], from);
@@ -339,30 +344,34 @@ __device__ __forceinline__ bool find_run_small(const PagedParams& p, int mt, int
   const SeqRows s = of(i);
   const int n = item_count(p, s, mt);
   int m = 0;
-  uint32_t c = 0;
 #pragma unroll 1
-  for (int m0 = 0;; m0 += 32) {   // the first item that ends behind the rest
-    c = item_cost<KT>(p, mt, s, n, m0 + lane);
+  for (int m0 = 0; n > 1; m0 += 32) {   // the first item that ends behind the rest
+    const uint32_t c = item_cost<KT>(p, mt, s, n, m0 + lane);
     const uint32_t end = warp_prefix(c, lane);
     const uint32_t hit = __ballot_sync(0xffffffffu, end > r);
     if (hit || m0 + 32 >= n) {
       const int k = __ffs(hit) - 1;
       m = m0 + k;
       r -= __shfl_sync(0xffffffffu, end - c, k);
-      c = __shfl_sync(0xffffffffu, c, k);
       break;
     }
     r -= __shfl_sync(0xffffffffu, end, 31);
   }
-  const uint32_t count = c / (uint32_t)p.n_kv_heads;
-  st.n = t1 - t0;
+  const uint32_t count = (uint32_t)item_tiles<KT>(p, s, mt, m).count;
+  st.n = tiles;
   st.t0 = t0;
   st.seq = i;
   st.m = m;
-  st.head = (int32_t)(r / count);
+  st.head = (int32_t)(r < (1u << 22) ? divide_small(r, count) : r / count);
   st.x = (int32_t)(r - (uint32_t)st.head * count);
   st.s = s;
   return true;
+}
+
+// The first tile of CTA `cta`.
+__device__ __forceinline__ int64_t run_start(int64_t all, int ctas, int cta) {
+  const int64_t base = all / ctas;
+  return base * cta + min((int64_t)cta, all - base * ctas);
 }
 
 // The run of CTA `cta` of at most `n_ctas` (all THREADS threads call; the
@@ -380,7 +389,7 @@ __device__ Start find_run(const PagedParams& p, int mt, int cta, int n_ctas, int
     all += total;
   }
   const int ctas = (int)min((int64_t)n_ctas, all);   // every run holds a tile
-  const int64_t t0 = cta < ctas ? all * cta / ctas : 0, t1 = cta < ctas ? all * (cta + 1) / ctas : 0;
+  const int64_t t0 = cta < ctas ? run_start(all, ctas, cta) : 0, t1 = cta < ctas ? run_start(all, ctas, cta + 1) : 0;
   if (threadIdx.x == 0) *out_s = Start{0, 0, all, ctas, 0, 0, 0, 0, {0, 0, 0}};
   __syncthreads();
   if (t1 <= t0) return *out_s;
@@ -454,9 +463,16 @@ struct Cursor {
 template <int KT>
 __device__ __forceinline__ int part_count(const Cursor<KT>& c, int64_t t_item, const Start& st, int cta) {
   const int64_t last = t_item + c.tiles.count - 1;
-  int64_t e = last * st.ctas / st.all;   // its last tile's CTA, up to rounding
-  while (e + 1 < st.ctas && st.all * (e + 1) / st.ctas <= last) ++e;
-  while (e > cta && st.all * e / st.ctas > last) --e;
+  // Runs of base + 1 tiles, then of base.
+  int64_t e;
+  if (st.all < INT32_MAX) {
+    const uint32_t all = (uint32_t)st.all, b = all / (uint32_t)st.ctas, rem = all - b * (uint32_t)st.ctas, l = (uint32_t)last;
+    e = l < rem * (b + 1) ? l / (b + 1) : rem + (l - rem * (b + 1)) / b;
+  } else {
+    const int64_t base = st.all / st.ctas;
+    const int64_t rem = st.all - base * st.ctas;
+    e = last < rem * (base + 1) ? last / (base + 1) : rem + (last - rem * (base + 1)) / base;
+  }
   return (int)(e - cta) + 1;
 }
 
