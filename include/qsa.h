@@ -579,7 +579,8 @@ typedef struct qsa_paged_cache {
 typedef struct qsa_paged_batch {
   const int32_t* table;        /* device [n_seqs, table_ld] page numbers */
   int64_t table_ld;            /* entries of a table row; tokens past them have no page */
-  const int32_t* lens;         /* device [n_seqs] tokens of each sequence */
+  const int32_t* lens;         /* device [n_seqs] tokens of each sequence (attention takes
+                                * more than 2^31 - 2^25 as that many) */
   const int32_t* row_start;    /* device [n_seqs + 1], ascending */
   int32_t n_seqs;
   int32_t n_rows;              /* rows of q and out (or of k_new and v_new) */

@@ -123,6 +123,9 @@ int paged_f32_wait_timeouts();
 
 namespace paged {
 
+// Lengths above this are taken as this: positions and tiles then keep to 32 bits.
+constexpr int32_t kMaxLen = INT32_MAX - (1 << 25);
+
 // One sequence's rows and tokens, as the device arrays give them.
 struct SeqRows {
   int32_t len, row0, n;
@@ -132,7 +135,7 @@ __device__ __forceinline__ SeqRows seq_rows(const PagedParams& p, int i) {
   const int32_t a = __ldcg(p.row_start + i), b = __ldcg(p.row_start + i + 1);
   s.row0 = max(a, 0);
   s.n = max(min(b, p.n_rows) - s.row0, 0);   // rows past q's end are not there
-  s.len = max(__ldcg(p.lens + i), 0);
+  s.len = min(max(__ldcg(p.lens + i), 0), kMaxLen);
   return s;
 }
 
@@ -260,15 +263,17 @@ __device__ __forceinline__ void place_in_seq(const PagedParams& p, int mt, int i
   }
   st.seq = i;
   st.m = m;
-  st.head = (int32_t)r / t.count;   // (below a tile count times the heads: 32 bits)
-  st.x = (int32_t)r - st.head * t.count;
+  st.head = (int32_t)(r / t.count);
+  st.x = (int32_t)(r - (int64_t)st.head * t.count);
   st.s = s;
 }
 
-// Key tiles of item m of a sequence, all KV heads; 0 behind its last item.
+// Key tiles of item m of a sequence, all KV heads (2^21 if they are more); 0
+// behind its last item.
 template <int KT>
 __device__ __forceinline__ uint32_t item_cost(const PagedParams& p, int mt, const SeqRows& s, int items, int m) {
-  return m < items ? (uint32_t)item_tiles<KT>(p, s, mt, m).count * (uint32_t)p.n_kv_heads : 0u;
+  const uint64_t all = (uint64_t)(uint32_t)item_tiles<KT>(p, s, mt, m).count * (uint32_t)p.n_kv_heads;
+  return m < items ? (uint32_t)min(all, (uint64_t)1 << 21) : 0u;
 }
 __device__ __forceinline__ uint32_t warp_prefix(uint32_t v, int lane) {   // inclusive
 #pragma unroll
@@ -319,12 +324,16 @@ __device__ __forceinline__ bool find_run_small(const PagedParams& p, int mt, int
     const int n = item_count(p, s, mt);
     uint32_t sum = 0;
 #pragma unroll 1
-    for (int m = lane; m < n; m += 32) sum += min(item_cost<KT>(p, mt, s, n, m), 1u << 13);   // (an item past it: large)
+    for (int m = lane; m < n; m += 32) {   // (at most 4,096 items of at most 2^13 tiles: 32 bits)
+      const uint32_t c = item_cost<KT>(p, mt, s, n, m);
+      large |= c > (1u << 13);
+      sum += min(c, 1u << 13);
+    }
     sum = __reduce_add_sync(0xffffffffu, sum);
     if (lane == from) {
       if (k == 0) cost[0] = sum;
       else cost[1] = sum;
-      large |= sum > (1u << 20) || item_cost<KT>(p, mt, s, n, n - 1) >= (1u << 13);
+      large |= sum > (1u << 20);
     }
   }
   if (__any_sync(0xffffffffu, large)) return false;

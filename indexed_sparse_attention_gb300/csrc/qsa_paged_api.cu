@@ -21,6 +21,7 @@ int log2_of(int64_t x) {
 // A cache's shape and addresses for head_dim and dtype of cfg.
 qsa_status check_cache(const qsa_paged_cache* c, const qsa_attn_config* cfg, const char* fn) {
   if (!c) return fail(QSA_ERR_INVALID_ARG, "%s: null cache", fn);
+  if (cfg->n_kv_heads >= 1 << 16) return fail(QSA_ERR_UNSUPPORTED, "%s: %d KV heads", fn, cfg->n_kv_heads);
   if (!c->k || !c->v) return fail(QSA_ERR_INVALID_ARG, "%s: cache has a null K/V", fn);
   if (cfg->kv_dtype == QSA_Q8_0) return fail(QSA_ERR_UNSUPPORTED, "%s: Q8_0 caches are not paged", fn);
   if (c->n_pages < 1) return fail(QSA_ERR_INVALID_ARG, "%s: n_pages=%d", fn, c->n_pages);
@@ -148,7 +149,7 @@ QSA_API qsa_status qsa_paged_attn(const qsa_paged_cache* cache, const qsa_paged_
   p.group = cfg->n_q_heads / cfg->n_kv_heads;
   p.group_magic = p.group == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32) + p.group - 1) / p.group);
   p.scale = cfg->scale > 0.f ? cfg->scale : 1.0f / sqrtf((float)cfg->head_dim);
-  p.window = window;
+  p.window = window < paged::kMaxLen ? window : 0;   // no sequence is longer
   p.n_sinks = n_sinks;
   p.q = q;
   p.out = out;

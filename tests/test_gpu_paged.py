@@ -235,6 +235,61 @@ def test_pages_past_32_bits():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp8", "f32"])
+def test_lengths_and_windows_at_the_ends_of_32_bits(dtype):
+    # A length behind every table: only the first tokens have pages, and the window's are skipped.
+    x = make_paged([40, 40], [3, 2], dtype=dtype, D=128, seed=41)
+    cache, batch, q = x.device()
+    out, lse = torch.full(q.shape, 7.0, device=dev()), torch.full(q.shape[:2], 7.0, device=dev())
+    batch.lens[0] = 2 ** 31 - 1
+    qsa.paged_attn(cache, batch, q, out, lse, window=64, n_sinks=40)
+    torch.cuda.synchronize()
+    assert qsa.check_device_status()[0] == qsa.ERR_DEVICE_CHECK
+    seen = Paged(x.k, x.v, x.scale, x.table, [40], [3], x.row_start[:2], x.q[:3], x.page, x.order)
+    K, V = (t.float() for t in seen.seq_kv(0))
+    G = x.q.shape[1] // K.shape[0]
+    z = torch.einsum("rhgd,htd->rhgt", x.q[:3].float().view(3, -1, G, 128), K) * 128 ** -0.5
+    want = torch.einsum("rhgt,htd->rhgd", z.softmax(-1), V).reshape(3, -1, 128)
+    # Weights rounded to bf16 (2^-8 of the largest value), the rest in 32 bits.
+    assert (out[:3].cpu() - want).abs().max() < ((0 if dtype == "f32" else 2.0 ** -8) + 1e-4) * V.abs().max()
+    # Windows longer than any sequence, rows before the first token among the others.
+    x = make_paged([3, 50], [3, 2], dtype=dtype, D=128, seed=42)
+    a, b = run(x), run(x, window=2 ** 31 - 1, sinks=2 ** 31 - 1)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    cache, batch, q = x.device()
+    batch.lens[0] = 1                                          # rows at positions -2, -1 and 0
+    for window in (0, 2 ** 31 - 1, 2 ** 31 - 2 ** 26):
+        qsa.paged_attn(cache, batch, q, out[:5], lse[:5], window=window)
+        torch.cuda.synchronize()
+        assert (out[:2] == 0).all() and torch.isinf(lse[:2]).all() and torch.isfinite(lse[2:5]).all()
+    assert qsa.check_device_status() == (0, "")
+
+
+def test_windows_whose_items_differ_by_a_tile():
+    # Items of 2,731 and 2,730 tiles of 32 tokens by three heads: 8,193 and 8,190.
+    Hkv, D, P, W = 3, 128, 1024, 2730 * 32 - 20
+    fits = [n for n in range(W + 200, W + 232)
+            if (-(-(n - 8) // 32) - (n - 40 - W + 1) // 32, -(-n // 32) - (n - 8 - W + 1) // 32) == (2731, 2730)]
+    n = fits[0]
+    pages = -(-n // P)
+    g = torch.Generator(device="cuda").manual_seed(43)
+    k, v = (torch.randn(pages, Hkv, P, D, device=dev(), generator=g) for _ in range(2))
+    q = torch.randn(40, Hkv, D, device=dev(), generator=g)
+    table = torch.arange(pages, dtype=torch.int32, device=dev())[None].contiguous()
+    batch = qsa.PagedBatch(table, _ints([n]), _ints([0, 40]), n_rows=40)
+    out, lse = torch.empty_like(q), torch.empty(40, Hkv, device=dev())
+    qsa.paged_attn(qsa.PagedCache(k, v), batch, q, out, lse, window=W)
+    K, V = (t.transpose(0, 1).reshape(Hkv, -1, D)[:, :n].double() for t in (k, v))
+    z = torch.einsum("rhd,htd->rht", q.double(), K) * D ** -0.5
+    pos, t = torch.arange(n - 40, n, device=dev())[:, None], torch.arange(n, device=dev())[None]
+    z.masked_fill_(~((t <= pos) & (t > pos - W))[:, None], float("-inf"))
+    want = torch.einsum("rht,htd->rhd", z.softmax(-1), V)
+    # 87,000 nearly equal weights: sums within n u of |V|'s mean, here 2 (n + 40) 2^-24 0.8.
+    assert (out.double() - want).abs().max() < 2 * (W + 40) * 2.0 ** -24
+    assert (lse.double() - torch.logsumexp(z, -1)).abs().max() < (W + 40) * 2.0 ** -24 + 2e-4
+    assert qsa.check_device_status() == (0, "")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8", "f32"])
 def test_missing_pages_are_skipped_and_reported(dtype):
     x = make_paged([200, 90], [2, 3], dtype=dtype, D=128, page=16, seed=11, poison=True)
     y = make_paged([200, 90], [2, 3], dtype=dtype, D=128, page=16, seed=11, poison=True)
