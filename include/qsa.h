@@ -599,8 +599,9 @@ typedef struct qsa_paged_batch {
  * A row that sees no token (a negative position, or none of its pages in the
  * table) gets out = 0 and lse = -inf.  Tokens that no row of the call sees are
  * not part of any sum, whatever their pages hold (NaN and infinities too);
- * pages that hold no visible token are not read.  A V value that some row sees
- * must be finite for the sums of that sequence's other rows of the call to be.
+ * pages that hold no visible token are not read.  A V value (or an fp8 scale)
+ * that some row sees must be finite for the sums of that sequence's other rows
+ * of the call to be.
  * Table entries outside [0, n_pages) under visible tokens: those tokens are
  * skipped and qsa_check_device_status reports them.
  *   cache, batch   host structs

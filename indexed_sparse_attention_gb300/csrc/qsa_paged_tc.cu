@@ -135,7 +135,7 @@ struct Scales {
   float v[8][kKT];
   float q[4][128];   // of an item's rows of Q: the power of two that its codes were divided by
 };
-static_assert(sizeof(Head) <= kHeadBytes, "shared memory head");
+static_assert(sizeof(Head) <= kHeadBytes && (kHeadBytes + sizeof(Scales)) % 1024 == 0, "shared memory head");
 
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
