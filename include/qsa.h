@@ -620,7 +620,9 @@ typedef struct qsa_paged_batch {
  *                  must not run concurrently (captured calls neither)
  * Sums and softmax statistics are 32-bit; bf16 and fp8 caches: the weights
  * exp(z - m) are rounded to bf16 for the product with V (at most 2^-8 of each,
- * independently), out once to out_dtype.  The result depends on the
+ * independently), out once to out_dtype.  fp8: q enters as the sum of two E4M3
+ * codes a value, exact from 2^-9 of its row's largest magnitude on and off by at
+ * most 2^-17 of that below.  The result depends on the
  * lengths and the number of runs, not on timing: it is reproducible.
  * Errors: QSA_ERR_INVALID_ARG, QSA_ERR_UNSUPPORTED, QSA_ERR_MISALIGNED,
  * QSA_ERR_WORKSPACE, QSA_ERR_CUDA.  n_rows == 0 or n_seqs == 0 is a no-op.
