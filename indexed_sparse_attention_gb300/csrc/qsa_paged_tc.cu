@@ -134,6 +134,7 @@ struct Scales {
   float k[8][kKT];   // times the logit scale and log2(e)
   float v[8][kKT];
   float q[4][128];   // of an item's rows of Q: the power of two that its codes were divided by
+  float mx[2][2][128];   // maxima of an even and an odd tile, by group
 };
 static_assert(sizeof(Head) <= kHeadBytes && (kHeadBytes + sizeof(Scales)) % 1024 == 0, "shared memory head");
 
@@ -838,160 +839,229 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
         move = fminf(kMoveMax / zc, 1e30f);
       };
       float m = -INFINITY, l = 0.f;   // the maximum that this thread's sum l is relative to
-      for (int j = (tj ^ group) & 1; j < T; j += 2) {
-        const int g = tj + j, buf = g % NB, t0 = c.tiles.token(c.x + j);
-        const uint32_t s_col = lanes + (uint32_t)(buf * kKT);
-        wait(&h.s_full[buf], (uint32_t)((g / NB) & 1), abrt);
-        __syncwarp();
-        fence_after();
-        const uint32_t bad = h.bad[g & 15];
-        const bool partly = bad != 0 || t0 + kKT - 1 > ir.first ||
-                            (p.window > 0 && t0 <= ir.last - p.window && t0 + kKT > p.n_sinks);
-        uint32_t xa[32], xb[32];
-        // What a row does not see becomes -infinity, in TMEM: the passes below
-        // stay short (with the masks unrolled into them they no longer fit the
-        // instruction cache and take four times as long).
-        if (partly) {
+      // What a row does not see of keys [from, to) of a tile becomes -infinity, in
+      // TMEM: the passes below stay short (with the masks unrolled into them they no
+      // longer fit the instruction cache and take four times as long).
+      auto hide = [&](int t0, uint32_t bad, uint32_t s_col, int from, int to, uint32_t(&x)[32]) {
+        if (bad == 0 && t0 + kKT - 1 <= ir.first &&
+            !(p.window > 0 && t0 <= ir.last - p.window && t0 + kKT > p.n_sinks))
+          return;
 #pragma unroll 1
-          for (int col = 0; col < kKT; col += 32) {
-            // Keys t .. t + 31: seen are those up to pos, from low on or among the first n_sinks.
-            const int t = t0 + col;
-            uint32_t see = below(pos + 1 - t) & (~below(low - t) | below(p.n_sinks - t));
-            see &= ~((((bad >> (col / 16)) & 1u) * 0xffffu) | (((bad >> (col / 16 + 1)) & 1u) * 0xffff0000u));
-            if (__all_sync(0xffffffffu, see == 0xffffffffu)) continue;
-            tmem_ld32_start(s_col + (uint32_t)col, xa);
-            tmem_ld_wait(xa);
+        for (int col = from; col < to; col += 32) {
+          // Keys t .. t + 31: seen are those up to pos, from low on or among the first n_sinks.
+          const int t = t0 + col;
+          uint32_t see = below(pos + 1 - t) & (~below(low - t) | below(p.n_sinks - t));
+          see &= ~((((bad >> (col / 16)) & 1u) * 0xffffu) | (((bad >> (col / 16 + 1)) & 1u) * 0xffff0000u));
+          if (__all_sync(0xffffffffu, see == 0xffffffffu)) continue;
+          tmem_ld32_start(s_col + (uint32_t)col, x);
+          tmem_ld_wait(x);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) xa[i] = see & (1u << i) ? xa[i] : 0xff800000u;
-            tmem_st32(s_col + (uint32_t)col, xa);
-          }
+          for (int i = 0; i < 32; ++i) x[i] = see & (1u << i) ? x[i] : 0xff800000u;
+          tmem_st32(s_col + (uint32_t)col, x);
         }
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        if constexpr (F8) {
+      };
+      if constexpr (F8) {
+        // Both groups take every tile, 64 keys each, and exchange their maxima: the
+        // scales make this the longest step of a tile's chain, and half the keys a
+        // thread (which then stay in registers) nearly halve it.
+        const int pair = 2 + (warp & 3), c0 = 64 * group;   // the barrier of the two warps of the same entries
+#pragma unroll 1
+        for (int j = 0; j < T; ++j) {
+          const int g = tj + j, buf = g % NB, t0 = c.tiles.token(c.x + j);
+          const uint32_t s_col = lanes + (uint32_t)(buf * kKT);
+          wait(&h.s_full[buf], (uint32_t)((g / NB) & 1), abrt);
+          __syncwarp();
+          fence_after();
+          uint32_t xa[32], xb[32];
+          hide(t0, h.bad[g & 15], s_col, c0, c0 + 64, xa);
           wait(&h.sc_full[g & 7], (uint32_t)((g >> 3) & 1), abrt);
           factor();
-        }
-        const float* ks = F8 ? sc.k[g & 7] : nullptr;
-        const float* vs = F8 ? sc.v[g & 7] : nullptr;
-        auto take_max = [&](uint32_t(&x)[32], uint32_t col) {
-          if constexpr (F8) {
+          tmem_ld32_start(s_col + (uint32_t)c0, xa);
+          tmem_ld_wait(xa);
+          tmem_ld32_start(s_col + (uint32_t)c0 + 32, xb);
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          auto take_max = [&](uint32_t(&x)[32], const float* ks) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-              const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(ks + col + i);
+              const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(ks + i);
               float a[4];
               unpack2(mul2(pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), f.x), a[0], a[1]);
               unpack2(mul2(pack2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), f.y), a[2], a[3]);
+              m4[(i >> 2) & 3] = fmaxf(fmaxf(m4[(i >> 2) & 3], fmaxf(a[0], a[1])), fmaxf(a[2], a[3]));
 #pragma unroll
               for (int e = 0; e < 4; ++e) x[i + e] = __float_as_uint(a[e]);
             }
-          }
-#pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            m4[(i >> 1) & 3] = fmaxf(fmaxf(m4[(i >> 1) & 3], __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
-        };
-        tmem_ld32_start(s_col, xa);
-        tmem_ld_wait(xa);
-#pragma unroll 1
-        for (uint32_t col = 0; col < kKT; col += 64) {
-          tmem_ld32_start(s_col + col + 32, xb);
-          take_max(xa, col);
+          };
+          take_max(xa, sc.k[g & 7] + c0);
           tmem_ld_wait(xb);
-          tmem_ld32_start(s_col + ((col + 64) & (kKT - 1)), xa);   // at the end the first ones again, for the weights
-          take_max(xb, col + 32);
-          tmem_ld_wait(xa);
-        }
-        // Lanes without an entry hold whatever their rows of Q gave; nothing reads
-        // their weights, and they must not move a maximum.
-        const float mx = mine ? fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) : -INFINITY;
-        // The running maximum after the tile before this one, then after this one.
-        if (g > 0) wait(&h.m_done[group ^ 1], (uint32_t)(((g - 1) >> 1) & 1), abrt);
-        const float before = j == 0 ? -INFINITY : h.m_run[row];
-        const bool moves = j == 0 ? mx != -INFINITY : mx > before + move;
-        const float now = moves ? mx : before;
-        h.m_run[row] = now;
-        __syncwarp();
-        if (lane == 0) bar_arrive(&h.m_done[group]);
-        if (now != m) {
-          l *= ex2((m - now) * zc);
-          m = now;
-        }
-        if (j > 0 && __any_sync(0xffffffffu, moves)) {
-          const float alpha = moves ? ex2((before - now) * zc) : 1.f;
-          wait(&h.pv_done[(g - 1) & 1], (uint32_t)(((g - 1) >> 1) & 1), abrt);
-          __syncwarp();
+          take_max(xb, sc.k[g & 7] + c0 + 32);
+          float mx = mine ? fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) : -INFINITY;
+          // (Also: both groups have read their logits, over which the weights go.)
+          sc.mx[g & 1][group][row] = mx;
+          fence_before();
+          named_sync(pair, 64);
           fence_after();
+          mx = fmaxf(mx, sc.mx[g & 1][group ^ 1][row]);
+          const bool moves = j == 0 ? mx != -INFINITY : mx > m + move;
+          if (__any_sync(0xffffffffu, moves)) {   // (the same in both warps)
+            const float alpha = moves ? ex2((m - mx) * zc) : 1.f;
+            if (moves) {
+              l *= alpha;
+              m = mx;
+            }
+            if (j > 0) {
+              wait(&h.pv_done[(g - 1) & 1], (uint32_t)(((g - 1) >> 1) & 1), abrt);
+              __syncwarp();
+              fence_after();
 #pragma unroll 1
-          for (int s = 0; s < D / 32; ++s) {
-            tmem_ld32_start(lanes + kOCol + (uint32_t)(32 * s), xb);
-            tmem_ld_wait(xb);
+              for (int s = 0; s < D / 64; ++s) {   // the group's half of the channels
+                uint32_t o[32];
+                const uint32_t at = lanes + kOCol + (uint32_t)(group * (D / 2) + 32 * s);
+                tmem_ld32_start(at, o);
+                tmem_ld_wait(o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) xb[i] = __float_as_uint(__uint_as_float(xb[i]) * alpha);
-            tmem_st32(lanes + kOCol + (uint32_t)(32 * s), xb);
-          }
-        }
-        // Weights: in bf16 for the product, their sum in 32 bits.  32 logits
-        // become 16 columns of weights, always behind the logits still to be read.
-        const float shift = m == -INFINITY ? 0.f : -m * zc;
-        const uint64_t zc2 = pack2(zc, zc);
-        const uint64_t shift2 = pack2(shift, shift);
-        uint64_t sum2[2] = {0ull, 0ull};
-        auto weigh = [&](uint32_t(&x)[32], uint32_t col) {
-          uint32_t w[16];
-          [[maybe_unused]] ulonglong2 kk = {0ull, 0ull}, vv = {0ull, 0ull};   // scales of four keys
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float a, b;
-            uint64_t z = pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-            if constexpr (F8) {
-              if (!(i & 1)) {
-                kk = *reinterpret_cast<const ulonglong2*>(ks + col + 2 * i);
-                vv = *reinterpret_cast<const ulonglong2*>(vs + col + 2 * i);
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                tmem_st32(at, o);
               }
-              z = mul2(z, i & 1 ? kk.y : kk.x);
+              fence_before();
+              named_sync(pair, 64);   // either half of the weights lets the product begin
             }
-            z = fma2(z, zc2, shift2);
-            unpack2(z, a, b);
-            a = ex2(a);
-            b = ex2(b);
-            uint64_t e = pack2(a, b);
-            sum2[i & 1] = add2(sum2[i & 1], e);
-            if constexpr (F8) {   // V's scale goes with the weight, which is rounded once
-              e = mul2(e, i & 1 ? vv.y : vv.x);
-              unpack2(e, a, b);
-            }
-            w[i] = pack_bf16(a, b);
           }
-          tmem_st16(s_col + col / 2, w);
-        };
-        __syncwarp();
-#pragma unroll 1
-        for (uint32_t col = 0; col < kKT; col += 64) {
-          tmem_ld32_start(s_col + col + 32, xb);
-          weigh(xa, col);
-          tmem_ld_wait(xb);
-          if (col == 0) tmem_ld32_start(s_col + 64, xa);
-          weigh(xb, col + 32);
+          const float shift = m == -INFINITY ? 0.f : -m * zc;
+          const uint64_t zc2 = pack2(zc, zc), shift2 = pack2(shift, shift);
+          uint64_t sum2[2] = {0ull, 0ull};
+          auto weigh = [&](uint32_t(&x)[32], const float* vs, uint32_t to) {
+            uint32_t w[16];
+            ulonglong2 vv = {0ull, 0ull};
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float a, b;
+              if (!(i & 1)) vv = *reinterpret_cast<const ulonglong2*>(vs + 2 * i);
+              unpack2(fma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), zc2, shift2), a, b);
+              const uint64_t e = pack2(ex2(a), ex2(b));
+              sum2[i & 1] = add2(sum2[i & 1], e);
+              unpack2(mul2(e, i & 1 ? vv.y : vv.x), a, b);   // V's scale goes with the weight, which is rounded once
+              w[i] = pack_bf16(a, b);
+            }
+            tmem_st16(to, w);
+          };
+          __syncwarp();
+          weigh(xa, sc.v[g & 7] + c0, s_col + (uint32_t)(c0 / 2));
+          weigh(xb, sc.v[g & 7] + c0 + 32, s_col + (uint32_t)(c0 / 2 + 16));
           tmem_st_wait();
           fence_before();
           __syncwarp();
-          if (lane == 0) bar_arrive(&h.p_full[col / 64][buf]);
-          if (col == 0) tmem_ld_wait(xa);
+          if (lane == 0) bar_arrive(&h.p_full[group][buf]);
+          float s0, s1;
+          unpack2(add2(sum2[0], sum2[1]), s0, s1);
+          l += s0 + s1;
         }
-        float s0, s1;
-        unpack2(add2(sum2[0], sum2[1]), s0, s1);
-        l += s0 + s1;
+      } else {
+        for (int j = (tj ^ group) & 1; j < T; j += 2) {
+          const int g = tj + j, buf = g % NB, t0 = c.tiles.token(c.x + j);
+          const uint32_t s_col = lanes + (uint32_t)(buf * kKT);
+          wait(&h.s_full[buf], (uint32_t)((g / NB) & 1), abrt);
+          __syncwarp();
+          fence_after();
+          uint32_t xa[32], xb[32];
+          hide(t0, h.bad[g & 15], s_col, 0, kKT, xa);
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          auto take_max = [&](uint32_t(&x)[32]) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+              m4[(i >> 1) & 3] = fmaxf(fmaxf(m4[(i >> 1) & 3], __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
+          };
+          tmem_ld32_start(s_col, xa);
+          tmem_ld_wait(xa);
+#pragma unroll 1
+          for (uint32_t col = 0; col < kKT; col += 64) {
+            tmem_ld32_start(s_col + col + 32, xb);
+            take_max(xa);
+            tmem_ld_wait(xb);
+            tmem_ld32_start(s_col + ((col + 64) & (kKT - 1)), xa);   // at the end the first ones again, for the weights
+            take_max(xb);
+            tmem_ld_wait(xa);
+          }
+          // Lanes without an entry hold whatever their rows of Q gave; nothing reads
+          // their weights, and they must not move a maximum.
+          const float mx = mine ? fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) : -INFINITY;
+          // The running maximum after the tile before this one, then after this one.
+          if (g > 0) wait(&h.m_done[group ^ 1], (uint32_t)(((g - 1) >> 1) & 1), abrt);
+          const float before = j == 0 ? -INFINITY : h.m_run[row];
+          const bool moves = j == 0 ? mx != -INFINITY : mx > before + move;
+          const float now = moves ? mx : before;
+          h.m_run[row] = now;
+          __syncwarp();
+          if (lane == 0) bar_arrive(&h.m_done[group]);
+          if (now != m) {
+            l *= ex2((m - now) * zc);
+            m = now;
+          }
+          if (j > 0 && __any_sync(0xffffffffu, moves)) {
+            const float alpha = moves ? ex2((before - now) * zc) : 1.f;
+            wait(&h.pv_done[(g - 1) & 1], (uint32_t)(((g - 1) >> 1) & 1), abrt);
+            __syncwarp();
+            fence_after();
+#pragma unroll 1
+            for (int s = 0; s < D / 32; ++s) {
+              tmem_ld32_start(lanes + kOCol + (uint32_t)(32 * s), xb);
+              tmem_ld_wait(xb);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) xb[i] = __float_as_uint(__uint_as_float(xb[i]) * alpha);
+              tmem_st32(lanes + kOCol + (uint32_t)(32 * s), xb);
+            }
+          }
+          // Weights: in bf16 for the product, their sum in 32 bits.  32 logits
+          // become 16 columns of weights, always behind the logits still to be read.
+          const float shift = m == -INFINITY ? 0.f : -m * zc;
+          const uint64_t zc2 = pack2(zc, zc);
+          const uint64_t shift2 = pack2(shift, shift);
+          uint64_t sum2[2] = {0ull, 0ull};
+          auto weigh = [&](uint32_t(&x)[32], uint32_t col) {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float a, b;
+              uint64_t z = pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+              z = fma2(z, zc2, shift2);
+              unpack2(z, a, b);
+              a = ex2(a);
+              b = ex2(b);
+              sum2[i & 1] = add2(sum2[i & 1], pack2(a, b));
+              w[i] = pack_bf16(a, b);
+            }
+            tmem_st16(s_col + col / 2, w);
+          };
+          __syncwarp();
+#pragma unroll 1
+          for (uint32_t col = 0; col < kKT; col += 64) {
+            tmem_ld32_start(s_col + col + 32, xb);
+            weigh(xa, col);
+            tmem_ld_wait(xb);
+            if (col == 0) tmem_ld32_start(s_col + 64, xa);
+            weigh(xb, col + 32);
+            tmem_st_wait();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&h.p_full[col / 64][buf]);
+            if (col == 0) tmem_ld_wait(xa);
+          }
+          float s0, s1;
+          unpack2(add2(sum2[0], sum2[1]), s0, s1);
+          l += s0 + s1;
+        }
       }
       tj += T;
       // The item's result, or this run's part of it: both groups' sums, relative
       // to the last maximum.
       named_sync(1, soft_threads);
-      if constexpr (F8) {   // (a group without a tile of the item)
-        factor();
+      if constexpr (F8) {
         ++it;
+      } else {
+        const float m_last = h.m_run[row];
+        if (m_last != m) l *= ex2((m - m_last) * zc);
+        m = m_last;
       }
-      const float m_last = h.m_run[row];
-      if (m_last != m) l *= ex2((m - m_last) * zc);
-      m = m_last;
       h.sums[group][row] = l;
       named_sync(1, soft_threads);
       l += h.sums[group ^ 1][row];
