@@ -11,9 +11,13 @@
 //   P_j = exp(S_j - m), rounded to bf16, over S_j's own columns in TMEM;
 //   O  += P_j V_j     M = 128, N = 128 channels a slab, K = 128 keys, P from TMEM and
 //                     V from shared memory (MN-major), O in 128 or 256 TMEM columns.
-// Two groups of four softmax warps take the tiles in turn; a thread owns one
-// entry, so row statistics need no shuffles, and the groups hand the running
-// maximum over.  The maximum m is only moved, and O rescaled, when a logit exceeds
+// Two groups of four softmax warps take 64 keys each of every tile; a thread owns
+// one entry, so row statistics need one exchange with the thread of the other
+// group and no shuffles, and its 64 logits stay in registers.  (Tiles of 128 keys
+// in turn between the groups: the chain logits - weights - output of a tile, which
+// two tiles in flight have to cover, was 3,300 cycles for head_dim 128; 2,048 rows
+// over 16k tokens 303 against 295 us, the ragged fp8 batch 181 against 172.)
+// The maximum m is only moved, and O rescaled, when a logit exceeds
 // it by more than 2^8 in the weight: weights stay below 2^8, which the 32-bit sums
 // and bf16's exponent hold as well as 1, and the quotient by l is the same.
 //
@@ -31,7 +35,7 @@
 // product), and K's scales times the logit scale are applied to S by column; V's
 // codes become bf16 in shared memory, and V's scales go with the weights, which
 // are rounded once.  (K through bf16 as well: 351 us on a ragged batch of 16
-// sequences where this takes 179.)
+// sequences where this takes 174.)
 //
 // Roles: warps 0-7 softmax and output, warps 8 and 10 copy K and V, warp 9 issues
 // the MMAs; bf16: warp 11 copies Q and clears V's ends; fp8: warps 12-15 write Q's
@@ -43,11 +47,11 @@
 // 1,941 TFLOP/s): few rows, the K/V bytes -- 261,120 tokens x 4 rows 89 of 79; the
 // call's start and the joining launch are what a 65,536-token row (32 of 20) and a
 // windowed batch of 64 (49 of 33) add.  2,048 rows: over 16k tokens (head_dim 128)
-// 303 of 199, the chain logits -> weights -> output, at the power limit; over a
-// 4,096-token window (256) 174 of 108, the shared memory's 128 bytes a cycle, which
+// 295 of 199, the tensor pipe 65% busy at the power limit; over a
+// 4,096-token window (256) 173 of 108, the shared memory's 128 bytes a cycle, which
 // Q and K take whole in the logits' product (2,700 cycles a tile where the products
-// alone take 2,048).  fp8: 179 of 115, V's way through the registers and the shared
-// memory (158 without it).
+// alone take 2,048).  fp8: 174 of 115, shared memory again, which V's codes cross three
+// times more than bf16 values do.
 #include <math.h>
 
 #include <cuda_fp16.h>
@@ -118,23 +122,22 @@ __device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, int* abort) {
 struct Head {
   uint64_t full[2][kMaxSlabs], empty[2][kMaxSlabs];   // K, V
   uint64_t v_ready[kMaxSlabs];                        // bf16: V, without what no row sees
-  uint64_t s_full[2], p_full[2][2], pv_done[2], m_done[2], o_free, q_full, q_free, q_used, mma_done;
+  uint64_t s_full[2], p_full[2][2], pv_done[2], o_free, q_full, q_free, q_used, mma_done;
   uint64_t code_full[kMaxCodeSlabs], code_empty[kMaxCodeSlabs], sc_full[8];   // fp8 caches: V's codes, scales
   int64_t scan[16];
   Start start;
   uint32_t tmem;
   int abort;
   uint32_t bad[16];             // 16-token pieces of a tile that have no page (fewer are under way)
-  float m_run[128];             // the entries' running maxima
+  float mx[2][2][128];          // maxima of an even and an odd tile, by group
   float sums[2][128];           // the two groups' sums of weights
 };
-constexpr int kHeadBytes = 3 * 1024;
+constexpr int kHeadBytes = 4 * 1024;
 // fp8 caches: scales of the tiles in flight, behind the head.
 struct Scales {
   float k[8][kKT];   // times the logit scale and log2(e)
   float v[8][kKT];
   float q[4][128];   // of an item's rows of Q: the power of two that its codes were divided by
-  float mx[2][2][128];   // maxima of an even and an odd tile, by group
 };
 static_assert(sizeof(Head) <= kHeadBytes && (kHeadBytes + sizeof(Scales)) % 1024 == 0, "shared memory head");
 
@@ -376,7 +379,6 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(&h.pv_done[i], 1);
-      bar_init(&h.m_done[i], quarters);
     }
     bar_init(&h.o_free, 2 * quarters);
     bar_init(&h.q_full, F8 ? kCodeWarps : 1);
@@ -779,8 +781,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       // buffer that its weights leave.
 #pragma unroll 1
       for (int j = 0; j < T; ++j) {
-        // The weights come in two halves of 64 keys, the first while the second is
-        // still being computed.
+        // The weights come in two halves of 64 keys, one from each group.
         const uint32_t phase = (p_phase >> p_buf) & 1;
         p_phase ^= 1u << p_buf;
         const Ring first = va;
@@ -817,8 +818,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
     bar_wait(&h.mma_done, 0u, &g_timeouts);
   } else if (warp < kSoftWarps && (warp & 3) < quarters) {
     // ------------------------------------------------------------ softmax and output
-    // Two groups of four warps take the tiles in turn: one group's exponentials
-    // run beside the other's maxima.  A thread owns one entry.
+    // A thread owns one entry, and the keys [64 group, 64 group + 64) of each tile.
     const int group = warp >> 2, row = 32 * (warp & 3) + lane;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     // Logits to base 2; the scales of an fp8 cache's keys hold the factor already,
@@ -860,208 +860,111 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
           tmem_st32(s_col + (uint32_t)col, x);
         }
       };
-      if constexpr (F8) {
-        // Both groups take every tile, 64 keys each, and exchange their maxima: the
-        // scales make this the longest step of a tile's chain, and half the keys a
-        // thread (which then stay in registers) nearly halve it.
-        const int pair = 2 + (warp & 3), c0 = 64 * group;   // the barrier of the two warps of the same entries
+      const int pair = 2 + (warp & 3), c0 = 64 * group;   // the barrier of the two warps of the same entries
 #pragma unroll 1
-        for (int j = 0; j < T; ++j) {
-          const int g = tj + j, buf = g % NB, t0 = c.tiles.token(c.x + j);
-          const uint32_t s_col = lanes + (uint32_t)(buf * kKT);
-          wait(&h.s_full[buf], (uint32_t)((g / NB) & 1), abrt);
-          __syncwarp();
-          fence_after();
-          uint32_t xa[32], xb[32];
-          hide(t0, h.bad[g & 15], s_col, c0, c0 + 64, xa);
+      for (int j = 0; j < T; ++j) {
+        const int g = tj + j, buf = g % NB, t0 = c.tiles.token(c.x + j);
+        const uint32_t s_col = lanes + (uint32_t)(buf * kKT);
+        wait(&h.s_full[buf], (uint32_t)((g / NB) & 1), abrt);
+        __syncwarp();
+        fence_after();
+        uint32_t xa[32], xb[32];
+        hide(t0, h.bad[g & 15], s_col, c0, c0 + 64, xa);
+        if constexpr (F8) {
           wait(&h.sc_full[g & 7], (uint32_t)((g >> 3) & 1), abrt);
           factor();
-          tmem_ld32_start(s_col + (uint32_t)c0, xa);
-          tmem_ld_wait(xa);
-          tmem_ld32_start(s_col + (uint32_t)c0 + 32, xb);
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          auto take_max = [&](uint32_t(&x)[32], const float* ks) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(ks + i);
-              float a[4];
-              unpack2(mul2(pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), f.x), a[0], a[1]);
-              unpack2(mul2(pack2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), f.y), a[2], a[3]);
-              m4[(i >> 2) & 3] = fmaxf(fmaxf(m4[(i >> 2) & 3], fmaxf(a[0], a[1])), fmaxf(a[2], a[3]));
-#pragma unroll
-              for (int e = 0; e < 4; ++e) x[i + e] = __float_as_uint(a[e]);
-            }
-          };
-          take_max(xa, sc.k[g & 7] + c0);
-          tmem_ld_wait(xb);
-          take_max(xb, sc.k[g & 7] + c0 + 32);
-          float mx = mine ? fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) : -INFINITY;
-          // (Also: both groups have read their logits, over which the weights go.)
-          sc.mx[g & 1][group][row] = mx;
-          fence_before();
-          named_sync(pair, 64);
-          fence_after();
-          mx = fmaxf(mx, sc.mx[g & 1][group ^ 1][row]);
-          const bool moves = j == 0 ? mx != -INFINITY : mx > m + move;
-          if (__any_sync(0xffffffffu, moves)) {   // (the same in both warps)
-            const float alpha = moves ? ex2((m - mx) * zc) : 1.f;
-            if (moves) {
-              l *= alpha;
-              m = mx;
-            }
-            if (j > 0) {
-              wait(&h.pv_done[(g - 1) & 1], (uint32_t)(((g - 1) >> 1) & 1), abrt);
-              __syncwarp();
-              fence_after();
-#pragma unroll 1
-              for (int s = 0; s < D / 64; ++s) {   // the group's half of the channels
-                uint32_t o[32];
-                const uint32_t at = lanes + kOCol + (uint32_t)(group * (D / 2) + 32 * s);
-                tmem_ld32_start(at, o);
-                tmem_ld_wait(o);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                tmem_st32(at, o);
-              }
-              fence_before();
-              named_sync(pair, 64);   // either half of the weights lets the product begin
-            }
-          }
-          const float shift = m == -INFINITY ? 0.f : -m * zc;
-          const uint64_t zc2 = pack2(zc, zc), shift2 = pack2(shift, shift);
-          uint64_t sum2[2] = {0ull, 0ull};
-          auto weigh = [&](uint32_t(&x)[32], const float* vs, uint32_t to) {
-            uint32_t w[16];
-            ulonglong2 vv = {0ull, 0ull};
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float a, b;
-              if (!(i & 1)) vv = *reinterpret_cast<const ulonglong2*>(vs + 2 * i);
-              unpack2(fma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), zc2, shift2), a, b);
-              const uint64_t e = pack2(ex2(a), ex2(b));
-              sum2[i & 1] = add2(sum2[i & 1], e);
-              unpack2(mul2(e, i & 1 ? vv.y : vv.x), a, b);   // V's scale goes with the weight, which is rounded once
-              w[i] = pack_bf16(a, b);
-            }
-            tmem_st16(to, w);
-          };
-          __syncwarp();
-          weigh(xa, sc.v[g & 7] + c0, s_col + (uint32_t)(c0 / 2));
-          weigh(xb, sc.v[g & 7] + c0 + 32, s_col + (uint32_t)(c0 / 2 + 16));
-          tmem_st_wait();
-          fence_before();
-          __syncwarp();
-          if (lane == 0) bar_arrive(&h.p_full[group][buf]);
-          float s0, s1;
-          unpack2(add2(sum2[0], sum2[1]), s0, s1);
-          l += s0 + s1;
         }
-      } else {
-        for (int j = (tj ^ group) & 1; j < T; j += 2) {
-          const int g = tj + j, buf = g % NB, t0 = c.tiles.token(c.x + j);
-          const uint32_t s_col = lanes + (uint32_t)(buf * kKT);
-          wait(&h.s_full[buf], (uint32_t)((g / NB) & 1), abrt);
-          __syncwarp();
-          fence_after();
-          uint32_t xa[32], xb[32];
-          hide(t0, h.bad[g & 15], s_col, 0, kKT, xa);
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          auto take_max = [&](uint32_t(&x)[32]) {
+        tmem_ld32_start(s_col + (uint32_t)c0, xa);
+        tmem_ld_wait(xa);
+        tmem_ld32_start(s_col + (uint32_t)c0 + 32, xb);
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto take_max = [&](uint32_t(&x)[32], const float* ks) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 2)
-              m4[(i >> 1) & 3] = fmaxf(fmaxf(m4[(i >> 1) & 3], __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
-          };
-          tmem_ld32_start(s_col, xa);
-          tmem_ld_wait(xa);
-#pragma unroll 1
-          for (uint32_t col = 0; col < kKT; col += 64) {
-            tmem_ld32_start(s_col + col + 32, xb);
-            take_max(xa);
-            tmem_ld_wait(xb);
-            tmem_ld32_start(s_col + ((col + 64) & (kKT - 1)), xa);   // at the end the first ones again, for the weights
-            take_max(xb);
-            tmem_ld_wait(xa);
+          for (int i = 0; i < 32; i += 4) {
+            float a[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[e] = __uint_as_float(x[i + e]);
+            if constexpr (F8) {
+              const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(ks + i);
+              unpack2(mul2(pack2(a[0], a[1]), f.x), a[0], a[1]);
+              unpack2(mul2(pack2(a[2], a[3]), f.y), a[2], a[3]);
+            }
+            m4[(i >> 2) & 3] = fmaxf(fmaxf(m4[(i >> 2) & 3], fmaxf(a[0], a[1])), fmaxf(a[2], a[3]));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[i + e] = __float_as_uint(a[e]);
           }
-          // Lanes without an entry hold whatever their rows of Q gave; nothing reads
-          // their weights, and they must not move a maximum.
-          const float mx = mine ? fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) : -INFINITY;
-          // The running maximum after the tile before this one, then after this one.
-          if (g > 0) wait(&h.m_done[group ^ 1], (uint32_t)(((g - 1) >> 1) & 1), abrt);
-          const float before = j == 0 ? -INFINITY : h.m_run[row];
-          const bool moves = j == 0 ? mx != -INFINITY : mx > before + move;
-          const float now = moves ? mx : before;
-          h.m_run[row] = now;
-          __syncwarp();
-          if (lane == 0) bar_arrive(&h.m_done[group]);
-          if (now != m) {
-            l *= ex2((m - now) * zc);
-            m = now;
+        };
+        take_max(xa, F8 ? sc.k[g & 7] + c0 : nullptr);
+        tmem_ld_wait(xb);
+        take_max(xb, F8 ? sc.k[g & 7] + c0 + 32 : nullptr);
+        float mx = mine ? fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) : -INFINITY;
+        // (Also: both groups have read their logits, over which the weights go.)
+        h.mx[g & 1][group][row] = mx;
+        fence_before();
+        named_sync(pair, 64);
+        fence_after();
+        mx = fmaxf(mx, h.mx[g & 1][group ^ 1][row]);
+        const bool moves = j == 0 ? mx != -INFINITY : mx > m + move;
+        if (__any_sync(0xffffffffu, moves)) {   // (the same in both warps)
+          const float alpha = moves ? ex2((m - mx) * zc) : 1.f;
+          if (moves) {
+            l *= alpha;
+            m = mx;
           }
-          if (j > 0 && __any_sync(0xffffffffu, moves)) {
-            const float alpha = moves ? ex2((before - now) * zc) : 1.f;
+          if (j > 0) {
             wait(&h.pv_done[(g - 1) & 1], (uint32_t)(((g - 1) >> 1) & 1), abrt);
             __syncwarp();
             fence_after();
 #pragma unroll 1
-            for (int s = 0; s < D / 32; ++s) {
-              tmem_ld32_start(lanes + kOCol + (uint32_t)(32 * s), xb);
-              tmem_ld_wait(xb);
+            for (int s = 0; s < D / 64; ++s) {   // the group's half of the channels
+              uint32_t o[32];
+              const uint32_t at = lanes + kOCol + (uint32_t)(group * (D / 2) + 32 * s);
+              tmem_ld32_start(at, o);
+              tmem_ld_wait(o);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) xb[i] = __float_as_uint(__uint_as_float(xb[i]) * alpha);
-              tmem_st32(lanes + kOCol + (uint32_t)(32 * s), xb);
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(at, o);
             }
-          }
-          // Weights: in bf16 for the product, their sum in 32 bits.  32 logits
-          // become 16 columns of weights, always behind the logits still to be read.
-          const float shift = m == -INFINITY ? 0.f : -m * zc;
-          const uint64_t zc2 = pack2(zc, zc);
-          const uint64_t shift2 = pack2(shift, shift);
-          uint64_t sum2[2] = {0ull, 0ull};
-          auto weigh = [&](uint32_t(&x)[32], uint32_t col) {
-            uint32_t w[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float a, b;
-              uint64_t z = pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-              z = fma2(z, zc2, shift2);
-              unpack2(z, a, b);
-              a = ex2(a);
-              b = ex2(b);
-              sum2[i & 1] = add2(sum2[i & 1], pack2(a, b));
-              w[i] = pack_bf16(a, b);
-            }
-            tmem_st16(s_col + col / 2, w);
-          };
-          __syncwarp();
-#pragma unroll 1
-          for (uint32_t col = 0; col < kKT; col += 64) {
-            tmem_ld32_start(s_col + col + 32, xb);
-            weigh(xa, col);
-            tmem_ld_wait(xb);
-            if (col == 0) tmem_ld32_start(s_col + 64, xa);
-            weigh(xb, col + 32);
-            tmem_st_wait();
             fence_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive(&h.p_full[col / 64][buf]);
-            if (col == 0) tmem_ld_wait(xa);
+            named_sync(pair, 64);   // either half of the weights lets the product begin
           }
-          float s0, s1;
-          unpack2(add2(sum2[0], sum2[1]), s0, s1);
-          l += s0 + s1;
         }
+        const float shift = m == -INFINITY ? 0.f : -m * zc;
+        const uint64_t zc2 = pack2(zc, zc), shift2 = pack2(shift, shift);
+        uint64_t sum2[2] = {0ull, 0ull};
+        auto weigh = [&](uint32_t(&x)[32], const float* vs, uint32_t to) {
+          uint32_t w[16];
+          ulonglong2 vv = {0ull, 0ull};
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float a, b;
+            if (F8 && !(i & 1)) vv = *reinterpret_cast<const ulonglong2*>(vs + 2 * i);
+            unpack2(fma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), zc2, shift2), a, b);
+            a = ex2(a);
+            b = ex2(b);
+            const uint64_t e = pack2(a, b);
+            sum2[i & 1] = add2(sum2[i & 1], e);
+            if constexpr (F8) unpack2(mul2(e, i & 1 ? vv.y : vv.x), a, b);   // V's scale goes with the weight, rounded once
+            w[i] = pack_bf16(a, b);
+          }
+          tmem_st16(to, w);
+        };
+        __syncwarp();
+        weigh(xa, F8 ? sc.v[g & 7] + c0 : nullptr, s_col + (uint32_t)(c0 / 2));
+        weigh(xb, F8 ? sc.v[g & 7] + c0 + 32 : nullptr, s_col + (uint32_t)(c0 / 2 + 16));
+        tmem_st_wait();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&h.p_full[group][buf]);
+        float s0, s1;
+        unpack2(add2(sum2[0], sum2[1]), s0, s1);
+        l += s0 + s1;
       }
       tj += T;
       // The item's result, or this run's part of it: both groups' sums, relative
       // to the last maximum.
       named_sync(1, soft_threads);
-      if constexpr (F8) {
-        ++it;
-      } else {
-        const float m_last = h.m_run[row];
-        if (m_last != m) l *= ex2((m - m_last) * zc);
-        m = m_last;
-      }
+      if constexpr (F8) ++it;
       h.sums[group][row] = l;
       named_sync(1, soft_threads);
       l += h.sums[group ^ 1][row];

@@ -279,8 +279,10 @@ def test_windows_whose_items_differ_by_a_tile():
     out, lse = torch.empty_like(q), torch.empty(40, Hkv, device=dev())
     qsa.paged_attn(qsa.PagedCache(k, v), batch, q, out, lse, window=W)
     K, V = (t.transpose(0, 1).reshape(Hkv, -1, D)[:, :n].double() for t in (k, v))
-    z = torch.einsum("rhd,htd->rht", q.double(), K) * D ** -0.5
-    pos, t = torch.arange(n - 40, n, device=dev())[:, None], torch.arange(n, device=dev())[None]
+    rows = [0, 31, 32, 39]                                     # the items' first and last
+    out, lse = out[rows], lse[rows]
+    z = torch.einsum("rhd,htd->rht", q[rows].double(), K) * D ** -0.5
+    pos, t = torch.tensor([n - 40 + r for r in rows], device=dev())[:, None], torch.arange(n, device=dev())[None]
     z.masked_fill_(~((t <= pos) & (t > pos - W))[:, None], float("-inf"))
     want = torch.einsum("rht,htd->rhd", z.softmax(-1), V)
     # 87,000 nearly equal weights: sums within n u of |V|'s mean, here 2 (n + 40) 2^-24 0.8.
