@@ -738,7 +738,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
         const uint32_t d = tmem + (uint32_t)(s_buf * kKT);
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
-          live = __all_sync(0xffffffffu, wait(&h.full[0][ka.slot], ka.use & 1, abrt) && live);
+          live = wait(&h.full[0][ka.slot], ka.use & 1, abrt) && live;
           fence_after();
           if (leader && live) {
             const uint64_t k = k_desc + (uint32_t)(ka.slot * (kKeySlab >> 4)), q = q_desc + (F8 ? 1 : 2) * s * q_step;
@@ -787,13 +787,14 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
         const Ring first = va;
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
+          // (V is there first as a rule, so the weights are waited for last.)
+          if (part == 0) live = wait(v_full + va.slot, va.use & 1, abrt) && live;
           live = wait(&h.p_full[part][p_buf], phase, abrt) && live;
           if (part == 0 && j == 0 && it > 0) wait(&h.o_free, (uint32_t)((it - 1) & 1), abrt);
           va = first;
 #pragma unroll
           for (int s = 0; s < NS; ++s) {
-            if (part == 0) live = wait(v_full + va.slot, va.use & 1, abrt) && live;
-            live = __all_sync(0xffffffffu, live);
+            if (part == 0 && s > 0) live = wait(v_full + va.slot, va.use & 1, abrt) && live;
             fence_after();
             if (leader && live) {
               const uint64_t v = v_desc + (uint32_t)(va.slot * (kSlab >> 4));
