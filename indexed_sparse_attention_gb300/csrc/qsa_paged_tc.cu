@@ -35,7 +35,7 @@
 // product), and K's scales times the logit scale are applied to S by column; V's
 // codes become bf16 in shared memory, and V's scales go with the weights, which
 // are rounded once.  (K through bf16 as well: 351 us on a ragged batch of 16
-// sequences where this takes 174.)
+// sequences where this takes 169.)
 //
 // Roles: warps 0-7 softmax and output, warps 8 and 10 copy K and V, warp 9 issues
 // the MMAs; bf16: warp 11 copies Q and clears V's ends; fp8: warps 12-15 write Q's
@@ -47,10 +47,10 @@
 // 1,941 TFLOP/s): few rows, the K/V bytes -- 261,120 tokens x 4 rows 89 of 79; the
 // call's start and the joining launch are what a 65,536-token row (32 of 20) and a
 // windowed batch of 64 (49 of 33) add.  2,048 rows: over 16k tokens (head_dim 128)
-// 295 of 199, the tensor pipe 65% busy at the power limit; over a
-// 4,096-token window (256) 173 of 108, the shared memory's 128 bytes a cycle, which
+// 290 of 199, the tensor pipe 67% busy at the power limit; over a
+// 4,096-token window (256) 170 of 108, the shared memory's 128 bytes a cycle, which
 // Q and K take whole in the logits' product (2,700 cycles a tile where the products
-// alone take 2,048).  fp8: 174 of 115, shared memory again, which V's codes cross three
+// alone take 2,048).  fp8: 169 of 115, shared memory again, which V's codes cross three
 // times more than bf16 values do.
 #include <math.h>
 
@@ -122,7 +122,7 @@ __device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, int* abort) {
 struct Head {
   uint64_t full[2][kMaxSlabs], empty[2][kMaxSlabs];   // K, V
   uint64_t v_ready[kMaxSlabs];                        // bf16: V, without what no row sees
-  uint64_t s_full[2], p_full[2][2], pv_done[2], o_free, q_full, q_free, q_used, mma_done;
+  uint64_t s_full[2], p_full[2], pv_done[2], o_free, q_full, q_free, q_used, mma_done;
   uint64_t code_full[kMaxCodeSlabs], code_empty[kMaxCodeSlabs], sc_full[8];   // fp8 caches: V's codes, scales
   int64_t scan[16];
   Start start;
@@ -374,8 +374,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
     for (int i = 0; F8 && i < 8; ++i) bar_init(&h.sc_full[i], kCodeWarps);
     for (int i = 0; i < 2; ++i) {
       bar_init(&h.s_full[i], 1);
-      bar_init(&h.p_full[0][i], quarters);
-      bar_init(&h.p_full[1][i], quarters);
+      bar_init(&h.p_full[i], 2 * quarters);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(&h.pv_done[i], 1);
@@ -781,33 +780,26 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       // buffer that its weights leave.
 #pragma unroll 1
       for (int j = 0; j < T; ++j) {
-        // The weights come in two halves of 64 keys, one from each group.
-        const uint32_t phase = (p_phase >> p_buf) & 1;
+        // (V is there first as a rule, so the weights are waited for last.)
+        live = wait(v_full + va.slot, va.use & 1, abrt) && live;
+        live = wait(&h.p_full[p_buf], (p_phase >> p_buf) & 1, abrt) && live;
         p_phase ^= 1u << p_buf;
-        const Ring first = va;
+        if (j == 0 && it > 0) wait(&h.o_free, (uint32_t)((it - 1) & 1), abrt);
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          // (V is there first as a rule, so the weights are waited for last.)
-          if (part == 0) live = wait(v_full + va.slot, va.use & 1, abrt) && live;
-          live = wait(&h.p_full[part][p_buf], phase, abrt) && live;
-          if (part == 0 && j == 0 && it > 0) wait(&h.o_free, (uint32_t)((it - 1) & 1), abrt);
-          va = first;
+        for (int s = 0; s < NS; ++s) {
+          if (s > 0) live = wait(v_full + va.slot, va.use & 1, abrt) && live;
+          fence_after();
+          if (leader && live) {
+            const uint64_t v = v_desc + (uint32_t)(va.slot * (kSlab >> 4));
 #pragma unroll
-          for (int s = 0; s < NS; ++s) {
-            if (part == 0 && s > 0) live = wait(v_full + va.slot, va.use & 1, abrt) && live;
-            fence_after();
-            if (leader && live) {
-              const uint64_t v = v_desc + (uint32_t)(va.slot * (kSlab >> 4));
-#pragma unroll
-              for (int x = 4 * part; x < 4 * part + 4; ++x)
-                mma_bf16_ts(tmem + kOCol + (uint32_t)(s * 128), tmem + (uint32_t)(p_buf * kKT + 8 * x), v + 128 * x,
-                            kIdescO, (j | x) != 0 ? 1u : 0u);
-              if (part == 1) commit(&h.empty[1][va.slot]);
-              if (part == 1 && s == NS - 1) commit(&h.pv_done[odd]);
-            }
-            __syncwarp();
-            va.step(tp.n_v);
+            for (int x = 0; x < 8; ++x)
+              mma_bf16_ts(tmem + kOCol + (uint32_t)(s * 128), tmem + (uint32_t)(p_buf * kKT + 8 * x), v + 128 * x,
+                          kIdescO, (j | x) != 0 ? 1u : 0u);
+            commit(&h.empty[1][va.slot]);
+            if (s == NS - 1) commit(&h.pv_done[odd]);
           }
+          __syncwarp();
+          va.step(tp.n_v);
         }
         odd ^= 1;
         p_buf = p_buf + 1 == NB ? 0 : p_buf + 1;
@@ -927,7 +919,6 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
               tmem_st32(at, o);
             }
             fence_before();
-            named_sync(pair, 64);   // either half of the weights lets the product begin
           }
         }
         const float shift = m == -INFINITY ? 0.f : -m * zc;
@@ -956,7 +947,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
         tmem_st_wait();
         fence_before();
         __syncwarp();
-        if (lane == 0) bar_arrive(&h.p_full[group][buf]);
+        if (lane == 0) bar_arrive(&h.p_full[buf]);
         float s0, s1;
         unpack2(add2(sum2[0], sum2[1]), s0, s1);
         l += s0 + s1;

@@ -280,14 +280,16 @@ def test_windows_whose_items_differ_by_a_tile():
     qsa.paged_attn(qsa.PagedCache(k, v), batch, q, out, lse, window=W)
     K, V = (t.transpose(0, 1).reshape(Hkv, -1, D)[:, :n].double() for t in (k, v))
     rows = [0, 31, 32, 39]                                     # the items' first and last
-    out, lse = out[rows], lse[rows]
-    z = torch.einsum("rhd,htd->rht", q[rows].double(), K) * D ** -0.5
-    pos, t = torch.tensor([n - 40 + r for r in rows], device=dev())[:, None], torch.arange(n, device=dev())[None]
-    z.masked_fill_(~((t <= pos) & (t > pos - W))[:, None], float("-inf"))
-    want = torch.einsum("rht,htd->rhd", z.softmax(-1), V)
+    want, want_lse = [], []
+    for r in rows:
+        t = torch.arange(n, device=dev())
+        z = ((K * q[r].double()[:, None]).sum(-1) * D ** -0.5).masked_fill((t > n - 40 + r) | (t <= n - 40 + r - W), float("-inf"))
+        want.append((z.softmax(-1)[..., None] * V).sum(1))
+        want_lse.append(torch.logsumexp(z, -1))
+    out, lse, want, want_lse = out[rows], lse[rows], torch.stack(want), torch.stack(want_lse)
     # 87,000 nearly equal weights: sums within n u of |V|'s mean, here 2 (n + 40) 2^-24 0.8.
     assert (out.double() - want).abs().max() < 2 * (W + 40) * 2.0 ** -24
-    assert (lse.double() - torch.logsumexp(z, -1)).abs().max() < (W + 40) * 2.0 ** -24 + 2e-4
+    assert (lse.double() - want_lse).abs().max() < (W + 40) * 2.0 ** -24 + 2e-4
     assert qsa.check_device_status() == (0, "")
 
 
