@@ -50,8 +50,8 @@
 // 290 of 199, the tensor pipe 67% busy at the power limit; over a
 // 4,096-token window (256) 170 of 108, the shared memory's 128 bytes a cycle, which
 // Q and K take whole in the logits' product (2,700 cycles a tile where the products
-// alone take 2,048).  fp8: 169 of 115, shared memory again, which V's codes cross three
-// times more than bf16 values do.
+// alone take 2,048).  fp8: 170 of 115, shared memory too: the products, V's conversion
+// and the scales pass over it 3,200 cycles a tile where HBM needs 2,800.
 #include <math.h>
 
 #include <cuda_fp16.h>
