@@ -612,7 +612,8 @@ typedef struct qsa_paged_batch {
  *   window         0 (no window) or the tokens a row sees, its own included
  *   n_sinks        >= 0 first tokens that stay visible (no meaning without a window)
  *   q              device [n_rows, Hq, head_dim], cfg->q_dtype
- *   out            device [n_rows, Hq, head_dim], cfg->out_dtype
+ *   out            device [n_rows, Hq, head_dim], cfg->out_dtype; out, lse
+ *                  and the workspace overlap nothing that the call reads
  *   lse            device f32 [n_rows, Hq]; may be NULL
  *   workspace      device scratch of >= qsa_paged_attn_workspace_size bytes; it
  *                  depends on max_rows, cfg and the device, not on the lengths;

@@ -79,6 +79,35 @@ def test_page_sizes_and_scale():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp8", "f32"])
+@pytest.mark.parametrize("D,page", [(128, 16), (256, 1024)])
+def test_caches_that_are_views(dtype, D, page):
+    # K and V side by side in one tensor of pages, of which every second one is the cache's; scales likewise.
+    x = make_paged([1500, 70, 3], [4, 1, 2], dtype=dtype, D=D, page=page, seed=44, poison=True)
+    n, Hkv = x.k.shape[:2]
+    kv = torch.zeros(2 * n, 2, Hkv, page, D, dtype=x.k.dtype, device=dev())
+    kv[::2, 0], kv[::2, 1] = x.k.to(dev()), x.v.to(dev())
+    sc = None
+    if x.scale is not None:
+        sc = torch.zeros(2 * n, page, Hkv, 2, dtype=torch.float16, device=dev()).transpose(1, 2)
+        sc[::2] = x.scale.to(dev())
+        sc = sc[::2]
+    _, batch, q = x.device()
+    cache = qsa.PagedCache(kv[::2, 0], kv[::2, 1], sc)
+    out, lse = torch.empty(q.shape, device=dev()), torch.empty(q.shape[:2], device=dev())
+    for window, sinks in ((0, 0), (90, 7)):
+        qsa.paged_attn(cache, batch, q, out, lse, window=window, n_sinks=sinks)
+        torch.cuda.synchronize()
+        assert_attended(out, lse, attend64(x, window, sinks))
+    before = kv.clone()
+    rows = torch.ones(q.shape[0], Hkv, D, dtype=cache.row_dtype, device=dev())
+    qsa.paged_append(cache, batch, rows, 2 * rows)
+    torch.cuda.synchronize()
+    assert torch.equal(kv[1::2].view(torch.uint8), before[1::2].view(torch.uint8))   # the pages between are not the cache's
+    assert not torch.equal(kv[::2].view(torch.uint8), before[::2].view(torch.uint8))
+    assert qsa.check_device_status() == (0, "")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8", "f32"])
 @pytest.mark.parametrize("D", [128, 256])
 def test_queries_of_any_size(dtype, D):
     # A channel far above the others, rows of zeros, of the smallest and of large values, next to ordinary ones.
