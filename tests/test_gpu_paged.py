@@ -78,6 +78,39 @@ def test_page_sizes_and_scale():
         check(x, scale=0.05)
 
 
+def test_steps_at_once_on_two_streams():
+    # Two steps with their own workspaces, plain and captured, interleaved on two streams.
+    cases = [make_paged([3000, 40, 700], [4, 1, 30], dtype=d, D=D, page=32, seed=45) for d, D in (("bf16", 256), ("fp8", 128))]
+    steps, alone, graphs = [], [], []
+    streams = [torch.cuda.Stream() for _ in cases]
+    for x in cases:
+        cache, batch, q = x.device()
+        steps.append(qsa.PagedStep(cache, batch, q, window=900, n_sinks=5))
+    for st in steps:
+        out, lse = st.attend()
+        torch.cuda.synchronize()
+        alone.append((out.clone(), lse.clone()))
+    for st, stream in zip(steps, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=stream):
+            for _ in range(3):
+                st.attend()
+        graphs.append(g)
+    for turn in range(10):
+        for st, stream, g in zip(steps, streams, graphs):
+            with torch.cuda.stream(stream):
+                st.out.zero_()
+                if turn % 2:
+                    g.replay()
+                else:
+                    for _ in range(4):
+                        st.attend()
+        torch.cuda.synchronize()
+        for st, (out, lse) in zip(steps, alone):
+            assert torch.equal(st.out, out) and torch.equal(st.lse, lse)
+    assert qsa.check_device_status() == (0, "")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp8", "f32"])
 @pytest.mark.parametrize("D,page", [(128, 16), (256, 1024)])
 def test_caches_that_are_views(dtype, D, page):
