@@ -1,0 +1,67 @@
+"""Scratch that a call allocates itself belongs to the stream the call runs on."""
+import pytest
+import torch
+
+import indexed_sparse_attention_gb300 as qsa
+from indexed_sparse_attention_gb300 import paged
+from paged_cases import dev, make_paged
+
+
+def test_scratch_is_allocated_on_the_stream_of_the_call(monkeypatch):
+    # Without a GPU: which stream is the current one when the block is allocated.
+    current, seen, empty = ["the current stream"], [], torch.empty
+
+    class On:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            current.append(self.stream)
+
+        def __exit__(self, *_):
+            current.pop()
+
+    def fake_empty(n, dtype, device):
+        seen.append(current[-1])
+        return empty(n, dtype=dtype)
+
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: f"stream {handle} of {device}")
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    monkeypatch.setattr(torch, "empty", fake_empty)
+    assert paged._scratch(100, torch.device("cuda", 0), None).numel() == 100
+    assert paged._scratch(0, torch.device("cuda", 0), 77).numel() == 16
+    assert seen == ["the current stream", "stream 77 of cuda:0"] and len(current) == 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("handle", [False, True])
+def test_calls_without_a_workspace_on_streams_that_run_at_once(handle):
+    # Long calls on the current stream whose scratch is free for Python while they still run, and a call
+    # on a stream that nothing orders behind them.
+    long = make_paged([9000, 3000], [600, 1], dtype="bf16", D=128, page=64, seed=70)
+    short = make_paged([4000, 50], [3, 1], dtype="bf16", D=128, page=64, seed=71)
+    side = torch.cuda.Stream()
+    cases = []
+    for x in (long, short):
+        cache, batch, q = x.device()
+        # (One shape of call, so that one's scratch would fit the other.)
+        batch = qsa.PagedBatch(batch.table, batch.lens, batch.row_start, n_rows=batch.n_rows, max_rows=600)
+        out, lse = torch.empty(q.shape, device=dev()), torch.empty(q.shape[:2], device=dev())
+        qsa.paged_attn(cache, batch, q, out, lse)
+        torch.cuda.synchronize()
+        cases.append((cache, batch, q, out, lse, out.clone(), lse.clone()))
+    (lc, lb, lq, lo, ll, want_lo, want_ll), (sc, sb, sq, so, sl, want_so, want_sl) = cases
+    for _ in range(20):
+        lo.zero_()
+        so.zero_()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            qsa.paged_attn(lc, lb, lq, lo, ll)
+        for _ in range(3):
+            qsa.paged_attn(sc, sb, sq, so, sl, stream=side.cuda_stream if handle else side)
+        filler = torch.full((1 << 22,), 3.0, device=dev())       # may not take the side stream's scratch either
+        torch.cuda.synchronize()
+        assert torch.equal(lo, want_lo) and torch.equal(ll, want_ll)
+        assert torch.equal(so, want_so) and torch.equal(sl, want_sl)
+        del filler
+    assert qsa.check_device_status() == (0, "")
