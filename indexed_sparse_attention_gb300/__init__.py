@@ -176,6 +176,20 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _scratch(n_bytes: int, device, stream) -> torch.Tensor:
+    """A workspace for work on `stream` (None: the device's current stream).  It is
+    allocated with that stream as the current one: the allocator hands blocks on
+    in the order of the stream they were allocated on, so neither a block whose
+    last work is still queued elsewhere is taken, nor this one given away early."""
+    n = max(int(n_bytes), 16)
+    if stream is None:
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=torch.uint8, device=device)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -275,7 +289,7 @@ def score_blocks(seqs, q_idx: torch.Tensor, scores: torch.Tensor, stream=None, s
     if workspace is None:
         need = score_workspace_size(None, q_idx, seq_array=arr)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=scores.device)
+            workspace = _scratch(need, scores.device, stream)
     _check("qsa_score_blocks", lib().qsa_score_blocks(
         arr, len(arr), q_idx.data_ptr(), _dtype_code(q_idx), scores.data_ptr(), scores.stride(0),
         _ptr(group_max), 0 if group_max is None else group_max.stride(0), _ptr(workspace),
@@ -304,7 +318,7 @@ def pool_score_blocks(seqs, q_idx: torch.Tensor, scores: torch.Tensor, stream=No
     if workspace is None:
         need = score_workspace_size(None, q_idx, seq_array=arr)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=scores.device)
+            workspace = _scratch(need, scores.device, stream)
     _check("qsa_pool_score_blocks", lib().qsa_pool_score_blocks(
         arr, len(arr), ia[0], ia[1], ia[2], q_idx.data_ptr(), _dtype_code(q_idx), scores.data_ptr(),
         scores.stride(0), _ptr(group_max), 0 if group_max is None else group_max.stride(0), _ptr(workspace),
@@ -319,7 +333,7 @@ def select_topk(seqs, scores: torch.Tensor, sel: torch.Tensor, cnt: torch.Tensor
     arr = seq_array if seq_array is not None else make_seq_array(seqs)
     need = lib().qsa_select_workspace_size(arr, len(arr), top_k)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=scores.device)
+        workspace = _scratch(need, scores.device, stream)
     _check("qsa_select_topk", lib().qsa_select_topk(
         arr, len(arr), scores.data_ptr(), scores.stride(0), _ptr(group_max),
         0 if group_max is None else group_max.stride(0), int(top_k), sel.data_ptr(), cnt.data_ptr(),
@@ -332,7 +346,7 @@ def score_select_topk(seqs, q_idx: torch.Tensor, scores: torch.Tensor, sel: torc
     arr = seq_array if seq_array is not None else make_seq_array(seqs)
     need = lib().qsa_score_select_workspace_size(arr, len(arr), top_k)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=scores.device)
+        workspace = _scratch(need, scores.device, stream)
     _check("qsa_score_select_topk", lib().qsa_score_select_topk(
         arr, len(arr), q_idx.data_ptr(), _dtype_code(q_idx), scores.data_ptr(), scores.stride(0), int(top_k),
         sel.data_ptr(), cnt.data_ptr(), _ptr(workspace), 0 if workspace is None else workspace.numel(),
@@ -374,7 +388,7 @@ def append_score_blocks(seq: Seq, k_new: torch.Tensor, v_new: torch.Tensor, idx_
     if workspace is None:
         need = score_workspace_size(None, q_idx, seq_array=arr)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=scores.device)
+            workspace = _scratch(need, scores.device, stream)
     idxk = seq.idx_keys
     _check("qsa_append_score_blocks", lib().qsa_append_score_blocks(
         arr, ctypes.byref(cfg), k_new.data_ptr(), v_new.data_ptr(), idx_new.data_ptr(), idxk.data_ptr(),
@@ -455,7 +469,7 @@ def score_select_topk_blocked(seqs, q_idx: torch.Tensor, sel: torch.Tensor, cnt:
     arr = seq_array if seq_array is not None else make_seq_array(seqs)
     need = score_select_blocked_workspace_size(None, top_k, block_keys, seq_array=arr)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q_idx.device)
+        workspace = _scratch(need, q_idx.device, stream)
     _check("qsa_score_select_topk_blocked", lib().qsa_score_select_topk_blocked(
         arr, len(arr), q_idx.data_ptr(), _dtype_code(q_idx), int(top_k), int(block_keys), sel.data_ptr(),
         cnt.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(stream)))
@@ -496,7 +510,7 @@ def sparse_attn(seqs, q: torch.Tensor, sel: torch.Tensor, cnt: torch.Tensor, out
         cfg = attn_config(q, n_kv_heads, out.dtype, scale, n_splits, kv_dtype=_kv_dtype(seqs))
     need = lib().qsa_attn_workspace_size(arr, len(arr), ctypes.byref(cfg), sel.stride(0))
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _scratch(need, q.device, stream)
     _check("qsa_sparse_attn", lib().qsa_sparse_attn(
         arr, len(arr), ctypes.byref(cfg), q.data_ptr(), sel.data_ptr(), cnt.data_ptr(), sel.stride(0),
         out.data_ptr(), _ptr(lse), _ptr(workspace), 0 if workspace is None else workspace.numel(),

@@ -14,7 +14,7 @@ from typing import Sequence
 
 import torch
 
-from . import AttnConfig, BF16, F32, FP8, _check, _dtype_code, _ptr, lib
+from . import AttnConfig, BF16, F32, FP8, _check, _dtype_code, _ptr, _scratch, lib
 
 
 class PagedCacheDesc(ctypes.Structure):
@@ -86,20 +86,6 @@ def _call(name: str, device, stream, *args):
             status = fn(*args, _raw_stream(stream, device))
     if status:
         _check(name, status)
-
-
-def _scratch(n_bytes: int, device, stream) -> torch.Tensor:
-    """A workspace for work on `stream` (None: the device's current stream).  It is
-    allocated with that stream as the current one: the allocator hands blocks on
-    in the order of the stream they were allocated on, so neither a block whose
-    last work is still queued elsewhere is taken, nor this one given away early."""
-    n = max(int(n_bytes), 16)
-    if stream is None:
-        return torch.empty(n, dtype=torch.uint8, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_raw_stream(stream, device), device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def _int_list(name: str, t: torch.Tensor, like: torch.Tensor) -> torch.Tensor:

@@ -7,8 +7,9 @@ from indexed_sparse_attention_gb300 import paged
 from paged_cases import dev, make_paged
 
 
-def test_scratch_is_allocated_on_the_stream_of_the_call(monkeypatch):
-    # Without a GPU: which stream is the current one when the block is allocated.
+@pytest.fixture
+def allocations(monkeypatch):
+    """Without a GPU: the stream that is the current one at each allocation of scratch."""
     current, seen, empty = ["the current stream"], [], torch.empty
 
     class On:
@@ -21,16 +22,47 @@ def test_scratch_is_allocated_on_the_stream_of_the_call(monkeypatch):
         def __exit__(self, *_):
             current.pop()
 
-    def fake_empty(n, dtype, device):
-        seen.append(current[-1])
-        return empty(n, dtype=dtype)
+    def fake_empty(*size, **kw):
+        if kw.get("dtype") is torch.uint8:
+            seen.append(current[-1])
+            kw.pop("device", None)
+        return empty(*size, **kw)
 
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: f"stream {handle} of {device}")
     monkeypatch.setattr(torch.cuda, "stream", On)
     monkeypatch.setattr(torch, "empty", fake_empty)
+    yield seen
+    assert len(current) == 1
+
+
+def test_scratch_is_allocated_on_the_stream_of_the_call(allocations):
     assert paged._scratch(100, torch.device("cuda", 0), None).numel() == 100
     assert paged._scratch(0, torch.device("cuda", 0), 77).numel() == 16
-    assert seen == ["the current stream", "stream 77 of cuda:0"] and len(current) == 1
+    assert allocations == ["the current stream", "stream 77 of cuda:0"]
+
+
+def test_scratch_of_the_layer_step_calls_too(allocations, monkeypatch):
+    # Every call of the package that allocates its scratch when none is given, over a library that only says "64 bytes".
+    class Fake:
+        def __getattr__(self, name):
+            return lambda *args: 64 if name.endswith("workspace_size") else 0
+
+    monkeypatch.setattr(qsa, "lib", lambda: Fake())
+    z = torch.zeros
+    pooled, scores, q_idx = z(16, 128), z(1, 16), z(1, 4, 128)
+    sel, cnt, q, out = z(1, 16, dtype=torch.int32), z(1, dtype=torch.int32), z(1, 4, 128), z(1, 4, 128)
+    seq = qsa.Seq(40, 1, pooled, [qsa.Segment(z(2, 40, 128), z(2, 40, 128), 0)], idx_keys=z(40, 128))
+    calls = [lambda s: qsa.score_blocks([seq], q_idx, scores, s),
+             lambda s: qsa.pool_score_blocks([seq], q_idx, scores, s),
+             lambda s: qsa.select_topk([seq], scores, sel, cnt, stream=s),
+             lambda s: qsa.score_select_topk([seq], q_idx, scores, sel, cnt, stream=s),
+             lambda s: qsa.score_select_topk_blocked([seq], q_idx, sel, cnt, stream=s),
+             lambda s: qsa.append_score_blocks(seq, z(2, 1, 128), z(2, 1, 128), z(1, 128), q_idx, scores, s),
+             lambda s: qsa.sparse_attn([seq], q, sel, cnt, out, stream=s)]
+    for call in calls:
+        allocations.clear()
+        call(77)
+        assert allocations == ["stream 77 of cpu"]
 
 
 @pytest.mark.gpu
