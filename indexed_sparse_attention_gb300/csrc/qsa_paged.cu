@@ -26,14 +26,14 @@ __device__ int g_f32_timeouts;
 __device__ int g_bad_pages;   // table entries outside [0, n_pages) among the tokens that a call read
 
 // ------------------------------------------------------------------ f32 caches
-// (A windowed batch of five sequences, 1 to 37 rows, head_dim 256: 54 us, of which
+// (A windowed batch of five sequences, 1 to 37 rows, head_dim 256: 56 us, of which
 // the three tf32 products are 22 and the start, the waits for the next call and
 // the joining launch about 12; the rest is the splitting and the exchange of
 // partial logits between two barriers a tile.)
 //
 // Products of f32 values on the tensor pipe, by tf32 halves: x = hi + lo with hi
-// = x rounded to 11 significant bits and lo = x - hi rounded likewise, and
-//   a b = hi_a hi_b + hi_a lo_b + lo_a hi_b  (+ lo_a lo_b, below 2^-22 |a b|, left out).
+// = x rounded to 11 significant bits and lo = x - hi cut off after as many, and
+//   a b = hi_a hi_b + hi_a lo_b + lo_a hi_b  (+ lo_a lo_b, at most 2^-22 |a b|, left out).
 // The tensor pipe cuts its 32-bit sums off instead of rounding them, so few are
 // taken on one accumulator: a tile's sums are added to the running ones in plain
 // 32-bit arithmetic.  (With the running ones as accumulators, outputs were 2.8e-6
@@ -70,11 +70,16 @@ struct F32Layout {
 
 // The halves of x.  Adding half a unit of the 11th significant bit to the pattern
 // and clearing the 13 bits below rounds to nearest (halves away from zero); of lo
-// the tensor pipe ignores those bits itself.  (In plain integer operations: the
-// conversion instruction took most of the kernel's time.)
+// the tensor pipe ignores those bits itself, at most 2^-22 |x|.  (In plain integer
+// operations: the conversion instruction took most of the kernel's time.)  Patterns
+// whose rounding would reach infinity, or past the NaNs the other sign, are taken as
+// the largest one below: hi is always finite, and what is infinite or no number in x
+// is so in lo, hence in two of the three products and never in opposite signs.  (The
+// two minima cost 2 us of 54.  Rounding lo as well, which needs a third: 58 us, and
+// the same error against 64 bits, 1.4e-7 in the root mean square of that batch.)
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
-  lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;
+  hi = (min((uint32_t)min(__float_as_int(x), 0x7f7fefff), 0xff7fefffu) + 0x1000u) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
 }
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"

@@ -1,0 +1,135 @@
+"""Paged attention of values at the ends of their types: NaN as a GPU writes it
+and the largest f32 values.  Tolerances are derived in paged_cases."""
+import pytest
+import torch
+
+import indexed_sparse_attention_gb300 as qsa
+from paged_cases import Paged, assert_attended, attend64, dev, make_paged
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from indexed_sparse_attention_gb300 import build
+    build.build()
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need CUDA")
+    qsa.check_device_status()
+
+
+def run(x: Paged, **kw):
+    cache, batch, q = x.device()
+    out, lse = torch.empty(q.shape, device=dev()), torch.empty(q.shape[:2], device=dev())
+    qsa.paged_attn(cache, batch, q, out, lse, **kw)
+    torch.cuda.synchronize()
+    assert qsa.check_device_status() == (0, "")
+    return out.cpu(), lse.cpu()
+
+
+# ------------------------------------------------------------------ NaN
+#: Bit patterns of NaN: what f32 arithmetic on the GPU returns, its negative, and the smallest and the usual payload.
+PATTERNS = {"f32": [0x7FFFFFFF, 0xFFFFFFFF, 0x7F800001, 0xFF800001, 0x7FC00000],
+            "bf16": [0x7FFF, 0xFFFF, 0x7F81, 0x7FC0], "fp8": [0x7F, 0xFF]}
+NANS = [(d, p) for d, ps in PATTERNS.items() for p in ps]
+
+
+def set_bits(t: torch.Tensor, at, pattern: int):
+    bits = t.view({4: torch.int32, 2: torch.int16, 1: torch.uint8}[t.element_size()])
+    width = 8 * t.element_size()
+    bits[at] = pattern - (1 << width) if bits.dtype != torch.uint8 and pattern >> (width - 1) else pattern
+
+
+def nan_case(dtype):
+    # A chunk whose rows see different tokens, and a sequence of many key tiles that is split over runs.
+    return make_paged([300, 5000], [40, 2], dtype=dtype, D=128, page=32, seed=61)
+
+
+def place(x: Paged, i: int, t: int):
+    return int(x.table[i, t // x.page]), t % x.page
+
+
+def same_but(good, bad, wrong):
+    """Rows (and channels) outside `wrong` hold the same bits, those inside are NaN."""
+    assert torch.isnan(bad[wrong]).all()
+    assert torch.equal(good[~wrong], bad[~wrong])
+
+
+@pytest.mark.parametrize("dtype,pattern", NANS + [("fp8", 0x7FFF)])
+def test_nan_in_a_query(dtype, pattern):
+    if dtype == "fp8" and pattern < 0x100:
+        pattern = 0xFF80 | pattern                        # queries of an fp8 cache are bf16
+    x = nan_case(dtype)
+    good = run(x)
+    wrong = torch.zeros(x.q.shape[:2], dtype=torch.bool)
+    for r, h in ((3, 1), (39, 23), (41, 7)):
+        set_bits(x.q, (r, h, 77), pattern)
+        wrong[r, h] = True
+    bad = run(x)
+    same_but(good[0], bad[0], wrong[..., None].expand_as(bad[0]))
+    same_but(good[1], bad[1], wrong)
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (30, 4)])
+@pytest.mark.parametrize("dtype,pattern", NANS)
+def test_nan_in_a_key(dtype, pattern, window, sinks):
+    x = nan_case(dtype)
+    good = run(x, window=window, n_sinks=sinks)
+    wrong = torch.zeros(x.q.shape[:2], dtype=torch.bool)
+    for i, t, h in ((0, 275, 0), (1, 4990, 1), (1, 2, 0)):
+        p, s = place(x, i, t)
+        set_bits(x.k, (p, h, s, 9), pattern)
+        for j in range(x.rows[i]):
+            pos = x.lens[i] - x.rows[i] + j
+            if t <= pos and (not window or t > pos - window or t < sinks):
+                wrong[int(x.row_start[i]) + j, 12 * h:12 * h + 12] = True
+    bad = run(x, window=window, n_sinks=sinks)
+    assert wrong.any() and not wrong.all()
+    same_but(good[0], bad[0], wrong[..., None].expand_as(bad[0]))
+    same_but(good[1], bad[1], wrong)
+
+
+@pytest.mark.parametrize("dtype,pattern", NANS)
+def test_nan_in_a_value(dtype, pattern):
+    # (Of tokens that every row of their sequence sees: the others' weights are zero, and 0 x NaN is NaN.)
+    x = nan_case(dtype)
+    good = run(x)
+    wrong = torch.zeros(x.q.shape, dtype=torch.bool)
+    for i, t, h, c in ((0, 100, 0, 5), (1, 3000, 1, 127)):
+        p, s = place(x, i, t)
+        set_bits(x.v, (p, h, s, c), pattern)
+        wrong[int(x.row_start[i]):int(x.row_start[i + 1]), 12 * h:12 * h + 12, c] = True
+    bad = run(x)
+    same_but(good[0], bad[0], wrong)
+    assert torch.equal(good[1], bad[1])
+
+
+# ------------------------------------------------------------------ f32
+@pytest.mark.parametrize("bits", [0x7F7FFFFF, 0x7F7FF800, 0x7F7FEFFF, 0xFF7FFFFF, 0x7F000000])
+def test_f32_values_up_to_the_largest(bits):
+    # A row that sees one token returns its V, whose two tf32 parts hold 22 bits: cut off after them, 2^-21 at most.
+    x = make_paged([40], [1], dtype="f32", D=128, seed=62)
+    p, s = place(x, 0, 39)
+    set_bits(x.v, (p, 1, s, 3), bits)
+    value = float(x.v[p, 1, s, 3])
+    out, lse = run(x, window=1)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    assert ((out[0, 12:, 3].double() - value).abs() <= 2.0 ** -21 * abs(value)).all()
+    # A key of that size against a query that brings the product back to the usual range.
+    x = make_paged([40], [1], dtype="f32", D=128, seed=63)
+    set_bits(x.k, (p, 1, s, 3), bits)
+    x.q[0, :, 3] = 2.0 ** -125
+    out, lse = run(x)
+    assert_attended(out, lse, attend64(x))
+
+
+def test_f32_infinities_of_values():
+    # The weights' sum over a V with an infinity is that infinity.
+    x = make_paged([300, 33], [1, 1], dtype="f32", D=128, seed=64)
+    good = run(x)
+    p, s = place(x, 0, 120)
+    x.v[p, 0, s, 8], x.v[p, 1, s, 9] = float("inf"), float("-inf")
+    out, lse = run(x)
+    assert (out[0, :12, 8] == float("inf")).all() and (out[0, 12:, 9] == float("-inf")).all()
+    out[0, :12, 8], out[0, 12:, 9] = good[0][0, :12, 8], good[0][0, 12:, 9]
+    assert torch.equal(out, good[0]) and torch.equal(lse, good[1])
