@@ -552,7 +552,7 @@ qsa_status qsa_lse_merge(const float* o_parts, const float* lse_parts, int32_t n
  * V likewise.  QSA_FP8_E4M3: k and v hold E4M3 codes and the (K, V) f16 scale
  * pair of (page, h, slot) is the 4-byte record at kv_scale + 4 * (page *
  * scale_page_stride + h * scale_head_stride + slot * scale_tok_stride), as for
- * segments.  f32, bf16 and fp8 caches; QSA_Q8_0 caches are not paged
+ * segments.  A scale may be any f16: zero, negative, infinite or NaN as it stands.  f32, bf16 and fp8 caches; QSA_Q8_0 caches are not paged
  * (QSA_ERR_UNSUPPORTED: the scales of its 32-channel blocks do not factor out
  * of a row's product, which is what lets the pages be read as stored). */
 typedef struct qsa_paged_cache {

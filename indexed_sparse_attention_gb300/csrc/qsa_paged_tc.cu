@@ -131,6 +131,7 @@ struct Head {
   uint32_t bad[16];             // 16-token pieces of a tile that have no page (fewer are under way)
   float mx[2][2][128];          // maxima of an even and an odd tile, by group
   float sums[2][128];           // the two groups' sums of weights
+  uint4 odd_scale[8][2];        // fp8 caches: a tile's K scales that are negative, or no number (see put_scales)
 };
 constexpr int kHeadBytes = 4 * 1024;
 // fp8 caches: scales of the tiles in flight, behind the head.
@@ -586,9 +587,15 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       // further back had left.
       auto put_scales = [&](int j) {
         const __half2 both = *reinterpret_cast<const __half2*>(&record);
-        // (At least 1e-30: minus infinity times it stays minus infinity.)
-        sc.k[(tj + j) & 7][ct] = fmaxf(__low2float(both) * zs, 1e-30f);
+        // Logits are hidden by minus infinity before they are scaled, so the factors
+        // are positive numbers: magnitudes, 1e-30 for zero.  Negative scales and NaN are
+        // left to the softmax, as bits of a tile's 32 tokens: it changes the sign of
+        // their logits, or makes them NaN, before it hides what a row does not see.
+        const float f = __low2float(both) * zs;
+        const uint32_t neg = __ballot_sync(0xffffffffu, f < 0.f), nan = __ballot_sync(0xffffffffu, f != f);
+        sc.k[(tj + j) & 7][ct] = fabsf(f) > 0.f ? fabsf(f) : 1e-30f;
         sc.v[(tj + j) & 7][ct] = __high2float(both);
+        if (lane == 0) reinterpret_cast<uint2*>(h.odd_scale[(tj + j) & 7])[cw] = make_uint2(neg, nan);
         __syncwarp();
         if (lane == 0) bar_arrive(&h.sc_full[(tj + j) & 7]);
         record = load(j + 1, page);
@@ -835,8 +842,13 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       // What a row does not see of keys [from, to) of a tile becomes -infinity, in
       // TMEM: the passes below stay short (with the masks unrolled into them they no
       // longer fit the instruction cache and take four times as long).
-      auto hide = [&](int t0, uint32_t bad, uint32_t s_col, int from, int to, uint32_t(&x)[32]) {
-        if (bad == 0 && t0 + kKT - 1 <= ir.first &&
+      auto hide = [&](int t0, uint32_t bad, uint32_t s_col, int from, int to, uint32_t(&x)[32], const uint4* odd_scale) {
+        uint32_t odd = 0u;
+        if constexpr (F8) {
+          const uint4 o = odd_scale[from / 64];
+          odd = o.x | o.y | o.z | o.w;
+        }
+        if (bad == 0 && odd == 0 && t0 + kKT - 1 <= ir.first &&
             !(p.window > 0 && t0 <= ir.last - p.window && t0 + kKT > p.n_sinks))
           return;
 #pragma unroll 1
@@ -845,9 +857,15 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
           const int t = t0 + col;
           uint32_t see = below(pos + 1 - t) & (~below(low - t) | below(p.n_sinks - t));
           see &= ~((((bad >> (col / 16)) & 1u) * 0xffffu) | (((bad >> (col / 16 + 1)) & 1u) * 0xffff0000u));
-          if (__all_sync(0xffffffffu, see == 0xffffffffu)) continue;
+          if (__all_sync(0xffffffffu, see == 0xffffffffu) && odd == 0) continue;
           tmem_ld32_start(s_col + (uint32_t)col, x);
           tmem_ld_wait(x);
+          if (odd != 0) {   // (fp8)
+            const uint2 o = reinterpret_cast<const uint2*>(odd_scale)[col / 32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              x[i] = o.y & (1u << i) ? 0x7fffffffu : o.x & (1u << i) ? x[i] ^ 0x80000000u : x[i];
+          }
 #pragma unroll
           for (int i = 0; i < 32; ++i) x[i] = see & (1u << i) ? x[i] : 0xff800000u;
           tmem_st32(s_col + (uint32_t)col, x);
@@ -862,11 +880,11 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
         __syncwarp();
         fence_after();
         uint32_t xa[32], xb[32];
-        hide(t0, h.bad[g & 15], s_col, c0, c0 + 64, xa);
         if constexpr (F8) {
           wait(&h.sc_full[g & 7], (uint32_t)((g >> 3) & 1), abrt);
           factor();
         }
+        hide(t0, h.bad[g & 15], s_col, c0, c0 + 64, xa, h.odd_scale[g & 7]);
         tmem_ld32_start(s_col + (uint32_t)c0, xa);
         tmem_ld_wait(xa);
         tmem_ld32_start(s_col + (uint32_t)c0 + 32, xb);

@@ -1,5 +1,5 @@
-"""Paged attention of values at the ends of their types: NaN as a GPU writes it
-and the largest f32 values.  Tolerances are derived in paged_cases."""
+"""Paged attention of values at the ends of their types: NaN as a GPU writes it,
+the largest f32 values, and fp8 scales of any sign.  Tolerances are derived in paged_cases."""
 import pytest
 import torch
 
@@ -133,3 +133,35 @@ def test_f32_infinities_of_values():
     assert (out[0, :12, 8] == float("inf")).all() and (out[0, 12:, 9] == float("-inf")).all()
     out[0, :12, 8], out[0, 12:, 9] = good[0][0, :12, 8], good[0][0, 12:, 9]
     assert torch.equal(out, good[0]) and torch.equal(lse, good[1])
+
+
+# ------------------------------------------------------------------ fp8
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 6)])
+def test_fp8_scales_of_either_sign_and_zero(D, window, sinks):
+    x = make_paged([700, 150, 3], [5, 40, 1], dtype="fp8", D=D, page=32, seed=65, poison=True)
+    g = torch.Generator().manual_seed(66)
+    pick = torch.rand(x.scale.shape, generator=g)
+    x.scale[pick < 0.2] *= -1
+    x.scale[pick > 0.9] = 0
+    out, lse = run(x, window=window, n_sinks=sinks)
+    assert_attended(out, lse, attend64(x, window, sinks))
+
+
+@pytest.mark.parametrize("bits", [0x7E00, 0xFE00, 0x7FFF, 0xFFFF])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (30, 4)])
+def test_fp8_scale_of_a_key_that_is_no_number(bits, window, sinks):
+    x = nan_case("fp8")
+    good = run(x, window=window, n_sinks=sinks)
+    wrong = torch.zeros(x.q.shape[:2], dtype=torch.bool)
+    for i, t, h in ((0, 275, 0), (1, 4990, 1), (1, 2, 0)):
+        p, s = place(x, i, t)
+        set_bits(x.scale, (p, h, s, 0), bits)
+        for j in range(x.rows[i]):
+            pos = x.lens[i] - x.rows[i] + j
+            if t <= pos and (not window or t > pos - window or t < sinks):
+                wrong[int(x.row_start[i]) + j, 12 * h:12 * h + 12] = True
+    bad = run(x, window=window, n_sinks=sinks)
+    assert wrong.any() and not wrong.all()
+    same_but(good[0], bad[0], wrong[..., None].expand_as(bad[0]))
+    same_but(good[1], bad[1], wrong)
