@@ -552,9 +552,10 @@ qsa_status qsa_lse_merge(const float* o_parts, const float* lse_parts, int32_t n
  * V likewise.  QSA_FP8_E4M3: k and v hold E4M3 codes and the (K, V) f16 scale
  * pair of (page, h, slot) is the 4-byte record at kv_scale + 4 * (page *
  * scale_page_stride + h * scale_head_stride + slot * scale_tok_stride), as for
- * segments.  A scale may be any f16: zero, negative, infinite or NaN as it stands.  f32, bf16 and fp8 caches; QSA_Q8_0 caches are not paged
- * (QSA_ERR_UNSUPPORTED: the scales of its 32-channel blocks do not factor out
- * of a row's product, which is what lets the pages be read as stored). */
+ * segments.  A scale may be any f16: zero, negative, infinite or NaN, as it stands.
+ * f32, bf16 and fp8 caches; QSA_Q8_0 caches are not paged (QSA_ERR_UNSUPPORTED:
+ * the scales of its 32-channel blocks do not factor out of a row's product, which
+ * is what lets the pages be read as stored). */
 typedef struct qsa_paged_cache {
   const void* k;               /* device, kv_dtype; written by the calls that write a cache */
   const void* v;
@@ -621,9 +622,9 @@ typedef struct qsa_paged_batch {
  *                  must not run concurrently (captured calls neither)
  * Sums and softmax statistics are 32-bit; bf16 and fp8 caches: the weights
  * exp(z - m) are rounded to bf16 for the product with V (at most 2^-8 of each,
- * independently), out once to out_dtype.  fp8: q enters as the sum of two E4M3
- * codes a value, exact from 2^-9 of its row's largest magnitude on and off by at
- * most 2^-17 of that below.  The result depends on the
+ * independently), out once to out_dtype.  fp8: q enters as the sum of two 8-bit
+ * codes a value, exact from 2^-13 of the largest magnitude of its row and head on,
+ * and off by at most 2^-21 of that below.  The result depends on the
  * lengths and the number of runs, not on timing: it is reproducible.
  * Errors: QSA_ERR_INVALID_ARG, QSA_ERR_UNSUPPORTED, QSA_ERR_MISALIGNED,
  * QSA_ERR_WORKSPACE, QSA_ERR_CUDA.  n_rows == 0 or n_seqs == 0 is a no-op.

@@ -31,11 +31,11 @@
 // not read.
 //
 // fp8 caches: the logits' product takes K's codes as they are, against Q as the
-// sum of two E4M3 codes a value (as many bytes, and as much time, as one bf16
-// product), and K's scales times the logit scale are applied to S by column; V's
-// codes become bf16 in shared memory, and V's scales go with the weights, which
-// are rounded once.  (K through bf16 as well: 351 us on a ragged batch of 16
-// sequences where this takes 169.)
+// sum of two 8-bit codes a value, E5M2 and E4M3 (as many bytes, and as much time,
+// as one bf16 product), and K's scales times the logit scale are applied to S by
+// column; V's codes become bf16 in shared memory, and V's scales go with the
+// weights, which are rounded once.  (That step, from K through bf16 as well, took a
+// ragged batch of 16 sequences from 351 to 230 us; later ones to 172.)
 //
 // Roles: warps 0-7 softmax and output, warps 8 and 10 copy K and V, warp 9 issues
 // the MMAs; bf16: warp 11 copies Q and clears V's ends; fp8: warps 12-15 write Q's
@@ -88,8 +88,10 @@ constexpr float kMoveMax = 8.f;               // log2 of the weight at which the
 
 constexpr uint32_t kIdescS = idesc_bf16(128, kKT, false, false);
 constexpr uint32_t kIdescO = idesc_bf16(128, 128, false, true);
-// kind::f8f6f4 with a 32-bit accumulator: E4M3 A and B (bits 7-12 = 0), both K-major.
-constexpr uint32_t kIdescS8 = (1u << 4) | ((uint32_t)(kKT >> 3) << 17) | (8u << 24);
+// kind::f8f6f4 with a 32-bit accumulator: A, Q's second or first codes, is E4M3 or
+// E5M2 (bits 7-9 = 0 or 1), B, K's codes, E4M3 (bits 10-12 = 0), both K-major.
+constexpr uint32_t kIdescLo8 = (1u << 4) | ((uint32_t)(kKT >> 3) << 17) | (8u << 24);
+constexpr uint32_t kIdescHi8 = kIdescLo8 | (1u << 7);
 
 __device__ int g_timeouts;
 __device__ int g_bad_pages;
@@ -170,15 +172,20 @@ __device__ __forceinline__ void mma_f8_ts(uint32_t d, uint32_t a, uint64_t b, ui
 __device__ __forceinline__ void tmem_cp_rows(uint32_t taddr, uint64_t desc) {
   asm volatile("tcgen05.cp.cta_group::1.128x256b [%0], %1;\n" ::"r"(taddr), "l"(desc) : "memory");
 }
-// Two values to E4M3, the first in the low byte, and back.
+// Two values to E4M3 or E5M2, the first in the low byte, and back.
 __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
   unsigned short r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ float2 from_e4m3x2(uint32_t two) {
+__device__ __forceinline__ uint32_t to_e5m2x2(float lo, float hi) {
+  unsigned short r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 from_e5m2x2(uint32_t two) {
   uint32_t h2;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((unsigned short)two));
+  asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h2) : "h"((unsigned short)two));
   return __half22float2(*reinterpret_cast<const __half2*>(&h2));
 }
 // A box of a page's tokens: (token of the page, 64-channel block, KV head, page).
@@ -510,13 +517,15 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
         return record;
       };
       int page = look_up(0);
-      // Q as E4M3: with the row's largest magnitude brought to [2^7, 2^8) by a power
-      // of two, a value is the sum of its nearest code and the nearest code of what
-      // that leaves.  bf16 has 8 significant bits and a code 4, so the sum is exact
-      // from 2^-9 of the row's maximum on; below, it is off by at most 2^-10, 2^-17
-      // of that maximum.  (Larger rows of Q than that against smaller channels reach
-      // the logits less than the weights' own rounding to bf16, 2^-9, reaches the
-      // output.)  A warp a row, D / 32 channels a lane, four rows in flight.
+      // Q as codes: with the row's largest magnitude brought to [2^11, 2^12) by a power
+      // of two, a value v of [2^e, 2^(e + 1)) is the sum of its nearest E5M2 code (3
+      // significant bits) and the nearest E4M3 code (4) of what that leaves, which is at
+      // most 16 of bf16's units 2^(e - 7) and so exact where the unit is a step of E4M3:
+      // 2^-9 or more, for e >= -2, values from 2^-13 of the row's largest on.  Smaller
+      // ones are off by at most half of that step, 2^-21 of the largest.  (Two E4M3
+      // codes, which have to start at 2^8, are exact from 2^-9 on only: with a channel
+      // 1,000 times the others, logits were off by up to 1e-2.)  A warp a row, D / 32
+      // channels a lane, four rows in flight.
       if (own) {
         if (it > 0) wait(&h.q_free, (uint32_t)((it - 1) & 1), abrt);
         constexpr int kCh = D / 32, kBatch = 4;
@@ -547,8 +556,8 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
             for (int i = 0; i < kCh / 2; ++i)
               most = max(most, max((x[b][i] << 16) & 0x7fff0000u, x[b][i] & 0x7fff0000u));
             most = __reduce_max_sync(0xffffffffu, most);
-            // 2^(exponent - 7), at least 2^-100: a row of smaller values keeps fewer bits.
-            const int e = max((int)(most >> 23) - 127 - 7, -100);
+            // 2^(exponent - 11), at least 2^-100: a row of smaller values keeps fewer bits.
+            const int e = max((int)(most >> 23) - 127 - 11, -100);
             const float up = __uint_as_float((uint32_t)(127 - e) << 23);
             const bool odd = most >= 0x7f800000u;   // infinity or NaN: the row's logits are NaN
             uint32_t hi[kCh / 4], lo[kCh / 4];
@@ -557,8 +566,8 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
               const float v0 = __uint_as_float(x[b][2 * i] << 16) * up, v1 = __uint_as_float(x[b][2 * i] & 0xffff0000u) * up,
                           v2 = __uint_as_float(x[b][2 * i + 1] << 16) * up,
                           v3 = __uint_as_float(x[b][2 * i + 1] & 0xffff0000u) * up;
-              const uint32_t h01 = to_e4m3x2(v0, v1), h23 = to_e4m3x2(v2, v3);
-              const float2 b01 = from_e4m3x2(h01), b23 = from_e4m3x2(h23);
+              const uint32_t h01 = to_e5m2x2(v0, v1), h23 = to_e5m2x2(v2, v3);
+              const float2 b01 = from_e5m2x2(h01), b23 = from_e5m2x2(h23);
               hi[i] = odd ? 0x7f7f7f7fu : h01 | h23 << 16;
               lo[i] = odd ? 0u : to_e4m3x2(v0 - b01.x, v1 - b01.y) | to_e4m3x2(v2 - b23.x, v3 - b23.y) << 16;
             }
@@ -750,13 +759,14 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
             const uint64_t k = k_desc + (uint32_t)(ka.slot * (kKeySlab >> 4)), q = q_desc + (F8 ? 1 : 2) * s * q_step;
 #pragma unroll
             for (int x = 0; QT && x < 8; ++x) {
-              if constexpr (F8) mma_f8_ts(d, tmem + kQCol + 8u * x, k + 2 * (x & 3), kIdescS8, x != 0 ? 1u : 0u);
+              if constexpr (F8) mma_f8_ts(d, tmem + kQCol + 8u * x, k + 2 * (x & 3), x < 4 ? kIdescHi8 : kIdescLo8, x != 0 ? 1u : 0u);
               else
                 mma_bf16_ts(d, tmem + kQCol + 8u * x, k + (x >> 2) * (kHalf >> 4) + 2 * (x & 3), kIdescS, x != 0 ? 1u : 0u);
             }
 #pragma unroll
             for (int x = 0; !QT && F8 && x < 8; ++x)   // both codes of Q's values
-              mma_f8(d, q + (x >> 2) * NS * q_step + 2 * (x & 3), k + 2 * (x & 3), kIdescS8, (s | x) != 0 ? 1u : 0u);
+              mma_f8(d, q + (x >> 2) * NS * q_step + 2 * (x & 3), k + 2 * (x & 3), x < 4 ? kIdescHi8 : kIdescLo8,
+                     (s | x) != 0 ? 1u : 0u);
 #pragma unroll
             for (int x = 0; !QT && !F8 && x < 8; ++x)
               mma_bf16(d, q + (x >> 2) * q_step + 2 * (x & 3), k + (x >> 2) * (kHalf >> 4) + 2 * (x & 3), kIdescS,

@@ -1,5 +1,8 @@
 """Paged attention of values at the ends of their types: NaN as a GPU writes it,
-the largest f32 values, and fp8 scales of any sign.  Tolerances are derived in paged_cases."""
+the largest f32 values, fp8 scales of any sign, and queries with a channel far
+above the others.  Tolerances are derived in paged_cases."""
+import dataclasses
+
 import pytest
 import torch
 
@@ -165,3 +168,28 @@ def test_fp8_scale_of_a_key_that_is_no_number(bits, window, sinks):
     assert wrong.any() and not wrong.all()
     same_but(good[0], bad[0], wrong[..., None].expand_as(bad[0]))
     same_but(good[1], bad[1], wrong)
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("times", [150, 1000, 4000])
+def test_fp8_queries_with_a_channel_far_above_the_others(D, times):
+    # The keys of that channel are smaller by as much, so that all channels matter to the logits.
+    x = make_paged([900, 130], [4, 2], dtype="fp8", D=D, page=32, seed=67)
+    x.q[:, :, 5] = x.q[:, :, 5] * times
+    x.k[:, :, :, 5] = (torch.randn(x.k.shape[:3], generator=torch.Generator().manual_seed(68)) * 150 / times).to(
+        torch.float8_e4m3fn).view(torch.uint8)
+    k, v = (c.view(torch.float8_e4m3fn).double() * x.scale[..., w:w + 1].double() for c, w in ((x.k, 0), (x.v, 1)))
+    plain = dataclasses.replace(x, k=k, v=v, scale=None)
+    ref, l, ref_tol, l_tol = attend64(plain)       # (the bounds of queries that are not split)
+    wabs = attend64(dataclasses.replace(plain, v=v.abs()))[0]
+    # Q is the sum of two codes, exact from 2^-13 of its row's largest value qmax on and off by dq <= 2^-21 qmax
+    # below: logits by up to max_t scale * sum_d dq_d |k_td|, weights by twice that (weight and maximum).
+    qmax = x.q.double().abs().amax(-1, keepdim=True)
+    dq = torch.where(x.q.double().abs() < 2.0 ** -13 * qmax, torch.minimum(x.q.double().abs(), 2.0 ** -21 * qmax), 0.0)
+    for i, n in enumerate(x.lens):
+        rows, K = slice(int(x.row_start[i]), int(x.row_start[i + 1])), plain.seq_kv(i)[0]
+        lost = torch.einsum("rhgd,htd->rhgt", dq[rows].view(-1, 2, 12, D), K.abs()).amax(-1).flatten(1) * D ** -0.5
+        l_tol[rows] += 2 * lost
+        ref_tol[rows] += 4 * lost[..., None] * wabs[rows]
+    out, lse = run(x)
+    assert_attended(out, lse, (ref, l, ref_tol, l_tol))
