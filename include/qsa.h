@@ -683,7 +683,16 @@ typedef struct qsa_page_pool {
  *
  * qsa_pages_extend   lens[seqs[i]] += n_new[i], with new pages for tokens past
  *                    the last one.  Not served: n_new[i] < 0, more tokens than
- *                    table_ld pages hold.
+ *                    table_ld pages hold.  A step that follows must not take
+ *                    lens for a place that was not served: its rows would sit at
+ *                    the place's last tokens, and an append would write over
+ *                    them, in shared pages too.
+ * qsa_pages_extend_step  the same, and the lengths to give the step (the lens of
+ *                    its qsa_paged_batch): step_lens[s], device [n_seqs], becomes
+ *                    lens[s] as the call leaves it, and 0 for a place of which a
+ *                    request was not served.  Rows of a sequence of no tokens are
+ *                    written nowhere and see nothing, so the step leaves such a
+ *                    place as it is.  n == 0 copies the lengths.
  * qsa_pages_fork     dst[i] (an empty place) becomes a copy of src[i]'s first
  *                    min(keep[i], lens[src[i]]) tokens (keep NULL: all): full
  *                    pages are shared, a last page that is not full is copied
@@ -718,6 +727,8 @@ size_t qsa_pages_workspace_size(const qsa_page_pool* pool);
 
 qsa_status qsa_pages_extend(const qsa_page_pool* pool, const int32_t* seqs, const int32_t* n_new, int32_t n,
                             void* stream);
+qsa_status qsa_pages_extend_step(const qsa_page_pool* pool, const int32_t* seqs, const int32_t* n_new, int32_t n,
+                                 int32_t* step_lens, void* stream);
 qsa_status qsa_pages_fork(const qsa_page_pool* pool, const qsa_paged_cache* caches, int32_t n_caches,
                           const qsa_attn_config* cfg, const int32_t* src, const int32_t* dst, const int32_t* keep,
                           int32_t n, void* workspace, size_t workspace_bytes, void* stream);

@@ -72,7 +72,7 @@ EXPORTS = ("qsa_status_string", "qsa_last_error", "qsa_version", "qsa_pool_index
            "qsa_arena_base", "qsa_arena_mapped", "qsa_arena_reserved", "qsa_arena_granularity", "qsa_arena_destroy",
            "qsa_check_device_status", "qsa_selftest_wait_timeout", "qsa_pool_score_blocks",
            "qsa_append_score_blocks", "qsa_paged_attn_workspace_size", "qsa_paged_attn", "qsa_paged_append",
-           "qsa_pages_workspace_size", "qsa_pages_extend", "qsa_pages_fork", "qsa_pages_free", "qsa_pages_compact",
+           "qsa_pages_workspace_size", "qsa_pages_extend", "qsa_pages_extend_step", "qsa_pages_fork", "qsa_pages_free", "qsa_pages_compact",
            "qsa_pages_copy")
 NOALLOC_SCRATCH_BYTES = 4 << 20
 

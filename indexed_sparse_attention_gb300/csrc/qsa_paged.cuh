@@ -97,7 +97,7 @@ struct PageCaches {
   int32_t row_shift;         // log2 of the 16-byte pieces of a row
 };
 cudaError_t launch_pages_extend(const qsa_page_pool& pool, const int32_t* seqs, const int32_t* n_new, int n,
-                                cudaStream_t st);
+                                int32_t* step_lens, cudaStream_t st);
 cudaError_t launch_pages_fork_plan(const qsa_page_pool& pool, const int32_t* src, const int32_t* dst,
                                    const int32_t* keep, int n, void* ws, cudaStream_t st);
 cudaError_t launch_pages_fork(const qsa_page_pool& pool, const PageCaches& caches, bool rows, int n, const void* ws,

@@ -298,17 +298,29 @@ QSA_API size_t qsa_pages_workspace_size(const qsa_page_pool* pool) {
   return check_pool(pool, "qsa_pages_workspace_size") == QSA_OK ? pages_workspace_bytes(*pool) : 0;
 }
 
-QSA_API qsa_status qsa_pages_extend(const qsa_page_pool* pool, const int32_t* seqs, const int32_t* n_new, int32_t n,
-                                    void* stream) {
-  const NvtxRange nvtx_range("qsa_pages_extend");
-  const char* fn = "qsa_pages_extend";
+static qsa_status extend(const qsa_page_pool* pool, const int32_t* seqs, const int32_t* n_new, int32_t n,
+                         int32_t* step_lens, void* stream, const char* fn) {
   qsa_status s = check_pool(pool, fn);
   if (s != QSA_OK) return s;
   if ((s = check_requests(seqs, n, fn)) != QSA_OK) return s;
-  if (n == 0) return ok();
-  if (!n_new) return fail(QSA_ERR_INVALID_ARG, "%s: null n_new", fn);
-  const cudaError_t e = launch_pages_extend(*pool, seqs, n_new, n, as_stream(stream));
+  if (n > 0 && !n_new) return fail(QSA_ERR_INVALID_ARG, "%s: null n_new", fn);
+  if (n == 0 && !step_lens) return ok();
+  const cudaError_t e = launch_pages_extend(*pool, seqs, n_new, n, step_lens, as_stream(stream));
   return e == cudaSuccess ? ok() : cuda_fail(e, fn);
+}
+
+QSA_API qsa_status qsa_pages_extend(const qsa_page_pool* pool, const int32_t* seqs, const int32_t* n_new, int32_t n,
+                                    void* stream) {
+  const NvtxRange nvtx_range("qsa_pages_extend");
+  return extend(pool, seqs, n_new, n, nullptr, stream, "qsa_pages_extend");
+}
+
+QSA_API qsa_status qsa_pages_extend_step(const qsa_page_pool* pool, const int32_t* seqs, const int32_t* n_new,
+                                         int32_t n, int32_t* step_lens, void* stream) {
+  const NvtxRange nvtx_range("qsa_pages_extend_step");
+  const char* fn = "qsa_pages_extend_step";
+  if (!step_lens) return fail(QSA_ERR_INVALID_ARG, "%s: null step_lens", fn);
+  return extend(pool, seqs, n_new, n, step_lens, stream, fn);
 }
 
 QSA_API qsa_status qsa_pages_fork(const qsa_page_pool* pool, const qsa_paged_cache* caches, int32_t n_caches,

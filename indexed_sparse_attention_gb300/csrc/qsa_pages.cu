@@ -149,7 +149,7 @@ __device__ __forceinline__ int request_of(const int* off_s, int n, int r) {
 
 // ------------------------------------------------------------------ extend
 __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const qsa_page_pool pool, const int32_t* seqs,
-                                                              const int32_t* n_new, int n) {
+                                                              const int32_t* n_new, int n, int32_t* step_lens) {
   __shared__ __align__(16) int list_s[QSA_MAX_PAGE_REQUESTS], off_s[QSA_MAX_PAGE_REQUESTS + 1], have_s[QSA_MAX_PAGE_REQUESTS];
   __shared__ int scan_s[32];
   grid_dependency_sync();
@@ -174,10 +174,17 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const qsa_page_poo
     pool.table[list_s[q] * pool.table_ld + have_s[q] + (rank - off_s[q])] = page;
     pool.refs[page] = 1;
   });
+  const bool ok = i >= n || (valid && served);
   if (i < n) {
-    if (valid && served) pool.lens[list_s[i]] = len + add;
+    if (ok) pool.lens[list_s[i]] = len + add;
     else atomicAdd(&g_unserved, 1);
   }
+  if (!step_lens) return;
+  // The step's lengths: no tokens for a place with a request that was not served.
+  __syncthreads();
+  for (int s = i; s < pool.n_seqs; s += kPlanThreads) step_lens[s] = __ldcg(pool.lens + s);
+  __syncthreads();
+  if (!ok && (uint32_t)list_s[i] < (uint32_t)pool.n_seqs) step_lens[list_s[i]] = 0;
 }
 
 // ------------------------------------------------------------------ fork
@@ -478,8 +485,8 @@ size_t pages_workspace_bytes(const qsa_page_pool& pool) {
 }
 
 cudaError_t launch_pages_extend(const qsa_page_pool& pool, const int32_t* seqs, const int32_t* n_new, int n,
-                                cudaStream_t st) {
-  return launch_kernel(extend_kernel, dim3(1), dim3(kPlanThreads), 0, st, 0u, pool, seqs, n_new, n);
+                                int32_t* step_lens, cudaStream_t st) {
+  return launch_kernel(extend_kernel, dim3(1), dim3(kPlanThreads), 0, st, 0u, pool, seqs, n_new, n, step_lens);
 }
 
 cudaError_t launch_pages_fork_plan(const qsa_page_pool& pool, const int32_t* src, const int32_t* dst,

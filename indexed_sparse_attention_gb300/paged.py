@@ -2,7 +2,8 @@
 (include/qsa.h, "Paged K/V caches").  Argument marshalling only.
 
     pages = PagePool(table, lens, refs, caches)          # who holds which page
-    pages.extend(seqs, n_new)                            # room for the step's tokens
+    batch = PagedBatch(pages.table, pages.step_lens, row_start, n_rows=R, max_rows=M)
+    pages.extend(seqs, n_new)                            # room for the step's tokens, and its lengths
     step = PagedStep(caches[layer], batch, q, window=W, n_sinks=S)
     out, lse = step.run(k_new, v_new)                    # append, then attend
 """
@@ -52,13 +53,14 @@ def declare(L: ctypes.CDLL):
     L.qsa_pages_workspace_size.argtypes = [poolp]
     L.qsa_pages_workspace_size.restype = sz
     L.qsa_pages_extend.argtypes = [poolp, vp, vp, i32, vp]
+    L.qsa_pages_extend_step.argtypes = [poolp, vp, vp, i32, vp, vp]
     L.qsa_pages_fork.argtypes = [poolp, cachep, i32, cfgp, vp, vp, vp, i32, vp, sz, vp]
     L.qsa_pages_free.argtypes = [poolp, vp, vp, i32, vp]
     L.qsa_pages_compact.argtypes = [poolp, cachep, i32, cfgp, vp, vp, sz, vp]
     L.qsa_pages_copy.argtypes = [cachep, i32, cfgp, vp, vp, i32, vp]
     for name in ("attn", "append"):
         getattr(L, f"qsa_paged_{name}").restype = i32
-    for name in ("extend", "fork", "free", "compact", "copy"):
+    for name in ("extend", "extend_step", "fork", "free", "compact", "copy"):
         getattr(L, f"qsa_pages_{name}").restype = i32
 
 
@@ -281,7 +283,12 @@ class PagePool:
     """Who holds which page, on the GPU: table [places, pages] (-1: none), lens
     [places] and refs [n_pages] are int32 tensors, and caches are the layers
     whose pages move together.  Every call is asynchronous; requests that could
-    not be served are counted (check_device_status) and change nothing."""
+    not be served are counted (check_device_status) and change nothing.
+
+    step_lens [places] are the lengths for the step that follows an extend, the
+    lens of its PagedBatch: those of the pool, and 0 for a place that did not get
+    its room, whose rows are then written nowhere and see nothing.  (With the
+    pool's own lens such rows would be written over its last tokens.)"""
 
     def __init__(self, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, caches: Sequence[PagedCache] = (),
                  page_tokens: int | None = None):
@@ -299,6 +306,7 @@ class PagePool:
             raise ValueError("the pool's arrays are on another device than a cache")
         self.table, self.lens, self.refs, self.caches = table, lens, refs, list(caches)
         self.page_tokens = int(page_tokens)
+        self.step_lens = lens.clone()
         self._c = _cache_array(self.caches)
         self.desc = PagePoolDesc(table.data_ptr(), int(table.shape[1]), lens.data_ptr(), refs.data_ptr(),
                                  int(table.shape[0]), int(refs.numel()), self.page_tokens)
@@ -322,9 +330,11 @@ class PagePool:
         return a.numel()
 
     def extend(self, seqs: torch.Tensor, n_new: torch.Tensor, stream=None):
-        """lens[seqs] += n_new, with the lowest free pages for what they lack."""
+        """lens[seqs] += n_new, with the lowest free pages for what they lack; step_lens
+        become the lengths of the step."""
         n = self._pair("seqs", seqs, "n_new", n_new)
-        _call("qsa_pages_extend", self.table.device, stream, self.byref, seqs.data_ptr(), n_new.data_ptr(), n)
+        _call("qsa_pages_extend_step", self.table.device, stream, self.byref, seqs.data_ptr(), n_new.data_ptr(), n,
+              self.step_lens.data_ptr())
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor, keep: torch.Tensor | None = None, stream=None):
         """The empty places dst become copies of src (their first keep tokens):
