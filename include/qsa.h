@@ -678,8 +678,9 @@ typedef struct qsa_page_pool {
  * always the free page with the lowest number, in list order, so results are
  * reproducible.  A request that cannot be served changes nothing and is
  * counted by qsa_check_device_status: a place outside [0, n_seqs), a place
- * listed before, too few free pages left for it after those before it, and
- * what each call adds.  n == 0 is a no-op.
+ * listed before, too few free pages left for it after what those before it ask
+ * for (also of one that is not served: put a request that may be too large last,
+ * or in a call of its own), and what each call adds.  n == 0 is a no-op.
  *
  * qsa_pages_extend   lens[seqs[i]] += n_new[i], with new pages for tokens past
  *                    the last one.  Not served: n_new[i] < 0, more tokens than

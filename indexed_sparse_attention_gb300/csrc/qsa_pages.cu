@@ -22,7 +22,11 @@ constexpr int kCopyThreads = 256;
 
 __device__ int g_unserved;   // requests that could not be served, page numbers outside a pool
 
-// Sum of one value per thread over the CTA, and the exclusive prefix.
+// Sum of one value per thread over the CTA, and the exclusive prefix.  Values are
+// 0 .. 2^24 (pages, or those of a table row), and sums of 2^29 and more need not be
+// exact, only no smaller: 1,024 requests may want 2^34 pages together, of which none
+// behind the pool's 2^24 exist.
+constexpr int kManyPages = 1 << 29;
 __device__ __forceinline__ int scan(int v, int* smem, int& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int inc = v;
@@ -38,7 +42,7 @@ __device__ __forceinline__ int scan(int v, int* smem, int& total) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int up = __shfl_up_sync(0xffffffffu, w, o);
-    if (lane >= o) w += up;
+    if (lane >= o) w = min(w + up, kManyPages);
   }
   total = __shfl_sync(0xffffffffu, w, 31);
   const int before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);

@@ -1,4 +1,5 @@
-"""The keeping of pages at its ends: pools that run out inside a serving step."""
+"""The keeping of pages at its ends: pools that run out inside a serving step, and
+requests for more pages than 32 bits count."""
 import pytest
 import torch
 
@@ -130,4 +131,25 @@ def test_captured_steps_until_the_pool_is_full():
     out, lse = torch.empty(2, 4, D, device=dev()), torch.empty(2, 4, device=dev())
     qsa.paged_attn(pool.caches[0], batch, q.to(dev()), out, lse)
     assert_attended(out, lse, attend64(plain))
+    assert qsa.check_device_status()[0] == qsa.ERR_DEVICE_CHECK
+
+
+# ------------------------------------------------------------------ requests of any size
+def test_requests_for_more_pages_than_32_bits_count():
+    # 140 places that want 2^24 pages each: 2.3e9, of which the pool has 100.
+    ld, places, n_pages = 1 << 24, 143, 100
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 10 GB")
+    table = torch.full((places, ld), -1, dtype=torch.int32, device=dev())
+    pool = qsa.PagePool(table, _ints([0] * places), _ints([0] * n_pages), page_tokens=16)
+    pool.extend(_ints(list(range(places))), _ints([33] + [1 << 28] * 140 + [16, 0]))
+    assert pool.lens.tolist() == [33] + [0] * (places - 1)      # (the others are behind requests that take all)
+    assert pool.step_lens.tolist() == pool.lens.tolist()
+    assert table[0, :3].tolist() == [0, 1, 2] and pool.refs.tolist() == [1] * 3 + [0] * (n_pages - 3)
+    assert int((table.view(-1)[3:] != -1).sum()) == 0
+    status, why = qsa.check_device_status()
+    assert status == qsa.ERR_DEVICE_CHECK and "141 page requests" in why
+    pool.extend(_ints([1, 142]), _ints([16 * 97, 5]))           # all that is left, then one more
+    assert pool.lens.tolist() == [33, 16 * 97] + [0] * (places - 2)
+    assert table[1, :97].tolist() == list(range(3, 100))
     assert qsa.check_device_status()[0] == qsa.ERR_DEVICE_CHECK
