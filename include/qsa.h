@@ -710,7 +710,8 @@ typedef struct qsa_page_pool {
  *                    0 .. used - 1 (whole pages, in all n_caches caches; in
  *                    ascending order on both sides), and writes `used` to
  *                    *n_used (device, may be NULL): what lies behind them can
- *                    be given back.
+ *                    be given back.  A table entry whose page counts no user
+ *                    stays as it is.
  * qsa_pages_copy     copies page src[i] to page dst[i], whole, in all n_caches
  *                    caches, for device lists of n (any number) pages.  The
  *                    destinations are distinct and none of them is a source;

@@ -422,6 +422,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const qsa_pa
   for (int k = sl.lo; k < sl.hi; ++k) {
     const bool in_use = __ldcg(pool.refs + k) > 0;
     if (k >= used && in_use) src[u - low_s] = k;
+    if (k >= used && !in_use) to[k] = k;   // (a table that names a page nobody counts keeps it)
     if (k < used && !in_use) dst[k - u] = k;
     u += in_use;
   }

@@ -1,5 +1,5 @@
-"""The keeping of pages at its ends: pools that run out inside a serving step, and
-requests for more pages than 32 bits count."""
+"""The keeping of pages at its ends: pools that run out inside a serving step,
+requests for more pages than 32 bits count, and tables that name pages nobody counts."""
 import pytest
 import torch
 
@@ -153,3 +153,19 @@ def test_requests_for_more_pages_than_32_bits_count():
     assert pool.lens.tolist() == [33, 16 * 97] + [0] * (places - 2)
     assert table[1, :97].tolist() == list(range(3, 100))
     assert qsa.check_device_status()[0] == qsa.ERR_DEVICE_CHECK
+
+
+# ------------------------------------------------------------------ compact
+def test_compact_keeps_entries_of_pages_that_nobody_counts():
+    k, v = (torch.randn(12, 2, 16, 128, device=dev()).bfloat16() for _ in range(2))
+    pool = qsa.PagePool.empty(3, 4, [qsa.PagedCache(k, v)])
+    pool.table.copy_(torch.tensor([[9, 3, -1, -1], [10, 11, 40, -1], [-1] * 4], dtype=torch.int32))
+    pool.lens.copy_(torch.tensor([20, 40, 0], dtype=torch.int32))
+    pool.refs[9] = pool.refs[3] = pool.refs[11] = 1             # nobody counts page 10, and page 40 does not exist
+    was = k.clone()
+    for junk in (0x5A, 0xFF, 0x00):                             # (whatever the workspace held before)
+        pool.ws.fill_(junk)
+        pool.compact()
+        assert pool.table.tolist() == [[1, 0, -1, -1], [10, 2, 40, -1], [-1] * 4]      # pages 3, 9 and 11 to 0, 1 and 2
+        assert pool.refs.tolist() == [1] * 3 + [0] * 9
+        assert all(torch.equal(k[to], was[page]) for to, page in ((0, 3), (1, 9), (2, 11)))
