@@ -718,7 +718,8 @@ typedef struct qsa_page_pool {
  *                    numbers outside [0, n_pages) are skipped and counted.
  *
  *   caches           host array of n_caches <= QSA_MAX_CACHES caches, each with the
- *                    pool's page_tokens and at least its n_pages pages
+ *                    pool's page_tokens and at least its n_pages pages; K and V of
+ *                    a page below 32 GB each
  *   cfg              n_kv_heads, head_dim, kv_dtype of all of them
  *   workspace        device scratch of qsa_pages_workspace_size bytes; as for
  *                    the other calls

@@ -248,6 +248,10 @@ qsa_status check_caches(const qsa_page_pool* pool, const qsa_paged_cache* caches
   if (s != QSA_OK) return s;
   for (int i = 0; i < n_caches; ++i) {
     if ((s = check_cache(caches + i, cfg, fn)) != QSA_OK) return s;
+    // The copies count a page's 16-byte pieces, a batch of them ahead, in 32 bits.
+    const int64_t bytes = (int64_t)caches[i].page_tokens * cfg->n_kv_heads * cfg->head_dim * (int64_t)dtype_size(cfg->kv_dtype);
+    if (bytes / 16 > INT32_MAX - 4096)
+      return fail(QSA_ERR_UNSUPPORTED, "%s: cache %d has pages of %lld bytes of K (below 32 GB)", fn, i, (long long)bytes);
     if (caches[i].page_tokens != (pool ? pool->page_tokens : caches[0].page_tokens))
       return fail(QSA_ERR_INVALID_ARG, "%s: cache %d has pages of another size", fn, i);
     if (pool ? caches[i].n_pages < pool->n_pages : caches[i].n_pages != caches[0].n_pages)

@@ -22,3 +22,16 @@ def test_extend_step_checks(L):
     assert call(seqs=None) == 1 and call(new=None) == 1 and call(n=-1) == 1 and call(n=1025) == 2
     assert call(p=None) == 1 and call(p=paged.PagePoolDesc(FAKE, 8, FAKE, FAKE, 4, 10, 20)) == 2
     assert "qsa_pages_extend_step" in L.qsa_last_error().decode()
+
+
+def test_pages_of_more_pieces_than_32_bits_count(L):
+    # 1,024 tokens of 32,768 heads of 1,024 bytes: 2^31 pieces of 16 bytes.
+    def calls(heads):
+        cache = paged.PagedCacheDesc(FAKE, FAKE, 1 << 36, 256, 1 << 25, None, 0, 0, 0, 10, 1024)
+        cfg = qsa.AttnConfig(heads, heads, 256, qsa.F32, qsa.F32, qsa.F32, 0.0, 0)
+        pool = paged.PagePoolDesc(FAKE, 8, FAKE, FAKE, 4, 10, 1024)
+        return (L.qsa_pages_fork(pool, cache, 1, cfg, FAKE, FAKE, None, 1, None, 0, None),
+                L.qsa_pages_compact(pool, cache, 1, cfg, None, None, 0, None),
+                L.qsa_pages_copy(cache, 1, cfg, None, FAKE, 1, None))
+    assert calls(32768) == (2, 2, 2) and calls(65535) == (2, 2, 2)
+    assert calls(32767) == (4, 4, 1)                            # only the workspace, or the list, is missing
