@@ -715,7 +715,8 @@ typedef struct qsa_page_pool {
  * qsa_pages_copy     copies page src[i] to page dst[i], whole, in all n_caches
  *                    caches, for device lists of n (any number) pages.  The
  *                    destinations are distinct and none of them is a source;
- *                    numbers outside [0, n_pages) are skipped and counted.
+ *                    numbers outside [0, n_pages) of any of the caches are
+ *                    skipped and counted.
  *
  *   caches           host array of n_caches <= QSA_MAX_CACHES caches, each with the
  *                    pool's page_tokens and at least its n_pages pages; K and V of

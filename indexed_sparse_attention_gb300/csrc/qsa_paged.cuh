@@ -92,7 +92,7 @@ struct PageCache {
 struct PageCaches {
   PageCache c[kPageCaches];
   int32_t n;
-  int32_t n_pages;           // of every cache
+  int32_t n_pages;           // that every cache of the call has
   int32_t n_kv_heads, page_shift;
   int32_t row_shift;         // log2 of the 16-byte pieces of a row
 };

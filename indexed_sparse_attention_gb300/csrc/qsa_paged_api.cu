@@ -254,7 +254,7 @@ qsa_status check_caches(const qsa_page_pool* pool, const qsa_paged_cache* caches
       return fail(QSA_ERR_UNSUPPORTED, "%s: cache %d has pages of %lld bytes of K (below 32 GB)", fn, i, (long long)bytes);
     if (caches[i].page_tokens != (pool ? pool->page_tokens : caches[0].page_tokens))
       return fail(QSA_ERR_INVALID_ARG, "%s: cache %d has pages of another size", fn, i);
-    if (pool ? caches[i].n_pages < pool->n_pages : caches[i].n_pages != caches[0].n_pages)
+    if (pool && caches[i].n_pages < pool->n_pages)
       return fail(QSA_ERR_INVALID_ARG, "%s: cache %d has %d pages", fn, i, caches[i].n_pages);
   }
   return QSA_OK;
@@ -289,7 +289,8 @@ PageCaches caches_of(const qsa_paged_cache* caches, int n_caches, const qsa_attn
                          4 * c.scale_head_stride,
                          4 * c.scale_tok_stride};
   }
-  out.n_pages = caches[at].n_pages;
+  out.n_pages = caches[0].n_pages;   // what all of the call's caches have
+  for (int i = 1; i < n_caches; ++i) out.n_pages = std::min(out.n_pages, caches[i].n_pages);
   out.n_kv_heads = cfg->n_kv_heads;
   out.page_shift = log2_of(caches[at].page_tokens);
   out.row_shift = log2_of(cfg->head_dim * es / 16);

@@ -169,3 +169,19 @@ def test_compact_keeps_entries_of_pages_that_nobody_counts():
         assert pool.table.tolist() == [[1, 0, -1, -1], [10, 2, 40, -1], [-1] * 4]      # pages 3, 9 and 11 to 0, 1 and 2
         assert pool.refs.tolist() == [1] * 3 + [0] * 9
         assert all(torch.equal(k[to], was[page]) for to, page in ((0, 3), (1, 9), (2, 11)))
+
+
+# ------------------------------------------------------------------ copy
+def test_copy_in_caches_of_unequal_numbers_of_pages():
+    # A pool has the pages that all of its caches have; 35 of them take two launches.
+    n = [8, 6] + [7] * 33
+    caches = [qsa.PagedCache(*(torch.randn(m, 2, 16, 128, device=dev()).bfloat16() for _ in range(2))) for m in n]
+    pool = qsa.PagePool.empty(2, 2, caches)
+    assert pool.refs.numel() == 6
+    want = [(c.k.clone(), c.v.clone()) for c in caches]
+    pool.copy(_ints([1, 6, 5]), _ints([2, 3, 7]))               # pages 6 and 7 are not in every cache
+    for c, (k, v) in zip(caches, want):
+        k[2], v[2] = k[1], v[1]
+        assert torch.equal(c.k, k) and torch.equal(c.v, v)
+    status, why = qsa.check_device_status()
+    assert status == qsa.ERR_DEVICE_CHECK and "page requests" in why
