@@ -80,6 +80,8 @@ def _raw_stream(stream, device) -> int:
 def _call(name: str, device, stream, *args):
     """One library call with the tensors' device as the current one (the library
     launches there), on `stream` or that device's current stream."""
+    if device.type != "cuda":
+        raise ValueError(f"{name}: the tensors are on {device}, not on a GPU")
     fn = getattr(lib(), name)
     if device.index == torch.cuda.current_device():
         status = fn(*args, _raw_stream(stream, device))
@@ -197,6 +199,10 @@ def paged_attn_workspace_size(batch: PagedBatch, cfg: AttnConfig) -> int:
         return size()
 
 
+#: What a configuration says of the tensors of its call.
+_CALL_FIELDS = ("n_q_heads", "n_kv_heads", "head_dim", "q_dtype", "kv_dtype", "out_dtype")
+
+
 def paged_attn(cache: PagedCache, batch: PagedBatch, q: torch.Tensor, out: torch.Tensor,
                lse: torch.Tensor | None = None, *, window: int = 0, n_sinks: int = 0, scale: float = 0.0,
                n_splits: int = 0, workspace: torch.Tensor | None = None, stream=None, cfg: AttnConfig | None = None):
@@ -209,10 +215,16 @@ def paged_attn(cache: PagedCache, batch: PagedBatch, q: torch.Tensor, out: torch
         _check_rows("lse", lse, q.shape[:2], torch.float32, cache.device)
     if not (out.is_contiguous() and (lse is None or lse.is_contiguous())):
         raise ValueError("out and lse must be contiguous")
+    own = cache.config(q.shape[1], out.dtype, scale, n_splits)
     if cfg is None:
-        cfg = cache.config(q.shape[1], out.dtype, scale, n_splits)
+        cfg = own
+    elif any(getattr(cfg, f) != getattr(own, f) for f in _CALL_FIELDS):
+        raise ValueError("cfg describes another call than the tensors: " + ", ".join(
+            f"{f}={getattr(cfg, f)} for {getattr(own, f)}" for f in _CALL_FIELDS if getattr(cfg, f) != getattr(own, f)))
     if workspace is None:
         workspace = _scratch(paged_attn_workspace_size(batch, cfg), cache.device, stream)
+    elif workspace.device != cache.device or not workspace.is_contiguous() or workspace.dtype != torch.uint8:
+        raise ValueError(f"workspace must be contiguous uint8 on {cache.device}")
     _call("qsa_paged_attn", cache.device, stream, cache.byref, batch.byref, ctypes.byref(cfg), int(window),
           int(n_sinks), q.data_ptr(), out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel())
 

@@ -1,6 +1,7 @@
 """Refusals of the paged calls, without a GPU (device pointers are fake aligned
 addresses)."""
 import pytest
+import torch
 
 import indexed_sparse_attention_gb300 as qsa
 from indexed_sparse_attention_gb300 import build as qsa_build
@@ -35,3 +36,35 @@ def test_pages_of_more_pieces_than_32_bits_count(L):
                 L.qsa_pages_copy(cache, 1, cfg, None, FAKE, 1, None))
     assert calls(32768) == (2, 2, 2) and calls(65535) == (2, 2, 2)
     assert calls(32767) == (4, 4, 1)                            # only the workspace, or the list, is missing
+
+
+def test_configurations_and_workspaces_of_other_calls():
+    k = torch.zeros(4, 2, 16, 128, dtype=torch.bfloat16)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    cache, batch = qsa.PagedCache(k, k.clone()), qsa.PagedBatch(i32(2, 4), i32(2), i32(3), n_rows=2)
+    q = torch.zeros(2, 24, 128, dtype=torch.bfloat16)
+    for cfg in (cache.config(32, q.dtype), cache.config(24, torch.float32),
+                qsa.PagedCache(k.float(), k.float()).config(24, q.dtype),
+                qsa.PagedCache(k[:, :1], k[:, :1]).config(24, q.dtype),
+                qsa.PagedCache(k.view(4, 2, 8, 256), k.view(4, 2, 8, 256)).config(24, q.dtype)):
+        with pytest.raises(ValueError, match="another call"):
+            qsa.paged_attn(cache, batch, q, q.clone(), cfg=cfg)
+    for ws in (torch.empty(1 << 20, dtype=torch.uint8, device="meta"), torch.empty(1 << 20),
+               torch.empty(1 << 20, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            qsa.paged_attn(cache, batch, q, q.clone(), workspace=ws)
+
+
+def test_tensors_that_are_not_on_a_gpu():
+    k = torch.zeros(4, 2, 16, 128, dtype=torch.bfloat16)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    cache, batch = qsa.PagedCache(k, k.clone()), qsa.PagedBatch(i32(2, 4), i32(2), i32(3), n_rows=2)
+    q, new = torch.zeros(2, 24, 128, dtype=torch.bfloat16), torch.zeros(2, 2, 128, dtype=torch.bfloat16)
+    pool = qsa.PagePool.empty(2, 4, [cache])
+    for call in (lambda: qsa.paged_attn(cache, batch, q, q.clone(), workspace=torch.empty(64, dtype=torch.uint8), stream=7),
+                 lambda: qsa.paged_append(cache, batch, new, new, stream=7),
+                 lambda: pool.extend(i32(1), i32(1), stream=7), lambda: pool.fork(i32(1), i32(1), stream=7),
+                 lambda: pool.free(i32(1), stream=7), lambda: pool.compact(stream=7),
+                 lambda: pool.copy(i32(1), i32(1), stream=7)):
+        with pytest.raises(ValueError, match="not on a GPU"):
+            call()
