@@ -266,7 +266,8 @@ qsa_status qsa_pool_index_keys(const void* idx_keys, qsa_dtype idx_dtype, int64_
  *                  state is quantized, and each (K or V, head, token) row is
  *                  then written in it: QSA_FP8_E4M3 -- scale = f16(f32(amax /
  *                  448)), codes = the E4M3 values nearest to f32(x / scale),
- *                  ties to even, saturated at 448; QSA_Q8_0 -- per block of
+ *                  ties to even, saturated at 448 (NaN: a NaN code, and no
+ *                  part of amax); QSA_Q8_0 -- per block of
  *                  32, scale = f16(f32(amax / 127)), codes = the integers
  *                  nearest to f32(x / scale), halves away from zero, within
  *                  +-127 (0 codes where a scale is 0)
@@ -639,7 +640,7 @@ qsa_status qsa_paged_attn(const qsa_paged_cache* cache, const qsa_paged_batch* b
  * Writing new tokens into their pages: row r at position p of sequence i (as
  * above: the lengths already count the new tokens) goes to slot p mod
  * page_tokens of page table[i][p / page_tokens], copied, or quantized exactly
- * as qsa_append_tokens does (bf16 rows into an fp8 cache).
+ * as qsa_append_tokens does (bf16 rows into an fp8 cache; NaN stays NaN).
  *   cfg            n_kv_heads, head_dim, kv_dtype (the other fields are checked
  *                  as for qsa_paged_attn)
  *   k_new, v_new   device, element (r, h, d) at r * row_stride + h * head_stride

@@ -34,14 +34,6 @@ __device__ __forceinline__ float4 load_key4(const void* base, int dtype, int64_t
   return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
 }
 
-// Two binary32 values -> two E4M3 codes (x0 in the low byte), nearest with
-// ties to even, saturated at +-448.
-__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float x0, float x1) {
-  unsigned short r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(x1), "f"(x0));
-  return r;
-}
-
 __device__ __forceinline__ const AppendSeg* seg_of(const AppendParams& p, int64_t t) {
   for (int s = 0; s < p.n_segs; ++s)
     if (t >= p.seg[s].first && t < p.seg[s].first + p.seg[s].n) return &p.seg[s];
@@ -89,10 +81,10 @@ __device__ __forceinline__ void quantize_row(const AppendParams& p, int64_t row,
   uint32_t c[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    if (sc == 0.f) {
+    if (p.kvq == 1) {
+      c[k] = e4m3_codes(x[2 * k], x[2 * k + 1], sc);
+    } else if (sc == 0.f) {
       c[k] = 0u;
-    } else if (p.kvq == 1) {
-      c[k] = f32x2_to_e4m3x2(__fdiv_rn(x[2 * k], sc), __fdiv_rn(x[2 * k + 1], sc));
     } else {
       const float a = fminf(127.f, fmaxf(-127.f, roundf(__fdiv_rn(x[2 * k], sc))));
       const float b = fminf(127.f, fmaxf(-127.f, roundf(__fdiv_rn(x[2 * k + 1], sc))));

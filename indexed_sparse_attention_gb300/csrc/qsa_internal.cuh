@@ -367,6 +367,21 @@ __device__ __forceinline__ void grid_dependency_release() {
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 }
 
+// E4M3 codes (the first in the low byte) of two values of a row with scale sc: the
+// nearest to f32(x / sc), ties to even, saturated at +-448.  A row whose scale rounds
+// to 0 stores zero codes; NaN stays NaN in each row, also in one that is all NaN, whose
+// largest magnitude counts as 0.
+__device__ __forceinline__ uint32_t e4m3_codes(float x0, float x1, float sc) {
+  if (sc == 0.f) {
+    x0 = x0 == x0 ? 0.f : x0;
+    x1 = x1 == x1 ? 0.f : x1;
+    sc = 1.f;
+  }
+  unsigned short r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(__fdiv_rn(x1, sc)), "f"(__fdiv_rn(x0, sc)));
+  return r;
+}
+
 // Asynchronous global -> shared copies (cp.async): a copy whose valid is
 // false writes zeros and reads nothing; wait_group N waits until at most N
 // committed groups are pending.

@@ -24,13 +24,6 @@ namespace {
 constexpr int kThreads = 128;
 __device__ int g_bad_pages;
 
-// Two binary32 values -> two E4M3 codes (x0 in the low byte).
-__device__ __forceinline__ uint32_t e4m3x2(float x0, float x1) {
-  unsigned short r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(x1), "f"(x0));
-  return r;
-}
-
 // The sequence of row r and the row's position in it, for all threads of the
 // CTA; -1 when no range holds the row.
 __device__ __forceinline__ int row_sequence(const PagedAppendParams& p, int r, int& pos) {
@@ -138,8 +131,7 @@ __global__ void __launch_bounds__(kThreads) paged_quantize_kernel(const PagedApp
     const float sc = __half2float(sh);
     uint32_t c[PER / 2];
 #pragma unroll
-    for (int k = 0; k < PER / 2; ++k)
-      c[k] = sc == 0.f ? 0u : e4m3x2(__fdiv_rn(x[2 * k], sc), __fdiv_rn(x[2 * k + 1], sc));
+    for (int k = 0; k < PER / 2; ++k) c[k] = e4m3_codes(x[2 * k], x[2 * k + 1], sc);
     uint8_t* dst = static_cast<uint8_t*>(which ? p.v : p.k) + page * p.page_stride + h * p.head_stride +
                    slot * p.tok_stride + lane * PER;
     if constexpr (PER == 8)

@@ -193,3 +193,55 @@ def test_fp8_queries_with_a_channel_far_above_the_others(D, times):
         ref_tol[rows] += 4 * lost[..., None] * wabs[rows]
     out, lse = run(x)
     assert_attended(out, lse, (ref, l, ref_tol, l_tol))
+
+
+# ------------------------------------------------------------------ rows to quantize
+@pytest.mark.parametrize("D", [128, 256])
+def test_fp8_rows_with_nan_keep_it(D):
+    # NaN among ordinary values, a row of nothing else, one of NaN and zeros and one of NaN and values whose scale
+    # rounds to 0: the codes of NaN are NaN, the others as without it.
+    n = 6
+    g = torch.Generator().manual_seed(69)
+    k_new, v_new = (torch.randn(n, 2, D, generator=g).bfloat16() for _ in range(2))
+    k_new[1, 0, 7] = k_new[1, 1, D - 1] = float("nan")
+    v_new[2] = float("nan")
+    k_new[3] = 0
+    k_new[3, 0, ::3] = float("nan")
+    v_new[4] = 1e-9
+    v_new[4, 1, 5] = float("nan")
+    set_bits(k_new, (5, 0, 0), 0xFFFF)
+    rows = [t.clone() for t in (k_new, v_new)]
+    for t in rows:
+        t[torch.isnan(t)] = 0
+    caches, state = [], []
+    one = lambda *v: torch.tensor(v, dtype=torch.int32, device=dev())
+    for k, v in (rows, (k_new, v_new)):
+        cache = qsa.PagedCache(*(torch.zeros(1, 2, 16, D, dtype=torch.uint8, device=dev()) for _ in range(2)),
+                               torch.zeros(1, 2, 16, 2, dtype=torch.float16, device=dev()))
+        qsa.paged_append(cache, qsa.PagedBatch(one(0)[None], one(n), one(0, n), n_rows=n), k.to(dev()), v.to(dev()))
+        caches.append(cache)
+        state.append([cache.k[0, :, :n].cpu(), cache.v[0, :, :n].cpu(), cache.kv_scale.cpu()])
+    for was, now, x in zip(state[0], state[1], (k_new, v_new)):
+        nan = torch.isnan(x).transpose(0, 1)
+        assert ((now & 0x7F) == 0x7F)[nan].all() and torch.equal(now[~nan], was[~nan])
+    assert torch.equal(state[0][2], state[1][2])
+    # The append into segments gives the same codes ...
+    seg = [torch.zeros(2, 16, D, dtype=torch.uint8, device=dev()) for _ in range(2)]
+    sc = torch.zeros(2, 16, 2, dtype=torch.float16, device=dev())
+    seq = qsa.Seq(n, n, torch.zeros(4, 128, device=dev()), [qsa.Segment(seg[0], seg[1], 0, sc)],
+                  idx_keys=torch.zeros(16, 128, dtype=torch.bfloat16, device=dev()))
+    qsa.append_tokens(seq, k_new.transpose(0, 1).contiguous().to(dev()), v_new.transpose(0, 1).contiguous().to(dev()),
+                      torch.zeros(n, 128, dtype=torch.bfloat16, device=dev()))
+    assert torch.equal(caches[1].k[0], seg[0]) and torch.equal(caches[1].v[0], seg[1])
+    assert torch.equal(caches[1].kv_scale[0], sc)
+    # ... and rows that see such a token are NaN.
+    q = torch.randn(n, 4, D, generator=g).bfloat16().to(dev())
+    out, lse = torch.empty(q.shape, device=dev()), torch.empty(q.shape[:2], device=dev())
+    qsa.paged_attn(caches[1], qsa.PagedBatch(one(0)[None], one(n), one(0, n), n_rows=n), q, out, lse, window=1)
+    nan_k, nan_v = torch.isnan(k_new).any(-1), torch.isnan(v_new)
+    assert torch.equal(torch.isnan(lse.cpu()), nan_k.repeat_interleave(2, 1))
+    for r in (2, 5):                                      # (rows of one token, the others' weights are zero)
+        last = qsa.PagedBatch(one(0)[None], one(r + 1), one(0, 1), n_rows=1)
+        qsa.paged_attn(caches[1], last, q[r:r + 1], out[r:r + 1], lse[r:r + 1], window=1)
+        want = (nan_k[r][:, None] | nan_v[r]).repeat_interleave(2, 0)
+        assert torch.equal(torch.isnan(out[r].cpu()), want)
