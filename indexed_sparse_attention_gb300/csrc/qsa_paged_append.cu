@@ -35,7 +35,7 @@ __device__ __forceinline__ int row_sequence(const PagedAppendParams& p, int r, i
     if (n < kThreads) break;
   }
   if (seq >= p.n_seqs || r < __ldcg(p.row_start + seq)) return -1;
-  pos = __ldcg(p.lens + seq) - (min(__ldcg(p.row_start + seq + 1), p.n_rows) - r);
+  pos = max(__ldcg(p.lens + seq), 0) - (min(__ldcg(p.row_start + seq + 1), p.n_rows) - r);
   return seq;
 }
 

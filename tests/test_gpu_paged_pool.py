@@ -1,5 +1,6 @@
 """The keeping of pages at its ends: pools that run out inside a serving step,
-requests for more pages than 32 bits count, and tables that name pages nobody counts."""
+requests for more pages than 32 bits count, tables that name pages nobody counts, and
+lengths below zero."""
 import pytest
 import torch
 
@@ -185,3 +186,20 @@ def test_copy_in_caches_of_unequal_numbers_of_pages():
         assert torch.equal(c.k, k) and torch.equal(c.v, v)
     status, why = qsa.check_device_status()
     assert status == qsa.ERR_DEVICE_CHECK and "page requests" in why
+
+
+# ------------------------------------------------------------------ append
+@pytest.mark.parametrize("length", [0, -1, -(2 ** 31), -(2 ** 31) + 2])
+def test_append_to_sequences_of_no_tokens(length):
+    # The rows sit before the first token and are skipped without a report, as attention gives them nothing.
+    # (The table has a page for each position that fits 31 bits.)
+    page, ld = 1024, 1 << 21
+    k, v = (torch.zeros(2, 1, page, 128, dtype=torch.bfloat16, device=dev()) for _ in range(2))
+    table = torch.zeros(1, ld, dtype=torch.int32, device=dev())
+    cache, batch = qsa.PagedCache(k, v), qsa.PagedBatch(table, _ints([length]), _ints([0, 5]), n_rows=5)
+    rows = torch.ones(5, 1, 128, dtype=torch.bfloat16, device=dev())
+    qsa.paged_append(cache, batch, rows, rows)
+    out, lse = torch.ones(5, 4, 128, device=dev()), torch.ones(5, 4, device=dev())
+    qsa.paged_attn(cache, batch, torch.ones(5, 4, 128, dtype=torch.bfloat16, device=dev()), out, lse)
+    assert not k.any() and not v.any() and not out.any() and torch.isneginf(lse).all()
+    assert qsa.check_device_status() == (0, "")
