@@ -603,7 +603,9 @@ typedef struct qsa_paged_batch {
  * not part of any sum, whatever their pages hold (NaN and infinities too);
  * pages that hold no visible token are not read.  A V value (or an fp8 scale)
  * that some row sees must be finite for the sums of that sequence's other rows
- * of the call to be.
+ * of the call to be.  Sums are kept relative to a maximum that may lag the row's
+ * own by a factor 2^8 in the weight, so V of about 2^119 / (visible tokens) and
+ * more can overflow them.
  * Table entries outside [0, n_pages) under visible tokens: those tokens are
  * skipped and qsa_check_device_status reports them.
  *   cache, batch   host structs

@@ -27,8 +27,8 @@ __device__ int g_bad_pages;   // table entries outside [0, n_pages) among the to
 
 // ------------------------------------------------------------------ f32 caches
 // (A windowed batch of five sequences, 1 to 37 rows, head_dim 256: 56 us, of which
-// the three tf32 products are 22 and the start, the waits for the next call and
-// the joining launch about 12; the rest is the splitting and the exchange of
+// the three tf32 products are 22 at the rate of mma.sync, and the start, the waits
+// for the next call and the joining launch about 12; the rest is the splitting and the exchange of
 // partial logits between two barriers a tile.)
 //
 // Products of f32 values on the tensor pipe, by tf32 halves: x = hi + lo with hi

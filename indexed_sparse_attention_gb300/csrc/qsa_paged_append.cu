@@ -9,10 +9,11 @@
 // arithmetic of qsa_append_tokens: scale = f16(f32(amax / 448)), code = the
 // E4M3 value nearest to f32(x / scale), ties to even, saturated.
 //
-// What bounds it: latencies, a launch and three dependent reads (range, length,
-// page) a row.  160 rows of bf16 in 64 sequences take 2.1 us on the GPU, 2,048
-// rows for an fp8 cache (6.3 MB, 0.9 us at the measured bandwidth) 6.3 us; a call
-// on its own is the host's 6 us.
+// What bounds it: for a step's rows latencies, a launch and three dependent reads
+// (range, length, page): 147 rows of bf16 in 64 sequences take 2.0 us on the GPU (in
+// a graph of 50 such calls).  2,048 rows for an fp8 cache (6.3 MB, 0.9 us at the
+// measured bandwidth) take 6.5 us: each row's CTA looks for its sequence by itself,
+// reads 16 bytes a thread and writes 8.  A call on its own is the host's 6 to 7 us.
 #include <cuda_fp16.h>
 
 #include "qsa_paged.cuh"

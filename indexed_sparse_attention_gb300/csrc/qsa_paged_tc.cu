@@ -15,8 +15,9 @@
 // one entry, so row statistics need one exchange with the thread of the other
 // group and no shuffles, and its 64 logits stay in registers.  (Tiles of 128 keys
 // in turn between the groups: the chain logits - weights - output of a tile, which
-// two tiles in flight have to cover, was 3,300 cycles for head_dim 128; 2,048 rows
-// over 16k tokens 303 against 295 us, the ragged fp8 batch 181 against 172.)
+// two tiles in flight have to cover, was 3,300 cycles for head_dim 128; with that,
+// 2,048 rows over 16k tokens took 303 us and this way 296, the ragged fp8 batch 181
+// and 172.)
 // The maximum m is only moved, and O rescaled, when a logit exceeds
 // it by more than 2^8 in the weight: weights stay below 2^8, which the 32-bit sums
 // and bf16's exponent hold as well as 1, and the quotient by l is the same.
@@ -47,7 +48,7 @@
 // 1,941 TFLOP/s): few rows, the K/V bytes -- 261,120 tokens x 4 rows 89 of 79; the
 // call's start and the joining launch are what a 65,536-token row (32 of 20) and a
 // windowed batch of 64 (49 of 33) add.  2,048 rows: over 16k tokens (head_dim 128)
-// 290 of 199, the tensor pipe 67% busy at the power limit; over a
+// 292 of 199, the tensor pipe 67% busy at the power limit; over a
 // 4,096-token window (256) 170 of 108, the shared memory's 128 bytes a cycle, which
 // Q and K take whole in the logits' product (2,700 cycles a tile where the products
 // alone take 2,048).  fp8: 170 of 115, shared memory too: the products, V's conversion

@@ -147,7 +147,9 @@ class PagedCache:
 class PagedBatch:
     """The sequences and rows of a call.  table [n_seqs, >= pages], lens [n_seqs]
     and row_start [n_seqs + 1] are int32 tensors on the GPU, read when the work
-    runs; n_rows is the rows of q, max_rows the most that one sequence has."""
+    runs; n_rows is the rows of q, max_rows the most that one sequence has.  Give
+    max_rows: without it the call is laid out for one sequence of all rows, which
+    is right for a single prompt and slower for a batch of few rows each."""
 
     def __init__(self, table: torch.Tensor, lens: torch.Tensor, row_start: torch.Tensor, *, n_rows: int,
                  max_rows: int | None = None):
@@ -247,7 +249,12 @@ class PagedStep:
     """Preallocated buffers for one layer's attention over its paged cache, so
     the same call can be replayed (or captured in a CUDA graph): `out`, `lse`
     and the workspace belong to the step, and what the table, the lengths and
-    the row ranges hold is read when the work runs."""
+    the row ranges hold is read when the work runs.
+
+    The buffers are allocated on the stream that is the current one when the step
+    is made.  Before its first run on another stream, have that one wait for it
+    (Stream.wait_stream): their memory may still be in use by work queued there.
+    One step's runs must not overlap each other."""
 
     def __init__(self, cache: PagedCache, batch: PagedBatch, q: torch.Tensor, *, out_dtype=torch.float32,
                  window: int = 0, n_sinks: int = 0, scale: float = 0.0, n_splits: int = 0):
@@ -300,7 +307,11 @@ class PagePool:
     step_lens [places] are the lengths for the step that follows an extend, the
     lens of its PagedBatch: those of the pool, and 0 for a place that did not get
     its room, whose rows are then written nowhere and see nothing.  (With the
-    pool's own lens such rows would be written over its last tokens.)"""
+    pool's own lens such rows would be written over its last tokens.)
+
+    The pool's calls follow each other on one stream, or on streams that the
+    caller orders; so does the first of them behind the stream that was the
+    current one when the pool was made, where its buffers were allocated."""
 
     def __init__(self, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, caches: Sequence[PagedCache] = (),
                  page_tokens: int | None = None):
