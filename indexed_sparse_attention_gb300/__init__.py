@@ -185,7 +185,8 @@ def _scratch(n_bytes: int, device, stream) -> torch.Tensor:
     if stream is None:
         return torch.empty(n, dtype=torch.uint8, device=device)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+        handle = _stream(stream)   # (0 is the default stream; ExternalStream(0) is a new one)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
     with torch.cuda.stream(stream):
         return torch.empty(n, dtype=torch.uint8, device=device)
 

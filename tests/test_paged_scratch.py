@@ -29,6 +29,7 @@ def allocations(monkeypatch):
         return empty(*size, **kw)
 
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: f"stream {handle} of {device}")
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: f"default stream of {device}")
     monkeypatch.setattr(torch.cuda, "stream", On)
     monkeypatch.setattr(torch, "empty", fake_empty)
     yield seen
@@ -38,7 +39,8 @@ def allocations(monkeypatch):
 def test_scratch_is_allocated_on_the_stream_of_the_call(allocations):
     assert paged._scratch(100, torch.device("cuda", 0), None).numel() == 100
     assert paged._scratch(0, torch.device("cuda", 0), 77).numel() == 16
-    assert allocations == ["the current stream", "stream 77 of cuda:0"]
+    paged._scratch(9, torch.device("cuda", 0), 0)           # the handle of the default stream
+    assert allocations == ["the current stream", "stream 77 of cuda:0", "default stream of cuda:0"]
 
 
 def test_scratch_of_the_layer_step_calls_too(allocations, monkeypatch):
@@ -63,6 +65,22 @@ def test_scratch_of_the_layer_step_calls_too(allocations, monkeypatch):
         allocations.clear()
         call(77)
         assert allocations == ["stream 77 of cpu"]
+
+
+@pytest.mark.gpu
+def test_the_handle_of_the_default_stream():
+    # Scratch of a call with handle 0 is the default stream's, whichever is the current one.
+    seen = {}
+    side = torch.cuda.Stream()
+    for name, stream in (("default", torch.cuda.default_stream()), ("handle", 0)):
+        with torch.cuda.stream(side):
+            ws = paged._scratch(40 << 20, dev(), stream)
+            seen[name] = ws.data_ptr()
+            del ws
+    # (The block went back to the stream it came from and is handed out there again.)
+    ws = torch.empty(40 << 20, dtype=torch.uint8, device=dev())
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    assert seen["handle"] == seen["default"] == ws.data_ptr()
 
 
 @pytest.mark.gpu
