@@ -72,6 +72,7 @@ extern "C" {
 #define QSA_MAX_PAGE_TOKENS 1024   /* ... to here */
 #define QSA_MAX_PAGE_REQUESTS 1024 /* sequences that one qsa_pages_* call takes */
 #define QSA_MAX_CACHES 256         /* cache layers that one qsa_pages_* call takes */
+#define QSA_MAX_ROPE_PAIRS 128     /* channel pairs of a rotation */
 
 typedef enum qsa_status {
   QSA_OK = 0,
@@ -88,7 +89,8 @@ typedef enum qsa_dtype {
   QSA_F32 = 0,               /* IEEE binary32 */
   QSA_BF16 = 1,              /* bfloat16 */
   QSA_FP8_E4M3 = 2,          /* K/V state only: E4M3 codes with per-(head, token) f16 scales */
-  QSA_Q8_0 = 3               /* K/V state only: int8 codes with an f16 scale per 32 elements */
+  QSA_Q8_0 = 3,              /* K/V state only: int8 codes with an f16 scale per 32 elements */
+  QSA_Q4_1 = 4               /* state of paged caches only: 4-bit codes with an f16 scale and minimum per 32 elements */
 } qsa_dtype;
 
 /* One contiguous piece of a sequence's K/V cache (MTPLX pull request #610:
@@ -538,6 +540,67 @@ qsa_status qsa_lse_merge(const float* o_parts, const float* lse_parts, int32_t n
 
 /*
  * ---------------------------------------------------------------------------
+ * Rotary positions.  The first rot_dim channels of a head are rot_dim / 2 pairs,
+ * channels (i, i + rot_dim / 2), or with `pairs` (2i, 2i + 1); a row at position p
+ * has pair i = (a, b) turned by the angle p w_i and multiplied by `magnitude`:
+ *   a' = magnitude (a cos(p w_i) - b sin(p w_i))
+ *   b' = magnitude (a sin(p w_i) + b cos(p w_i)).
+ * The other channels stay as they are.  Angles are kept in turns as 64-bit
+ * fractions, so that p w_i is reduced to one turn exactly whatever p is (negative
+ * positions turn backwards): what is left is the rounding of w_i, 2^-53 of it, and of
+ * the reduced angle, cosine and sine in binary32 (2^-22 together).  Arithmetic is
+ * 32-bit, each result rounded once to the row's type.
+ */
+typedef struct qsa_rope {      /* host struct; filled by qsa_rope_init, consumed before a call returns */
+  int32_t rot_dim;             /* a multiple of 16, 16 .. 2 QSA_MAX_ROPE_PAIRS */
+  int32_t pairs;               /* 0: channels (i, i + rot_dim / 2); 1: (2i, 2i + 1) */
+  float magnitude;
+  int32_t reserved;
+  uint64_t turns[QSA_MAX_ROPE_PAIRS];   /* w_i / (2 pi) modulo 1, times 2^64 */
+} qsa_rope;
+
+typedef enum qsa_rope_scaling {
+  QSA_ROPE_PLAIN = 0,          /* w_i = base^(-2 i / rot_dim) */
+  QSA_ROPE_LINEAR = 1,         /* ... / factor: positions interpolated */
+  QSA_ROPE_PARTS = 2           /* frequencies that turn often over the first context stay, the others are divided */
+} qsa_rope_scaling;
+
+/*
+ * Host functions.  qsa_rope_frequencies writes the rot_dim / 2 frequencies w_i
+ * (radians a position) of a base and a scaling, and the magnitude that goes with
+ * them: 1, or for QSA_ROPE_PARTS (Peng et al., "YaRN: Efficient Context Window
+ * Extension of Large Language Models", 2023, section 3) 0.1 ln(factor) + 1, with
+ *   r_i = original_tokens w_i / (2 pi),  g_i = clamp((r_i - slow) / (fast - slow), 0, 1),
+ *   w_i' = (1 - g_i) w_i / factor + g_i w_i        (the paper: fast 32, slow 1).
+ * qsa_rope_init makes a rotation from any frequencies.
+ *   base >= 1, factor >= 1 (not used by PLAIN), original_tokens, fast > slow >= 0
+ *   (used by PARTS)
+ * Errors: QSA_ERR_INVALID_ARG (null pointers, numbers that are not finite or outside
+ * the above), QSA_ERR_UNSUPPORTED (rot_dim, an unknown scaling).
+ */
+qsa_status qsa_rope_frequencies(int32_t rot_dim, double base, qsa_rope_scaling scaling, double factor,
+                                double original_tokens, double fast, double slow, double* w, float* magnitude);
+qsa_status qsa_rope_init(qsa_rope* rope, int32_t rot_dim, int32_t pairs, const double* w, float magnitude);
+
+/*
+ * y[r][h] = x[r][h] rotated for position positions[r].
+ *   positions       device int32 [n_rows]
+ *   x, y            device, element (r, h, d) at r * row_stride + h * head_stride + d
+ *                   of dtype (QSA_F32 or QSA_BF16); y may be x itself (with the same
+ *                   strides: rotation in place, the other channels are not touched),
+ *                   else the two do not overlap
+ *   head_dim        a multiple of 16, rot_dim .. 1,024
+ *   strides         elements, >= 0, multiples of 16 bytes; rows and heads of y do not
+ *                   overlap (y strides >= head_dim where there are several)
+ * Errors: QSA_ERR_INVALID_ARG, QSA_ERR_UNSUPPORTED, QSA_ERR_MISALIGNED, QSA_ERR_CUDA.
+ * n_rows == 0 or n_heads == 0 is a no-op.
+ */
+qsa_status qsa_rotate(const qsa_rope* rope, const int32_t* positions, int32_t n_rows, int32_t n_heads,
+                      int32_t head_dim, qsa_dtype dtype, const void* x, int64_t x_row_stride, int64_t x_head_stride,
+                      void* y, int64_t y_row_stride, int64_t y_head_stride, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
  * Paged K/V caches: the other attention layers of a model beside its QSA
  * layers (dense, or with a sliding window), over the cache a serving loop
  * keeps in pages.  A page holds the K and V of page_tokens consecutive tokens
@@ -554,17 +617,24 @@ qsa_status qsa_lse_merge(const float* o_parts, const float* lse_parts, int32_t n
  * pair of (page, h, slot) is the 4-byte record at kv_scale + 4 * (page *
  * scale_page_stride + h * scale_head_stride + slot * scale_tok_stride), as for
  * segments.  A scale may be any f16: zero, negative, infinite or NaN, as it stands.
- * f32, bf16 and fp8 caches; QSA_Q8_0 caches are not paged (QSA_ERR_UNSUPPORTED:
- * the scales of its 32-channel blocks do not factor out of a row's product, which
- * is what lets the pages be read as stored). */
+ * QSA_Q4_1: a row is D / 32 blocks of 32 channels, value = code * scale + minimum of
+ * its block with codes 0 .. 15, two to a byte: an element is half a byte, and
+ * strides are counted in elements all the same (multiples of 32: 16 bytes).  Channel
+ * 32 g + 4 n + j (n < 8, j < 4) of a row is nibble j, from the lowest, of the row's
+ * 16-bit unit n * (D / 32) + g: 16 bytes then hold channels of all blocks, as the
+ * products want them.  The (K, V) record of (page, h, slot) is the K row's D / 32
+ * pairs (scale, minimum) of f16, then the V row's: D / 4 bytes, 16-byte aligned, at
+ * kv_scale + D / 4 * (page * scale_page_stride + ...).  Scales and minima may be any
+ * f16 as they stand.
+ * f32, bf16, fp8 and 4-bit caches; QSA_Q8_0 caches are not paged (QSA_ERR_UNSUPPORTED). */
 typedef struct qsa_paged_cache {
   const void* k;               /* device, kv_dtype; written by the calls that write a cache */
   const void* v;
   int64_t page_stride;         /* elements between pages */
   int64_t head_stride;         /* elements between KV heads of a page */
   int64_t tok_stride;          /* elements between tokens of a page, >= head_dim */
-  const void* kv_scale;        /* fp8: device scale records */
-  int64_t scale_page_stride;   /* fp8: records */
+  const void* kv_scale;        /* fp8, 4-bit: device scale records */
+  int64_t scale_page_stride;   /* fp8, 4-bit: records */
   int64_t scale_head_stride;
   int64_t scale_tok_stride;
   int32_t n_pages;             /* pages in k and v */
@@ -610,7 +680,7 @@ typedef struct qsa_paged_batch {
  * skipped and qsa_check_device_status reports them.
  *   cache, batch   host structs
  *   cfg            as for qsa_sparse_attn: Hq / Hkv <= 16, head_dim 128 or 256,
- *                  q_dtype = kv_dtype (bf16 for an fp8 cache); n_splits: the most
+ *                  q_dtype = kv_dtype (bf16 for an fp8 or 4-bit cache); n_splits: the most
  *                  runs the call's keys are divided into (CTAs that share
  *                  them), 0 = as many as the GPU takes at a time
  *   window         0 (no window) or the tokens a row sees, its own included
@@ -627,7 +697,10 @@ typedef struct qsa_paged_batch {
  * exp(z - m) are rounded to bf16 for the product with V (at most 2^-8 of each,
  * independently), out once to out_dtype.  fp8: q enters as the sum of two 8-bit
  * codes a value, exact from 2^-13 of the largest magnitude of its row and head on,
- * and off by at most 2^-21 of that below.  The result depends on the
+ * and off by at most 2^-21 of that below.  4-bit: the logits are those of the
+ * stored values (q is exact from 2^-25 of the largest magnitude of its row and head on,
+ * off by at most 2^-33 of it below); weights are rounded to f16, alone and times V's
+ * scales (2^-11 each).  The result depends on the
  * lengths and the number of runs, not on timing: it is reproducible.
  * Errors: QSA_ERR_INVALID_ARG, QSA_ERR_UNSUPPORTED, QSA_ERR_MISALIGNED,
  * QSA_ERR_WORKSPACE, QSA_ERR_CUDA.  n_rows == 0 or n_seqs == 0 is a no-op.
@@ -642,7 +715,13 @@ qsa_status qsa_paged_attn(const qsa_paged_cache* cache, const qsa_paged_batch* b
  * Writing new tokens into their pages: row r at position p of sequence i (as
  * above: the lengths already count the new tokens) goes to slot p mod
  * page_tokens of page table[i][p / page_tokens], copied, or quantized exactly
- * as qsa_append_tokens does (bf16 rows into an fp8 cache; NaN stays NaN).
+ * as qsa_append_tokens does (bf16 rows into an fp8 cache; NaN stays NaN).  4-bit
+ * caches: per block of 32 channels, lo and hi its smallest and largest value,
+ *   minimum = f16(lo), scale = f16(f32(f32(hi - lo) / 15)),
+ *   code = the integer nearest to f32(f32(x - minimum) / scale), ties to even, within
+ *   0 .. 15 (0 where the scale is 0);
+ * a block that holds an infinity or NaN, or whose scale or minimum f16 does not hold,
+ * gets scale NaN and reads as NaN: nothing is cut off silently.
  *   cfg            n_kv_heads, head_dim, kv_dtype (the other fields are checked
  *                  as for qsa_paged_attn)
  *   k_new, v_new   device, element (r, h, d) at r * row_stride + h * head_stride
@@ -657,6 +736,38 @@ qsa_status qsa_paged_attn(const qsa_paged_cache* cache, const qsa_paged_batch* b
 qsa_status qsa_paged_append(const qsa_paged_cache* cache, const qsa_paged_batch* batch, const qsa_attn_config* cfg,
                             const void* k_new, const void* v_new, int64_t row_stride, int64_t head_stride,
                             void* stream);
+
+/*
+ * qsa_paged_append with the rotation of K on the way, and of the step's queries
+ * beside it, in one launch.  Row r's K heads are rotated for its position p, rounded
+ * to the type of the rows (so the cache holds what qsa_rotate into such a tensor and
+ * qsa_paged_append would leave) and written; V is written as it is; with q,
+ * q_out[r][h] = q[r][h] rotated for p.
+ *   rope           the rotation (rot_dim <= head_dim)
+ *   q              device, element (r, h, d) at r * q_row_stride + h * q_head_stride
+ *                  + d, of cfg->q_dtype, cfg->n_q_heads heads; NULL: none (cfg->n_q_heads
+ *                  is then not used, but checked)
+ *   q_out          device [n_rows, Hq, head_dim], contiguous; may be q itself when
+ *                  q is contiguous, else it overlaps nothing the call reads
+ * Queries of rows that belong to a sequence are rotated whether or not their K has a
+ * page; rows of nobody are left as they were.
+ * Errors: as qsa_paged_append and qsa_rotate.
+ */
+qsa_status qsa_paged_append_rotate(const qsa_paged_cache* cache, const qsa_paged_batch* batch,
+                                   const qsa_attn_config* cfg, const qsa_rope* rope, const void* k_new,
+                                   const void* v_new, int64_t row_stride, int64_t head_stride, const void* q,
+                                   int64_t q_row_stride, int64_t q_head_stride, void* q_out, void* stream);
+
+/*
+ * The rows of a batch back out of their pages: what paged_append wrote for row r, as
+ * cfg->out_dtype (f32, or bf16: rounded once).
+ *   k_out, v_out   device [n_rows, Hkv, head_dim], contiguous
+ * Rows at negative positions, without a page in the table (reported as above) or of
+ * nobody are left as they were.  f32, bf16, fp8 and 4-bit caches.
+ * Errors: as qsa_paged_append.  n_rows == 0 or n_seqs == 0 is a no-op.
+ */
+qsa_status qsa_paged_read(const qsa_paged_cache* cache, const qsa_paged_batch* batch, const qsa_attn_config* cfg,
+                          void* k_out, void* v_out, void* stream);
 
 /*
  * Who holds which page: a page table of n_seqs places for sequences, their

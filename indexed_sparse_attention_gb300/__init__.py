@@ -23,7 +23,8 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libqsa.so")
 
-F32, BF16, FP8, Q8 = 0, 1, 2, 3   # FP8 / Q8: quantized K/V state (E4M3 / int8 codes + f16 scales)
+# FP8, Q8, Q4: quantized K/V state (E4M3, int8, 4-bit codes + f16 scales; Q4: paged caches only)
+F32, BF16, FP8, Q8, Q4 = 0, 1, 2, 3, 4
 INDEX_DIM = 128
 INDEX_HEADS = 4
 TOP_K = 512
@@ -73,7 +74,8 @@ EXPORTS = ("qsa_status_string", "qsa_last_error", "qsa_version", "qsa_pool_index
            "qsa_check_device_status", "qsa_selftest_wait_timeout", "qsa_pool_score_blocks",
            "qsa_append_score_blocks", "qsa_paged_attn_workspace_size", "qsa_paged_attn", "qsa_paged_append",
            "qsa_pages_workspace_size", "qsa_pages_extend", "qsa_pages_extend_step", "qsa_pages_fork", "qsa_pages_free", "qsa_pages_compact",
-           "qsa_pages_copy")
+           "qsa_pages_copy", "qsa_rope_frequencies", "qsa_rope_init", "qsa_rotate", "qsa_paged_append_rotate",
+           "qsa_paged_read")
 NOALLOC_SCRATCH_BYTES = 4 << 20
 
 
@@ -131,6 +133,7 @@ def lib() -> ctypes.CDLL:
                  "qsa_append_tokens", "qsa_arena_create", "qsa_arena_ensure", "qsa_arena_destroy"):
         getattr(L, name).restype = i32
     paged.declare(L)
+    rope.declare(L)
     _lib = L
     return L
 
@@ -660,7 +663,8 @@ class LayerStep:
         return self.out, self.lse
 
 
-# The paged caches' part of the binding builds on the names above.
-from . import paged  # noqa: E402
+# The rotations' and the paged caches' parts of the binding build on the names above.
+from . import paged, rope  # noqa: E402
 from .paged import (PagedBatch, PagedCache, PagedStep, PagePool, paged_append, paged_attn,  # noqa: E402, F401
-                    paged_attn_workspace_size)
+                    paged_attn_workspace_size, paged_read)
+from .rope import Rope, RopeScaling, rotate  # noqa: E402, F401

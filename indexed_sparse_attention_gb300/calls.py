@@ -1,0 +1,31 @@
+"""A library call on a tensor's device and stream."""
+from __future__ import annotations
+
+import torch
+
+from . import _check, lib
+
+#: The handle of a device's current stream; torch.cuda.current_stream builds a Stream object around it (2 us a call).
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _raw_stream(stream, device) -> int:
+    if stream is None:
+        return _current_stream(device.index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _call(name: str, device, stream, *args):
+    """One library call with the tensors' device as the current one (the library
+    launches there), on `stream` or that device's current stream."""
+    if device.type != "cuda":
+        raise ValueError(f"{name}: the tensors are on {device}, not on a GPU")
+    fn = getattr(lib(), name)
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(stream, device))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _raw_stream(stream, device))
+    if status:
+        _check(name, status)

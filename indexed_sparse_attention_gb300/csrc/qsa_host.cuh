@@ -34,5 +34,7 @@ inline bool valid_kv_dtype(int d) { return valid_dtype(d) || quantized(d); }
 inline cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
 qsa_status check_attn_config(const qsa_attn_config* cfg, const char* fn);
+// A rotation for heads of head_dim channels (qsa_rotate.cu).
+qsa_status check_rope(const qsa_rope* rope, int head_dim, const char* fn);
 
 }  // namespace qsa

@@ -80,6 +80,26 @@ struct PagedAppendParams {
 cudaError_t launch_paged_append(const PagedAppendParams& p, qsa_dtype kv_dtype, cudaStream_t st);
 int paged_append_bad_pages_take();
 
+// The same with a rotation on the way, and 4-bit caches; rows back out of their
+// pages (qsa_paged_rows.cu).
+struct PagedRowsParams {
+  PagedAppendParams a;
+  qsa_rope rope;             // rot_dim 0: none
+  const void* q;             // or null
+  int64_t q_row_stride, q_head_stride;                  // elements
+  void* q_out;               // [n_rows, Hq, D]
+  int32_t n_q_heads;
+};
+struct PagedReadParams {
+  PagedAppendParams a;       // k_new, v_new: not used
+  void* k_out;               // [n_rows, Hkv, D]
+  void* v_out;
+  int32_t rows_warp;         // rows that a warp takes
+};
+cudaError_t launch_paged_rows(const PagedRowsParams& p, qsa_dtype kv_dtype, cudaStream_t st);
+cudaError_t launch_paged_read(PagedReadParams p, qsa_dtype kv_dtype, qsa_dtype out_dtype, cudaStream_t st);
+int paged_rows_bad_pages_take();
+
 // Keeping the pages of a pool (qsa_pages.cu).
 constexpr int kPageCaches = 32;   // caches of one launch
 struct PageCache {
@@ -95,6 +115,7 @@ struct PageCaches {
   int32_t n_pages;           // that every cache of the call has
   int32_t n_kv_heads, page_shift;
   int32_t row_shift;         // log2 of the 16-byte pieces of a row
+  int32_t record_pieces;     // 16-byte pieces of a scale record; 0: one of 4 bytes
 };
 cudaError_t launch_pages_extend(const qsa_page_pool& pool, const int32_t* seqs, const int32_t* n_new, int n,
                                 int32_t* step_lens, cudaStream_t st);
@@ -117,6 +138,10 @@ cudaError_t launch_paged_f32(const PagedParams& p, int head_dim, int grid, cudaS
 cudaError_t launch_paged_tc(const PagedParams& p, qsa_dtype kv_dtype, int head_dim, int grid, cudaStream_t st);
 int paged_tc_bad_pages_take();
 int paged_tc_wait_timeouts();
+// 4-bit caches (qsa_paged_q4.cu).
+cudaError_t launch_paged_q4(const PagedParams& p, int head_dim, int grid, cudaStream_t st);
+int paged_q4_bad_pages_take();
+int paged_q4_wait_timeouts();
 cudaError_t launch_paged_merge(const PagedParams& p, int head_dim, int runs, cudaStream_t st);
 int paged_bad_pages_take();
 int paged_f32_wait_timeouts();
@@ -125,6 +150,37 @@ namespace paged {
 
 // Lengths above this are taken as this: positions and tiles then keep to 32 bits.
 constexpr int32_t kMaxLen = INT32_MAX - (1 << 25);
+
+// The sequence of row r and the row's position in it, for all threads of the
+// CTA; -1 when no range holds the row.
+template <int THREADS>
+__device__ __forceinline__ int row_sequence(const PagedAppendParams& p, int r, int& pos) {
+  int seq = 0;
+  for (int i0 = 0; i0 < p.n_seqs; i0 += THREADS) {
+    const int i = i0 + (int)threadIdx.x;
+    const int n = __syncthreads_count(i < p.n_seqs && __ldcg(p.row_start + i + 1) <= r);
+    seq += n;
+    if (n < THREADS) break;
+  }
+  if (seq >= p.n_seqs || r < __ldcg(p.row_start + seq)) return -1;
+  pos = max(__ldcg(p.lens + seq), 0) - (min(__ldcg(p.row_start + seq + 1), p.n_rows) - r);
+  return seq;
+}
+
+// The row's page and slot; false when it has none (a page outside the cache is counted).
+__device__ __forceinline__ bool row_page(const PagedAppendParams& p, int seq, int pos, int64_t& page, int64_t& slot,
+                                         int* bad_pages) {
+  if (seq < 0 || pos < 0) return false;
+  const int64_t j = pos >> p.page_shift;
+  const int32_t id = j < p.table_ld ? __ldcg(p.table + seq * p.table_ld + j) : -1;
+  if ((uint32_t)id >= (uint32_t)p.n_pages) {
+    if (threadIdx.x == 0) atomicAdd(bad_pages, 1);
+    return false;
+  }
+  page = id;
+  slot = pos & ((1 << p.page_shift) - 1);
+  return true;
+}
 
 // One sequence's rows and tokens, as the device arrays give them.
 struct SeqRows {

@@ -18,6 +18,9 @@ int log2_of(int64_t x) {
   return s;
 }
 
+// Bytes of n elements of a cache (4-bit: two elements a byte).
+int64_t state_bytes(qsa_dtype d, int64_t n) { return d == QSA_Q4_1 ? n / 2 : n * (int64_t)dtype_size(d); }
+
 // A cache's shape and addresses for head_dim and dtype of cfg.
 qsa_status check_cache(const qsa_paged_cache* c, const qsa_attn_config* cfg, const char* fn) {
   if (!c) return fail(QSA_ERR_INVALID_ARG, "%s: null cache", fn);
@@ -29,19 +32,28 @@ qsa_status check_cache(const qsa_paged_cache* c, const qsa_attn_config* cfg, con
       (c->page_tokens & (c->page_tokens - 1)) != 0)
     return fail(QSA_ERR_UNSUPPORTED, "%s: page_tokens=%d (a power of two in %d..%d)", fn, c->page_tokens,
                 QSA_MIN_PAGE_TOKENS, QSA_MAX_PAGE_TOKENS);
-  const int64_t es = (int64_t)dtype_size(cfg->kv_dtype), most = (int64_t)1 << 38;   // a tensor map holds strides below 2^40 bytes
+  const int64_t most = (int64_t)1 << 38;   // a tensor map holds strides below 2^40 bytes
+  const qsa_dtype kd = cfg->kv_dtype;
+  auto ragged = [&](int64_t stride) { return state_bytes(kd, stride) % 16 != 0 || (kd == QSA_Q4_1 && stride % 2 != 0); };
   if (c->tok_stride < cfg->head_dim || c->head_stride < cfg->head_dim || c->page_stride < cfg->head_dim ||
       c->tok_stride > most || c->head_stride > most || c->page_stride > most)
     return fail(QSA_ERR_INVALID_ARG, "%s: cache strides page=%lld head=%lld tok=%lld (each >= head_dim=%d)", fn,
                 (long long)c->page_stride, (long long)c->head_stride, (long long)c->tok_stride, cfg->head_dim);
-  if (!aligned16(c->k) || !aligned16(c->v) || (c->tok_stride * es) % 16 || (c->head_stride * es) % 16 ||
-      (c->page_stride * es) % 16)
+  if (!aligned16(c->k) || !aligned16(c->v) || ragged(c->tok_stride) || ragged(c->head_stride) || ragged(c->page_stride))
     return fail(QSA_ERR_MISALIGNED, "%s: cache K/V or strides not 16-byte aligned", fn);
   if (cfg->kv_dtype == QSA_FP8_E4M3) {
     if (!c->kv_scale) return fail(QSA_ERR_INVALID_ARG, "%s: fp8 cache has no scales", fn);
     if (reinterpret_cast<uintptr_t>(c->kv_scale) & 3u)
       return fail(QSA_ERR_MISALIGNED, "%s: scale records not 4-byte aligned", fn);
     if (c->scale_page_stride < 1 || c->scale_head_stride < 1 || c->scale_tok_stride < 1)
+      return fail(QSA_ERR_INVALID_ARG, "%s: bad scale strides", fn);
+  }
+  if (kd == QSA_Q4_1) {
+    if (!c->kv_scale) return fail(QSA_ERR_INVALID_ARG, "%s: 4-bit cache has no scales", fn);
+    if (!aligned16(c->kv_scale)) return fail(QSA_ERR_MISALIGNED, "%s: scale records not 16-byte aligned", fn);
+    const int64_t longest = most / 64;   // records of up to 64 bytes, by tensor copies
+    if (c->scale_page_stride < 1 || c->scale_head_stride < 1 || c->scale_tok_stride < 1 ||
+        c->scale_page_stride > longest || c->scale_head_stride > longest || c->scale_tok_stride > longest)
       return fail(QSA_ERR_INVALID_ARG, "%s: bad scale strides", fn);
   }
   return QSA_OK;
@@ -60,15 +72,17 @@ qsa_status check_batch(const qsa_paged_batch* b, const char* fn) {
 
 // Kernel of a call and how it divides the work.
 struct Plan {
-  bool tensor_cores;
+  bool tensor_cores;   // tcgen05 (bf16, fp8)
   int mt;     // entries of an item
   int grid;   // runs
 };
 
 Plan plan_attn(const qsa_paged_batch* b, const qsa_attn_config* cfg) {
   Plan pl;
-  pl.tensor_cores = cfg->kv_dtype != QSA_F32;
-  if (pl.tensor_cores) {
+  pl.tensor_cores = cfg->kv_dtype == QSA_BF16 || cfg->kv_dtype == QSA_FP8_E4M3;
+  if (cfg->kv_dtype == QSA_Q4_1) {
+    pl.mt = 16;
+  } else if (pl.tensor_cores) {
     // Whole rows, as many as a sequence has, up to the 128 entries that are the
     // MMA's rows: what Q does not take of the shared memory is the ring's.
     const int group = cfg->n_q_heads / cfg->n_kv_heads;
@@ -91,7 +105,10 @@ size_t workspace_bytes_of(const Plan& pl, int head_dim) {
 }
 
 qsa_status check_config(const qsa_attn_config* cfg, const char* fn) {
-  const qsa_status s = check_attn_config(cfg, fn);
+  qsa_attn_config c{};
+  if (cfg) c = *cfg;
+  if (c.kv_dtype == QSA_Q4_1) c.kv_dtype = QSA_FP8_E4M3;   // paged caches only; asks the same of the rest
+  const qsa_status s = check_attn_config(cfg ? &c : nullptr, fn);
   if (s != QSA_OK) return s;
   if (cfg->n_splits < 0) return fail(QSA_ERR_INVALID_ARG, "%s: n_splits=%d", fn, cfg->n_splits);
   return QSA_OK;
@@ -161,29 +178,16 @@ QSA_API qsa_status qsa_paged_attn(const qsa_paged_cache* cache, const qsa_paged_
   p.part_lse = reinterpret_cast<float*>(ws + lse_offset(pl));
   p.part_o = reinterpret_cast<float*>(ws + out_offset(pl));
   cudaStream_t st = as_stream(stream);
-  cudaError_t e = pl.tensor_cores ? launch_paged_tc(p, cfg->kv_dtype, cfg->head_dim, pl.grid, st)
-                                  : launch_paged_f32(p, cfg->head_dim, pl.grid, st);
+  cudaError_t e = cfg->kv_dtype == QSA_Q4_1 ? launch_paged_q4(p, cfg->head_dim, pl.grid, st)
+                  : pl.tensor_cores         ? launch_paged_tc(p, cfg->kv_dtype, cfg->head_dim, pl.grid, st)
+                                            : launch_paged_f32(p, cfg->head_dim, pl.grid, st);
   if (e == cudaSuccess) e = launch_paged_merge(p, cfg->head_dim, pl.grid, st);
   return e == cudaSuccess ? ok() : cuda_fail(e, fn);
 }
 
-QSA_API qsa_status qsa_paged_append(const qsa_paged_cache* cache, const qsa_paged_batch* batch,
-                                    const qsa_attn_config* cfg, const void* k_new, const void* v_new,
-                                    int64_t row_stride, int64_t head_stride, void* stream) {
-  const NvtxRange nvtx_range("qsa_paged_append");
-  const char* fn = "qsa_paged_append";
-  qsa_status s = check_config(cfg, fn);
-  if (s != QSA_OK) return s;
-  if ((s = check_cache(cache, cfg, fn)) != QSA_OK) return s;
-  if ((s = check_batch(batch, fn)) != QSA_OK) return s;
-  if (batch->n_seqs == 0 || batch->n_rows == 0) return ok();
-  const int64_t es = cfg->kv_dtype == QSA_F32 ? 4 : 2, most = (int64_t)1 << 40;
-  if (!k_new || !v_new) return fail(QSA_ERR_INVALID_ARG, "%s: null pointer", fn);
-  if (row_stride < 0 || head_stride < 0 || row_stride > most || head_stride > most)
-    return fail(QSA_ERR_INVALID_ARG, "%s: row_stride=%lld, head_stride=%lld", fn, (long long)row_stride,
-                (long long)head_stride);
-  if (!aligned16(k_new) || !aligned16(v_new) || (row_stride * es) % 16 || (head_stride * es) % 16)
-    return fail(QSA_ERR_MISALIGNED, "%s: k_new, v_new or their strides not 16-byte aligned", fn);
+namespace {
+
+PagedAppendParams rows_params(const qsa_paged_cache* cache, const qsa_paged_batch* batch, const qsa_attn_config* cfg) {
   PagedAppendParams p{};
   p.k = const_cast<void*>(cache->k);
   p.v = const_cast<void*>(cache->v);
@@ -204,11 +208,98 @@ QSA_API qsa_status qsa_paged_append(const qsa_paged_cache* cache, const qsa_page
   p.n_rows = batch->n_rows;
   p.n_kv_heads = cfg->n_kv_heads;
   p.head_dim = cfg->head_dim;
-  p.k_new = k_new;
-  p.v_new = v_new;
-  p.row_stride = row_stride;
-  p.new_head_stride = head_stride;
-  const cudaError_t e = launch_paged_append(p, cfg->kv_dtype, as_stream(stream));
+  return p;
+}
+
+// Strided rows: addresses and strides of es-byte elements.
+qsa_status check_strided(const void* a, const void* b, int64_t row_stride, int64_t head_stride, int64_t es,
+                         const char* what, const char* fn) {
+  const int64_t most = (int64_t)1 << 40;
+  if (!a || !b) return fail(QSA_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (row_stride < 0 || head_stride < 0 || row_stride > most || head_stride > most)
+    return fail(QSA_ERR_INVALID_ARG, "%s: row_stride=%lld, head_stride=%lld", fn, (long long)row_stride,
+                (long long)head_stride);
+  if (!aligned16(a) || !aligned16(b) || (row_stride * es) % 16 || (head_stride * es) % 16)
+    return fail(QSA_ERR_MISALIGNED, "%s: %s or their strides not 16-byte aligned", fn, what);
+  return QSA_OK;
+}
+
+}  // namespace
+
+QSA_API qsa_status qsa_paged_append(const qsa_paged_cache* cache, const qsa_paged_batch* batch,
+                                    const qsa_attn_config* cfg, const void* k_new, const void* v_new,
+                                    int64_t row_stride, int64_t head_stride, void* stream) {
+  const NvtxRange nvtx_range("qsa_paged_append");
+  const char* fn = "qsa_paged_append";
+  qsa_status s = check_config(cfg, fn);
+  if (s != QSA_OK) return s;
+  if ((s = check_cache(cache, cfg, fn)) != QSA_OK) return s;
+  if ((s = check_batch(batch, fn)) != QSA_OK) return s;
+  if (batch->n_seqs == 0 || batch->n_rows == 0) return ok();
+  const int64_t es = cfg->kv_dtype == QSA_F32 ? 4 : 2;
+  if ((s = check_strided(k_new, v_new, row_stride, head_stride, es, "k_new, v_new", fn)) != QSA_OK) return s;
+  PagedRowsParams p{};
+  p.a = rows_params(cache, batch, cfg);
+  p.a.k_new = k_new;
+  p.a.v_new = v_new;
+  p.a.row_stride = row_stride;
+  p.a.new_head_stride = head_stride;
+  const cudaError_t e = cfg->kv_dtype == QSA_Q4_1 ? launch_paged_rows(p, cfg->kv_dtype, as_stream(stream))
+                                                  : launch_paged_append(p.a, cfg->kv_dtype, as_stream(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e, fn);
+}
+
+QSA_API qsa_status qsa_paged_append_rotate(const qsa_paged_cache* cache, const qsa_paged_batch* batch,
+                                           const qsa_attn_config* cfg, const qsa_rope* rope, const void* k_new,
+                                           const void* v_new, int64_t row_stride, int64_t head_stride, const void* q,
+                                           int64_t q_row_stride, int64_t q_head_stride, void* q_out, void* stream) {
+  const NvtxRange nvtx_range("qsa_paged_append_rotate");
+  const char* fn = "qsa_paged_append_rotate";
+  qsa_status s = check_config(cfg, fn);
+  if (s != QSA_OK) return s;
+  if ((s = check_cache(cache, cfg, fn)) != QSA_OK) return s;
+  if ((s = check_batch(batch, fn)) != QSA_OK) return s;
+  if ((s = check_rope(rope, cfg->head_dim, fn)) != QSA_OK) return s;
+  if (batch->n_seqs == 0 || batch->n_rows == 0) return ok();
+  const int64_t es = cfg->kv_dtype == QSA_F32 ? 4 : 2;
+  if ((s = check_strided(k_new, v_new, row_stride, head_stride, es, "k_new, v_new", fn)) != QSA_OK) return s;
+  if (q && (s = check_strided(q, q_out, q_row_stride, q_head_stride, es, "q, q_out", fn)) != QSA_OK) return s;
+  if (q && q == q_out && ((cfg->n_q_heads > 1 && q_head_stride != cfg->head_dim) ||
+                          (batch->n_rows > 1 && q_row_stride != (int64_t)cfg->n_q_heads * cfg->head_dim)))
+    return fail(QSA_ERR_INVALID_ARG, "%s: q in place has to be contiguous", fn);
+  PagedRowsParams p{};
+  p.a = rows_params(cache, batch, cfg);
+  p.a.k_new = k_new;
+  p.a.v_new = v_new;
+  p.a.row_stride = row_stride;
+  p.a.new_head_stride = head_stride;
+  p.rope = *rope;
+  p.q = q;
+  p.q_row_stride = q_row_stride;
+  p.q_head_stride = q_head_stride;
+  p.q_out = q_out;
+  p.n_q_heads = cfg->n_q_heads;
+  const cudaError_t e = launch_paged_rows(p, cfg->kv_dtype, as_stream(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e, fn);
+}
+
+QSA_API qsa_status qsa_paged_read(const qsa_paged_cache* cache, const qsa_paged_batch* batch,
+                                  const qsa_attn_config* cfg, void* k_out, void* v_out, void* stream) {
+  const NvtxRange nvtx_range("qsa_paged_read");
+  const char* fn = "qsa_paged_read";
+  qsa_status s = check_config(cfg, fn);
+  if (s != QSA_OK) return s;
+  if ((s = check_cache(cache, cfg, fn)) != QSA_OK) return s;
+  if ((s = check_batch(batch, fn)) != QSA_OK) return s;
+  if (batch->n_seqs == 0 || batch->n_rows == 0) return ok();
+  if (!k_out || !v_out) return fail(QSA_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (!aligned16(k_out) || !aligned16(v_out))
+    return fail(QSA_ERR_MISALIGNED, "%s: k_out/v_out not 16-byte aligned", fn);
+  PagedReadParams p{};
+  p.a = rows_params(cache, batch, cfg);
+  p.k_out = k_out;
+  p.v_out = v_out;
+  const cudaError_t e = launch_paged_read(p, cfg->kv_dtype, cfg->out_dtype, as_stream(stream));
   return e == cudaSuccess ? ok() : cuda_fail(e, fn);
 }
 
@@ -249,7 +340,7 @@ qsa_status check_caches(const qsa_page_pool* pool, const qsa_paged_cache* caches
   for (int i = 0; i < n_caches; ++i) {
     if ((s = check_cache(caches + i, cfg, fn)) != QSA_OK) return s;
     // The copies count a page's 16-byte pieces, a batch of them ahead, in 32 bits.
-    const int64_t bytes = (int64_t)caches[i].page_tokens * cfg->n_kv_heads * cfg->head_dim * (int64_t)dtype_size(cfg->kv_dtype);
+    const int64_t bytes = state_bytes(cfg->kv_dtype, (int64_t)caches[i].page_tokens * cfg->n_kv_heads * cfg->head_dim);
     if (bytes / 16 > INT32_MAX - 4096)
       return fail(QSA_ERR_UNSUPPORTED, "%s: cache %d has pages of %lld bytes of K (below 32 GB)", fn, i, (long long)bytes);
     if (caches[i].page_tokens != (pool ? pool->page_tokens : caches[0].page_tokens))
@@ -276,24 +367,26 @@ PageCaches caches_of(const qsa_paged_cache* caches, int n_caches, const qsa_attn
     out.n = 0;
     return out;
   }
-  const int64_t es = (int64_t)dtype_size(cfg->kv_dtype);
+  const qsa_dtype kd = cfg->kv_dtype;
+  const int64_t record = kd == QSA_Q4_1 ? cfg->head_dim / 4 : 4;
   for (int i = 0; i < out.n; ++i) {
     const qsa_paged_cache& c = caches[at + i];
     out.c[i] = PageCache{const_cast<void*>(c.k),
                          const_cast<void*>(c.v),
-                         cfg->kv_dtype == QSA_FP8_E4M3 ? const_cast<void*>(c.kv_scale) : nullptr,
-                         c.page_stride * es,
-                         c.head_stride * es,
-                         c.tok_stride * es,
-                         4 * c.scale_page_stride,
-                         4 * c.scale_head_stride,
-                         4 * c.scale_tok_stride};
+                         kd == QSA_FP8_E4M3 || kd == QSA_Q4_1 ? const_cast<void*>(c.kv_scale) : nullptr,
+                         state_bytes(kd, c.page_stride),
+                         state_bytes(kd, c.head_stride),
+                         state_bytes(kd, c.tok_stride),
+                         record * c.scale_page_stride,
+                         record * c.scale_head_stride,
+                         record * c.scale_tok_stride};
   }
   out.n_pages = caches[0].n_pages;   // what all of the call's caches have
   for (int i = 1; i < n_caches; ++i) out.n_pages = std::min(out.n_pages, caches[i].n_pages);
   out.n_kv_heads = cfg->n_kv_heads;
   out.page_shift = log2_of(caches[at].page_tokens);
-  out.row_shift = log2_of(cfg->head_dim * es / 16);
+  out.row_shift = log2_of(state_bytes(kd, cfg->head_dim) / 16);
+  out.record_pieces = kd == QSA_Q4_1 ? cfg->head_dim / 64 : 0;
   return out;
 }
 

@@ -25,35 +25,6 @@ namespace {
 constexpr int kThreads = 128;
 __device__ int g_bad_pages;
 
-// The sequence of row r and the row's position in it, for all threads of the
-// CTA; -1 when no range holds the row.
-__device__ __forceinline__ int row_sequence(const PagedAppendParams& p, int r, int& pos) {
-  int seq = 0;
-  for (int i0 = 0; i0 < p.n_seqs; i0 += kThreads) {
-    const int i = i0 + (int)threadIdx.x;
-    const int n = __syncthreads_count(i < p.n_seqs && __ldcg(p.row_start + i + 1) <= r);
-    seq += n;
-    if (n < kThreads) break;
-  }
-  if (seq >= p.n_seqs || r < __ldcg(p.row_start + seq)) return -1;
-  pos = max(__ldcg(p.lens + seq), 0) - (min(__ldcg(p.row_start + seq + 1), p.n_rows) - r);
-  return seq;
-}
-
-// The row's page and slot; false when it has none.
-__device__ __forceinline__ bool row_page(const PagedAppendParams& p, int seq, int pos, int64_t& page, int64_t& slot) {
-  if (seq < 0 || pos < 0) return false;
-  const int64_t j = pos >> p.page_shift;
-  const int32_t id = j < p.table_ld ? __ldcg(p.table + seq * p.table_ld + j) : -1;
-  if ((uint32_t)id >= (uint32_t)p.n_pages) {
-    if (threadIdx.x == 0) atomicAdd(&g_bad_pages, 1);
-    return false;
-  }
-  page = id;
-  slot = pos & ((1 << p.page_shift) - 1);
-  return true;
-}
-
 // ES: bytes of an element.
 template <int ES>
 __global__ void __launch_bounds__(kThreads) paged_copy_kernel(const PagedAppendParams p) {
@@ -76,7 +47,7 @@ __global__ void __launch_bounds__(kThreads) paged_copy_kernel(const PagedAppendP
   }
   int pos = 0;
   int64_t page, slot;
-  if (!row_page(p, row_sequence(p, r, pos), pos, page, slot)) return;
+  if (!paged::row_page(p, paged::row_sequence<kThreads>(p, r, pos), pos, page, slot, &g_bad_pages)) return;
   auto put = [&](int i, const uint4& x) {
     const int c = i % row_chunks, hv = i / row_chunks;
     const int which = hv >= p.n_kv_heads, h = which ? hv - p.n_kv_heads : hv;
@@ -119,7 +90,7 @@ __global__ void __launch_bounds__(kThreads) paged_quantize_kernel(const PagedApp
   if (warp < rows) load(warp, x);
   int pos = 0;
   int64_t page, slot;
-  if (!row_page(p, row_sequence(p, r, pos), pos, page, slot)) return;
+  if (!paged::row_page(p, paged::row_sequence<kThreads>(p, r, pos), pos, page, slot, &g_bad_pages)) return;
   for (int hv = warp; hv < rows; hv += kThreads / 32) {
     if (hv != warp) load(hv, x);
     const int which = hv >= p.n_kv_heads, h = which ? hv - p.n_kv_heads : hv;

@@ -1,0 +1,385 @@
+// A batch's rows into the pages of a cache with a rotation on the way, 4-bit
+// caches, and rows back out of their pages (include/qsa.h,
+// qsa_paged_append_rotate, qsa_paged_append of 4-bit caches, qsa_paged_read).
+//
+// Writing: one CTA a row.  Its loads of Q, K and V are issued first, then the row's
+// sequence and position are found and the (cos, sin) of its pairs put into shared
+// memory once for all heads.  Rows that are stored as they are (f32, bf16) and Q go
+// in jobs of the two 16-byte pieces that a rotation joins; a row that is quantized
+// is a warp's, D / 32 channels a lane, its pairs exchanged by shuffles.  K is
+// rounded to the rows' type before it is stored or quantized, so the cache holds
+// what the rotation by itself and the append leave.
+//
+// 4 bits: blocks of 32 channels are 4 lanes (D = 256) or 8 (128): minimum and maximum
+// by shuffles; the codes' order in the row (16-bit unit n * (D / 32) + g holds
+// channels 32 g + 4 n .. + 3) gives each lane one 32-bit word of two units that two
+// other lanes hold.
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "qsa_attn_common.cuh"
+#include "qsa_paged.cuh"
+#include "qsa_rope.cuh"
+
+namespace qsa {
+
+namespace {
+
+using namespace paged;
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+__device__ int g_bad_pages;
+
+// D / 32 consecutive values of a row of bf16 from lane * (D / 32) on.
+template <int D>
+__device__ __forceinline__ void load_lane(const __nv_bfloat16* src, uint32_t (&u)[D / 64]) {
+  if constexpr (D == 256) {
+    const uint4 w = *reinterpret_cast<const uint4*>(src);
+    u[0] = w.x, u[1] = w.y, u[2] = w.z, u[3] = w.w;
+  } else {
+    const uint2 w = *reinterpret_cast<const uint2*>(src);
+    u[0] = w.x, u[1] = w.y;
+  }
+}
+
+// The rotation of a row that lies over a warp, rounded to bf16.
+template <int D>
+__device__ __forceinline__ void rotate_lane(uint32_t (&u)[D / 64], const qsa_rope& r, const float2* cs, int lane) {
+  constexpr int PER = D / 32;
+  const int c0 = lane * PER, half = r.rot_dim / 2;
+  const bool turns = c0 < r.rot_dim, upper = c0 >= half;
+  uint32_t y[D / 64];
+  if (r.pairs) {
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k) {
+      const float2 t = cs[turns ? c0 / 2 + k : 0];
+      const float a = bf16_lo(u[k]), b = bf16_hi(u[k]);
+      const __nv_bfloat162 w = __floats2bfloat162_rn(rope::low_of(a, b, t), rope::high_of(a, b, t));
+      y[k] = *reinterpret_cast<const uint32_t*>(&w);
+    }
+  } else {
+    // (rot_dim is a multiple of 16: half of it is whole lanes.)
+    const int from = turns ? (upper ? lane - half / PER : lane + half / PER) : lane;
+    const int i0 = turns ? c0 - (upper ? half : 0) : 0;
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k) {
+      const uint32_t other = __shfl_sync(0xffffffffu, u[k], from);
+      const float2 t0 = cs[i0 + 2 * k], t1 = cs[i0 + 2 * k + 1];
+      const float m0 = bf16_lo(u[k]), m1 = bf16_hi(u[k]), o0 = bf16_lo(other), o1 = bf16_hi(other);
+      const __nv_bfloat162 w = upper ? __floats2bfloat162_rn(rope::high_of(o0, m0, t0), rope::high_of(o1, m1, t1))
+                                     : __floats2bfloat162_rn(rope::low_of(m0, o0, t0), rope::low_of(m1, o1, t1));
+      y[k] = *reinterpret_cast<const uint32_t*>(&w);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < D / 64; ++k) u[k] = turns ? y[k] : u[k];
+}
+
+// A row that lies over a warp, as E4M3 codes and a scale (as qsa_append_tokens).
+template <int D>
+__device__ __forceinline__ void store_fp8(const PagedAppendParams& p, const uint32_t (&u)[D / 64], int which, int64_t row,
+                                          int64_t record, int lane) {
+  constexpr int PER = D / 32;
+  float x[PER];
+#pragma unroll
+  for (int k = 0; k < PER / 2; ++k) {
+    x[2 * k] = bf16_lo(u[k]);
+    x[2 * k + 1] = bf16_hi(u[k]);
+  }
+  float amax = 0.f;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) amax = fmaxf(amax, fabsf(x[k]));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const __half sh = __float2half_rn(__fdiv_rn(amax, 448.0f));
+  const float sc = __half2float(sh);
+  uint32_t c[PER / 2];
+#pragma unroll
+  for (int k = 0; k < PER / 2; ++k) c[k] = e4m3_codes(x[2 * k], x[2 * k + 1], sc);
+  uint8_t* dst = static_cast<uint8_t*>(which ? p.v : p.k) + row + lane * PER;
+  if constexpr (PER == 8)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = c[0] | (c[1] << 16);
+  if (lane == 0) static_cast<__half*>(p.kv_scale)[2 * record + which] = sh;
+}
+
+// ... as 4-bit codes with a scale and a minimum for each 32 channels.
+template <int D>
+__device__ __forceinline__ void store_q4(const PagedAppendParams& p, const uint32_t (&u)[D / 64], int which, int64_t row,
+                                         int64_t record, int lane) {
+  constexpr int PER = D / 32, G = D / 32, LB = 32 / G;   // LB: lanes of a block
+  float x[PER];
+#pragma unroll
+  for (int k = 0; k < PER / 2; ++k) {
+    x[2 * k] = bf16_lo(u[k]);
+    x[2 * k + 1] = bf16_hi(u[k]);
+  }
+  float lo = INFINITY, hi = -INFINITY;
+  bool odd = false;   // infinity or NaN in the block
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    lo = fminf(lo, x[k]);
+    hi = fmaxf(hi, x[k]);
+    odd |= !(fabsf(x[k]) < INFINITY);
+  }
+#pragma unroll
+  for (int o = LB / 2; o; o >>= 1) {
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  }
+  odd = ((__ballot_sync(0xffffffffu, odd) >> (lane / LB * LB)) & ((1u << LB) - 1u)) != 0u;
+  const __half mh = __float2half_rn(lo);
+  __half sh = __float2half_rn(__fdiv_rn(hi - lo, 15.0f));
+  if (odd || __hisinf(mh) || __hisinf(sh)) sh = __ushort_as_half((unsigned short)0x7fff);
+  const float m = __half2float(mh), s = __half2float(sh);
+  uint32_t codes = 0u;   // 4 bits a channel
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    // (A scale that is 0 or NaN leaves code 0.)
+    const float c = s > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(x[k] - m, s)), 0.f), 15.f) : 0.f;
+    codes |= (uint32_t)c << (4 * k);
+  }
+  // 32-bit word w of the row: units 2 w and 2 w + 1, of blocks g and g + 1 and the same n.
+  uint8_t* dst = static_cast<uint8_t*>(which ? p.v : p.k) + row;
+  const int n = 2 * lane / G, g = (2 * lane) % G;
+  if constexpr (D == 256) {   // lane 4 g + n / 2 holds units n (even: low half)
+    const uint32_t a = __shfl_sync(0xffffffffu, codes, 4 * g + n / 2), b = __shfl_sync(0xffffffffu, codes, 4 * g + 4 + n / 2);
+    reinterpret_cast<uint32_t*>(dst)[lane] = __byte_perm(a, b, n & 1 ? 0x7632 : 0x5410);
+  } else {                    // lane 8 g + n holds unit n
+    const uint32_t a = __shfl_sync(0xffffffffu, codes, (8 * g + n) & 31), b = __shfl_sync(0xffffffffu, codes, (8 * g + 8 + n) & 31);
+    if (lane < 16) reinterpret_cast<uint32_t*>(dst)[lane] = __byte_perm(a, b, 0x5410);
+  }
+  if (lane % LB == 0) {
+    const __half2 pair = __halves2half2(sh, mh);
+    reinterpret_cast<__half2*>(static_cast<char*>(p.kv_scale) + record * (D / 4))[which * G + lane / LB] = pair;
+  }
+}
+
+// STATE: how the cache holds K and V.  D: head_dim.
+template <int STATE, int D>
+__global__ void __launch_bounds__(kThreads) paged_rows_kernel(const __grid_constant__ PagedRowsParams p) {
+  constexpr bool QUANT = STATE == QSA_FP8_E4M3 || STATE == QSA_Q4_1;
+  constexpr int ES = STATE == QSA_F32 ? 4 : 2;          // of the rows
+  constexpr int J = D * ES / 32;                        // jobs of a head
+  const PagedAppendParams& a = p.a;
+  __shared__ __align__(16) float2 cs[QSA_MAX_ROPE_PAIRS];
+  grid_dependency_sync();
+  const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int r = (int)blockIdx.x;
+  const int q_heads = p.q ? p.n_q_heads : 0;
+  // Job i of the row: Q's heads, then (rows stored as they are) K's and V's.
+  const int jobs = (q_heads + (QUANT ? 0 : 2 * a.n_kv_heads)) * J;
+  auto source = [&](int hh) {
+    if (hh < q_heads) return static_cast<const char*>(p.q) + (r * p.q_row_stride + hh * p.q_head_stride) * ES;
+    const int hv = hh - q_heads, which = hv >= a.n_kv_heads, h = which ? hv - a.n_kv_heads : hv;
+    return static_cast<const char*>(which ? a.v_new : a.k_new) + (r * a.row_stride + h * a.new_head_stride) * ES;
+  };
+  constexpr int kAhead = 2;
+  uint4 x0[kAhead], x1[kAhead];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = i0 + k * kThreads;
+      if (i >= jobs) continue;
+      const rope::Job b = rope::job_of<ES>(p.rope.rot_dim, p.rope.pairs, i % J);
+      const char* from = source(i / J);
+      x0[k] = *reinterpret_cast<const uint4*>(from + 16 * b.p0);
+      x1[k] = *reinterpret_cast<const uint4*>(from + 16 * b.p1);
+    }
+  };
+  // Rows that are quantized: the first of the warp's.
+  uint32_t u[QUANT ? D / 64 : 1];
+  auto load_row = [&](int hv) {
+    const int which = hv >= a.n_kv_heads, h = which ? hv - a.n_kv_heads : hv;
+    if constexpr (QUANT)
+      load_lane<D>(static_cast<const __nv_bfloat16*>(which ? a.v_new : a.k_new) + r * a.row_stride + h * a.new_head_stride +
+                       lane * (D / 32),
+                   u);
+  };
+  if (QUANT && warp < 2 * a.n_kv_heads) load_row(warp);
+  load(tid);
+  int pos = 0;
+  int64_t page = 0, slot = 0;
+  const int seq = row_sequence<kThreads>(a, r, pos);
+  if (seq < 0) return;
+  const bool stored = row_page(a, seq, pos, page, slot, &g_bad_pages);
+  if (tid < p.rope.rot_dim / 2) cs[tid] = rope::turn(p.rope, tid, pos);
+  __syncthreads();
+  for (int i0 = tid; i0 < jobs; i0 += kAhead * kThreads) {
+    if (i0 != tid) load(i0);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = i0 + k * kThreads;
+      if (i >= jobs) continue;
+      const int hh = i / J, j = i % J;
+      const rope::Job b = rope::job_of<ES>(p.rope.rot_dim, p.rope.pairs, j);
+      const int hv = hh - q_heads;
+      if (b.turns && hv < a.n_kv_heads) rope::rotate_job<ES>(x0[k], x1[k], p.rope.pairs, j, cs);
+      char* to;
+      if (hv < 0) {
+        to = static_cast<char*>(p.q_out) + ((int64_t)r * q_heads + hh) * (D * ES);
+      } else {
+        if (!stored) continue;
+        const int which = hv >= a.n_kv_heads, h = which ? hv - a.n_kv_heads : hv;
+        to = static_cast<char*>(which ? a.v : a.k) + (page * a.page_stride + h * a.head_stride + slot * a.tok_stride) * ES;
+      }
+      *reinterpret_cast<uint4*>(to + 16 * b.p0) = x0[k];
+      *reinterpret_cast<uint4*>(to + 16 * b.p1) = x1[k];
+    }
+  }
+  if constexpr (QUANT) {
+    if (!stored) return;
+    for (int hv = warp; hv < 2 * a.n_kv_heads; hv += kWarps) {
+      if (hv != warp) load_row(hv);
+      const int which = hv >= a.n_kv_heads, h = which ? hv - a.n_kv_heads : hv;
+      if (which == 0 && p.rope.rot_dim > 0) rotate_lane<D>(u, p.rope, cs, lane);
+      const int64_t at = page * a.page_stride + h * a.head_stride + slot * a.tok_stride;
+      const int64_t record = page * a.s_page_stride + h * a.s_head_stride + slot * a.s_tok_stride;
+      if constexpr (STATE == QSA_Q4_1) store_q4<D>(a, u, which, at / 2, record, lane);
+      else store_fp8<D>(a, u, which, at, record, lane);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ reading
+// A warp takes rows_warp rows: lane i looks up row i's page, so their chains of
+// dependent reads (range, length, table) run side by side; then K and V of every head
+// of a row at a time, D / 32 values a lane.
+template <typename OUT>
+__device__ __forceinline__ void put4(OUT* to, float a, float b, float c, float d) {
+  if constexpr (sizeof(OUT) == 4) {
+    *reinterpret_cast<float4*>(to) = make_float4(a, b, c, d);
+  } else {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(a, b), hi = __floats2bfloat162_rn(c, d);
+    *reinterpret_cast<uint2*>(to) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  }
+}
+
+template <int STATE, int D, typename OUT>
+__global__ void __launch_bounds__(kThreads) paged_read_kernel(const __grid_constant__ PagedReadParams p) {
+  const PagedAppendParams& a = p.a;
+  grid_dependency_sync();
+  const int lane = (int)threadIdx.x & 31;
+  const int r0 = ((int)blockIdx.x * kWarps + ((int)threadIdx.x >> 5)) * p.rows_warp;
+  // This lane's row.
+  int64_t page = -1, slot = 0;
+  const int mine = r0 + lane;
+  if (lane < p.rows_warp && mine < a.n_rows) {
+    int lo = 0, hi = a.n_seqs;   // the sequences that end at or before it: found in [lo, hi]
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldcg(a.row_start + mid + 1) <= mine) lo = mid + 1;
+      else hi = mid;
+    }
+    if (lo < a.n_seqs && mine >= __ldcg(a.row_start + lo)) {
+      const int pos = max(__ldcg(a.lens + lo), 0) - (min(__ldcg(a.row_start + lo + 1), a.n_rows) - mine);
+      if (pos >= 0) {
+        const int64_t j = pos >> a.page_shift;
+        const int32_t id = j < a.table_ld ? __ldcg(a.table + lo * a.table_ld + j) : -1;
+        slot = pos & ((1 << a.page_shift) - 1);
+        if ((uint32_t)id < (uint32_t)a.n_pages) page = id;
+        else atomicAdd(&g_bad_pages, 1);
+      }
+    }
+  }
+  const int n = min(p.rows_warp, a.n_rows - r0), all = 2 * a.n_kv_heads;
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    const int64_t pg = __shfl_sync(0xffffffffu, page, i), sl = __shfl_sync(0xffffffffu, slot, i);
+    if (pg < 0) continue;
+#pragma unroll 4
+    for (int hv = 0; hv < all; ++hv) {
+      const int which = hv >= a.n_kv_heads, h = which ? hv - a.n_kv_heads : hv;
+      const int64_t at = pg * a.page_stride + h * a.head_stride + sl * a.tok_stride;
+      const int64_t record = pg * a.s_page_stride + h * a.s_head_stride + sl * a.s_tok_stride;
+      const char* from = static_cast<const char*>(which ? a.v : a.k);
+      OUT* to = static_cast<OUT*>(which ? p.v_out : p.k_out) + ((int64_t)(r0 + i) * a.n_kv_heads + h) * D;
+      if constexpr (STATE == QSA_Q4_1) {
+        constexpr int G = D / 32;
+        if (lane >= D / 8) continue;   // a lane a 32-bit word: units n of blocks g and g + 1
+        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(from + at / 2) + lane);
+        const int unit = 2 * lane, nn = unit / G, g = unit % G;
+        const uint2 rec = __ldg(reinterpret_cast<const uint2*>(static_cast<const char*>(a.kv_scale) + record * (D / 4) +
+                                                               which * (G * 4) + g * 4));
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const uint32_t word = b ? rec.y : rec.x;
+          const __half2 sm = *reinterpret_cast<const __half2*>(&word);
+          const float s = __low2float(sm), m = __high2float(sm);
+          const uint32_t c = w >> (16 * b);
+          put4(to + 32 * (g + b) + 4 * nn, fmaf((float)(c & 15u), s, m), fmaf((float)((c >> 4) & 15u), s, m),
+               fmaf((float)((c >> 8) & 15u), s, m), fmaf((float)((c >> 12) & 15u), s, m));
+        }
+      } else {
+        constexpr int ES = STATE == QSA_F32 ? 4 : STATE == QSA_BF16 ? 2 : 1;
+#pragma unroll
+        for (int c0 = 0; c0 < D; c0 += 128) {
+          const char* src = from + (at + c0 + lane * 4) * ES;
+          float x[4];
+          if constexpr (STATE == QSA_F32) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(src));
+            x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+          } else if constexpr (STATE == QSA_BF16) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+            x[0] = bf16_lo(v.x), x[1] = bf16_hi(v.x), x[2] = bf16_lo(v.y), x[3] = bf16_hi(v.y);
+          } else {
+            const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(src));
+            const float s = __half2float(__ldg(static_cast<const __half*>(a.kv_scale) + 2 * record + which));
+            const uint32_t b0 = attn::e4m3x2_to_bf16x2(v & 0xffffu), b1 = attn::e4m3x2_to_bf16x2(v >> 16);
+            x[0] = bf16_lo(b0) * s, x[1] = bf16_hi(b0) * s, x[2] = bf16_lo(b1) * s, x[3] = bf16_hi(b1) * s;
+          }
+          put4(to + c0 + lane * 4, x[0], x[1], x[2], x[3]);
+        }
+      }
+    }
+  }
+}
+
+template <int STATE>
+cudaError_t launch_rows(const PagedRowsParams& p, cudaStream_t st) {
+  const dim3 grid((unsigned)p.a.n_rows), block(kThreads);
+  return p.a.head_dim == 256 ? launch_kernel(paged_rows_kernel<STATE, 256>, grid, block, 0, st, 0u, p)
+                             : launch_kernel(paged_rows_kernel<STATE, 128>, grid, block, 0, st, 0u, p);
+}
+
+template <int STATE, typename OUT>
+cudaError_t launch_read(const PagedReadParams& p, cudaStream_t st) {
+  const dim3 grid((unsigned)((p.a.n_rows + kWarps * p.rows_warp - 1) / (kWarps * p.rows_warp))), block(kThreads);
+  return p.a.head_dim == 256 ? launch_kernel(paged_read_kernel<STATE, 256, OUT>, grid, block, 0, st, 0u, p)
+                             : launch_kernel(paged_read_kernel<STATE, 128, OUT>, grid, block, 0, st, 0u, p);
+}
+template <int STATE>
+cudaError_t launch_read_as(const PagedReadParams& p, qsa_dtype out, cudaStream_t st) {
+  return out == QSA_F32 ? launch_read<STATE, float>(p, st) : launch_read<STATE, __nv_bfloat16>(p, st);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_rows(const PagedRowsParams& p, qsa_dtype kv_dtype, cudaStream_t st) {
+  switch (kv_dtype) {
+    case QSA_F32: return launch_rows<QSA_F32>(p, st);
+    case QSA_BF16: return launch_rows<QSA_BF16>(p, st);
+    case QSA_FP8_E4M3: return launch_rows<QSA_FP8_E4M3>(p, st);
+    default: return launch_rows<QSA_Q4_1>(p, st);
+  }
+}
+
+cudaError_t launch_paged_read(PagedReadParams p, qsa_dtype kv_dtype, qsa_dtype out_dtype, cudaStream_t st) {
+  // As many rows a warp as leave a warp for every SM's place.
+  const int64_t warps = (int64_t)device_sm_count() * 64;
+  p.rows_warp = 1;
+  while (p.rows_warp < 32 && p.a.n_rows > warps * p.rows_warp) p.rows_warp *= 2;
+  switch (kv_dtype) {
+    case QSA_F32: return launch_read_as<QSA_F32>(p, out_dtype, st);
+    case QSA_BF16: return launch_read_as<QSA_BF16>(p, out_dtype, st);
+    case QSA_FP8_E4M3: return launch_read_as<QSA_FP8_E4M3>(p, out_dtype, st);
+    default: return launch_read_as<QSA_Q4_1>(p, out_dtype, st);
+  }
+}
+
+int paged_rows_bad_pages_take() { return take_counter(g_bad_pages); }
+
+}  // namespace qsa

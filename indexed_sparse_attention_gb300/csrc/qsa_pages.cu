@@ -273,9 +273,15 @@ __device__ __forceinline__ void copy_page(const PageCaches& cs, const PageCache&
   if (which == 0 && c.kv_scale) {
     const char* sf = static_cast<const char*>(c.kv_scale) + src * c.s_page_stride;
     char* st = static_cast<char*>(c.kv_scale) + dst * c.s_page_stride;
-    for (int r = (int)threadIdx.x; r < rows; r += kCopyThreads) {
+    for (int i = (int)threadIdx.x; i < rows * max(cs.record_pieces, 1); i += kCopyThreads) {
+      const int r = cs.record_pieces > 1 ? i / cs.record_pieces : i;
       const int64_t o = (r / fill) * c.s_head_stride + (r % fill) * c.s_tok_stride;
-      *reinterpret_cast<uint32_t*>(st + o) = *reinterpret_cast<const uint32_t*>(sf + o);
+      if (cs.record_pieces == 0) {
+        *reinterpret_cast<uint32_t*>(st + o) = *reinterpret_cast<const uint32_t*>(sf + o);
+      } else {
+        const int64_t at = o + (i - r * cs.record_pieces) * 16;
+        *reinterpret_cast<uint4*>(st + at) = *reinterpret_cast<const uint4*>(sf + at);
+      }
     }
   }
 }

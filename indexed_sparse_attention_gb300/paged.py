@@ -5,7 +5,7 @@
     batch = PagedBatch(pages.table, pages.step_lens, row_start, n_rows=R, max_rows=M)
     pages.extend(seqs, n_new)                            # room for the step's tokens, and its lengths
     step = PagedStep(caches[layer], batch, q, window=W, n_sinks=S)
-    out, lse = step.run(k_new, v_new)                    # append, then attend
+    out, lse = step.run(k_new, v_new)                    # append, then attend (with rope=: rotate K and q on the way)
 """
 from __future__ import annotations
 
@@ -15,7 +15,9 @@ from typing import Sequence
 
 import torch
 
-from . import AttnConfig, BF16, F32, FP8, _check, _dtype_code, _ptr, _scratch, lib
+from . import AttnConfig, BF16, F32, FP8, Q4, _dtype_code, _ptr, _scratch, lib
+from .calls import _call
+from .rope import Rope, RopeDesc, _strides
 
 
 class PagedCacheDesc(ctypes.Structure):
@@ -50,6 +52,8 @@ def declare(L: ctypes.CDLL):
     L.qsa_paged_attn_workspace_size.restype = sz
     L.qsa_paged_attn.argtypes = [cachep, batchp, cfgp, i32, i32, vp, vp, vp, vp, sz, vp]
     L.qsa_paged_append.argtypes = [cachep, batchp, cfgp, vp, vp, i64, i64, vp]
+    L.qsa_paged_append_rotate.argtypes = [cachep, batchp, cfgp, ctypes.POINTER(RopeDesc), vp, vp, i64, i64, vp, i64, i64, vp, vp]
+    L.qsa_paged_read.argtypes = [cachep, batchp, cfgp, vp, vp, vp]
     L.qsa_pages_workspace_size.argtypes = [poolp]
     L.qsa_pages_workspace_size.restype = sz
     L.qsa_pages_extend.argtypes = [poolp, vp, vp, i32, vp]
@@ -58,38 +62,10 @@ def declare(L: ctypes.CDLL):
     L.qsa_pages_free.argtypes = [poolp, vp, vp, i32, vp]
     L.qsa_pages_compact.argtypes = [poolp, cachep, i32, cfgp, vp, vp, sz, vp]
     L.qsa_pages_copy.argtypes = [cachep, i32, cfgp, vp, vp, i32, vp]
-    for name in ("attn", "append"):
+    for name in ("attn", "append", "append_rotate", "read"):
         getattr(L, f"qsa_paged_{name}").restype = i32
     for name in ("extend", "extend_step", "fork", "free", "compact", "copy"):
         getattr(L, f"qsa_pages_{name}").restype = i32
-
-
-# ---------------------------------------------------------------------- devices and streams
-
-#: The handle of a device's current stream; torch.cuda.current_stream builds a Stream object around it (2 us a call).
-_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
-def _raw_stream(stream, device) -> int:
-    if stream is None:
-        return _current_stream(device.index)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _call(name: str, device, stream, *args):
-    """One library call with the tensors' device as the current one (the library
-    launches there), on `stream` or that device's current stream."""
-    if device.type != "cuda":
-        raise ValueError(f"{name}: the tensors are on {device}, not on a GPU")
-    fn = getattr(lib(), name)
-    if device.index == torch.cuda.current_device():
-        status = fn(*args, _raw_stream(stream, device))
-    else:
-        with torch.cuda.device(device):
-            status = fn(*args, _raw_stream(stream, device))
-    if status:
-        _check(name, status)
 
 
 def _int_list(name: str, t: torch.Tensor, like: torch.Tensor) -> torch.Tensor:
@@ -106,36 +82,70 @@ class PagedCache:
     """One layer's cache: k, v are [n_pages, Hkv, page_tokens, D] views (channel
     stride 1, equal strides; any order of the other axes in memory).  fp8: E4M3
     codes (float8_e4m3fn or uint8) and kv_scale, an [n_pages, Hkv, page_tokens, 2]
-    float16 view of the (K, V) scale pairs."""
+    float16 view of the (K, V) scale pairs.  4 bits (kv_dtype=Q4): uint8 views of
+    [n_pages, Hkv, page_tokens, D / 2] codes and an [n_pages, Hkv, page_tokens, D / 8]
+    float16 view of the records, (scale, minimum) of K's blocks, then V's; the order of
+    the codes is include/qsa.h's, and paged_append and paged_read write and read it.
+    PagedCache.zeros makes a cache of any kind."""
 
-    def __init__(self, k: torch.Tensor, v: torch.Tensor, kv_scale: torch.Tensor | None = None):
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, kv_scale: torch.Tensor | None = None,
+                 kv_dtype: int | None = None):
         if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
             raise ValueError("k and v must be [n_pages, Hkv, page_tokens, D] of one shape, dtype and device")
         if k.stride(3) != 1 or k.stride() != v.stride():
             raise TypeError("k and v need unit channel stride and equal strides")
         self.k, self.v, self.kv_scale = k, v, kv_scale
         self.n_pages, self.n_kv_heads, self.page_tokens, self.head_dim = (int(x) for x in k.shape)
-        self.kv_dtype = _dtype_code(k)
+        self.kv_dtype = _dtype_code(k) if kv_dtype is None else int(kv_dtype)
+        q4 = self.kv_dtype == Q4
+        if kv_dtype is not None and (k.dtype is not torch.uint8 if q4 else self.kv_dtype != _dtype_code(k)):
+            raise TypeError(f"kv_dtype {kv_dtype} does not hold {k.dtype}")
+        per = 2 if q4 else 1   # elements of a byte
+        self.head_dim *= per
         d = self.desc = PagedCacheDesc()
         d.k, d.v = k.data_ptr(), v.data_ptr()
-        d.page_stride, d.head_stride, d.tok_stride = k.stride(0), k.stride(1), k.stride(2)
+        d.page_stride, d.head_stride, d.tok_stride = (per * k.stride(i) for i in range(3))
         d.n_pages, d.page_tokens = self.n_pages, self.page_tokens
-        if (kv_scale is not None) != (self.kv_dtype == FP8):
-            raise ValueError("kv_scale goes with an fp8 cache")
+        if (kv_scale is not None) != (self.kv_dtype in (FP8, Q4)):
+            raise ValueError("kv_scale goes with an fp8 or 4-bit cache")
         if kv_scale is not None:
             s = kv_scale
-            if s.dtype != torch.float16 or tuple(s.shape) != (*k.shape[:3], 2) or s.stride(3) != 1 or any(
-                    s.stride(i) % 2 for i in range(3)):
-                raise TypeError("kv_scale must be a float16 [n_pages, Hkv, page_tokens, 2] view of whole scale records")
+            n = self.head_dim // 8 if q4 else 2   # halves of a record
+            if s.dtype != torch.float16 or tuple(s.shape) != (*k.shape[:3], n) or s.stride(3) != 1 or any(
+                    s.stride(i) % n for i in range(3)):
+                raise TypeError(f"kv_scale must be a float16 [n_pages, Hkv, page_tokens, {n}] view of whole scale records")
             if s.device != k.device:
                 raise ValueError("kv_scale on another device than k")
             d.kv_scale = s.data_ptr()
-            d.scale_page_stride, d.scale_head_stride, d.scale_tok_stride = (s.stride(i) // 2 for i in range(3))
+            d.scale_page_stride, d.scale_head_stride, d.scale_tok_stride = (s.stride(i) // n for i in range(3))
         self.byref = ctypes.byref(d)
         self.device = k.device
         self.row_dtype = torch.float32 if self.kv_dtype == F32 else torch.bfloat16   # of new rows and queries
         self._row_cfg = self.config()
         self._row_cfg_ref = ctypes.byref(self._row_cfg)
+        self._read_cfg = [ctypes.byref(self.config(out_dtype=t)) for t in (torch.float32, torch.bfloat16)]
+        self._rows_cfgs = {}
+
+    def _rows_cfg(self, n_q_heads: int):
+        if n_q_heads not in self._rows_cfgs:
+            self._rows_cfgs[n_q_heads] = ctypes.byref(self.config(n_q_heads))
+        return self._rows_cfgs[n_q_heads]
+
+    @classmethod
+    def zeros(cls, n_pages: int, n_kv_heads: int, page_tokens: int, head_dim: int, kv_dtype: int = BF16,
+              device="cuda") -> "PagedCache":
+        """A cache of zeros, its pages' heads one after the other; kv_dtype F32, BF16, FP8 or Q4."""
+        kinds = {F32: torch.float32, BF16: torch.bfloat16, FP8: torch.float8_e4m3fn, Q4: torch.uint8}
+        if kv_dtype not in kinds:
+            raise ValueError(f"no paged cache of kv_dtype {kv_dtype}")
+        if kv_dtype == Q4 and int(head_dim) % 32:
+            raise ValueError(f"4-bit rows are blocks of 32 channels, head_dim is {head_dim}")
+        shape = (int(n_pages), int(n_kv_heads), int(page_tokens))
+        width = int(head_dim) // 2 if kv_dtype == Q4 else int(head_dim)
+        k, v = (torch.zeros(*shape, width, dtype=kinds[kv_dtype], device=device) for _ in range(2))
+        record = {FP8: 2, Q4: int(head_dim) // 8}.get(kv_dtype)
+        scale = None if record is None else torch.zeros(*shape, record, dtype=torch.float16, device=device)
+        return cls(k, v, scale, kv_dtype)
 
     def config(self, n_q_heads: int | None = None, out_dtype=torch.float32, scale: float = 0.0,
                n_splits: int = 0) -> AttnConfig:
@@ -231,9 +241,12 @@ def paged_attn(cache: PagedCache, batch: PagedBatch, q: torch.Tensor, out: torch
           int(n_sinks), q.data_ptr(), out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel())
 
 
-def paged_append(cache: PagedCache, batch: PagedBatch, k_new: torch.Tensor, v_new: torch.Tensor, stream=None):
+def paged_append(cache: PagedCache, batch: PagedBatch, k_new: torch.Tensor, v_new: torch.Tensor, stream=None, *,
+                 rope: Rope | None = None, q: torch.Tensor | None = None, q_out: torch.Tensor | None = None):
     """Write the batch's rows k_new, v_new ([n_rows, Hkv, D], unit channel stride,
-    equal strides: slices of one projection will do) into their pages."""
+    equal strides: slices of one projection will do) into their pages.  With rope, K
+    is rotated for the rows' positions on the way, and q [n_rows, Hq, D] (unit channel
+    stride; a slice of the projection will do) into q_out, contiguous, beside it."""
     shape = (batch.n_rows, cache.n_kv_heads, cache.head_dim)
     _check_rows("k_new", k_new, shape, cache.row_dtype, cache.device)
     _check_rows("v_new", v_new, shape, cache.row_dtype, cache.device)
@@ -241,8 +254,41 @@ def paged_append(cache: PagedCache, batch: PagedBatch, k_new: torch.Tensor, v_ne
     if strides != v_new.stride() or strides[2] != 1:
         raise ValueError("k_new and v_new need unit channel stride and equal strides")
     _check_batch(cache, batch)
-    _call("qsa_paged_append", cache.device, stream, cache.byref, batch.byref, cache._row_cfg_ref, k_new.data_ptr(),
-          v_new.data_ptr(), strides[0], strides[1])
+    if rope is None:
+        if q is not None or q_out is not None:
+            raise ValueError("q and q_out go with a rope")
+        _call("qsa_paged_append", cache.device, stream, cache.byref, batch.byref, cache._row_cfg_ref, k_new.data_ptr(),
+              v_new.data_ptr(), strides[0], strides[1])
+        return
+    cfg, at_q, to_q, q_strides = cache._row_cfg_ref, None, None, (0, 0)
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        if q.dim() != 3 or q.stride(2) != 1:
+            raise ValueError("q must be [n_rows, Hq, D] with unit channel stride")
+        _check_rows("q", q, (batch.n_rows, q.shape[1], cache.head_dim), cache.row_dtype, cache.device)
+        _check_rows("q_out", q_out, q.shape, cache.row_dtype, cache.device)
+        if not q_out.is_contiguous():
+            raise ValueError("q_out must be contiguous")
+        cfg = cache._rows_cfg(q.shape[1])
+        at_q, to_q, q_strides = q.data_ptr(), q_out.data_ptr(), _strides(q)
+    _call("qsa_paged_append_rotate", cache.device, stream, cache.byref, batch.byref, cfg, rope.byref, k_new.data_ptr(),
+          v_new.data_ptr(), *_strides(k_new), at_q, *q_strides, to_q)
+
+
+def paged_read(cache: PagedCache, batch: PagedBatch, k_out: torch.Tensor, v_out: torch.Tensor, stream=None):
+    """The batch's rows back out of their pages, into k_out and v_out ([n_rows, Hkv, D],
+    contiguous, both f32 or both bf16); rows without a page are left as they were."""
+    shape = (batch.n_rows, cache.n_kv_heads, cache.head_dim)
+    if k_out.dtype is not torch.float32 and k_out.dtype is not torch.bfloat16:
+        raise TypeError(f"k_out must be float32 or bfloat16, not {k_out.dtype}")
+    _check_rows("k_out", k_out, shape, k_out.dtype, cache.device)
+    _check_rows("v_out", v_out, shape, k_out.dtype, cache.device)
+    if not (k_out.is_contiguous() and v_out.is_contiguous()):
+        raise ValueError("k_out and v_out must be contiguous")
+    _check_batch(cache, batch)
+    _call("qsa_paged_read", cache.device, stream, cache.byref, batch.byref,
+          cache._read_cfg[k_out.dtype is torch.bfloat16], k_out.data_ptr(), v_out.data_ptr())
 
 
 class PagedStep:
@@ -254,13 +300,22 @@ class PagedStep:
     The buffers are allocated on the stream that is the current one when the step
     is made.  Before its first run on another stream, have that one wait for it
     (Stream.wait_stream): their memory may still be in use by work queued there.
-    One step's runs must not overlap each other."""
+    One step's runs must not overlap each other.
+
+    With a rope, q holds the queries before their rotation (a slice of the projection
+    that the new rows are slices of will do), append rotates K and them, these into
+    the step's q_rotated, and attend takes that."""
 
     def __init__(self, cache: PagedCache, batch: PagedBatch, q: torch.Tensor, *, out_dtype=torch.float32,
-                 window: int = 0, n_sinks: int = 0, scale: float = 0.0, n_splits: int = 0):
-        _check_queries(cache, batch, q)
+                 window: int = 0, n_sinks: int = 0, scale: float = 0.0, n_splits: int = 0, rope: Rope | None = None):
         dev = cache.device
-        self.cache, self.batch, self.q = cache, batch, q
+        self.cache, self.batch, self.rope, self.q_in = cache, batch, rope, q
+        if rope is not None:
+            if q.dim() != 3 or q.stride(2) != 1:
+                raise ValueError("q must be [n_rows, Hq, D] with unit channel stride")
+            q = self.q_rotated = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        _check_queries(cache, batch, q)
+        self.q = q
         self.window, self.n_sinks = int(window), int(n_sinks)
         self.cfg = cache.config(q.shape[1], out_dtype, scale, n_splits)
         self.out = torch.empty(q.shape, dtype=out_dtype, device=dev)
@@ -270,7 +325,10 @@ class PagedStep:
                       self.out.data_ptr(), self.lse.data_ptr(), self.ws.data_ptr(), self.ws.numel())
 
     def append(self, k_new: torch.Tensor, v_new: torch.Tensor, stream=None):
-        paged_append(self.cache, self.batch, k_new, v_new, stream)
+        if self.rope is None:
+            paged_append(self.cache, self.batch, k_new, v_new, stream)
+        else:
+            paged_append(self.cache, self.batch, k_new, v_new, stream, rope=self.rope, q=self.q_in, q_out=self.q_rotated)
 
     def attend(self, stream=None):
         _call("qsa_paged_attn", self.q.device, stream, *self._args)
