@@ -625,7 +625,8 @@ qsa_status qsa_rotate(const qsa_rope* rope, const int32_t* positions, int32_t n_
  * products want them.  The (K, V) record of (page, h, slot) is the K row's D / 32
  * pairs (scale, minimum) of f16, then the V row's: D / 4 bytes, 16-byte aligned, at
  * kv_scale + D / 4 * (page * scale_page_stride + ...).  Scales and minima may be any
- * f16 as they stand.
+ * f16 whose values for the codes 0 .. 15 lie within f16's +-65,504 (others: infinities
+ * and NaN).
  * f32, bf16, fp8 and 4-bit caches; QSA_Q8_0 caches are not paged (QSA_ERR_UNSUPPORTED). */
 typedef struct qsa_paged_cache {
   const void* k;               /* device, kv_dtype; written by the calls that write a cache */
@@ -697,10 +698,11 @@ typedef struct qsa_paged_batch {
  * exp(z - m) are rounded to bf16 for the product with V (at most 2^-8 of each,
  * independently), out once to out_dtype.  fp8: q enters as the sum of two 8-bit
  * codes a value, exact from 2^-13 of the largest magnitude of its row and head on,
- * and off by at most 2^-21 of that below.  4-bit: the logits are those of the
- * stored values (q is exact from 2^-25 of the largest magnitude of its row and head on,
- * off by at most 2^-33 of it below); weights are rounded to f16, alone and times V's
- * scales (2^-11 each).  The result depends on the
+ * and off by at most 2^-21 of that below.  4-bit: with up to 16 entries (max_rows *
+ * Hq / Hkv) the logits are those of the stored values, q exact from 2^-25 of the largest
+ * magnitude of its row and head on and off by at most 2^-33 of it below, and weights are
+ * rounded to f16, alone and times V's scales (2^-11 each); with more, K, V and the
+ * weights are rounded to f16 (2^-11 each).  The result depends on the
  * lengths and the number of runs, not on timing: it is reproducible.
  * Errors: QSA_ERR_INVALID_ARG, QSA_ERR_UNSUPPORTED, QSA_ERR_MISALIGNED,
  * QSA_ERR_WORKSPACE, QSA_ERR_CUDA.  n_rows == 0 or n_seqs == 0 is a no-op.
@@ -720,8 +722,9 @@ qsa_status qsa_paged_attn(const qsa_paged_cache* cache, const qsa_paged_batch* b
  *   minimum = f16(lo), scale = f16(f32(f32(hi - lo) / 15)),
  *   code = the integer nearest to f32(f32(x - minimum) / scale), ties to even, within
  *   0 .. 15 (0 where the scale is 0);
- * a block that holds an infinity or NaN, or whose scale or minimum f16 does not hold,
- * gets scale NaN and reads as NaN: nothing is cut off silently.
+ * a block that holds an infinity, NaN or a magnitude above 65,280 (the largest bf16
+ * value that f16 holds) gets scale NaN and minimum 0 and reads as NaN: nothing is cut
+ * off silently.
  *   cfg            n_kv_heads, head_dim, kv_dtype (the other fields are checked
  *                  as for qsa_paged_attn)
  *   k_new, v_new   device, element (r, h, d) at r * row_stride + h * head_stride

@@ -72,15 +72,19 @@ qsa_status check_batch(const qsa_paged_batch* b, const char* fn) {
 
 // Kernel of a call and how it divides the work.
 struct Plan {
-  bool tensor_cores;   // tcgen05 (bf16, fp8)
+  bool tensor_cores;   // tcgen05
   int mt;     // entries of an item
   int grid;   // runs
 };
 
 Plan plan_attn(const qsa_paged_batch* b, const qsa_attn_config* cfg) {
   Plan pl;
-  pl.tensor_cores = cfg->kv_dtype == QSA_BF16 || cfg->kv_dtype == QSA_FP8_E4M3;
-  if (cfg->kv_dtype == QSA_Q4_1) {
+  // 4 bits: up to 16 entries a sequence and KV head are one row tile of mma.sync, which
+  // takes the codes as they are; more share the values that they are expanded to.
+  const int group_of = cfg->n_q_heads / cfg->n_kv_heads;
+  const bool few = cfg->kv_dtype == QSA_Q4_1 && (int64_t)b->max_rows * group_of <= 16;
+  pl.tensor_cores = cfg->kv_dtype != QSA_F32 && !few;
+  if (few) {
     pl.mt = 16;
   } else if (pl.tensor_cores) {
     // Whole rows, as many as a sequence has, up to the 128 entries that are the
@@ -178,9 +182,9 @@ QSA_API qsa_status qsa_paged_attn(const qsa_paged_cache* cache, const qsa_paged_
   p.part_lse = reinterpret_cast<float*>(ws + lse_offset(pl));
   p.part_o = reinterpret_cast<float*>(ws + out_offset(pl));
   cudaStream_t st = as_stream(stream);
-  cudaError_t e = cfg->kv_dtype == QSA_Q4_1 ? launch_paged_q4(p, cfg->head_dim, pl.grid, st)
-                  : pl.tensor_cores         ? launch_paged_tc(p, cfg->kv_dtype, cfg->head_dim, pl.grid, st)
-                                            : launch_paged_f32(p, cfg->head_dim, pl.grid, st);
+  cudaError_t e = pl.tensor_cores              ? launch_paged_tc(p, cfg->kv_dtype, cfg->head_dim, pl.grid, st)
+                  : cfg->kv_dtype == QSA_Q4_1 ? launch_paged_q4(p, cfg->head_dim, pl.grid, st)
+                                              : launch_paged_f32(p, cfg->head_dim, pl.grid, st);
   if (e == cudaSuccess) e = launch_paged_merge(p, cfg->head_dim, pl.grid, st);
   return e == cudaSuccess ? ok() : cuda_fail(e, fn);
 }

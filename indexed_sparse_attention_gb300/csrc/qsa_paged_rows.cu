@@ -118,12 +118,14 @@ __device__ __forceinline__ void store_q4(const PagedAppendParams& p, const uint3
     x[2 * k + 1] = bf16_hi(u[k]);
   }
   float lo = INFINITY, hi = -INFINITY;
-  bool odd = false;   // infinity or NaN in the block
+  // What f16 does not hold (65,280 is the largest bf16 value that it does, and leaves the
+  // rounding of scale and minimum room): infinities, NaN, larger values.
+  bool odd = false;
 #pragma unroll
   for (int k = 0; k < PER; ++k) {
     lo = fminf(lo, x[k]);
     hi = fmaxf(hi, x[k]);
-    odd |= !(fabsf(x[k]) < INFINITY);
+    odd |= !(fabsf(x[k]) <= 65280.f);
   }
 #pragma unroll
   for (int o = LB / 2; o; o >>= 1) {
@@ -131,9 +133,9 @@ __device__ __forceinline__ void store_q4(const PagedAppendParams& p, const uint3
     hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
   odd = ((__ballot_sync(0xffffffffu, odd) >> (lane / LB * LB)) & ((1u << LB) - 1u)) != 0u;
-  const __half mh = __float2half_rn(lo);
+  const __half mh = odd ? __ushort_as_half((unsigned short)0) : __float2half_rn(lo);
   __half sh = __float2half_rn(__fdiv_rn(hi - lo, 15.0f));
-  if (odd || __hisinf(mh) || __hisinf(sh)) sh = __ushort_as_half((unsigned short)0x7fff);
+  if (odd) sh = __ushort_as_half((unsigned short)0x7fff);
   const float m = __half2float(mh), s = __half2float(sh);
   uint32_t codes = 0u;   // 4 bits a channel
 #pragma unroll

@@ -80,9 +80,19 @@ constexpr int kSlab = 2 * kHalf;              // bytes of 128 channels: what the
 constexpr int kMaxSlabs = 6;                 // of K, and of V
 constexpr int kKeyWarp = 8, kMmaWarp = 9, kValueWarp = 10, kQWarp = 11, kCodeWarp = 12, kCodeWarps = 4;
 constexpr int kSoftWarps = 8;
-__host__ __device__ constexpr int threads_of(bool f8) { return 32 * (f8 ? kCodeWarp + kCodeWarps : kQWarp + 1); }
+// How the cache holds K and V.
+constexpr int kBf16 = 0, kFp8 = 1, kQ4 = 2;
+__host__ __device__ constexpr int threads_of(int kind) { return 32 * (kind != kBf16 ? kCodeWarp + kCodeWarps : kQWarp + 1); }
 constexpr int kCodeSlab = kKT * 128;          // bytes of the codes of a slab (fp8 caches)
 constexpr int kMaxCodeSlabs = 4;             // of V
+// 4-bit caches: a slot of codes is the K, or the V, of 32 (head_dim 256, where Q and the
+// operands leave 32 KB) or 128 tokens, with their block scales and minima.
+template <int D>
+struct Q4Slot {
+  static constexpr int kTokens = D == 256 ? 32 : 128;
+  static constexpr int kCodes = kTokens * D / 2, kBytes = kCodes + kTokens * D / 8;
+};
+constexpr int kMaxQ4Slots = 8;               // of K, and of V
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSmemLimit = 227 * 1024;
 constexpr float kMoveMax = 8.f;               // log2 of the weight at which the running maximum is moved
@@ -93,6 +103,9 @@ constexpr uint32_t kIdescO = idesc_bf16(128, 128, false, true);
 // E5M2 (bits 7-9 = 0 or 1), B, K's codes, E4M3 (bits 10-12 = 0), both K-major.
 constexpr uint32_t kIdescLo8 = (1u << 4) | ((uint32_t)(kKT >> 3) << 17) | (8u << 24);
 constexpr uint32_t kIdescHi8 = kIdescLo8 | (1u << 7);
+// kind::f16 with f16 operands (bits 7-9 and 10-12 = 0 where bf16 has 1).
+constexpr uint32_t kF16Operands = ~((1u << 7) | (1u << 10));
+constexpr float kF16Weights = 7.f;            // log2 of the weight at the running maximum, f16 weights: 2^15 is the largest
 
 __device__ int g_timeouts;
 __device__ int g_bad_pages;
@@ -101,10 +114,11 @@ struct TcParams {
   // {64 channels, page_tokens, D / 64, Hkv, n_pages}: boxes of 64 channels x min(page_tokens, 128)
   // tokens, of two channel blocks where the page has 128 tokens.
   CUtensorMap k, v;
+  CUtensorMap r;         // 4-bit: the records
   CUtensorMap q;         // {D, Hq, n_rows}: boxes of 64 channels x a KV head's query heads x an item's rows
   PagedParams p;
   int32_t n_k, n_v;              // slabs in the rings of K (fp8 caches: of codes) and V
-  int32_t n_code_v;              // fp8 caches: slabs of V's codes
+  int32_t n_code_v;              // fp8 caches: slabs of V's codes; 4-bit: slots of K's, and of V's
 };
 
 // bar_wait with everything behind its first try out of line: the loops of the
@@ -143,7 +157,17 @@ struct Scales {
   float v[8][kKT];
   float q[4][128];   // of an item's rows of Q: the power of two that its codes were divided by
 };
+// 4-bit caches: Q's powers of two, and the rings of codes.
+struct Q4Head {
+  float q[4][128];
+  uint64_t code_full[2][kMaxQ4Slots], code_empty[2][kMaxQ4Slots];   // K, V
+};
+constexpr int kQ4HeadBytes = 3 * 1024;
 static_assert(sizeof(Head) <= kHeadBytes && (kHeadBytes + sizeof(Scales)) % 1024 == 0, "shared memory head");
+static_assert(sizeof(Q4Head) <= kQ4HeadBytes && (kHeadBytes + kQ4HeadBytes) % 1024 == 0, "shared memory head");
+__host__ __device__ constexpr int extra_bytes(int kind) {
+  return kind == kFp8 ? (int)sizeof(Scales) : kind == kQ4 ? kQ4HeadBytes : 0;
+}
 
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -241,6 +265,16 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// a * b + c of two f16 values, rounded once.
+__device__ __forceinline__ uint32_t fma_f16(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
@@ -340,8 +374,9 @@ struct Ring {
   }
 };
 
-template <int D, bool F8>
-__global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __grid_constant__ TcParams tp) {
+template <int D, int KIND>
+__global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __grid_constant__ TcParams tp) {
+  constexpr bool F8 = KIND == kFp8, Q4 = KIND == kQ4, CODES = F8 || Q4;
   constexpr int NS = D / 128;            // slabs of a tile
   constexpr int NB = 2;                  // buffers of logits in TMEM
   constexpr uint32_t kOCol = NB * kKT;   // O behind them
@@ -356,7 +391,8 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
   extern __shared__ __align__(1024) uint8_t raw[];
   Head& h = *reinterpret_cast<Head*>(raw);
   Scales& sc = *reinterpret_cast<Scales*>(raw + kHeadBytes);
-  uint8_t* q_s = raw + kHeadBytes + (F8 ? sizeof(Scales) : 0);
+  Q4Head& q4 = *reinterpret_cast<Q4Head*>(raw + kHeadBytes);
+  uint8_t* q_s = raw + kHeadBytes + extra_bytes(KIND);
   const int q_slab = (p.mt * 128 + 1023) / 1024 * 1024;
   uint8_t* k_ring = q_s + 2 * NS * q_slab;
   constexpr int kKeySlab = F8 ? kCodeSlab : kSlab;   // (the products take K's codes as they are)
@@ -371,7 +407,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
   if (tid == 0) {
     for (int kv = 0; kv < 2; ++kv) {
       for (int i = 0; i < kMaxSlabs; ++i) {
-        bar_init(&h.full[kv][i], F8 && kv == 1 ? code_warps : 1);
+        bar_init(&h.full[kv][i], Q4 || (F8 && kv == 1) ? code_warps : 1);
         bar_init(&h.empty[kv][i], 1);
       }
     }
@@ -380,7 +416,11 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       bar_init(&h.code_full[i], 1);
       bar_init(&h.code_empty[i], code_warps);
     }
-    for (int i = 0; F8 && i < 8; ++i) bar_init(&h.sc_full[i], kCodeWarps);
+    for (int i = 0; CODES && i < 8; ++i) bar_init(&h.sc_full[i], kCodeWarps);
+    for (int i = 0; Q4 && i < 2 * kMaxQ4Slots; ++i) {
+      bar_init(&q4.code_full[0][0] + i, 1);
+      bar_init(&q4.code_empty[0][0] + i, code_warps);
+    }
     for (int i = 0; i < 2; ++i) {
       bar_init(&h.s_full[i], 1);
       bar_init(&h.p_full[i], 2 * quarters);
@@ -389,7 +429,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       bar_init(&h.pv_done[i], 1);
     }
     bar_init(&h.o_free, 2 * quarters);
-    bar_init(&h.q_full, F8 ? kCodeWarps : 1);
+    bar_init(&h.q_full, CODES ? kCodeWarps : 1);
     bar_init(&h.q_free, 1);
     bar_init(&h.q_used, 1);
     bar_init(&h.mma_done, 1);
@@ -397,14 +437,14 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
     bar_init_fence();
   }
   if (warp == kMmaWarp) tmem_alloc(&h.tmem, kTmemCols);
-  if (warp == kQWarp && lane < (F8 ? 2 : 3)) prefetch_map(lane == 0 ? &tp.k : lane == 1 ? &tp.v : &tp.q);
+  if (warp == kQWarp && lane < (F8 ? 2 : 3)) prefetch_map(lane == 0 ? &tp.k : lane == 1 ? &tp.v : Q4 ? &tp.r : &tp.q);
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = h.tmem;
   grid_dependency_wait();
   grid_dependency_release();
-  const Start st = find_run<threads_of(F8), kKT>(p, p.mt, blockIdx.x, gridDim.x, h.scan, &h.start);
+  const Start st = find_run<threads_of(KIND), kKT>(p, p.mt, blockIdx.x, gridDim.x, h.scan, &h.start);
   Cursor<kKT> c;
   c.begin(p, p.mt, st);
   if (tid == 0) h.start = st;   // for the end (this thread's): registers are short
@@ -417,15 +457,21 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
     // issues, with values that all lanes agree on; see the products below.
     const int kv = warp == kValueWarp ? 1 : 0;
     const CUtensorMap* map = kv ? &tp.v : &tp.k;
-    const int box = min(1 << p.page_shift, kKT), n_box = kKT / box, page_mask = (1 << p.page_shift) - 1;
-    constexpr int kBytes = F8 ? kCodeSlab : kSlab;
-    const int n_copies = F8 || n_box == 1 ? n_box : 2 * n_box;   // copies of a slab; lane b's: box b % n_box, ...
-    const int my_box = lane % n_box, half = !F8 && n_box > 1 && lane >= n_box ? 1 : 0;   // ... channels 64 * half on
-    const int at_box = my_box * box * 128 + half * kHalf;
-    uint64_t* fulls = F8 && kv ? h.code_full : h.full[kv];
-    uint64_t* empties = F8 && kv ? h.code_empty : h.empty[kv];
-    uint8_t* const to_ring = kv ? (F8 ? v_codes : v_ring) : k_ring;
-    const int n_ring = kv ? (F8 ? tp.n_code_v : tp.n_v) : tp.n_k;
+    constexpr int kSlotTokens = Q4 ? Q4Slot<D>::kTokens : kKT;   // 4-bit: slots of fewer tokens, all channels
+    const int box = min(1 << p.page_shift, kSlotTokens), n_box = kKT / box, page_mask = (1 << p.page_shift) - 1;
+    constexpr int kBytes = Q4 ? Q4Slot<D>::kBytes : F8 ? kCodeSlab : kSlab;
+    // Copies of a slab (4-bit: of a tile); lane b's: box b % n_box, ...
+    const int n_copies = Q4 ? 2 * n_box : F8 || n_box == 1 ? n_box : 2 * n_box;
+    // ... channels 64 * half on (4-bit: codes, or records).
+    const int my_box = lane % n_box, half = !F8 && (Q4 || n_box > 1) && lane >= n_box ? 1 : 0;
+    const int my_slot = my_box * box / kSlotTokens;              // 4-bit: slot of the tile
+    const int at_box = !Q4 ? my_box * box * 128 + half * kHalf
+                           : half ? Q4Slot<D>::kCodes + (my_box * box - my_slot * kSlotTokens) * (D / 8)
+                                  : (my_box * box - my_slot * kSlotTokens) * (D / 2);
+    uint64_t* fulls = Q4 ? q4.code_full[kv] : F8 && kv ? h.code_full : h.full[kv];
+    uint64_t* empties = Q4 ? q4.code_empty[kv] : F8 && kv ? h.code_empty : h.empty[kv];
+    uint8_t* const to_ring = Q4 ? v_codes + kv * tp.n_code_v * Q4Slot<D>::kBytes : kv ? (F8 ? v_codes : v_ring) : k_ring;
+    const int n_ring = Q4 ? tp.n_code_v : kv ? (F8 ? tp.n_code_v : tp.n_v) : tp.n_k;
     const bool leader = elect_one();
     Ring at;
     int tj = 0;
@@ -461,8 +507,10 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
           h.bad[(tj + j) & 15] = 0u;
         }
         const int slot_in_page = c.tiles.token(c.x + j) & page_mask;
+        // (4-bit: a page of 128 tokens and more has several boxes of a tile.)
+        [[maybe_unused]] const int page_offset = box > page_mask ? 0 : (my_box * box) & page_mask;
 #pragma unroll 1
-        for (int s = 0; s < NS; ++s) {
+        for (int s = 0; s < (Q4 ? kKT / kSlotTokens : NS); ++s) {
           uint64_t* full = fulls + at.slot;
           uint8_t* dst = to_ring + at.slot * kBytes;
           if (at.use > 0 && !wait(empties + at.slot, (at.use - 1) & 1, abrt)) live = false;
@@ -472,7 +520,9 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
           __syncwarp();
           // A lane a box: of 128 channels (fp8, or pages of 128 tokens), or of 64.
           if (lane < n_copies) {
-            if constexpr (F8) tma_4d(dst + at_box, map, 128 * s, slot_in_page, c.head, page, full);
+            if constexpr (Q4) {
+              if (my_slot == s) tma_4d(dst + at_box, half ? &tp.r : map, half ? kv * (D / 8) : 0, slot_in_page + page_offset, c.head, page, full);
+            } else if constexpr (F8) tma_4d(dst + at_box, map, 128 * s, slot_in_page, c.head, page, full);
             else tma_5d(dst + at_box, map, slot_in_page, 2 * s + half, c.head, page, full);
           }
           __syncwarp();
@@ -487,6 +537,156 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
     if (lane < n_ring) {
       const uint32_t uses = at.use + (lane < at.slot ? 1u : 0u);
       if (uses > 0) bar_wait(fulls + lane, (uses - 1) & 1, &g_timeouts);
+    }
+  } else if (Q4 && (warp >= kCodeWarp || (warp < kSoftWarps && (warp & 3) >= quarters))) {
+    // ------------------------------------------------------------ 4-bit: Q, K, V
+    const int cw = warp >= kCodeWarp ? warp - kCodeWarp : kCodeWarps + (warp >> 2) * (4 - quarters) + (warp & 3) - quarters;
+    const bool own = cw < kCodeWarps;   // Q is these warps'
+    constexpr int G = D / 32, kSlotTokens = Q4Slot<D>::kTokens, kBlocks = kSlotTokens / 8;
+    Ring in[2], out[2];
+    int it = 0;
+    for (bool more = true; more; more = c.next(p, p.mt), ++it) {
+      const ItemRows ir = item_rows(p, c);
+      const int T = c.x1 - c.x;
+      // Q as f16: times a power of two that brings the row's largest magnitude to [2^14,
+      // 2^15) a value of bf16's 8 bits is exact from 2^-31 of it on, and off by at most
+      // 2^-39 of it below.  A warp a row, D / 32 channels a lane, four rows in flight.
+      if (own) {
+        if (it > 0) wait(&h.q_free, (uint32_t)((it - 1) & 1), abrt);
+        constexpr int kCh = D / 32, kBatch = 4;
+        const int at_c = lane * kCh;
+        uint8_t* const to = q_s + (at_c >> 6) * q_slab;
+#pragma unroll 1
+        for (int r0 = cw; r0 < ir.nf; r0 += kBatch * kCodeWarps) {
+          uint32_t x[kBatch][kCh / 2];
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            const int f = ir.f0 + min(r0 + b * kCodeWarps, ir.nf - 1), r = row_of(p, f);
+            const int64_t entry = (int64_t)(c.s.row0 + r) * p.n_q_heads + c.head * p.group + (f - r * p.group);
+            const char* from = static_cast<const char*>(p.q) + (entry * D + at_c) * 2;
+            if constexpr (kCh == 8) {
+              const uint4 v = __ldg(reinterpret_cast<const uint4*>(from));
+              x[b][0] = v.x, x[b][1] = v.y, x[b][2] = v.z, x[b][3] = v.w;
+            } else {
+              const uint2 v = __ldg(reinterpret_cast<const uint2*>(from));
+              x[b][0] = v.x, x[b][1] = v.y;
+            }
+          }
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            const int row = r0 + b * kCodeWarps;
+            uint32_t most = 0u;
+#pragma unroll
+            for (int i = 0; i < kCh / 2; ++i)
+              most = max(most, max((x[b][i] << 16) & 0x7fff0000u, x[b][i] & 0x7fff0000u));
+            most = __reduce_max_sync(0xffffffffu, most);
+            // 2^(exponent - 14), at least 2^-100: a row of smaller values keeps fewer bits.
+            const int e = max((int)(most >> 23) - 127 - 14, -100);
+            const float up = __uint_as_float((uint32_t)(127 - e) << 23);
+            const bool odd = most >= 0x7f800000u;   // infinity or NaN: the row's logits are NaN
+            uint32_t f16[kCh / 2];
+#pragma unroll
+            for (int i = 0; i < kCh / 2; ++i)
+              f16[i] = odd ? 0x7fff7fffu : pack_f16(__uint_as_float(x[b][i] << 16) * up, __uint_as_float(x[b][i] & 0xffff0000u) * up);
+            if (row < ir.nf) {
+              const int byte = (at_c & 63) * 2;
+              const int at = row * 128 + ((((byte >> 4) ^ (row & 7)) << 4) | (byte & 15));
+              if constexpr (kCh == 8) *reinterpret_cast<uint4*>(to + at) = make_uint4(f16[0], f16[1], f16[2], f16[3]);
+              else *reinterpret_cast<uint2*>(to + at) = make_uint2(f16[0], f16[1]);
+              if (lane == 0) q4.q[it & 3][row] = odd ? 1.f : __uint_as_float((uint32_t)(127 + e) << 23);
+            }
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(&h.sc_full[it & 3]);
+          bar_arrive(&h.q_full);
+        }
+      }
+      // K's or V's codes of a tile to f16 in the layout the products read: value = code *
+      // scale + minimum, rounded once.  V: tokens that no row sees become zeros.
+      // Four lanes a token, each the units 2 i and 2 i + 1 (8 channels) of every block;
+      // lanes next to each other take tokens that differ in bits 0 and 2, so that the
+      // loads and the stores of eight lanes touch all 32 banks.
+      const int i = lane & 3, q8 = lane >> 2, in8 = q8 & 1 ? (q8 >> 1) ^ 5 : q8 >> 1;
+      auto expand = [&](int kv, int j) {
+        const int t0 = c.tiles.token(c.x + j);
+        auto slot_of = [&](int t) { return min(max(t - t0, 0), kKT); };
+        const int cut = slot_of(ir.last + 1);
+        const int gap0 = p.window > 0 ? slot_of(p.n_sinks) : 0;
+        const int gap1 = p.window > 0 ? slot_of(ir.first - p.window + 1) : 0;
+        const bool some = kv == 1 && (cut < kKT || gap0 < gap1);
+        const int n_ring = kv ? tp.n_v : tp.n_k;
+        uint8_t* const ring = kv ? v_ring : k_ring;
+        int block = cw;   // the warp's next eight tokens, counted from the slot's first
+        uint8_t* slabs[NS];
+        Ring o = out[kv];
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+          if (o.use > 0) wait(&h.empty[kv][o.slot], (o.use - 1) & 1, abrt);
+          slabs[s] = ring + o.slot * kSlab;
+          o.step(n_ring);
+        }
+#pragma unroll 1
+        for (int sub = 0; sub < kKT / kSlotTokens; ++sub) {
+          wait(&q4.code_full[kv][in[kv].slot], in[kv].use & 1, abrt);
+          const uint8_t* src = v_codes + (kv * tp.n_code_v + in[kv].slot) * Q4Slot<D>::kBytes;
+#pragma unroll 1
+          for (; block < kBlocks; block += code_warps) {
+            const int r = 8 * block + in8, R = sub * kSlotTokens + r;
+            uint32_t a[G / 2], b[G / 2], rec[G];   // units 2 i, 2 i + 1 of blocks (0, 1), (2, 3), ...
+            if constexpr (D == 256) {
+              const uint4 x = *reinterpret_cast<const uint4*>(src + r * 128 + ((2 * i ^ (r & 7)) << 4)),
+                          y = *reinterpret_cast<const uint4*>(src + r * 128 + (((2 * i + 1) ^ (r & 7)) << 4));
+              a[0] = x.x, a[1] = x.y, a[2] = x.z, a[3] = x.w;
+              b[0] = y.x, b[1] = y.y, b[2] = y.z, b[3] = y.w;
+            } else {
+              const uint4 x = *reinterpret_cast<const uint4*>(src + r * 64 + ((i ^ ((r >> 1) & 3)) << 4));
+              a[0] = x.x, a[1] = x.y, b[0] = x.z, b[1] = x.w;
+            }
+#pragma unroll
+            for (int g = 0; g < G; g += 4) {
+              const uint4 x = *reinterpret_cast<const uint4*>(src + Q4Slot<D>::kCodes + r * (D / 8) + 4 * g);
+              rec[g] = x.x, rec[g + 1] = x.y, rec[g + 2] = x.z, rec[g + 3] = x.w;
+            }
+            const bool gone = some && (R >= cut || (R >= gap0 && R < gap1));
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              const uint32_t s2 = __byte_perm(rec[g], 0u, 0x1010), m2 = __byte_perm(rec[g], 0u, 0x3232);
+              uint32_t w[4];
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                // A unit's nibbles 0 and 1 (then 2 and 3) under the exponents of 1024 and 64,
+                // which the first fma takes off exactly.
+                const uint32_t two = __byte_perm(u ? b[g / 2] : a[g / 2], 0u, g & 1 ? 0x3232 : 0x1010), hi = two >> 8;
+                w[2 * u] = fma_f16(fma_f16((two & 0x00f0000fu) | 0x64006400u, 0x2c003c00u, 0xd400e400u), s2, m2);
+                w[2 * u + 1] = fma_f16(fma_f16((hi & 0x00f0000fu) | 0x64006400u, 0x2c003c00u, 0xd400e400u), s2, m2);
+              }
+              if (gone) w[0] = w[1] = w[2] = w[3] = 0u;
+              const int chunk = ((g & 1) << 2) | i;
+              *reinterpret_cast<uint4*>(slabs[g >> 2] + ((g >> 1) & 1) * kHalf + R * 128 + ((chunk ^ (R & 7)) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+          block -= kBlocks;
+          __syncwarp();
+          if (lane == 0) bar_arrive(&q4.code_empty[kv][in[kv].slot]);
+          in[kv].step(tp.n_code_v);
+        }
+        fence_async_smem();
+        __syncwarp();
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+          if (lane == 0) bar_arrive(&h.full[kv][out[kv].slot]);
+          out[kv].step(n_ring);
+        }
+      };
+#pragma unroll 1
+      for (int j = 0; j < T + NB - 1; ++j) {
+        if (j < T) expand(0, j);
+        if (j >= NB - 1) expand(1, j - (NB - 1));
+      }
     }
   } else if (F8 && (warp >= kCodeWarp || (warp < kSoftWarps && (warp & 3) >= quarters))) {
     // ------------------------------------------------------------ fp8: Q, scales, V
@@ -661,7 +861,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       }
       tj += T;
     }
-  } else if (!F8 && warp == kQWarp) {
+  } else if (!CODES && warp == kQWarp) {
     // ------------------------------------------------------------ Q, and V's ends
     // An item holds whole rows, so its entries are one box for each 64 channels.
     // The next item's are copied before the last tile's V is waited for.
@@ -742,7 +942,8 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
     const uint64_t q_desc = desc_sw128(q_s, 16, 1024), k_desc = desc_sw128(k_ring, 16, 1024),
                    v_desc = desc_sw128(v_ring, kHalf, 1024);
     const uint32_t q_step = (uint32_t)q_slab >> 4;
-    uint64_t* const v_full = F8 ? h.full[1] : h.v_ready;   // (who passes bf16's V on has waited for the copies)
+    uint64_t* const v_full = CODES ? h.full[1] : h.v_ready;   // (who passes bf16's V on has waited for the copies)
+    constexpr uint32_t kOperands = Q4 ? kF16Operands : ~0u;
     Ring ka, va;
     int it = 0;
     int s_buf = 0, p_buf = 0, odd = 0;   // buffers of the next logits and the next weights; parity of the next output
@@ -762,7 +963,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
             for (int x = 0; QT && x < 8; ++x) {
               if constexpr (F8) mma_f8_ts(d, tmem + kQCol + 8u * x, k + 2 * (x & 3), x < 4 ? kIdescHi8 : kIdescLo8, x != 0 ? 1u : 0u);
               else
-                mma_bf16_ts(d, tmem + kQCol + 8u * x, k + (x >> 2) * (kHalf >> 4) + 2 * (x & 3), kIdescS, x != 0 ? 1u : 0u);
+                mma_bf16_ts(d, tmem + kQCol + 8u * x, k + (x >> 2) * (kHalf >> 4) + 2 * (x & 3), kIdescS & kOperands, x != 0 ? 1u : 0u);
             }
 #pragma unroll
             for (int x = 0; !QT && F8 && x < 8; ++x)   // both codes of Q's values
@@ -770,7 +971,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
                      (s | x) != 0 ? 1u : 0u);
 #pragma unroll
             for (int x = 0; !QT && !F8 && x < 8; ++x)
-              mma_bf16(d, q + (x >> 2) * q_step + 2 * (x & 3), k + (x >> 2) * (kHalf >> 4) + 2 * (x & 3), kIdescS,
+              mma_bf16(d, q + (x >> 2) * q_step + 2 * (x & 3), k + (x >> 2) * (kHalf >> 4) + 2 * (x & 3), kIdescS & kOperands,
                        (s | x) != 0 ? 1u : 0u);
             commit(&h.empty[0][ka.slot]);
             if (s == NS - 1) commit(&h.s_full[s_buf]);
@@ -812,7 +1013,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
 #pragma unroll
             for (int x = 0; x < 8; ++x)
               mma_bf16_ts(tmem + kOCol + (uint32_t)(s * 128), tmem + (uint32_t)(p_buf * kKT + 8 * x), v + 128 * x,
-                          kIdescO, (j | x) != 0 ? 1u : 0u);
+                          kIdescO & kOperands, (j | x) != 0 ? 1u : 0u);
             commit(&h.empty[1][va.slot]);
             if (s == NS - 1) commit(&h.pv_done[odd]);
           }
@@ -846,9 +1047,14 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       // (Not known before a tile's scales are, which follow Q's.  Four items: a group
       // may be one behind the other, Q one ahead of both.)
       auto factor = [&] {
-        zc = mine ? sc.q[it & 3][row] : 1.f;
+        zc = mine ? (Q4 ? q4.q : sc.q)[it & 3][row] : 1.f;
+        if constexpr (Q4) zc = fmaxf(zc * (p.scale * kLog2e), 1e-37f);   // (not 0: hidden logits are -infinity times it)
         move = fminf(kMoveMax / zc, 1e30f);
       };
+      if constexpr (Q4) {
+        wait(&h.sc_full[it & 3], (uint32_t)((it >> 2) & 1), abrt);
+        factor();
+      }
       float m = -INFINITY, l = 0.f;   // the maximum that this thread's sum l is relative to
       // What a row does not see of keys [from, to) of a tile becomes -infinity, in
       // TMEM: the passes below stay short (with the masks unrolled into them they no
@@ -950,7 +1156,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
             fence_before();
           }
         }
-        const float shift = m == -INFINITY ? 0.f : -m * zc;
+        const float shift = m == -INFINITY ? 0.f : (Q4 ? kF16Weights : 0.f) - m * zc;
         const uint64_t zc2 = pack2(zc, zc), shift2 = pack2(shift, shift);
         uint64_t sum2[2] = {0ull, 0ull};
         auto weigh = [&](uint32_t(&x)[32], const float* vs, uint32_t to) {
@@ -966,7 +1172,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
             const uint64_t e = pack2(a, b);
             sum2[i & 1] = add2(sum2[i & 1], e);
             if constexpr (F8) unpack2(mul2(e, i & 1 ? vv.y : vv.x), a, b);   // V's scale goes with the weight, rounded once
-            w[i] = pack_bf16(a, b);
+            w[i] = Q4 ? pack_f16(a, b) : pack_bf16(a, b);
           }
           tmem_st16(to, w);
         };
@@ -985,7 +1191,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       // The item's result, or this run's part of it: both groups' sums, relative
       // to the last maximum.
       named_sync(1, soft_threads);
-      if constexpr (F8) ++it;
+      if constexpr (CODES) ++it;
       h.sums[group][row] = l;
       named_sync(1, soft_threads);
       l += h.sums[group ^ 1][row];
@@ -1026,7 +1232,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1) paged_tc_kernel(const __gri
       __syncwarp();
       if (lane == 0) bar_arrive(&h.o_free);
       if (mine && group == 0) {
-        const float lse2 = l == 0.f ? -INFINITY : fmaf(m, zc, log2f(l));
+        const float lse2 = l == 0.f ? -INFINITY : fmaf(m, zc, log2f(l)) - (Q4 ? kF16Weights : 0.f);
         if (!whole) p.part_lse[part] = lse2;
         else if (p.lse) p.lse[entry] = lse2 * kLn2;
       }
@@ -1092,37 +1298,65 @@ bool encode_queries(CUtensorMap* map, const PagedParams& p, int head_dim) {
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool F8>
+// Rows of `bytes` of a 4-bit cache's codes or records, in copies of `take` bytes and `tokens` tokens; strides in bytes.
+bool encode_q4(CUtensorMap* map, const void* base, const PagedParams& p, int bytes, int take, int tokens, int64_t tok,
+               int64_t head, int64_t page_stride, CUtensorMapSwizzle swizzle) {
+  PFN_cuTensorMapEncodeTiled_v12000 f = encoder();
+  if (!f) return false;
+  const cuuint64_t page = (cuuint64_t)1 << p.page_shift;
+  const cuuint64_t dims[4] = {(cuuint64_t)bytes, page, (cuuint64_t)p.n_kv_heads, (cuuint64_t)p.n_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)tok, (cuuint64_t)head, (cuuint64_t)page_stride};
+  const cuuint32_t box[4] = {(cuuint32_t)take, (cuuint32_t)std::min<cuuint64_t>(page, (cuuint64_t)tokens), 1, 1}, step[4] = {1, 1, 1, 1};
+  return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, step,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int KIND>
 cudaError_t launch_d(const PagedParams& p, int grid, cudaStream_t st) {
+  constexpr bool F8 = KIND == kFp8, Q4 = KIND == kQ4;
   TcParams tp{};
   tp.p = p;
-  if (!encode_pages(&tp.k, p.k, p, D, F8, true) || !encode_pages(&tp.v, p.v, p, D, F8, !F8) ||
-      (!F8 && !encode_queries(&tp.q, p, D)))
+  if constexpr (Q4) {
+    constexpr int kTokens = Q4Slot<D>::kTokens, kRecord = D / 4;
+    const CUtensorMapSwizzle sw = D == 256 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    if (!encode_q4(&tp.k, p.k, p, D / 2, D / 2, kTokens, p.tok_stride / 2, p.head_stride / 2, p.page_stride / 2, sw) ||
+        !encode_q4(&tp.v, p.v, p, D / 2, D / 2, kTokens, p.tok_stride / 2, p.head_stride / 2, p.page_stride / 2, sw) ||
+        !encode_q4(&tp.r, p.kv_scale, p, kRecord, kRecord / 2, kTokens, p.s_tok_stride * kRecord, p.s_head_stride * kRecord,
+                   p.s_page_stride * kRecord, CU_TENSOR_MAP_SWIZZLE_NONE))
+      return cudaErrorInvalidValue;
+  } else if (!encode_pages(&tp.k, p.k, p, D, F8, true) || !encode_pages(&tp.v, p.v, p, D, F8, !F8) ||
+             (!F8 && !encode_queries(&tp.q, p, D))) {
     return cudaErrorInvalidValue;
+  }
   const int q_slab = (p.mt * 128 + 1023) / 1024 * 1024;
-  const int fixed = kHeadBytes + (F8 ? (int)sizeof(Scales) : 0) + D / 64 * q_slab, room = kSmemLimit - fixed;
+  const int fixed = kHeadBytes + extra_bytes(KIND) + D / 64 * q_slab, room = kSmemLimit - fixed;
   if (F8) {   // operands of a whole tile of V, the rest for codes
     tp.n_v = 2;
     const int n = (room - tp.n_v * kSlab) / kCodeSlab;
     tp.n_code_v = std::min(n / 2, kMaxCodeSlabs);
     tp.n_k = std::min(n - tp.n_code_v, kMaxSlabs);
+  } else if (Q4) {   // operands of a whole tile of K and V (two of head_dim 128), the rest for codes
+    tp.n_k = tp.n_v = 2;
+    tp.n_code_v = std::min((room - 4 * kSlab) / (2 * Q4Slot<D>::kBytes), kMaxQ4Slots);
   } else {
     const int n = room / kSlab;
     tp.n_k = std::min((n + 1) / 2, 3);
     tp.n_v = std::min(n / 2, 3);
   }
   const size_t smem = (size_t)fixed + (size_t)tp.n_k * (F8 ? kCodeSlab : kSlab) + (size_t)tp.n_v * kSlab +
-                      (size_t)tp.n_code_v * kCodeSlab;
-  cudaError_t e = allow_dynamic_smem((const void*)paged_tc_kernel<D, F8>, kSmemLimit);
+                      (Q4 ? (size_t)tp.n_code_v * 2 * Q4Slot<D>::kBytes : (size_t)tp.n_code_v * kCodeSlab);
+  cudaError_t e = allow_dynamic_smem((const void*)paged_tc_kernel<D, KIND>, kSmemLimit);
   if (e != cudaSuccess) return e;
-  return launch_kernel(paged_tc_kernel<D, F8>, dim3((unsigned)grid), dim3(threads_of(F8)), smem, st, 0u, tp);
+  return launch_kernel(paged_tc_kernel<D, KIND>, dim3((unsigned)grid), dim3(threads_of(KIND)), smem, st, 0u, tp);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_tc(const PagedParams& p, qsa_dtype kv_dtype, int head_dim, int grid, cudaStream_t st) {
-  if (kv_dtype == QSA_FP8_E4M3) return head_dim == 256 ? launch_d<256, true>(p, grid, st) : launch_d<128, true>(p, grid, st);
-  return head_dim == 256 ? launch_d<256, false>(p, grid, st) : launch_d<128, false>(p, grid, st);
+  if (kv_dtype == QSA_Q4_1) return head_dim == 256 ? launch_d<256, kQ4>(p, grid, st) : launch_d<128, kQ4>(p, grid, st);
+  if (kv_dtype == QSA_FP8_E4M3) return head_dim == 256 ? launch_d<256, kFp8>(p, grid, st) : launch_d<128, kFp8>(p, grid, st);
+  return head_dim == 256 ? launch_d<256, kBf16>(p, grid, st) : launch_d<128, kBf16>(p, grid, st);
 }
 
 int paged_tc_bad_pages_take() { return take_counter(g_bad_pages); }

@@ -19,6 +19,13 @@ blocks, n visible tokens; v_tc = s code + m of a block):
            below f16's normal numbers (the largest is 2^2 or more, when the scales
            are below 2^6) are off by 2^-25: n 2^-27 (15 + max |m|).
   lse      e + (n + 16) 2 u + 4 u |lse|.
+
+Calls with more than 16 entries a sequence and KV head take K, V and the weights
+rounded to f16: |dz| grows by (2^-11 1.01) kmag, kmag = max_t scale sum_c |q_c| |k_tc|
+(values below f16's normal numbers: 2^-25 scale sum_c |q_c|), z's own sums are of |k|;
+q is exact from 2^-31 qmax on (2^-39 below), out is off by another
+2^-10 1.01 sum_t w_t |v_t| / sum_t w_t, V below f16's normal numbers by 2^-25, and
+weights below them (the largest is 2^7 or more) by n 2^-32 max |v|.
 """
 from __future__ import annotations
 
@@ -42,12 +49,11 @@ def encode4(x: torch.Tensor):
     header defines them."""
     D = x.shape[-1]
     b = x.float().reshape(*x.shape[:-1], D // 32, 32)
-    odd = ~torch.isfinite(b).all(-1, keepdim=True)
-    b0 = torch.where(torch.isfinite(b), b, torch.zeros_like(b))
-    lo = torch.where(torch.isfinite(b), b, torch.full_like(b, math.inf)).amin(-1, keepdim=True)
-    hi = torch.where(torch.isfinite(b), b, torch.full_like(b, -math.inf)).amax(-1, keepdim=True)
+    odd = ~(b.abs() <= 65280.0).all(-1, keepdim=True)
+    b0 = torch.where(odd, torch.zeros_like(b), b)
+    lo, hi = b0.amin(-1, keepdim=True), b0.amax(-1, keepdim=True)
     m, s = lo.half(), ((hi - lo) / 15.0).half()
-    s = torch.where(odd | torch.isinf(m) | torch.isinf(s), torch.full_like(s, math.nan), s)
+    s = torch.where(odd, torch.full_like(s, math.nan), s)
     sf = s.float()
     c = torch.where(sf > 0, torch.round((b0 - m.float()) / sf).clamp(0, 15), torch.zeros_like(b0)).to(torch.uint8)
     nib = torch.zeros(*x.shape[:-1], D, dtype=torch.uint8)
@@ -113,12 +119,14 @@ def make_paged4(lens, rows, *, poison=False, lean=1.0, **kw) -> Paged4:
     return y
 
 
-def attend4(x: Paged4, window=0, sinks=0, scale=None):
-    """(out, lse, out tolerance without output rounding, lse tolerance) in 64 bits."""
+def attend4(x: Paged4, window=0, sinks=0, scale=None, most=None):
+    """(out, lse, out tolerance without output rounding, lse tolerance) in 64 bits; most: the call's max_rows, where
+    it is not x's."""
     R, Hq, D = x.q.shape
     Hkv = x.k.shape[1]
     G = Hq // Hkv
     scale = scale or D ** -0.5
+    wide = (max(x.rows, default=0) if most is None else most) * G > 16
     out = torch.zeros(R, Hq, D, dtype=torch.float64)
     lse = torch.full((R, Hq), -math.inf, dtype=torch.float64)
     otol = torch.zeros(R, Hq, D, dtype=torch.float64)
@@ -137,22 +145,29 @@ def attend4(x: Paged4, window=0, sinks=0, scale=None):
         cnt = see.sum(1)[:, None].double()
         for h in range(Hkv):
             kc, ks, km, vc, vs, vm = (torch.where(live[:, None], y[h], 0.0) for y in (*K, *V))
-            kh, kmag = kc * ks + km, (kc * ks).abs() + km.abs()
+            kh, vh = kc * ks + km, vc * vs + vm
+            kmag = kh.abs() if wide else (kc * ks).abs() + km.abs()
             qh = x.q[r0:r0 + r, h * G:(h + 1) * G].double()
             hide = ~see[:, None]
             z = (torch.einsum("rgd,td->rgt", qh, kh) * scale).masked_fill(hide, -math.inf)
             mag = (torch.einsum("rgd,td->rgt", qh.abs(), kmag) * scale).masked_fill(hide, 0.0).amax(-1)
-            lost = (2.0 ** -33 * scale * qh.abs().amax(-1, keepdim=True) * kmag.sum(-1)).masked_fill(hide, 0.0).amax(-1)
+            lost = (2.0 ** (-39 if wide else -33) * scale * qh.abs().amax(-1, keepdim=True) * kmag.sum(-1)).masked_fill(hide, 0.0).amax(-1)
+            if wide:
+                lost = lost + 2.0 ** -11 * 1.01 * mag + 2.0 ** -25 * scale * qh.abs().sum(-1)
             e = 2 * ((2 * D + 4 * (D // 32) + 24) * U * mag + lost) + 8 * U
             L = torch.logsumexp(z, -1)
             w = torch.exp(z - L[..., None]).nan_to_num(0.0)
             sl = slice(h * G, (h + 1) * G)
-            out[r0:r0 + r, sl] = torch.einsum("rgt,td->rgd", w, vc * vs + vm)
+            out[r0:r0 + r, sl] = torch.einsum("rgt,td->rgd", w, vh)
             wcode, wmin = torch.einsum("rgt,td->rgd", w, (vc * vs).abs()), torch.einsum("rgt,td->rgd", w, vm.abs())
             lse[r0:r0 + r, sl] = L
-            floor = cnt[..., None] * 2.0 ** -27 * (15 + vm.abs().max())
-            otol[r0:r0 + r, sl] = ((2 * (e + (cnt + 16) * 2 * U))[..., None] * (wcode + wmin)
-                                   + 1.01 * (2.0 ** -10 * wcode + 2.0 ** -11 * wmin) + floor)
+            if wide:
+                wabs = torch.einsum("rgt,td->rgd", w, vh.abs())
+                rounded = 1.01 * 2.0 ** -10 * wabs + 2.0 ** -25 + cnt[..., None] * 2.0 ** -32 * vh.abs().max()
+            else:
+                wabs = wcode + wmin
+                rounded = 1.01 * (2.0 ** -10 * wcode + 2.0 ** -11 * wmin) + cnt[..., None] * 2.0 ** -27 * (15 + vm.abs().max())
+            otol[r0:r0 + r, sl] = (2 * (e + (cnt + 16) * 2 * U))[..., None] * wabs + rounded
             ltol[r0:r0 + r, sl] = e + (cnt + 16) * 2 * U + 4 * U * L.abs().nan_to_num(0.0, posinf=0.0)
     return out, lse, otol, ltol
 

@@ -110,7 +110,7 @@ def test_rows_that_see_nothing_and_rows_of_nobody():
     y = Paged4(x.k, x.v, x.scale, x.table, [50, 0, 30, 3], [2, 0, 0, 3], torch.tensor([1, 3, 3, 3, 6]), None, 16, "head")
     y.q = torch.cat((x.q[:3], x.q[6:9]))
     keep = [1, 2, 6, 7, 8]
-    assert_attended(out[keep], lse[keep], tuple(t[[1, 2, 3, 4, 5]] for t in attend4(y)))
+    assert_attended(out[keep], lse[keep], tuple(t[[1, 2, 3, 4, 5]] for t in attend4(y, most=5)))
     for r in (3, 4, 5):
         assert (out[r] == 0).all() and torch.isneginf(lse[r]).all()
     for r in (0, 9):
@@ -214,11 +214,12 @@ def test_scales_of_any_size(D, rows):
     rec[..., 0, 1, 0] *= -0.5
     rec[..., 0, 2, 0] = 2.0 ** -24
     rec[..., 1, 3, :] *= 1e-4
-    for t, s in ((7, 60000.0), (123, 3000.0), (400, -65504.0)):
+    rec[..., 1, :, :].clamp_(-2000.0, 2000.0)              # (values have to lie within f16's range)
+    for t, s in ((7, 4000.0), (123, 3000.0), (400, -4000.0)):
         rec[x.table[0, t // 32], 0, t % 32, 1, 2, 0] = s
-    x.scale = rec.clamp(-65504.0, 65504.0).half().view(x.scale.shape)
+    x.scale = rec.half().view(x.scale.shape)
     # The weights are kept to 2^-11 of their own (see q4_cases) and to 2^-27 of the largest, less what the largest
-    # scale that a row's run has met takes off them: 2^11 for 65504.
+    # scale that a row's run has met takes off them: less than 2^11.
     out, lse, otol, ltol = attend4(x)
     V = max(float((c * s).abs().max()) for i in range(3) for c, s, _ in [x.seq_parts(i)[1]])
     big = torch.zeros_like(otol)
@@ -230,7 +231,7 @@ def test_scales_of_any_size(D, rows):
 
 def test_logits_that_climb():
     # Every tile's logits are above the last one's: the maximum moves all the time, and once by a lot.
-    for rows, D in (([1], 256), ([5], 128)):
+    for rows, D in (([1], 256), ([5], 128), ([9], 128), ([8], 256)):
         x = make_paged4([1500], rows, D=D, Hkv=1, G=3, page=64, seed=18, lean=0.0)
         x.q[:] = 0.0
         x.q[..., 0] = torch.linspace(1.0, 3.0, 3)[None].bfloat16()

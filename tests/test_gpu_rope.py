@@ -241,7 +241,8 @@ def test_blocks_that_4_bits_do_not_hold():
     cache, batch, _ = x.device()
     new = torch.randn(8, 2, 256, device=dev()).bfloat16()
     new[0, 0, 5], new[1, 1, 33], new[2, 0, 70], new[3, 1, 255] = float("nan"), float("inf"), float("-inf"), 3e38
-    new[4, 0, 0], new[4, 0, 1] = 65000.0, -65000.0
+    new[3, 0, 130] = 65536.0
+    new[7, 0, 0], new[7, 0, 1] = 65280.0, -65280.0
     qsa.paged_append(cache, batch, new, new)
     for i in range(8):
         c, p = encode4(new[i].float().cpu())
@@ -252,11 +253,12 @@ def test_blocks_that_4_bits_do_not_hold():
             assert torch.equal(torch.isnan(got[:, w, :, 0]), torch.isnan(p[..., 0]))
             ok = ~torch.isnan(p[..., 0])
             assert torch.equal(got[:, w][ok], p[ok])
+    assert not torch.isnan(p[..., 0]).any()                # (the largest magnitudes that are held)
     k_out = torch.empty(8, 2, 256, device=dev())
     qsa.paged_read(cache, batch, k_out, torch.empty_like(k_out))
     bad = torch.isnan(k_out).reshape(8, 2, 8, 32)
-    assert bad.all(-1).nonzero().tolist() == [[0, 0, 0], [1, 1, 1], [2, 0, 2], [3, 1, 7]]
-    assert int(bad.sum()) == 4 * 32 and qsa.check_device_status() == (0, "")
+    assert bad.all(-1).nonzero().tolist() == [[0, 0, 0], [1, 1, 1], [2, 0, 2], [3, 0, 4], [3, 1, 7]]
+    assert int(bad.sum()) == 5 * 32 and qsa.check_device_status() == (0, "")
 
 
 # ------------------------------------------------------------------ reading
