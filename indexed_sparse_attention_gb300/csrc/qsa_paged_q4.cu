@@ -114,26 +114,27 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ uint4 lds128(uint32_t at) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t at) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t at) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at));
-  return v;
-}
+__device__ __forceinline__ uint4 lds128(const uint8_t* at) { return *reinterpret_cast<const uint4*>(at); }
+__device__ __forceinline__ uint2 lds64(const uint8_t* at) { return *reinterpret_cast<const uint2*>(at); }
+__device__ __forceinline__ uint32_t lds32(const uint8_t* at) { return *reinterpret_cast<const uint32_t*>(at); }
+// c += a b, and c = a b.  (Not volatile: products of registers, which may be moved past
+// each other.)
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};\n"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};\n"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};\n"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// acc += f * d, two binary32 values at once.
+__device__ __forceinline__ void fma2(float& a0, float& a1, float f0, float f1, float d0, float d1) {
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%0, %1};\n"
+      " fma.rn.f32x2 z, x, y, z;\n mov.b64 {%0, %1}, z;\n}\n"
+      : "+f"(a0), "+f"(a1)
+      : "f"(f0), "f"(f1), "f"(d0), "f"(d1));
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -144,7 +145,7 @@ __device__ __forceinline__ uint32_t mul_f16(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ float low_half(uint32_t w) { return __half2float(__ushort_as_half((unsigned short)(w & 0xffffu))); }
+__device__ __forceinline__ float low_half(uint32_t w) { return __low2float(*reinterpret_cast<const __half2*>(&w)); }
 
 struct ItemRows {
   int f0, nf, pos0, first, last;
@@ -180,8 +181,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
   const PagedParams& p = qp.p;
   extern __shared__ __align__(1024) uint8_t raw[];
   Head& h = *reinterpret_cast<Head*>(raw);
-  const uint32_t ring = smem_addr(raw) + kHeadBytes;   // (1,024-byte boundaries: the head is 2 KB, slots are multiples)
-  const uint32_t q_s = ring + qp.n_slots * L::kSlot;
+  uint8_t* const ring = raw + kHeadBytes;   // (1,024-byte boundaries: the head is 2 KB, slots are multiples)
+  uint8_t* const q_s = ring + qp.n_slots * L::kSlot;
   float* const join_s = reinterpret_cast<float*>(raw + kHeadBytes + qp.n_slots * L::kSlot + L::kQ);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int* abrt = &h.abort;
@@ -216,24 +217,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
     // ------------------------------------------------------------ copies
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsCopy));
     if (warp > kWarps) return;
-    // A lane a box of K, V or the records.
+    // A lane a box of tokens: its K, V and records.
     const int box = min(1 << p.page_shift, kKT), n_box = kKT / box, page_mask = (1 << p.page_shift) - 1;
-    const int which = lane / n_box, my_box = lane % n_box;
-    const CUtensorMap* map = which == 0 ? &qp.k : which == 1 ? &qp.v : &qp.r;
-    const uint32_t at_box = which == 2 ? (uint32_t)(2 * L::kCodes + my_box * box * L::kRecord)
-                                       : (uint32_t)(which * L::kCodes + my_box * box * L::kRow);
-    const bool copies = which < 3;
+    const bool copies = lane < n_box;
     int tj = 0;
     bool live = true;
     for (bool more = true; more && live; more = c.next(p, kMT)) {
       const ItemRows ir = item_rows(p, c);
       const int T = c.x1 - c.x;
       auto wanted = [&](int j) {
-        const int t = c.tiles.token(c.x + j) + my_box * box, end = min(t + box - 1, ir.last);
+        const int t = c.tiles.token(c.x + j) + lane * box, end = min(t + box - 1, ir.last);
         return copies && t <= ir.last && (p.window == 0 || end > ir.first - p.window || t < p.n_sinks);
       };
       auto look_up = [&](int j) {
-        const int64_t s = (int64_t)(c.tiles.token(c.x + j) + my_box * box) >> p.page_shift;
+        const int64_t s = (int64_t)(c.tiles.token(c.x + j) + lane * box) >> p.page_shift;
         int32_t page = -1;
         if (wanted(j) && s < p.table_ld) page = __ldcg(p.table + c.seq * p.table_ld + s);
         return page;
@@ -248,15 +245,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
         const bool want = wanted(j), missing = want && (uint32_t)page >= (uint32_t)p.n_pages;
         if (!want || missing) page = p.n_pages;   // past the last page: zeros
         const uint32_t bad =
-            __reduce_or_sync(0xffffffffu, missing ? ((1u << (box / 16)) - 1u) << (my_box * (box / 16)) : 0u);
-        if (missing && which == 0) atomicAdd(&g_bad_pages, 1);
+            __reduce_or_sync(0xffffffffu, missing ? ((1u << (box / 16)) - 1u) << (lane * (box / 16)) : 0u);
+        if (missing) atomicAdd(&g_bad_pages, 1);
         if (lane == 0) {
           h.bad[(tj + j) & 15] = bad;
           bar_expect_tx(&h.full[slot], L::kSlot);
         }
         __syncwarp();
-        if (copies)
-          tma_4d(ring + slot * L::kSlot + at_box, map, 0, c.tiles.token(c.x + j) & page_mask, c.head, page, &h.full[slot]);
+        if (copies) {
+          const uint32_t to = smem_addr(ring) + slot * L::kSlot;
+          const int token = c.tiles.token(c.x + j) & page_mask;
+          tma_4d(to + lane * box * L::kRow, &qp.k, 0, token, c.head, page, &h.full[slot]);
+          tma_4d(to + L::kCodes + lane * box * L::kRow, &qp.v, 0, token, c.head, page, &h.full[slot]);
+          tma_4d(to + 2 * L::kCodes + lane * box * L::kRecord, &qp.r, 0, token, c.head, page, &h.full[slot]);
+        }
         __syncwarp();
         step();
         page = next;
@@ -349,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
           if (g == warp) {
 #pragma unroll
             for (int x2 = 0; x2 < 2; ++x2)
-              *reinterpret_cast<uint4*>(raw + (q_s - smem_addr(raw)) + (2 * g + x2) * 512 + lane * 16) =
+              *reinterpret_cast<uint4*>(q_s + (2 * g + x2) * 512 + lane * 16) =
                   make_uint4(frag[x2][0], frag[x2][1], frag[x2][2], frag[x2][3]);
           }
         } else {
@@ -404,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
       const bool gone = (h.bad[(tj + j) & 15] >> warp) & 1u;
       const bool any = !gone && t0 <= ir.last && (p.window == 0 || t0 + 15 > ir.first - p.window || t0 < p.n_sinks);
       if (any) {
-        const uint32_t ks = ring + slot * L::kSlot, vs = ks + L::kCodes, rs = ks + 2 * L::kCodes;
+        const uint8_t *const ks = ring + slot * L::kSlot, *const vs = ks + L::kCodes, *const rs = ks + 2 * L::kCodes;
         const bool edge = t0 + 15 > ir.first || (p.window > 0 && t0 <= ir.last - p.window && t0 + 16 > p.n_sinks);
         // ---- logits of two key columns of eight
         float z[2][4];
@@ -433,17 +435,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
 #pragma unroll
           for (int g = 0; g < G; ++g) {
             const uint32_t w = __byte_perm(wa[g / 2], wb[g / 2], g & 1 ? 0x7632 : 0x5410), w8 = w >> 8;
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
+            float d[4];
             uint32_t a[4];
             q_frag(2 * g, a);
-            mma(d, a, w & 0x000f000fu, w & 0x00f000f0u);
+            mma_first(d, a, w & 0x000f000fu, w & 0x00f000f0u);
             q_frag(2 * g + 1, a);
             mma(d, a, w8 & 0x000f000fu, w8 & 0x00f000f0u);
             const float f0 = low_half(s0[g]), f1 = low_half(s1[g]);
-            acc[0] = fmaf(f0, d[0], acc[0]);
-            acc[1] = fmaf(f1, d[1], acc[1]);
-            acc[2] = fmaf(f0, d[2], acc[2]);
-            acc[3] = fmaf(f1, d[3], acc[3]);
+            fma2(acc[0], acc[1], f0, f1, d[0], d[1]);
+            fma2(acc[2], acc[3], f0, f1, d[2], d[3]);
           }
           // Minima of blocks 2 t, 2 t + 1 of key column n, against both halves of the sums.
           uint32_t mm = 0u;
@@ -451,8 +451,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
             const uint2 two = lds64(rs + swizzled<L::kRecord>(kr, t >> 1) + 8 * (t & 1));
             mm = __byte_perm(two.x, two.y, 0x7632);
           }
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
-          mma(d, qm, mm, mm);
+          float d[4];
+          mma_first(d, qm, mm, mm);
 #pragma unroll
           for (int e = 0; e < 4; ++e) z[hf][e] = fmaf(acc[e], 0x1p20f, d[e]);
         }

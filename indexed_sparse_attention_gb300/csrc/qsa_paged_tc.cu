@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __g
   if (tid == 0) {
     for (int kv = 0; kv < 2; ++kv) {
       for (int i = 0; i < kMaxSlabs; ++i) {
-        bar_init(&h.full[kv][i], Q4 || (F8 && kv == 1) ? code_warps : 1);
+        bar_init(&h.full[kv][i], Q4 ? code_warps / 2 : F8 && kv == 1 ? code_warps : 1);
         bar_init(&h.empty[kv][i], 1);
       }
     }
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __g
     for (int i = 0; CODES && i < 8; ++i) bar_init(&h.sc_full[i], kCodeWarps);
     for (int i = 0; Q4 && i < 2 * kMaxQ4Slots; ++i) {
       bar_init(&q4.code_full[0][0] + i, 1);
-      bar_init(&q4.code_empty[0][0] + i, code_warps);
+      bar_init(&q4.code_empty[0][0] + i, code_warps / 2);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(&h.s_full[i], 1);
@@ -543,7 +543,12 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __g
     const int cw = warp >= kCodeWarp ? warp - kCodeWarp : kCodeWarps + (warp >> 2) * (4 - quarters) + (warp & 3) - quarters;
     const bool own = cw < kCodeWarps;   // Q is these warps'
     constexpr int G = D / 32, kSlotTokens = Q4Slot<D>::kTokens, kBlocks = kSlotTokens / 8;
-    Ring in[2], out[2];
+    // Half of the warps expand K, the others V: each waits for its own ring only.
+    const int kv = cw & 1, kv_warps = code_warps / 2;
+    const int n_ring = kv ? tp.n_v : tp.n_k;
+    uint8_t* const ring = kv ? v_ring : k_ring;
+    const uint8_t* const codes = v_codes + kv * tp.n_code_v * Q4Slot<D>::kBytes;
+    Ring in, out;
     int it = 0;
     for (bool more = true; more; more = c.next(p, p.mt), ++it) {
       const ItemRows ir = item_rows(p, c);
@@ -610,18 +615,17 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __g
       // lanes next to each other take tokens that differ in bits 0 and 2, so that the
       // loads and the stores of eight lanes touch all 32 banks.
       const int i = lane & 3, q8 = lane >> 2, in8 = q8 & 1 ? (q8 >> 1) ^ 5 : q8 >> 1;
-      auto expand = [&](int kv, int j) {
+#pragma unroll 1
+      for (int j = 0; j < T; ++j) {
         const int t0 = c.tiles.token(c.x + j);
         auto slot_of = [&](int t) { return min(max(t - t0, 0), kKT); };
         const int cut = slot_of(ir.last + 1);
         const int gap0 = p.window > 0 ? slot_of(p.n_sinks) : 0;
         const int gap1 = p.window > 0 ? slot_of(ir.first - p.window + 1) : 0;
         const bool some = kv == 1 && (cut < kKT || gap0 < gap1);
-        const int n_ring = kv ? tp.n_v : tp.n_k;
-        uint8_t* const ring = kv ? v_ring : k_ring;
-        int block = cw;   // the warp's next eight tokens, counted from the slot's first
+        int block = cw >> 1;   // the warp's next eight tokens, counted from the slot's first
         uint8_t* slabs[NS];
-        Ring o = out[kv];
+        Ring o = out;
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
           if (o.use > 0) wait(&h.empty[kv][o.slot], (o.use - 1) & 1, abrt);
@@ -630,10 +634,10 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __g
         }
 #pragma unroll 1
         for (int sub = 0; sub < kKT / kSlotTokens; ++sub) {
-          wait(&q4.code_full[kv][in[kv].slot], in[kv].use & 1, abrt);
-          const uint8_t* src = v_codes + (kv * tp.n_code_v + in[kv].slot) * Q4Slot<D>::kBytes;
-#pragma unroll 1
-          for (; block < kBlocks; block += code_warps) {
+          wait(&q4.code_full[kv][in.slot], in.use & 1, abrt);
+          const uint8_t* src = codes + in.slot * Q4Slot<D>::kBytes;
+#pragma unroll 2
+          for (; block < kBlocks; block += kv_warps) {
             const int r = 8 * block + in8, R = sub * kSlotTokens + r;
             uint32_t a[G / 2], b[G / 2], rec[G];   // units 2 i, 2 i + 1 of blocks (0, 1), (2, 3), ...
             if constexpr (D == 256) {
@@ -671,21 +675,16 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __g
           }
           block -= kBlocks;
           __syncwarp();
-          if (lane == 0) bar_arrive(&q4.code_empty[kv][in[kv].slot]);
-          in[kv].step(tp.n_code_v);
+          if (lane == 0) bar_arrive(&q4.code_empty[kv][in.slot]);
+          in.step(tp.n_code_v);
         }
         fence_async_smem();
         __syncwarp();
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
-          if (lane == 0) bar_arrive(&h.full[kv][out[kv].slot]);
-          out[kv].step(n_ring);
+          if (lane == 0) bar_arrive(&h.full[kv][out.slot]);
+          out.step(n_ring);
         }
-      };
-#pragma unroll 1
-      for (int j = 0; j < T + NB - 1; ++j) {
-        if (j < T) expand(0, j);
-        if (j >= NB - 1) expand(1, j - (NB - 1));
       }
     }
   } else if (F8 && (warp >= kCodeWarp || (warp < kSoftWarps && (warp & 3) >= quarters))) {
