@@ -57,8 +57,8 @@ constexpr int kRegsCompute = 232, kRegsCopy = 40;
 constexpr int kMT = 16;                  // entries of an item
 constexpr int kMaxSlots = 10;
 constexpr int kSmemLimit = 227 * 1024;
-constexpr float kTop = 6.f;              // log2 of the largest weight when the maximum is up to date
-constexpr float kLag = 4.f;              // log2 of what a weight may pass it by
+constexpr float kTop = 3.f;              // log2 of the largest weight when the maximum is up to date
+constexpr float kLag = 7.f;              // log2 of what a weight may pass it by
 constexpr float kScaleTop = 5.f;         // log2 of the scales that this leaves room for
 
 __device__ int g_timeouts;

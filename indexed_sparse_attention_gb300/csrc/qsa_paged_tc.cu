@@ -276,6 +276,11 @@ __device__ __forceinline__ uint32_t fma_f16(uint32_t a, uint32_t b, uint32_t c) 
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
+__device__ __forceinline__ uint32_t add_f16(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
@@ -555,7 +560,8 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __g
       const int T = c.x1 - c.x;
       // Q as f16: times a power of two that brings the row's largest magnitude to [2^14,
       // 2^15) a value of bf16's 8 bits is exact from 2^-31 of it on, and off by at most
-      // 2^-39 of it below.  A warp a row, D / 32 channels a lane, four rows in flight.
+      // 2^-39 of it below.  Of each 8 channels, j and 4 + j lie side by side, as K's do (see
+      // below).  A warp a row, D / 32 channels a lane, four rows in flight.
       if (own) {
         if (it > 0) wait(&h.q_free, (uint32_t)((it - 1) & 1), abrt);
         constexpr int kCh = D / 32, kBatch = 4;
@@ -589,10 +595,21 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __g
             const int e = max((int)(most >> 23) - 127 - 14, -100);
             const float up = __uint_as_float((uint32_t)(127 - e) << 23);
             const bool odd = most >= 0x7f800000u;   // infinity or NaN: the row's logits are NaN
+            // Pairs of channels (j, 4 + j); of head_dim 128 the other half of the 8 is with the
+            // lane beside this one, which takes j = 2 and 3 where this one takes 0 and 1.
+            uint32_t lo4[2], hi4[2];   // channels 0 1, 2 3 and 4 5, 6 7
+            if constexpr (kCh == 8) {
+              lo4[0] = x[b][0], lo4[1] = x[b][1], hi4[0] = x[b][2], hi4[1] = x[b][3];
+            } else {
+              const uint32_t other = __shfl_xor_sync(0xffffffffu, lane & 1 ? x[b][0] : x[b][1], 1);
+              lo4[0] = lane & 1 ? other : x[b][0], hi4[0] = lane & 1 ? x[b][1] : other;
+            }
             uint32_t f16[kCh / 2];
 #pragma unroll
-            for (int i = 0; i < kCh / 2; ++i)
-              f16[i] = odd ? 0x7fff7fffu : pack_f16(__uint_as_float(x[b][i] << 16) * up, __uint_as_float(x[b][i] & 0xffff0000u) * up);
+            for (int i = 0; i < kCh / 4; ++i) {
+              f16[2 * i] = odd ? 0x7fff7fffu : pack_f16(__uint_as_float(lo4[i] << 16) * up, __uint_as_float(hi4[i] << 16) * up);
+              f16[2 * i + 1] = odd ? 0x7fff7fffu : pack_f16(__uint_as_float(lo4[i] & 0xffff0000u) * up, __uint_as_float(hi4[i] & 0xffff0000u) * up);
+            }
             if (row < ir.nf) {
               const int byte = (at_c & 63) * 2;
               const int at = row * 128 + ((((byte >> 4) ^ (row & 7)) << 4) | (byte & 15));
@@ -613,8 +630,12 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __g
       // scale + minimum, rounded once.  V: tokens that no row sees become zeros.
       // Four lanes a token, each the units 2 i and 2 i + 1 (8 channels) of every block;
       // lanes next to each other take tokens that differ in bits 0 and 2, so that the
-      // loads and the stores of eight lanes touch all 32 banks.
+      // loads and the stores of eight lanes touch all 32 banks.  Of a block's 8 channels, j
+      // and 4 + j (nibbles j of the two units) are one pair of halves and stay side by side.
       const int i = lane & 3, q8 = lane >> 2, in8 = q8 & 1 ? (q8 >> 1) ^ 5 : q8 >> 1;
+      constexpr int kRow = D / 2, kRec = D / 8;   // bytes of a token
+      const int from = in8 * kRow + (D == 256 ? (2 * i ^ in8) << 4 : (i ^ (in8 >> 1)) << 4);
+      const int to = in8 * 128 + ((i ^ in8) << 4);
 #pragma unroll 1
       for (int j = 0; j < T; ++j) {
         const int t0 = c.tiles.token(c.x + j);
@@ -624,53 +645,51 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __g
         const int gap1 = p.window > 0 ? slot_of(ir.first - p.window + 1) : 0;
         const bool some = kv == 1 && (cut < kKT || gap0 < gap1);
         int block = cw >> 1;   // the warp's next eight tokens, counted from the slot's first
-        uint8_t* slabs[NS];
         Ring o = out;
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
           if (o.use > 0) wait(&h.empty[kv][o.slot], (o.use - 1) & 1, abrt);
-          slabs[s] = ring + o.slot * kSlab;
           o.step(n_ring);
         }
+        // (A tile of head_dim 256 takes both slabs of the ring, in order.)
+        uint8_t* const slab = ring + out.slot * kSlab + to;
 #pragma unroll 1
         for (int sub = 0; sub < kKT / kSlotTokens; ++sub) {
           wait(&q4.code_full[kv][in.slot], in.use & 1, abrt);
-          const uint8_t* src = codes + in.slot * Q4Slot<D>::kBytes;
+          const uint8_t* const src = codes + in.slot * Q4Slot<D>::kBytes;
 #pragma unroll 2
           for (; block < kBlocks; block += kv_warps) {
-            const int r = 8 * block + in8, R = sub * kSlotTokens + r;
             uint32_t a[G / 2], b[G / 2], rec[G];   // units 2 i, 2 i + 1 of blocks (0, 1), (2, 3), ...
             if constexpr (D == 256) {
-              const uint4 x = *reinterpret_cast<const uint4*>(src + r * 128 + ((2 * i ^ (r & 7)) << 4)),
-                          y = *reinterpret_cast<const uint4*>(src + r * 128 + (((2 * i + 1) ^ (r & 7)) << 4));
+              const uint4 x = *reinterpret_cast<const uint4*>(src + (block * 8 * kRow + from)),
+                          y = *reinterpret_cast<const uint4*>(src + (block * 8 * kRow + (from ^ 16)));
               a[0] = x.x, a[1] = x.y, a[2] = x.z, a[3] = x.w;
               b[0] = y.x, b[1] = y.y, b[2] = y.z, b[3] = y.w;
             } else {
-              const uint4 x = *reinterpret_cast<const uint4*>(src + r * 64 + ((i ^ ((r >> 1) & 3)) << 4));
+              const uint4 x = *reinterpret_cast<const uint4*>(src + (block * 8 * kRow + from));
               a[0] = x.x, a[1] = x.y, b[0] = x.z, b[1] = x.w;
             }
 #pragma unroll
             for (int g = 0; g < G; g += 4) {
-              const uint4 x = *reinterpret_cast<const uint4*>(src + Q4Slot<D>::kCodes + r * (D / 8) + 4 * g);
+              const uint4 x = *reinterpret_cast<const uint4*>(src + Q4Slot<D>::kCodes + (block * 8 + in8) * kRec + 4 * g);
               rec[g] = x.x, rec[g + 1] = x.y, rec[g + 2] = x.z, rec[g + 3] = x.w;
             }
-            const bool gone = some && (R >= cut || (R >= gap0 && R < gap1));
+            const int R0 = sub * kSlotTokens + block * 8, R = R0 + in8;
+            if (some && (R >= cut || (R >= gap0 && R < gap1))) {
+#pragma unroll
+              for (int g = 0; g < G; ++g) rec[g] = 0u;
+            }
+            uint8_t* const at = slab + R0 * 128;
 #pragma unroll
             for (int g = 0; g < G; ++g) {
               const uint32_t s2 = __byte_perm(rec[g], 0u, 0x1010), m2 = __byte_perm(rec[g], 0u, 0x3232);
-              uint32_t w[4];
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                // A unit's nibbles 0 and 1 (then 2 and 3) under the exponents of 1024 and 64,
-                // which the first fma takes off exactly.
-                const uint32_t two = __byte_perm(u ? b[g / 2] : a[g / 2], 0u, g & 1 ? 0x3232 : 0x1010), hi = two >> 8;
-                w[2 * u] = fma_f16(fma_f16((two & 0x00f0000fu) | 0x64006400u, 0x2c003c00u, 0xd400e400u), s2, m2);
-                w[2 * u + 1] = fma_f16(fma_f16((hi & 0x00f0000fu) | 0x64006400u, 0x2c003c00u, 0xd400e400u), s2, m2);
-              }
-              if (gone) w[0] = w[1] = w[2] = w[3] = 0u;
-              const int chunk = ((g & 1) << 2) | i;
-              *reinterpret_cast<uint4*>(slabs[g >> 2] + ((g >> 1) & 1) * kHalf + R * 128 + ((chunk ^ (R & 7)) << 4)) =
-                  make_uint4(w[0], w[1], w[2], w[3]);
+              const uint32_t lo = __byte_perm(a[g / 2], b[g / 2], g & 1 ? 0x7632 : 0x5410), hi = lo >> 8;
+              // Bits 0-3 of the halves are the units of 1024's mantissa, bits 4-7 those of 64's.
+              *reinterpret_cast<uint4*>((g & 1 ? slab + ((to ^ 64) - to) + R0 * 128 : at) + (g >> 2) * kSlab + ((g >> 1) & 1) * kHalf) =
+                  make_uint4(fma_f16(add_f16((lo & 0x000f000fu) | 0x64006400u, 0xe400e400u), s2, m2),
+                             fma_f16(add_f16((lo & 0x00f000f0u) | 0x54005400u, 0xd400d400u), s2, m2),
+                             fma_f16(add_f16((hi & 0x000f000fu) | 0x64006400u, 0xe400e400u), s2, m2),
+                             fma_f16(add_f16((hi & 0x00f000f0u) | 0x54005400u, 0xd400d400u), s2, m2));
             }
           }
           block -= kBlocks;
@@ -1211,6 +1230,14 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __g
         tmem_ld32_start(lanes + kOCol + (uint32_t)d, o);
         tmem_ld_wait(o);
         if (!mine) continue;
+        if constexpr (Q4) {   // columns 2 j and 2 j + 1 of 8 are channels j and 4 + j
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            const uint32_t x[8] = {o[e], o[e + 2], o[e + 4], o[e + 6], o[e + 1], o[e + 3], o[e + 5], o[e + 7]};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[e + k] = x[k];
+          }
+        }
         if (!whole || p.out_dtype == QSA_F32) {
           float* to = (whole ? static_cast<float*>(p.out) + entry * D : p.part_o + part * D) + d;
 #pragma unroll
