@@ -276,6 +276,13 @@ __device__ __forceinline__ uint32_t fma_f16(uint32_t a, uint32_t b, uint32_t c) 
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
+// (a & mask) | b in one instruction: b from a register.
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(a), "n"(MASK), "r"(b));
+  return r;
+}
 __device__ __forceinline__ uint32_t add_f16(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -634,6 +641,8 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __g
       // and 4 + j (nibbles j of the two units) are one pair of halves and stay side by side.
       const int i = lane & 3, q8 = lane >> 2, in8 = q8 & 1 ? (q8 >> 1) ^ 5 : q8 >> 1;
       constexpr int kRow = D / 2, kRec = D / 8;   // bytes of a token
+      uint32_t m1024 = 0x64006400u, m64 = 0x54005400u;   // kept in registers
+      asm volatile("" : "+r"(m1024), "+r"(m64));
       const int from = in8 * kRow + (D == 256 ? (2 * i ^ in8) << 4 : (i ^ (in8 >> 1)) << 4);
       const int to = in8 * 128 + ((i ^ in8) << 4);
 #pragma unroll 1
@@ -686,10 +695,10 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __g
               const uint32_t lo = __byte_perm(a[g / 2], b[g / 2], g & 1 ? 0x7632 : 0x5410), hi = lo >> 8;
               // Bits 0-3 of the halves are the units of 1024's mantissa, bits 4-7 those of 64's.
               *reinterpret_cast<uint4*>((g & 1 ? slab + ((to ^ 64) - to) + R0 * 128 : at) + (g >> 2) * kSlab + ((g >> 1) & 1) * kHalf) =
-                  make_uint4(fma_f16(add_f16((lo & 0x000f000fu) | 0x64006400u, 0xe400e400u), s2, m2),
-                             fma_f16(add_f16((lo & 0x00f000f0u) | 0x54005400u, 0xd400d400u), s2, m2),
-                             fma_f16(add_f16((hi & 0x000f000fu) | 0x64006400u, 0xe400e400u), s2, m2),
-                             fma_f16(add_f16((hi & 0x00f000f0u) | 0x54005400u, 0xd400d400u), s2, m2));
+                  make_uint4(fma_f16(add_f16(and_or<0x000f000fu>(lo, m1024), 0xe400e400u), s2, m2),
+                             fma_f16(add_f16(and_or<0x00f000f0u>(lo, m64), 0xd400d400u), s2, m2),
+                             fma_f16(add_f16(and_or<0x000f000fu>(hi, m1024), 0xe400e400u), s2, m2),
+                             fma_f16(add_f16(and_or<0x00f000f0u>(hi, m64), 0xd400d400u), s2, m2));
             }
           }
           block -= kBlocks;
