@@ -82,7 +82,18 @@ constexpr int kKeyWarp = 8, kMmaWarp = 9, kValueWarp = 10, kQWarp = 11, kCodeWar
 constexpr int kSoftWarps = 8;
 // How the cache holds K and V.
 constexpr int kBf16 = 0, kFp8 = 1, kQ4 = 2;
-__host__ __device__ constexpr int threads_of(int kind) { return 32 * (kind != kBf16 ? kCodeWarp + kCodeWarps : kQWarp + 1); }
+// 4-bit caches: four more warps expand codes, 20 in all, with 96 registers a thread at
+// launch (61,440).  The copying and issuing warpgroup leaves what the softmax's two need:
+// 256 * 136 + 128 * 48 + 256 * 80 = 61,440.
+constexpr int kQ4CodeWarps = 8;
+constexpr int kQ4SoftRegs = 136, kQ4CopyRegs = 48, kQ4CodeRegs = 80;
+__host__ __device__ constexpr int code_warps_of(int kind) { return kind == kBf16 ? 0 : kind == kQ4 ? kQ4CodeWarps : kCodeWarps; }
+__host__ __device__ constexpr int threads_of(int kind) { return 32 * (kind != kBf16 ? kCodeWarp + code_warps_of(kind) : kQWarp + 1); }
+template <int REGS, bool MORE>
+__device__ __forceinline__ void set_registers() {
+  if constexpr (MORE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(REGS));
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(REGS));
+}
 constexpr int kCodeSlab = kKT * 128;          // bytes of the codes of a slab (fp8 caches)
 constexpr int kMaxCodeSlabs = 4;             // of V
 // 4-bit caches: a slot of codes is the K, or the V, of 32 (head_dim 256, where Q and the
@@ -126,8 +137,12 @@ struct TcParams {
 __device__ __noinline__ bool wait_slow(uint64_t* b, uint32_t parity, int* abort) {
   return bar_wait(b, parity, &g_timeouts, abort);
 }
-__device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, int* abort) {
-  return bar_try(b, parity) || wait_slow(b, parity, abort);
+// (With registers moved between warpgroups the compiler takes no calls.)
+template <bool INLINE>
+__device__ __forceinline__ bool wait_for(uint64_t* b, uint32_t parity, int* abort) {
+  if (bar_try(b, parity)) return true;
+  if constexpr (INLINE) return bar_wait(b, parity, &g_timeouts, abort);
+  else return wait_slow(b, parity, abort);
 }
 
 // Shared memory: this, then Q, then the ring (both on 1,024-byte boundaries).
@@ -389,6 +404,8 @@ struct Ring {
 template <int D, int KIND>
 __global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __grid_constant__ TcParams tp) {
   constexpr bool F8 = KIND == kFp8, Q4 = KIND == kQ4, CODES = F8 || Q4;
+  constexpr int kCodeWarps = code_warps_of(KIND);
+  auto wait = [](uint64_t* b, uint32_t parity, int* abort) { return wait_for<Q4>(b, parity, abort); };
   constexpr int NS = D / 128;            // slabs of a tile
   constexpr int NB = 2;                  // buffers of logits in TMEM
   constexpr uint32_t kOCol = NB * kKT;   // O behind them
@@ -412,8 +429,8 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __g
   uint8_t* v_codes = v_ring + tp.n_v * kSlab;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int quarters = (p.mt + 31) / 32, soft_threads = 64 * quarters;
-  // Warps that convert V's codes: their own four, and those of the softmax's eight without entries.
-  const int code_warps = kCodeWarps + (kSoftWarps - 2 * quarters);
+  // Warps that convert codes: their own, and (fp8) those of the softmax's eight without entries.
+  const int code_warps = kCodeWarps + (Q4 ? 0 : kSoftWarps - 2 * quarters);
   int* abrt = &h.abort;
 
   if (tid == 0) {
@@ -461,12 +478,14 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __g
   c.begin(p, p.mt, st);
   if (tid == 0) h.start = st;   // for the end (this thread's): registers are short
 
+  // (4-bit: the roles end by themselves, so that registers need not be the same again behind them.)
   if (st.n == 0) {
     if (tid == 0) p.parts[blockIdx.x] = PagedPart{};
   } else if (warp == kKeyWarp || warp == kValueWarp) {
     // ------------------------------------------------------------ K, or V
     // (bf16: into the ring of operands; fp8: codes into their own.)  One lane
     // issues, with values that all lanes agree on; see the products below.
+    if constexpr (Q4) set_registers<kQ4CopyRegs, false>();
     const int kv = warp == kValueWarp ? 1 : 0;
     const CUtensorMap* map = kv ? &tp.v : &tp.k;
     constexpr int kSlotTokens = Q4 ? Q4Slot<D>::kTokens : kKT;   // 4-bit: slots of fewer tokens, all channels
@@ -550,10 +569,11 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __g
       const uint32_t uses = at.use + (lane < at.slot ? 1u : 0u);
       if (uses > 0) bar_wait(fulls + lane, (uses - 1) & 1, &g_timeouts);
     }
-  } else if (Q4 && (warp >= kCodeWarp || (warp < kSoftWarps && (warp & 3) >= quarters))) {
+    if constexpr (Q4) return;
+  } else if (Q4 && warp >= kCodeWarp) {
     // ------------------------------------------------------------ 4-bit: Q, K, V
-    const int cw = warp >= kCodeWarp ? warp - kCodeWarp : kCodeWarps + (warp >> 2) * (4 - quarters) + (warp & 3) - quarters;
-    const bool own = cw < kCodeWarps;   // Q is these warps'
+    if constexpr (Q4) set_registers<kQ4CodeRegs, false>();
+    const int cw = warp - kCodeWarp;
     constexpr int G = D / 32, kSlotTokens = Q4Slot<D>::kTokens, kBlocks = kSlotTokens / 8;
     // Half of the warps expand K, the others V: each waits for its own ring only.
     const int kv = cw & 1, kv_warps = code_warps / 2;
@@ -569,7 +589,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __g
       // 2^15) a value of bf16's 8 bits is exact from 2^-31 of it on, and off by at most
       // 2^-39 of it below.  Of each 8 channels, j and 4 + j lie side by side, as K's do (see
       // below).  A warp a row, D / 32 channels a lane, four rows in flight.
-      if (own) {
+      {
         if (it > 0) wait(&h.q_free, (uint32_t)((it - 1) & 1), abrt);
         constexpr int kCh = D / 32, kBatch = 4;
         const int at_c = lane * kCh;
@@ -666,7 +686,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __g
         for (int sub = 0; sub < kKT / kSlotTokens; ++sub) {
           wait(&q4.code_full[kv][in.slot], in.use & 1, abrt);
           const uint8_t* const src = codes + in.slot * Q4Slot<D>::kBytes;
-#pragma unroll 2
+#pragma unroll 1
           for (; block < kBlocks; block += kv_warps) {
             uint32_t a[G / 2], b[G / 2], rec[G];   // units 2 i, 2 i + 1 of blocks (0, 1), (2, 3), ...
             if constexpr (D == 256) {
@@ -715,6 +735,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __g
         }
       }
     }
+    return;
   } else if (F8 && (warp >= kCodeWarp || (warp < kSoftWarps && (warp & 3) >= quarters))) {
     // ------------------------------------------------------------ fp8: Q, scales, V
     const int cw = warp >= kCodeWarp ? warp - kCodeWarp : kCodeWarps + (warp >> 2) * (4 - quarters) + (warp & 3) - quarters;
@@ -965,6 +986,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __g
     // all its lanes, and one lane issues: descriptors then stay in uniform
     // registers.  (One lane that walks alone has to move each of them over:
     // 115 cycles an MMA instead of the 32 and 64 that the products take.)
+    if constexpr (Q4) set_registers<kQ4CopyRegs, false>();
     const bool leader = elect_one();
     const uint64_t q_desc = desc_sw128(q_s, 16, 1024), k_desc = desc_sw128(k_ring, 16, 1024),
                    v_desc = desc_sw128(v_ring, kHalf, 1024);
@@ -1055,9 +1077,16 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __g
     if (leader) commit(&h.mma_done);   // every MMA has completed before TMEM is released
     __syncwarp();
     bar_wait(&h.mma_done, 0u, &g_timeouts);
-  } else if (warp < kSoftWarps && (warp & 3) < quarters) {
+    if constexpr (Q4) {
+      named_sync(15, 32 * (kSoftWarps + 1));   // the softmax's warps have read TMEM
+      fence_after();
+      tmem_dealloc(tmem, kTmemCols);
+      return;
+    }
+  } else if (warp < kSoftWarps && (Q4 || (warp & 3) < quarters)) {
     // ------------------------------------------------------------ softmax and output
     // A thread owns one entry, and the keys [64 group, 64 group + 64) of each tile.
+    if constexpr (Q4) set_registers<kQ4SoftRegs, true>();
     const int group = warp >> 2, row = 32 * (warp & 3) + lane;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     // Logits to base 2; the scales of an fp8 cache's keys hold the factor already,
@@ -1065,7 +1094,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __g
     float zc = p.scale * kLog2e, move = fminf(kMoveMax / zc, 1e30f);
     int tj = 0;   // tiles done
     [[maybe_unused]] int it = 0;
-    for (bool more = true; more;) {
+    for (bool more = !Q4 || (warp & 3) < quarters; more;) {
       const ItemRows ir = item_rows(p, c);
       const int T = c.x1 - c.x;
       const bool mine = row < ir.nf;
@@ -1274,6 +1303,15 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __g
       more = c.next(p, p.mt);
       if (!more && tid == 0) describe_part(p, c, h.start, blockIdx.x);   // (still at its last item)
     }
+    if constexpr (Q4) {
+      __syncwarp();
+      fence_before();
+      asm volatile("bar.arrive %0, %1;\n" ::"r"(15), "r"(32 * (kSoftWarps + 1)) : "memory");
+      return;
+    }
+  } else if constexpr (Q4) {
+    set_registers<kQ4CopyRegs, false>();   // the copying warpgroup's fourth warp
+    return;
   }
   __syncwarp();
   fence_before();
