@@ -574,9 +574,10 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __g
     // ------------------------------------------------------------ 4-bit: Q, K, V
     if constexpr (Q4) set_registers<kQ4CodeRegs, false>();
     const int cw = warp - kCodeWarp;
-    constexpr int G = D / 32, kSlotTokens = Q4Slot<D>::kTokens, kBlocks = kSlotTokens / 8;
+    constexpr int G = D / 32, kSlotTokens = Q4Slot<D>::kTokens, kSlots = kKT / kSlotTokens;
+    static_assert(kQ4CodeWarps == 8 && (kSlots == 1 || kSlots == 4), "four warps a tile of K, and of V");
     // Half of the warps expand K, the others V: each waits for its own ring only.
-    const int kv = cw & 1, kv_warps = code_warps / 2;
+    const int kv = cw & 1;
     const int n_ring = kv ? tp.n_v : tp.n_k;
     uint8_t* const ring = kv ? v_ring : k_ring;
     const uint8_t* const codes = v_codes + kv * tp.n_code_v * Q4Slot<D>::kBytes;
@@ -673,58 +674,62 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __g
         const int gap0 = p.window > 0 ? slot_of(p.n_sinks) : 0;
         const int gap1 = p.window > 0 ? slot_of(ir.first - p.window + 1) : 0;
         const bool some = kv == 1 && (cut < kKT || gap0 < gap1);
-        int block = cw >> 1;   // the warp's next eight tokens, counted from the slot's first
-        Ring o = out;
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
-          if (o.use > 0) wait(&h.empty[kv][o.slot], (o.use - 1) & 1, abrt);
-          o.step(n_ring);
-        }
-        // (A tile of head_dim 256 takes both slabs of the ring, in order.)
-        uint8_t* const slab = ring + out.slot * kSlab + to;
+        // The warp's four blocks of eight tokens: one of each slot, or four of the one.  Codes
+        // go to registers, as many as there are, before the slab they will fill is free.
+        constexpr int kAhead = D == 256 ? 2 : 4;
 #pragma unroll 1
-        for (int sub = 0; sub < kKT / kSlotTokens; ++sub) {
-          wait(&q4.code_full[kv][in.slot], in.use & 1, abrt);
-          const uint8_t* const src = codes + in.slot * Q4Slot<D>::kBytes;
-#pragma unroll 1
-          for (; block < kBlocks; block += kv_warps) {
-            uint32_t a[G / 2], b[G / 2], rec[G];   // units 2 i, 2 i + 1 of blocks (0, 1), (2, 3), ...
-            if constexpr (D == 256) {
-              const uint4 x = *reinterpret_cast<const uint4*>(src + (block * 8 * kRow + from)),
-                          y = *reinterpret_cast<const uint4*>(src + (block * 8 * kRow + (from ^ 16)));
-              a[0] = x.x, a[1] = x.y, a[2] = x.z, a[3] = x.w;
-              b[0] = y.x, b[1] = y.y, b[2] = y.z, b[3] = y.w;
-            } else {
-              const uint4 x = *reinterpret_cast<const uint4*>(src + (block * 8 * kRow + from));
-              a[0] = x.x, a[1] = x.y, b[0] = x.z, b[1] = x.w;
-            }
+        for (int b0 = 0; b0 < 4; b0 += kAhead) {
+          uint4 w[kAhead][G / 4], rec[kAhead][G / 4];   // units 2 i and 2 i + 1; scales and minima
 #pragma unroll
-            for (int g = 0; g < G; g += 4) {
-              const uint4 x = *reinterpret_cast<const uint4*>(src + Q4Slot<D>::kCodes + (block * 8 + in8) * kRec + 4 * g);
-              rec[g] = x.x, rec[g + 1] = x.y, rec[g + 2] = x.z, rec[g + 3] = x.w;
-            }
-            const int R0 = sub * kSlotTokens + block * 8, R = R0 + in8;
-            if (some && (R >= cut || (R >= gap0 && R < gap1))) {
+          for (int k = 0; k < kAhead; ++k) {
+            const bool opens = kSlots == 4 || k == 0, closes = kSlots == 4 || k == kAhead - 1;
+            const int block = (cw >> 1) + (kSlots == 4 ? 0 : 4 * k);
+            if (opens) wait(&q4.code_full[kv][in.slot], in.use & 1, abrt);
+            const uint8_t* const src = codes + in.slot * Q4Slot<D>::kBytes;
 #pragma unroll
-              for (int g = 0; g < G; ++g) rec[g] = 0u;
+            for (int x = 0; x < G / 4; ++x) {
+              w[k][x] = *reinterpret_cast<const uint4*>(src + (block * 8 * kRow + (from ^ (16 * x))));
+              rec[k][x] = *reinterpret_cast<const uint4*>(src + Q4Slot<D>::kCodes + (block * 8 + in8) * kRec + 16 * x);
             }
-            uint8_t* const at = slab + R0 * 128;
+            if (closes) {
+              __syncwarp();
+              if (lane == 0) bar_arrive(&q4.code_empty[kv][in.slot]);
+              in.step(tp.n_code_v);
+            }
+          }
+          if (b0 == 0) {
+            Ring o = out;
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+              if (o.use > 0) wait(&h.empty[kv][o.slot], (o.use - 1) & 1, abrt);
+              o.step(n_ring);
+            }
+          }
+          // (A tile of head_dim 256 takes both slabs of the ring, in order.)
+          uint8_t* const slab = ring + out.slot * kSlab + to;
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) {
+            const int R0 = kSlots == 4 ? (b0 + k) * kSlotTokens + (cw >> 1) * 8 : ((cw >> 1) + 4 * k) * 8, R = R0 + in8;
+            const bool gone = some && (R >= cut || (R >= gap0 && R < gap1));
+            uint8_t *const even = slab + R0 * 128, *const odd = even + ((to ^ 64) - to);
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-              const uint32_t s2 = __byte_perm(rec[g], 0u, 0x1010), m2 = __byte_perm(rec[g], 0u, 0x3232);
-              const uint32_t lo = __byte_perm(a[g / 2], b[g / 2], g & 1 ? 0x7632 : 0x5410), hi = lo >> 8;
+              const uint32_t a4[4] = {w[k][0].x, w[k][0].y, w[k][0].z, w[k][0].w},
+                             b4[4] = {w[k][G / 4 - 1].x, w[k][G / 4 - 1].y, w[k][G / 4 - 1].z, w[k][G / 4 - 1].w},
+                             r4[4] = {rec[k][g / 4].x, rec[k][g / 4].y, rec[k][g / 4].z, rec[k][g / 4].w};
+              // Unit 2 i of blocks (g, g + 1), and unit 2 i + 1: 16 bytes each, or one 16 bytes of both.
+              const uint32_t ua = D == 256 ? a4[g / 2] : a4[(g / 2) & 1], ub = D == 256 ? b4[g / 2] : b4[2 + ((g / 2) & 1)];
+              const uint32_t r1 = gone ? 0u : r4[g & 3];
+              const uint32_t s2 = __byte_perm(r1, 0u, 0x1010), m2 = __byte_perm(r1, 0u, 0x3232);
+              const uint32_t lo = __byte_perm(ua, ub, g & 1 ? 0x7632 : 0x5410), hi = lo >> 8;
               // Bits 0-3 of the halves are the units of 1024's mantissa, bits 4-7 those of 64's.
-              *reinterpret_cast<uint4*>((g & 1 ? slab + ((to ^ 64) - to) + R0 * 128 : at) + (g >> 2) * kSlab + ((g >> 1) & 1) * kHalf) =
+              *reinterpret_cast<uint4*>((g & 1 ? odd : even) + (g >> 2) * kSlab + ((g >> 1) & 1) * kHalf) =
                   make_uint4(fma_f16(add_f16(and_or<0x000f000fu>(lo, m1024), 0xe400e400u), s2, m2),
                              fma_f16(add_f16(and_or<0x00f000f0u>(lo, m64), 0xd400d400u), s2, m2),
                              fma_f16(add_f16(and_or<0x000f000fu>(hi, m1024), 0xe400e400u), s2, m2),
                              fma_f16(add_f16(and_or<0x00f000f0u>(hi, m64), 0xd400d400u), s2, m2));
             }
           }
-          block -= kBlocks;
-          __syncwarp();
-          if (lane == 0) bar_arrive(&q4.code_empty[kv][in.slot]);
-          in.step(tp.n_code_v);
         }
         fence_async_smem();
         __syncwarp();
