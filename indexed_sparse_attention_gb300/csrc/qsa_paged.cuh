@@ -89,6 +89,7 @@ struct PagedRowsParams {
   int64_t q_row_stride, q_head_stride;                  // elements
   void* q_out;               // [n_rows, Hq, D]
   int32_t n_q_heads;
+  int32_t rows;              // of a CTA
 };
 struct PagedReadParams {
   PagedAppendParams a;       // k_new, v_new: not used

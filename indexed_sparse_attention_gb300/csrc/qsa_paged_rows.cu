@@ -2,9 +2,10 @@
 // caches, and rows back out of their pages (include/qsa.h,
 // qsa_paged_append_rotate, qsa_paged_append of 4-bit caches, qsa_paged_read).
 //
-// Writing: one CTA a row.  Its loads of Q, K and V are issued first, then the row's
-// sequence and position are found and the (cos, sin) of its pairs put into shared
-// memory once for all heads.  Rows that are stored as they are (f32, bf16) and Q go
+// Writing: one CTA a row, or up to four of a call of more rows than the GPU has places
+// for.  Loads of Q, K and V are issued first, then a warp a row finds its sequence,
+// position and page, and the (cos, sin) of its pairs go to shared memory once for all
+// heads.  Rows that are stored as they are (f32, bf16) and Q go
 // in jobs of the two 16-byte pieces that a rotation joins; a row that is quantized
 // is a warp's, D / 32 channels a lane, its pairs exchanged by shuffles.  K is
 // rounded to the rows' type before it is stored or quantized, so the cache holds
@@ -30,6 +31,7 @@ using namespace paged;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMaxRows = 4;   // of a CTA that writes
 __device__ int g_bad_pages;
 
 // D / 32 consecutive values of a row of bf16 from lane * (D / 32) on.
@@ -160,6 +162,23 @@ __device__ __forceinline__ void store_q4(const PagedAppendParams& p, const uint3
   }
 }
 
+// The sequence of row r, by one warp: how many ranges end at or before it.
+__device__ __forceinline__ int warp_sequence(const PagedAppendParams& a, int r, int lane) {
+  int n = 0;
+  for (int i0 = 0; i0 < a.n_seqs; i0 += 256) {   // eight loads a lane in flight
+    int mine = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = i0 + 32 * k + lane;
+      mine += i < a.n_seqs && __ldcg(a.row_start + i + 1) <= r;
+    }
+    const int sum = __reduce_add_sync(0xffffffffu, mine);
+    n += sum;
+    if (sum < 256) break;
+  }
+  return n;
+}
+
 // STATE: how the cache holds K and V.  D: head_dim.
 template <int STATE, int D>
 __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const __grid_constant__ PagedRowsParams p) {
@@ -167,77 +186,111 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const __grid_const
   constexpr int ES = STATE == QSA_F32 ? 4 : 2;          // of the rows
   constexpr int J = D * ES / 32;                        // jobs of a head
   const PagedAppendParams& a = p.a;
-  __shared__ __align__(16) float2 cs[QSA_MAX_ROPE_PAIRS];
+  __shared__ __align__(16) float2 cs[kMaxRows][QSA_MAX_ROPE_PAIRS];
+  __shared__ int64_t page_s[kMaxRows];                  // -1: no page, -2: nobody's row
+  __shared__ int pos_s[kMaxRows];
   grid_dependency_sync();
   const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int r = (int)blockIdx.x;
+  const int r0 = (int)blockIdx.x * p.rows, rows = min(p.rows, a.n_rows - r0);
   const int q_heads = p.q ? p.n_q_heads : 0;
-  // Job i of the row: Q's heads, then (rows stored as they are) K's and V's.
-  const int jobs = (q_heads + (QUANT ? 0 : 2 * a.n_kv_heads)) * J;
-  auto source = [&](int hh) {
+  // Job i of the rows: Q's heads of a row, then (rows stored as they are) K's and V's, then the next row.
+  const int jobs = (q_heads + (QUANT ? 0 : 2 * a.n_kv_heads)) * J, all = rows * jobs;
+  auto row_of_job = [&](int i) { return p.rows == 1 ? 0 : i / jobs; };
+  auto source = [&](int r, int hh) {
     if (hh < q_heads) return static_cast<const char*>(p.q) + (r * p.q_row_stride + hh * p.q_head_stride) * ES;
     const int hv = hh - q_heads, which = hv >= a.n_kv_heads, h = which ? hv - a.n_kv_heads : hv;
     return static_cast<const char*>(which ? a.v_new : a.k_new) + (r * a.row_stride + h * a.new_head_stride) * ES;
   };
-  constexpr int kAhead = 2;
+  constexpr int kAhead = 3;
   uint4 x0[kAhead], x1[kAhead];
   auto load = [&](int i0) {
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const int i = i0 + k * kThreads;
-      if (i >= jobs) continue;
-      const rope::Job b = rope::job_of<ES>(p.rope.rot_dim, p.rope.pairs, i % J);
-      const char* from = source(i / J);
+      if (i >= all) continue;
+      const int r = row_of_job(i), jj = i - r * jobs;
+      const rope::Job b = rope::job_of<ES>(p.rope.rot_dim, p.rope.pairs, jj % J);
+      const char* from = source(r0 + r, jj / J);
       x0[k] = *reinterpret_cast<const uint4*>(from + 16 * b.p0);
       x1[k] = *reinterpret_cast<const uint4*>(from + 16 * b.p1);
     }
   };
-  // Rows that are quantized: the first of the warp's.
+  // Rows that are quantized, a warp each: unit w of the rows is K or V of a head of a row.
+  const int units = QUANT ? rows * 2 * a.n_kv_heads : 0;
   uint32_t u[QUANT ? D / 64 : 1];
-  auto load_row = [&](int hv) {
+  auto load_row = [&](int w) {
+    const int r = w / (2 * a.n_kv_heads), hv = w - r * 2 * a.n_kv_heads;
     const int which = hv >= a.n_kv_heads, h = which ? hv - a.n_kv_heads : hv;
     if constexpr (QUANT)
-      load_lane<D>(static_cast<const __nv_bfloat16*>(which ? a.v_new : a.k_new) + r * a.row_stride + h * a.new_head_stride +
-                       lane * (D / 32),
+      load_lane<D>(static_cast<const __nv_bfloat16*>(which ? a.v_new : a.k_new) + (r0 + r) * a.row_stride +
+                       h * a.new_head_stride + lane * (D / 32),
                    u);
   };
-  if (QUANT && warp < 2 * a.n_kv_heads) load_row(warp);
+  if (warp < units) load_row(warp);
   load(tid);
-  int pos = 0;
-  int64_t page = 0, slot = 0;
-  const int seq = row_sequence<kThreads>(a, r, pos);
-  if (seq < 0) return;
-  const bool stored = row_page(a, seq, pos, page, slot, &g_bad_pages);
-  if (tid < p.rope.rot_dim / 2) cs[tid] = rope::turn(p.rope, tid, pos);
+  if (warp < rows) {   // the warp's row: its sequence, position and page
+    const int r = r0 + warp, seq = warp_sequence(a, r, lane);
+    int64_t page = -2;
+    int pos = 0;
+    if (seq < a.n_seqs) {
+      const int first = __ldcg(a.row_start + seq), end = __ldcg(a.row_start + seq + 1), len = __ldcg(a.lens + seq);
+      if (r >= first) {
+        pos = max(len, 0) - (min(end, a.n_rows) - r);
+        page = -1;
+        if (pos >= 0) {
+          const int64_t j = pos >> a.page_shift;
+          const int32_t id = j < a.table_ld ? __ldcg(a.table + seq * a.table_ld + j) : -1;
+          if ((uint32_t)id < (uint32_t)a.n_pages) page = id;
+          else if (lane == 0) atomicAdd(&g_bad_pages, 1);
+        }
+      }
+    }
+    if (lane == 0) {
+      page_s[warp] = page;
+      pos_s[warp] = pos;
+    }
+  }
   __syncthreads();
-  for (int i0 = tid; i0 < jobs; i0 += kAhead * kThreads) {
+  const int half = p.rope.rot_dim / 2;
+  for (int i = tid; i < rows * half; i += kThreads) {
+    const int r = i / half, k = i - r * half;
+    cs[r][k] = rope::turn(p.rope, k, pos_s[r]);
+  }
+  __syncthreads();
+  const int page_mask = (1 << a.page_shift) - 1;
+  for (int i0 = tid; i0 < all; i0 += kAhead * kThreads) {
     if (i0 != tid) load(i0);
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const int i = i0 + k * kThreads;
-      if (i >= jobs) continue;
-      const int hh = i / J, j = i % J;
+      if (i >= all) continue;
+      const int r = row_of_job(i), jj = i - r * jobs, hh = jj / J, j = jj % J;
+      const int64_t page = page_s[r];
+      if (page == -2) continue;
       const rope::Job b = rope::job_of<ES>(p.rope.rot_dim, p.rope.pairs, j);
       const int hv = hh - q_heads;
-      if (b.turns && hv < a.n_kv_heads) rope::rotate_job<ES>(x0[k], x1[k], p.rope.pairs, j, cs);
+      if (b.turns && hv < a.n_kv_heads) rope::rotate_job<ES>(x0[k], x1[k], p.rope.pairs, j, cs[r]);
       char* to;
       if (hv < 0) {
-        to = static_cast<char*>(p.q_out) + ((int64_t)r * q_heads + hh) * (D * ES);
+        to = static_cast<char*>(p.q_out) + ((int64_t)(r0 + r) * q_heads + hh) * (D * ES);
       } else {
-        if (!stored) continue;
+        if (page < 0) continue;
         const int which = hv >= a.n_kv_heads, h = which ? hv - a.n_kv_heads : hv;
-        to = static_cast<char*>(which ? a.v : a.k) + (page * a.page_stride + h * a.head_stride + slot * a.tok_stride) * ES;
+        to = static_cast<char*>(which ? a.v : a.k) +
+             (page * a.page_stride + h * a.head_stride + (pos_s[r] & page_mask) * a.tok_stride) * ES;
       }
       *reinterpret_cast<uint4*>(to + 16 * b.p0) = x0[k];
       *reinterpret_cast<uint4*>(to + 16 * b.p1) = x1[k];
     }
   }
   if constexpr (QUANT) {
-    if (!stored) return;
-    for (int hv = warp; hv < 2 * a.n_kv_heads; hv += kWarps) {
-      if (hv != warp) load_row(hv);
+    for (int w = warp; w < units; w += kWarps) {
+      if (w != warp) load_row(w);
+      const int r = w / (2 * a.n_kv_heads), hv = w - r * 2 * a.n_kv_heads;
+      const int64_t page = page_s[r], slot = pos_s[r] & page_mask;
+      if (page < 0) continue;
       const int which = hv >= a.n_kv_heads, h = which ? hv - a.n_kv_heads : hv;
-      if (which == 0 && p.rope.rot_dim > 0) rotate_lane<D>(u, p.rope, cs, lane);
+      if (which == 0 && half > 0) rotate_lane<D>(u, p.rope, cs[r], lane);
       const int64_t at = page * a.page_stride + h * a.head_stride + slot * a.tok_stride;
       const int64_t record = page * a.s_page_stride + h * a.s_head_stride + slot * a.s_tok_stride;
       if constexpr (STATE == QSA_Q4_1) store_q4<D>(a, u, which, at / 2, record, lane);
@@ -248,8 +301,9 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const __grid_const
 
 // ------------------------------------------------------------------ reading
 // A warp takes rows_warp rows: lane i looks up row i's page, so their chains of
-// dependent reads (range, length, table) run side by side; then K and V of every head
-// of a row at a time, D / 32 values a lane.
+// dependent reads (range, length, table) run side by side; then K and V of their heads,
+// 16 bytes of codes a lane (4-bit: 32 values, so that several rows are under way), or a
+// row over the warp.
 template <typename OUT>
 __device__ __forceinline__ void put4(OUT* to, float a, float b, float c, float d) {
   if constexpr (sizeof(OUT) == 4) {
@@ -287,53 +341,80 @@ __global__ void __launch_bounds__(kThreads) paged_read_kernel(const __grid_const
       }
     }
   }
-  const int n = min(p.rows_warp, a.n_rows - r0), all = 2 * a.n_kv_heads;
+  // Units: K or V of a head of a row.  LU lanes share one, 32 / LU at a time.
+  constexpr int LU = STATE == QSA_Q4_1 ? D / 32 : 32, UW = 32 / LU;
+  const int n = min(p.rows_warp, a.n_rows - r0), each = 2 * a.n_kv_heads, all = n * each;
+  const int sub = lane / LU, li = lane % LU;
+  constexpr int kAhead = 2;   // units of a lane in flight
 #pragma unroll 1
-  for (int i = 0; i < n; ++i) {
-    const int64_t pg = __shfl_sync(0xffffffffu, page, i), sl = __shfl_sync(0xffffffffu, slot, i);
-    if (pg < 0) continue;
-#pragma unroll 4
-    for (int hv = 0; hv < all; ++hv) {
+  for (int u0 = 0; u0 < all; u0 += kAhead * UW) {
+    constexpr int ES = STATE == QSA_F32 ? 4 : STATE == QSA_BF16 ? 2 : 1;
+    constexpr int NW = STATE == QSA_Q4_1 ? 1 + D / 128 : (D * ES / 32 + 15) / 16;   // 16-byte pieces of a lane
+    uint4 w[kAhead][NW];
+    float sc[kAhead];
+    OUT* to[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int u = u0 + k * UW + sub, i = u / each, hv = u - i * each;
+      const int64_t pg = __shfl_sync(0xffffffffu, page, i & 31), sl = __shfl_sync(0xffffffffu, slot, i & 31);
+      to[k] = nullptr;
+      if (u >= all || pg < 0) continue;
       const int which = hv >= a.n_kv_heads, h = which ? hv - a.n_kv_heads : hv;
       const int64_t at = pg * a.page_stride + h * a.head_stride + sl * a.tok_stride;
       const int64_t record = pg * a.s_page_stride + h * a.s_head_stride + sl * a.s_tok_stride;
       const char* from = static_cast<const char*>(which ? a.v : a.k);
-      OUT* to = static_cast<OUT*>(which ? p.v_out : p.k_out) + ((int64_t)(r0 + i) * a.n_kv_heads + h) * D;
+      to[k] = static_cast<OUT*>(which ? p.v_out : p.k_out) + ((int64_t)(r0 + i) * a.n_kv_heads + h) * D;
       if constexpr (STATE == QSA_Q4_1) {
-        constexpr int G = D / 32;
-        if (lane >= D / 8) continue;   // a lane a 32-bit word: units n of blocks g and g + 1
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(from + at / 2) + lane);
-        const int unit = 2 * lane, nn = unit / G, g = unit % G;
-        const uint2 rec = __ldg(reinterpret_cast<const uint2*>(static_cast<const char*>(a.kv_scale) + record * (D / 4) +
-                                                               which * (G * 4) + g * 4));
+        w[k][0] = __ldcs(reinterpret_cast<const uint4*>(from + at / 2) + li);
+        const uint4* rec = reinterpret_cast<const uint4*>(static_cast<const char*>(a.kv_scale) + record * (D / 4) + which * (D / 8));
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const uint32_t word = b ? rec.y : rec.x;
+        for (int x = 0; x < D / 128; ++x) w[k][1 + x] = __ldg(rec + x);
+      } else if constexpr (D * ES / 32 >= 16) {
+#pragma unroll
+        for (int x = 0; x < NW; ++x) w[k][x] = __ldcs(reinterpret_cast<const uint4*>(from + at * ES) + 32 * x + lane);
+      } else if constexpr (D * ES / 32 == 8) {
+        const uint2 v = __ldcs(reinterpret_cast<const uint2*>(from + at * ES) + lane);
+        w[k][0] = make_uint4(v.x, v.y, 0u, 0u);
+      } else {
+        w[k][0].x = __ldcs(reinterpret_cast<const uint32_t*>(from + at * ES) + lane);
+      }
+      if constexpr (STATE == QSA_FP8_E4M3) sc[k] = __half2float(__ldg(static_cast<const __half*>(a.kv_scale) + 2 * record + which));
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (to[k] == nullptr) continue;
+      if constexpr (STATE == QSA_Q4_1) {
+        // The lane's 16 bytes: unit li of all eight blocks (D = 256), or units 2 li and 2 li + 1 of all four.
+        constexpr int G = D / 32;
+        const uint32_t c4[4] = {w[k][0].x, w[k][0].y, w[k][0].z, w[k][0].w};
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const int g = x % G, unit = D == 256 ? li : 2 * li + x / G;
+          const uint4 r4 = w[k][1 + g / 4];
+          const uint32_t word = (g & 3) == 0 ? r4.x : (g & 3) == 1 ? r4.y : (g & 3) == 2 ? r4.z : r4.w;
           const __half2 sm = *reinterpret_cast<const __half2*>(&word);
           const float s = __low2float(sm), m = __high2float(sm);
-          const uint32_t c = w >> (16 * b);
-          put4(to + 32 * (g + b) + 4 * nn, fmaf((float)(c & 15u), s, m), fmaf((float)((c >> 4) & 15u), s, m),
+          const uint32_t c = c4[x / 2] >> (16 * (x & 1));
+          put4(to[k] + 32 * g + 4 * unit, fmaf((float)(c & 15u), s, m), fmaf((float)((c >> 4) & 15u), s, m),
                fmaf((float)((c >> 8) & 15u), s, m), fmaf((float)((c >> 12) & 15u), s, m));
         }
-      } else {
-        constexpr int ES = STATE == QSA_F32 ? 4 : STATE == QSA_BF16 ? 2 : 1;
+      } else if constexpr (STATE == QSA_F32) {
 #pragma unroll
-        for (int c0 = 0; c0 < D; c0 += 128) {
-          const char* src = from + (at + c0 + lane * 4) * ES;
-          float x[4];
-          if constexpr (STATE == QSA_F32) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(src));
-            x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-          } else if constexpr (STATE == QSA_BF16) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
-            x[0] = bf16_lo(v.x), x[1] = bf16_hi(v.x), x[2] = bf16_lo(v.y), x[3] = bf16_hi(v.y);
-          } else {
-            const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(src));
-            const float s = __half2float(__ldg(static_cast<const __half*>(a.kv_scale) + 2 * record + which));
-            const uint32_t b0 = attn::e4m3x2_to_bf16x2(v & 0xffffu), b1 = attn::e4m3x2_to_bf16x2(v >> 16);
-            x[0] = bf16_lo(b0) * s, x[1] = bf16_hi(b0) * s, x[2] = bf16_lo(b1) * s, x[3] = bf16_hi(b1) * s;
-          }
-          put4(to + c0 + lane * 4, x[0], x[1], x[2], x[3]);
+        for (int x = 0; x < NW; ++x)
+          put4(to[k] + 128 * x + 4 * lane, __uint_as_float(w[k][x].x), __uint_as_float(w[k][x].y), __uint_as_float(w[k][x].z),
+               __uint_as_float(w[k][x].w));
+      } else if constexpr (STATE == QSA_BF16) {
+        constexpr int PER = D / 32;
+        put4(to[k] + PER * lane, bf16_lo(w[k][0].x), bf16_hi(w[k][0].x), bf16_lo(w[k][0].y), bf16_hi(w[k][0].y));
+        if constexpr (PER == 8)
+          put4(to[k] + PER * lane + 4, bf16_lo(w[k][0].z), bf16_hi(w[k][0].z), bf16_lo(w[k][0].w), bf16_hi(w[k][0].w));
+      } else {
+        constexpr int PER = D / 32;
+#pragma unroll
+        for (int x = 0; x < PER / 4; ++x) {
+          const uint32_t v = x ? w[k][0].y : w[k][0].x;
+          const uint32_t b0 = attn::e4m3x2_to_bf16x2(v & 0xffffu), b1 = attn::e4m3x2_to_bf16x2(v >> 16);
+          put4(to[k] + PER * lane + 4 * x, bf16_lo(b0) * sc[k], bf16_hi(b0) * sc[k], bf16_lo(b1) * sc[k], bf16_hi(b1) * sc[k]);
         }
       }
     }
@@ -341,8 +422,11 @@ __global__ void __launch_bounds__(kThreads) paged_read_kernel(const __grid_const
 }
 
 template <int STATE>
-cudaError_t launch_rows(const PagedRowsParams& p, cudaStream_t st) {
-  const dim3 grid((unsigned)p.a.n_rows), block(kThreads);
+cudaError_t launch_rows(PagedRowsParams p, cudaStream_t st) {
+  // As many rows a CTA as leave eight CTAs for every SM.
+  p.rows = 1;
+  while (p.rows < kMaxRows && p.a.n_rows > 8 * device_sm_count() * p.rows) p.rows *= 2;
+  const dim3 grid((unsigned)((p.a.n_rows + p.rows - 1) / p.rows)), block(kThreads);
   return p.a.head_dim == 256 ? launch_kernel(paged_rows_kernel<STATE, 256>, grid, block, 0, st, 0u, p)
                              : launch_kernel(paged_rows_kernel<STATE, 128>, grid, block, 0, st, 0u, p);
 }

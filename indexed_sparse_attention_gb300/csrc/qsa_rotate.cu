@@ -1,9 +1,10 @@
 // Rotary positions (include/qsa.h): the host functions that make a rotation, and
 // the rotation of rows by themselves.
 //
-// One CTA takes a row at a time: its (cos, sin) by pair go to shared memory once and
-// serve all heads; a thread then takes jobs of two 16-byte pieces, the two that a
-// rotation joins, so that nothing is exchanged.  Each value is read and written
+// One CTA takes one row, or up to four of a call that has more rows than the GPU has
+// places for CTAs: their (cos, sin) by pair go to shared memory once and serve all
+// heads; a thread then takes jobs of two 16-byte pieces, the two that a rotation joins,
+// so that nothing is exchanged, four of them in flight.  Each value is read and written
 // once; the bound is HBM for a prompt's rows and the launch with a chain of three
 // dependent steps (position, angles, rows) for a step's.
 #include <math.h>
@@ -17,7 +18,7 @@ namespace qsa {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kMaxRows = 4;
 
 struct RotateParams {
   qsa_rope rope;
@@ -25,57 +26,73 @@ struct RotateParams {
   const void* x;
   void* y;
   int64_t x_row, x_head, y_row, y_head;   // bytes
-  int32_t n_rows, jobs_head;              // jobs of a head
-  int32_t jobs;                           // of a row
-  uint32_t magic;                         // ceil(2^32 / jobs_head); 1 job: not used
+  int32_t n_rows, rows;                   // rows: of a CTA
+  int32_t jobs_head, jobs;                // jobs of a head, of a row
+  uint32_t magic_head, magic_row;         // ceil(2^32 / jobs_head), ceil(2^32 / jobs); 1: not used
   int32_t in_place;
 };
 
+// a / b by its magic number (a < 2^25, b < 2^24: the product's error stays below 1).
+__device__ __forceinline__ int divide(int a, int b, uint32_t magic) {
+  if (b == 1) return a;
+  int q = (int)__umulhi((uint32_t)a, magic);
+  if (q * b > a) --q;
+  return q;
+}
+
 template <int ES>
-__global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant__ RotateParams p) {
-  __shared__ __align__(16) float2 cs[QSA_MAX_ROPE_PAIRS];
+__global__ void __launch_bounds__(kThreads, 4) rotate_kernel(const __grid_constant__ RotateParams p) {
+  __shared__ __align__(16) float2 cs[kMaxRows][QSA_MAX_ROPE_PAIRS];
   grid_dependency_sync();
   const int tid = (int)threadIdx.x;
-  for (int r = (int)blockIdx.x; r < p.n_rows; r += (int)gridDim.x) {
-    const char* xr = static_cast<const char*>(p.x) + r * p.x_row;
-    char* yr = static_cast<char*>(p.y) + r * p.y_row;
-    constexpr int kAhead = 2;   // jobs of a thread in flight
-    uint4 x0[kAhead], x1[kAhead];
-    int64_t at0[kAhead], at1[kAhead];
-    auto load = [&](int i0) {
+  const int r0 = (int)blockIdx.x * p.rows, rows = min(p.rows, p.n_rows - r0), all = rows * p.jobs;
+  constexpr int kAhead = 4;   // jobs of a thread in flight
+  uint4 x0[kAhead], x1[kAhead];
+  struct Place {
+    int r, h, j;
+  };
+  auto place = [&](int i) {
+    Place a;
+    a.r = divide(i, p.jobs, p.magic_row);
+    const int k = i - a.r * p.jobs;
+    a.h = divide(k, p.jobs_head, p.magic_head);
+    a.j = k - a.h * p.jobs_head;
+    return a;
+  };
+  auto load = [&](int i0) {
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int i = i0 + k * kThreads;
-        if (i >= p.jobs) continue;
-        const int h = p.jobs_head == 1 ? i : (int)__umulhi((uint32_t)i, p.magic), j = i - h * p.jobs_head;
-        const rope::Job b = rope::job_of<ES>(p.rope.rot_dim, p.rope.pairs, j);
-        if (p.in_place && !b.turns) continue;
-        const char* from = xr + h * p.x_head;
-        x0[k] = *reinterpret_cast<const uint4*>(from + 16 * b.p0);
-        x1[k] = *reinterpret_cast<const uint4*>(from + 16 * b.p1);
-        at0[k] = h * p.y_head + 16 * b.p0;
-        at1[k] = h * p.y_head + 16 * b.p1;
-      }
-    };
-    load(tid);
-    const int pos = __ldg(p.positions + r);
-    if (tid < p.rope.rot_dim / 2) cs[tid] = rope::turn(p.rope, tid, pos);
-    __syncthreads();
-    for (int i0 = tid; i0 < p.jobs; i0 += kAhead * kThreads) {
-      if (i0 != tid) load(i0);
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int i = i0 + k * kThreads;
-        if (i >= p.jobs) continue;
-        const int h = p.jobs_head == 1 ? i : (int)__umulhi((uint32_t)i, p.magic), j = i - h * p.jobs_head;
-        const rope::Job b = rope::job_of<ES>(p.rope.rot_dim, p.rope.pairs, j);
-        if (p.in_place && !b.turns) continue;
-        if (b.turns) rope::rotate_job<ES>(x0[k], x1[k], p.rope.pairs, j, cs);
-        *reinterpret_cast<uint4*>(yr + at0[k]) = x0[k];
-        *reinterpret_cast<uint4*>(yr + at1[k]) = x1[k];
-      }
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = i0 + k * kThreads;
+      if (i >= all) continue;
+      const Place a = place(i);
+      const rope::Job b = rope::job_of<ES>(p.rope.rot_dim, p.rope.pairs, a.j);
+      if (p.in_place && !b.turns) continue;
+      const char* from = static_cast<const char*>(p.x) + (r0 + a.r) * p.x_row + a.h * p.x_head;
+      x0[k] = __ldcs(reinterpret_cast<const uint4*>(from) + b.p0);
+      x1[k] = __ldcs(reinterpret_cast<const uint4*>(from) + b.p1);
     }
-    __syncthreads();   // cs is the next row's
+  };
+  load(tid);
+  const int half = p.rope.rot_dim / 2;
+  for (int i = tid; i < rows * half; i += kThreads) {
+    const int r = i / half, k = i - r * half;
+    cs[r][k] = rope::turn(p.rope, k, __ldg(p.positions + r0 + r));
+  }
+  __syncthreads();
+  for (int i0 = tid; i0 < all; i0 += kAhead * kThreads) {
+    if (i0 != tid) load(i0);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = i0 + k * kThreads;
+      if (i >= all) continue;
+      const Place a = place(i);
+      const rope::Job b = rope::job_of<ES>(p.rope.rot_dim, p.rope.pairs, a.j);
+      if (p.in_place && !b.turns) continue;
+      if (b.turns) rope::rotate_job<ES>(x0[k], x1[k], p.rope.pairs, a.j, cs[a.r]);
+      char* to = static_cast<char*>(p.y) + (r0 + a.r) * p.y_row + a.h * p.y_head;
+      __stcs(reinterpret_cast<uint4*>(to) + b.p0, x0[k]);
+      __stcs(reinterpret_cast<uint4*>(to) + b.p1, x1[k]);
+    }
   }
 }
 
@@ -193,9 +210,14 @@ QSA_API qsa_status qsa_rotate(const qsa_rope* rope, const int32_t* positions, in
   p.n_rows = n_rows;
   p.jobs_head = (int32_t)(head_dim * es / 32);
   p.jobs = n_heads * p.jobs_head;
-  p.magic = p.jobs_head == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32) + p.jobs_head - 1) / p.jobs_head);
+  auto magic = [](int n) { return n == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32) + n - 1) / n); };
+  p.magic_head = magic(p.jobs_head);
+  p.magic_row = magic(p.jobs);
   p.in_place = in_place ? 1 : 0;
-  const dim3 grid((unsigned)std::min<int64_t>(n_rows, (int64_t)1 << 30)), block(kThreads);
+  // As many rows a CTA as leave eight CTAs for every SM, and no more than its threads have work for.
+  p.rows = 1;
+  while (p.rows < kMaxRows && n_rows > 8 * device_sm_count() * p.rows && p.rows * p.jobs < 4 * kThreads) p.rows *= 2;
+  const dim3 grid((unsigned)((n_rows + p.rows - 1) / p.rows)), block(kThreads);
   const cudaError_t e = dtype == QSA_F32 ? launch_kernel(rotate_kernel<4>, grid, block, 0, as_stream(stream), 0u, p)
                                          : launch_kernel(rotate_kernel<2>, grid, block, 0, as_stream(stream), 0u, p);
   return e == cudaSuccess ? ok() : cuda_fail(e, fn);
