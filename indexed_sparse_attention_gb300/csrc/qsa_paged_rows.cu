@@ -56,7 +56,7 @@ __device__ __forceinline__ void rotate_lane(uint32_t (&u)[D / 64], const qsa_rop
   if (r.pairs) {
 #pragma unroll
     for (int k = 0; k < D / 64; ++k) {
-      const float2 t = cs[turns ? c0 / 2 + k : 0];
+      const float2 t = cs[rope::cs_at<2>(r.rot_dim, turns ? c0 / 2 + k : 0)];
       const float a = bf16_lo(u[k]), b = bf16_hi(u[k]);
       const __nv_bfloat162 w = __floats2bfloat162_rn(rope::low_of(a, b, t), rope::high_of(a, b, t));
       y[k] = *reinterpret_cast<const uint32_t*>(&w);
@@ -68,7 +68,7 @@ __device__ __forceinline__ void rotate_lane(uint32_t (&u)[D / 64], const qsa_rop
 #pragma unroll
     for (int k = 0; k < D / 64; ++k) {
       const uint32_t other = __shfl_sync(0xffffffffu, u[k], from);
-      const float2 t0 = cs[i0 + 2 * k], t1 = cs[i0 + 2 * k + 1];
+      const float2 t0 = cs[rope::cs_at<2>(r.rot_dim, i0 + 2 * k)], t1 = cs[rope::cs_at<2>(r.rot_dim, i0 + 2 * k + 1)];
       const float m0 = bf16_lo(u[k]), m1 = bf16_hi(u[k]), o0 = bf16_lo(other), o1 = bf16_hi(other);
       const __nv_bfloat162 w = upper ? __floats2bfloat162_rn(rope::high_of(o0, m0, t0), rope::high_of(o1, m1, t1))
                                      : __floats2bfloat162_rn(rope::low_of(m0, o0, t0), rope::low_of(m1, o1, t1));
@@ -162,26 +162,46 @@ __device__ __forceinline__ void store_q4(const PagedAppendParams& p, const uint3
   }
 }
 
-// The sequence of row r, by one warp: how many ranges end at or before it.
-__device__ __forceinline__ int warp_sequence(const PagedAppendParams& a, int r, int lane) {
-  int n = 0;
-  for (int i0 = 0; i0 < a.n_seqs; i0 += 256) {   // eight loads a lane in flight
-    int mine = 0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int i = i0 + 32 * k + lane;
-      mine += i < a.n_seqs && __ldcg(a.row_start + i + 1) <= r;
-    }
-    const int sum = __reduce_add_sync(0xffffffffu, mine);
-    n += sum;
-    if (sum < 256) break;
+// The sequence of row r and its position, by one warp (-1: nobody's).  The first 32
+// sequences' ranges and lengths are read at once; more are counted 256 at a time.
+__device__ __forceinline__ int warp_sequence(const PagedAppendParams& a, int r, int lane, int& pos) {
+  int first = 0, end = 0, len = 0;
+  if (lane < a.n_seqs) {
+    first = __ldcg(a.row_start + lane);
+    end = __ldcg(a.row_start + lane + 1);
+    len = __ldcg(a.lens + lane);
   }
-  return n;
+  int seq = __popc(__ballot_sync(0xffffffffu, lane < a.n_seqs && end <= r));   // ranges that end at or before it
+  if (seq < 32) {
+    first = __shfl_sync(0xffffffffu, first, seq);
+    end = __shfl_sync(0xffffffffu, end, seq);
+    len = __shfl_sync(0xffffffffu, len, seq);
+  } else {
+    for (int i0 = 32; i0 < a.n_seqs; i0 += 256) {
+      int mine = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = i0 + 32 * k + lane;
+        mine += i < a.n_seqs && __ldcg(a.row_start + i + 1) <= r;
+      }
+      const int sum = __reduce_add_sync(0xffffffffu, mine);
+      seq += sum;
+      if (sum < 256) break;
+    }
+    if (seq < a.n_seqs) {
+      first = __ldcg(a.row_start + seq);
+      end = __ldcg(a.row_start + seq + 1);
+      len = __ldcg(a.lens + seq);
+    }
+  }
+  if (seq >= a.n_seqs || r < first) return -1;
+  pos = max(len, 0) - (min(end, a.n_rows) - r);
+  return seq;
 }
 
 // STATE: how the cache holds K and V.  D: head_dim.
 template <int STATE, int D>
-__global__ void __launch_bounds__(kThreads) paged_rows_kernel(const __grid_constant__ PagedRowsParams p) {
+__global__ void __launch_bounds__(kThreads, 4) paged_rows_kernel(const __grid_constant__ PagedRowsParams p) {
   constexpr bool QUANT = STATE == QSA_FP8_E4M3 || STATE == QSA_Q4_1;
   constexpr int ES = STATE == QSA_F32 ? 4 : 2;          // of the rows
   constexpr int J = D * ES / 32;                        // jobs of a head
@@ -228,33 +248,31 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const __grid_const
   };
   if (warp < units) load_row(warp);
   load(tid);
-  if (warp < rows) {   // the warp's row: its sequence, position and page
-    const int r = r0 + warp, seq = warp_sequence(a, r, lane);
-    int64_t page = -2;
+  // A warp a row: its sequence and position; its page arrives while the angles are computed.
+  int64_t page = -2;
+  int32_t id = 0;
+  if (warp < rows) {
     int pos = 0;
-    if (seq < a.n_seqs) {
-      const int first = __ldcg(a.row_start + seq), end = __ldcg(a.row_start + seq + 1), len = __ldcg(a.lens + seq);
-      if (r >= first) {
-        pos = max(len, 0) - (min(end, a.n_rows) - r);
-        page = -1;
-        if (pos >= 0) {
-          const int64_t j = pos >> a.page_shift;
-          const int32_t id = j < a.table_ld ? __ldcg(a.table + seq * a.table_ld + j) : -1;
-          if ((uint32_t)id < (uint32_t)a.n_pages) page = id;
-          else if (lane == 0) atomicAdd(&g_bad_pages, 1);
-        }
-      }
+    const int seq = warp_sequence(a, r0 + warp, lane, pos);
+    if (seq >= 0) {
+      const int64_t j = pos >> a.page_shift;
+      page = pos >= 0 ? 0 : -1;
+      id = pos >= 0 && j < a.table_ld ? __ldcg(a.table + seq * a.table_ld + j) : -1;
     }
-    if (lane == 0) {
-      page_s[warp] = page;
-      pos_s[warp] = pos;
-    }
+    if (lane == 0) pos_s[warp] = pos;
   }
   __syncthreads();
   const int half = p.rope.rot_dim / 2;
   for (int i = tid; i < rows * half; i += kThreads) {
     const int r = i / half, k = i - r * half;
-    cs[r][k] = rope::turn(p.rope, k, pos_s[r]);
+    cs[r][rope::cs_at<ES>(p.rope.rot_dim, k)] = rope::turn(p.rope, k, pos_s[r]);
+  }
+  if (warp < rows && lane == 0) {
+    if (page == 0) {
+      page = (uint32_t)id < (uint32_t)a.n_pages ? id : -1;
+      if (page < 0) atomicAdd(&g_bad_pages, 1);
+    }
+    page_s[warp] = page;
   }
   __syncthreads();
   const int page_mask = (1 << a.page_shift) - 1;
@@ -269,7 +287,7 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const __grid_const
       if (page == -2) continue;
       const rope::Job b = rope::job_of<ES>(p.rope.rot_dim, p.rope.pairs, j);
       const int hv = hh - q_heads;
-      if (b.turns && hv < a.n_kv_heads) rope::rotate_job<ES>(x0[k], x1[k], p.rope.pairs, j, cs[r]);
+      if (b.turns && hv < a.n_kv_heads) rope::rotate_job<ES>(x0[k], x1[k], p.rope.rot_dim, p.rope.pairs, j, cs[r]);
       char* to;
       if (hv < 0) {
         to = static_cast<char*>(p.q_out) + ((int64_t)(r0 + r) * q_heads + hh) * (D * ES);

@@ -80,21 +80,23 @@ __device__ __forceinline__ Job job_of(int rot_dim, int pairs, int j) {
   b.p1 = b.turns && !pairs ? j + n : 2 * j + 1;
   return b;
 }
-// Rotates job j's pieces in place; cs: the row's (cos, sin) by pair.
+// A row's (cos, sin) in shared memory: of job j's pairs E j .. E j + E - 1, pair e is at e
+// times the jobs plus j, so that a warp's loads (a job a lane) are consecutive.
 template <int ES>
-__device__ __forceinline__ void rotate_job(uint4& x0, uint4& x1, int pairs, int j, const float2* cs) {
+__device__ __forceinline__ int cs_at(int rot_dim, int pair) {
+  constexpr int E = 16 / ES;
+  return pair % E * (rot_dim / (2 * E)) + pair / E;
+}
+// Rotates job j's pieces in place; cs: the row's (cos, sin).
+template <int ES>
+__device__ __forceinline__ void rotate_job(uint4& x0, uint4& x1, int rot_dim, int pairs, int j, const float2* cs) {
   constexpr int E = 16 / ES;
   float a[E], b[E], c[E], d[E];
   open<ES>(x0, a);
   open<ES>(x1, b);
-  const float4* at = reinterpret_cast<const float4*>(cs + E * j);
   float2 t[E];
 #pragma unroll
-  for (int e = 0; e < E; e += 2) {
-    const float4 two = at[e / 2];
-    t[e] = make_float2(two.x, two.y);
-    t[e + 1] = make_float2(two.z, two.w);
-  }
+  for (int e = 0; e < E; ++e) t[e] = cs[e * (rot_dim / (2 * E)) + j];
   if (pairs) {
 #pragma unroll
     for (int e = 0; e < E / 2; ++e) {

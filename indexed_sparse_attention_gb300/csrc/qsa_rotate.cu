@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kThreads, 4) rotate_kernel(const __grid_consta
   const int half = p.rope.rot_dim / 2;
   for (int i = tid; i < rows * half; i += kThreads) {
     const int r = i / half, k = i - r * half;
-    cs[r][k] = rope::turn(p.rope, k, __ldg(p.positions + r0 + r));
+    cs[r][rope::cs_at<ES>(p.rope.rot_dim, k)] = rope::turn(p.rope, k, __ldg(p.positions + r0 + r));
   }
   __syncthreads();
   for (int i0 = tid; i0 < all; i0 += kAhead * kThreads) {
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, 4) rotate_kernel(const __grid_consta
       const Place a = place(i);
       const rope::Job b = rope::job_of<ES>(p.rope.rot_dim, p.rope.pairs, a.j);
       if (p.in_place && !b.turns) continue;
-      if (b.turns) rope::rotate_job<ES>(x0[k], x1[k], p.rope.pairs, a.j, cs[a.r]);
+      if (b.turns) rope::rotate_job<ES>(x0[k], x1[k], p.rope.rot_dim, p.rope.pairs, a.j, cs[a.r]);
       char* to = static_cast<char*>(p.y) + (r0 + a.r) * p.y_row + a.h * p.y_head;
       __stcs(reinterpret_cast<uint4*>(to) + b.p0, x0[k]);
       __stcs(reinterpret_cast<uint4*>(to) + b.p1, x1[k]);
