@@ -8,6 +8,8 @@ from . import _check, lib
 #: The handle of a device's current stream; torch.cuda.current_stream builds a Stream object around it (2 us a call).
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+#: The current device's number, without torch.cuda.current_device's look at whether CUDA is up (a tensor is there).
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _raw_stream(stream, device) -> int:
@@ -22,7 +24,7 @@ def _call(name: str, device, stream, *args):
     if device.type != "cuda":
         raise ValueError(f"{name}: the tensors are on {device}, not on a GPU")
     fn = getattr(lib(), name)
-    if device.index == torch.cuda.current_device():
+    if device.index == _current_device():
         status = fn(*args, _raw_stream(stream, device))
     else:
         with torch.cuda.device(device):

@@ -125,6 +125,7 @@ class PagedCache:
         self._row_cfg_ref = ctypes.byref(self._row_cfg)
         self._read_cfg = [ctypes.byref(self.config(out_dtype=t)) for t in (torch.float32, torch.bfloat16)]
         self._rows_cfgs = {}
+        self._last_call = None, None
 
     def _rows_cfg(self, n_q_heads: int):
         if n_q_heads not in self._rows_cfgs:
@@ -151,7 +152,15 @@ class PagedCache:
                n_splits: int = 0) -> AttnConfig:
         hq = self.n_kv_heads if n_q_heads is None else int(n_q_heads)
         return AttnConfig(hq, self.n_kv_heads, self.head_dim, F32 if self.kv_dtype == F32 else BF16, self.kv_dtype,
-                          _dtype_code(torch.empty(0, dtype=out_dtype)), float(scale), int(n_splits))
+                          F32 if out_dtype is torch.float32 else BF16 if out_dtype is torch.bfloat16
+                          else _dtype_code(torch.empty(0, dtype=out_dtype)), float(scale), int(n_splits))
+
+    def _call_config(self, n_q_heads: int, out_dtype, scale: float, n_splits: int) -> AttnConfig:
+        """config() of the last call, while calls ask for the same."""
+        key = (n_q_heads, out_dtype, scale, n_splits)
+        if self._last_call[0] != key:
+            self._last_call = key, self.config(n_q_heads, out_dtype, scale, n_splits)
+        return self._last_call[1]
 
 
 class PagedBatch:
@@ -193,7 +202,8 @@ def _check_batch(cache: PagedCache, batch: PagedBatch):
 
 
 def _check_queries(cache: PagedCache, batch: PagedBatch, q: torch.Tensor):
-    _check_rows("q", q, (batch.n_rows, q.shape[1] if q.dim() == 3 else 0, cache.head_dim), cache.row_dtype, cache.device)
+    shape = q.shape
+    _check_rows("q", q, (batch.n_rows, shape[1] if len(shape) == 3 else 0, cache.head_dim), cache.row_dtype, cache.device)
     if not q.is_contiguous():
         raise ValueError("q must be contiguous")
     _check_batch(cache, batch)
@@ -222,12 +232,13 @@ def paged_attn(cache: PagedCache, batch: PagedBatch, q: torch.Tensor, out: torch
     every token up to the row's own, or with window >= 1 the last `window` of
     them and the first n_sinks tokens."""
     _check_queries(cache, batch, q)
-    _check_rows("out", out, q.shape, out.dtype, cache.device)
+    shape = q.shape
+    _check_rows("out", out, shape, out.dtype, cache.device)
     if lse is not None:
-        _check_rows("lse", lse, q.shape[:2], torch.float32, cache.device)
+        _check_rows("lse", lse, shape[:2], torch.float32, cache.device)
     if not (out.is_contiguous() and (lse is None or lse.is_contiguous())):
         raise ValueError("out and lse must be contiguous")
-    own = cache.config(q.shape[1], out.dtype, scale, n_splits)
+    own = cache._call_config(shape[1], out.dtype, scale, n_splits)
     if cfg is None:
         cfg = own
     elif any(getattr(cfg, f) != getattr(own, f) for f in _CALL_FIELDS):
@@ -264,16 +275,18 @@ def paged_append(cache: PagedCache, batch: PagedBatch, k_new: torch.Tensor, v_ne
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     if q is not None:
-        if q.dim() != 3 or q.stride(2) != 1:
+        q_shape, q_st = q.shape, q.stride()
+        if len(q_shape) != 3 or q_st[2] != 1:
             raise ValueError("q must be [n_rows, Hq, D] with unit channel stride")
-        _check_rows("q", q, (batch.n_rows, q.shape[1], cache.head_dim), cache.row_dtype, cache.device)
-        _check_rows("q_out", q_out, q.shape, cache.row_dtype, cache.device)
+        _check_rows("q", q, (batch.n_rows, q_shape[1], cache.head_dim), cache.row_dtype, cache.device)
+        _check_rows("q_out", q_out, q_shape, cache.row_dtype, cache.device)
         if not q_out.is_contiguous():
             raise ValueError("q_out must be contiguous")
-        cfg = cache._rows_cfg(q.shape[1])
-        at_q, to_q, q_strides = q.data_ptr(), q_out.data_ptr(), _strides(q)
+        cfg = cache._rows_cfg(q_shape[1])
+        at_q, to_q, q_strides = q.data_ptr(), q_out.data_ptr(), _strides(q_shape, q_st)
+    row_stride, head_stride = _strides(shape, strides)
     _call("qsa_paged_append_rotate", cache.device, stream, cache.byref, batch.byref, cfg, rope.byref, k_new.data_ptr(),
-          v_new.data_ptr(), *_strides(k_new), at_q, *q_strides, to_q)
+          v_new.data_ptr(), row_stride, head_stride, at_q, *q_strides, to_q)
 
 
 def paged_read(cache: PagedCache, batch: PagedBatch, k_out: torch.Tensor, v_out: torch.Tensor, stream=None):

@@ -80,27 +80,38 @@ class Rope:
         self.byref = ctypes.byref(self.desc)
 
 
-def _strides(t: torch.Tensor):
+_KINDS = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _strides(shape, strides):
     """Row and head strides of [rows, heads, dim]; those of an axis of one do not matter."""
-    return (t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2], t.stride(1) if t.shape[1] > 1 else t.shape[2])
+    return strides[0] if shape[0] > 1 else shape[1] * shape[2], strides[1] if shape[1] > 1 else shape[2]
 
 
 def rotate(rope: Rope, positions: torch.Tensor, x: torch.Tensor, out: torch.Tensor | None = None, stream=None):
     """out[r, h] = x[r, h] rotated for position positions[r] (int32, on the GPU).  x is
     [rows, heads, dim] of f32 or bf16 with unit channel stride; out may be x itself, and
     is x by default."""
-    out = x if out is None else out
-    if x.dim() != 3 or out.shape != x.shape or out.dtype is not x.dtype or out.device != x.device:
+    shape, x_strides, device, dtype = x.shape, x.stride(), x.device, x.dtype
+    if out is None:
+        out = x
+    elif out is not x and (out.shape != shape or out.dtype is not dtype or out.device != device):
         raise ValueError("x and out must be [rows, heads, dim] of one shape, dtype and device")
-    if x.dtype is not torch.float32 and x.dtype is not torch.bfloat16:
-        raise TypeError(f"x must be float32 or bfloat16, not {x.dtype}")
-    if x.shape[2] > 1 and (x.stride(2) != 1 or out.stride(2) != 1):
+    if len(shape) != 3:
+        raise ValueError("x and out must be [rows, heads, dim] of one shape, dtype and device")
+    kind = _KINDS.get(dtype)
+    if kind is None:
+        raise TypeError(f"x must be float32 or bfloat16, not {dtype}")
+    out_strides = x_strides if out is x else out.stride()
+    rows, heads, dim = shape
+    if (x_strides[2] != 1 or out_strides[2] != 1) and dim > 1:
         raise ValueError("x and out need unit channel stride")
-    if positions.dtype is not torch.int32 or positions.shape != x.shape[:1] or not positions.is_contiguous():
+    if positions.dtype is not torch.int32 or positions.shape != (rows,) or not positions.is_contiguous():
         raise TypeError("positions must be a contiguous int32 vector with an entry for each row")
-    if positions.device != x.device:
-        raise ValueError(f"positions is on {positions.device}, x on {x.device}")
-    rows, heads, dim = x.shape
-    _call("qsa_rotate", x.device, stream, rope.byref, positions.data_ptr(), rows, heads, dim,
-          F32 if x.dtype is torch.float32 else BF16, x.data_ptr(), *_strides(x), out.data_ptr(), *_strides(out))
+    if positions.device != device:
+        raise ValueError(f"positions is on {positions.device}, x on {device}")
+    x_row, x_head = _strides(shape, x_strides)
+    y_row, y_head = _strides(shape, out_strides)
+    _call("qsa_rotate", device, stream, rope.byref, positions.data_ptr(), rows, heads, dim, kind, x.data_ptr(), x_row,
+          x_head, out.data_ptr(), y_row, y_head)
     return out
