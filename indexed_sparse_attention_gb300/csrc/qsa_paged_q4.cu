@@ -1,34 +1,36 @@
-// Attention over a paged K/V cache held in 4 bits (QSA_Q4_1: blocks of 32 channels,
-// value = code * scale + minimum; see include/qsa.h for the layout, qsa_paged.cuh for
-// the division of the work into runs of key tiles, and qsa_paged.cu for the joining
-// launch).
+// Attention of up to 16 query entries over a paged K/V cache held in 4 bits (QSA_Q4_1:
+// blocks of 32 channels, value = code * scale + minimum; see include/qsa.h for the
+// layout, qsa_paged.cuh for the division of the work into runs of key tiles, and
+// qsa_paged.cu for the joining launch), on the 5th-generation tensor cores.
 //
-// An item's 16 entries (query row, head of the KV head's group) are the M rows of
-// mma.sync.m16n8k16 f16 products; a tile is 128 keys, 16 for each of eight warps.  A
-// warp works through its keys by itself -- logits, softmax with statistics of its
-// own, output -- so nothing is exchanged until an item ends, when the eight parts
-// are joined through shared memory.
+// An item's entries (query row, head of the KV head's group) are the 16 N columns of the
+// products, and K and V the A operands, which warps bring from their codes into TMEM (128
+// lanes) in registers: with entries as columns a product's time and its shared memory
+// traffic stay small, and what is expanded never passes through shared memory.
+//   logits   z_t = sum_g s_tg (sum_c q_c code_tc) + sum_g m_tg (sum_c q_c), lanes = a
+//            tile's 128 keys.  A code is the E4M3 byte of code * 2^-9, subnormal or not:
+//            masks only, eight codes in three instructions.  q times a power of two that
+//            brings its row's largest magnitude to [2^7, 2^8) is the sum of two E4M3 codes,
+//            the second that of what the first leaves: exact for bf16's 8 bits from 2^-10 of
+//            that largest on, off by at most 2^-10 (2^-17 of the largest) below.  A block's
+//            sum is a product of its own, kind::f8f6f4 with 32 of K, and the softmax, where a
+//            thread owns a key, adds the blocks up times their scales in 32 bits.  The
+//            minima are one more product, kind::f16, with the sums of q as two f16 halves.
+//   output   O^T += V^T P^T, lanes = 128 channels (twice for head_dim 256), kind::f16: V as
+//            f16, code * scale + minimum rounded once.  A thread owns the four channels of a
+//            code unit, of two keys a cell, in the fragment shape of tcgen05.st.
+//            P^T = 2^(z - m) as f16 through shared memory, K-major like q.
+// A row's maximum would be a reduction over lanes: instead the reference m of the weights
+// stays until a logit passes it by 2^8 (one vote a tile), and only then the tile's maxima
+// are reduced and O and the sums rescaled.  Weights are f16 with 2^7 at the reference, so
+// 2^15 is the largest.
 //
-// Codes enter the products as they are: a nibble in bits 0-3 (4-7) of a half is the
-// f16 subnormal code * 2^-24 (2^-20), exactly, so unpacking is masks only (5 for 8
-// values) and no conversion.
-//   logits   z_t = sum_g s_tg (sum_c q_c code_tc) + sum_g m_tg (sum_c q_c): the inner
-//            sum is a product of two k-steps a block, 32-bit, scaled in 32 bits; the
-//            second is one more product, of the block sums of q as two f16 halves
-//            against the minima.  q times a power of two that brings its row's
-//            largest magnitude to [2^8, 2^9) is exact in f16 from 2^-25 of that on
-//            and off by at most 2^-33 of it below, so the logits are those of the
-//            stored values.
-//   output   sum_t w_t v_t = sum_t (w_t s_tg) code_tc + sum_t w_t m_tg: w_t and
-//            f16(w_t s_tg) are f16 (two roundings of 2^-12 a weight); weights are kept
-//            relative to a maximum so that 2^6 is the largest, lagging by up to 2^4,
-//            and to scales above 2^5 (with |s| < 65504 nothing overflows), so that a
-//            weight is exact to 2^-31 of the largest.
-//
-// K, V and their records come through TMA, 40 KB (head_dim 256) a tile, into a ring
-// of as many tiles as fit; boxes of pages without visible tokens are aimed past the
-// last page, which fills zeros without reading.  Every wait gives up after about two
-// seconds (counted; nothing more is issued then, and the CTA runs to its end).
+// Roles (20 warps): 0-7 expand codes (four warps a half of K's channels, and of V's keys),
+// 8-15 softmax and output (a warpgroup eight columns), 16 copies, 17 issues the logits'
+// products, 18 the output's, 19 writes Q.  K, V and their records come through TMA, 64
+// keys a slot; boxes of pages without visible tokens are aimed past the last page, which
+// fills zeros without reading.  Every wait gives up after about two seconds (counted;
+// nothing more is issued then, and the CTA runs to its end).
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 #include <math.h>
@@ -48,18 +50,20 @@ using namespace tc;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kWarps = 12;               // that compute
-constexpr int kThreads = 32 * (kWarps + 4);   // four warpgroups: three that compute, one whose first warp copies
-// Registers of a thread: 128 at launch (512 threads share 65,536), of which the copying
-// warpgroup leaves 96 to the others: 384 * 160 + 128 * 32 = 65,536.
-constexpr int kRegsCompute = 160, kRegsCopy = 32;
-constexpr int kMT = 16;                  // entries of an item
-constexpr int kTeams = kWarps / 4, kMaxSlots = 5 * kTeams;
-constexpr int kKT = 64;                  // keys of a tile: 16 for each of a team's four warps
+constexpr int kKT = 128;                 // keys of a tile
+constexpr int kHalfKeys = 64;            // of a slot, and of a half of V's product
+constexpr int kCodeWarps = 8, kSoftWarp = 8, kCopyWarp = 16, kLogitWarp = 17, kOutWarp = 18;   // (19: Q)
+constexpr int kThreads = 640;
+constexpr int kEntries = 16, kNC = 8;     // columns, and those of a softmax warpgroup
+constexpr int kMaxSlots = 20;
 constexpr int kSmemLimit = 227 * 1024;
-constexpr float kTop = 3.f;              // log2 of the largest weight when the maximum is up to date
-constexpr float kLag = 7.f;              // log2 of what a weight may pass it by
-constexpr float kScaleTop = 5.f;         // log2 of the scales that this leaves room for
+constexpr float kTop = 7.f;              // log2 of the weight at the reference
+constexpr float kLag = 8.f;              // log2 of what a weight may pass it by
+constexpr float kUnset = 1e38f;          // shift of a column that has seen no logit: any finite one passes it
+constexpr uint32_t kTmemCols = 512;
+// TMEM columns: logits (16 a block, then the minima's), the minima, the output's two slabs, K's codes, two buffers
+// of V's values.
+constexpr uint32_t kSCol = 0, kMinCol = 144, kOCol = 160, kKCol = 192, kVCol = 256;
 
 __device__ int g_timeouts;
 __device__ int g_bad_pages;
@@ -67,40 +71,43 @@ __device__ int g_bad_pages;
 struct Q4Params {
   CUtensorMap k, v, r;   // {bytes of a row or record, page_tokens, Hkv, n_pages}: boxes of min(page_tokens, 64) tokens
   PagedParams p;
+  int32_t n_slots;
 };
 
+// A wait by parity tells a phase from its neighbours only: whoever waits for one has seen
+// the phase before it, or caused it.
 struct Head {
-  uint64_t full[kMaxSlots], empty[kMaxSlots];
+  uint64_t code_full[kMaxSlots], code_empty[kMaxSlots];
+  uint64_t k_full, k_empty, s_full, s_empty;
+  uint64_t v_full[2][2], v_empty[2][2];                    // halves of V's keys, of even and odd tiles
+  uint64_t p_full[2], pv_done[2];                          // even and odd tiles
+  uint64_t q_full, q_free, o_free, mma_done;
+  uint64_t row_full[4];                                    // an item's q below
   int64_t scan[kThreads / 32];
   Start start;
+  uint32_t tmem;
   int abort;
-  uint32_t bad[kMaxSlots];   // 16-token pieces of the slot's tile that have no page
-  float m[kWarps][kMT], l[kWarps][kMT];
+  uint8_t bad[16][2];              // 16-token pieces of a tile's halves that have no page (fewer tiles are under way)
+  float q[4][kEntries];         // of an item's entries: the power of two that Q's row was divided by
+  alignas(16) float2 column[kEntries];   // weight = 2^(logit * x + y)
+  float ref[kEntries], factor[kEntries], inv[kEntries];
+  int64_t to[kEntries];         // where the entry's outputs go, in elements
+  int pos[kEntries];
+  float mx[4][kEntries], sums[4][kEntries];
+  alignas(16) uint4 scale[4][kKT];   // of K's blocks, of the last tiles
 };
-constexpr int kHeadBytes = 4 * 1024;
+constexpr int kHeadBytes = 11 * 1024;
+constexpr int kPBytes = 2 * kEntries * 128;   // a buffer of weights: slabs of 64 keys
 static_assert(sizeof(Head) <= kHeadBytes, "shared memory head");
 
-// Three teams of four warps take an item's tiles in turn, each with a ring of slots and a
-// copying warp of its own: a slot's phases then follow each other for everyone who waits
-// for one.  A warp computes the logits and weights of
-// 16 keys, all channels; of head_dim 256, two warps exchange their weights and take half
-// of the channels of all 32 keys each for the output (which is what 12 warps' registers
-// hold).
 template <int D>
-struct Layout {
-  static constexpr int kHalves = D / 128, kPairs = kWarps / kHalves;
+struct Slot {
   static constexpr int kRow = D / 2, kRecord = D / 4;
-  static constexpr int kCodes = kKT * kRow, kSlot = 2 * kCodes + kKT * kRecord;
-  static constexpr int kQ = 1024 * D / 32;         // Q's fragments, two k-steps a block
-  // Joining: 32 channels of the 16 rows of each warp, rows 4 floats apart in banks (before
-  // that, the weights' exchange).
-  static constexpr int kPitch = 36, kJoin = kWarps * kMT * kPitch * 4;
-  static constexpr int kFixed = kHeadBytes + kQ + kJoin;
-  static constexpr int kFit = (kSmemLimit - kFixed) / (kTeams * kSlot);
-  static constexpr int kTeamSlots = kFit < kMaxSlots / kTeams ? kFit : kMaxSlots / kTeams, kSlots = kTeams * kTeamSlots;
+  static constexpr int kQSlab = kEntries * 128, kQ = (2 * (D / 128) + 1) * kQSlab;   // both codes of q, and its sums
+  static constexpr int kCodes = kHalfKeys * kRow, kBytes = 2 * kCodes + kHalfKeys * kRecord;
 };
 
-__device__ __forceinline__ bool wait_slow(uint64_t* b, uint32_t parity, int* abort) {
+__device__ __noinline__ bool wait_slow(uint64_t* b, uint32_t parity, int* abort) {
   return bar_wait(b, parity, &g_timeouts, abort);
 }
 __device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, int* abort) {
@@ -113,615 +120,783 @@ __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
       : "memory");
 }
-__device__ __forceinline__ void named_sync(int id, int threads) {
-  asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+__device__ __forceinline__ void soft_sync(int id) { asm volatile("bar.sync %0, 128;\n" ::"r"(id) : "memory"); }
+// Whether any of the warpgroup's threads says so.
+__device__ __forceinline__ bool soft_any(int id, bool x) {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+               : "=r"(r)
+               : "r"((uint32_t)x), "r"(id)
+               : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+  return one != 0;
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ uint4 lds128(const uint8_t* at) { return *reinterpret_cast<const uint4*>(at); }
-__device__ __forceinline__ uint2 lds64(const uint8_t* at) { return *reinterpret_cast<const uint2*>(at); }
-__device__ __forceinline__ uint32_t lds32(const uint8_t* at) { return *reinterpret_cast<const uint32_t*>(at); }
-// (Not volatile: products of registers, which may be moved past each other.)
-__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};\n"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ void mma_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {   // c = a b
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};\n"
-      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+// Two values to E4M3, the first in the low byte, and back.
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+  unsigned short r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
 }
-__device__ __forceinline__ void mma8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b, bool first) {   // 8 of k
-  if (first)
-    asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%7, %7, %7, %7};\n"
-        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-        : "r"(a0), "r"(a1), "r"(b), "f"(0.f));
-  else
-    asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%0, %1, %2, %3};\n"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(b));
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t two) {
+  uint32_t h2;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((unsigned short)two));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h2));
 }
-// acc += f * d, two binary32 values at once.
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b) {   // (a & MASK) | b
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(a), "n"(MASK), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t add_f16(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t fma_f16(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+// D[tmem] (+)= A[tmem] B[smem], f16.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// The same of E4M3 values, 32 of K.
+__device__ __forceinline__ void mma_f8_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Four consecutive columns of this thread's lane; tmem_st_wait before others read them.
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0, %1, %2, %3};\n" ::"r"(a), "r"(b), "r"(c), "r"(d), "r"(taddr)
+               : "memory");
+}
+// 16 lanes x 16 columns in two fragments of eight columns: of each, thread 4 i + j holds columns 2 j and
+// 2 j + 1 of lane i, then of lane 8 + i.
+__device__ __forceinline__ void tmem_st_fragments(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};\n" ::"r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};\n" ::"r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+               : "memory");
+}
+// Eight consecutive columns of this thread's lane; the values are there after tmem_ld_wait of them.
+__device__ __forceinline__ void tmem_ld8_start(uint32_t taddr, float* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void tmem_ld_done(float* r) {   // (uses of r stay behind the wait)
+  asm volatile("" : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]));
+}
+
+// v[0 .. 7] of every lane, reduced over the warp: lane x returns that of v[x / 4].
+template <typename F>
+__device__ __forceinline__ float reduce_columns(const float* from, int lane, F op) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = from[i];
+#pragma unroll
+  for (int n = 4; n >= 1; n >>= 1) {
+    const bool up = (lane & (4 * n)) != 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float keep = up ? v[n + i] : v[i], give = up ? v[i] : v[n + i];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, 4 * n));
+    }
+  }
+  v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 2));
+  return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
+}
+
+// (a0, a1) += (f0, f1) (d0, d1).
 __device__ __forceinline__ void fma2(float& a0, float& a1, float f0, float f1, float d0, float d1) {
   asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%0, %1};\n"
       " fma.rn.f32x2 z, x, y, z;\n mov.b64 {%0, %1}, z;\n}\n"
       : "+f"(a0), "+f"(a1)
       : "f"(f0), "f"(f1), "f"(d0), "f"(d1));
 }
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t mul_f16(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ float low_half(uint32_t w) { return __low2float(*reinterpret_cast<const __half2*>(&w)); }
 
 struct ItemRows {
   int f0, nf, pos0, first, last;
 };
 __device__ __forceinline__ ItemRows item_rows(const PagedParams& p, const Cursor<kKT>& c) {
   ItemRows r;
-  r.f0 = c.m * kMT;
-  r.nf = min(kMT, c.s.n * p.group - r.f0);
+  r.f0 = c.m * p.mt;
+  r.nf = min(p.mt, c.s.n * p.group - r.f0);
   r.pos0 = c.s.len - c.s.n;
   r.first = r.pos0 + row_of(p, r.f0);
   r.last = r.pos0 + row_of(p, r.f0 + r.nf - 1);
   return r;
 }
 
-// The row of 16 keys at tile column n of either half: the order that spreads the rows
-// which one load of a warp touches over all banks (K: columns 2 i and 2 i + 1 differ in
-// the lowest bit; V and the records: columns 0, 2, 4, 6, and 1, 3, 5, 7, are two rows of
-// each parity, two apart).
-__device__ __forceinline__ int key_of(int n) { return n ^ ((n >> 1) & 1); }
-
-// Where a tile's rows lie under TMA's swizzles: chunk c (16 bytes) of row r of codes or
-// records.  Rows 8 on are 8 whole rows on, and chunks that differ by one bit are that bit
-// of the offset apart, so a lane needs one offset for each of the rows it reads.
+// Where TMA's swizzles put chunk c (16 bytes) of row r of codes or records.
 template <int BYTES>
 __device__ __forceinline__ int swizzled(int r, int c) {
   if constexpr (BYTES == 128) return r * 128 + ((c ^ (r & 7)) << 4);
   else if constexpr (BYTES == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
   else return r * 32 + ((c ^ ((r >> 2) & 1)) << 4);
 }
+__device__ __forceinline__ uint4 lds128(const uint8_t* at) { return *reinterpret_cast<const uint4*>(at); }
+__device__ __forceinline__ uint2 lds64(const uint8_t* at) { return *reinterpret_cast<const uint2*>(at); }
+__device__ __forceinline__ uint32_t lds32(const uint8_t* at) { return *reinterpret_cast<const uint32_t*>(at); }
+
+// Four codes of two units (nibbles j of both are the halves of word j) to values.  A code in
+// bits 0-3 of a half is 1024 + code as the bits of an f16, in bits 4-7 with another
+// exponent 64 + code; the difference is exact.
+__device__ __forceinline__ void expand(uint32_t w, uint32_t scale, uint32_t minimum, uint32_t m1024, uint32_t m64,
+                                       uint32_t (&v)[4]) {
+  const uint32_t u = w >> 8;
+  v[0] = fma_f16(add_f16(and_or<0x000f000fu>(w, m1024), 0xe400e400u), scale, minimum);
+  v[1] = fma_f16(add_f16(and_or<0x00f000f0u>(w, m64), 0xd400d400u), scale, minimum);
+  v[2] = fma_f16(add_f16(and_or<0x000f000fu>(u, m1024), 0xe400e400u), scale, minimum);
+  v[3] = fma_f16(add_f16(and_or<0x00f000f0u>(u, m64), 0xd400d400u), scale, minimum);
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_constant__ Q4Params qp) {
-  using L = Layout<D>;
-  constexpr int G = D / 32, H = L::kHalves, KT = kKT;
+  using L = Slot<D>;
+  constexpr int G = D / 32, NS = D / 128;
   const PagedParams& p = qp.p;
   extern __shared__ __align__(1024) uint8_t raw[];
   Head& h = *reinterpret_cast<Head*>(raw);
-  uint8_t* const ring = raw + kHeadBytes;   // (1,024-byte boundaries: the head is 4 KB, slots are multiples)
-  uint8_t* const q_s = ring + L::kSlots * L::kSlot;
-  float* const join_s = reinterpret_cast<float*>(q_s + L::kQ);
+  uint8_t* const q_s = raw + kHeadBytes;          // K-major: slabs of 128 channels of the first codes, of the second; sums
+  uint8_t* const p_s = q_s + L::kQ;
+  uint8_t* const ring = p_s + 2 * kPBytes;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int* abrt = &h.abort;
   if (tid == 0) {
-    for (int i = 0; i < L::kSlots; ++i) {
-      bar_init(&h.full[i], 1);
-      bar_init(&h.empty[i], kWarps / kTeams);
+    for (int i = 0; i < qp.n_slots; ++i) {
+      bar_init(&h.code_full[i], 1);
+      bar_init(&h.code_empty[i], kCodeWarps);     // four warps read its K, four its V
     }
+    bar_init(&h.k_full, kCodeWarps);
+    bar_init(&h.k_empty, 1);
+    bar_init(&h.s_full, 1);
+    bar_init(&h.s_empty, 8);
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&h.p_full[i], 8);
+      bar_init(&h.pv_done[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      bar_init(&h.v_full[0][0] + i, 4);
+      bar_init(&h.v_empty[0][0] + i, 1);
+      bar_init(&h.row_full[i], 2);
+    }
+    bar_init(&h.q_full, 2);
+    bar_init(&h.q_free, 1);
+    bar_init(&h.o_free, 8);
+    bar_init(&h.mma_done, 2);
     h.abort = 0;
     bar_init_fence();
   }
+  if (warp == kLogitWarp) tmem_alloc(&h.tmem, kTmemCols);
+  if (warp == kCopyWarp && lane < 3) prefetch_map(lane == 0 ? &qp.k : lane == 1 ? &qp.v : &qp.r);
+  fence_before();
   __syncthreads();
+  fence_after();
+  const uint32_t tmem = h.tmem;
   grid_dependency_wait();
   grid_dependency_release();
-  const Start st = find_run<kThreads, KT>(p, kMT, blockIdx.x, gridDim.x, h.scan, &h.start);
-  Cursor<KT> c;
-  c.begin(p, kMT, st);
-  if (tid == 0) h.start = st;   // for the end (this thread's): registers are short
+  const Start st = find_run<kThreads, kKT>(p, p.mt, blockIdx.x, gridDim.x, h.scan, &h.start);
+  Cursor<kKT> c;
+  c.begin(p, p.mt, st);
+  if (tid == 32 * kSoftWarp) h.start = st;   // for the end (this thread's): registers are short
   if (st.n == 0) {
     if (tid == 0) p.parts[blockIdx.x] = PagedPart{};
-    return;
-  }
-  if (warp >= kWarps) {
-    // ------------------------------------------------------------ copies
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsCopy));
-    // A warp for each team; a lane a box of tokens: its K, V and records.
-    const int team = warp - kWarps;
-    if (team >= kTeams) return;
-    const int box = min(1 << p.page_shift, KT), n_box = KT / box, page_mask = (1 << p.page_shift) - 1;
-    const bool copies = lane < n_box;
-    int done = 0;   // the team's tiles
-    bool live = true;
-    for (bool more = true; more && live; more = c.next(p, kMT)) {
+  } else if (warp < kCodeWarps) {
+    // ------------------------------------------------------------ codes to values
+    const int part = warp >> 2, quarter = warp & 3;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
+    uint32_t m1024 = 0x64006400u, m64 = 0x54005400u;   // kept in registers
+    asm volatile("" : "+r"(m1024), "+r"(m64));
+    // K: the thread's key is row kr of half kh; the warp's half of the channels is that of units n in [4 part, 4 part + 4).
+    const int kh = quarter >> 1, kr = 32 * (quarter & 1) + lane;
+    // V: units n of block g, or of blocks g and g + 1 (head_dim 256): of each 16 keys rows 2 j,
+    // 2 j + 1, 2 j + 8 and 2 j + 9, whose codes lie in different banks.
+    const int a8 = lane >> 2, j2 = 2 * (lane & 3), vn = 2 * quarter + (a8 >> 2), vg = (D == 256 ? 2 : 1) * (a8 & 3);
+    int slot = 0;        // of the tile's first half; the second is the next
+    uint32_t use = 0;
+    int g = 0;           // tiles done
+    for (bool more = true; more; more = c.next(p, p.mt)) {
       const ItemRows ir = item_rows(p, c);
       const int T = c.x1 - c.x;
-      auto wanted = [&](int j) {
-        const int t = c.tiles.token(c.x + j) + lane * box, end = min(t + box - 1, ir.last);
-        return copies && t <= ir.last && (p.window == 0 || end > ir.first - p.window || t < p.n_sinks);
-      };
-      auto look_up = [&](int j) {
-        const int64_t s = (int64_t)(c.tiles.token(c.x + j) + lane * box) >> p.page_shift;
-        int32_t page = -1;
-        if (wanted(j) && s < p.table_ld) page = __ldcg(p.table + c.seq * p.table_ld + s);
-        return page;
-      };
-      int page = team < T ? look_up(team) : -1, next = team + kTeams < T ? look_up(team + kTeams) : -1;
 #pragma unroll 1
-      for (int j = team; j < T; j += kTeams, ++done) {
-        const int ahead = j + 2 * kTeams < T ? look_up(j + 2 * kTeams) : -1;
-        const int use = done / L::kTeamSlots, slot = team * L::kTeamSlots + done % L::kTeamSlots;
-        if (use > 0 && !wait(&h.empty[slot], (uint32_t)(use - 1) & 1, abrt)) live = false;
-        live = __all_sync(0xffffffffu, live);
-        if (!live) break;
-        const bool want = wanted(j), missing = want && (uint32_t)page >= (uint32_t)p.n_pages;
-        if (!want || missing) page = p.n_pages;   // past the last page: zeros
-        const uint32_t bad =
-            __reduce_or_sync(0xffffffffu, missing ? ((1u << (box / 16)) - 1u) << (lane * (box / 16)) : 0u);
-        if (missing) atomicAdd(&g_bad_pages, 1);
-        if (lane == 0) {
-          h.bad[slot] = bad;
-          bar_expect_tx(&h.full[slot], L::kSlot);
+      for (int j = 0; j < T; ++j, ++g) {
+        int other = slot + 1;
+        uint32_t other_use = use;
+        if (other == qp.n_slots) other = 0, ++other_use;
+        {
+          const int sk = kh ? other : slot;
+          wait(&h.code_full[sk], (kh ? other_use : use) & 1, abrt);
+          __syncwarp();
+          const uint8_t* const at = ring + sk * L::kBytes;
+          uint32_t w[2 * G], pair[G / 2][2];   // four units n of G blocks; scales and minima of two blocks
+#pragma unroll
+          for (int i = 0; i < G / 2; ++i) {
+            const uint4 x = lds128(at + swizzled<L::kRow>(kr, part * (G / 2) + i));
+            w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+          }
+#pragma unroll
+          for (int i = 0; i < G / 4; ++i) {
+            const uint4 x = lds128(at + 2 * L::kCodes + swizzled<L::kRecord>(kr, i));
+            pair[2 * i][0] = __byte_perm(x.x, x.y, 0x5410), pair[2 * i][1] = __byte_perm(x.x, x.y, 0x7632);
+            pair[2 * i + 1][0] = __byte_perm(x.z, x.w, 0x5410), pair[2 * i + 1][1] = __byte_perm(x.z, x.w, 0x7632);
+          }
+          __syncwarp();
+          if (lane == 0) bar_arrive(&h.code_empty[sk]);
+          if (g > 0) wait(&h.k_empty, (uint32_t)(g - 1) & 1, abrt);
+          __syncwarp();
+          fence_after();
+          if (part == 0) {
+            if constexpr (D == 256) h.scale[g & 3][32 * quarter + lane] = make_uint4(pair[0][0], pair[1][0], pair[G / 2 - 2][0], pair[G / 2 - 1][0]);
+            else h.scale[g & 3][32 * quarter + lane] = make_uint4(pair[0][0], pair[1][0], 0u, 0u);
+          }
+          // The minima twice, for both halves of q's sums.
+          const uint32_t at_min = lanes + kMinCol + 4u * part;
+          if constexpr (D == 256) tmem_st4(at_min, pair[0][1], pair[1][1], pair[G / 2 - 2][1], pair[G / 2 - 1][1]);
+          else if (part == 0) tmem_st4(at_min, pair[0][1], pair[1][1], pair[0][1], pair[1][1]);
+          else tmem_st4(at_min, 0u, 0u, 0u, 0u);
+          // Words i + G / 2 n of w are units n of blocks 2 i and 2 i + 1; cells of a block: of two units nibbles 0 and
+          // 2, then 1 and 3.
+#pragma unroll
+          for (int i = 0; i < G / 2; ++i)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const uint32_t x = __byte_perm(w[i], w[i + G / 2], b ? 0x7632 : 0x5410), y = __byte_perm(w[i + G], w[i + G + G / 2], b ? 0x7632 : 0x5410);
+              tmem_st4(lanes + kKCol + (uint32_t)(8 * (2 * i + b) + 4 * part), x & 0x0f0f0f0fu, (x >> 4) & 0x0f0f0f0fu,
+                       y & 0x0f0f0f0fu, (y >> 4) & 0x0f0f0f0fu);
+            }
+          tmem_st_wait();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(&h.k_full);
         }
+        const int sv = part ? other : slot;
+        wait(&h.code_full[sv], (part ? other_use : use) & 1, abrt);
         __syncwarp();
-        if (copies) {
-          const uint32_t to = smem_addr(ring) + slot * L::kSlot;
-          const int token = c.tiles.token(c.x + j) & page_mask;
-          tma_4d(to + lane * box * L::kRow, &qp.k, 0, token, c.head, page, &h.full[slot]);
-          tma_4d(to + L::kCodes + lane * box * L::kRow, &qp.v, 0, token, c.head, page, &h.full[slot]);
-          tma_4d(to + 2 * L::kCodes + lane * box * L::kRecord, &qp.r, 0, token, c.head, page, &h.full[slot]);
+        const uint8_t* const at = ring + sv * L::kBytes + L::kCodes;
+        const uint8_t* const rec = at + L::kCodes;
+        const int t0 = c.tiles.token(c.x + j) + kHalfKeys * part;
+        // Tokens that no row sees become zeros: each of the four warps clears their records.
+        if (t0 + kHalfKeys - 1 > ir.last || (p.window > 0 && t0 <= ir.first - p.window && t0 + kHalfKeys > p.n_sinks)) {
+          uint8_t* const mine = ring + sv * L::kBytes + 2 * L::kCodes;
+#pragma unroll 1
+          for (int r = lane; r < kHalfKeys; r += 32) {
+            const int t = t0 + r;
+            if (t <= ir.last && (p.window == 0 || t > ir.first - p.window || t < p.n_sinks)) continue;
+#pragma unroll
+            for (int x = 0; x < NS; ++x)
+              *reinterpret_cast<uint4*>(mine + swizzled<L::kRecord>(r, NS + x)) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_async_smem();   // (copies will write there again)
+          __syncwarp();
         }
-        __syncwarp();
-        page = next;
-        next = ahead;
-      }
-    }
-    // Every copy has landed before the CTA ends: a lane a slot, the last tile that went there.
-    if (lane < L::kTeamSlots && lane < done) {
-      const int last = done - 1 - (done - 1 - lane) % L::kTeamSlots;
-      bar_wait(&h.full[team * L::kTeamSlots + lane], (uint32_t)(last / L::kTeamSlots) & 1, &g_timeouts);
-    }
-    return;
-  }
-
-  // -------------------------------------------------------------- products
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegsCompute));
-  const int n = lane >> 2, t = lane & 3;   // MMA row (and n + 8) and key column; k slot
-  const int team = warp >> 2, piece = warp & 3, half = H == 2 ? warp & 1 : 0;
-  const int k0 = 16 * piece;               // the warp's keys of a tile
-  // Weights on their way to the other warp of the pair (two buffers in turn), and what they
-  // are relative to: 512 bytes and 16 numbers a warp.
-  uint4* const pair_w = reinterpret_cast<uint4*>(join_s);
-  float* const pair_r = reinterpret_cast<float*>(join_s) + 2 * kWarps * 128;
-  const uint8_t* const my_q = q_s + lane * 16;
-  // Offsets in a tile: K's codes of key column n; the records of key columns 2 t, 2 t + 1
-  // and n; V's codes of key columns 2 t, 2 t + 1 (of the tile's first 16 keys).
-  constexpr int kRow = L::kRow, kRec = L::kRecord, kRecords = 2 * L::kCodes;
-  int at_k = swizzled<kRow>(k0 + key_of(n), D == 256 ? 2 * t : t);
-  int at_r0 = kRecords + swizzled<kRec>(key_of(2 * t), 0), at_r1 = kRecords + swizzled<kRec>(key_of(2 * t + 1), 0);
-  int at_m = kRecords + swizzled<kRec>(k0 + key_of(n), 0) + 8 * (t & 1);
-  int at_v0 = L::kCodes + swizzled<kRow>(key_of(2 * t), D == 256 ? n : n >> 1) + 8 * (D == 256 ? half : n & 1);
-  int at_v1 = L::kCodes + swizzled<kRow>(key_of(2 * t + 1), D == 256 ? n : n >> 1) + 8 * (D == 256 ? half : n & 1);
-  const int to_v = (H + half) << 4;        // from K's part of a record to the warp's part of V's: these bits change
-  // (Kept: the compiler would work them out again for every tile.)
-  asm volatile("" : "+r"(at_k), "+r"(at_r0), "+r"(at_r1), "+r"(at_m), "+r"(at_v0), "+r"(at_v1));
-  int done = 0;   // the team's tiles
-  for (bool more = true; more;) {
-    const ItemRows ir = item_rows(p, c);
-    const int T = c.x1 - c.x;
-    const int pos_lo = ir.pos0 + row_of(p, ir.f0 + min(n, ir.nf - 1)), pos_hi = ir.pos0 + row_of(p, ir.f0 + min(n + 8, ir.nf - 1));
-    // Q: row n (and n + 8), channels 32 g + 8 t .. + 7 of each block.
-    uint32_t qm[2][H];                     // sums of four blocks: high halves in slots 0-3, low in 4-7
-    float zc_lo, zc_hi;
-    {
-      const uint4* from[2];
-      float up[2];
-      bool odd[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int f = ir.f0 + min(n + 8 * i, ir.nf - 1), r = row_of(p, f);
-        const int64_t entry = (int64_t)(c.s.row0 + r) * p.n_q_heads + c.head * p.group + (f - r * p.group);
-        from[i] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + entry * D) + t;
-        uint32_t most = 0u;
+        for (int i2 = 0; i2 < kHalfKeys / 32; ++i2) {
+          uint32_t cell[NS][2][8];
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          const uint4 x = __ldg(from[i] + 4 * g);
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) most = max(most, max((w[e] << 16) & 0x7fff0000u, w[e] & 0x7fff0000u));
-        }
-        most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
-        most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
-        // 2^(exponent - 8), at least 2^-100: a row of smaller values keeps fewer bits.
-        const int e = max((int)(most >> 23) - 127 - 8, -100);
-        odd[i] = most >= 0x7f800000u;      // infinity or NaN: the row's logits are NaN
-        up[i] = __uint_as_float((uint32_t)(127 - e) << 23);
-        const float down = odd[i] ? 1.f : __uint_as_float((uint32_t)(127 + e) << 23);
-        // (Not 0, also where scale and power are both tiny: hidden logits are -infinity times it.)
-        (i ? zc_hi : zc_lo) = fmaxf(p.scale * kLog2e * down, 1e-37f);
-      }
-#pragma unroll
-      for (int hh = 0; hh < H; ++hh) {
-        float sums[2][2] = {{0.f, 0.f}, {0.f, 0.f}};   // of blocks 2 (t & 1) and the next
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          uint32_t frag[2][4];             // k-steps 0 and 1
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint4 x = __ldg(from[i] + 4 * (4 * hh + b));
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-            float v[8];
+          for (int i1 = 0; i1 < 2; ++i1) {
+            uint32_t w[4], lo[4], hi[4];   // units; records of block g (and, head_dim 256, g + 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              v[2 * e] = odd[i] ? __uint_as_float(0x7fffffffu) : bf16_lo(w[e]) * up[i];
-              v[2 * e + 1] = odd[i] ? __uint_as_float(0x7fffffffu) : bf16_hi(w[e]) * up[i];
-            }
-            float s = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s += v[e];
-            s += __shfl_xor_sync(0xffffffffu, s, 1);
-            s += __shfl_xor_sync(0xffffffffu, s, 2);
-            if ((t & 1) == b >> 1) sums[i][b & 1] = s;
-            // Slots 2 t, 2 t + 1 of a step hold channels j and 4 + j; the codes of even j are
-            // 2^4 smaller.
-#pragma unroll
-            for (int x2 = 0; x2 < 2; ++x2) {
-              frag[x2][i] = pack_f16(v[2 * x2] * 16.f, v[4 + 2 * x2] * 16.f);
-              frag[x2][2 + i] = pack_f16(v[2 * x2 + 1], v[5 + 2 * x2]);
-            }
-          }
-          if (warp == 4 * hh + b) {
-#pragma unroll
-            for (int x2 = 0; x2 < 2; ++x2)
-              *reinterpret_cast<uint4*>(q_s + (2 * warp + x2) * 512 + lane * 16) =
-                  make_uint4(frag[x2][0], frag[x2][1], frag[x2][2], frag[x2][3]);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t hi = pack_f16(sums[i][0], sums[i][1]);
-          const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-          qm[i][hh] = t < 2 ? hi : pack_f16(sums[i][0] - back.x, sums[i][1] - back.y);
-        }
-      }
-      named_sync(1, 32 * kWarps);
-    }
-
-    float o[4][4][4], om[4];
-#pragma unroll
-    for (int g = 0; g < 4; ++g)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[g][j][e] = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) om[e] = 0.f;
-    // What the output's weights are relative to (whole numbers; the same in both warps of a
-    // pair), and the sums of this thread's columns.
-    float m_lo = -INFINITY, m_hi = -INFINITY, l_lo = 0.f, l_hi = 0.f;
-    [[maybe_unused]] int turn = 0;   // of the exchange's two buffers: one barrier between writes to the same
-
-#pragma unroll 1
-    for (int j = team; j < T; j += kTeams, ++done) {
-      const int slot = team * L::kTeamSlots + done % L::kTeamSlots, t0 = c.tiles.token(c.x + j);
-      wait(&h.full[slot], (uint32_t)(done / L::kTeamSlots) & 1, abrt);
-      __syncwarp();
-      const uint32_t bad = h.bad[slot];
-      auto seen = [&](int tk) { return tk <= ir.last && (p.window == 0 || tk > ir.first - p.window || tk < p.n_sinks); };
-      // Tiles that every row sees whole are the rule.
-      const bool edge = bad != 0u || t0 + KT - 1 > ir.first || (p.window > 0 && t0 <= ir.last - p.window && t0 + KT > p.n_sinks);
-      bool mine = true, other = H == 2;
-      if (edge) {
-        auto some = [&](int pc) {   // a piece with keys that some row sees
-          const int a = t0 + 16 * pc;
-          return !((bad >> pc) & 1u) && a <= ir.last && (p.window == 0 || a + 15 > ir.first - p.window || a < p.n_sinks);
-        };
-        mine = some(piece);
-        other = H == 2 && some(piece ^ 1);
-      }
-      if (mine || other) {   // (the same in both warps of a pair)
-        const uint8_t* const at = ring + slot * L::kSlot;
-        uint32_t pw[4] = {0u, 0u, 0u, 0u};
-        float r_lo = m_lo, r_hi = m_hi, add_lo = 0.f, add_hi = 0.f;   // what pw is relative to, and its sums
-        if (mine) {
-          // ---- logits of two key columns of eight
-          float z[2][4], acc[2][4];
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[hf][e] = 0.f;
-#pragma unroll
-          for (int hh = 0; hh < H; ++hh) {
-            uint32_t w[2][4];              // units 2 t and 2 t + 1 (halves) of a block
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              uint2 a, b;
+              const int r = 32 * i2 + 16 * i1 + j2 + (e & 1) + 8 * (e >> 1);
               if constexpr (D == 256) {
-                a = lds64(at + at_k + 8 * kRow * hf + 8 * hh);
-                b = lds64(at + (at_k ^ 16) + 8 * kRow * hf + 8 * hh);
+                w[e] = lds32(at + swizzled<L::kRow>(r, vn) + 2 * vg);
+                const uint2 x = lds64(rec + swizzled<L::kRecord>(r, 2 + (vg >> 2)) + 4 * (vg & 3));
+                lo[e] = x.x, hi[e] = x.y;
               } else {
-                const uint4 both = lds128(at + at_k + 8 * kRow * hf);
-                a = make_uint2(both.x, both.y), b = make_uint2(both.z, both.w);
+                w[e] = *reinterpret_cast<const uint16_t*>(at + swizzled<L::kRow>(r, vn >> 1) + 8 * (vn & 1) + 2 * vg);
+                lo[e] = lds32(rec + swizzled<L::kRecord>(r, 1) + 4 * vg);
+                hi[e] = 0u;
               }
-              w[hf][0] = __byte_perm(a.x, b.x, 0x5410), w[hf][1] = __byte_perm(a.x, b.x, 0x7632);
-              w[hf][2] = __byte_perm(a.y, b.y, 0x5410), w[hf][3] = __byte_perm(a.y, b.y, 0x7632);
             }
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              // Scales of the thread's two key columns.
-              const uint4 s0 = lds128(at + (at_r0 ^ (16 * hh)) + k0 * kRec + 8 * kRec * hf),
-                          s1 = lds128(at + (at_r1 ^ (16 * hh)) + k0 * kRec + 8 * kRec * hf);
-              const uint32_t r0[4] = {s0.x, s0.y, s0.z, s0.w}, r1[4] = {s1.x, s1.y, s1.z, s1.w};
-              // Minima of two blocks of key column n, against the high or the low halves of the sums.
-              const uint2 two = lds64(at + (at_m ^ (16 * hh)) + 8 * kRec * hf);
-              mma8(z[hf], qm[0][hh], qm[1][hh], __byte_perm(two.x, two.y, 0x7632), hh == 0);
+            for (int k = 0; k < 2; ++k) {   // keys 0, 1 and 2, 3: columns 2 j and 2 j + 1
 #pragma unroll
-              for (int g = 0; g < 4; ++g) {
-                const uint4 qa = lds128(my_q + (8 * hh + 2 * g) * 512), qb = lds128(my_q + (8 * hh + 2 * g + 1) * 512);
-                const uint32_t a0[4] = {qa.x, qa.y, qa.z, qa.w}, a1[4] = {qb.x, qb.y, qb.z, qb.w};
-                const uint32_t x = w[hf][g], x8 = x >> 8;
-                float d[4];
-                mma_first(d, a0, x & 0x000f000fu, x & 0x00f000f0u);
-                mma(d, a1, x8 & 0x000f000fu, x8 & 0x00f000f0u);
-                const float f0 = low_half(r0[g]), f1 = low_half(r1[g]);
-                fma2(acc[hf][0], acc[hf][1], f0, f1, d[0], d[1]);
-                fma2(acc[hf][2], acc[hf][3], f0, f1, d[2], d[3]);
+              for (int b = 0; b < NS; ++b) {
+                const uint32_t r0 = b ? hi[2 * k] : lo[2 * k], r1 = b ? hi[2 * k + 1] : lo[2 * k + 1];
+                uint32_t v[4];
+                expand(__byte_perm(w[2 * k], w[2 * k + 1], b ? 0x7632 : 0x5410), __byte_perm(r0, r1, 0x5410),
+                       __byte_perm(r0, r1, 0x7632), m1024, m64, v);
+                cell[b][0][4 * i1 + k] = v[0], cell[b][0][4 * i1 + 2 + k] = v[1];
+                cell[b][1][4 * i1 + k] = v[2], cell[b][1][4 * i1 + 2 + k] = v[3];
               }
             }
           }
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) z[hf][e] = fmaf(acc[hf][e], 0x1p20f, z[hf][e]);
-          if (edge) {
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int tk = t0 + k0 + 8 * hf + key_of(2 * t + (e & 1));
-                if (!sees(p, e < 2 ? pos_lo : pos_hi, tk)) z[hf][e] = -INFINITY;
-              }
+          if (i2 == kHalfKeys / 32 - 1) {
+            __syncwarp();
+            if (lane == 0) bar_arrive(&h.code_empty[sv]);
           }
-          // V's scales of 2^5 and more ask for smaller weights: a lane looks at four blocks of a key.
-          float big = 0.f;
-          {
-            const int kr = k0 + (H == 2 ? lane >> 1 : lane & 15);
-            uint4 x = lds128(at + kRecords + swizzled<kRec>(kr, H + (H == 2 ? lane & 1 : 0)));
-            if (edge && !seen(t0 + kr)) x = make_uint4(0u, 0u, 0u, 0u);
-            if (__any_sync(0xffffffffu, ((x.x | x.y | x.z | x.w) & 0x4000u) != 0u)) {
-              const uint32_t most = __reduce_max_sync(0xffffffffu, max(max(x.x & 0x7fffu, x.y & 0x7fffu), max(x.z & 0x7fffu, x.w & 0x7fffu)));
-              // (|s| < 2^(exponent - 14))
-              big = fmaxf((float)((int)(most >> 10) - 14) - kScaleTop, 0.f);
-            }
+          if (i2 == 0) {
+            if (g >= 2) wait(&h.v_empty[part][g & 1], (uint32_t)((g - 2) >> 1) & 1, abrt);
+            __syncwarp();
+            fence_after();
           }
-          // ---- the rows' maxima and weights
-          float x_lo = fmaxf(fmaxf(z[0][0], z[0][1]), fmaxf(z[1][0], z[1][1]));
-          float x_hi = fmaxf(fmaxf(z[0][2], z[0][3]), fmaxf(z[1][2], z[1][3]));
-          x_lo = fmaxf(x_lo, __shfl_xor_sync(0xffffffffu, x_lo, 1));
-          x_hi = fmaxf(x_hi, __shfl_xor_sync(0xffffffffu, x_hi, 1));
-          x_lo = fmaxf(x_lo, __shfl_xor_sync(0xffffffffu, x_lo, 2));
-          x_hi = fmaxf(x_hi, __shfl_xor_sync(0xffffffffu, x_hi, 2));
-          const float need_lo = ceilf(fmaf(x_lo, zc_lo, big)), need_hi = ceilf(fmaf(x_hi, zc_hi, big));
-          if (m_lo == -INFINITY || need_lo > m_lo + kLag) r_lo = fmaxf(need_lo, m_lo);
-          if (m_hi == -INFINITY || need_hi > m_hi + kLag) r_hi = fmaxf(need_hi, m_hi);
-          const float sh_lo = r_lo == -INFINITY ? 0.f : kTop - r_lo, sh_hi = r_hi == -INFINITY ? 0.f : kTop - r_hi;
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const float w0 = ex2(fmaf(z[hf][0], zc_lo, sh_lo)), w1 = ex2(fmaf(z[hf][1], zc_lo, sh_lo)),
-                        w2 = ex2(fmaf(z[hf][2], zc_hi, sh_hi)), w3 = ex2(fmaf(z[hf][3], zc_hi, sh_hi));
-            add_lo += w0 + w1;
-            add_hi += w2 + w3;
-            pw[2 * hf] = pack_f16(w0, w1);
-            pw[2 * hf + 1] = pack_f16(w2, w3);
-          }
+          for (int b = 0; b < NS; ++b)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              tmem_st_fragments(lanes + ((uint32_t)(16 * x) << 16) + kVCol + (uint32_t)(128 * (g & 1) + 64 * b + 32 * part + 16 * i2), cell[b][x]);
         }
-        // ---- the pair's weights (the warp's own, then the other's), relative to the larger of two references
-        uint32_t pv[H][4];
-        float new_lo = r_lo, new_hi = r_hi;
-        if constexpr (H == 2) {
-          const int me = turn * kWarps + warp, you = me ^ 1;
-          turn ^= 1;
-          pair_w[me * 32 + lane] = make_uint4(pw[0], pw[1], pw[2], pw[3]);
-          if (t == 0) {
-            pair_r[me * 16 + n] = r_lo;
-            pair_r[me * 16 + n + 8] = r_hi;
-          }
-          named_sync(2 + (warp >> 1), 64);
-          const uint4 x = pair_w[you * 32 + lane];
-          const float u_lo = pair_r[you * 16 + n], u_hi = pair_r[you * 16 + n + 8];
-          const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-          new_lo = fmaxf(r_lo, u_lo);
-          new_hi = fmaxf(r_hi, u_hi);
-          // (Powers of two: exact, or below what f16 holds.)
-          const float a_lo = r_lo == new_lo ? 1.f : ex2(r_lo - new_lo), a_hi = r_hi == new_hi ? 1.f : ex2(r_hi - new_hi),
-                      b_lo = u_lo == new_lo ? 1.f : ex2(u_lo - new_lo), b_hi = u_hi == new_hi ? 1.f : ex2(u_hi - new_hi);
-          if (__any_sync(0xffffffffu, r_lo != u_lo || r_hi != u_hi)) {
-            add_lo *= a_lo;
-            add_hi *= a_hi;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              pv[0][e] = mul_f16(pw[e], pack_f16(e & 1 ? a_hi : a_lo, e & 1 ? a_hi : a_lo));
-              pv[H - 1][e] = mul_f16(y[e], pack_f16(e & 1 ? b_hi : b_lo, e & 1 ? b_hi : b_lo));
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              pv[0][e] = pw[e];
-              pv[H - 1][e] = y[e];
-            }
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) pv[0][e] = pw[e];
-        }
-        const bool move_lo = new_lo != m_lo, move_hi = new_hi != m_hi;   // (NaN: the weights are NaN anyway)
-        if (__any_sync(0xffffffffu, move_lo || move_hi)) {
-          const float a_lo = move_lo ? ex2(m_lo - new_lo) : 1.f, a_hi = move_hi ? ex2(m_hi - new_hi) : 1.f;
-          m_lo = new_lo;
-          m_hi = new_hi;
-          l_lo *= a_lo;
-          l_hi *= a_hi;
-#pragma unroll
-          for (int g = 0; g < 4; ++g)
-#pragma unroll
-            for (int jj = 0; jj < 4; ++jj) {
-              o[g][jj][0] *= a_lo;
-              o[g][jj][1] *= a_lo;
-              o[g][jj][2] *= a_hi;
-              o[g][jj][3] *= a_hi;
-            }
-          om[0] *= a_lo;
-          om[1] *= a_lo;
-          om[2] *= a_hi;
-          om[3] *= a_hi;
-        }
-        l_lo += add_lo;
-        l_hi += add_hi;
-        // ---- output: 16 keys at a time, the warp's 128 channels
-#pragma unroll
-        for (int s = 0; s < H; ++s) {
-          if (!(s == 0 ? mine : other)) continue;
-          const uint8_t* const mv = at + 16 * (s == 0 ? piece : piece ^ 1) * kRow;
-          const uint8_t* const mr = at + 16 * (s == 0 ? piece : piece ^ 1) * kRec;
-          uint32_t sab[4], scd[4], mab = 0u, mcd = 0u;   // scales, minima: pairs of the thread's keys
-          {
-            uint4 rec[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) rec[i] = lds128(mr + ((i & 1 ? at_r1 : at_r0) ^ to_v) + 8 * kRec * (i >> 1));
-            sab[0] = __byte_perm(rec[0].x, rec[1].x, 0x5410), scd[0] = __byte_perm(rec[2].x, rec[3].x, 0x5410);
-            sab[1] = __byte_perm(rec[0].y, rec[1].y, 0x5410), scd[1] = __byte_perm(rec[2].y, rec[3].y, 0x5410);
-            sab[2] = __byte_perm(rec[0].z, rec[1].z, 0x5410), scd[2] = __byte_perm(rec[2].z, rec[3].z, 0x5410);
-            sab[3] = __byte_perm(rec[0].w, rec[1].w, 0x5410), scd[3] = __byte_perm(rec[2].w, rec[3].w, 0x5410);
-            if (n < 4) {   // minima of block n
-              uint32_t x[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                x[i] = lds32(mr + ((i & 1 ? at_r1 : at_r0) ^ to_v) + 8 * kRec * (i >> 1) + 4 * n);
-              mab = __byte_perm(x[0], x[1], 0x7632);
-              mcd = __byte_perm(x[2], x[3], 0x7632);
-            }
-            if (edge) {   // what no row sees may hold anything
-              uint32_t keep[2] = {0u, 0u};
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (seen(t0 + 16 * (s == 0 ? piece : piece ^ 1) + 8 * (i >> 1) + key_of(2 * t + (i & 1)))) keep[i >> 1] |= i & 1 ? 0xffff0000u : 0xffffu;
-#pragma unroll
-              for (int g = 0; g < 4; ++g) {
-                sab[g] &= keep[0];
-                scd[g] &= keep[1];
-              }
-              mab &= keep[0];
-              mcd &= keep[1];
-            }
-          }
-          mma(om, pv[s], mab, mcd);
-          uint2 vw[4];   // the thread's four keys: unit n of blocks (0, 1) and (2, 3)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            vw[i] = lds64(mv + (i & 1 ? at_v1 : at_v0) + 8 * kRow * (i >> 1));
-          }
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const uint32_t a[4] = {mul_f16(pv[s][0], sab[g]), mul_f16(pv[s][1], sab[g]), mul_f16(pv[s][2], scd[g]), mul_f16(pv[s][3], scd[g])};
-            const uint32_t w0 = __byte_perm(g < 2 ? vw[0].x : vw[0].y, g < 2 ? vw[1].x : vw[1].y, g & 1 ? 0x7632 : 0x5410),
-                           w1 = __byte_perm(g < 2 ? vw[2].x : vw[2].y, g < 2 ? vw[3].x : vw[3].y, g & 1 ? 0x7632 : 0x5410);
-            const uint32_t u0 = w0 >> 8, u1 = w1 >> 8;
-            mma(o[g][0], a, w0 & 0x000f000fu, w1 & 0x000f000fu);
-            mma(o[g][1], a, w0 & 0x00f000f0u, w1 & 0x00f000f0u);
-            mma(o[g][2], a, u0 & 0x000f000fu, u1 & 0x000f000fu);
-            mma(o[g][3], a, u0 & 0x00f000f0u, u1 & 0x00f000f0u);
-          }
-        }
+        tmem_st_wait();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&h.v_full[part][g & 1]);
+        slot = other + 1;
+        use = other_use;
+        if (slot == qp.n_slots) slot = 0, ++use;
       }
+    }
+  } else if (warp < kCopyWarp) {
+    // ------------------------------------------------------------ softmax and output
+    // Each of two warpgroups takes half of the columns; a thread owns a key of a tile, and a
+    // channel of each slab of the output.
+    const int group = (warp - kSoftWarp) >> 2, quarter = warp & 3, me = tid & 127, bar = 1 + group;
+    const int col0 = kNC * group;   // columns [col0, col0 + 8)
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
+    // Where the key's weights lie: V's keys of each 16 are in the order of its fragments.
+    const int key = 32 * (quarter & 1) + lane;
+    const int at_k = (key & 48) | ((key & 6) << 1) | ((key & 8) >> 2) | (key & 1);
+    const int to_p = (quarter >> 1) * (kPBytes / 2) + (((at_k >> 3) << 4) | ((at_k & 7) << 1)) + col0 * 128;
+    const int channel = (D == 256 ? 64 : 32) * (lane & 3) + 4 * (2 * quarter + ((lane >> 2) & 1)) + (lane >> 3);   // (and 32 further)
+    int g = 0, it = 0;   // tiles and items done
+    for (bool more = true; more;) {
+      const ItemRows ir = item_rows(p, c);
+      const int T = c.x1 - c.x;
+      const bool whole = c.whole();
+      const bool mine = me < kNC && col0 + me < ir.nf;   // the thread has a column's statistics, too
+      wait(&h.row_full[it & 3], (uint32_t)(it >> 2) & 1, abrt);
+      if (me < kNC) {
+        const int e = col0 + me, f = ir.f0 + min(e, ir.nf - 1), r = row_of(p, f);
+        // (The factor is not 0: hidden logits are -infinity times it.)
+        h.column[e] = mine ? make_float2(fmaxf(h.q[it & 3][e] * (p.scale * kLog2e), 1e-37f), kUnset) : make_float2(0.f, -1000.f);
+        h.ref[e] = -INFINITY;
+        h.pos[e] = ir.pos0 + r;
+        h.to[e] = (whole ? (int64_t)(c.s.row0 + r) * p.n_q_heads + c.head * p.group + (f - r * p.group)
+                         : (int64_t)c.slot(blockIdx.x) * p.mt + e) * D;
+      }
+      soft_sync(bar);
+      // Of the columns: weight = 2^(logit * x + y), kept from tile to tile.
+      float2 k[kNC];
+      auto columns = [&] {
+#pragma unroll
+        for (int e = 0; e < kNC; e += 2) {
+          const float4 two = *reinterpret_cast<const float4*>(&h.column[col0 + e]);
+          k[e] = make_float2(two.x, two.y), k[e + 1] = make_float2(two.z, two.w);
+        }
+      };
+      columns();
+      float l[kNC];
+#pragma unroll
+      for (int e = 0; e < kNC; ++e) l[e] = 0.f;
+#pragma unroll 1
+      for (int j = 0; j < T; ++j, ++g) {
+        const int buf = g & 1, t0 = c.tiles.token(c.x + j);
+        wait(&h.s_full, (uint32_t)g & 1, abrt);
+        __syncwarp();
+        fence_after();
+        // The minima's part, and the blocks' times their scales (codes are times 2^-9).
+        float z[kNC], acc[kNC], part[G][kNC];
+#pragma unroll
+        for (int i = 0; i < G; ++i) tmem_ld8_start(lanes + kSCol + (uint32_t)(16 * i + col0), part[i]);
+        tmem_ld8_start(lanes + kSCol + (uint32_t)(16 * G + col0), z);
+        const uint4 sc = h.scale[g & 3][32 * quarter + lane];
+        const uint32_t bad = h.bad[g & 15][0] | (uint32_t)h.bad[g & 15][1] << 4;
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < G; ++i) tmem_ld_done(part[i]);
+        tmem_ld_done(z);
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&h.s_empty);
+#pragma unroll
+        for (int e = 0; e < kNC; ++e) acc[e] = 0.f;
+        const uint32_t scales[4] = {sc.x, sc.y, sc.z, sc.w};
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+          const float2 two = __half22float2(*reinterpret_cast<const __half2*>(&scales[i / 2]));
+          const float f = i & 1 ? two.y : two.x;
+#pragma unroll
+          for (int e = 0; e < kNC; e += 2) fma2(acc[e], acc[e + 1], f, f, part[i][e], part[i][e + 1]);
+        }
+#pragma unroll
+        for (int e = 0; e < kNC; ++e) z[e] = fmaf(acc[e], 512.f, z[e]);
+        // Tiles that every row sees whole are the rule.
+        if (bad != 0u || t0 + kKT - 1 > ir.first || (p.window > 0 && t0 <= ir.last - p.window && t0 + kKT > p.n_sinks)) {
+          const int tk = t0 + 32 * quarter + lane;
+          const bool gone = (bad >> (2 * quarter + (lane >> 4))) & 1u;
+#pragma unroll
+          for (int e = 0; e < kNC; ++e)
+            if (gone || !sees(p, h.pos[col0 + e], tk)) z[e] = -INFINITY;
+        }
+        // Whether a weight would be larger than the reference leaves room for.
+        float y[kNC];
+#pragma unroll
+        for (int e = 0; e < kNC; ++e) y[e] = fmaf(z[e], k[e].x, k[e].y);
+#pragma unroll
+        for (int n = kNC / 2; n >= 1; n >>= 1)
+#pragma unroll
+          for (int e = 0; e < n; ++e) y[e] = fmaxf(y[e], y[n + e]);
+        if (soft_any(bar, y[0] > kTop + kLag)) {
+          const float top = reduce_columns(z, lane, [](float a, float b) { return fmaxf(a, b); });
+          if ((lane & 3) == 0) h.mx[quarter][col0 + (lane >> 2)] = top;
+          soft_sync(bar);
+          if (me < kNC) {
+            const int e = col0 + me;
+            float factor = 1.f;
+            if (mine) {
+              const float top = fmaxf(fmaxf(h.mx[0][e], h.mx[1][e]), fmaxf(h.mx[2][e], h.mx[3][e]));
+              const float old = h.ref[e], need = ceilf(top * h.column[e].x);
+              const float now = top == -INFINITY ? old : old == -INFINITY || need > old + kLag ? need : old;
+              if (old != -INFINITY && now != old) factor = ex2(old - now);
+              h.ref[e] = now;
+              h.column[e].y = now == -INFINITY ? kUnset : kTop - now;
+            }
+            h.factor[e] = factor;
+          }
+          soft_sync(bar);
+#pragma unroll
+          for (int e = 0; e < kNC; ++e) l[e] *= h.factor[col0 + e];
+          columns();
+          if (j > 0) {   // the output as well
+            wait(&h.pv_done[buf ^ 1], (uint32_t)((g - 1) >> 1) & 1, abrt);
+            __syncwarp();
+            fence_after();
+#pragma unroll 1
+            for (int b = 0; b < NS; ++b) {
+              const uint32_t at = lanes + kOCol + (uint32_t)(16 * b + col0);
+              float o[kNC];
+              uint32_t w[kNC];
+              tmem_ld8_start(at, o);
+              tmem_ld_wait();
+              tmem_ld_done(o);
+#pragma unroll
+              for (int e = 0; e < kNC; ++e) w[e] = __float_as_uint(o[e] * h.factor[col0 + e]);
+              tmem_st8(at, w);
+            }
+            tmem_st_wait();
+          }
+        }
+        if (g >= 2) wait(&h.pv_done[buf], (uint32_t)((g - 2) >> 1) & 1, abrt);   // the buffer's weights have been used
+        uint8_t* const to = p_s + buf * kPBytes;
+        uint32_t w2[kNC / 2];
+#pragma unroll
+        for (int e = 0; e < kNC; e += 2) {
+          const float a = ex2(fmaf(z[e], k[e].x, k[e].y)), b = ex2(fmaf(z[e + 1], k[e + 1].x, k[e + 1].y));
+          l[e] += a;
+          l[e + 1] += b;
+          w2[e / 2] = pack_f16(a, b);
+        }
+#pragma unroll
+        for (int e = 0; e < kNC; ++e)   // (col0 is a multiple of 8)
+          *reinterpret_cast<uint16_t*>(to + (to_p ^ (e << 4)) + e * 128) = (uint16_t)(e & 1 ? w2[e / 2] >> 16 : w2[e / 2]);
+        fence_before();
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&h.p_full[buf]);
+      }
+      // The item's result, or this run's part of it.
+      const float part_sum = reduce_columns(l, lane, [](float a, float b) { return a + b; });
+      if ((lane & 3) == 0) h.sums[quarter][col0 + (lane >> 2)] = part_sum;
+      soft_sync(bar);
+      if (mine) {
+        const int e = col0 + me;
+        const float sum = (h.sums[0][e] + h.sums[1][e]) + (h.sums[2][e] + h.sums[3][e]);
+        h.inv[e] = sum == 0.f ? 0.f : 1.f / sum;   // (NaN stays)
+        const float lse2 = sum == 0.f ? -INFINITY : h.ref[e] - kTop + log2f(sum);
+        if (!whole) p.part_lse[h.to[e] / D] = lse2;
+        else if (p.lse) p.lse[h.to[e] / D] = lse2 * kLn2;
+      }
+      soft_sync(bar);
+      wait(&h.pv_done[(g - 1) & 1], (uint32_t)((g - 1) >> 1) & 1, abrt);
       __syncwarp();
-      if (lane == 0) bar_arrive(&h.empty[slot]);
-    }
-
-    // ---- the warps' parts of the item
-    l_lo += __shfl_xor_sync(0xffffffffu, l_lo, 1);
-    l_hi += __shfl_xor_sync(0xffffffffu, l_hi, 1);
-    l_lo += __shfl_xor_sync(0xffffffffu, l_lo, 2);
-    l_hi += __shfl_xor_sync(0xffffffffu, l_hi, 2);
-    if (t == 0) {
-      h.m[warp][n] = m_lo;
-      h.m[warp][n + 8] = m_hi;
-      h.l[warp][n] = l_lo;
-      h.l[warp][n + 8] = l_hi;
-    }
-    named_sync(1, 32 * kWarps);
-    float top_lo = -INFINITY, top_hi = -INFINITY;
+      fence_after();
+      const bool f32 = !whole || p.out_dtype == QSA_F32;
+      float* const to32 = (whole ? static_cast<float*>(p.out) : p.part_o) + channel;
+      __nv_bfloat16* const to16 = static_cast<__nv_bfloat16*>(p.out) + channel;
+      float o[NS][kNC];
 #pragma unroll
-    for (int w = 0; w < L::kPairs; ++w) {
-      top_lo = fmaxf(top_lo, h.m[H * w][n]);
-      top_hi = fmaxf(top_hi, h.m[H * w][n + 8]);
-    }
-    const float f_lo = m_lo == -INFINITY ? 1.f : ex2(m_lo - top_lo), f_hi = m_hi == -INFINITY ? 1.f : ex2(m_hi - top_hi);
-    // 128 H threads join: row jr, four channels from jc on of half jh, of a block a pass.
-    const int jr = (tid >> 3) & 15, jc = 4 * (tid & 7), jh = tid >> 7;
-    const bool joins = jh < H && jr < ir.nf;
-    float l = 0.f, top = -INFINITY;
+      for (int b = 0; b < NS; ++b) tmem_ld8_start(lanes + kOCol + (uint32_t)(16 * b + col0), o[b]);
+      tmem_ld_wait();
 #pragma unroll
-    for (int w = 0; w < L::kPairs; ++w) top = fmaxf(top, h.m[H * w][jr]);
+      for (int b = 0; b < NS; ++b) tmem_ld_done(o[b]);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float mw = h.m[w][jr];
-      l += h.l[w][jr] * (mw == -INFINITY ? 1.f : ex2(mw - top));   // (no weights: 0, or NaN)
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const bool whole = c.whole();
-    const int64_t part = (int64_t)c.slot(blockIdx.x) * kMT + jr;
-    const int fr = ir.f0 + min(jr, ir.nf - 1), rr = row_of(p, fr);
-    const int64_t entry = (int64_t)(c.s.row0 + rr) * p.n_q_heads + c.head * p.group + (fr - rr * p.group);
+      for (int e = 0; e < kNC; ++e) {
+        if (col0 + e >= ir.nf) break;
+        const float inv = h.inv[col0 + e];
+        const int64_t at = h.to[col0 + e];
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      if (g > 0) named_sync(1, 32 * kWarps);
-      // The block's minima's sums are column g: with the thread g / 2 of the row's four.
-      const int from = (lane & ~3) | (g >> 1);
-      const float mlo = __shfl_sync(0xffffffffu, om[g & 1], from), mhi = __shfl_sync(0xffffffffu, om[2 + (g & 1)], from);
-      float v[2][8];
-#pragma unroll
-      for (int jj = 0; jj < 4; ++jj) {
-        const float s = jj & 1 ? 0x1p20f : 0x1p24f;
-        v[0][jj] = fmaf(o[g][jj][0], s, mlo) * f_lo;
-        v[0][4 + jj] = fmaf(o[g][jj][1], s, mlo) * f_lo;
-        v[1][jj] = fmaf(o[g][jj][2], s, mhi) * f_hi;
-        v[1][4 + jj] = fmaf(o[g][jj][3], s, mhi) * f_hi;
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float4* to = reinterpret_cast<float4*>(join_s + (warp * kMT + n + 8 * i) * L::kPitch + 8 * t);
-        to[0] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
-        to[1] = make_float4(v[i][4], v[i][5], v[i][6], v[i][7]);
-      }
-      named_sync(1, 32 * kWarps);
-      if (joins) {
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < L::kPairs; ++w) {
-          const float4 x = *reinterpret_cast<const float4*>(join_s + ((H * w + jh) * kMT + jr) * L::kPitch + jc);
-          sum = make_float4(sum.x + x.x, sum.y + x.y, sum.z + x.z, sum.w + x.w);
-        }
-        const int d = 128 * jh + 32 * g + jc;
-        sum = make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
-        if (!whole) {
-          *reinterpret_cast<float4*>(p.part_o + part * D + d) = sum;
-        } else if (p.out_dtype == QSA_F32) {
-          *reinterpret_cast<float4*>(static_cast<float*>(p.out) + entry * D + d) = sum;
-        } else {
-          const __nv_bfloat162 lo = __floats2bfloat162_rn(sum.x, sum.y), hi = __floats2bfloat162_rn(sum.z, sum.w);
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + entry * D + d) =
-              make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        for (int b = 0; b < NS; ++b) {
+          if (f32) to32[at + 32 * b] = o[b][e] * inv;
+          else to16[at + 32 * b] = __float2bfloat16_rn(o[b][e] * inv);
         }
       }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(&h.o_free);
+      soft_sync(bar);   // the columns are the next item's
+      ++it;
+      more = c.next(p, p.mt);
+      if (!more && tid == 32 * kSoftWarp) describe_part(p, c, h.start, blockIdx.x);   // (still at its last item)
     }
-    if (joins && jh == 0 && jc == 0) {
-      const float lse2 = l == 0.f ? -INFINITY : top - kTop + log2f(l);
-      if (!whole) p.part_lse[part] = lse2;
-      else if (p.lse) p.lse[entry] = lse2 * kLn2;
+  } else if (warp == kCopyWarp) {
+    // ------------------------------------------------------------ copies
+    // A lane a box of tokens: its K, V and records.  The table's entries come a warp's lanes
+    // at a time, the next ones while these are under way.
+    const int box = min(1 << p.page_shift, kHalfKeys), n_box = kHalfKeys / box, page_mask = (1 << p.page_shift) - 1;
+    const int per = 32 / n_box;   // slots of a look-up (4 boxes at most: 8 to 32)
+    const int my_box = lane % n_box, my_slot = lane / n_box;
+    int slot = 0, total = 0;
+    uint32_t use = 0;
+    int gt = 0;                   // tiles done
+    bool live = true;
+    for (bool more = true; more && live; more = c.next(p, p.mt)) {
+      const ItemRows ir = item_rows(p, c);
+      const int n = 2 * (c.x1 - c.x);   // slots
+      auto token_of = [&](int i, int b) { return c.tiles.token(c.x + (i >> 1)) + kHalfKeys * (i & 1) + b * box; };
+      auto wanted = [&](int t) {   // whether the box at token t holds a visible one
+        return t <= ir.last && (p.window == 0 || t + box - 1 > ir.first - p.window || t < p.n_sinks);
+      };
+      // -2: not wanted.
+      auto look_up = [&](int i) {
+        if (i >= n) return -2;
+        const int t = token_of(i, my_box);
+        if (!wanted(t)) return -2;
+        const int64_t s = (int64_t)t >> p.page_shift;
+        return s < p.table_ld ? max(__ldcg(p.table + c.seq * p.table_ld + s), -1) : -1;
+      };
+      int pages = look_up(my_slot);
+#pragma unroll 1
+      for (int i0 = 0; i0 < n && live; i0 += per) {
+        const int next = look_up(i0 + per + my_slot);
+#pragma unroll 1
+        for (int i = i0; i < min(i0 + per, n); ++i) {
+          if (use > 0 && !wait(&h.code_empty[slot], (use - 1) & 1, abrt)) live = false;
+          live = __all_sync(0xffffffffu, live);
+          if (!live) break;
+          const bool copies = lane < n_box;
+          int page = __shfl_sync(0xffffffffu, pages, (i - i0) * n_box + my_box);
+          const bool missing = copies && page != -2 && (uint32_t)page >= (uint32_t)p.n_pages;
+          if ((uint32_t)page >= (uint32_t)p.n_pages) page = p.n_pages;   // past the last page: zeros
+          const uint32_t bad = __reduce_or_sync(0xffffffffu, missing ? ((1u << (box / 16)) - 1u) << (lane * (box / 16)) : 0u);
+          if (missing) atomicAdd(&g_bad_pages, 1);
+          if (lane == 0) {
+            h.bad[gt & 15][i & 1] = (uint8_t)bad;
+            bar_expect_tx(&h.code_full[slot], L::kBytes);
+          }
+          __syncwarp();
+          if (copies) {
+            const uint32_t to = smem_addr(ring) + slot * L::kBytes;
+            const int token = token_of(i, lane) & page_mask;
+            tma_4d(to + lane * box * L::kRow, &qp.k, 0, token, c.head, page, &h.code_full[slot]);
+            tma_4d(to + L::kCodes + lane * box * L::kRow, &qp.v, 0, token, c.head, page, &h.code_full[slot]);
+            tma_4d(to + 2 * L::kCodes + lane * box * L::kRecord, &qp.r, 0, token, c.head, page, &h.code_full[slot]);
+          }
+          __syncwarp();
+          gt += i & 1;
+          ++total;
+          if (++slot == qp.n_slots) slot = 0, ++use;
+        }
+        pages = next;
+      }
     }
-    named_sync(1, 32 * kWarps);   // the statistics, Q and the buffers are the next item's
-    more = c.next(p, kMT);
-    if (!more && tid == 0) describe_part(p, c, h.start, blockIdx.x);
+    // Every copy has landed before the CTA ends: a lane a slot, the last one that went there.
+    if (lane < qp.n_slots && lane < total) {
+      const int last = total - 1 - (total - 1 - lane) % qp.n_slots;
+      bar_wait(&h.code_full[lane], (uint32_t)(last / qp.n_slots) & 1, &g_timeouts);
+    }
+  } else if (warp == kLogitWarp) {
+    // ------------------------------------------------------------ logits
+    // The whole warp walks through the tiles with values that are the same in all its
+    // lanes, and one lane issues.
+    const bool leader = elect_one();
+    // 32-bit accumulators, both K-major, M = 128, N = 16; E4M3 and f16 operands are both 0.
+    constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(kEntries >> 3) << 17) | (8u << 24);
+    const uint64_t q_desc = desc_sw128(q_s, 16, 1024);
+    constexpr uint32_t kSlab = L::kQSlab >> 4;
+    int g = 0, it = 0;
+    bool live = true;   // no wait of this CTA has given up: nothing is issued after one has
+    for (bool more = true; more; more = __shfl_sync(0xffffffffu, (int)c.next(p, p.mt), 0) != 0, ++it) {
+      const int T = __shfl_sync(0xffffffffu, c.x1 - c.x, 0);
+      live = __all_sync(0xffffffffu, wait(&h.q_full, (uint32_t)it & 1, abrt) && live);
+#pragma unroll 1
+      for (int j = 0; j < T; ++j, ++g) {
+        if (g > 0) live = __all_sync(0xffffffffu, wait(&h.s_empty, (uint32_t)(g - 1) & 1, abrt) && live);
+        live = __all_sync(0xffffffffu, wait(&h.k_full, (uint32_t)g & 1, abrt) && live);
+        fence_after();
+        if (leader && live) {
+#pragma unroll
+          for (int x = 0; x < G; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)   // both codes of q
+              mma_f8_ts(tmem + kSCol + 16u * x, tmem + kKCol + 8u * x, q_desc + (uint32_t)(NS * y + (x >> 2)) * kSlab + 2 * (x & 3),
+                        kIdesc, (uint32_t)y);
+          mma_f16_ts(tmem + kSCol + 16u * G, tmem + kMinCol, q_desc + 2 * NS * kSlab, kIdesc, 0u);
+          commit(&h.k_empty);
+          commit(&h.s_full);
+          if (j + 1 == T) commit(&h.q_free);
+        }
+        __syncwarp();
+      }
+    }
+    if (leader) commit(&h.mma_done);   // every MMA has completed before TMEM is released
+    __syncwarp();
+    bar_wait(&h.mma_done, 0u, &g_timeouts);
+  } else {
+    // ------------------------------------------------------------ Q
+    // Two E4M3 codes of each value (see above) and the sums of its blocks, a row's 16
+    // channels a lane, in the order of K's cells: of channels 8 i .. 8 i + 7 the bytes are
+    // 0, 2, 4, 6, 1, 3, 5, 7.  (The first item's with the warp that has no output to issue yet.)
+    constexpr int kLanes = D / 16, kRows = 32 / kLanes, kBatch = kEntries / (2 * kRows);
+    const int chunk = lane % kLanes;
+    auto queries = [&](int it, int first, int warps) {
+      const ItemRows ir = item_rows(p, c);
+      if (it > 0) wait(&h.q_free, (uint32_t)(it - 1) & 1, abrt);
+      __syncwarp();
+#pragma unroll 1
+      for (int r0 = first * kRows + lane / kLanes; r0 < kEntries; r0 += kBatch * warps * kRows) {
+        uint4 a[kBatch], b[kBatch];
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+          const int f = ir.f0 + min(r0 + x * warps * kRows, ir.nf - 1), r = row_of(p, f);
+          const int64_t entry = (int64_t)(c.s.row0 + r) * p.n_q_heads + c.head * p.group + (f - r * p.group);
+          const uint4* from = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + entry * D + 16 * chunk);
+          a[x] = __ldg(from);
+          b[x] = __ldg(from + 1);
+        }
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+          const int row = r0 + x * warps * kRows;
+          const uint32_t w[8] = {a[x].x, a[x].y, a[x].z, a[x].w, b[x].x, b[x].y, b[x].z, b[x].w};
+          uint32_t most = 0u;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) most = max(most, max((w[e] << 16) & 0x7fff0000u, w[e] & 0x7fff0000u));
+#pragma unroll
+          for (int o = kLanes / 2; o >= 1; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+          // 2^(exponent - 7), at least 2^-100: a row of smaller values keeps fewer bits.
+          const int e = max((int)(most >> 23) - 127 - 7, -100);
+          const float up = row < ir.nf ? __uint_as_float((uint32_t)(127 - e) << 23) : 0.f;
+          const bool odd = most >= 0x7f800000u;   // infinity or NaN: the row's logits are NaN
+          uint32_t hi[4], lo[4];
+          float sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {   // bytes 4 i .. 4 i + 3: words 4 (i / 2) on, their low halves or their high ones
+            float v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t x2 = w[4 * (i >> 1) + k];
+              v[k] = (i & 1 ? bf16_hi(x2) : bf16_lo(x2)) * up;
+              sum += v[k];
+            }
+            const uint32_t c0 = to_e4m3x2(v[0], v[1]), c1 = to_e4m3x2(v[2], v[3]);
+            const float2 d0 = from_e4m3x2(c0), d1 = from_e4m3x2(c1);
+            hi[i] = c0 | c1 << 16;
+            lo[i] = to_e4m3x2(v[0] - d0.x, v[1] - d0.y) | to_e4m3x2(v[2] - d1.x, v[3] - d1.y) << 16;
+            if (odd) hi[i] = lo[i] = 0x7f7f7f7fu;
+          }
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          const __half s_hi = __float2half_rn(odd ? __uint_as_float(0x7fffffffu) : sum), s_lo = __float2half_rn(sum - __half2float(s_hi));
+          const int swap = row & 7;
+          uint8_t* const to = q_s + row * 128;
+          *reinterpret_cast<uint4*>(to + (chunk >> 3) * L::kQSlab + (((chunk & 7) ^ swap) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(to + (NS + (chunk >> 3)) * L::kQSlab + (((chunk & 7) ^ swap) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          // Sums: the high halves of the blocks, their low ones, zeros (head_dim 128) up to 16.
+          uint8_t* const to_sum = to + 2 * NS * L::kQSlab;
+          const int block = chunk >> 1;
+          if ((chunk & 1) == 0) {
+            const int x0 = block, x1 = G + block;
+            *reinterpret_cast<__half*>(to_sum + (((x0 >> 3) ^ swap) << 4) + 2 * (x0 & 7)) = s_hi;
+            *reinterpret_cast<__half*>(to_sum + (((x1 >> 3) ^ swap) << 4) + 2 * (x1 & 7)) = s_lo;
+          } else if (D == 128 && block == 0) {
+            *reinterpret_cast<uint4*>(to_sum + ((1 ^ swap) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          if (chunk == 0) h.q[it & 3][row] = odd ? 1.f : __uint_as_float((uint32_t)(127 + e) << 23);
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      for (int x = warps; x <= 2 && lane == 0; ++x) {   // (two arrivals)
+        bar_arrive(&h.row_full[it & 3]);
+        bar_arrive(&h.q_full);
+      }
+    };
+    if (warp == kOutWarp) queries(0, 1, 2);
+    else
+      for (int it = 0, more = 1; more; more = c.next(p, p.mt), ++it) queries(it, 0, it == 0 ? 2 : 1);
+    if (warp == kOutWarp) {
+      // ---------------------------------------------------------- output
+      const bool leader = elect_one();
+      constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(kEntries >> 3) << 17) | (8u << 24);
+      const uint64_t p_desc = desc_sw128(p_s, 16, 1024);
+      int g = 0, it = 0;
+      bool live = true;
+      for (bool more = true; more; more = __shfl_sync(0xffffffffu, (int)c.next(p, p.mt), 0) != 0, ++it) {
+        const int T = __shfl_sync(0xffffffffu, c.x1 - c.x, 0);
+#pragma unroll 1
+        for (int j = 0; j < T; ++j, ++g) {
+          const int buf = g & 1;
+          live = __all_sync(0xffffffffu, wait(&h.p_full[buf], (uint32_t)(g >> 1) & 1, abrt) && live);
+          if (j == 0 && it > 0) live = __all_sync(0xffffffffu, wait(&h.o_free, (uint32_t)(it - 1) & 1, abrt) && live);
+#pragma unroll
+          for (int a = 0; a < 2; ++a) {
+            live = __all_sync(0xffffffffu, wait(&h.v_full[a][buf], (uint32_t)(g >> 1) & 1, abrt) && live);
+            fence_after();
+            if (leader && live) {
+#pragma unroll
+              for (int b = 0; b < NS; ++b)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                  mma_f16_ts(tmem + kOCol + 16u * b, tmem + kVCol + 128u * buf + 64u * b + 32u * a + 8u * x,
+                             p_desc + (uint32_t)(2 * buf + a) * (kPBytes >> 5) + 2 * x, kIdesc, (j | a | x) != 0 ? 1u : 0u);
+              commit(&h.v_empty[a][buf]);
+              if (a == 1) commit(&h.pv_done[buf]);
+            }
+            __syncwarp();
+          }
+        }
+      }
+      if (leader) commit(&h.mma_done);
+      __syncwarp();
+    }
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  if (warp == kLogitWarp) {
+    fence_after();
+    tmem_dealloc(tmem, kTmemCols);
   }
 }
 
@@ -755,15 +930,17 @@ bool encode_rows(CUtensorMap* map, const void* base, const PagedParams& p, int b
 
 template <int D>
 cudaError_t launch_d(const PagedParams& p, int grid, cudaStream_t st) {
-  using L = Layout<D>;
+  using L = Slot<D>;
   Q4Params qp{};
   qp.p = p;
-  if (!encode_rows(&qp.k, p.k, p, L::kRow, kKT, p.tok_stride / 2, p.head_stride / 2, p.page_stride / 2) ||
-      !encode_rows(&qp.v, p.v, p, L::kRow, kKT, p.tok_stride / 2, p.head_stride / 2, p.page_stride / 2) ||
-      !encode_rows(&qp.r, p.kv_scale, p, L::kRecord, kKT, p.s_tok_stride * L::kRecord, p.s_head_stride * L::kRecord,
+  if (!encode_rows(&qp.k, p.k, p, L::kRow, kHalfKeys, p.tok_stride / 2, p.head_stride / 2, p.page_stride / 2) ||
+      !encode_rows(&qp.v, p.v, p, L::kRow, kHalfKeys, p.tok_stride / 2, p.head_stride / 2, p.page_stride / 2) ||
+      !encode_rows(&qp.r, p.kv_scale, p, L::kRecord, kHalfKeys, p.s_tok_stride * L::kRecord, p.s_head_stride * L::kRecord,
                    p.s_page_stride * L::kRecord))
     return cudaErrorInvalidValue;
-  const size_t smem = (size_t)L::kFixed + (size_t)L::kSlots * L::kSlot;
+  constexpr int fixed = kHeadBytes + L::kQ + 2 * kPBytes;
+  qp.n_slots = std::min((kSmemLimit - fixed) / L::kBytes, kMaxSlots);
+  const size_t smem = (size_t)fixed + (size_t)qp.n_slots * L::kBytes;
   cudaError_t e = allow_dynamic_smem((const void*)paged_q4_kernel<D>, smem);
   if (e != cudaSuccess) return e;
   return launch_kernel(paged_q4_kernel<D>, dim3((unsigned)grid), dim3(kThreads), smem, st, 0u, qp);
