@@ -11,7 +11,7 @@
 //            tile's 128 keys.  A code is the E4M3 byte of code * 2^-9, subnormal or not:
 //            masks only, eight codes in three instructions.  q times a power of two that
 //            brings its row's largest magnitude to [2^7, 2^8) is the sum of two E4M3 codes,
-//            the second that of what the first leaves: exact for bf16's 8 bits from 2^-10 of
+//            the second that of what the first leaves: exact for bf16's 8 bits from 2^-9 of
 //            that largest on, off by at most 2^-10 (2^-17 of the largest) below.  A block's
 //            sum is a product of its own, kind::f8f6f4 with 32 of K, and the softmax, where a
 //            thread owns a key, adds the blocks up times their scales in 32 bits.  The
@@ -30,7 +30,18 @@
 // products, 18 the output's, 19 writes Q.  K, V and their records come through TMA, 64
 // keys a slot; boxes of pages without visible tokens are aimed past the last page, which
 // fills zeros without reading.  Every wait gives up after about two seconds (counted;
-// nothing more is issued then, and the CTA runs to its end).
+// nothing more is issued then, and the CTA runs to its end); its loop is out of line, as
+// warps that wait in the middle of the roles' code take issue slots and instruction cache
+// from those that expand (a ragged batch of 16 sequences 146 us so, 136 this way).
+//
+// What bounds it (us a call on one GB300, 24 query and 2 KV heads of 256): 16 sequences of
+// 4k to 262k tokens 136, where HBM needs 77 and the copies alone take 95.  The rest is
+// instructions, the two roles' side by side: without V's expansion 118, without the
+// softmax's arithmetic 125, without both 107.  (Warps that multiply the codes with mma.sync
+// and 12 warps' registers full of output took 162; K expanded to f16 like V 151; 16
+// expanding warps, at 64 registers, 163; one slab of V's cells for both parities 145.)  One
+// sequence of 65,536 tokens 29, of which 10 are the call's start, the joining launch and the
+// first tiles' way through the roles.
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 #include <math.h>
@@ -88,10 +99,10 @@ struct Head {
   uint32_t tmem;
   int abort;
   uint8_t bad[16][2];              // 16-token pieces of a tile's halves that have no page (fewer tiles are under way)
-  float q[4][kEntries];         // of an item's entries: the power of two that Q's row was divided by
+  float q[4][kEntries];            // of an item's entries: the power of two that Q's row was divided by
   alignas(16) float2 column[kEntries];   // weight = 2^(logit * x + y)
   float ref[kEntries], factor[kEntries], inv[kEntries];
-  int64_t to[kEntries];         // where the entry's outputs go, in elements
+  int64_t to[kEntries];            // where the entry's outputs go, in elements
   int pos[kEntries];
   float mx[4][kEntries], sums[4][kEntries];
   alignas(16) uint4 scale[4][kKT];   // of K's blocks, of the last tiles
