@@ -15,6 +15,12 @@
 // by shuffles; the codes' order in the row (16-bit unit n * (D / 32) + g holds
 // channels 32 g + 4 n .. + 3) gives each lane one 32-bit word of two units that two
 // other lanes hold.
+//
+// On one GB300: 2,048 rows of Q, K and V of 256 into a 4-bit cache 25 us, where HBM needs 9
+// (three rounds of dependent reads -- lengths and ranges, page, rows -- before the first
+// store, and 13 rows an SM in which to hide them); ragged prompts of 128 into an fp8 cache
+// 28.6 of 14.3 (48 with a row a CTA); 65,536 rows of 256 back out of 4 bits 33 of 26 (52 with
+// eight bytes of codes a lane); steps of a few rows 5.7 to 8.4, the host's call.
 #include <cuda_fp16.h>
 
 #include <algorithm>

@@ -1,5 +1,5 @@
 // Attention over a paged K/V cache on the 5th-generation tensor cores: bf16 and
-// fp8 caches (see qsa_paged.cuh for the division of the work into runs of key
+// fp8 caches, and 4-bit caches of more than 16 entries an item (see qsa_paged.cuh for the division of the work into runs of key
 // tiles, and qsa_paged.cu for the formulas and the joining launch).
 //
 // An item's MT <= 128 entries (query row, head of the KV head's group) are the
@@ -38,11 +38,19 @@
 // weights, which are rounded once.  (That step, from K through bf16 as well, took a
 // ragged batch of 16 sequences from 351 to 230 us; later ones to 172.)
 //
+// 4-bit caches: codes and records go through rings of their own, and eight warps write
+// them to the slabs as f16, code * scale + minimum rounded once, in the order that two
+// masks of a code word give (each 8 channels as 0, 4, 1, 5, 2, 6, 3, 7; Q in the same
+// order, and the output put back); Q is f16 times a power of two of each row (its largest
+// magnitude to [2^14, 2^15): exact from 2^-31 of that on, off by at most 2^-39 of it
+// below), and weights are f16 with 2^7 at the maximum, so that 2^15 is the largest.
+//
 // Roles: warps 0-7 softmax and output, warps 8 and 10 copy K and V, warp 9 issues
 // the MMAs; bf16: warp 11 copies Q and clears V's ends; fp8: warps 12-15 write Q's
 // codes and the scales and convert V, with those of warps 0-7 that have no
-// entries.  Every wait gives up after about two seconds (counted; nothing more is
-// issued then, and the CTA runs to its end).
+// entries; 4-bit: warps 12-19 write Q, K and V, and registers move from the copying warps
+// to the softmax's.  Every wait gives up after about two seconds (counted; nothing more
+// is issued then, and the CTA runs to its end).
 //
 // What bounds it (us a call on one GB300, floor at the measured 6,791 GB/s and
 // 1,941 TFLOP/s): few rows, the K/V bytes -- 261,120 tokens x 4 rows 89 of 79; the
@@ -52,7 +60,12 @@
 // 4,096-token window (256) 170 of 108, the shared memory's 128 bytes a cycle, which
 // Q and K take whole in the logits' product (2,700 cycles a tile where the products
 // alone take 2,048).  fp8: 170 of 115, shared memory too: the products, V's conversion
-// and the scales pass over it 3,200 cycles a tile where HBM needs 2,800.
+// and the scales pass over it 3,200 cycles a tile where HBM needs 2,800.  4-bit: 2,048
+// rows over 16k tokens 402 of 199 (bf16: 292): expanding 256 values a thread and tile beside the
+// softmax (without its arithmetic 300 to 312); 261,120 tokens x 4 rows 90 of 25, shared
+// memory, over which Q, the expanded values twice and the codes pass 2,900 cycles a tile,
+// and slabs for one tile only, so that expanding and products take turns (without the
+// arithmetic 68).
 #include <math.h>
 
 #include <cuda_fp16.h>

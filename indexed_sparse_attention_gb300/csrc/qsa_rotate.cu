@@ -6,7 +6,9 @@
 // heads; a thread then takes jobs of two 16-byte pieces, the two that a rotation joins,
 // so that nothing is exchanged, four of them in flight.  Each value is read and written
 // once; the bound is HBM for a prompt's rows and the launch with a chain of three
-// dependent steps (position, angles, rows) for a step's.
+// dependent steps (position, angles, rows) for a step's.  On one GB300 16,384 rows of 24
+// heads of 256, in and out, take 64.6 us (6.2 TB/s of the 6.7 that a copy reaches; 76 with
+// a row a CTA), a step's 64 rows the 6.7 us of the host's call.
 #include <math.h>
 
 #include <algorithm>
