@@ -70,7 +70,7 @@ constexpr int kMaxSlots = 20;
 constexpr int kSmemLimit = 227 * 1024;
 constexpr float kTop = 7.f;              // log2 of the weight at the reference
 constexpr float kLag = 8.f;              // log2 of what a weight may pass it by
-constexpr float kUnset = 1e38f;          // shift of a column that has seen no logit: any finite one passes it
+constexpr float kUnset = 3.402823466e38f; // shift of a column that has seen no logit: any finite one passes it
 constexpr uint32_t kTmemCols = 512;
 // TMEM columns: logits (16 a block, then the minima's), the minima, the output's two slabs, K's codes, two buffers
 // of V's values.

@@ -158,9 +158,10 @@ class PagedCache:
     def _call_config(self, n_q_heads: int, out_dtype, scale: float, n_splits: int) -> AttnConfig:
         """config() of the last call, while calls ask for the same."""
         key = (n_q_heads, out_dtype, scale, n_splits)
-        if self._last_call[0] != key:
-            self._last_call = key, self.config(n_q_heads, out_dtype, scale, n_splits)
-        return self._last_call[1]
+        last = self._last_call   # (one read: other threads may call, too)
+        if last[0] != key:
+            last = self._last_call = key, self.config(n_q_heads, out_dtype, scale, n_splits)
+        return last[1]
 
 
 class PagedBatch:
@@ -317,7 +318,7 @@ class PagedStep:
 
     With a rope, q holds the queries before their rotation (a slice of the projection
     that the new rows are slices of will do), append rotates K and them, these into
-    the step's q_rotated, and attend takes that."""
+    the step's q_rotated, and attend takes that; run then needs the new rows."""
 
     def __init__(self, cache: PagedCache, batch: PagedBatch, q: torch.Tensor, *, out_dtype=torch.float32,
                  window: int = 0, n_sinks: int = 0, scale: float = 0.0, n_splits: int = 0, rope: Rope | None = None):
@@ -349,6 +350,8 @@ class PagedStep:
 
     def run(self, k_new: torch.Tensor | None = None, v_new: torch.Tensor | None = None, stream=None):
         """Append (when given new rows), then attend."""
+        if k_new is None and self.rope is not None:
+            raise ValueError("a step with a rope rotates q as it appends: give run the new rows, or call attend")
         if k_new is not None:
             self.append(k_new, v_new, stream)
         return self.attend(stream)

@@ -119,6 +119,19 @@ def test_rows_that_see_nothing_and_rows_of_nobody():
 
 
 @pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("most", [1, 2])
+def test_more_rows_than_promised(D, most):
+    # Items then end inside a row's heads (16 entries of 12 heads), or there are several of whole rows.
+    x = make_paged4([400, 90, 33], [5, 1, 33], D=D, Hkv=2, G=12, page=32, seed=25)
+    cache, batch, q = x.device()
+    batch = qsa.PagedBatch(batch.table, batch.lens, batch.row_start, n_rows=q.shape[0], max_rows=most)
+    for window, sinks in ((0, 0), (20, 3)):
+        out, lse = torch.empty(q.shape, device=dev()), torch.empty(q.shape[:2], device=dev())
+        qsa.paged_attn(cache, batch, q, out, lse, window=window, n_sinks=sinks)
+        assert_attended(out, lse, attend4(x, window, sinks, most=most))
+
+
+@pytest.mark.parametrize("D", [128, 256])
 @pytest.mark.parametrize("rows", [[1, 1, 1], [4, 1, 2]])
 def test_divisions_agree_and_repeat(D, rows):
     x = make_paged4([3000, 70, 900], rows, D=D, page=64, seed=7)
@@ -218,15 +231,7 @@ def test_scales_of_any_size(D, rows):
     for t, s in ((7, 4000.0), (123, 3000.0), (400, -4000.0)):
         rec[x.table[0, t // 32], 0, t % 32, 1, 2, 0] = s
     x.scale = rec.half().view(x.scale.shape)
-    # The weights are kept to 2^-11 of their own (see q4_cases) and to 2^-27 of the largest, less what the largest
-    # scale that a row's run has met takes off them: less than 2^11.
-    out, lse, otol, ltol = attend4(x)
-    V = max(float((c * s).abs().max()) for i in range(3) for c, s, _ in [x.seq_parts(i)[1]])
-    big = torch.zeros_like(otol)
-    for i, (n, r) in enumerate(zip(x.lens, x.rows)):
-        big[int(x.row_start[i]):int(x.row_start[i]) + r] = n * 2.0 ** -16 * (15 + (V / 15 if i == 0 else 1) * 2.0 ** -11)
-    got, got_lse = run(x)
-    assert_attended(got, got_lse, (out, lse, otol + big, ltol))
+    check(x)
 
 
 def test_logits_that_climb():
@@ -455,3 +460,15 @@ def test_a_serving_run_with_rotation(D, window, sinks, rot, pairs):
     pool.compact()
     step([1, 1, 0, 20, 2])
     assert qsa.check_device_status() == (0, "")
+
+
+def test_a_step_with_a_rope_takes_new_rows():
+    x = make_paged4([40], [1], D=128, page=16, seed=26)
+    cache, batch, q = x.device()
+    st = qsa.PagedStep(cache, batch, q, rope=qsa.Rope(64))
+    with pytest.raises(ValueError, match="new rows"):
+        st.run()
+    rows = torch.zeros(1, cache.n_kv_heads, 128, dtype=torch.bfloat16, device=dev())
+    out, lse = st.run(rows, rows)
+    again, lse2 = (t.clone() for t in (out, lse))
+    assert torch.equal(st.attend()[0], again) and torch.equal(lse, lse2)
