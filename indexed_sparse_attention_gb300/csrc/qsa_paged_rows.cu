@@ -16,11 +16,12 @@
 // channels 32 g + 4 n .. + 3) gives each lane one 32-bit word of two units that two
 // other lanes hold.
 //
-// On one GB300: 2,048 rows of Q, K and V of 256 into a 4-bit cache 25 us, where HBM needs 9
-// (three rounds of dependent reads -- lengths and ranges, page, rows -- before the first
-// store, and 13 rows an SM in which to hide them); ragged prompts of 128 into an fp8 cache
-// 28.6 of 14.3 (48 with a row a CTA); 65,536 rows of 256 back out of 4 bits 33 of 26 (52 with
-// eight bytes of codes a lane); steps of a few rows 5.7 to 8.4, the host's call.
+// On one GB300: 2,048 rows of Q, K and V of 256 into a 4-bit cache, and the rows read
+// back, 22.9 us, where HBM needs 9 (dependent reads -- lengths and ranges, page -- before
+// the first store, and 13 rows an SM in which to hide them); ragged prompts of 128 into an
+// fp8 cache 27.3 of 14.3 (44 with a row a CTA; 20 were the sequences known); 65,536 rows of
+// 256 back out of 4 bits 33 of 26 (52 with eight bytes of codes a lane); steps of a few
+// rows 5.7 to 8.7, the host's call.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -148,8 +149,11 @@ __device__ __forceinline__ void store_q4(const PagedAppendParams& p, const uint3
   uint32_t codes = 0u;   // 4 bits a channel
 #pragma unroll
   for (int k = 0; k < PER; ++k) {
-    // (A scale that is 0 or NaN leaves code 0.)
-    const float c = s > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(x[k] - m, s)), 0.f), 15.f) : 0.f;
+    // (A scale that is 0 or NaN leaves code 0; so do differences that are not above 0, which
+    // are not divided: every block has one that is 0, and a division of 0 takes ten times as
+    // long.)
+    const float d = x[k] - m;
+    const float c = s > 0.f && d > 0.f ? fminf(rintf(__fdiv_rn(d > 0.f ? d : s, s)), 15.f) : 0.f;
     codes |= (uint32_t)c << (4 * k);
   }
   // 32-bit word w of the row: units 2 w and 2 w + 1, of blocks g and g + 1 and the same n.
@@ -219,41 +223,46 @@ __global__ void __launch_bounds__(kThreads, 4) paged_rows_kernel(const __grid_co
   const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r0 = (int)blockIdx.x * p.rows, rows = min(p.rows, a.n_rows - r0);
   const int q_heads = p.q ? p.n_q_heads : 0;
-  // Job i of the rows: Q's heads of a row, then (rows stored as they are) K's and V's, then the next row.
-  const int jobs = (q_heads + (QUANT ? 0 : 2 * a.n_kv_heads)) * J, all = rows * jobs;
-  auto row_of_job = [&](int i) { return p.rows == 1 ? 0 : i / jobs; };
-  auto source = [&](int r, int hh) {
-    if (hh < q_heads) return static_cast<const char*>(p.q) + (r * p.q_row_stride + hh * p.q_head_stride) * ES;
-    const int hv = hh - q_heads, which = hv >= a.n_kv_heads, h = which ? hv - a.n_kv_heads : hv;
-    return static_cast<const char*>(which ? a.v_new : a.k_new) + (r * a.row_stride + h * a.new_head_stride) * ES;
+  // A row is 256, 128 or 64 threads' (rows of a CTA are a power of two).  Its heads -- Q's,
+  // then those of rows stored as they are, K's and V's -- are J jobs each, of which a
+  // thread takes the same one of every `step`th head: its pieces and angles stay the same.
+  const int row_shift = p.rows == 1 ? 8 : p.rows == 2 ? 7 : 6, per = 1 << row_shift;
+  const int my = tid >> row_shift, t = tid & (per - 1);
+  const int h0 = t / J, j = t % J, step = per / J;
+  const int heads = my < rows ? q_heads + (QUANT ? 0 : 2 * a.n_kv_heads) : 0;
+  const int64_t r = (int64_t)r0 + my;
+  const rope::Job job = rope::job_of<ES>(p.rope.rot_dim, p.rope.pairs, j);
+  const char* const q_row = static_cast<const char*>(p.q) + r * p.q_row_stride * ES;
+  auto source = [&](int h) {
+    if (h < q_heads) return q_row + h * p.q_head_stride * ES;
+    const int hv = h - q_heads, v = hv >= a.n_kv_heads;
+    return static_cast<const char*>(v ? a.v_new : a.k_new) + (r * a.row_stride + (v ? hv - a.n_kv_heads : hv) * a.new_head_stride) * ES;
   };
-  constexpr int kAhead = 3;
+  constexpr int kAhead = 2;   // (3 spill)
   uint4 x0[kAhead], x1[kAhead];
-  auto load = [&](int i0) {
+  auto load = [&](int from) {
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const int i = i0 + k * kThreads;
-      if (i >= all) continue;
-      const int r = row_of_job(i), jj = i - r * jobs;
-      const rope::Job b = rope::job_of<ES>(p.rope.rot_dim, p.rope.pairs, jj % J);
-      const char* from = source(r0 + r, jj / J);
-      x0[k] = *reinterpret_cast<const uint4*>(from + 16 * b.p0);
-      x1[k] = *reinterpret_cast<const uint4*>(from + 16 * b.p1);
+      const int h = from + k * step;
+      if (h >= heads) break;
+      const uint4* const x = reinterpret_cast<const uint4*>(source(h));
+      x0[k] = x[job.p0];
+      x1[k] = x[job.p1];
     }
   };
-  // Rows that are quantized, a warp each: unit w of the rows is K or V of a head of a row.
-  const int units = QUANT ? rows * 2 * a.n_kv_heads : 0;
+  // Rows that are quantized, a warp each: unit w of the row is K or V of a head.
+  const int units = QUANT && my < rows ? 2 * a.n_kv_heads : 0, unit0 = t >> 5, unit_step = per >> 5;
   uint32_t u[QUANT ? D / 64 : 1];
   auto load_row = [&](int w) {
-    const int r = w / (2 * a.n_kv_heads), hv = w - r * 2 * a.n_kv_heads;
-    const int which = hv >= a.n_kv_heads, h = which ? hv - a.n_kv_heads : hv;
-    if constexpr (QUANT)
-      load_lane<D>(static_cast<const __nv_bfloat16*>(which ? a.v_new : a.k_new) + (r0 + r) * a.row_stride +
-                       h * a.new_head_stride + lane * (D / 32),
+    if constexpr (QUANT) {
+      const int v = w >= a.n_kv_heads;
+      load_lane<D>(static_cast<const __nv_bfloat16*>(v ? a.v_new : a.k_new) + r * a.row_stride +
+                       (v ? w - a.n_kv_heads : w) * a.new_head_stride + lane * (D / 32),
                    u);
+    }
   };
-  if (warp < units) load_row(warp);
-  load(tid);
+  if (unit0 < units) load_row(unit0);
+  load(h0);
   // A warp a row: its sequence and position; its page arrives while the angles are computed.
   int64_t page = -2;
   int32_t id = 0;
@@ -261,17 +270,17 @@ __global__ void __launch_bounds__(kThreads, 4) paged_rows_kernel(const __grid_co
     int pos = 0;
     const int seq = warp_sequence(a, r0 + warp, lane, pos);
     if (seq >= 0) {
-      const int64_t j = pos >> a.page_shift;
+      const int64_t at = pos >> a.page_shift;
       page = pos >= 0 ? 0 : -1;
-      id = pos >= 0 && j < a.table_ld ? __ldcg(a.table + seq * a.table_ld + j) : -1;
+      id = pos >= 0 && at < a.table_ld ? __ldcg(a.table + seq * a.table_ld + at) : -1;
     }
     if (lane == 0) pos_s[warp] = pos;
   }
   __syncthreads();
   const int half = p.rope.rot_dim / 2;
-  for (int i = tid; i < rows * half; i += kThreads) {
-    const int r = i / half, k = i - r * half;
-    cs[r][rope::cs_at<ES>(p.rope.rot_dim, k)] = rope::turn(p.rope, k, pos_s[r]);
+  if (my < rows) {
+    const int pos = pos_s[my];
+    for (int k = t; k < half; k += per) cs[my][rope::cs_at<ES>(p.rope.rot_dim, k)] = rope::turn(p.rope, k, pos);
   }
   if (warp < rows && lane == 0) {
     if (page == 0) {
@@ -281,44 +290,45 @@ __global__ void __launch_bounds__(kThreads, 4) paged_rows_kernel(const __grid_co
     page_s[warp] = page;
   }
   __syncthreads();
-  const int page_mask = (1 << a.page_shift) - 1;
-  for (int i0 = tid; i0 < all; i0 += kAhead * kThreads) {
-    if (i0 != tid) load(i0);
+  if (my >= rows) return;
+  page = page_s[my];
+  if (page == -2) return;
+  const int64_t slot = pos_s[my] & ((1 << a.page_shift) - 1);
+  if (heads > 0) {
+    char* const q_to = static_cast<char*>(p.q_out) + r * q_heads * (D * ES);
+    const int64_t kv_to = (page * a.page_stride + slot * a.tok_stride) * ES;
+    for (int from = h0; from < heads; from += kAhead * step) {
+      if (from != h0) load(from);
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int i = i0 + k * kThreads;
-      if (i >= all) continue;
-      const int r = row_of_job(i), jj = i - r * jobs, hh = jj / J, j = jj % J;
-      const int64_t page = page_s[r];
-      if (page == -2) continue;
-      const rope::Job b = rope::job_of<ES>(p.rope.rot_dim, p.rope.pairs, j);
-      const int hv = hh - q_heads;
-      if (b.turns && hv < a.n_kv_heads) rope::rotate_job<ES>(x0[k], x1[k], p.rope.rot_dim, p.rope.pairs, j, cs[r]);
-      char* to;
-      if (hv < 0) {
-        to = static_cast<char*>(p.q_out) + ((int64_t)(r0 + r) * q_heads + hh) * (D * ES);
-      } else {
-        if (page < 0) continue;
-        const int which = hv >= a.n_kv_heads, h = which ? hv - a.n_kv_heads : hv;
-        to = static_cast<char*>(which ? a.v : a.k) +
-             (page * a.page_stride + h * a.head_stride + (pos_s[r] & page_mask) * a.tok_stride) * ES;
+      for (int k = 0; k < kAhead; ++k) {
+        const int h = from + k * step;
+        if (h >= heads) break;
+        const int hv = h - q_heads, v = hv >= a.n_kv_heads;
+        if (job.turns && hv < a.n_kv_heads) {
+          float2 angle[16 / ES];
+          rope::angles_of<ES>(p.rope.rot_dim, j, cs[my], angle);
+          rope::rotate_job<ES>(x0[k], x1[k], p.rope.pairs, angle);
+        }
+        char* to = q_to + h * (D * ES);
+        if (hv >= 0) {
+          if (page < 0) break;
+          to = static_cast<char*>(v ? a.v : a.k) + kv_to + (v ? hv - a.n_kv_heads : hv) * a.head_stride * ES;
+        }
+        reinterpret_cast<uint4*>(to)[job.p0] = x0[k];
+        reinterpret_cast<uint4*>(to)[job.p1] = x1[k];
       }
-      *reinterpret_cast<uint4*>(to + 16 * b.p0) = x0[k];
-      *reinterpret_cast<uint4*>(to + 16 * b.p1) = x1[k];
     }
   }
   if constexpr (QUANT) {
-    for (int w = warp; w < units; w += kWarps) {
-      if (w != warp) load_row(w);
-      const int r = w / (2 * a.n_kv_heads), hv = w - r * 2 * a.n_kv_heads;
-      const int64_t page = page_s[r], slot = pos_s[r] & page_mask;
-      if (page < 0) continue;
-      const int which = hv >= a.n_kv_heads, h = which ? hv - a.n_kv_heads : hv;
-      if (which == 0 && half > 0) rotate_lane<D>(u, p.rope, cs[r], lane);
-      const int64_t at = page * a.page_stride + h * a.head_stride + slot * a.tok_stride;
-      const int64_t record = page * a.s_page_stride + h * a.s_head_stride + slot * a.s_tok_stride;
-      if constexpr (STATE == QSA_Q4_1) store_q4<D>(a, u, which, at / 2, record, lane);
-      else store_fp8<D>(a, u, which, at, record, lane);
+    if (page < 0) return;
+    const int64_t row = page * a.page_stride + slot * a.tok_stride, record = page * a.s_page_stride + slot * a.s_tok_stride;
+    for (int w = unit0; w < units; w += unit_step) {
+      if (w != unit0) load_row(w);
+      const int v = w >= a.n_kv_heads, h = v ? w - a.n_kv_heads : w;
+      if (!v && half > 0) rotate_lane<D>(u, p.rope, cs[my], lane);
+      const int64_t at = row + h * a.head_stride, rec = record + h * a.s_head_stride;
+      if constexpr (STATE == QSA_Q4_1) store_q4<D>(a, u, v, at / 2, rec, lane);
+      else store_fp8<D>(a, u, v, at, rec, lane);
     }
   }
 }

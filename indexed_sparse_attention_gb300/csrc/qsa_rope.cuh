@@ -87,16 +87,20 @@ __device__ __forceinline__ int cs_at(int rot_dim, int pair) {
   constexpr int E = 16 / ES;
   return pair % E * (rot_dim / (2 * E)) + pair / E;
 }
-// Rotates job j's pieces in place; cs: the row's (cos, sin).
+// Those of job j's pairs.
 template <int ES>
-__device__ __forceinline__ void rotate_job(uint4& x0, uint4& x1, int rot_dim, int pairs, int j, const float2* cs) {
+__device__ __forceinline__ void angles_of(int rot_dim, int j, const float2* cs, float2 (&t)[16 / ES]) {
+  constexpr int E = 16 / ES;
+#pragma unroll
+  for (int e = 0; e < E; ++e) t[e] = cs[e * (rot_dim / (2 * E)) + j];
+}
+// Rotates a job's pieces in place.
+template <int ES>
+__device__ __forceinline__ void rotate_job(uint4& x0, uint4& x1, int pairs, const float2 (&t)[16 / ES]) {
   constexpr int E = 16 / ES;
   float a[E], b[E], c[E], d[E];
   open<ES>(x0, a);
   open<ES>(x1, b);
-  float2 t[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) t[e] = cs[e * (rot_dim / (2 * E)) + j];
   if (pairs) {
 #pragma unroll
     for (int e = 0; e < E / 2; ++e) {

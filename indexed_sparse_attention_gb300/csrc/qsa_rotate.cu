@@ -90,7 +90,11 @@ __global__ void __launch_bounds__(kThreads, 4) rotate_kernel(const __grid_consta
       const Place a = place(i);
       const rope::Job b = rope::job_of<ES>(p.rope.rot_dim, p.rope.pairs, a.j);
       if (p.in_place && !b.turns) continue;
-      if (b.turns) rope::rotate_job<ES>(x0[k], x1[k], p.rope.rot_dim, p.rope.pairs, a.j, cs[a.r]);
+      if (b.turns) {
+        float2 angle[16 / ES];
+        rope::angles_of<ES>(p.rope.rot_dim, a.j, cs[a.r], angle);
+        rope::rotate_job<ES>(x0[k], x1[k], p.rope.pairs, angle);
+      }
       char* to = static_cast<char*>(p.y) + (r0 + a.r) * p.y_row + a.h * p.y_head;
       __stcs(reinterpret_cast<uint4*>(to) + b.p0, x0[k]);
       __stcs(reinterpret_cast<uint4*>(to) + b.p1, x1[k]);
