@@ -353,10 +353,10 @@ __global__ void __launch_bounds__(kThreads) paged_read_kernel(const __grid_const
   const PagedAppendParams& a = p.a;
   grid_dependency_sync();
   const int lane = (int)threadIdx.x & 31;
-  const int r0 = ((int)blockIdx.x * kWarps + ((int)threadIdx.x >> 5)) * p.rows_warp;
+  const int64_t r0 = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * p.rows_warp;
   // This lane's row.
   int64_t page = -1, slot = 0;
-  const int mine = r0 + lane;
+  const int64_t mine = r0 + lane;
   if (lane < p.rows_warp && mine < a.n_rows) {
     int lo = 0, hi = a.n_seqs;   // the sequences that end at or before it: found in [lo, hi]
     while (lo < hi) {
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kThreads) paged_read_kernel(const __grid_const
       else hi = mid;
     }
     if (lo < a.n_seqs && mine >= __ldcg(a.row_start + lo)) {
-      const int pos = max(__ldcg(a.lens + lo), 0) - (min(__ldcg(a.row_start + lo + 1), a.n_rows) - mine);
+      const int pos = max(__ldcg(a.lens + lo), 0) - (min(__ldcg(a.row_start + lo + 1), a.n_rows) - (int)mine);
       if (pos >= 0) {
         const int64_t j = pos >> a.page_shift;
         const int32_t id = j < a.table_ld ? __ldcg(a.table + lo * a.table_ld + j) : -1;
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kThreads) paged_read_kernel(const __grid_const
   }
   // Units: K or V of a head of a row.  LU lanes share one, 32 / LU at a time.
   constexpr int LU = STATE == QSA_Q4_1 ? D / 32 : 32, UW = 32 / LU;
-  const int n = min(p.rows_warp, a.n_rows - r0), each = 2 * a.n_kv_heads, all = n * each;
+  const int n = (int)min((int64_t)p.rows_warp, a.n_rows - r0), each = 2 * a.n_kv_heads, all = n * each;
   const int sub = lane / LU, li = lane % LU;
   constexpr int kAhead = 2;   // units of a lane in flight
 #pragma unroll 1
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kThreads) paged_read_kernel(const __grid_const
       const int64_t at = pg * a.page_stride + h * a.head_stride + sl * a.tok_stride;
       const int64_t record = pg * a.s_page_stride + h * a.s_head_stride + sl * a.s_tok_stride;
       const char* from = static_cast<const char*>(which ? a.v : a.k);
-      to[k] = static_cast<OUT*>(which ? p.v_out : p.k_out) + ((int64_t)(r0 + i) * a.n_kv_heads + h) * D;
+      to[k] = static_cast<OUT*>(which ? p.v_out : p.k_out) + ((r0 + i) * a.n_kv_heads + h) * D;
       if constexpr (STATE == QSA_Q4_1) {
         w[k][0] = __ldcs(reinterpret_cast<const uint4*>(from + at / 2) + li);
         const uint4* rec = reinterpret_cast<const uint4*>(static_cast<const char*>(a.kv_scale) + record * (D / 4) + which * (D / 8));
@@ -460,14 +460,14 @@ cudaError_t launch_rows(PagedRowsParams p, cudaStream_t st) {
   // As many rows a CTA as leave eight CTAs for every SM.
   p.rows = 1;
   while (p.rows < kMaxRows && p.a.n_rows > 8 * device_sm_count() * p.rows) p.rows *= 2;
-  const dim3 grid((unsigned)((p.a.n_rows + p.rows - 1) / p.rows)), block(kThreads);
+  const dim3 grid((unsigned)(((int64_t)p.a.n_rows + p.rows - 1) / p.rows)), block(kThreads);
   return p.a.head_dim == 256 ? launch_kernel(paged_rows_kernel<STATE, 256>, grid, block, 0, st, 0u, p)
                              : launch_kernel(paged_rows_kernel<STATE, 128>, grid, block, 0, st, 0u, p);
 }
 
 template <int STATE, typename OUT>
 cudaError_t launch_read(const PagedReadParams& p, cudaStream_t st) {
-  const dim3 grid((unsigned)((p.a.n_rows + kWarps * p.rows_warp - 1) / (kWarps * p.rows_warp))), block(kThreads);
+  const dim3 grid((unsigned)(((int64_t)p.a.n_rows + kWarps * p.rows_warp - 1) / (kWarps * p.rows_warp))), block(kThreads);
   return p.a.head_dim == 256 ? launch_kernel(paged_read_kernel<STATE, 256, OUT>, grid, block, 0, st, 0u, p)
                              : launch_kernel(paged_read_kernel<STATE, 128, OUT>, grid, block, 0, st, 0u, p);
 }

@@ -223,7 +223,7 @@ QSA_API qsa_status qsa_rotate(const qsa_rope* rope, const int32_t* positions, in
   // As many rows a CTA as leave eight CTAs for every SM, and no more than its threads have work for.
   p.rows = 1;
   while (p.rows < kMaxRows && n_rows > 8 * device_sm_count() * p.rows && p.rows * p.jobs < 4 * kThreads) p.rows *= 2;
-  const dim3 grid((unsigned)((n_rows + p.rows - 1) / p.rows)), block(kThreads);
+  const dim3 grid((unsigned)(((int64_t)n_rows + p.rows - 1) / p.rows)), block(kThreads);
   const cudaError_t e = dtype == QSA_F32 ? launch_kernel(rotate_kernel<4>, grid, block, 0, as_stream(stream), 0u, p)
                                          : launch_kernel(rotate_kernel<2>, grid, block, 0, as_stream(stream), 0u, p);
   return e == cudaSuccess ? ok() : cuda_fail(e, fn);
