@@ -25,23 +25,24 @@
 // are reduced and O and the sums rescaled.  Weights are f16 with 2^7 at the reference, so
 // 2^15 is the largest.
 //
-// Roles (20 warps): 0-7 expand codes (four warps a half of K's channels, and of V's keys),
-// 8-15 softmax and output (a warpgroup eight columns), 16 copies, 17 issues the logits'
-// products, 18 the output's, 19 writes Q.  K, V and their records come through TMA, 64
+// Roles (16 warps): 0-7 expand codes (four warps a half of K's channels, and of V's keys),
+// 8-11 softmax and output, 12 copies, 13 issues the logits' products, 14 the output's, 15
+// writes Q.  K, V and their records come through TMA, 64
 // keys a slot; boxes of pages without visible tokens are aimed past the last page, which
 // fills zeros without reading.  Every wait gives up after about two seconds (counted;
 // nothing more is issued then, and the CTA runs to its end); its loop is out of line, as
 // warps that wait in the middle of the roles' code take issue slots and instruction cache
-// from those that expand (a ragged batch of 16 sequences 146 us so, 136 this way).
+// from those that expand (a ragged batch of 16 sequences took 146 us so, and 136 this way).
 //
 // What bounds it (us a call on one GB300, 24 query and 2 KV heads of 256): 16 sequences of
-// 4k to 262k tokens 136, where HBM needs 77 and the copies alone take 95.  The rest is
-// instructions, the two roles' side by side: without V's expansion 118, without the
-// softmax's arithmetic 125, without both 107.  (Warps that multiply the codes with mma.sync
-// and 12 warps' registers full of output took 162; K expanded to f16 like V 151; 16
-// expanding warps, at 64 registers, 163; one slab of V's cells for both parities 145.)  One
-// sequence of 65,536 tokens 29, of which 10 are the call's start, the joining launch and the
-// first tiles' way through the roles.
+// 4k to 262k tokens 127, where HBM needs 77 and the copies alone take 95.  The rest is
+// instructions, the expansion's and the softmax's side by side: with the softmax on two
+// warpgroups of eight columns, which does more work, 136 -- then 118 without V's expansion,
+// 125 without the softmax's arithmetic, 107 without both.  (Codes multiplied with mma.sync by
+// 12 warps whose registers are full of output took 162; K expanded to f16 like V 151; 16
+// expanding warps, at 64 registers, 163; 12, four of them for K, 140; one buffer of V's cells
+// 145.)  One sequence of 65,536 tokens 28, of which 10 are the call's start, the joining launch
+// and the first tiles' way through the roles.
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 #include <math.h>
@@ -63,9 +64,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kKT = 128;                 // keys of a tile
 constexpr int kHalfKeys = 64;            // of a slot, and of a half of V's product
-constexpr int kCodeWarps = 8, kSoftWarp = 8, kCopyWarp = 16, kLogitWarp = 17, kOutWarp = 18;   // (19: Q)
-constexpr int kThreads = 640;
-constexpr int kEntries = 16, kNC = 8;     // columns, and those of a softmax warpgroup
+constexpr int kCodeWarps = 8, kSoftWarp = 8, kCopyWarp = 12, kLogitWarp = 13, kOutWarp = 14;   // (15: Q)
+constexpr int kThreads = 512;
+constexpr int kEntries = 16;             // columns
 constexpr int kMaxSlots = 20;
 constexpr int kSmemLimit = 227 * 1024;
 constexpr float kTop = 7.f;              // log2 of the weight at the reference
@@ -134,13 +135,13 @@ __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
-__device__ __forceinline__ void soft_sync(int id) { asm volatile("bar.sync %0, 128;\n" ::"r"(id) : "memory"); }
-// Whether any of the warpgroup's threads says so.
-__device__ __forceinline__ bool soft_any(int id, bool x) {
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 128;\n" ::: "memory"); }
+// Whether any of the softmax's threads says so.
+__device__ __forceinline__ bool soft_any(bool x) {
   uint32_t r;
-  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
                : "=r"(r)
-               : "r"((uint32_t)x), "r"(id)
+               : "r"((uint32_t)x)
                : "memory");
   return r != 0;
 }
@@ -298,7 +299,7 @@ __device__ __forceinline__ void expand(uint32_t w, uint32_t scale, uint32_t mini
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_constant__ Q4Params qp) {
   using L = Slot<D>;
-  constexpr int G = D / 32, NS = D / 128;
+  constexpr int G = D / 32, NS = D / 128, N = kEntries;
   const PagedParams& p = qp.p;
   extern __shared__ __align__(1024) uint8_t raw[];
   Head& h = *reinterpret_cast<Head*>(raw);
@@ -315,9 +316,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
     bar_init(&h.k_full, kCodeWarps);
     bar_init(&h.k_empty, 1);
     bar_init(&h.s_full, 1);
-    bar_init(&h.s_empty, 8);
+    bar_init(&h.s_empty, 4);
     for (int i = 0; i < 2; ++i) {
-      bar_init(&h.p_full[i], 8);
+      bar_init(&h.p_full[i], 4);
       bar_init(&h.pv_done[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
     }
     bar_init(&h.q_full, 2);
     bar_init(&h.q_free, 1);
-    bar_init(&h.o_free, 8);
+    bar_init(&h.o_free, 4);
     bar_init(&h.mma_done, 2);
     h.abort = 0;
     bar_init_fence();
@@ -414,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
           __syncwarp();
           if (lane == 0) bar_arrive(&h.k_full);
         }
-        const int sv = part ? other : slot;
+        const int sv = part ? other : slot, vb = g & 1;
         wait(&h.code_full[sv], (part ? other_use : use) & 1, abrt);
         __syncwarp();
         const uint8_t* const at = ring + sv * L::kBytes + L::kCodes;
@@ -471,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
             if (lane == 0) bar_arrive(&h.code_empty[sv]);
           }
           if (i2 == 0) {
-            if (g >= 2) wait(&h.v_empty[part][g & 1], (uint32_t)((g - 2) >> 1) & 1, abrt);
+            if (g >= 2) wait(&h.v_empty[part][vb], (uint32_t)((g - 2) >> 1) & 1, abrt);
             __syncwarp();
             fence_after();
           }
@@ -479,12 +480,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
           for (int b = 0; b < NS; ++b)
 #pragma unroll
             for (int x = 0; x < 2; ++x)
-              tmem_st_fragments(lanes + ((uint32_t)(16 * x) << 16) + kVCol + (uint32_t)(128 * (g & 1) + 64 * b + 32 * part + 16 * i2), cell[b][x]);
+              tmem_st_fragments(lanes + ((uint32_t)(16 * x) << 16) + kVCol + (uint32_t)(128 * vb + 64 * b + 32 * part + 16 * i2), cell[b][x]);
         }
         tmem_st_wait();
         fence_before();
         __syncwarp();
-        if (lane == 0) bar_arrive(&h.v_full[part][g & 1]);
+        if (lane == 0) bar_arrive(&h.v_full[part][vb]);
         slot = other + 1;
         use = other_use;
         if (slot == qp.n_slots) slot = 0, ++use;
@@ -492,25 +493,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
     }
   } else if (warp < kCopyWarp) {
     // ------------------------------------------------------------ softmax and output
-    // Each of two warpgroups takes half of the columns; a thread owns a key of a tile, and a
-    // channel of each slab of the output.
-    const int group = (warp - kSoftWarp) >> 2, quarter = warp & 3, me = tid & 127, bar = 1 + group;
-    const int col0 = kNC * group;   // columns [col0, col0 + 8)
+    // A thread owns a key of a tile, and a channel of each slab of the output.
+    const int quarter = warp & 3, me = tid & 127;
     const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
     // Where the key's weights lie: V's keys of each 16 are in the order of its fragments.
     const int key = 32 * (quarter & 1) + lane;
     const int at_k = (key & 48) | ((key & 6) << 1) | ((key & 8) >> 2) | (key & 1);
-    const int to_p = (quarter >> 1) * (kPBytes / 2) + (((at_k >> 3) << 4) | ((at_k & 7) << 1)) + col0 * 128;
+    const int to_p = (quarter >> 1) * (kPBytes / 2) + (((at_k >> 3) << 4) | ((at_k & 7) << 1));
     const int channel = (D == 256 ? 64 : 32) * (lane & 3) + 4 * (2 * quarter + ((lane >> 2) & 1)) + (lane >> 3);   // (and 32 further)
     int g = 0, it = 0;   // tiles and items done
     for (bool more = true; more;) {
       const ItemRows ir = item_rows(p, c);
       const int T = c.x1 - c.x;
       const bool whole = c.whole();
-      const bool mine = me < kNC && col0 + me < ir.nf;   // the thread has a column's statistics, too
+      const bool mine = me < ir.nf;   // the thread has a column's statistics, too
       wait(&h.row_full[it & 3], (uint32_t)(it >> 2) & 1, abrt);
-      if (me < kNC) {
-        const int e = col0 + me, f = ir.f0 + min(e, ir.nf - 1), r = row_of(p, f);
+      if (me < N) {
+        const int e = me, f = ir.f0 + min(e, ir.nf - 1), r = row_of(p, f);
         // (The factor is not 0: hidden logits are -infinity times it.)
         h.column[e] = mine ? make_float2(fmaxf(h.q[it & 3][e] * (p.scale * kLog2e), 1e-37f), kUnset) : make_float2(0.f, -1000.f);
         h.ref[e] = -INFINITY;
@@ -518,74 +517,91 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
         h.to[e] = (whole ? (int64_t)(c.s.row0 + r) * p.n_q_heads + c.head * p.group + (f - r * p.group)
                          : (int64_t)c.slot(blockIdx.x) * p.mt + e) * D;
       }
-      soft_sync(bar);
-      // Of the columns: weight = 2^(logit * x + y), kept from tile to tile.
-      float2 k[kNC];
-      auto columns = [&] {
+      soft_sync();
+      // Of eight columns: weight = 2^(logit * x + y).
+      float2 k[8];
+      auto columns = [&](int x) {
 #pragma unroll
-        for (int e = 0; e < kNC; e += 2) {
-          const float4 two = *reinterpret_cast<const float4*>(&h.column[col0 + e]);
+        for (int e = 0; e < 8; e += 2) {
+          const float4 two = *reinterpret_cast<const float4*>(&h.column[x + e]);
           k[e] = make_float2(two.x, two.y), k[e + 1] = make_float2(two.z, two.w);
         }
       };
-      columns();
-      float l[kNC];
+      float l[N];
 #pragma unroll
-      for (int e = 0; e < kNC; ++e) l[e] = 0.f;
+      for (int e = 0; e < N; ++e) l[e] = 0.f;
 #pragma unroll 1
       for (int j = 0; j < T; ++j, ++g) {
         const int buf = g & 1, t0 = c.tiles.token(c.x + j);
         wait(&h.s_full, (uint32_t)g & 1, abrt);
         __syncwarp();
         fence_after();
-        // The minima's part, and the blocks' times their scales (codes are times 2^-9).
-        float z[kNC], acc[kNC], part[G][kNC];
-#pragma unroll
-        for (int i = 0; i < G; ++i) tmem_ld8_start(lanes + kSCol + (uint32_t)(16 * i + col0), part[i]);
-        tmem_ld8_start(lanes + kSCol + (uint32_t)(16 * G + col0), z);
+        // The blocks' sums times their scales (codes are times 2^-9), and the minima's part:
+        // three at a time in registers.
         const uint4 sc = h.scale[g & 3][32 * quarter + lane];
         const uint32_t bad = h.bad[g & 15][0] | (uint32_t)h.bad[g & 15][1] << 4;
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < G; ++i) tmem_ld_done(part[i]);
-        tmem_ld_done(z);
-        fence_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&h.s_empty);
-#pragma unroll
-        for (int e = 0; e < kNC; ++e) acc[e] = 0.f;
         const uint32_t scales[4] = {sc.x, sc.y, sc.z, sc.w};
+        float z[N];
 #pragma unroll
-        for (int i = 0; i < G; ++i) {
-          const float2 two = __half22float2(*reinterpret_cast<const __half2*>(&scales[i / 2]));
-          const float f = i & 1 ? two.y : two.x;
+        for (int e = 0; e < N; ++e) z[e] = 0.f;
+        constexpr int kAtOnce = 3;
 #pragma unroll
-          for (int e = 0; e < kNC; e += 2) fma2(acc[e], acc[e + 1], f, f, part[i][e], part[i][e + 1]);
+        for (int i0 = 0; i0 <= G; i0 += kAtOnce) {
+          float part[kAtOnce][N];
+#pragma unroll
+          for (int i = 0; i < kAtOnce && i0 + i <= G; ++i)
+#pragma unroll
+            for (int x = 0; x < N; x += 8) tmem_ld8_start(lanes + kSCol + (uint32_t)(N * (i0 + i) + x), part[i] + x);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < kAtOnce && i0 + i <= G; ++i)
+#pragma unroll
+            for (int x = 0; x < N; x += 8) tmem_ld_done(part[i] + x);
+          if (i0 + kAtOnce > G) {
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&h.s_empty);
+          }
+#pragma unroll
+          for (int i = 0; i < kAtOnce && i0 + i <= G; ++i) {
+            const int u = i0 + i;
+            const float2 two = __half22float2(*reinterpret_cast<const __half2*>(&scales[u / 2 % 4]));
+            const float f = u == G ? 1.f : 512.f * (u & 1 ? two.y : two.x);
+#pragma unroll
+            for (int e = 0; e < N; e += 2) fma2(z[e], z[e + 1], f, f, part[i][e], part[i][e + 1]);
+          }
         }
-#pragma unroll
-        for (int e = 0; e < kNC; ++e) z[e] = fmaf(acc[e], 512.f, z[e]);
         // Tiles that every row sees whole are the rule.
         if (bad != 0u || t0 + kKT - 1 > ir.first || (p.window > 0 && t0 <= ir.last - p.window && t0 + kKT > p.n_sinks)) {
           const int tk = t0 + 32 * quarter + lane;
           const bool gone = (bad >> (2 * quarter + (lane >> 4))) & 1u;
 #pragma unroll
-          for (int e = 0; e < kNC; ++e)
-            if (gone || !sees(p, h.pos[col0 + e], tk)) z[e] = -INFINITY;
+          for (int e = 0; e < N; ++e)
+            if (gone || !sees(p, h.pos[e], tk)) z[e] = -INFINITY;
         }
         // Whether a weight would be larger than the reference leaves room for.
-        float y[kNC];
+        float most = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < kNC; ++e) y[e] = fmaf(z[e], k[e].x, k[e].y);
+        for (int x = 0; x < N; x += 8) {
+          columns(x);
+          float y[8];
 #pragma unroll
-        for (int n = kNC / 2; n >= 1; n >>= 1)
+          for (int e = 0; e < 8; ++e) y[e] = fmaf(z[x + e], k[e].x, k[e].y);
 #pragma unroll
-          for (int e = 0; e < n; ++e) y[e] = fmaxf(y[e], y[n + e]);
-        if (soft_any(bar, y[0] > kTop + kLag)) {
-          const float top = reduce_columns(z, lane, [](float a, float b) { return fmaxf(a, b); });
-          if ((lane & 3) == 0) h.mx[quarter][col0 + (lane >> 2)] = top;
-          soft_sync(bar);
-          if (me < kNC) {
-            const int e = col0 + me;
+          for (int n = 4; n >= 1; n >>= 1)
+#pragma unroll
+            for (int e = 0; e < n; ++e) y[e] = fmaxf(y[e], y[n + e]);
+          most = fmaxf(most, y[0]);
+        }
+        if (soft_any(most > kTop + kLag)) {
+#pragma unroll
+          for (int x = 0; x < N; x += 8) {
+            const float top = reduce_columns(z + x, lane, [](float a, float b) { return fmaxf(a, b); });
+            if ((lane & 3) == 0) h.mx[quarter][x + (lane >> 2)] = top;
+          }
+          soft_sync();
+          if (me < N) {
+            const int e = me;   // (threads 0 to 15 have a column each)
             float factor = 1.f;
             if (mine) {
               const float top = fmaxf(fmaxf(h.mx[0][e], h.mx[1][e]), fmaxf(h.mx[2][e], h.mx[3][e]));
@@ -597,24 +613,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
             }
             h.factor[e] = factor;
           }
-          soft_sync(bar);
+          soft_sync();
 #pragma unroll
-          for (int e = 0; e < kNC; ++e) l[e] *= h.factor[col0 + e];
-          columns();
+          for (int e = 0; e < N; ++e) l[e] *= h.factor[e];
           if (j > 0) {   // the output as well
             wait(&h.pv_done[buf ^ 1], (uint32_t)((g - 1) >> 1) & 1, abrt);
             __syncwarp();
             fence_after();
 #pragma unroll 1
-            for (int b = 0; b < NS; ++b) {
-              const uint32_t at = lanes + kOCol + (uint32_t)(16 * b + col0);
-              float o[kNC];
-              uint32_t w[kNC];
+            for (int x = 0; x < NS * N; x += 8) {
+              const int b = x >= N ? 1 : 0, x0 = x - b * N;
+              const uint32_t at = lanes + kOCol + (uint32_t)(N * b + x0);
+              float o[8];
+              uint32_t w[8];
               tmem_ld8_start(at, o);
               tmem_ld_wait();
               tmem_ld_done(o);
 #pragma unroll
-              for (int e = 0; e < kNC; ++e) w[e] = __float_as_uint(o[e] * h.factor[col0 + e]);
+              for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[e] * h.factor[x0 + e]);
               tmem_st8(at, w);
             }
             tmem_st_wait();
@@ -622,62 +638,72 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
         }
         if (g >= 2) wait(&h.pv_done[buf], (uint32_t)((g - 2) >> 1) & 1, abrt);   // the buffer's weights have been used
         uint8_t* const to = p_s + buf * kPBytes;
-        uint32_t w2[kNC / 2];
+        uint32_t w2[N / 2];
 #pragma unroll
-        for (int e = 0; e < kNC; e += 2) {
-          const float a = ex2(fmaf(z[e], k[e].x, k[e].y)), b = ex2(fmaf(z[e + 1], k[e + 1].x, k[e + 1].y));
-          l[e] += a;
-          l[e + 1] += b;
-          w2[e / 2] = pack_f16(a, b);
+        for (int x = 0; x < N; x += 8) {   // (all before the stores, which the loads would wait behind)
+          columns(x);
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            const float a = ex2(fmaf(z[x + e], k[e].x, k[e].y)), b = ex2(fmaf(z[x + e + 1], k[e + 1].x, k[e + 1].y));
+            l[x + e] += a;
+            l[x + e + 1] += b;
+            w2[(x + e) / 2] = pack_f16(a, b);
+          }
         }
 #pragma unroll
-        for (int e = 0; e < kNC; ++e)   // (col0 is a multiple of 8)
-          *reinterpret_cast<uint16_t*>(to + (to_p ^ (e << 4)) + e * 128) = (uint16_t)(e & 1 ? w2[e / 2] >> 16 : w2[e / 2]);
+        for (int e = 0; e < N; ++e)
+          *reinterpret_cast<uint16_t*>(to + (to_p ^ ((e & 7) << 4)) + e * 128) = (uint16_t)(e & 1 ? w2[e / 2] >> 16 : w2[e / 2]);
         fence_before();
         fence_async_smem();
         __syncwarp();
         if (lane == 0) bar_arrive(&h.p_full[buf]);
       }
       // The item's result, or this run's part of it.
-      const float part_sum = reduce_columns(l, lane, [](float a, float b) { return a + b; });
-      if ((lane & 3) == 0) h.sums[quarter][col0 + (lane >> 2)] = part_sum;
-      soft_sync(bar);
+#pragma unroll
+      for (int x = 0; x < N; x += 8) {
+        const float sum = reduce_columns(l + x, lane, [](float a, float b) { return a + b; });
+        if ((lane & 3) == 0) h.sums[quarter][x + (lane >> 2)] = sum;
+      }
+      soft_sync();
       if (mine) {
-        const int e = col0 + me;
+        const int e = me;
         const float sum = (h.sums[0][e] + h.sums[1][e]) + (h.sums[2][e] + h.sums[3][e]);
         h.inv[e] = sum == 0.f ? 0.f : 1.f / sum;   // (NaN stays)
         const float lse2 = sum == 0.f ? -INFINITY : h.ref[e] - kTop + log2f(sum);
         if (!whole) p.part_lse[h.to[e] / D] = lse2;
         else if (p.lse) p.lse[h.to[e] / D] = lse2 * kLn2;
       }
-      soft_sync(bar);
+      soft_sync();
       wait(&h.pv_done[(g - 1) & 1], (uint32_t)((g - 1) >> 1) & 1, abrt);
       __syncwarp();
       fence_after();
       const bool f32 = !whole || p.out_dtype == QSA_F32;
       float* const to32 = (whole ? static_cast<float*>(p.out) : p.part_o) + channel;
       __nv_bfloat16* const to16 = static_cast<__nv_bfloat16*>(p.out) + channel;
-      float o[NS][kNC];
+#pragma unroll 1
+      for (int x = 0; x < ir.nf; x += 8) {
+        float o[NS][8];
 #pragma unroll
-      for (int b = 0; b < NS; ++b) tmem_ld8_start(lanes + kOCol + (uint32_t)(16 * b + col0), o[b]);
-      tmem_ld_wait();
+        for (int b = 0; b < NS; ++b) tmem_ld8_start(lanes + kOCol + (uint32_t)(N * b + x), o[b]);
+        tmem_ld_wait();
 #pragma unroll
-      for (int b = 0; b < NS; ++b) tmem_ld_done(o[b]);
+        for (int b = 0; b < NS; ++b) tmem_ld_done(o[b]);
 #pragma unroll
-      for (int e = 0; e < kNC; ++e) {
-        if (col0 + e >= ir.nf) break;
-        const float inv = h.inv[col0 + e];
-        const int64_t at = h.to[col0 + e];
+        for (int e = 0; e < 8; ++e) {
+          if (x + e >= ir.nf) break;
+          const float inv = h.inv[x + e];
+          const int64_t at = h.to[x + e];
 #pragma unroll
-        for (int b = 0; b < NS; ++b) {
-          if (f32) to32[at + 32 * b] = o[b][e] * inv;
-          else to16[at + 32 * b] = __float2bfloat16_rn(o[b][e] * inv);
+          for (int b = 0; b < NS; ++b) {
+            if (f32) to32[at + 32 * b] = o[b][e] * inv;
+            else to16[at + 32 * b] = __float2bfloat16_rn(o[b][e] * inv);
+          }
         }
       }
       fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive(&h.o_free);
-      soft_sync(bar);   // the columns are the next item's
+      soft_sync();   // the columns are the next item's
       ++it;
       more = c.next(p, p.mt);
       if (!more && tid == 32 * kSoftWarp) describe_part(p, c, h.start, blockIdx.x);   // (still at its last item)
@@ -753,8 +779,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
     // The whole warp walks through the tiles with values that are the same in all its
     // lanes, and one lane issues.
     const bool leader = elect_one();
-    // 32-bit accumulators, both K-major, M = 128, N = 16; E4M3 and f16 operands are both 0.
-    constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(kEntries >> 3) << 17) | (8u << 24);
+    // 32-bit accumulators, both K-major, M = 128; E4M3 and f16 operands are both 0.
+    constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
     const uint64_t q_desc = desc_sw128(q_s, 16, 1024);
     constexpr uint32_t kSlab = L::kQSlab >> 4;
     int g = 0, it = 0;
@@ -772,9 +798,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
           for (int x = 0; x < G; ++x)
 #pragma unroll
             for (int y = 0; y < 2; ++y)   // both codes of q
-              mma_f8_ts(tmem + kSCol + 16u * x, tmem + kKCol + 8u * x, q_desc + (uint32_t)(NS * y + (x >> 2)) * kSlab + 2 * (x & 3),
+              mma_f8_ts(tmem + kSCol + (uint32_t)(N * x), tmem + kKCol + 8u * x, q_desc + (uint32_t)(NS * y + (x >> 2)) * kSlab + 2 * (x & 3),
                         kIdesc, (uint32_t)y);
-          mma_f16_ts(tmem + kSCol + 16u * G, tmem + kMinCol, q_desc + 2 * NS * kSlab, kIdesc, 0u);
+          mma_f16_ts(tmem + kSCol + (uint32_t)(N * G), tmem + kMinCol, q_desc + 2 * NS * kSlab, kIdesc, 0u);
           commit(&h.k_empty);
           commit(&h.s_full);
           if (j + 1 == T) commit(&h.q_free);
@@ -790,14 +816,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
     // Two E4M3 codes of each value (see above) and the sums of its blocks, a row's 16
     // channels a lane, in the order of K's cells: of channels 8 i .. 8 i + 7 the bytes are
     // 0, 2, 4, 6, 1, 3, 5, 7.  (The first item's with the warp that has no output to issue yet.)
-    constexpr int kLanes = D / 16, kRows = 32 / kLanes, kBatch = kEntries / (2 * kRows);
+    constexpr int kLanes = D / 16, kRows = 32 / kLanes, kBatch = 8 / kRows;   // 16 rows of two warps
     const int chunk = lane % kLanes;
     auto queries = [&](int it, int first, int warps) {
       const ItemRows ir = item_rows(p, c);
       if (it > 0) wait(&h.q_free, (uint32_t)(it - 1) & 1, abrt);
       __syncwarp();
 #pragma unroll 1
-      for (int r0 = first * kRows + lane / kLanes; r0 < kEntries; r0 += kBatch * warps * kRows) {
+      for (int r0 = first * kRows + lane / kLanes; r0 < N; r0 += kBatch * warps * kRows) {
         uint4 a[kBatch], b[kBatch];
 #pragma unroll
         for (int x = 0; x < kBatch; ++x) {
@@ -869,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
     if (warp == kOutWarp) {
       // ---------------------------------------------------------- output
       const bool leader = elect_one();
-      constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(kEntries >> 3) << 17) | (8u << 24);
+      constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
       const uint64_t p_desc = desc_sw128(p_s, 16, 1024);
       int g = 0, it = 0;
       bool live = true;
@@ -877,21 +903,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
         const int T = __shfl_sync(0xffffffffu, c.x1 - c.x, 0);
 #pragma unroll 1
         for (int j = 0; j < T; ++j, ++g) {
-          const int buf = g & 1;
+          const int buf = g & 1, vb = g & 1;
           live = __all_sync(0xffffffffu, wait(&h.p_full[buf], (uint32_t)(g >> 1) & 1, abrt) && live);
           if (j == 0 && it > 0) live = __all_sync(0xffffffffu, wait(&h.o_free, (uint32_t)(it - 1) & 1, abrt) && live);
 #pragma unroll
           for (int a = 0; a < 2; ++a) {
-            live = __all_sync(0xffffffffu, wait(&h.v_full[a][buf], (uint32_t)(g >> 1) & 1, abrt) && live);
+            live = __all_sync(0xffffffffu, wait(&h.v_full[a][vb], (uint32_t)(g >> 1) & 1, abrt) && live);
             fence_after();
             if (leader && live) {
 #pragma unroll
               for (int b = 0; b < NS; ++b)
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
-                  mma_f16_ts(tmem + kOCol + 16u * b, tmem + kVCol + 128u * buf + 64u * b + 32u * a + 8u * x,
+                  mma_f16_ts(tmem + kOCol + (uint32_t)(N * b), tmem + kVCol + 128u * vb + 64u * b + 32u * a + 8u * x,
                              p_desc + (uint32_t)(2 * buf + a) * (kPBytes >> 5) + 2 * x, kIdesc, (j | a | x) != 0 ? 1u : 0u);
-              commit(&h.v_empty[a][buf]);
+              commit(&h.v_empty[a][vb]);
               if (a == 1) commit(&h.pv_done[buf]);
             }
             __syncwarp();
