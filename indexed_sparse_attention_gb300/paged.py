@@ -16,7 +16,7 @@ from typing import Sequence
 import torch
 
 from . import AttnConfig, BF16, F32, FP8, Q4, _dtype_code, _ptr, _scratch, lib
-from .calls import _call
+from .calls import _call, _call_at
 from .rope import Rope, RopeDesc, _strides
 
 
@@ -119,7 +119,7 @@ class PagedCache:
             d.kv_scale = s.data_ptr()
             d.scale_page_stride, d.scale_head_stride, d.scale_tok_stride = (s.stride(i) // n for i in range(3))
         self.byref = ctypes.byref(d)
-        self.device = k.device
+        self.device, self.index = k.device, k.get_device()
         self.row_dtype = torch.float32 if self.kv_dtype == F32 else torch.bfloat16   # of new rows and queries
         self._row_cfg = self.config()
         self._row_cfg_ref = ctypes.byref(self._row_cfg)
@@ -184,6 +184,7 @@ class PagedBatch:
         if len({t.device for t in (table, lens, row_start)}) != 1:
             raise ValueError("table, lens and row_start on different devices")
         self.table, self.lens, self.row_start = table, lens, row_start
+        self.index = table.get_device()
         self.n_seqs, self.n_rows = n, int(n_rows)
         self.max_rows = self.n_rows if max_rows is None else int(max_rows)
         ld = int(table.shape[1])
@@ -192,19 +193,19 @@ class PagedBatch:
         self.byref = ctypes.byref(self.desc)
 
 
-def _check_rows(what: str, t: torch.Tensor, shape, dtype, device):
-    if t.shape != shape or t.dtype is not dtype or t.device != device:
-        raise ValueError(f"{what} must be {list(shape)} of {dtype} on {device}, not {list(t.shape)} of {t.dtype} on {t.device}")
+def _check_rows(what: str, t: torch.Tensor, shape, dtype, cache: PagedCache):
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != cache.index:
+        raise ValueError(f"{what} must be {list(shape)} of {dtype} on {cache.device}, not {list(t.shape)} of {t.dtype} on {t.device}")
 
 
 def _check_batch(cache: PagedCache, batch: PagedBatch):
-    if batch.table.device != cache.device:
+    if batch.index != cache.index:
         raise ValueError("the batch's arrays are on another device than the cache")
 
 
 def _check_queries(cache: PagedCache, batch: PagedBatch, q: torch.Tensor):
     shape = q.shape
-    _check_rows("q", q, (batch.n_rows, shape[1] if len(shape) == 3 else 0, cache.head_dim), cache.row_dtype, cache.device)
+    _check_rows("q", q, (batch.n_rows, shape[1] if len(shape) == 3 else 0, cache.head_dim), cache.row_dtype, cache)
     if not q.is_contiguous():
         raise ValueError("q must be contiguous")
     _check_batch(cache, batch)
@@ -234,9 +235,9 @@ def paged_attn(cache: PagedCache, batch: PagedBatch, q: torch.Tensor, out: torch
     them and the first n_sinks tokens."""
     _check_queries(cache, batch, q)
     shape = q.shape
-    _check_rows("out", out, shape, out.dtype, cache.device)
+    _check_rows("out", out, shape, out.dtype, cache)
     if lse is not None:
-        _check_rows("lse", lse, shape[:2], torch.float32, cache.device)
+        _check_rows("lse", lse, shape[:2], torch.float32, cache)
     if not (out.is_contiguous() and (lse is None or lse.is_contiguous())):
         raise ValueError("out and lse must be contiguous")
     own = cache._call_config(shape[1], out.dtype, scale, n_splits)
@@ -247,9 +248,9 @@ def paged_attn(cache: PagedCache, batch: PagedBatch, q: torch.Tensor, out: torch
             f"{f}={getattr(cfg, f)} for {getattr(own, f)}" for f in _CALL_FIELDS if getattr(cfg, f) != getattr(own, f)))
     if workspace is None:
         workspace = _scratch(paged_attn_workspace_size(batch, cfg), cache.device, stream)
-    elif workspace.device != cache.device or not workspace.is_contiguous() or workspace.dtype != torch.uint8:
+    elif workspace.get_device() != cache.index or not workspace.is_contiguous() or workspace.dtype != torch.uint8:
         raise ValueError(f"workspace must be contiguous uint8 on {cache.device}")
-    _call("qsa_paged_attn", cache.device, stream, cache.byref, batch.byref, ctypes.byref(cfg), int(window),
+    _call_at("qsa_paged_attn", cache.index, stream, cache.byref, batch.byref, ctypes.byref(cfg), int(window),
           int(n_sinks), q.data_ptr(), out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel())
 
 
@@ -260,8 +261,8 @@ def paged_append(cache: PagedCache, batch: PagedBatch, k_new: torch.Tensor, v_ne
     is rotated for the rows' positions on the way, and q [n_rows, Hq, D] (unit channel
     stride; a slice of the projection will do) into q_out, contiguous, beside it."""
     shape = (batch.n_rows, cache.n_kv_heads, cache.head_dim)
-    _check_rows("k_new", k_new, shape, cache.row_dtype, cache.device)
-    _check_rows("v_new", v_new, shape, cache.row_dtype, cache.device)
+    _check_rows("k_new", k_new, shape, cache.row_dtype, cache)
+    _check_rows("v_new", v_new, shape, cache.row_dtype, cache)
     strides = k_new.stride()
     if strides != v_new.stride() or strides[2] != 1:
         raise ValueError("k_new and v_new need unit channel stride and equal strides")
@@ -269,7 +270,7 @@ def paged_append(cache: PagedCache, batch: PagedBatch, k_new: torch.Tensor, v_ne
     if rope is None:
         if q is not None or q_out is not None:
             raise ValueError("q and q_out go with a rope")
-        _call("qsa_paged_append", cache.device, stream, cache.byref, batch.byref, cache._row_cfg_ref, k_new.data_ptr(),
+        _call_at("qsa_paged_append", cache.index, stream, cache.byref, batch.byref, cache._row_cfg_ref, k_new.data_ptr(),
               v_new.data_ptr(), strides[0], strides[1])
         return
     cfg, at_q, to_q, q_strides = cache._row_cfg_ref, None, None, (0, 0)
@@ -279,14 +280,14 @@ def paged_append(cache: PagedCache, batch: PagedBatch, k_new: torch.Tensor, v_ne
         q_shape, q_st = q.shape, q.stride()
         if len(q_shape) != 3 or q_st[2] != 1:
             raise ValueError("q must be [n_rows, Hq, D] with unit channel stride")
-        _check_rows("q", q, (batch.n_rows, q_shape[1], cache.head_dim), cache.row_dtype, cache.device)
-        _check_rows("q_out", q_out, q_shape, cache.row_dtype, cache.device)
+        _check_rows("q", q, (batch.n_rows, q_shape[1], cache.head_dim), cache.row_dtype, cache)
+        _check_rows("q_out", q_out, q_shape, cache.row_dtype, cache)
         if not q_out.is_contiguous():
             raise ValueError("q_out must be contiguous")
-        cfg = cache._rows_cfg(q_shape[1])
+        cfg = cache._rows_cfgs.get(q_shape[1]) or cache._rows_cfg(q_shape[1])
         at_q, to_q, q_strides = q.data_ptr(), q_out.data_ptr(), _strides(q_shape, q_st)
     row_stride, head_stride = _strides(shape, strides)
-    _call("qsa_paged_append_rotate", cache.device, stream, cache.byref, batch.byref, cfg, rope.byref, k_new.data_ptr(),
+    _call_at("qsa_paged_append_rotate", cache.index, stream, cache.byref, batch.byref, cfg, rope.byref, k_new.data_ptr(),
           v_new.data_ptr(), row_stride, head_stride, at_q, *q_strides, to_q)
 
 
@@ -296,12 +297,12 @@ def paged_read(cache: PagedCache, batch: PagedBatch, k_out: torch.Tensor, v_out:
     shape = (batch.n_rows, cache.n_kv_heads, cache.head_dim)
     if k_out.dtype is not torch.float32 and k_out.dtype is not torch.bfloat16:
         raise TypeError(f"k_out must be float32 or bfloat16, not {k_out.dtype}")
-    _check_rows("k_out", k_out, shape, k_out.dtype, cache.device)
-    _check_rows("v_out", v_out, shape, k_out.dtype, cache.device)
+    _check_rows("k_out", k_out, shape, k_out.dtype, cache)
+    _check_rows("v_out", v_out, shape, k_out.dtype, cache)
     if not (k_out.is_contiguous() and v_out.is_contiguous()):
         raise ValueError("k_out and v_out must be contiguous")
     _check_batch(cache, batch)
-    _call("qsa_paged_read", cache.device, stream, cache.byref, batch.byref,
+    _call_at("qsa_paged_read", cache.index, stream, cache.byref, batch.byref,
           cache._read_cfg[k_out.dtype is torch.bfloat16], k_out.data_ptr(), v_out.data_ptr())
 
 
@@ -345,7 +346,7 @@ class PagedStep:
             paged_append(self.cache, self.batch, k_new, v_new, stream, rope=self.rope, q=self.q_in, q_out=self.q_rotated)
 
     def attend(self, stream=None):
-        _call("qsa_paged_attn", self.q.device, stream, *self._args)
+        _call_at("qsa_paged_attn", self.cache.index, stream, *self._args)
         return self.out, self.lse
 
     def run(self, k_new: torch.Tensor | None = None, v_new: torch.Tensor | None = None, stream=None):

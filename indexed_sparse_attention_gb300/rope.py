@@ -13,7 +13,7 @@ from typing import Sequence
 import torch
 
 from . import BF16, F32, _check, _dtype_code, lib
-from .calls import _call
+from .calls import _call_at
 
 MAX_ROPE_PAIRS = 128
 _SCALINGS = {None: 0, "linear": 1, "parts": 2}
@@ -92,26 +92,31 @@ def rotate(rope: Rope, positions: torch.Tensor, x: torch.Tensor, out: torch.Tens
     """out[r, h] = x[r, h] rotated for position positions[r] (int32, on the GPU).  x is
     [rows, heads, dim] of f32 or bf16 with unit channel stride; out may be x itself, and
     is x by default."""
-    shape, x_strides, device, dtype = x.shape, x.stride(), x.device, x.dtype
-    if out is None:
-        out = x
-    elif out is not x and (out.shape != shape or out.dtype is not dtype or out.device != device):
-        raise ValueError("x and out must be [rows, heads, dim] of one shape, dtype and device")
+    shape, x_strides, device, dtype = x.shape, x.stride(), x.get_device(), x.dtype
+    if out is None or out is x:
+        out, out_strides = x, x_strides
+    else:
+        out_strides = out.stride()
+        if out.shape != shape or out.dtype is not dtype or out.get_device() != device:
+            raise ValueError("x and out must be [rows, heads, dim] of one shape, dtype and device")
     if len(shape) != 3:
         raise ValueError("x and out must be [rows, heads, dim] of one shape, dtype and device")
     kind = _KINDS.get(dtype)
     if kind is None:
         raise TypeError(f"x must be float32 or bfloat16, not {dtype}")
-    out_strides = x_strides if out is x else out.stride()
     rows, heads, dim = shape
     if (x_strides[2] != 1 or out_strides[2] != 1) and dim > 1:
         raise ValueError("x and out need unit channel stride")
     if positions.dtype is not torch.int32 or positions.shape != (rows,) or not positions.is_contiguous():
         raise TypeError("positions must be a contiguous int32 vector with an entry for each row")
-    if positions.device != device:
-        raise ValueError(f"positions is on {positions.device}, x on {device}")
-    x_row, x_head = _strides(shape, x_strides)
-    y_row, y_head = _strides(shape, out_strides)
-    _call("qsa_rotate", device, stream, rope.byref, positions.data_ptr(), rows, heads, dim, kind, x.data_ptr(), x_row,
+    if positions.get_device() != device:
+        raise ValueError(f"positions is on {positions.device}, x on {x.device}")
+    if rows > 1 and heads > 1:
+        x_row, x_head, _ = x_strides
+        y_row, y_head, _ = out_strides
+    else:
+        x_row, x_head = _strides(shape, x_strides)
+        y_row, y_head = _strides(shape, out_strides)
+    _call_at("qsa_rotate", device, stream, rope.byref, positions.data_ptr(), rows, heads, dim, kind, x.data_ptr(), x_row,
           x_head, out.data_ptr(), y_row, y_head)
     return out
