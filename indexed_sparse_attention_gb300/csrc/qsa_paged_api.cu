@@ -81,9 +81,9 @@ Plan plan_attn(const qsa_paged_batch* b, const qsa_attn_config* cfg) {
   Plan pl;
   // 4 bits: up to 16 entries a sequence and KV head are the columns of products whose other
   // operand is expanded in registers; more are the rows of products that share the values
-  // expanded to shared memory.  16 sequences of 58,368 tokens, 12 entries: 151 us this way,
-  // 252 the other; 24 entries, two items of up to 16: 287 and 253.  One of 128 tokens: 10
-  // and 12.
+  // expanded to shared memory.  16 sequences of 58,368 tokens, 12 entries: 137 us this way,
+  // 252 the other; 24 entries, two items of up to 16: 258 and 254 (16 of 128 tokens: 18 and
+  // 13).  One of 128 tokens, 12 entries: 10 and 12.
   const int group_of = cfg->n_q_heads / cfg->n_kv_heads;
   const bool few = cfg->kv_dtype == QSA_Q4_1 && (int64_t)b->max_rows * group_of <= 16;
   pl.tensor_cores = cfg->kv_dtype != QSA_F32 && !few;

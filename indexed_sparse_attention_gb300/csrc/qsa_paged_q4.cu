@@ -27,9 +27,8 @@
 //
 // Roles (16 warps): 0-7 expand codes (four warps a half of K's channels, and of V's keys),
 // 8-11 softmax and output, 12 copies, 13 issues the logits' products, 14 the output's, 15
-// writes Q.  K, V and their records come through TMA, 64
-// keys a slot; boxes of pages without visible tokens are aimed past the last page, which
-// fills zeros without reading.  Every wait gives up after about two seconds (counted;
+// writes Q.  K, V and their records come through TMA, 64 keys a slot; boxes of pages
+// without visible tokens are aimed past the last page, which fills zeros without reading.  Every wait gives up after about two seconds (counted;
 // nothing more is issued then, and the CTA runs to its end); its loop is out of line, as
 // warps that wait in the middle of the roles' code take issue slots and instruction cache
 // from those that expand (a ragged batch of 16 sequences took 146 us so, and 136 this way).
