@@ -193,13 +193,16 @@ class PagedBatch:
         self.byref = ctypes.byref(self.desc)
 
 
+# Devices are compared by their numbers, which costs half of comparing them; what is no GPU (CPU, meta) has -1 in
+# common, and is compared as what it is before the call is refused for it.
 def _check_rows(what: str, t: torch.Tensor, shape, dtype, cache: PagedCache):
-    if t.shape != shape or t.dtype is not dtype or t.get_device() != cache.index:
+    index = cache.index
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or (index < 0 and t.device != cache.device):
         raise ValueError(f"{what} must be {list(shape)} of {dtype} on {cache.device}, not {list(t.shape)} of {t.dtype} on {t.device}")
 
 
 def _check_batch(cache: PagedCache, batch: PagedBatch):
-    if batch.index != cache.index:
+    if batch.index != cache.index or (cache.index < 0 and batch.table.device != cache.device):
         raise ValueError("the batch's arrays are on another device than the cache")
 
 
@@ -248,7 +251,8 @@ def paged_attn(cache: PagedCache, batch: PagedBatch, q: torch.Tensor, out: torch
             f"{f}={getattr(cfg, f)} for {getattr(own, f)}" for f in _CALL_FIELDS if getattr(cfg, f) != getattr(own, f)))
     if workspace is None:
         workspace = _scratch(paged_attn_workspace_size(batch, cfg), cache.device, stream)
-    elif workspace.get_device() != cache.index or not workspace.is_contiguous() or workspace.dtype != torch.uint8:
+    elif workspace.get_device() != cache.index or (cache.index < 0 and workspace.device != cache.device) or (
+            not workspace.is_contiguous() or workspace.dtype != torch.uint8):
         raise ValueError(f"workspace must be contiguous uint8 on {cache.device}")
     _call_at("qsa_paged_attn", cache.index, stream, cache.byref, batch.byref, ctypes.byref(cfg), int(window),
           int(n_sinks), q.data_ptr(), out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel())

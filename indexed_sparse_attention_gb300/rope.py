@@ -97,7 +97,8 @@ def rotate(rope: Rope, positions: torch.Tensor, x: torch.Tensor, out: torch.Tens
         out, out_strides = x, x_strides
     else:
         out_strides = out.stride()
-        if out.shape != shape or out.dtype is not dtype or out.get_device() != device:
+        if out.shape != shape or out.dtype is not dtype or out.get_device() != device or (
+                device < 0 and out.device != x.device):   # (what is no GPU has -1 in common)
             raise ValueError("x and out must be [rows, heads, dim] of one shape, dtype and device")
     if len(shape) != 3:
         raise ValueError("x and out must be [rows, heads, dim] of one shape, dtype and device")
@@ -109,7 +110,7 @@ def rotate(rope: Rope, positions: torch.Tensor, x: torch.Tensor, out: torch.Tens
         raise ValueError("x and out need unit channel stride")
     if positions.dtype is not torch.int32 or positions.shape != (rows,) or not positions.is_contiguous():
         raise TypeError("positions must be a contiguous int32 vector with an entry for each row")
-    if positions.get_device() != device:
+    if positions.get_device() != device or (device < 0 and positions.device != x.device):
         raise ValueError(f"positions is on {positions.device}, x on {x.device}")
     if rows > 1 and heads > 1:
         x_row, x_head, _ = x_strides
