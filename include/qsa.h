@@ -572,6 +572,13 @@ typedef enum qsa_rope_scaling {
  * Extension of Large Language Models", 2023, section 3) 0.1 ln(factor) + 1, with
  *   r_i = original_tokens w_i / (2 pi),  g_i = clamp((r_i - slow) / (fast - slow), 0, 1),
  *   w_i' = (1 - g_i) w_i / factor + g_i w_i        (the paper: fast 32, slow 1).
+ * The ramp is linear in the turns r_i, as the paper's text has it.  Many models were
+ * trained with another one, linear in the pair's index, with the ends rounded to whole
+ * pairs: g_i = 1 - clamp((i - a) / (b - a), 0, 1), a = max(floor(i(fast)), 0),
+ * b = min(ceil(i(slow)), rot_dim - 1), i(r) = rot_dim ln(original_tokens / (2 pi r)) /
+ * (2 ln base).  Inside the ramp the two are far apart (up to 1.7 times w_i' for
+ * factor 4, 4 times for 32), so such a model takes frequencies worked out that way, by
+ * qsa_rope_init.
  * qsa_rope_init makes a rotation from any frequencies.
  *   base >= 1, factor >= 1 (not used by PLAIN), original_tokens, fast > slow >= 0
  *   (used by PARTS)

@@ -40,7 +40,9 @@ class RopeScaling:
     """How frequencies are stretched for contexts `factor` times as long: "linear"
     (all of them), or "parts": those that turn more than `fast` times over
     original_tokens stay, those that turn less than `slow` times are divided, with a
-    ramp between the two."""
+    ramp between the two that is linear in how often a pair turns.  Models trained with
+    a ramp that is linear in the pair's index take Rope(frequencies=) instead
+    (include/qsa.h has both formulas)."""
     kind: str
     factor: float
     original_tokens: float = 0.0

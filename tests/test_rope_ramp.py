@@ -39,3 +39,24 @@ def test_the_ramp_is_linear_in_turns(rot, base, factor, original, fast, slow):
         inside += 0 < g < 1
     assert inside >= 2 and len(got.frequencies) == rot // 2
     assert math.isclose(got.magnitude, 0.1 * math.log(factor) + 1, rel_tol=2.0 ** -23)
+
+
+def by_index(rot, base, factor, original, fast, slow):
+    """Frequencies whose ramp is linear in the pair's index, as README works them out."""
+    index = lambda turns: rot * math.log(original / (2 * math.pi * turns)) / (2 * math.log(base))  # noqa: E731
+    a, b = max(math.floor(index(fast)), 0), min(math.ceil(index(slow)), rot - 1)
+    keep = [1 - min(max((i - a) / max(b - a, 1e-3), 0), 1) for i in range(rot // 2)]
+    w = [base ** (-2 * i / rot) for i in range(rot // 2)]
+    return [(1 - k) * x / factor + k * x for x, k in zip(w, keep)]
+
+
+def test_a_ramp_by_index_is_another_one_and_can_be_given():
+    args = (128, 1e6, 4.0, 32768, 32.0, 1.0)
+    given = by_index(*args)
+    own = qsa.Rope(128, base=1e6, scaling=qsa.RopeScaling("parts", 4.0, original_tokens=32768)).frequencies
+    ratio = [a / b for a, b in zip(given, own)]
+    same = [i for i, r in enumerate(ratio) if abs(r - 1) < 1e-12]
+    # Both leave the pairs before the ramp and divide those behind it; inside they are different frequencies.
+    assert set(range(24)) <= set(same) and set(range(40, 64)) <= set(same) and 1.7 < max(ratio) < 1.75 and len(same) < 50
+    rope = qsa.Rope(128, frequencies=given, magnitude=0.1 * math.log(4.0) + 1)
+    assert rope.frequencies == tuple(given) and math.isclose(rope.magnitude, 1.1386294, rel_tol=1e-6)
