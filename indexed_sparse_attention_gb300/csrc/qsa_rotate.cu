@@ -192,6 +192,10 @@ QSA_API qsa_status qsa_rotate(const qsa_rope* rope, const int32_t* positions, in
   for (const int64_t st : {x_row_stride, x_head_stride, y_row_stride, y_head_stride})
     if (st < 0 || st > most)
       return fail(QSA_ERR_INVALID_ARG, "%s: a stride of %lld elements", fn, (long long)st);
+  // (Rows' offsets in bytes, and the sums below, then keep to 64 bits: heads are at most 2^16.)
+  if (n_rows > 1 && std::max(x_row_stride, y_row_stride) > ((int64_t)1 << 58) / (n_rows - 1))
+    return fail(QSA_ERR_INVALID_ARG, "%s: %d rows %lld elements apart pass 64 bits", fn, n_rows,
+                (long long)std::max(x_row_stride, y_row_stride));
   if ((n_rows > 1 && y_row_stride < head_dim) || (n_heads > 1 && y_head_stride < head_dim) ||
       (n_rows > 1 && n_heads > 1 && y_row_stride < (n_heads - 1) * y_head_stride + head_dim &&
        y_head_stride < (n_rows - 1) * y_row_stride + head_dim))
