@@ -546,8 +546,9 @@ qsa_status qsa_lse_merge(const float* o_parts, const float* lse_parts, int32_t n
  *   a' = magnitude (a cos(p w_i) - b sin(p w_i))
  *   b' = magnitude (a sin(p w_i) + b cos(p w_i)).
  * The other channels stay as they are.  Angles are kept in turns as 64-bit
- * fractions, so that p w_i is reduced to one turn exactly whatever p is (negative
- * positions turn backwards): what is left is the rounding of w_i, 2^-53 of it, and of
+ * fractions, w_i / (2 pi) to the nearest, so that whole turns of p w_i are dropped
+ * exactly whatever p is (negative positions turn backwards): what is left is half of
+ * 2^-64 of a turn a position (for the w_i as given: binary64), and the rounding of
  * the reduced angle, cosine and sine in binary32 (2^-22 together).  Arithmetic is
  * 32-bit, each result rounded once to the row's type.
  */

@@ -102,6 +102,19 @@ __global__ void __launch_bounds__(kThreads, 4) rotate_kernel(const __grid_consta
   }
 }
 
+// w / (2 pi) modulo 1 to the nearest 2^-64, opposite for -w.  2 pi and the quotient are
+// sums of two binary64 numbers each: an fma gives what the first quotient leaves.
+uint64_t turns_of(double w) {
+  const double two_pi = 6.283185307179586, rest_of_two_pi = 2.4492935982947064e-16, half = 4294967296.0;
+  const double x = fabs(w), q = x / two_pi;
+  const double left = fmod(fma(-q, rest_of_two_pi, fma(-q, two_pi, x)) / two_pi, 1.0);
+  // Both fractions in halves of 32 bits; what lies below 2^-64 counts once, in the sum.
+  const double f = (q - floor(q)) * half, g = left * half, high_f = floor(f), high_g = floor(g);
+  const uint64_t t = ((uint64_t)((int64_t)high_f + (int64_t)high_g) << 32) +
+                     (uint64_t)nearbyint((f - high_f) * half + (g - high_g) * half);
+  return w < 0.0 ? 0 - t : t;
+}
+
 }  // namespace
 
 qsa_status check_rope(const qsa_rope* rope, int head_dim, const char* fn) {
@@ -158,15 +171,9 @@ QSA_API qsa_status qsa_rope_init(qsa_rope* rope, int32_t rot_dim, int32_t pairs,
   r.magnitude = magnitude;
   const qsa_status s = check_rope(&r, 2 * QSA_MAX_ROPE_PAIRS, fn);
   if (s != QSA_OK) return s;
-  const double two_pi = 6.283185307179586476925286766559;
   for (int i = 0; i < rot_dim / 2; ++i) {
     if (!isfinite(w[i])) return fail(QSA_ERR_INVALID_ARG, "%s: frequency %d is not finite", fn, i);
-    double t = w[i] / two_pi;
-    t -= floor(t);   // [0, 1], 1 for what lies just below 0
-    // Two halves of 32 bits: each exact in binary64.
-    const double high = floor(t * 4294967296.0);
-    const double low = floor((t * 4294967296.0 - high) * 4294967296.0);
-    r.turns[i] = ((uint64_t)high << 32) + (uint64_t)low;
+    r.turns[i] = turns_of(w[i]);
   }
   *rope = r;
   return ok();
