@@ -9,14 +9,15 @@ namespace qsa {
 namespace rope {
 
 // (cos, sin) of pair i at position pos, times the magnitude.  The angle in turns is
-// (pos * turns[i] mod 2^64) / 2^64: one integer product, exact for every position.
-// Its nearest quarter turn is taken off as an integer, so that what becomes binary32
-// lies in [-1/8, 1/8] and keeps its 24 bits there.
+// (pos * turns[i] mod 2^64) / 2^64: one integer product, exact for every position.  Its
+// nearest quarter turn is taken off as an integer, and what is left, in [-1/8, 1/8] of a
+// turn, becomes binary32 from all of its bits: an angle however small keeps 24 of them,
+// and opposite positions have opposite angles.
 __device__ __forceinline__ float2 turn(const qsa_rope& r, int i, int pos) {
-  const uint32_t a = (uint32_t)((r.turns[i] * (uint64_t)(int64_t)pos) >> 32);
-  const uint32_t quarter = (a + 0x20000000u) >> 30;
+  const uint64_t a = r.turns[i] * (uint64_t)(int64_t)pos;
+  const uint32_t quarter = (uint32_t)((a + (1ull << 61)) >> 62);
   float s, c;
-  sincospif((float)(int32_t)(a - (quarter << 30)) * 0x1p-31f, &s, &c);
+  sincospif(__ll2float_rn((int64_t)(a - ((uint64_t)quarter << 62))) * 0x1p-63f, &s, &c);
   if (quarter & 1u) {
     const float t = c;
     c = -s;
