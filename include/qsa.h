@@ -707,8 +707,7 @@ typedef struct qsa_paged_batch {
  * independently), out once to out_dtype.  fp8: q enters as the sum of two 8-bit
  * codes a value, exact from 2^-13 of the largest magnitude of its row and head on,
  * and off by at most 2^-21 of that below.  4-bit: with up to 16 entries (max_rows *
- * Hq / Hkv) the logits are those of the stored values, q exact from 2^-9 of the largest
- * magnitude of its row and head on and off by at most 2^-17 of that below; with more, K is
+ * Hq / Hkv) the logits are those of the stored values, q as for fp8; with more, K is
  * rounded to f16 (2^-11 of each value) and q off by at most 2^-39.  Both round V and the
  * weights to f16 (2^-11 each).  The result depends on the
  * lengths and the number of runs, not on timing: it is reproducible.

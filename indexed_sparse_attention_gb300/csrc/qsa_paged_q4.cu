@@ -10,12 +10,15 @@
 //   logits   z_t = sum_g s_tg (sum_c q_c code_tc) + sum_g m_tg (sum_c q_c), lanes = a
 //            tile's 128 keys.  A code is the E4M3 byte of code * 2^-9, subnormal or not:
 //            masks only, eight codes in three instructions.  q times a power of two that
-//            brings its row's largest magnitude to [2^7, 2^8) is the sum of two E4M3 codes,
-//            the second that of what the first leaves: exact for bf16's 8 bits from 2^-9 of
-//            that largest on, off by at most 2^-10 (2^-17 of the largest) below.  A block's
+//            brings its row's largest magnitude to [2^11, 2^12) is the sum of an E5M2 code
+//            and the E4M3 code of what that leaves: at most 16 of bf16's units, 4 bits, so
+//            exact from 2^-13 of that largest on, off by at most 2^-10 (2^-21 of the
+//            largest) below.  (Two E4M3 codes start at 2^8 and are exact from 2^-9 on only:
+//            channels of 2^-13 were off by up to 1/16 of themselves.)  A block's
 //            sum is a product of its own, kind::f8f6f4 with 32 of K, and the softmax, where a
 //            thread owns a key, adds the blocks up times their scales in 32 bits.  The
-//            minima are one more product, kind::f16, with the sums of q as two f16 halves.
+//            minima are one more product, kind::f16, with 1/16 of the sums of q as two f16
+//            halves (22 bits; a block of 2^12 is 2^17).
 //   output   O^T += V^T P^T, lanes = 128 channels (twice for head_dim 256), kind::f16: V as
 //            f16, code * scale + minimum rounded once.  A thread owns the four channels of a
 //            code unit, of two keys a cell, in the fragment shape of tcgen05.st.
@@ -158,15 +161,20 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// Two values to E4M3, the first in the low byte, and back.
+// Two values to E4M3 or E5M2, the first in the low byte, and back.
 __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
   unsigned short r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ float2 from_e4m3x2(uint32_t two) {
+__device__ __forceinline__ uint32_t to_e5m2x2(float lo, float hi) {
+  unsigned short r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 from_e5m2x2(uint32_t two) {
   uint32_t h2;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((unsigned short)two));
+  asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h2) : "h"((unsigned short)two));
   return __half22float2(*reinterpret_cast<const __half2*>(&h2));
 }
 template <uint32_t MASK>
@@ -193,7 +201,7 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, u
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// The same of E4M3 values, 32 of K.
+// The same of 8-bit values, 32 of K.
 __device__ __forceinline__ void mma_f8_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
@@ -535,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
         wait(&h.s_full, (uint32_t)g & 1, abrt);
         __syncwarp();
         fence_after();
-        // The blocks' sums times their scales (codes are times 2^-9), and the minima's part:
+        // The blocks' sums times their scales (codes are times 2^-9), and the minima's part (sums are over 16):
         // three at a time in registers.
         const uint4 sc = h.scale[g & 3][32 * quarter + lane];
         const uint32_t bad = h.bad[g & 15][0] | (uint32_t)h.bad[g & 15][1] << 4;
@@ -565,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
           for (int i = 0; i < kAtOnce && i0 + i <= G; ++i) {
             const int u = i0 + i;
             const float2 two = __half22float2(*reinterpret_cast<const __half2*>(&scales[u / 2 % 4]));
-            const float f = u == G ? 1.f : 512.f * (u & 1 ? two.y : two.x);
+            const float f = u == G ? 16.f : 512.f * (u & 1 ? two.y : two.x);
 #pragma unroll
             for (int e = 0; e < N; e += 2) fma2(z[e], z[e + 1], f, f, part[i][e], part[i][e + 1]);
           }
@@ -778,8 +786,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
     // The whole warp walks through the tiles with values that are the same in all its
     // lanes, and one lane issues.
     const bool leader = elect_one();
-    // 32-bit accumulators, both K-major, M = 128; E4M3 and f16 operands are both 0.
-    constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+    // 32-bit accumulators, both K-major, M = 128; E4M3 and f16 operands are both 0, E5M2 (B: bits 10-12) is 1.
+    constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24), kIdescHi = kIdesc | (1u << 10);
     const uint64_t q_desc = desc_sw128(q_s, 16, 1024);
     constexpr uint32_t kSlab = L::kQSlab >> 4;
     int g = 0, it = 0;
@@ -798,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
 #pragma unroll
             for (int y = 0; y < 2; ++y)   // both codes of q
               mma_f8_ts(tmem + kSCol + (uint32_t)(N * x), tmem + kKCol + 8u * x, q_desc + (uint32_t)(NS * y + (x >> 2)) * kSlab + 2 * (x & 3),
-                        kIdesc, (uint32_t)y);
+                        y ? kIdesc : kIdescHi, (uint32_t)y);
           mma_f16_ts(tmem + kSCol + (uint32_t)(N * G), tmem + kMinCol, q_desc + 2 * NS * kSlab, kIdesc, 0u);
           commit(&h.k_empty);
           commit(&h.s_full);
@@ -812,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
     bar_wait(&h.mma_done, 0u, &g_timeouts);
   } else {
     // ------------------------------------------------------------ Q
-    // Two E4M3 codes of each value (see above) and the sums of its blocks, a row's 16
+    // An E5M2 and an E4M3 code of each value (see above) and the sums of its blocks, a row's 16
     // channels a lane, in the order of K's cells: of channels 8 i .. 8 i + 7 the bytes are
     // 0, 2, 4, 6, 1, 3, 5, 7.  (The first item's with the warp that has no output to issue yet.)
     constexpr int kLanes = D / 16, kRows = 32 / kLanes, kBatch = 8 / kRows;   // 16 rows of two warps
@@ -841,8 +849,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
           for (int e = 0; e < 8; ++e) most = max(most, max((w[e] << 16) & 0x7fff0000u, w[e] & 0x7fff0000u));
 #pragma unroll
           for (int o = kLanes / 2; o >= 1; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-          // 2^(exponent - 7), at least 2^-100: a row of smaller values keeps fewer bits.
-          const int e = max((int)(most >> 23) - 127 - 7, -100);
+          // 2^(exponent - 11), at least 2^-100: a row of smaller values keeps fewer bits.
+          const int e = max((int)(most >> 23) - 127 - 11, -100);
           const float up = row < ir.nf ? __uint_as_float((uint32_t)(127 - e) << 23) : 0.f;
           const bool odd = most >= 0x7f800000u;   // infinity or NaN: the row's logits are NaN
           uint32_t hi[4], lo[4];
@@ -856,13 +864,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
               v[k] = (i & 1 ? bf16_hi(x2) : bf16_lo(x2)) * up;
               sum += v[k];
             }
-            const uint32_t c0 = to_e4m3x2(v[0], v[1]), c1 = to_e4m3x2(v[2], v[3]);
-            const float2 d0 = from_e4m3x2(c0), d1 = from_e4m3x2(c1);
+            const uint32_t c0 = to_e5m2x2(v[0], v[1]), c1 = to_e5m2x2(v[2], v[3]);
+            const float2 d0 = from_e5m2x2(c0), d1 = from_e5m2x2(c1);
             hi[i] = c0 | c1 << 16;
             lo[i] = to_e4m3x2(v[0] - d0.x, v[1] - d0.y) | to_e4m3x2(v[2] - d1.x, v[3] - d1.y) << 16;
-            if (odd) hi[i] = lo[i] = 0x7f7f7f7fu;
+            if (odd) hi[i] = lo[i] = 0x7f7f7f7fu;   // NaN of both kinds
           }
-          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum = 0.0625f * (sum + __shfl_xor_sync(0xffffffffu, sum, 1));
           const __half s_hi = __float2half_rn(odd ? __uint_as_float(0x7fffffffu) : sum), s_lo = __float2half_rn(sum - __half2float(s_hi));
           const int swap = row & 7;
           uint8_t* const to = q_s + row * 128;
