@@ -39,7 +39,9 @@
 // ragged batch of 16 sequences from 351 to 230 us; later ones to 172.)
 //
 // 4-bit caches: codes and records go through rings of their own, and eight warps write
-// them to the slabs as f16, code * scale + minimum rounded once, in the order that two
+// them to the slabs as f16, code * scale + minimum rounded once (f16 keeps 2^-11 of a
+// value; rows that were bf16 have no two values in a block that differ by less than 2^-8
+// of its largest, so that neither rounding makes one of two), in the order that two
 // masks of a code word give (each 8 channels as 0, 4, 1, 5, 2, 6, 3, 7; Q in the same
 // order, and the output put back); Q is f16 times a power of two of each row (its largest
 // magnitude to [2^14, 2^15): exact from 2^-31 of that on, off by at most 2^-39 of it
