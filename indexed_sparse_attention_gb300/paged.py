@@ -323,7 +323,8 @@ class PagedStep:
 
     With a rope, q holds the queries before their rotation (a slice of the projection
     that the new rows are slices of will do), append rotates K and them, these into
-    the step's q_rotated, and attend takes that; run then needs the new rows."""
+    the step's q_rotated, and attend takes that; run then needs the new rows, and attend
+    an append before it."""
 
     def __init__(self, cache: PagedCache, batch: PagedBatch, q: torch.Tensor, *, out_dtype=torch.float32,
                  window: int = 0, n_sinks: int = 0, scale: float = 0.0, n_splits: int = 0, rope: Rope | None = None):
@@ -335,6 +336,7 @@ class PagedStep:
             q = self.q_rotated = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         _check_queries(cache, batch, q)
         self.q = q
+        self._has_q = rope is None
         self.window, self.n_sinks = int(window), int(n_sinks)
         self.cfg = cache.config(q.shape[1], out_dtype, scale, n_splits)
         self.out = torch.empty(q.shape, dtype=out_dtype, device=dev)
@@ -348,15 +350,18 @@ class PagedStep:
             paged_append(self.cache, self.batch, k_new, v_new, stream)
         else:
             paged_append(self.cache, self.batch, k_new, v_new, stream, rope=self.rope, q=self.q_in, q_out=self.q_rotated)
+            self._has_q = True
 
     def attend(self, stream=None):
+        if not self._has_q:
+            raise ValueError("a step with a rope attends with the queries that append rotates: append first")
         _call_at("qsa_paged_attn", self.cache.index, stream, *self._args)
         return self.out, self.lse
 
     def run(self, k_new: torch.Tensor | None = None, v_new: torch.Tensor | None = None, stream=None):
         """Append (when given new rows), then attend."""
         if k_new is None and self.rope is not None:
-            raise ValueError("a step with a rope rotates q as it appends: give run the new rows, or call attend")
+            raise ValueError("a step with a rope rotates q as it appends: give run the new rows (or, after an append, call attend)")
         if k_new is not None:
             self.append(k_new, v_new, stream)
         return self.attend(stream)
