@@ -26,7 +26,9 @@
 // A row's maximum would be a reduction over lanes: instead the reference m of the weights
 // stays until a logit passes it by 2^8 (one vote a tile), and only then the tile's maxima
 // are reduced and O and the sums rescaled.  Weights are f16 with 2^7 at the reference, so
-// 2^15 is the largest.
+// 2^15 is the largest.  From a reference of 2^20 on, where units of a logit in binary32
+// come near what f16 has room for, every tile is voted for, and the largest logit is taken
+// off the others before they are multiplied: their differences keep all bits.
 //
 // Roles (16 warps): 0-7 expand codes (four warps a half of K's channels, and of V's keys),
 // 8-11 softmax and output, 12 copies, 13 issues the logits' products, 14 the output's, 15
@@ -73,6 +75,7 @@ constexpr int kMaxSlots = 20;
 constexpr int kSmemLimit = 227 * 1024;
 constexpr float kTop = 7.f;              // log2 of the weight at the reference
 constexpr float kLag = 8.f;              // log2 of what a weight may pass it by
+constexpr float kFar = 1048576.f;        // references from here on are taken off the logits
 constexpr float kUnset = 3.402823466e38f; // shift of a column that has seen no logit: any finite one passes it
 constexpr uint32_t kTmemCols = 512;
 // TMEM columns: logits (16 a block, then the minima's), the minima, the output's two slabs, K's codes, two buffers
@@ -103,8 +106,11 @@ struct Head {
   int abort;
   uint8_t bad[16][2];              // 16-token pieces of a tile's halves that have no page (fewer tiles are under way)
   float q[4][kEntries];            // of an item's entries: the power of two that Q's row was divided by
-  alignas(16) float2 column[kEntries];   // weight = 2^(logit * x + y)
+  // Votes are about logit * x + y, and weights 2^(logit * x + y): the same but for references from kFar on.
+  alignas(16) float2 vote[kEntries], column[kEntries];
   float ref[kEntries], factor[kEntries], inv[kEntries];
+  alignas(16) float base[kEntries];   // the logit of such a reference, 0 else
+  int far;                         // whether there is any
   int64_t to[kEntries];            // where the entry's outputs go, in elements
   int pos[kEntries];
   float mx[4][kEntries], sums[4][kEntries];
@@ -238,6 +244,19 @@ __device__ __forceinline__ void tmem_ld8_start(uint32_t taddr, float* r) {
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void tmem_ld_done(float* r) {   // (uses of r stay behind the wait)
   asm volatile("" : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]));
+}
+
+// A reference from kFar on, or none yet, for a tile whose largest logit is top; the factor on what came before.  (Out
+// of line: the first vote of an item waits for its instructions as they are.)
+__device__ __noinline__ float far_reference(Head& h, int e, float top) {
+  const float x = h.column[e].x, base = h.base[e], old = h.ref[e];
+  if (base == 0.f ? top == -INFINITY : !((top - base) * x > kLag)) return 1.f;
+  h.base[e] = top;
+  h.ref[e] = top * x;
+  h.vote[e].y = kUnset;
+  h.column[e].y = kTop;
+  h.far = 1;
+  return old == -INFINITY ? 1.f : ex2(base == 0.f ? fmaf(-top, x, old) : (base - top) * x);
 }
 
 // v[0 .. 7] of every lane, reduced over the warp: lane x returns that of v[x / 4].
@@ -518,19 +537,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
       if (me < N) {
         const int e = me, f = ir.f0 + min(e, ir.nf - 1), r = row_of(p, f);
         // (The factor is not 0: hidden logits are -infinity times it.)
-        h.column[e] = mine ? make_float2(fmaxf(h.q[it & 3][e] * (p.scale * kLog2e), 1e-37f), kUnset) : make_float2(0.f, -1000.f);
+        h.vote[e] = h.column[e] = mine ? make_float2(fmaxf(h.q[it & 3][e] * (p.scale * kLog2e), 1e-37f), kUnset) : make_float2(0.f, -1000.f);
         h.ref[e] = -INFINITY;
+        h.base[e] = 0.f;
+        if (e == 0) h.far = 0;
         h.pos[e] = ir.pos0 + r;
         h.to[e] = (whole ? (int64_t)(c.s.row0 + r) * p.n_q_heads + c.head * p.group + (f - r * p.group)
                          : (int64_t)c.slot(blockIdx.x) * p.mt + e) * D;
       }
       soft_sync();
-      // Of eight columns: weight = 2^(logit * x + y).
+      // Eight columns' factors and shifts.
       float2 k[8];
-      auto columns = [&](int x) {
+      auto columns = [&](const float2* of) {
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
-          const float4 two = *reinterpret_cast<const float4*>(&h.column[x + e]);
+          const float4 two = *reinterpret_cast<const float4*>(of + e);
           k[e] = make_float2(two.x, two.y), k[e + 1] = make_float2(two.z, two.w);
         }
       };
@@ -590,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
         float most = -INFINITY;
 #pragma unroll
         for (int x = 0; x < N; x += 8) {
-          columns(x);
+          columns(h.vote + x);
           float y[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) y[e] = fmaf(z[x + e], k[e].x, k[e].y);
@@ -614,15 +635,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
               const float top = fmaxf(fmaxf(h.mx[0][e], h.mx[1][e]), fmaxf(h.mx[2][e], h.mx[3][e]));
               const float old = h.ref[e], need = ceilf(top * h.column[e].x);
               const float now = top == -INFINITY ? old : old == -INFINITY || need > old + kLag ? need : old;
-              if (old != -INFINITY && now != old) factor = ex2(old - now);
-              h.ref[e] = now;
-              h.column[e].y = now == -INFINITY ? kUnset : kTop - now;
+              if (fabsf(now) <= kFar) {
+                if (old != -INFINITY && now != old) factor = ex2(old - now);
+                h.ref[e] = now;
+                h.base[e] = 0.f;
+                h.vote[e].y = h.column[e].y = kTop - now;
+              } else {
+                factor = far_reference(h, e, top);
+              }
             }
             h.factor[e] = factor;
           }
           soft_sync();
 #pragma unroll
           for (int e = 0; e < N; ++e) l[e] *= h.factor[e];
+          if (__builtin_expect(h.far != 0, 0)) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) z[e] -= h.base[e];
+          }
           if (j > 0) {   // the output as well
             wait(&h.pv_done[buf ^ 1], (uint32_t)((g - 1) >> 1) & 1, abrt);
             __syncwarp();
@@ -648,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q4_kernel(const __grid_cons
         uint32_t w2[N / 2];
 #pragma unroll
         for (int x = 0; x < N; x += 8) {   // (all before the stores, which the loads would wait behind)
-          columns(x);
+          columns(h.column + x);
 #pragma unroll
           for (int e = 0; e < 8; e += 2) {
             const float a = ex2(fmaf(z[x + e], k[e].x, k[e].y)), b = ex2(fmaf(z[x + e + 1], k[e + 1].x, k[e + 1].y));

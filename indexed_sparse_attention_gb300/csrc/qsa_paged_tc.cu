@@ -45,7 +45,9 @@
 // masks of a code word give (each 8 channels as 0, 4, 1, 5, 2, 6, 3, 7; Q in the same
 // order, and the output put back); Q is f16 times a power of two of each row (its largest
 // magnitude to [2^14, 2^15): exact from 2^-31 of that on, off by at most 2^-39 of it
-// below), and weights are f16 with 2^7 at the maximum, so that 2^15 is the largest.
+// below), and weights are f16 with 2^7 at the maximum, so that 2^15 is the largest.  From a
+// maximum of 2^20 on, where units of a logit in binary32 come near what f16 has room for,
+// it is taken off the logits before they are multiplied.
 //
 // Roles: warps 0-7 softmax and output, warps 8 and 10 copy K and V, warp 9 issues
 // the MMAs; bf16: warp 11 copies Q and clears V's ends; fp8: warps 12-15 write Q's
@@ -131,6 +133,7 @@ constexpr uint32_t kIdescLo8 = (1u << 4) | ((uint32_t)(kKT >> 3) << 17) | (8u <<
 constexpr uint32_t kIdescHi8 = kIdescLo8 | (1u << 7);
 // kind::f16 with f16 operands (bits 7-9 and 10-12 = 0 where bf16 has 1).
 constexpr uint32_t kF16Operands = ~((1u << 7) | (1u << 10));
+constexpr float kFar = 1048576.f;             // f16 weights: maxima from here on are taken off the logits first
 constexpr float kF16Weights = 7.f;            // log2 of the weight at the running maximum, f16 weights: 2^15 is the largest
 
 __device__ int g_timeouts;
@@ -1208,7 +1211,8 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __g
         named_sync(pair, 64);
         fence_after();
         mx = fmaxf(mx, h.mx[g & 1][group ^ 1][row]);
-        const bool moves = j == 0 ? mx != -INFINITY : mx > m + move;
+        // (f16: m + move may be off by more than there is room.)
+        const bool moves = j == 0 ? mx != -INFINITY : Q4 ? mx - m > move : mx > m + move;
         if (__any_sync(0xffffffffu, moves)) {   // (the same in both warps)
           const float alpha = moves ? ex2((m - mx) * zc) : 1.f;
           if (moves) {
@@ -1232,7 +1236,18 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) paged_tc_kernel(const __g
             fence_before();
           }
         }
-        const float shift = m == -INFINITY ? 0.f : (Q4 ? kF16Weights : 0.f) - m * zc;
+        float shift = m == -INFINITY ? 0.f : (Q4 ? kF16Weights : 0.f) - m * zc;
+        if constexpr (Q4) {
+          if (__builtin_expect(__any_sync(0xffffffffu, !(fabsf(shift) <= kFar)), 0)) {
+            const float base = fabsf(shift) <= kFar ? 0.f : m;   // (a row's own: others keep their bits)
+            shift = fabsf(shift) <= kFar ? shift : kF16Weights;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              xa[i] = __float_as_uint(__uint_as_float(xa[i]) - base);
+              xb[i] = __float_as_uint(__uint_as_float(xb[i]) - base);
+            }
+          }
+        }
         const uint64_t zc2 = pack2(zc, zc), shift2 = pack2(shift, shift);
         uint64_t sum2[2] = {0ull, 0ull};
         auto weigh = [&](uint32_t(&x)[32], const float* vs, uint32_t to) {
