@@ -680,7 +680,7 @@ typedef struct qsa_paged_batch {
  * A row that sees no token (a negative position, or none of its pages in the
  * table) gets out = 0 and lse = -inf.  Tokens that no row of the call sees are
  * not part of any sum, whatever their pages hold (NaN and infinities too);
- * pages that hold no visible token are not read.  A V value (or an fp8 scale)
+ * pages that hold no visible token are not read.  A V value (or a scale or minimum)
  * that some row sees must be finite for the sums of that sequence's other rows
  * of the call to be.  Sums are kept relative to a maximum that may lag the row's
  * own by a factor 2^8 in the weight, so V of about 2^119 / (visible tokens) and

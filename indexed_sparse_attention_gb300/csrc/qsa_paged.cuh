@@ -28,8 +28,8 @@ struct PagedParams {
   const void* k;
   const void* v;
   int64_t page_stride, head_stride, tok_stride;   // elements
-  const uint8_t* kv_scale;                        // fp8 state: (K, V) f16 pairs
-  int64_t s_page_stride, s_head_stride, s_tok_stride;   // records of 4 bytes
+  const uint8_t* kv_scale;                        // fp8: (K, V) f16 pairs; 4-bit: (scale, minimum) pairs
+  int64_t s_page_stride, s_head_stride, s_tok_stride;   // records (4 bytes; 4-bit: D / 4)
   int32_t n_pages;
   int32_t page_shift;        // log2 of the tokens in a page
   const int32_t* table;      // [n_seqs, table_ld]
@@ -135,11 +135,11 @@ int pages_unserved_take();
 
 // f32 caches (qsa_paged.cu).
 cudaError_t launch_paged_f32(const PagedParams& p, int head_dim, int grid, cudaStream_t st);
-// On the tensor cores (qsa_paged_tc.cu): bf16 and fp8 caches.
+// On the tensor cores (qsa_paged_tc.cu): bf16 and fp8 caches, and 4-bit ones of more than 16 entries.
 cudaError_t launch_paged_tc(const PagedParams& p, qsa_dtype kv_dtype, int head_dim, int grid, cudaStream_t st);
 int paged_tc_bad_pages_take();
 int paged_tc_wait_timeouts();
-// 4-bit caches (qsa_paged_q4.cu).
+// 4-bit caches of up to 16 entries (qsa_paged_q4.cu).
 cudaError_t launch_paged_q4(const PagedParams& p, int head_dim, int grid, cudaStream_t st);
 int paged_q4_bad_pages_take();
 int paged_q4_wait_timeouts();

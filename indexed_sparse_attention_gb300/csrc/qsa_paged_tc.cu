@@ -1,6 +1,7 @@
 // Attention over a paged K/V cache on the 5th-generation tensor cores: bf16 and
-// fp8 caches, and 4-bit caches of more than 16 entries an item (see qsa_paged.cuh for the division of the work into runs of key
-// tiles, and qsa_paged.cu for the formulas and the joining launch).
+// fp8 caches, and 4-bit caches of calls of more than 16 entries (see qsa_paged.cuh for
+// the division of the work into runs of key tiles, and qsa_paged.cu for the formulas and
+// the joining launch).
 //
 // An item's MT <= 128 entries (query row, head of the KV head's group) are the
 // M rows of both products, 128 keys a tile:

@@ -1,31 +1,23 @@
 """Inputs and plain references for rotations and 4-bit paged caches.
 
-Tolerances of the attention over a 4-bit cache (u = 2^-24, D = head_dim, G = D / 32
-blocks, n visible tokens; v_tc = s code + m of a block):
-  logits   products of exact codes, summed in binary32 by the tensor cores (each
-           addition off by at most 2 u of the sum's largest part), scaled and summed
-           over the blocks, the minima against block sums of q whose two f16 halves
-           keep 2^-22: |dz| <= (2 D + 4 G + 16) u zmag + 4 u zmag,
-           zmag = max_t scale * sum_c |q_c| (|s code| + |m|) over visible t.
-           q times a power of two that brings its row's largest magnitude qmax to
-           [2^8, 2^9) is f16: exact from 2^-25 qmax on, off by at most 2^-33 qmax
-           below: zlost = 2^-33 qmax scale max_t sum_c |code s| + |m|.
-           Two roundings of the base-2 exponent and ex2 (2 ulp): (4 zmag + 4) u.
-  weights  off by a factor 1 +- e, e = 2 ((2 D + 4 G + 24) u zmag + zlost) + 8 u, sums
-           of n terms another n 2 u.
-  out      2 (e + (n + 16) 2 u) wabs, wabs = sum_t w_t (|s code| + |m|) / sum_t w_t; and
-           the weights' roundings to f16, 2^-11 of each: two before the codes'
-           product, one before the minima's: (2^-10 wcode + 2^-11 wmin) 1.01; weights
-           below f16's normal numbers (the largest is 2^2 or more, when the scales
-           are below 2^6) are off by 2^-25: n 2^-27 (15 + max |m|).
+Tolerances of the attention over a 4-bit cache, as attend4 has them (u = 2^-24, D = head_dim, G = D / 32 blocks, n
+visible tokens; v_tc = s code + m of a block).  `wide` is a call of more than 16 entries a sequence and KV head.
+  kmag     up to 16 entries: |s code| + |m|, as codes and minima meet q in products of their own; wide: |k|, K being
+           f16 values.  mag = max_t scale * sum_c |q_c| kmag_tc over visible t.
+  logits   products of exact codes (wide: f16 values), summed in binary32 by the tensor cores (each addition off by at
+           most 2 u of the sum's largest part), scaled and summed over the blocks, the minima against block sums of q
+           whose two f16 halves keep 2^-22; two roundings of the base-2 exponent: (2 D + 4 G + 24) u mag; ex2 2 ulp.
+  lost     what q loses.  Up to 16 entries it is an E5M2 and an E4M3 code, off by at most 2^-21 of its row's largest
+           magnitude; attend4 allows 2^-17 (test_gpu_q4_queries.py holds the kernel to 2^-21).  Wide: f16 times a power of
+           two that brings the largest to [2^14, 2^15), off by at most 2^-39 of it; and K rounded to f16, 2^-11 mag, or
+           where it is below f16's normal numbers 2^-25 scale sum_c |q_c|.
+  weights  off by a factor 1 +- e, e = 2 ((2 D + 4 G + 24) u mag + lost) + 8 u (weight and reference); sums of n terms
+           another n 2 u.
+  out      2 (e + (n + 16) 2 u) wabs, wabs = sum_t w_t |v_t| / sum_t w_t; V and the weights rounded to f16, 2^-11 each:
+           1.01 2^-10 wabs; V below f16's normal numbers 2^-25; weights below them are off by 2^-25, where the largest is
+           about 2^7: n 2^-32 max |v| (twice that where a rounded-up reference leaves the largest at 2^6, which no
+           case comes near).
   lse      e + (n + 16) 2 u + 4 u |lse|.
-
-Calls with more than 16 entries a sequence and KV head take K, V and the weights
-rounded to f16: |dz| grows by (2^-11 1.01) kmag, kmag = max_t scale sum_c |q_c| |k_tc|
-(values below f16's normal numbers: 2^-25 scale sum_c |q_c|), z's own sums are of |k|;
-q is exact from 2^-31 qmax on (2^-39 below), out is off by another
-2^-10 1.01 sum_t w_t |v_t| / sum_t w_t, V below f16's normal numbers by 2^-25, and
-weights below them (the largest is 2^7 or more) by n 2^-32 max |v|.
 """
 from __future__ import annotations
 
