@@ -39,13 +39,13 @@
 // from those that expand (a ragged batch of 16 sequences took 146 us so, and 136 this way).
 //
 // What bounds it (us a call on one GB300, 24 query and 2 KV heads of 256): 16 sequences of
-// 4k to 262k tokens 127, where HBM needs 77 and the copies alone take 95.  The rest is
+// 4k to 262k tokens 128, where HBM needs 77 and the copies alone take 95.  The rest is
 // instructions, the expansion's and the softmax's side by side: with the softmax on two
 // warpgroups of eight columns, which does more work, 136 -- then 118 without V's expansion,
 // 125 without the softmax's arithmetic, 107 without both.  (Codes multiplied with mma.sync by
 // 12 warps whose registers are full of output took 162; K expanded to f16 like V 151; 16
 // expanding warps, at 64 registers, 163; 12, four of them for K, 140; one buffer of V's cells
-// 145.)  One sequence of 65,536 tokens 28, of which 10 are the call's start, the joining launch
+// 145.)  One sequence of 65,536 tokens 28.5, of which 10 are the call's start, the joining launch
 // and the first tiles' way through the roles.
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>

@@ -20,8 +20,8 @@
 // back, 22.9 us, where HBM needs 9 (dependent reads -- lengths and ranges, page -- before
 // the first store, and 13 rows an SM in which to hide them); ragged prompts of 128 into an
 // fp8 cache 27.3 of 14.3 (44 with a row a CTA; 20 were the sequences known); 65,536 rows of
-// 256 back out of 4 bits 33 of 26 (52 with eight bytes of codes a lane); steps of a few
-// rows 5.1 to 8.1, the host's call.
+// 256 back out of 4 bits 33.5 of 26 (52 with eight bytes of codes a lane); steps of a few
+// rows 5.7 to 8.3, the host's call.
 #include <cuda_fp16.h>
 
 #include <algorithm>
